@@ -15,5 +15,11 @@ from .binding import (GDN_DTYPE_BF16, GDN_DTYPE_F32, GdnError, GdnProblem,  # no
                       gdn_decode_step_gated,
                       gdn_chunk_bwd, gdn_chunk_fwd, gdn_chunk_saved_bytes,
                       gdn_chunk_workspace_bytes, gdn_decode_step, lib, make_problem,
-                      status_string)
-from .autograd import chunk_gated_delta_rule  # noqa: E402,F401
+                      status_string,
+                      GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED, GDN_ROPE_SCALE_LINEAR,
+                      GDN_ROPE_SCALE_NONE, GDN_ROPE_SCALE_PARTS,
+                      gdn_linear_attn_bwd, gdn_linear_attn_fwd, gdn_linear_attn_prefill_paged,
+                      gdn_linear_attn_step, gdn_linear_attn_workspace_bytes, gdn_rope,
+                      gdn_rope_frequencies, linear_attn_bwd, linear_attn_fwd,
+                      linear_attn_prefill_paged, linear_attn_step, rope, rope_frequencies)
+from .autograd import chunk_gated_delta_rule, linear_attention, rotary  # noqa: E402,F401

@@ -80,3 +80,91 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, out
     if batched:
         o = o.unsqueeze(0)
     return o, ht
+
+
+def _linear_function():
+    import torch
+
+    class LinearAttention(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, log_decay, initial_state, cu_host, cu_dev, scale, output_final_state):
+            ctx.set_materialize_grads(False)
+            ctx.cu, ctx.scale = (cu_host, cu_dev), scale
+            ctx.save_for_backward(q, k, v, log_decay, initial_state)
+            return binding.linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=scale,
+                                           initial_state=initial_state,
+                                           output_final_state=output_final_state)
+
+        @staticmethod
+        def backward(ctx, d_o, d_ht):
+            q, k, v, log_decay, h0 = ctx.saved_tensors
+            if d_o is None:
+                d_o = torch.zeros_like(v)
+            gr = binding.linear_attn_bwd(q, k, v, log_decay, d_o.to(torch.bfloat16).contiguous(), *ctx.cu,
+                                         scale=ctx.scale, initial_state=h0,
+                                         d_final_state=None if d_ht is None else d_ht.float().contiguous(),
+                                         want_dh0=h0 is not None)
+            return gr["dq"], gr["dk"], gr["dv"], None, gr["dh0"], None, None, None, None
+
+    return LinearAttention
+
+
+def _rotary_function():
+    import torch
+
+    class Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, freq, layout, mscale):
+            ctx.args = (layout, mscale)
+            ctx.save_for_backward(positions, freq)
+            return binding.rope(q, k, positions, freq, layout=layout, mscale=mscale)
+
+        @staticmethod
+        def backward(ctx, dq, dk):
+            positions, freq = ctx.saved_tensors
+            layout, mscale = ctx.args
+            dq, dk = binding.rope(dq.contiguous(), dk.contiguous(), positions, freq, layout=layout,
+                                  mscale=mscale, backward=True)
+            return dq, dk, None, None, None, None
+
+    return Rotary
+
+
+_LINEAR = _ROTARY = None
+
+
+def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_final_state=False,
+                     cu_seqlens=None, cu_seqlens_cpu=None):
+    """Differentiable linear attention with a decay for each head, in the call shape of
+    chunk_gated_delta_rule: o (and the final state [N, HV, K, V] when output_final_state).
+
+    log_decay: fp32 [HV], <= 0, a constant of the layer: asking for its gradient is refused."""
+    global _LINEAR
+    if log_decay.requires_grad:
+        raise ValueError("log_decay has no gradient: pass it detached")
+    if _LINEAR is None:
+        _LINEAR = _linear_function()
+    import torch
+    batched = q.dim() == 4
+    if batched:
+        if q.shape[0] != 1:
+            raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
+        q, k, v = q[0], k[0], v[0]
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor([0, q.shape[0]], dtype=torch.int32, device=q.device)
+    if cu_seqlens_cpu is None:
+        cu_seqlens_cpu = cu_seqlens.cpu()
+    cu_host = np.asarray(cu_seqlens_cpu.cpu() if hasattr(cu_seqlens_cpu, "cpu") else cu_seqlens_cpu,
+                         dtype=np.int32)
+    o, ht = _LINEAR.apply(q.contiguous(), k.contiguous(), v.contiguous(), log_decay.contiguous(),
+                          initial_state, cu_host, cu_seqlens.to(torch.int32).contiguous(), scale,
+                          output_final_state)
+    return (o.unsqueeze(0) if batched else o), ht
+
+
+def rotary(q, k, positions, freq, layout="half", mscale=1.0):
+    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (binding.rope)."""
+    global _ROTARY
+    if _ROTARY is None:
+        _ROTARY = _rotary_function()
+    return _ROTARY.apply(q.contiguous(), k.contiguous(), positions, freq, layout, mscale)

@@ -7,6 +7,7 @@
 
 #include "../../include/gdn.h"
 #include "gdn_kernels.h"
+#include "gdn_linear.h"
 
 namespace {
 
@@ -440,6 +441,88 @@ gdn_status decode_impl(int32_t batch, int32_t num_k_heads, int32_t num_v_heads, 
     return cuda_status(e);
 }
 
+// ---------------------------------------------------------------- linear attention
+// Workspace of the decay-only calls: the fp32 outputs of dq and dk per value head when
+// value heads share key heads (summed in order afterwards).
+struct LinearWs {
+    float *part;
+};
+size_t carve_linear(const Dims &d, int for_backward, void *base, LinearWs *w) {
+    Carver cv(base);
+    w->part = nullptr;
+    if (for_backward && d.HV != d.H) w->part = cv.take<float>((size_t)d.T * d.HV * gdn::kDim);
+    return cv.used() > 0 ? cv.used() : kAlign;
+}
+
+gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const float *log_decay) {
+    gdn::LinearArgs a{};
+    a.N = d.N;
+    a.T = d.T;
+    a.HV = d.HV;
+    a.longest = 0;
+    for (int n = 0; n < d.N; ++n) {
+        const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
+        a.longest = len > a.longest ? len : a.longest;
+    }
+    a.log_decay = log_decay;
+    a.so = d.scale;
+    a.w = 1.f;
+    a.s_rs = 1;           // K-major states: S[r][c] at c * 128 + r
+    a.s_cs = gdn::kDim;
+    a.cu_dev = p->cu_seqlens_dev;
+    a.status = p->device_status;
+    return a;
+}
+
+// The roles of one scan: output reads q against the state of k and v.
+void linear_roles(gdn::LinearArgs &a, const void *q, int nq, const void *k, int nk, const void *v,
+                  int nv) {
+    a.q = static_cast<const bf16 *>(q);
+    a.k = static_cast<const bf16 *>(k);
+    a.v = static_cast<const bf16 *>(v);
+    a.nq = nq;
+    a.nk = nk;
+    a.nv = nv;
+}
+
+gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, const void *v,
+                           const float *log_decay, const float *initial_state, void *o,
+                           float *final_state, void *workspace, size_t ws_size,
+                           gdn_stream_t stream, const Paged *pg) {
+    Dims d;
+    gdn_status st = check_problem(p, &d);
+    if (st != GDN_OK) return st;
+    if (d.T > 0 && (!q || !k || !v || !o)) return GDN_ERR_INVALID_ARG;
+    if (!log_decay || !aligned_to(log_decay, 4)) return GDN_ERR_INVALID_ARG;
+    if (pg) {
+        if (!pg->pool || pg->num_slots < 1 || !pg->indices || !aligned16(pg->pool) ||
+            !aligned_to(pg->indices, 4) || !aligned_to(pg->resume, 4) || !aligned_to(pg->status, 4))
+            return GDN_ERR_INVALID_ARG;
+    }
+    const void *ptrs[] = {q, k, v, initial_state, o, final_state, workspace};
+    for (const void *x : ptrs)
+        if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
+    if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
+    if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    LinearWs ws;
+    if (ws_size < carve_linear(d, 0, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    gdn::LinearArgs a = linear_args(d, p, log_decay);
+    linear_roles(a, q, d.H, k, d.H, v, d.HV);
+    a.o = static_cast<bf16 *>(o);
+    a.s0 = initial_state;
+    a.s1 = final_state;
+    if (pg) {
+        a.pool = pg->pool;
+        a.num_slots = pg->num_slots;
+        a.pool_idx = pg->indices;
+        a.pool_resume = pg->resume;
+        a.pool_status = pg->status;
+        a.s_rs = gdn::kDim;   // V-major slots
+        a.s_cs = 1;
+    }
+    return cuda_status(gdn::launch_linear_scan(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -581,6 +664,175 @@ gdn_status gdn_decode_step(int32_t batch, int32_t num_k_heads, int32_t num_v_hea
     return gdn_decode_step_timed(batch, num_k_heads, num_v_heads, head_dim_k, head_dim_v, scale,
                                  q, k, v, g, beta, state_pool, num_slots, state_indices, o,
                                  device_status, stream, nullptr);
+}
+
+size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward) {
+    Dims d;
+    LinearWs ws;
+    if (for_backward < 0 || for_backward > 1) return 0;
+    if (check_problem(p, &d) != GDN_OK) return 0;
+    return carve_linear(d, for_backward, nullptr, &ws);
+}
+
+gdn_status gdn_linear_attn_fwd(const gdn_problem *p, const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *initial_state, void *o,
+                               float *final_state, void *workspace, size_t ws_size,
+                               gdn_stream_t stream) {
+    return linear_fwd_impl(p, q, k, v, log_decay, initial_state, o, final_state, workspace, ws_size,
+                           stream, nullptr);
+}
+
+gdn_status gdn_linear_attn_prefill_paged(const gdn_problem *p, const void *q, const void *k,
+                                         const void *v, const float *log_decay,
+                                         float *state_pool, int32_t num_slots,
+                                         const int32_t *state_indices,
+                                         const int32_t *has_initial_state, void *o,
+                                         int32_t *device_status, void *workspace,
+                                         size_t ws_size, gdn_stream_t stream) {
+    const Paged pg{state_pool, num_slots, state_indices, has_initial_state, device_status};
+    return linear_fwd_impl(p, q, k, v, log_decay, nullptr, o, nullptr, workspace, ws_size, stream, &pg);
+}
+
+gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *initial_state,
+                               const void *d_o, const float *d_final_state, void *dq, void *dk,
+                               void *dv, float *dh0, void *workspace, size_t ws_size,
+                               gdn_stream_t stream) {
+    Dims d;
+    gdn_status st = check_problem(p, &d);
+    if (st != GDN_OK) return st;
+    if (d.T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)) return GDN_ERR_INVALID_ARG;
+    if (!log_decay || !aligned_to(log_decay, 4)) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, v, initial_state, d_o, d_final_state, dq, dk, dv, dh0, workspace};
+    for (const void *x : ptrs)
+        if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
+    if (dh0 && dh0 == d_final_state) return GDN_ERR_INVALID_ARG;
+    if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    LinearWs ws;
+    if (ws_size < carve_linear(d, 1, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    // dq: a forward scan over (d_o, v, k), the state transposed
+    gdn::LinearArgs a = linear_args(d, p, log_decay);
+    linear_roles(a, d_o, d.HV, v, d.HV, k, d.H);
+    a.s0 = initial_state;
+    a.s_rs = gdn::kDim;
+    a.s_cs = 1;
+    a.o = static_cast<bf16 *>(dq);
+    a.part = ws.part;
+    if ((e = gdn::launch_linear_scan(a, s)) != cudaSuccess) return cuda_status(e);
+    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, d.HV, a.status, s)) != cudaSuccess)
+        return cuda_status(e);
+    // dk: a reverse scan over (v, d_o, q), the state transposed
+    a.reverse = 1;
+    a.s0 = d_final_state;
+    a.so = 1.f;
+    a.w = d.scale;
+    linear_roles(a, v, d.HV, d_o, d.HV, q, d.H);
+    a.o = static_cast<bf16 *>(dk);
+    if ((e = gdn::launch_linear_scan(a, s)) != cudaSuccess) return cuda_status(e);
+    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, d.HV, a.status, s)) != cudaSuccess)
+        return cuda_status(e);
+    // dv: a reverse scan over (k, q, d_o); it ends with dh0
+    linear_roles(a, k, d.H, q, d.H, d_o, d.HV);
+    a.s_rs = 1;
+    a.s_cs = gdn::kDim;
+    a.o = static_cast<bf16 *>(dv);
+    a.part = nullptr;
+    a.s1 = dh0;
+    return cuda_status(gdn::launch_linear_scan(a, s));
+}
+
+gdn_status gdn_linear_attn_step(int32_t batch, int32_t num_k_heads, int32_t num_v_heads,
+                                int32_t head_dim_k, int32_t head_dim_v, float scale,
+                                const void *q, const void *k, const void *v,
+                                const float *log_decay, float *state_pool, int32_t num_slots,
+                                const int32_t *state_indices, void *o, int32_t *device_status,
+                                gdn_stream_t stream) {
+    if (batch < 0 || num_k_heads < 1 || num_v_heads < 1 || num_slots < 1)
+        return GDN_ERR_INVALID_ARG;
+    if (head_dim_k != 128 || head_dim_v != 128) return GDN_ERR_UNSUPPORTED;
+    if (num_v_heads % num_k_heads != 0) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)batch * num_v_heads > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if (batch == 0) return GDN_OK;
+    if (!q || !k || !v || !log_decay || !state_pool || !state_indices || !o)
+        return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {q, k, v, state_pool, o};
+    for (const void *x : ptrs)
+        if (!aligned16(x)) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(log_decay, 4) || !aligned_to(state_indices, 4) || !aligned_to(device_status, 4))
+        return GDN_ERR_INVALID_ARG;
+    const float s = scale > 0.f ? scale : 1.0f / sqrtf((float)head_dim_k);
+    return cuda_status(gdn::launch_linear_step(
+        batch, num_k_heads, num_v_heads, s, static_cast<const bf16 *>(q),
+        static_cast<const bf16 *>(k), static_cast<const bf16 *>(v), log_decay, state_pool, num_slots,
+        state_indices, static_cast<bf16 *>(o), device_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                double trained_len, double low_turns, double high_turns,
+                                float *freq) {
+    if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !isfinite(base) || !freq)
+        return GDN_ERR_INVALID_ARG;
+    if (scaling != GDN_ROPE_SCALE_NONE && scaling != GDN_ROPE_SCALE_LINEAR &&
+        scaling != GDN_ROPE_SCALE_PARTS)
+        return GDN_ERR_INVALID_ARG;
+    if (scaling != GDN_ROPE_SCALE_NONE && (!(factor >= 1.0) || !isfinite(factor)))
+        return GDN_ERR_INVALID_ARG;
+    if (scaling == GDN_ROPE_SCALE_PARTS &&
+        (!(trained_len >= 1.0) || !isfinite(trained_len) || !(low_turns >= 0.0) ||
+         !(high_turns > low_turns) || !isfinite(high_turns)))
+        return GDN_ERR_INVALID_ARG;
+    const int half = rot_dim / 2;
+    for (int p = 0; p < half; ++p) {
+        double f = pow(base, -2.0 * p / rot_dim) / (2.0 * 3.14159265358979323846);
+        if (scaling == GDN_ROPE_SCALE_LINEAR) f /= factor;
+        if (scaling == GDN_ROPE_SCALE_PARTS) {
+            double keep = (f * trained_len - low_turns) / (high_turns - low_turns);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            f = f * keep + f / factor * (1.0 - keep);
+        }
+        freq[p] = (float)f;
+        freq[half + p] = (float)(f - (double)freq[p]);
+    }
+    return GDN_OK;
+}
+
+gdn_status gdn_rope(int64_t total_tokens, int32_t num_q_heads, int32_t num_k_heads,
+                    int32_t head_dim, int32_t rot_dim, int32_t layout, int32_t backward,
+                    float mscale, const void *q, const void *k, const int32_t *positions,
+                    const float *freq, void *q_out, void *k_out, gdn_stream_t stream) {
+    if (total_tokens < 0 || total_tokens > 0x7fffffffLL || num_q_heads < 1 || num_k_heads < 0 ||
+        num_q_heads > 65535 || num_k_heads > 65535)
+        return GDN_ERR_INVALID_ARG;
+    if (head_dim < 2 || head_dim > 1024 || head_dim % 2 != 0 || rot_dim < 2 || rot_dim > head_dim ||
+        rot_dim % 2 != 0)
+        return GDN_ERR_INVALID_ARG;
+    if ((layout != GDN_ROPE_HALF && layout != GDN_ROPE_INTERLEAVED) || (backward != 0 && backward != 1) ||
+        !isfinite(mscale))
+        return GDN_ERR_INVALID_ARG;
+    if (total_tokens == 0) return GDN_OK;
+    if (!q || !q_out || !positions || !freq || (num_k_heads > 0 && (!k || !k_out)))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned_to(positions, 4) || !aligned_to(freq, 4) ||
+        (num_k_heads > 0 && (!aligned16(k) || !aligned16(k_out))))
+        return GDN_ERR_INVALID_ARG;
+    gdn::RopeArgs a{};
+    a.T = (int)total_tokens;
+    a.Hq = num_q_heads;
+    a.Hk = num_k_heads;
+    a.D = head_dim;
+    a.rot = rot_dim;
+    a.interleaved = layout == GDN_ROPE_INTERLEAVED;
+    a.backward = backward;
+    a.mscale = mscale;
+    a.q = static_cast<const bf16 *>(q);
+    a.k = static_cast<const bf16 *>(k);
+    a.pos = positions;
+    a.freq = freq;
+    a.qo = static_cast<bf16 *>(q_out);
+    a.ko = static_cast<bf16 *>(k_out);
+    return cuda_status(gdn::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_check_indices(const int32_t *state_indices, int32_t batch, int32_t num_slots,

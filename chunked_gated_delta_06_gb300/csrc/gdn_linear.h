@@ -1,0 +1,58 @@
+// gdn_linear.h -- internal interface of the decay-only linear attention kernels.
+#pragma once
+
+#include "gdn_kernels.h"
+
+namespace gdn {
+
+// One scan of linear attention over packed sequences, for value head hv with decay
+// lam = e^{log_decay[hv]} (rows r = feature of v, columns c = feature of q and k):
+//   forward:  S <- lam S + w v_t k_t^T,  o_t = so S q_t           (t ascending)
+//   reverse:  S <- S + w v_t k_t^T,  o_t = so S q_t,  S <- lam S  (t descending)
+// The forward call is one such scan; the backward is three of them with the roles of
+// the tensors exchanged (see gdn_linear.cu).  A role tensor with n heads is read at
+// head hv / (HV / n).
+struct LinearArgs {
+    int N, T, HV;
+    int longest;              // tokens of the longest sequence (host copy of cu_seqlens)
+    const bf16 *q, *k, *v;    // [T, nq | nk | nv, 128]
+    int nq, nk, nv;
+    bf16 *o;                  // [T, HV, 128], or null
+    float *part;              // [T, HV, 128]: fp32 outputs instead of o (summed by launch_linear_heads)
+    const float *log_decay;   // [HV]
+    const float *s0;          // [N, HV, 128, 128] or null (zeros)
+    float *s1;                // the same shape, or null
+    int s_rs, s_cs;           // element strides of (r, c) in s0, s1 and the pool's slots
+    float *pool;              // [num_slots, HV, V, K] in place of s0 / s1 (paged prefill), or null
+    int num_slots;
+    const int *pool_idx, *pool_resume;
+    int *pool_status;
+    float so, w;              // output and update factors
+    int reverse;
+    const int *cu_dev;        // [N + 1]
+    int *status;
+};
+
+cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t s);
+// out[t][h] = sum of part[t][hv] over the HV / H value heads of key head h, in order, as bf16.
+cudaError_t launch_linear_heads(const float *part, bf16 *out, int T, int H, int HV, int *status,
+                                cudaStream_t s);
+
+cudaError_t launch_linear_step(int B, int H, int HV, float scale, const bf16 *q, const bf16 *k,
+                               const bf16 *v, const float *log_decay, float *pool, int num_slots,
+                               const int32_t *idx, bf16 *o, int32_t *status, cudaStream_t s);
+
+// Rotary positions: x1' = m (x1 c - x2 s), x2' = m (x2 c + x1 s) for the pairs of the first
+// `rot` elements of every head, c + i s = e^{2 pi i pos f}.
+struct RopeArgs {
+    int T, Hq, Hk, D, rot;
+    int interleaved, backward;
+    float mscale;
+    const bf16 *q, *k;
+    const int32_t *pos;       // [T]
+    const float *freq;        // [2, rot / 2]: turns per position, head and tail
+    bf16 *qo, *ko;
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s);
+
+}  // namespace gdn

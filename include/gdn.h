@@ -312,6 +312,115 @@ gdn_status gdn_decode_step_gated(int32_t batch, int32_t num_k_heads, int32_t num
                                  const int32_t *state_indices, void *o, int32_t *device_status,
                                  gdn_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head (no delta rule, no q/k norm):
+ *     S_t = e^{log_decay[hv]} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ * per sequence n and value head hv, key head h = hv / (HV / H), S (K x V) from
+ * initial_state[n, hv] (or 0).  log_decay (fp32 [HV], device) is a constant of
+ * the layer, <= 0 (0 = no decay, -inf = each token alone); it has no gradient.
+ * The packing, the layouts, the conventions and the checks are those of the
+ * chunk calls above: gdn_problem describes the pack (beta_dtype and
+ * scan_segment_chunks must be valid but are not used), device_status collects
+ * GDN_DEVICE_* bits, T == 0 passes the state through.  Within a chunk of tokens
+ * a NaN or infinity of one token may reach earlier tokens of the same sequence
+ * (its products are masked by zeros); it never reaches another sequence.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of scratch of gdn_linear_attn_fwd and gdn_linear_attn_prefill_paged
+ * (for_backward = 0) or gdn_linear_attn_bwd (1); never 0 for a valid problem.
+ * Returns 0 for an invalid problem or another for_backward value. */
+size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward);
+
+/* Forward.
+ *   q, k           bf16 [T, H, 128]
+ *   v              bf16 [T, HV, 128]
+ *   log_decay      fp32 [HV]
+ *   initial_state  fp32 [N, HV, 128(K), 128(V)], or NULL for zeros
+ *   o              bf16 [T, HV, 128] (out)
+ *   final_state    fp32 [N, HV, 128, 128] (out), or NULL; not initial_state
+ *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 0), 256-byte
+ *                  aligned */
+gdn_status gdn_linear_attn_fwd(const gdn_problem *p, const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *initial_state, void *o,
+                               float *final_state, void *workspace, size_t ws_bytes,
+                               gdn_stream_t stream);
+
+/* The forward over decode-pool slots, in place; state_pool, num_slots,
+ * state_indices, has_initial_state and device_status as in
+ * gdn_chunk_prefill_paged. */
+gdn_status gdn_linear_attn_prefill_paged(const gdn_problem *p, const void *q, const void *k,
+                                         const void *v, const float *log_decay,
+                                         float *state_pool, int32_t num_slots,
+                                         const int32_t *state_indices,
+                                         const int32_t *has_initial_state, void *o,
+                                         int32_t *device_status, void *workspace,
+                                         size_t ws_bytes, gdn_stream_t stream);
+
+/* Backward: needs only the forward's inputs (the states are rebuilt).
+ *   d_o            bf16 [T, HV, 128]
+ *   d_final_state  fp32 [N, HV, 128, 128], or NULL for zeros
+ *   dq, dk         bf16 [T, H, 128]  (out; summed over the HV/H value heads)
+ *   dv             bf16 [T, HV, 128] (out)
+ *   dh0            fp32 [N, HV, 128, 128] (out), or NULL; not d_final_state
+ *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 1), 256-byte
+ *                  aligned */
+gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *k, const void *v,
+                               const float *log_decay, const float *initial_state,
+                               const void *d_o, const float *d_final_state, void *dq, void *dk,
+                               void *dv, float *dh0, void *workspace, size_t ws_bytes,
+                               gdn_stream_t stream);
+
+/* One token per row over the slot-indexed pool; arguments as in
+ * gdn_decode_step, with log_decay (fp32 [HV]) in place of g and beta. */
+gdn_status gdn_linear_attn_step(int32_t batch, int32_t num_k_heads, int32_t num_v_heads,
+                                int32_t head_dim_k, int32_t head_dim_v, float scale,
+                                const void *q, const void *k, const void *v,
+                                const float *log_decay, float *state_pool, int32_t num_slots,
+                                const int32_t *state_indices, void *o, int32_t *device_status,
+                                gdn_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions.  The first rot_dim elements of every head are rot_dim / 2
+ * pairs; pair p of a token at position pos turns by a = 2 pi pos f_p:
+ *     x1' = m (x1 cos a - x2 sin a),   x2' = m (x2 cos a + x1 sin a)
+ * and the elements past rot_dim are copied.
+ * ------------------------------------------------------------------------- */
+#define GDN_ROPE_HALF 0          /* pair p = elements p and p + rot_dim / 2 */
+#define GDN_ROPE_INTERLEAVED 1   /* pair p = elements 2p and 2p + 1 */
+
+#define GDN_ROPE_SCALE_NONE 0
+#define GDN_ROPE_SCALE_LINEAR 1  /* f / factor */
+#define GDN_ROPE_SCALE_PARTS 2   /* f (keep + (1 - keep) / factor) with keep =
+                                    clamp((f trained_len - low_turns) /
+                                    (high_turns - low_turns), 0, 1): pairs that
+                                    turn often within the trained length keep
+                                    their frequency, slow ones are interpolated */
+
+/* Frequencies f_p = base^(-2p / rot_dim) / (2 pi) in turns per position, scaled
+ * as `scaling` says, as two fp32 rows: freq[p] + freq[rot_dim / 2 + p] = f_p to
+ * about 48 bits.  Host function; freq is host memory (float[rot_dim]).
+ * rot_dim even and >= 2, base > 1; LINEAR and PARTS: factor >= 1; PARTS:
+ * trained_len >= 1 and high_turns > low_turns >= 0. */
+gdn_status gdn_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                double trained_len, double low_turns, double high_turns,
+                                float *freq);
+
+/* Rotates q and k.
+ *   q, q_out   bf16 [T, num_q_heads, head_dim]  (num_q_heads >= 1)
+ *   k, k_out   bf16 [T, num_k_heads, head_dim]  (num_k_heads >= 0; NULL when 0)
+ *   positions  int32 [T] on the device, any value
+ *   freq       fp32 [2, rot_dim / 2] on the device (gdn_rope_frequencies)
+ *   mscale     the factor m (finite)
+ *   layout     GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED
+ *   backward   0: forward; 1: the gradient (turns by -a, same m)
+ * An output may be its own input (in place), and must not overlap another
+ * tensor of the call otherwise.  head_dim even, 2 .. 1024; rot_dim even,
+ * 2 .. head_dim; rows 16-byte aligned at the base. */
+gdn_status gdn_rope(int64_t total_tokens, int32_t num_q_heads, int32_t num_k_heads,
+                    int32_t head_dim, int32_t rot_dim, int32_t layout, int32_t backward,
+                    float mscale, const void *q, const void *k, const int32_t *positions,
+                    const float *freq, void *q_out, void *k_out, gdn_stream_t stream);
+
 /* Optional per-kernel timing, for profiling tools and benchmarks.  The caller
  * creates `capacity` pairs of CUDA events (cudaEvent_t, passed as void*) and
  * passes the struct to a *_timed entry point; the library records

@@ -1,0 +1,142 @@
+"""Host side of the decay-only linear attention and of rotary positions: the references'
+gradients against differences, argument checks that return before any launch, frequencies."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import chunked_gated_delta_06_gb300 as gdn
+from chunked_gated_delta_06_gb300 import binding, build
+
+import linear_reference as ref
+
+FAKE = 0x10000  # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.lib()
+
+
+def _problem(cu, H=2, HV=4, K=128, V=128, dev=0x1000):
+    return binding.make_problem(cu, H, HV, K, V, 0.0, cu_dev_ptr=dev)
+
+
+def test_reference_gradients_agree_with_differences():
+    rng = np.random.default_rng(5)
+    cu, H, HV = [0, 3, 3, 8], 1, 2
+    T = cu[-1]
+    x = dict(q=rng.standard_normal((T, H, 128)), k=rng.standard_normal((T, H, 128)),
+             v=rng.standard_normal((T, HV, 128)), h0=rng.standard_normal((3, HV, 128, 128)))
+    g = np.array([-0.3, 0.0])
+    do, dht = rng.standard_normal((T, HV, 128)), rng.standard_normal((3, HV, 128, 128))
+
+    def loss(d):
+        o, fin = ref.forward(d["q"], d["k"], d["v"], g, cu, d["h0"])
+        return float((o * do).sum() + (fin * dht).sum())
+    gr = ref.backward(x["q"], x["k"], x["v"], g, cu, do, x["h0"], dht)
+    for name, got in (("q", gr["dq"]), ("k", gr["dk"]), ("v", gr["dv"]), ("h0", gr["dh0"])):
+        step = rng.standard_normal(x[name].shape)
+        eps = 1e-5
+        up, dn = dict(x), dict(x)
+        up[name], dn[name] = x[name] + eps * step, x[name] - eps * step
+        want = (loss(up) - loss(dn)) / (2 * eps)
+        # the loss is at most bilinear in any one input: central differences are exact but for
+        # rounding, about 1e-16 * |loss| / eps
+        assert abs((got * step).sum() - want) <= 1e-6 * (1.0 + abs(want)), name
+
+
+@pytest.mark.parametrize("mut, status", [
+    (dict(K=64), binding.GDN_ERR_UNSUPPORTED),
+    (dict(H=3, HV=4), binding.GDN_ERR_UNSUPPORTED),
+    (dict(cu=[0, 5, 3]), binding.GDN_ERR_INVALID_ARG),
+    (dict(dev=0), binding.GDN_ERR_INVALID_ARG),
+])
+def test_invalid_problems_are_refused(mut, status):
+    kw = dict(cu=[0, 5, 9])
+    kw.update(mut)
+    p, keep = _problem(**kw)
+    assert gdn.gdn_linear_attn_workspace_bytes(p, 0) == 0
+    assert gdn.gdn_linear_attn_fwd(p, FAKE, FAKE, FAKE, FAKE, None, FAKE, None, FAKE, 1 << 40, None) == status
+    assert gdn.gdn_linear_attn_bwd(p, FAKE, FAKE, FAKE, FAKE, None, FAKE, None, FAKE, FAKE, FAKE, None,
+                                   FAKE, 1 << 40, None) == status
+    assert gdn.gdn_linear_attn_prefill_paged(p, FAKE, FAKE, FAKE, FAKE, FAKE, 4, FAKE, None, FAKE, None,
+                                             FAKE, 1 << 40, None) == status
+
+
+def test_missing_and_misaligned_buffers_are_refused():
+    p, keep = _problem([0, 5, 9])
+    bad = binding.GDN_ERR_INVALID_ARG
+    fwd = [FAKE] * 4 + [None, FAKE, None, FAKE, 1 << 40, None]
+    for i, x in ((0, None), (1, None), (2, None), (3, None), (5, None), (7, None),
+                 (0, FAKE + 2), (3, FAKE + 2), (4, FAKE + 4), (7, FAKE + 16)):
+        a = list(fwd)
+        a[i] = x
+        assert gdn.gdn_linear_attn_fwd(p, *a) == bad, i
+    a = list(fwd)
+    a[4] = a[6] = FAKE  # the final state over the initial state
+    assert gdn.gdn_linear_attn_fwd(p, *a) == bad
+    a = list(fwd)
+    a[8] = 0
+    assert gdn.gdn_linear_attn_fwd(p, *a) == binding.GDN_ERR_WORKSPACE_TOO_SMALL
+    bwd = [FAKE] * 4 + [None, FAKE, None, FAKE, FAKE, FAKE, None, FAKE, 1 << 40, None]
+    for i, x in ((3, None), (5, None), (7, None), (8, None), (9, None), (11, None), (5, FAKE + 8)):
+        a = list(bwd)
+        a[i] = x
+        assert gdn.gdn_linear_attn_bwd(p, *a) == bad, i
+    a = list(bwd)
+    a[12] = gdn.gdn_linear_attn_workspace_bytes(p, 1) - 1
+    assert gdn.gdn_linear_attn_bwd(p, *a) == binding.GDN_ERR_WORKSPACE_TOO_SMALL
+    paged = [FAKE] * 5 + [4, FAKE, None, FAKE, None, FAKE, 1 << 40, None]
+    for i, x in ((4, None), (5, 0), (6, None), (4, FAKE + 4), (9, FAKE + 2)):
+        a = list(paged)
+        a[i] = x
+        assert gdn.gdn_linear_attn_prefill_paged(p, *a) == bad, i
+    assert gdn.gdn_linear_attn_workspace_bytes(p, 2) == 0
+    assert gdn.gdn_linear_attn_workspace_bytes(p, -1) == 0
+    assert gdn.gdn_linear_attn_workspace_bytes(p, 0) > 0 and gdn.gdn_linear_attn_workspace_bytes(p, 1) > 0
+
+
+def test_step_arguments():
+    def call(batch=4, H=2, HV=4, K=128, pool=FAKE, slots=8, idx=FAKE, g=FAKE, q=FAKE):
+        return gdn.gdn_linear_attn_step(batch, H, HV, K, 128, 0.0, q, FAKE, FAKE, g, pool, slots, idx, FAKE,
+                                        None, None)
+    assert call(K=64) == binding.GDN_ERR_UNSUPPORTED
+    assert call(H=3) == binding.GDN_ERR_UNSUPPORTED
+    for kw in (dict(batch=-1), dict(slots=0), dict(idx=None), dict(pool=FAKE + 4), dict(g=None),
+               dict(g=FAKE + 2), dict(q=FAKE + 4)):
+        assert call(**kw) == binding.GDN_ERR_INVALID_ARG, kw
+    assert call(batch=0) == binding.GDN_OK
+
+
+def test_rope_arguments():
+    def call(T=4, Hq=2, Hk=1, D=128, rot=64, layout=0, backward=0, m=1.0, q=FAKE, k=FAKE, pos=FAKE,
+             freq=FAKE, qo=FAKE, ko=FAKE):
+        return gdn.gdn_rope(T, Hq, Hk, D, rot, layout, backward, m, q, k, pos, freq, qo, ko, None)
+    for kw in (dict(T=-1), dict(Hq=0), dict(Hk=-1), dict(D=127), dict(D=2048), dict(rot=0), dict(rot=63),
+               dict(rot=130), dict(layout=2), dict(backward=2), dict(m=float("nan")), dict(q=None),
+               dict(k=None), dict(pos=None), dict(freq=None), dict(qo=None), dict(ko=None),
+               dict(q=FAKE + 2), dict(pos=FAKE + 2)):
+        assert call(**kw) == binding.GDN_ERR_INVALID_ARG, kw
+    assert call(T=0, q=None, k=None) == binding.GDN_OK
+
+
+@pytest.mark.parametrize("rot", [2, 24, 128])
+def test_rope_frequencies(rot):
+    i = np.arange(rot // 2)
+    f = 10000.0 ** (-2.0 * i / rot) / (2 * np.pi)
+    kept = np.clip((f * 4096 - 1.0) / 31.0, 0, 1)
+    for kind, want in (("none", f), ("linear", f / 8), ("parts", f * kept + f / 8 * (1 - kept))):
+        got = gdn.rope_frequencies(rot, scaling=kind, factor=8.0, trained_len=4096, device="cpu").double()
+        assert got.shape == (2, rot // 2)
+        # head + tail hold 48 bits; pow and the division are good to a few 2^-53
+        np.testing.assert_allclose(got.sum(0).numpy(), want, rtol=2.0 ** -46, atol=0)
+    for kw in (dict(base=1.0), dict(scaling="linear", factor=0.5), dict(scaling="parts", factor=2.0),
+               dict(scaling="parts", factor=2.0, trained_len=4096, low_turns=4.0, high_turns=4.0)):
+        with pytest.raises(gdn.GdnError):
+            gdn.rope_frequencies(rot, device="cpu", **kw)
+    assert gdn.gdn_rope_frequencies(3, 1e4, 0, 1.0, 0.0, 1.0, 32.0, (ctypes.c_float * 4)()) \
+        == binding.GDN_ERR_INVALID_ARG
+    assert gdn.gdn_rope_frequencies(4, 1e4, 3, 1.0, 0.0, 1.0, 32.0, (ctypes.c_float * 4)()) \
+        == binding.GDN_ERR_INVALID_ARG

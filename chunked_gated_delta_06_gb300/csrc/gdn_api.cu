@@ -5,6 +5,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "../../include/gdn.h"
 #include "gdn_kernels.h"
 #include "gdn_linear.h"
@@ -464,6 +466,13 @@ gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const float *lo
         const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
         a.longest = len > a.longest ? len : a.longest;
     }
+    if (d.N <= gdn::kLinearOrder) {
+        for (int n = 0; n < d.N; ++n) a.order[n] = (uint16_t)n;
+        const int32_t *cu = p->cu_seqlens_host;
+        std::stable_sort(a.order, a.order + d.N, [cu](uint16_t x, uint16_t y) {
+            return cu[x + 1] - cu[x] > cu[y + 1] - cu[y];
+        });
+    }
     a.log_decay = log_decay;
     a.so = d.scale;
     a.w = 1.f;
@@ -520,7 +529,7 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
         a.s_rs = gdn::kDim;   // V-major slots
         a.s_cs = 1;
     }
-    return cuda_status(gdn::launch_linear_scan(a, reinterpret_cast<cudaStream_t>(stream)));
+    return cuda_status(gdn::launch_linear_tc(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -720,7 +729,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     a.s_cs = 1;
     a.o = static_cast<bf16 *>(dq);
     a.part = ws.part;
-    if ((e = gdn::launch_linear_scan(a, s)) != cudaSuccess) return cuda_status(e);
+    if ((e = gdn::launch_linear_tc(a, s)) != cudaSuccess) return cuda_status(e);
     if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, d.HV, a.status, s)) != cudaSuccess)
         return cuda_status(e);
     // dk: a reverse scan over (v, d_o, q), the state transposed
@@ -730,7 +739,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     a.w = d.scale;
     linear_roles(a, v, d.HV, d_o, d.HV, q, d.H);
     a.o = static_cast<bf16 *>(dk);
-    if ((e = gdn::launch_linear_scan(a, s)) != cudaSuccess) return cuda_status(e);
+    if ((e = gdn::launch_linear_tc(a, s)) != cudaSuccess) return cuda_status(e);
     if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, d.HV, a.status, s)) != cudaSuccess)
         return cuda_status(e);
     // dv: a reverse scan over (k, q, d_o); it ends with dh0
@@ -740,7 +749,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     a.o = static_cast<bf16 *>(dv);
     a.part = nullptr;
     a.s1 = dh0;
-    return cuda_status(gdn::launch_linear_scan(a, s));
+    return cuda_status(gdn::launch_linear_tc(a, s));
 }
 
 gdn_status gdn_linear_attn_step(int32_t batch, int32_t num_k_heads, int32_t num_v_heads,

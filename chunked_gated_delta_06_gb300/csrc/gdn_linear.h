@@ -5,6 +5,8 @@
 
 namespace gdn {
 
+constexpr int kLinearOrder = 128;   // packs of at most this many sequences start the longest first
+
 // One scan of linear attention over packed sequences, for value head hv with decay
 // lam = e^{log_decay[hv]} (rows r = feature of v, columns c = feature of q and k):
 //   forward:  S <- lam S + w v_t k_t^T,  o_t = so S q_t           (t ascending)
@@ -31,9 +33,11 @@ struct LinearArgs {
     int reverse;
     const int *cu_dev;        // [N + 1]
     int *status;
+    uint16_t order[kLinearOrder];  // N <= kLinearOrder: sequences by decreasing length
 };
 
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t s);
+cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s);
 // out[t][h] = sum of part[t][hv] over the HV / H value heads of key head h, in order, as bf16.
 cudaError_t launch_linear_heads(const float *part, bf16 *out, int T, int H, int HV, int *status,
                                 cudaStream_t s);

@@ -1,0 +1,525 @@
+// gdn_linear_tc.cu -- the scans of the decay-only linear attention on the tensor cores.
+//
+// A CTA walks the 128-token chunks of one (sequence, value head).  With i, j the positions
+// of a chunk's tokens, lam the head's decay, S (rows: features of v, columns: features of q
+// and k) the running state, for a forward scan
+//   o_i = so ( lam^{i+1} S q_i + w sum_{j<=i} lam^{i-j} (q_i . k_j) v_j )
+//   S  <- lam^L S + w sum_t lam^{L-1-t} v_t k_t^T
+// and for a reverse scan (the state enters behind the chunk's last token)
+//   o_i = so ( lam^{L-1-i} S q_i + w sum_{j>=i} lam^{j-i} (q_i . k_j) v_j ),
+//   S  <- lam^L S + w sum_t lam^{t+1} v_t k_t^T.
+//
+// Products per chunk (M = N = 128, tcgen05, bf16 operands, fp32 accumulation):
+//   P  = Q K^T                       both from shared memory
+//   O  = [P~ | Q~] [V ; S]           A from tensor memory, 256 deep
+//   KV = W^T K                       A = the weighted V, transposed, from tensor memory
+// where Q~_i = 2^{e_i} q_i is exact (a power of two: lam^{i+1} = m_i 2^{e_i}, 1 <= m_i < 2),
+// P~_ij = (lam^{i-j} / m_i) P_ij is rounded to bf16 once, and the epilogue multiplies row i
+// by so m_i: every term has one rounded factor, P~ or the bf16 copy of S, beside the output's
+// own rounding.  A row factor on the state's part alone would cost a second accumulator or
+// a round trip of O; a rounded Q~ a second rounding.
+//
+// The state is held in fp32 registers.  W = w lam^{..} v is split exactly into three bf16
+// parts (8 + 8 + 8 bits of the fp32 product), so that KV has fp32 accuracy: two parts leave
+// 2^-18, which shows in the fp32 states.  KV is formed alone for each chunk and added in the
+// registers with one rounding: accumulating in tensor memory over a long sequence would add
+// up the tensor core's truncations.  lam^L is kept to 48 bits, for the same reason.
+//
+// Since the products of a chunk never wait for the state (only the S rows of O do), the
+// CTA's warps run as a pipeline over chunks: 4 warps turn P into P~ and build Q~, 4 warps
+// build W, 8 warps hold the state, publish its bf16 copy and write O, and one thread each
+// issues the loads and the three products.
+#include <stddef.h>
+#include <string.h>
+
+#include "gdn_epi.cuh"
+#include "gdn_linear.h"
+#include "gdn_tma.h"
+#include "gdn_umma.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace umma;
+
+constexpr int kC = 128;                     // tokens of a chunk
+constexpr uint32_t kHalf = kC * 128;        // a 128 x 64 bf16 sub-tile
+constexpr uint32_t kTile = 2 * kHalf;       // a 128 x 128 tile
+constexpr int kGroupP = 4, kGroupW = 4, kGroupS = 8;  // warps of the three groups
+constexpr int kWarpLoad = kGroupP + kGroupW + kGroupS;
+constexpr int kThreads = (kWarpLoad + 4) * 32;
+
+// Tensor-memory columns
+constexpr uint32_t kColP = 0;      // P fp32 [0, 128); then P~ [0, 64) and Q~ [64, 128)
+constexpr uint32_t kColW = 128;    // two buffers of 48: 32 tokens of W, three parts of 16
+constexpr uint32_t kColKV = 256;
+constexpr uint32_t kColO = 384;
+constexpr uint32_t kCols = 512;
+
+struct LinSmem {
+    unsigned char q[2][kTile], k[2][kTile], v[2][kTile];  // TMA tiles, two stages
+    unsigned char s[kTile];                               // bf16 copy of S, row r K-major
+    float wtab[2 * kC];   // w lam^{127-x} (forward) or w lam^{x+1} (reverse), zeros above 128
+    float ptab[32];       // decays inside a block of 32 columns of P
+    float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
+    uint64_t full[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2];
+    uint64_t p_done, pt_ready, kv_free, s_ready, o_free, drain[3];
+    uint32_t tmem_base;
+    int dead;
+};
+static_assert(offsetof(LinSmem, s) % 1024 == 0, "SW128 tiles on 1024-byte boundaries");
+static_assert(sizeof(LinSmem) + 1024 <= 232448, "one CTA per SM");
+
+struct LinMaps {
+    CUtensorMap q, k, v;
+};
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A bounded wait that also gives up once any role of the CTA has.
+__device__ __forceinline__ bool wait(LinSmem &sm, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*(volatile int *)&sm.dead || global_ns() - t0 > kWaitLimitNs) {
+            *(volatile int *)&sm.dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The same for a whole warp: every lane gets one answer, so that the warp stays together.
+__device__ __forceinline__ bool wait_warp(LinSmem &sm, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(sm, bar, parity));
+}
+
+struct Walk {      // the chunks of this CTA's sequence, in scan order
+    int t0, len, n;
+    __device__ __forceinline__ int start(int c, bool rev) const { return t0 + (rev ? n - 1 - c : c) * kC; }
+    __device__ __forceinline__ int length(int c, bool rev) const {
+        const int i = rev ? n - 1 - c : c;
+        return min(kC, len - i * kC);
+    }
+};
+
+// lam^{i+1} (forward) or lam^{L-1-i} (reverse) as 2^{e + f}, e whole and 0 <= f < 1.
+template <bool kReverse>
+__device__ __forceinline__ void read_power(float g2, int i, int L, float &e, float &f) {
+    const float x = g2 * (float)(kReverse ? max(L - 1 - i, 0) : i + 1);
+    e = floorf(x);
+    f = x - e;
+}
+
+template <bool kReverse>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_tc(const LinearArgs a, const __grid_constant__ LinMaps maps) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    LinSmem &sm = smem_struct<LinSmem>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hv = blockIdx.x % a.HV;
+    int n = blockIdx.x / a.HV;
+    if (a.N <= kLinearOrder) n = a.order[n];
+    Walk wk;
+    {
+        const int t0 = a.cu_dev[n], t1 = a.cu_dev[n + 1];
+        if (t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 > a.longest) {
+            if (tid == 0 && a.status) atomicOr(a.status, GDN_DEVICE_CU_SEQLENS_MISMATCH);
+            return;
+        }
+        wk.t0 = t0;
+        wk.len = t1 - t0;
+        wk.n = (wk.len + kC - 1) / kC;
+    }
+    const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
+    const float g2 = g * 1.4426950408889634f;
+
+    if (warp == kWarpLoad) {
+        tmem_alloc(&sm.tmem_base, kCols);
+        tmem_relinquish();
+        if (lane == 0) {
+            tma_prefetch_maps(maps);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sm.full[i], 1);
+                mbar_init(&sm.v_ok[i], kGroupW * 32);
+                mbar_init(&sm.w_ready[i], kGroupW * 32);
+                mbar_init(&sm.w_free[i], 1);
+                mbar_init(&sm.kv_done[i], 1);
+                mbar_init(&sm.o_done[i], 1);
+            }
+            mbar_init(&sm.p_done, 1);
+            mbar_init(&sm.pt_ready, kGroupP * 32);
+            mbar_init(&sm.kv_free, kGroupS * 32);
+            mbar_init(&sm.s_ready, kGroupS * 32);
+            mbar_init(&sm.o_free, kGroupS * 32);
+            for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
+            sm.dead = 0;
+            fence_mbar_init();
+        }
+    }
+    if (tid < kC) {
+        const int power = kReverse ? tid + 1 : kC - 1 - tid;
+        sm.wtab[tid] = a.w * exp2f(g2 * (float)power);
+        sm.wtab[kC + tid] = 0.f;
+        if (tid < 32) sm.ptab[tid] = exp2f(g2 * (float)(kReverse ? tid : 31 - tid));
+    } else if (tid == kC || tid == kC + 32) {
+        const int tail = wk.len % kC;
+        const double x = exp((double)g * (double)(tid == kC ? kC : tail));
+        (tid == kC ? sm.full_hi : sm.part_hi) = (float)x;
+        (tid == kC ? sm.full_lo : sm.part_lo) = (float)(x - (double)(float)x);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = sm.tmem_base;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+
+    if (warp < kGroupP) {
+        // ---------------------------------------------------------- P~ and Q~
+        const int i = tid;  // row
+        for (int c = 0; c < wk.n; ++c) {
+            const int L = wk.length(c, kReverse);
+            float e, f;
+            read_power<kReverse>(g2, i, L, e, f);
+            if (!wait_warp(sm, &sm.p_done, c & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {   // 32 columns j = 32 b + jj
+                float x[16];
+                uint32_t *u = reinterpret_cast<uint32_t *>(x);
+                const bool none = kReverse ? b < warp : b > warp;
+                if (none) {
+#pragma unroll
+                    for (int p = 0; p < 16; ++p) u[p] = 0u;
+                } else {
+                    float r[32];
+                    tmem_ld32(tb + lanes + kColP + 32 * b, r);
+                    tmem_ld_wait();
+                    if (b == warp) {
+#pragma unroll
+                        for (int jj = 0; jj < 32; ++jj) {
+                            const int d = kReverse ? jj - lane : lane - jj;
+                            const float y = r[jj] * (a.w * ex2(fmaf(g2, (float)d, -f)));
+                            r[jj] = d >= 0 ? y : 0.f;
+                        }
+                    } else {
+                        const float row = a.w * ex2(fmaf(g2, (float)(kReverse ? 32 * b - i : i - 32 * b - 31), -f));
+#pragma unroll
+                        for (int jj = 0; jj < 32; ++jj) r[jj] *= row * sm.ptab[jj];
+                    }
+                    if (kReverse && L < kC) {
+#pragma unroll
+                        for (int jj = 0; jj < 32; ++jj) r[jj] = 32 * b + jj < L ? r[jj] : 0.f;
+                    }
+#pragma unroll
+                    for (int p = 0; p < 16; ++p) u[p] = epi::pack_bf2(r[2 * p], r[2 * p + 1]);
+                }
+                // the columns written lie in blocks already read
+                tmem_st16(tb + lanes + kColP + 16 * b, x);
+            }
+            const unsigned char *qt = sm.q[c & 1];
+            const __nv_bfloat162 pw = __float2bfloat162_rn(
+                e < -120.f ? 0.f : __int_as_float(((int)e + 127) << 23));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[32];
+                uint32_t *u = reinterpret_cast<uint32_t *>(x);
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const uint4 z = *reinterpret_cast<const uint4 *>(qt + h * kHalf + sw128_off(i, 8 * p));
+                    const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&zz[y]), pw);
+                        u[4 * p + y] = *reinterpret_cast<const uint32_t *>(&t);
+                    }
+                }
+                tmem_st32(tb + lanes + kColP + 64 + 32 * h, x);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sm.pt_ready);
+        }
+    } else if (warp < kGroupP + kGroupW) {
+        // ---------------------------------------------------------- W
+        const int r = tid - kGroupP * 32;   // feature of v
+        bool ok = true;
+        for (int c = 0; c < wk.n && ok; ++c) {
+            const int s = c & 1, L = wk.length(c, kReverse);
+            if (!(ok = wait_warp(sm, &sm.full[s], (c >> 1) & 1))) break;
+            if (L < kC) {
+                // rows past the sequence hold the next one's tokens: zeros instead
+                for (int x = r; x < (kC - L) * 16; x += kGroupW * 32) {
+                    const int row = L + (x >> 4), h = (x >> 3) & 1;
+                    const uint32_t at = h * kHalf + sw128_off(row, 8 * (x & 7));
+                    *reinterpret_cast<uint4 *>(sm.k[s] + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(sm.v[s] + at) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(&sm.v_ok[s]);
+            const unsigned char *vt = sm.v[s] + (r >> 6) * kHalf;
+            const float *wt = sm.wtab + (kReverse ? 0 : kC - L);
+            for (int qd = 0; qd < 4; ++qd) {
+                const int b = qd & 1, use = 2 * c + (qd >> 1);
+                float hi[16], mid[16], lo[16];
+                uint32_t *uh = reinterpret_cast<uint32_t *>(hi), *um = reinterpret_cast<uint32_t *>(mid),
+                         *ul = reinterpret_cast<uint32_t *>(lo);
+#pragma unroll
+                for (int p = 0; p < 16; ++p) {
+                    const int t = 32 * qd + 2 * p;
+                    float x[2], y[2], z[2];
+#pragma unroll
+                    for (int y2 = 0; y2 < 2; ++y2) {
+                        const uint32_t bits =
+                            *reinterpret_cast<const unsigned short *>(vt + sw128_off(t + y2, r & 63));
+                        x[y2] = t + y2 < L ? wt[t + y2] * __uint_as_float(bits << 16) : 0.f;
+                        y[y2] = x[y2] - __uint_as_float(__float_as_uint(x[y2]) & 0xffff0000u);
+                        z[y2] = y[y2] - __uint_as_float(__float_as_uint(y[y2]) & 0xffff0000u);
+                    }
+                    uh[p] = __byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632);
+                    um[p] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
+                    ul[p] = __byte_perm(__float_as_uint(z[0]), __float_as_uint(z[1]), 0x7632);
+                }
+                if (use > 0 && !(ok = wait_warp(sm, &sm.w_free[b], (use - 1) & 1))) break;
+                tc_fence_after();
+                const uint32_t at = tb + lanes + kColW + 48 * b;
+                tmem_st16(at, hi);
+                tmem_st16(at + 16, mid);
+                tmem_st16(at + 32, lo);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.w_ready[b]);
+            }
+        }
+    } else if (warp < kWarpLoad) {
+        // ---------------------------------------------------------- state and output
+        const int x0 = warp - kGroupP - kGroupW;
+        const int r = (warp & 3) * 32 + lane, col = (x0 >> 2) * 64;  // row of S and of O; columns
+        const float *src = a.s0 ? a.s0 + ((size_t)n * a.HV + hv) * kDim * kDim : nullptr;
+        float *dst = a.s1 ? a.s1 + ((size_t)n * a.HV + hv) * kDim * kDim : nullptr;
+        if (a.pool) {
+            const int slot = a.pool_idx[n];
+            if (slot >= a.num_slots && r == 0 && a.pool_status) *a.pool_status = 1;
+            if (slot > 0 && slot < a.num_slots) {
+                dst = a.pool + ((size_t)slot * a.HV + hv) * kDim * kDim;
+                src = (!a.pool_resume || a.pool_resume[n]) ? dst : nullptr;
+            }
+        }
+        float st[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) st[j] = 0.f;
+        if (src) {
+            if (a.s_cs == 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float4 z = *reinterpret_cast<const float4 *>(src + (size_t)r * kDim + col + 4 * j);
+                    st[4 * j] = z.x;
+                    st[4 * j + 1] = z.y;
+                    st[4 * j + 2] = z.z;
+                    st[4 * j + 3] = z.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) st[j] = src[(size_t)(col + j) * kDim + r];
+            }
+        }
+        unsigned char *srow = sm.s + (col >> 6) * kHalf;
+        auto publish = [&]() {
+            epi::put_row32(srow, r, 0, st);
+            epi::put_row32(srow, r, 32, st + 32);
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.s_ready);
+        };
+        if (wk.n > 0) publish();
+        for (int c = 0; c < wk.n; ++c) {
+            const int s = c & 1, L = wk.length(c, kReverse);
+            const float fh = L < kC ? sm.part_hi : sm.full_hi, fl = L < kC ? sm.part_lo : sm.full_lo;
+            if (!wait_warp(sm, &sm.kv_done[s], (c >> 1) & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                float x[16];
+                tmem_ld16(tb + lanes + kColKV + col + 16 * h, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    st[16 * h + j] = fmaf(st[16 * h + j], fh, fmaf(st[16 * h + j], fl, x[j]));
+            }
+            tc_fence_before();
+            mbar_arrive(&sm.kv_free);
+            if (!wait_warp(sm, &sm.o_done[s], (c >> 1) & 1)) break;
+            tc_fence_after();
+            if (c + 1 < wk.n) publish();
+            float e, f;
+            read_power<kReverse>(g2, r, L, e, f);
+            const float scale = a.so * ex2(f);
+            const size_t t = (size_t)wk.start(c, kReverse) + r;
+            const size_t row = (t * a.HV + hv) * kDim + col;
+            const bool mine = r < L && in_range(row, 64, (long long)a.T * a.HV * kDim, a.status);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                float x[16];
+                tmem_ld16(tb + lanes + kColO + col + 16 * h, x);
+                tmem_ld_wait();
+                if (mine && a.part) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4 *>(a.part + row + 16 * h + 4 * j) = make_float4(
+                            scale * x[4 * j], scale * x[4 * j + 1], scale * x[4 * j + 2], scale * x[4 * j + 3]);
+                } else if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<uint4 *>(a.o + row + 16 * h + 8 * j) = make_uint4(
+                            epi::pack_bf2(scale * x[8 * j], scale * x[8 * j + 1]),
+                            epi::pack_bf2(scale * x[8 * j + 2], scale * x[8 * j + 3]),
+                            epi::pack_bf2(scale * x[8 * j + 4], scale * x[8 * j + 5]),
+                            epi::pack_bf2(scale * x[8 * j + 6], scale * x[8 * j + 7]));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&sm.o_free);
+        }
+        if (dst && !*(volatile int *)&sm.dead) {
+            if (a.s_cs == 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    *reinterpret_cast<float4 *>(dst + (size_t)r * kDim + col + 4 * j) =
+                        make_float4(st[4 * j], st[4 * j + 1], st[4 * j + 2], st[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) dst[(size_t)(col + j) * kDim + r] = st[j];
+            }
+        }
+    } else if (lane == 0) {
+        const int role = warp - kWarpLoad;
+        if (role == 0) {
+            // ------------------------------------------------------ loads
+            const int hq = hv / (a.HV / a.nq), hk = hv / (a.HV / a.nk), hw = hv / (a.HV / a.nv);
+            int issued = 0;
+            for (int c = 0; c < wk.n; ++c) {
+                const int s = c & 1, t = wk.start(c, kReverse);
+                if (c >= 2 && (!wait(sm, &sm.o_done[s], ((c >> 1) - 1) & 1) ||
+                               !wait(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
+                    break;
+                mbar_arrive_expect_tx(&sm.full[s], 3 * kTile);
+                for (int h = 0; h < 2; ++h) {
+                    tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full[s]);
+                    tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full[s]);
+                }
+                for (int h = 0; h < 2; ++h) tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full[s]);
+                issued = c + 1;
+            }
+            // copies still in flight write this CTA's shared memory: wait for them (bounded)
+            for (int c = max(0, issued - 2); c < issued; ++c)
+                mbar_wait(&sm.full[c & 1], (c >> 1) & 1, kDrainLimitNs);
+        } else if (role == 1) {
+            // ------------------------------------------------------ P = Q K^T
+            const uint32_t id = idesc_bf16(128, 128, 0, 0);
+            for (int c = 0; c < wk.n; ++c) {
+                const int s = c & 1;
+                if (!wait(sm, &sm.full[s], (c >> 1) & 1)) break;
+                if (c > 0 && !wait(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1)) break;
+                tc_fence_after();
+                const uint32_t qs = smem_u32(sm.q[s]), ks = smem_u32(sm.k[s]);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t off = (x >> 2) * kHalf + (x & 3) * 32;
+                    mma_bf16(tb + kColP, sdesc(qs + off, 16, 1024), sdesc(ks + off, 16, 1024), id, x > 0);
+                }
+                mma_commit(&sm.p_done);
+            }
+        } else if (role == 2) {
+            // ------------------------------------------------------ O = [P~ | Q~] [V ; S]
+            const uint32_t idv = idesc_bf16(128, 128, 0, 1), ids = idesc_bf16(128, 128, 0, 0);
+            for (int c = 0; c < wk.n; ++c) {
+                const int s = c & 1;
+                if (!wait(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait(sm, &sm.s_ready, c & 1) ||
+                    !wait(sm, &sm.pt_ready, c & 1))
+                    break;
+                if (c > 0 && !wait(sm, &sm.o_free, (c - 1) & 1)) break;
+                tc_fence_after();
+                const uint32_t vs = smem_u32(sm.v[s]), ss = smem_u32(sm.s);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mma_ts(tb + kColO, tb + kColP + 64 + 8 * x,
+                           sdesc(ss + (x >> 2) * kHalf + (x & 3) * 32, 16, 1024), ids, x > 0);
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    mma_ts(tb + kColO, tb + kColP + 8 * x, sdesc(vs + x * 2048, kHalf, 1024), idv, true);
+                mma_commit(&sm.o_done[s]);
+            }
+        } else {
+            // ------------------------------------------------------ KV = W^T K
+            const uint32_t id = idesc_bf16(128, 128, 0, 1);
+            bool ok = true;
+            for (int c = 0; c < wk.n && ok; ++c) {
+                const int s = c & 1;
+                if (c > 0 && !wait(sm, &sm.kv_free, (c - 1) & 1)) break;
+                const uint32_t ks = smem_u32(sm.k[s]);
+                for (int qd = 0; qd < 4; ++qd) {
+                    const int b = qd & 1, use = 2 * c + (qd >> 1);
+                    if (!(ok = wait(sm, &sm.w_ready[b], use & 1))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint64_t bd = sdesc(ks + (2 * qd + x) * 2048, kHalf, 1024);
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+                            mma_ts(tb + kColKV, tb + kColW + 48 * b + 16 * part + 8 * x, bd, id,
+                                   qd > 0 || x > 0 || part > 0);
+                    }
+                    mma_commit(&sm.w_free[b]);
+                }
+                if (ok) mma_commit(&sm.kv_done[s]);
+            }
+        }
+        if (role > 0 && *(volatile int *)&sm.dead) {
+            // products in flight read tiles and tensor memory: wait for them (bounded)
+            mma_commit(&sm.drain[role - 1]);
+            mbar_wait(&sm.drain[role - 1], 0, kDrainLimitNs);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && sm.dead && a.status) atomicOr(a.status, GDN_DEVICE_WAIT_TIMEOUT);
+    if (warp == kWarpLoad) tmem_dealloc(tb, kCols);
+}
+
+template <bool kReverse>
+cudaError_t launch_dir(const LinearArgs &a, cudaStream_t s) {
+    const int smem = (int)sizeof(LinSmem) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_linear_tc<kReverse>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // (the call above has made the device's context current, which the encoder needs)
+    LinMaps m;
+    memset(&m, 0, sizeof(m));
+    if (a.T > 0) {
+        const uint64_t rowb = kDim * sizeof(bf16);
+        if (!encode_rows_bf16(&m.q, a.q, a.nq, a.T, rowb, rowb * a.nq, kC) ||
+            !encode_rows_bf16(&m.k, a.k, a.nk, a.T, rowb, rowb * a.nk, kC) ||
+            !encode_rows_bf16(&m.v, a.v, a.nv, a.T, rowb, rowb * a.nv, kC))
+            return cudaErrorInvalidValue;
+    }
+    k_linear_tc<kReverse><<<(unsigned)(a.N * a.HV), kThreads, smem, s>>>(a, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s) {
+    return a.reverse ? launch_dir<true>(a, s) : launch_dir<false>(a, s);
+}
+
+}  // namespace gdn

@@ -26,7 +26,7 @@
 // up the tensor core's truncations.  lam^L is kept to 48 bits, for the same reason.
 //
 // Since the products of a chunk never wait for the state (only the S rows of O do), the
-// CTA's warps run as a pipeline over chunks: 4 warps turn P into P~ and build Q~, 4 warps
+// CTA's warps run as a pipeline over chunks: 8 warps turn P into P~ and build Q~, 8 warps
 // build W, 8 warps hold the state, publish its bf16 copy and write O, and one thread each
 // issues the loads and the three products.
 #include <stddef.h>
@@ -45,12 +45,20 @@ using namespace umma;
 constexpr int kC = 128;                     // tokens of a chunk
 constexpr uint32_t kHalf = kC * 128;        // a 128 x 64 bf16 sub-tile
 constexpr uint32_t kTile = 2 * kHalf;       // a 128 x 128 tile
-constexpr int kGroupP = 4, kGroupW = 4, kGroupS = 8;  // warps of the three groups
+constexpr int kGroupP = 8, kGroupW = 8, kGroupS = 8;  // warps of the three groups
 constexpr int kWarpLoad = kGroupP + kGroupW + kGroupS;
 constexpr int kThreads = (kWarpLoad + 4) * 32;
 
+// Registers a thread: the state's warps hold 64 floats each.  The groups' shares must not
+// exceed what the launch gives (kThreads * kRegsLaunch), or the increase would never end.
+constexpr int kRegsLaunch = 72, kRegsWork = 56, kRegsState = 120, kRegsIssue = 40;
+static_assert((kGroupP + kGroupW) * kRegsWork + kGroupS * kRegsState + 4 * kRegsIssue <=
+                  (kWarpLoad + 4) * kRegsLaunch,
+              "register shares");
+
 // Tensor-memory columns
-constexpr uint32_t kColP = 0;      // P fp32 [0, 128); then P~ [0, 64) and Q~ [64, 128)
+constexpr uint32_t kColP = 0;      // P fp32 [0, 128); then, per half h of 64: P~ of tokens 64 h ..
+                                   // in 32 columns and Q~ of features 64 h .. in the next 32
 constexpr uint32_t kColW = 128;    // two buffers of 48: 32 tokens of W, three parts of 16
 constexpr uint32_t kColKV = 256;
 constexpr uint32_t kColO = 384;
@@ -62,8 +70,8 @@ struct LinSmem {
     float wtab[2 * kC];   // w lam^{127-x} (forward) or w lam^{x+1} (reverse), zeros above 128
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2];
-    uint64_t p_done, pt_ready, kv_free, s_ready, o_free, drain[3];
+    uint64_t full[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
+    uint64_t p_done, pt_ready, kv_free, s_ready, o_free, o_staged, drain[3];
     uint32_t tmem_base;
     int dead;
 };
@@ -71,7 +79,7 @@ static_assert(offsetof(LinSmem, s) % 1024 == 0, "SW128 tiles on 1024-byte bounda
 static_assert(sizeof(LinSmem) + 1024 <= 232448, "one CTA per SM");
 
 struct LinMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool acc) {
@@ -81,23 +89,91 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, u
         "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
+// Descriptor offset (16-byte units) of the x-th 16-deep step of a K-major tile.
+__device__ __forceinline__ constexpr uint64_t k_step(int x) { return ((x >> 2) * kHalf + (x & 3) * 32) >> 4; }
+
+// Column of the x-th 16-deep step of P~ (Q~: 32 further on).
+__device__ __forceinline__ constexpr uint32_t a_step(int x) { return kColP + 64 * (x >> 2) + 8 * (x & 3); }
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// A bounded wait that also gives up once any role of the CTA has.
+// Two fp32 at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t x;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t x;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t x;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+    return x;
+}
+// The upper 16 bits of both halves: a bf16 pair by truncation (the even token in the low half).
+__device__ __forceinline__ uint32_t tops(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+__device__ __forceinline__ uint64_t keep_tops(float2 x) {
+    return pair(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+}
+
+// Four 8 x 8 bf16 matrices of shared rows, each transposed: register m of lane l holds
+// (row 2 (l % 4) + {0, 1}, column l / 4) of matrix m, whose rows lanes 8 m .. 8 m + 7 point at.
+__device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 lanes x 16 columns: register 2 k + e of lane t goes to lane t / 4 + 8 e, column 4 k + t % 4.
+__device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t (&u)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A bounded wait that also gives up once any role of the CTA has.  The timer and the flag
+// are looked at every 32 polls only: the timer's reads are slow.
 __device__ __forceinline__ bool wait(LinSmem &sm, uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*(volatile int *)&sm.dead || global_ns() - t0 > kWaitLimitNs) {
+    uint64_t t0 = 0;
+    for (uint32_t polls = 1;; ++polls) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (polls % 32) continue;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (*(volatile int *)&sm.dead || now - t0 > kWaitLimitNs) {
             *(volatile int *)&sm.dead = 1;
             return false;
         }
     }
-    return true;
 }
 
 // The same for a whole warp: every lane gets one answer, so that the warp stays together.
@@ -153,16 +229,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sm.full[i], 1);
                 mbar_init(&sm.v_ok[i], kGroupW * 32);
-                mbar_init(&sm.w_ready[i], kGroupW * 32);
+                mbar_init(&sm.w_ready[i], kGroupW * 16);
                 mbar_init(&sm.w_free[i], 1);
                 mbar_init(&sm.kv_done[i], 1);
                 mbar_init(&sm.o_done[i], 1);
+                mbar_init(&sm.q_free[i], 1);
             }
             mbar_init(&sm.p_done, 1);
             mbar_init(&sm.pt_ready, kGroupP * 32);
             mbar_init(&sm.kv_free, kGroupS * 32);
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
+            mbar_init(&sm.o_staged, kGroupS * 32);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
@@ -187,36 +265,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kGroupP) {
         // ---------------------------------------------------------- P~ and Q~
-        const int i = tid;  // row
+        regs_down<kRegsWork>();
+        const int quad = warp & 3, half = warp >> 2;   // rows 32 quad .., columns 64 half ..
+        const int i = quad * 32 + lane;
+        const float at = (float)lane, lw = log2f(a.w);   // w > 0
+        const uint32_t mine = tb + lanes + kColP + 64 * half;
         for (int c = 0; c < wk.n; ++c) {
             const int L = wk.length(c, kReverse);
             float e, f;
             read_power<kReverse>(g2, i, L, e, f);
             if (!wait_warp(sm, &sm.p_done, c & 1)) break;
             tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {   // 32 columns j = 32 b + jj
+#pragma unroll 1
+            for (int b2 = 0; b2 < 2; ++b2) {   // columns j = 32 b + jj
+                const int b = 2 * half + b2;
                 float x[16];
                 uint32_t *u = reinterpret_cast<uint32_t *>(x);
-                const bool none = kReverse ? b < warp : b > warp;
-                if (none) {
+                if (kReverse ? b < quad : b > quad) {
 #pragma unroll
                     for (int p = 0; p < 16; ++p) u[p] = 0u;
                 } else {
                     float r[32];
-                    tmem_ld32(tb + lanes + kColP + 32 * b, r);
+                    tmem_ld32(mine + 32 * b2, r);
                     tmem_ld_wait();
-                    if (b == warp) {
+                    if (b == quad) {
 #pragma unroll
                         for (int jj = 0; jj < 32; ++jj) {
-                            const int d = kReverse ? jj - lane : lane - jj;
-                            const float y = r[jj] * (a.w * ex2(fmaf(g2, (float)d, -f)));
-                            r[jj] = d >= 0 ? y : 0.f;
+                            const float d = kReverse ? (float)jj - at : at - (float)jj;
+                            const float y = r[jj] * ex2(fmaf(g2, d, lw - f));
+                            r[jj] = d >= 0.f ? y : 0.f;
                         }
                     } else {
-                        const float row = a.w * ex2(fmaf(g2, (float)(kReverse ? 32 * b - i : i - 32 * b - 31), -f));
+                        const float row = ex2(fmaf(g2, (float)(kReverse ? 32 * b - i : i - 32 * b - 31), lw - f));
+                        const uint64_t row2 = pair(row, row);
 #pragma unroll
-                        for (int jj = 0; jj < 32; ++jj) r[jj] *= row * sm.ptab[jj];
+                        for (int jj = 0; jj < 32; jj += 4) {
+                            const float4 t = *reinterpret_cast<const float4 *>(&sm.ptab[jj]);
+                            const float2 y = unpair(mul2(pair(r[jj], r[jj + 1]), mul2(row2, pair(t.x, t.y))));
+                            const float2 z = unpair(mul2(pair(r[jj + 2], r[jj + 3]), mul2(row2, pair(t.z, t.w))));
+                            r[jj] = y.x;
+                            r[jj + 1] = y.y;
+                            r[jj + 2] = z.x;
+                            r[jj + 3] = z.y;
+                        }
                     }
                     if (kReverse && L < kC) {
 #pragma unroll
@@ -225,43 +316,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int p = 0; p < 16; ++p) u[p] = epi::pack_bf2(r[2 * p], r[2 * p + 1]);
                 }
-                // the columns written lie in blocks already read
-                tmem_st16(tb + lanes + kColP + 16 * b, x);
+                tmem_st16(mine + 16 * b2, x);   // over columns that this warp has read
             }
-            const unsigned char *qt = sm.q[c & 1];
+            const unsigned char *qt = sm.q[c & 1] + half * kHalf;
             const __nv_bfloat162 pw = __float2bfloat162_rn(
                 e < -120.f ? 0.f : __int_as_float(((int)e + 127) << 23));
+            float x[32];
+            uint32_t *u = reinterpret_cast<uint32_t *>(x);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                uint32_t *u = reinterpret_cast<uint32_t *>(x);
+            for (int p = 0; p < 8; ++p) {
+                const uint4 z = *reinterpret_cast<const uint4 *>(qt + sw128_off(i, 8 * p));
+                const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const uint4 z = *reinterpret_cast<const uint4 *>(qt + h * kHalf + sw128_off(i, 8 * p));
-                    const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&zz[y]), pw);
-                        u[4 * p + y] = *reinterpret_cast<const uint32_t *>(&t);
-                    }
+                for (int y = 0; y < 4; ++y) {
+                    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&zz[y]), pw);
+                    u[4 * p + y] = *reinterpret_cast<const uint32_t *>(&t);
                 }
-                tmem_st32(tb + lanes + kColP + 64 + 32 * h, x);
             }
+            tmem_st32(mine + 32, x);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.pt_ready);
         }
     } else if (warp < kGroupP + kGroupW) {
         // ---------------------------------------------------------- W
-        const int r = tid - kGroupP * 32;   // feature of v
+        // Half h of the group fills buffer h with the 32-token quarters h and h + 2.
+        regs_down<kRegsWork>();
+        const int quad = warp & 3, half = (warp - kGroupP) >> 2;
+        const uint32_t buf = tb + lanes + kColW + 48 * half;
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
             if (!(ok = wait_warp(sm, &sm.full[s], (c >> 1) & 1))) break;
             if (L < kC) {
-                // rows past the sequence hold the next one's tokens: zeros instead
-                for (int x = r; x < (kC - L) * 16; x += kGroupW * 32) {
-                    const int row = L + (x >> 4), h = (x >> 3) & 1;
+                // rows past the sequence hold the next one's tokens: zeros instead (each half
+                // clears its own quarters of K, which the product of a quarter waits for)
+                for (int x = quad * 32 + lane; x < 2 * 32 * 16; x += kGroupW * 16) {
+                    const int y = x >> 4, row = (y >> 5) * 64 + half * 32 + (y & 31), h = (x >> 3) & 1;
+                    if (row < L) continue;
                     const uint32_t at = h * kHalf + sw128_off(row, 8 * (x & 7));
                     *reinterpret_cast<uint4 *>(sm.k[s] + at) = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4 *>(sm.v[s] + at) = make_uint4(0, 0, 0, 0);
@@ -269,42 +361,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
             }
             mbar_arrive(&sm.v_ok[s]);
-            const unsigned char *vt = sm.v[s] + (r >> 6) * kHalf;
-            const float *wt = sm.wtab + (kReverse ? 0 : kC - L);
-            for (int qd = 0; qd < 4; ++qd) {
-                const int b = qd & 1, use = 2 * c + (qd >> 1);
-                float hi[16], mid[16], lo[16];
-                uint32_t *uh = reinterpret_cast<uint32_t *>(hi), *um = reinterpret_cast<uint32_t *>(mid),
-                         *ul = reinterpret_cast<uint32_t *>(lo);
-#pragma unroll
-                for (int p = 0; p < 16; ++p) {
-                    const int t = 32 * qd + 2 * p;
-                    float x[2], y[2], z[2];
-#pragma unroll
-                    for (int y2 = 0; y2 < 2; ++y2) {
-                        const uint32_t bits =
-                            *reinterpret_cast<const unsigned short *>(vt + sw128_off(t + y2, r & 63));
-                        x[y2] = t + y2 < L ? wt[t + y2] * __uint_as_float(bits << 16) : 0.f;
-                        y[y2] = x[y2] - __uint_as_float(__float_as_uint(x[y2]) & 0xffff0000u);
-                        z[y2] = y[y2] - __uint_as_float(__float_as_uint(y[y2]) & 0xffff0000u);
-                    }
-                    uh[p] = __byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632);
-                    um[p] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
-                    ul[p] = __byte_perm(__float_as_uint(z[0]), __float_as_uint(z[1]), 0x7632);
-                }
-                if (use > 0 && !(ok = wait_warp(sm, &sm.w_free[b], (use - 1) & 1))) break;
+            const float *wt = sm.wtab + (kReverse ? 0 : kC - L) + 2 * (lane & 3);
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                const int t0 = 64 * pass + 32 * half, use = 2 * c + pass;
+                if (use > 0 && !(ok = wait_warp(sm, &sm.w_free[half], (use - 1) & 1))) break;
                 tc_fence_after();
-                const uint32_t at = tb + lanes + kColW + 48 * b;
-                tmem_st16(at, hi);
-                tmem_st16(at + 16, mid);
-                tmem_st16(at + 32, lo);
+#pragma unroll 1
+                for (int g16 = 0; g16 < 2; ++g16) {   // features 32 quad + 16 g16 ..
+                    const int r0 = 32 * quad + 16 * g16;
+                    const uint32_t base = smem_u32(sm.v[s] + (r0 >> 6) * kHalf);
+                    uint32_t in[2][4], hi[8], mid[8], lo[8];
+                    ldmatrix4t(base + sw128_off(t0 + lane, r0 & 63), in[0]);
+                    ldmatrix4t(base + sw128_off(t0 + lane, (r0 + 8) & 63), in[1]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int t = t0 + 8 * k + 2 * (lane & 3);
+                        const uint64_t w2 = pair(wt[t0 + 8 * k], wt[t0 + 8 * k + 1]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t v2 = in[e][k];
+                            if (L < kC) v2 &= t + 1 < L ? 0xffffffffu : t < L ? 0xffffu : 0u;
+                            const float2 x = unpair(mul2(w2, pair(__uint_as_float(v2 << 16),
+                                                                  __uint_as_float(v2 & 0xffff0000u))));
+                            const float2 y = unpair(sub2(pair(x.x, x.y), keep_tops(x)));
+                            const float2 z = unpair(sub2(pair(y.x, y.y), keep_tops(y)));
+                            hi[2 * k + e] = tops(x);
+                            mid[2 * k + e] = tops(y);
+                            lo[2 * k + e] = tops(z);
+                        }
+                    }
+                    const uint32_t at = buf + ((uint32_t)(16 * g16) << 16);
+                    tmem_st16x128_x4(at, hi);
+                    tmem_st16x128_x4(at + 16, mid);
+                    tmem_st16x128_x4(at + 32, lo);
+                }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&sm.w_ready[b]);
+                mbar_arrive(&sm.w_ready[half]);
             }
         }
     } else if (warp < kWarpLoad) {
         // ---------------------------------------------------------- state and output
+        regs_up<kRegsState>();
         const int x0 = warp - kGroupP - kGroupW;
         const int r = (warp & 3) * 32 + lane, col = (x0 >> 2) * 64;  // row of S and of O; columns
         const float *src = a.s0 ? a.s0 + ((size_t)n * a.HV + hv) * kDim * kDim : nullptr;
@@ -343,8 +442,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sm.s_ready);
         };
         if (wk.n > 0) publish();
+        int stores = 0;
+        const bool storer = tid == (kGroupP + kGroupW) * 32;
         for (int c = 0; c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
+            if (storer && c > 0) {   // the last chunk's output has left its stage's Q tile
+                tma_store_wait_read();
+                mbar_arrive(&sm.q_free[s ^ 1]);
+            }
             const float fh = L < kC ? sm.part_hi : sm.full_hi, fl = L < kC ? sm.part_lo : sm.full_lo;
             if (!wait_warp(sm, &sm.kv_done[s], (c >> 1) & 1)) break;
             tc_fence_after();
@@ -354,8 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld16(tb + lanes + kColKV + col + 16 * h, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    st[16 * h + j] = fmaf(st[16 * h + j], fh, fmaf(st[16 * h + j], fl, x[j]));
+                for (int j = 0; j < 16; j += 2) {
+                    const uint64_t y = pair(st[16 * h + j], st[16 * h + j + 1]);
+                    const float2 z = unpair(fma2(y, pair(fh, fh), fma2(y, pair(fl, fl), pair(x[j], x[j + 1]))));
+                    st[16 * h + j] = z.x;
+                    st[16 * h + j + 1] = z.y;
+                }
             }
             tc_fence_before();
             mbar_arrive(&sm.kv_free);
@@ -367,30 +476,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float scale = a.so * ex2(f);
             const size_t t = (size_t)wk.start(c, kReverse) + r;
             const size_t row = (t * a.HV + hv) * kDim + col;
+            const bool staged = L == kC && !a.part;   // whole chunks of bf16 leave by TMA
             const bool mine = r < L && in_range(row, 64, (long long)a.T * a.HV * kDim, a.status);
-#pragma unroll
+            // the stage's Q tile is free: its readers finished before O did
+            unsigned char *orow = sm.q[s] + (col >> 6) * kHalf;
+#pragma unroll 1
             for (int h = 0; h < 4; ++h) {
                 float x[16];
                 tmem_ld16(tb + lanes + kColO + col + 16 * h, x);
                 tmem_ld_wait();
-                if (mine && a.part) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4 *>(a.part + row + 16 * h + 4 * j) = make_float4(
-                            scale * x[4 * j], scale * x[4 * j + 1], scale * x[4 * j + 2], scale * x[4 * j + 3]);
-                } else if (mine) {
+                for (int j = 0; j < 16; ++j) x[j] *= scale;
+                if (a.part) {
+                    if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<uint4 *>(a.o + row + 16 * h + 8 * j) = make_uint4(
-                            epi::pack_bf2(scale * x[8 * j], scale * x[8 * j + 1]),
-                            epi::pack_bf2(scale * x[8 * j + 2], scale * x[8 * j + 3]),
-                            epi::pack_bf2(scale * x[8 * j + 4], scale * x[8 * j + 5]),
-                            epi::pack_bf2(scale * x[8 * j + 6], scale * x[8 * j + 7]));
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4 *>(a.part + row + 16 * h + 4 * j) =
+                                make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 y = make_uint4(
+                            epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
+                            epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
+                        if (staged) *reinterpret_cast<uint4 *>(orow + sw128_off(r, 16 * h + 8 * j)) = y;
+                        else if (mine) *reinterpret_cast<uint4 *>(a.o + row + 16 * h + 8 * j) = y;
+                    }
                 }
+            }
+            if (staged) {
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.o_staged);
             }
             tc_fence_before();
             mbar_arrive(&sm.o_free);
+            if (staged) {
+                stores += 1;
+                if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1)) {
+                    for (int h = 0; h < 2; ++h)
+                        tma_store_3d(&maps.o, 64 * h, hv, wk.start(c, kReverse), sm.q[s] + h * kHalf);
+                    tma_store_commit();
+                }
+                __syncwarp();
+            }
         }
+        if (storer) tma_store_wait_all();
         if (dst && !*(volatile int *)&sm.dead) {
             if (a.s_cs == 1) {
 #pragma unroll
@@ -402,7 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 64; ++j) dst[(size_t)(col + j) * kDim + r] = st[j];
             }
         }
-    } else if (lane == 0) {
+    } else {
+      regs_down<kRegsIssue>();
+      if (lane == 0) {
         const int role = warp - kWarpLoad;
         if (role == 0) {
             // ------------------------------------------------------ loads
@@ -414,12 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                !wait(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
                     break;
                 mbar_arrive_expect_tx(&sm.full[s], 3 * kTile);
+                issued = c + 1;
                 for (int h = 0; h < 2; ++h) {
                     tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full[s]);
-                    tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full[s]);
+                    tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full[s]);
                 }
-                for (int h = 0; h < 2; ++h) tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full[s]);
-                issued = c + 1;
+                if (c >= 2 && !wait(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
+                for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full[s]);
             }
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
             for (int c = max(0, issued - 2); c < issued; ++c)
@@ -427,22 +561,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (role == 1) {
             // ------------------------------------------------------ P = Q K^T
             const uint32_t id = idesc_bf16(128, 128, 0, 0);
+            const uint64_t qd0 = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait(sm, &sm.full[s], (c >> 1) & 1)) break;
                 if (c > 0 && !wait(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1)) break;
                 tc_fence_after();
-                const uint32_t qs = smem_u32(sm.q[s]), ks = smem_u32(sm.k[s]);
+                const uint64_t qd = qd0 + ((s * kTile) >> 4), kd = kd0 + ((s * kTile) >> 4);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const uint32_t off = (x >> 2) * kHalf + (x & 3) * 32;
-                    mma_bf16(tb + kColP, sdesc(qs + off, 16, 1024), sdesc(ks + off, 16, 1024), id, x > 0);
-                }
+                for (int x = 0; x < 8; ++x) mma_bf16(tb + kColP, qd + k_step(x), kd + k_step(x), id, x > 0);
                 mma_commit(&sm.p_done);
             }
         } else if (role == 2) {
             // ------------------------------------------------------ O = [P~ | Q~] [V ; S]
             const uint32_t idv = idesc_bf16(128, 128, 0, 1), ids = idesc_bf16(128, 128, 0, 0);
+            const uint64_t vd0 = sdesc(smem_u32(sm.v), kHalf, 1024), sd0 = sdesc(smem_u32(sm.s), 16, 1024);
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait(sm, &sm.s_ready, c & 1) ||
@@ -450,35 +583,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 if (c > 0 && !wait(sm, &sm.o_free, (c - 1) & 1)) break;
                 tc_fence_after();
-                const uint32_t vs = smem_u32(sm.v[s]), ss = smem_u32(sm.s);
+                const uint64_t vd = vd0 + ((s * kTile) >> 4);
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    mma_ts(tb + kColO, tb + kColP + 64 + 8 * x,
-                           sdesc(ss + (x >> 2) * kHalf + (x & 3) * 32, 16, 1024), ids, x > 0);
+                    mma_ts(tb + kColO, tb + a_step(x) + 32, sd0 + k_step(x), ids, x > 0);
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    mma_ts(tb + kColO, tb + kColP + 8 * x, sdesc(vs + x * 2048, kHalf, 1024), idv, true);
+                for (int x = 0; x < 8; ++x) mma_ts(tb + kColO, tb + a_step(x), vd + 128 * x, idv, true);
                 mma_commit(&sm.o_done[s]);
             }
         } else {
             // ------------------------------------------------------ KV = W^T K
             const uint32_t id = idesc_bf16(128, 128, 0, 1);
+            const uint64_t kd0 = sdesc(smem_u32(sm.k), kHalf, 1024);
             bool ok = true;
             for (int c = 0; c < wk.n && ok; ++c) {
                 const int s = c & 1;
                 if (c > 0 && !wait(sm, &sm.kv_free, (c - 1) & 1)) break;
-                const uint32_t ks = smem_u32(sm.k[s]);
+                const uint64_t kd = kd0 + ((s * kTile) >> 4);
+#pragma unroll 1
                 for (int qd = 0; qd < 4; ++qd) {
                     const int b = qd & 1, use = 2 * c + (qd >> 1);
                     if (!(ok = wait(sm, &sm.w_ready[b], use & 1))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint64_t bd = sdesc(ks + (2 * qd + x) * 2048, kHalf, 1024);
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
-                            mma_ts(tb + kColKV, tb + kColW + 48 * b + 16 * part + 8 * x, bd, id,
-                                   qd > 0 || x > 0 || part > 0);
+                            mma_ts(tb + kColKV, tb + kColW + 48 * b + 16 * part + 8 * x,
+                                   kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
                     }
                     mma_commit(&sm.w_free[b]);
                 }
@@ -490,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&sm.drain[role - 1]);
             mbar_wait(&sm.drain[role - 1], 0, kDrainLimitNs);
         }
+      }
     }
     tc_fence_before();
     __syncthreads();
@@ -509,7 +642,8 @@ cudaError_t launch_dir(const LinearArgs &a, cudaStream_t s) {
         const uint64_t rowb = kDim * sizeof(bf16);
         if (!encode_rows_bf16(&m.q, a.q, a.nq, a.T, rowb, rowb * a.nq, kC) ||
             !encode_rows_bf16(&m.k, a.k, a.nk, a.T, rowb, rowb * a.nk, kC) ||
-            !encode_rows_bf16(&m.v, a.v, a.nv, a.T, rowb, rowb * a.nv, kC))
+            !encode_rows_bf16(&m.v, a.v, a.nv, a.T, rowb, rowb * a.nv, kC) ||
+            (!a.part && !encode_rows_bf16(&m.o, a.o, a.HV, a.T, rowb, rowb * a.HV, kC)))
             return cudaErrorInvalidValue;
     }
     k_linear_tc<kReverse><<<(unsigned)(a.N * a.HV), kThreads, smem, s>>>(a, m);

@@ -554,6 +554,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (c >= 2 && !wait(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
                 for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full[s]);
+                // the tiles after next start towards L2 while both stages are taken
+                if (c + 2 < wk.n) {
+                    const int t2 = wk.start(c + 2, kReverse);
+                    for (int h = 0; h < 2; ++h) {
+                        tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
+                        tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
+                        tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
+                    }
+                }
             }
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
             for (int c = max(0, issued - 2); c < issued; ++c)

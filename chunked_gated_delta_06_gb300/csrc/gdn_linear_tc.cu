@@ -57,11 +57,10 @@ static_assert((kGroupP + kGroupW) * kRegsWork + kGroupS * kRegsState + 4 * kRegs
               "register shares");
 
 // Tensor-memory columns
-constexpr uint32_t kColP = 0;      // P fp32 [0, 128); then, per half h of 64: P~ of tokens 64 h ..
-                                   // in 32 columns and Q~ of features 64 h .. in the next 32
-constexpr uint32_t kColW = 128;    // two buffers of 48: 32 tokens of W, three parts of 16
-constexpr uint32_t kColKV = 256;
-constexpr uint32_t kColO = 384;
+constexpr uint32_t kColP = 0;      // two buffers of 128: P fp32; then, per half h of 64: P~ of tokens
+                                   // 64 h .. in 32 columns and Q~ of features 64 h .. in the next 32
+constexpr uint32_t kColX = 256;    // KV of a chunk, then its O
+constexpr uint32_t kColW = 384;    // two buffers of 48: 32 tokens of W, three parts of 16
 constexpr uint32_t kCols = 512;
 
 struct LinSmem {
@@ -70,8 +69,8 @@ struct LinSmem {
     float wtab[2 * kC];   // w lam^{127-x} (forward) or w lam^{x+1} (reverse), zeros above 128
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
-    uint64_t p_done, pt_ready, kv_free, s_ready, o_free, o_staged, drain[3];
+    uint64_t full_kv[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
+    uint64_t kv_free, s_ready, o_free, o_staged, drain[3];
     uint32_t tmem_base;
     int dead;
 };
@@ -151,6 +150,12 @@ __device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t 
                  : "memory");
 }
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 template <int N>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -227,7 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             tma_prefetch_maps(maps);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sm.full[i], 1);
+                mbar_init(&sm.full_kv[i], 1);
+                mbar_init(&sm.full_q[i], 1);
+                mbar_init(&sm.p_done[i], 1);
+                mbar_init(&sm.pt_ready[i], kGroupP * 32);
                 mbar_init(&sm.v_ok[i], kGroupW * 32);
                 mbar_init(&sm.w_ready[i], kGroupW * 16);
                 mbar_init(&sm.w_free[i], 1);
@@ -235,8 +243,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.o_done[i], 1);
                 mbar_init(&sm.q_free[i], 1);
             }
-            mbar_init(&sm.p_done, 1);
-            mbar_init(&sm.pt_ready, kGroupP * 32);
             mbar_init(&sm.kv_free, kGroupS * 32);
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
@@ -269,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3, half = warp >> 2;   // rows 32 quad .., columns 64 half ..
         const int i = quad * 32 + lane;
         const float at = (float)lane, lw = log2f(a.w);   // w > 0
-        const uint32_t mine = tb + lanes + kColP + 64 * half;
         for (int c = 0; c < wk.n; ++c) {
+            const uint32_t mine = tb + lanes + kColP + 128 * (c & 1) + 64 * half;
             const int L = wk.length(c, kReverse);
             float e, f;
             read_power<kReverse>(g2, i, L, e, f);
-            if (!wait_warp(sm, &sm.p_done, c & 1)) break;
+            if (!wait_warp(sm, &sm.p_done[c & 1], (c >> 1) & 1)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int b2 = 0; b2 < 2; ++b2) {   // columns j = 32 b + jj
@@ -336,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(mine + 32, x);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&sm.pt_ready);
+            mbar_arrive(&sm.pt_ready[c & 1]);
         }
     } else if (warp < kGroupP + kGroupW) {
         // ---------------------------------------------------------- W
@@ -344,10 +350,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_down<kRegsWork>();
         const int quad = warp & 3, half = (warp - kGroupP) >> 2;
         const uint32_t buf = tb + lanes + kColW + 48 * half;
+        // this lane's row of the first quarter, and the four 8-feature chunks of the warp in it
+        const uint32_t vrow = smem_u32(sm.v[0] + (quad >> 1) * kHalf) + (32 * half + lane) * 128;
+        uint32_t chunk[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) chunk[x] = (uint32_t)((4 * (quad & 1) + x) ^ (lane & 7)) * 16;
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (!(ok = wait_warp(sm, &sm.full[s], (c >> 1) & 1))) break;
+            if (!(ok = wait_warp(sm, &sm.full_kv[s], (c >> 1) & 1))) break;
             if (L < kC) {
                 // rows past the sequence hold the next one's tokens: zeros instead (each half
                 // clears its own quarters of K, which the product of a quarter waits for)
@@ -361,29 +372,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
             }
             mbar_arrive(&sm.v_ok[s]);
-            const float *wt = sm.wtab + (kReverse ? 0 : kC - L) + 2 * (lane & 3);
+            const float *wt = sm.wtab + (kReverse ? 0 : kC - L) + 32 * half + 2 * (lane & 3);
+            const uint32_t vt = vrow + s * kTile;
 #pragma unroll 1
             for (int pass = 0; pass < 2; ++pass) {
-                const int t0 = 64 * pass + 32 * half, use = 2 * c + pass;
+                const int use = 2 * c + pass;
+                uint64_t w2[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w2[k] = pair(wt[64 * pass + 8 * k], wt[64 * pass + 8 * k + 1]);
                 if (use > 0 && !(ok = wait_warp(sm, &sm.w_free[half], (use - 1) & 1))) break;
                 tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                 for (int g16 = 0; g16 < 2; ++g16) {   // features 32 quad + 16 g16 ..
-                    const int r0 = 32 * quad + 16 * g16;
-                    const uint32_t base = smem_u32(sm.v[s] + (r0 >> 6) * kHalf);
                     uint32_t in[2][4], hi[8], mid[8], lo[8];
-                    ldmatrix4t(base + sw128_off(t0 + lane, r0 & 63), in[0]);
-                    ldmatrix4t(base + sw128_off(t0 + lane, (r0 + 8) & 63), in[1]);
+                    ldmatrix4t(vt + pass * 64 * 128 + chunk[2 * g16], in[0]);
+                    ldmatrix4t(vt + pass * 64 * 128 + chunk[2 * g16 + 1], in[1]);
+                    if (L < kC) {   // tokens past the sequence
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int left = L - (64 * pass + 32 * half + 8 * k + 2 * (lane & 3));
+                            const uint32_t keep = left > 1 ? 0xffffffffu : left > 0 ? 0xffffu : 0u;
+                            in[0][k] &= keep;
+                            in[1][k] &= keep;
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int t = t0 + 8 * k + 2 * (lane & 3);
-                        const uint64_t w2 = pair(wt[t0 + 8 * k], wt[t0 + 8 * k + 1]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            uint32_t v2 = in[e][k];
-                            if (L < kC) v2 &= t + 1 < L ? 0xffffffffu : t < L ? 0xffffu : 0u;
-                            const float2 x = unpair(mul2(w2, pair(__uint_as_float(v2 << 16),
-                                                                  __uint_as_float(v2 & 0xffff0000u))));
+                            const uint32_t v2 = in[e][k];
+                            const float2 x = unpair(mul2(w2[k], pair(__uint_as_float(v2 << 16),
+                                                                     __uint_as_float(v2 & 0xffff0000u))));
                             const float2 y = unpair(sub2(pair(x.x, x.y), keep_tops(x)));
                             const float2 z = unpair(sub2(pair(y.x, y.y), keep_tops(y)));
                             hi[2 * k + e] = tops(x);
@@ -454,23 +473,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_warp(sm, &sm.kv_done[s], (c >> 1) & 1)) break;
             tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                float x[16];
-                tmem_ld16(tb + lanes + kColKV + col + 16 * h, x);
+            for (int h = 0; h < 2; ++h) {
+                float x[32];
+                tmem_ld32(tb + lanes + kColX + col + 32 * h, x);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const uint64_t y = pair(st[16 * h + j], st[16 * h + j + 1]);
+                for (int j = 0; j < 32; j += 2) {
+                    const uint64_t y = pair(st[32 * h + j], st[32 * h + j + 1]);
                     const float2 z = unpair(fma2(y, pair(fh, fh), fma2(y, pair(fl, fl), pair(x[j], x[j + 1]))));
-                    st[16 * h + j] = z.x;
-                    st[16 * h + j + 1] = z.y;
+                    st[32 * h + j] = z.x;
+                    st[32 * h + j + 1] = z.y;
                 }
             }
             tc_fence_before();
             mbar_arrive(&sm.kv_free);
             if (!wait_warp(sm, &sm.o_done[s], (c >> 1) & 1)) break;
             tc_fence_after();
-            if (c + 1 < wk.n) publish();
             float e, f;
             read_power<kReverse>(g2, r, L, e, f);
             const float scale = a.so * ex2(f);
@@ -479,29 +497,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool staged = L == kC && !a.part;   // whole chunks of bf16 leave by TMA
             const bool mine = r < L && in_range(row, 64, (long long)a.T * a.HV * kDim, a.status);
             // the stage's Q tile is free: its readers finished before O did
-            unsigned char *orow = sm.q[s] + (col >> 6) * kHalf;
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-                float x[16];
-                tmem_ld16(tb + lanes + kColO + col + 16 * h, x);
-                tmem_ld_wait();
+            unsigned char *orow = sm.q[s] + (col >> 6) * kHalf + r * 128;
+            const uint64_t scale2 = pair(scale, scale);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= scale;
+            for (int h = 0; h < 2; ++h) {
+                float x[32];
+                tmem_ld32(tb + lanes + kColX + col + 32 * h, x);
+                tmem_ld_wait();
+                if (h == 1) {
+                    tc_fence_before();
+                    mbar_arrive(&sm.o_free);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 y = unpair(mul2(scale2, pair(x[j], x[j + 1])));
+                    x[j] = y.x;
+                    x[j + 1] = y.y;
+                }
                 if (a.part) {
                     if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<float4 *>(a.part + row + 16 * h + 4 * j) =
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(a.part + row + 32 * h + 4 * j) =
                                 make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
                     }
                 } else {
+                    uint4 y[4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 y = make_uint4(
+                    for (int j = 0; j < 4; ++j)
+                        y[j] = make_uint4(
                             epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
                             epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
-                        if (staged) *reinterpret_cast<uint4 *>(orow + sw128_off(r, 16 * h + 8 * j)) = y;
-                        else if (mine) *reinterpret_cast<uint4 *>(a.o + row + 16 * h + 8 * j) = y;
+                    if (staged) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4)) = y[j];
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.o + row + 32 * h + 8 * j) = y[j];
                     }
                 }
             }
@@ -509,8 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(&sm.o_staged);
             }
-            tc_fence_before();
-            mbar_arrive(&sm.o_free);
+            if (c + 1 < wk.n) publish();
             if (staged) {
                 stores += 1;
                 if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1)) {
@@ -534,52 +566,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-      regs_down<kRegsIssue>();
-      if (lane == 0) {
-        const int role = warp - kWarpLoad;
+        // ---------------------------------------------------------- issuing warps
+        // The whole warp waits and one elected lane issues: the operands stay in uniform
+        // registers (issued from a lane's own branch, each product took 80 to 130 cycles
+        // to issue, more than the 64 it runs).
+        regs_down<kRegsIssue>();
+        const int role = __shfl_sync(0xffffffffu, warp, 0) - kWarpLoad;
         if (role == 0) {
             // ------------------------------------------------------ loads
             const int hq = hv / (a.HV / a.nq), hk = hv / (a.HV / a.nk), hw = hv / (a.HV / a.nv);
-            int issued = 0;
+            int issued_kv = 0, issued_q = 0;
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1, t = wk.start(c, kReverse);
-                if (c >= 2 && (!wait(sm, &sm.o_done[s], ((c >> 1) - 1) & 1) ||
-                               !wait(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
+                if (c >= 2 && (!wait_warp(sm, &sm.o_done[s], ((c >> 1) - 1) & 1) ||
+                               !wait_warp(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
                     break;
-                mbar_arrive_expect_tx(&sm.full[s], 3 * kTile);
-                issued = c + 1;
-                for (int h = 0; h < 2; ++h) {
-                    tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full[s]);
-                    tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full[s]);
-                }
-                if (c >= 2 && !wait(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
-                for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full[s]);
-                // the tiles after next start towards L2 while both stages are taken
-                if (c + 2 < wk.n) {
-                    const int t2 = wk.start(c + 2, kReverse);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sm.full_kv[s], 2 * kTile);
                     for (int h = 0; h < 2; ++h) {
-                        tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
-                        tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
-                        tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
+                        tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full_kv[s]);
+                        tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_kv[s]);
                     }
                 }
+                issued_kv = c + 1;
+                if (c >= 2 && !wait_warp(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sm.full_q[s], kTile);
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_q[s]);
+                    // the tiles after next start towards L2 while both stages are taken
+                    if (c + 2 < wk.n) {
+                        const int t2 = wk.start(c + 2, kReverse);
+                        for (int h = 0; h < 2; ++h) {
+                            tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
+                            tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
+                            tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
+                        }
+                    }
+                }
+                issued_q = c + 1;
             }
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
-            for (int c = max(0, issued - 2); c < issued; ++c)
-                mbar_wait(&sm.full[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            for (int c = max(0, issued_kv - 2); c < issued_kv; ++c)
+                mbar_wait(&sm.full_kv[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            for (int c = max(0, issued_q - 2); c < issued_q; ++c)
+                mbar_wait(&sm.full_q[c & 1], (c >> 1) & 1, kDrainLimitNs);
         } else if (role == 1) {
             // ------------------------------------------------------ P = Q K^T
             const uint32_t id = idesc_bf16(128, 128, 0, 0);
             const uint64_t qd0 = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1;
-                if (!wait(sm, &sm.full[s], (c >> 1) & 1)) break;
-                if (c > 0 && !wait(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1)) break;
+                if (!wait_warp(sm, &sm.full_kv[s], (c >> 1) & 1) || !wait_warp(sm, &sm.full_q[s], (c >> 1) & 1))
+                    break;
+                // (loading this stage waited for O of chunk c - 2, which read this P buffer)
                 tc_fence_after();
                 const uint64_t qd = qd0 + ((s * kTile) >> 4), kd = kd0 + ((s * kTile) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) mma_bf16(tb + kColP, qd + k_step(x), kd + k_step(x), id, x > 0);
-                mma_commit(&sm.p_done);
+                    for (int x = 0; x < 8; ++x)
+                        mma_bf16(tb + kColP + 128 * s, qd + k_step(x), kd + k_step(x), id, x > 0);
+                    mma_commit(&sm.p_done[s]);
+                }
+                __syncwarp();
             }
         } else if (role == 2) {
             // ------------------------------------------------------ O = [P~ | Q~] [V ; S]
@@ -587,18 +636,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t vd0 = sdesc(smem_u32(sm.v), kHalf, 1024), sd0 = sdesc(smem_u32(sm.s), 16, 1024);
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1;
-                if (!wait(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait(sm, &sm.s_ready, c & 1) ||
-                    !wait(sm, &sm.pt_ready, c & 1))
+                if (!wait_warp(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait_warp(sm, &sm.s_ready, c & 1) ||
+                    !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) || !wait_warp(sm, &sm.kv_free, c & 1))
                     break;
-                if (c > 0 && !wait(sm, &sm.o_free, (c - 1) & 1)) break;
                 tc_fence_after();
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    mma_ts(tb + kColO, tb + a_step(x) + 32, sd0 + k_step(x), ids, x > 0);
+                    for (int x = 0; x < 8; ++x)
+                        mma_ts(tb + kColX, tb + 128 * s + a_step(x) + 32, sd0 + k_step(x), ids, x > 0);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) mma_ts(tb + kColO, tb + a_step(x), vd + 128 * x, idv, true);
-                mma_commit(&sm.o_done[s]);
+                    for (int x = 0; x < 8; ++x)
+                        mma_ts(tb + kColX, tb + 128 * s + a_step(x), vd + 128 * x, idv, true);
+                    mma_commit(&sm.o_done[s]);
+                }
+                __syncwarp();
             }
         } else {
             // ------------------------------------------------------ KV = W^T K
@@ -607,31 +659,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int c = 0; c < wk.n && ok; ++c) {
                 const int s = c & 1;
-                if (c > 0 && !wait(sm, &sm.kv_free, (c - 1) & 1)) break;
+                if (c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)) break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
-#pragma unroll 1
+#pragma unroll
                 for (int qd = 0; qd < 4; ++qd) {
                     const int b = qd & 1, use = 2 * c + (qd >> 1);
-                    if (!(ok = wait(sm, &sm.w_ready[b], use & 1))) break;
+                    ok = ok && wait_warp(sm, &sm.w_ready[b], use & 1);
+                    if (!ok) break;
                     tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int part = 0; part < 3; ++part)
-                            mma_ts(tb + kColKV, tb + kColW + 48 * b + 16 * part + 8 * x,
-                                   kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
+                            for (int part = 0; part < 3; ++part)
+                                mma_ts(tb + kColX, tb + kColW + 48 * b + 16 * part + 8 * x,
+                                       kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
+                        mma_commit(&sm.w_free[b]);
+                        if (qd == 3) mma_commit(&sm.kv_done[s]);
                     }
-                    mma_commit(&sm.w_free[b]);
+                    __syncwarp();
                 }
-                if (ok) mma_commit(&sm.kv_done[s]);
             }
         }
         if (role > 0 && *(volatile int *)&sm.dead) {
             // products in flight read tiles and tensor memory: wait for them (bounded)
-            mma_commit(&sm.drain[role - 1]);
+            if (elect_one()) mma_commit(&sm.drain[role - 1]);
+            __syncwarp();
             mbar_wait(&sm.drain[role - 1], 0, kDrainLimitNs);
         }
-      }
     }
     tc_fence_before();
     __syncthreads();

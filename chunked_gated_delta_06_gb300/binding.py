@@ -594,14 +594,15 @@ def _linear_inputs(q, k, v, log_decay):
     return T, H, HV
 
 
-def _linear_problem(q, v, cu_host, cu_dev, scale, status):
+def _linear_problem(q, v, cu_host, cu_dev, scale, status, scan_segment_chunks=0):
     import torch
     cu = np.ascontiguousarray(np.asarray(cu_host, dtype=np.int32))
     _need(cu_dev, "cu_dev", torch.int32, (len(cu),))
     if len(cu) == 0 or int(cu[-1]) != q.shape[0]:
         raise ValueError("cu_host must end with the number of tokens, %d" % q.shape[0])
     return make_problem(cu, q.shape[1], v.shape[1], q.shape[2], v.shape[2], scale or 0.0,
-                        cu_dev.data_ptr(), device_status_ptr=_ptr(status) or 0)
+                        cu_dev.data_ptr(), device_status_ptr=_ptr(status) or 0,
+                        scan_segment_chunks=scan_segment_chunks)
 
 
 def _linear_workspace(p, mode, workspace, device):
@@ -617,11 +618,11 @@ def _linear_workspace(p, mode, workspace, device):
 
 
 def linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=None, initial_state=None,
-                    output_final_state=True, workspace=None, device_status=None):
+                    output_final_state=True, workspace=None, device_status=None, scan_segment_chunks=0):
     """gdn_linear_attn_fwd on torch tensors.  Returns (o, final_state or None)."""
     import torch
     T, H, HV = _linear_inputs(q, k, v, log_decay)
-    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, device_status)
+    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, device_status, scan_segment_chunks)
     workspace = _linear_workspace(p, 0, workspace, q.device)
     shape = (p.num_seqs, HV, 128, 128)
     if initial_state is not None:
@@ -636,12 +637,12 @@ def linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=None, initial_sta
 
 def linear_attn_prefill_paged(q, k, v, log_decay, cu_host, cu_dev, state_pool, state_indices,
                               has_initial_state=None, scale=None, device_status=None, workspace=None,
-                              problem_status=None):
+                              problem_status=None, scan_segment_chunks=0):
     """gdn_linear_attn_prefill_paged on torch tensors (state_pool updated in place; slots and
     status words as in chunk_prefill_paged).  Returns o."""
     import torch
     T, H, HV = _linear_inputs(q, k, v, log_decay)
-    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, problem_status)
+    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, problem_status, scan_segment_chunks)
     workspace = _linear_workspace(p, 0, workspace, q.device)
     _need(state_pool, "state_pool", torch.float32, (state_pool.shape[0], HV, 128, 128))
     _need(state_indices, "state_indices", torch.int32, (p.num_seqs,))
@@ -657,11 +658,12 @@ def linear_attn_prefill_paged(q, k, v, log_decay, cu_host, cu_dev, state_pool, s
 
 
 def linear_attn_bwd(q, k, v, log_decay, d_o, cu_host, cu_dev, scale=None, initial_state=None,
-                    d_final_state=None, want_dh0=True, workspace=None, device_status=None):
+                    d_final_state=None, want_dh0=True, workspace=None, device_status=None,
+                    scan_segment_chunks=0):
     """gdn_linear_attn_bwd on torch tensors.  Returns dict dq, dk, dv, dh0."""
     import torch
     T, H, HV = _linear_inputs(q, k, v, log_decay)
-    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, device_status)
+    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, device_status, scan_segment_chunks)
     workspace = _linear_workspace(p, 1, workspace, q.device)
     shape = (p.num_seqs, HV, 128, 128)
     _need(d_o, "d_o", torch.bfloat16, (T, HV, 128))

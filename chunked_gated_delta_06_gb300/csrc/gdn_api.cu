@@ -444,34 +444,96 @@ gdn_status decode_impl(int32_t batch, int32_t num_k_heads, int32_t num_v_heads, 
 }
 
 // ---------------------------------------------------------------- linear attention
-// Workspace of the decay-only calls: the fp32 outputs of dq and dk per value head when
-// value heads share key heads (summed in order afterwards).
-struct LinearWs {
-    float *part;
+// How the scans of one problem are run: a CTA walks the 128-token chunks of one (sequence,
+// value head), about as long for each.  Few long sequences leave SMs idle, so a split plan
+// cuts every sequence into segments of `seg` chunks: a pass over the states alone, a stitch,
+// and the full pass over all segments at once.  Costs in chunks of the full pass: 0.45 for a
+// chunk of the state pass, 2.5 for a CTA's start and end, 2 for the two launches more; a
+// launch takes the longer of one CTA and the work over 152 SMs, and half a CTA more when
+// they take turns.  A split has to gain a tenth.  A function of the problem alone.
+struct LinearPlan {
+    int seg, items;
 };
-size_t carve_linear(const Dims &d, int for_backward, void *base, LinearWs *w) {
+LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
+    LinearPlan best{0, d.N};
+    if (d.N > gdn::kLinearOrder || p->scan_segment_chunks < 0) return best;
+    auto launch_cost = [&](double cta, double work) {
+        const double area = work * d.HV / 152.0;
+        return area <= cta ? cta : area + 0.5 * cta;
+    };
+    auto chunks = [&](int n) {
+        return (int)(((int64_t)p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n] + 127) / 128);
+    };
+    const double start = 2.5, state = 0.45;
+    int longest = 0;
+    double work = 0.0;
+    for (int n = 0; n < d.N; ++n) {
+        longest = std::max(longest, chunks(n));
+        work += chunks(n) + start;
+    }
+    if (p->scan_segment_chunks > 0) {
+        const int seg = p->scan_segment_chunks;
+        int64_t items = 0;
+        for (int n = 0; n < d.N; ++n) items += std::max(1, (chunks(n) - 1) / seg + 1);
+        if (items > d.N && items * d.HV <= 16384) best = {seg, (int)items};
+        return best;
+    }
+    double t = 0.9 * launch_cost(longest + start, work);
+    for (int seg : {4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256}) {
+        double work1 = 0.0, work2 = 0.0;
+        int64_t items = 0;
+        for (int n = 0; n < d.N; ++n) {
+            const int c = chunks(n), k = std::max(1, (c + seg - 1) / seg);
+            work1 += (k - 1) * (state * seg + start);
+            work2 += c + k * start;
+            items += k;
+        }
+        if (items == d.N || items * d.HV > 16384) continue;  // 1 GiB of states at most
+        const double cost = launch_cost(state * seg + start, work1) + launch_cost(seg + start, work2) + 2.0;
+        if (cost < t) {
+            t = cost;
+            best = {seg, (int)items};
+        }
+    }
+    return best;
+}
+
+// Workspace of the decay-only calls: the fp32 outputs of dq and dk when more than two value
+// heads, or an odd number, share a key head (summed in order afterwards), and the states
+// between the segments of a split scan.
+struct LinearWs {
+    float *part, *seg_state;
+};
+size_t carve_linear(const Dims &d, const LinearPlan &plan, int for_backward, void *base, LinearWs *w) {
     Carver cv(base);
-    w->part = nullptr;
-    if (for_backward && d.HV != d.H) w->part = cv.take<float>((size_t)d.T * d.HV * gdn::kDim);
+    const int r = d.HV / d.H, no = r % 2 ? d.HV : d.HV / 2;
+    w->part = w->seg_state = nullptr;
+    if (for_backward && no != d.H) w->part = cv.take<float>((size_t)d.T * no * gdn::kDim);
+    if (plan.seg) w->seg_state = cv.take<float>((size_t)plan.items * d.HV * gdn::kDim * gdn::kDim);
     return cv.used() > 0 ? cv.used() : kAlign;
 }
 
-gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const float *log_decay) {
+gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan, const LinearWs &ws,
+                            const float *log_decay) {
     gdn::LinearArgs a{};
+    const int32_t *cu = p->cu_seqlens_host;
     a.N = d.N;
     a.T = d.T;
-    a.HV = d.HV;
-    a.longest = 0;
-    for (int n = 0; n < d.N; ++n) {
-        const int len = p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n];
-        a.longest = len > a.longest ? len : a.longest;
-    }
+    a.HV = a.no = d.HV;
+    a.items = plan.items;
+    a.seg_chunks = plan.seg;
+    a.seg_state = ws.seg_state;
+    for (int n = 0; n < d.N; ++n) a.longest = std::max(a.longest, cu[n + 1] - cu[n]);
     if (d.N <= gdn::kLinearOrder) {
         for (int n = 0; n < d.N; ++n) a.order[n] = (uint16_t)n;
-        const int32_t *cu = p->cu_seqlens_host;
         std::stable_sort(a.order, a.order + d.N, [cu](uint16_t x, uint16_t y) {
             return cu[x + 1] - cu[x] > cu[y + 1] - cu[y];
         });
+        for (int x = 0; x < d.N; ++x) {
+            const int c = (int)(((int64_t)cu[a.order[x] + 1] - cu[a.order[x]] + 127) / 128);
+            a.seg_first[x + 1] = a.seg_first[x] + (plan.seg && c > 0 ? (c - 1) / plan.seg + 1 : 1);
+        }
+        for (int n = 0; n <= d.N; ++n) a.cu[n] = cu[n];
     }
     a.log_decay = log_decay;
     a.so = d.scale;
@@ -514,8 +576,10 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
     if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
     if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
-    if (ws_size < carve_linear(d, 0, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
-    gdn::LinearArgs a = linear_args(d, p, log_decay);
+    const LinearPlan plan = plan_linear(p, d);
+    if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if (ws_size < carve_linear(d, plan, 0, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    gdn::LinearArgs a = linear_args(d, p, plan, ws, log_decay);
     linear_roles(a, q, d.H, k, d.H, v, d.HV);
     a.o = static_cast<bf16 *>(o);
     a.s0 = initial_state;
@@ -680,7 +744,7 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward) {
     LinearWs ws;
     if (for_backward < 0 || for_backward > 1) return 0;
     if (check_problem(p, &d) != GDN_OK) return 0;
-    return carve_linear(d, for_backward, nullptr, &ws);
+    return carve_linear(d, plan_linear(p, d), for_backward, nullptr, &ws);
 }
 
 gdn_status gdn_linear_attn_fwd(const gdn_problem *p, const void *q, const void *k, const void *v,
@@ -718,11 +782,16 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     if (dh0 && dh0 == d_final_state) return GDN_ERR_INVALID_ARG;
     if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
-    if (ws_size < carve_linear(d, 1, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    const LinearPlan plan = plan_linear(p, d);
+    if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if (ws_size < carve_linear(d, plan, 1, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     // dq: a forward scan over (d_o, v, k), the state transposed
-    gdn::LinearArgs a = linear_args(d, p, log_decay);
+    gdn::LinearArgs a = linear_args(d, p, plan, ws, log_decay);
+    const int r = d.HV / d.H;
+    a.pair = r % 2 == 0;   // pairs of value heads are summed inside the scan
+    a.no = a.pair ? d.HV / 2 : d.HV;
     linear_roles(a, d_o, d.HV, v, d.HV, k, d.H);
     a.s0 = initial_state;
     a.s_rs = gdn::kDim;
@@ -730,7 +799,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     a.o = static_cast<bf16 *>(dq);
     a.part = ws.part;
     if ((e = gdn::launch_linear_tc(a, s)) != cudaSuccess) return cuda_status(e);
-    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, d.HV, a.status, s)) != cudaSuccess)
+    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, a.no, a.status, s)) != cudaSuccess)
         return cuda_status(e);
     // dk: a reverse scan over (v, d_o, q), the state transposed
     a.reverse = 1;
@@ -740,7 +809,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     linear_roles(a, v, d.HV, d_o, d.HV, q, d.H);
     a.o = static_cast<bf16 *>(dk);
     if ((e = gdn::launch_linear_tc(a, s)) != cudaSuccess) return cuda_status(e);
-    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, d.HV, a.status, s)) != cudaSuccess)
+    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, a.no, a.status, s)) != cudaSuccess)
         return cuda_status(e);
     // dv: a reverse scan over (k, q, d_o); it ends with dh0
     linear_roles(a, k, d.H, q, d.H, d_o, d.HV);
@@ -748,6 +817,8 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     a.s_cs = gdn::kDim;
     a.o = static_cast<bf16 *>(dv);
     a.part = nullptr;
+    a.pair = 0;
+    a.no = d.HV;
     a.s1 = dh0;
     return cuda_status(gdn::launch_linear_tc(a, s));
 }

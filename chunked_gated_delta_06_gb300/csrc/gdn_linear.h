@@ -19,8 +19,10 @@ struct LinearArgs {
     int longest;              // tokens of the longest sequence (host copy of cu_seqlens)
     const bf16 *q, *k, *v;    // [T, nq | nk | nv, 128]
     int nq, nk, nv;
-    bf16 *o;                  // [T, HV, 128], or null
-    float *part;              // [T, HV, 128]: fp32 outputs instead of o (summed by launch_linear_heads)
+    bf16 *o;                  // [T, no, 128], or null
+    float *part;              // [T, no, 128]: fp32 outputs instead of o (summed by launch_linear_heads)
+    int no;                   // output heads: HV, or HV / 2 with pair
+    int pair;                 // value heads 2 x and 2 x + 1 are summed into output head x
     const float *log_decay;   // [HV]
     const float *s0;          // [N, HV, 128, 128] or null (zeros)
     float *s1;                // the same shape, or null
@@ -33,7 +35,13 @@ struct LinearArgs {
     int reverse;
     const int *cu_dev;        // [N + 1]
     int *status;
-    uint16_t order[kLinearOrder];  // N <= kLinearOrder: sequences by decreasing length
+    // Work items: (sequence, segment), grid order.  seg_chunks > 0 (N <= kLinearOrder only) cuts
+    // the sequences into segments of that many chunks, which are walked at once.
+    int items, seg_chunks;
+    float *seg_state;              // [items, HV, 128, 128] states after each inner segment
+    uint16_t order[kLinearOrder];  // N <= kLinearOrder: sequences by decreasing length,
+    int seg_first[kLinearOrder + 1];  // the first item of each, in that order,
+    int cu[kLinearOrder + 1];      // and the host's cu_seqlens, which the device's must equal
 };
 
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t s);

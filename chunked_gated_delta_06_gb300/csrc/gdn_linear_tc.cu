@@ -32,6 +32,8 @@
 #include <stddef.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "gdn_epi.cuh"
 #include "gdn_linear.h"
 #include "gdn_tma.h"
@@ -70,7 +72,8 @@ struct LinSmem {
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
     uint64_t full_kv[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
-    uint64_t kv_free, s_ready, o_free, o_staged, drain[3];
+    uint64_t kv_free[2], s_ready, o_free, o_staged, drain[3];
+    uint64_t peer_ok, rx_full;   // pair mode: the peer's Q tile is free; the peer's half of O is here
     uint32_t tmem_base;
     int dead;
 };
@@ -156,6 +159,33 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
     return p != 0;
 }
+// ---- the other CTA of a cluster
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void remote_arrive(uint64_t *bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
+                 : "memory");
+}
+__device__ __forceinline__ void remote_store(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 template <int N>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -167,10 +197,11 @@ __device__ __forceinline__ void regs_down() {
 
 // A bounded wait that also gives up once any role of the CTA has.  The timer and the flag
 // are looked at every 32 polls only: the timer's reads are slow.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait(LinSmem &sm, uint64_t *bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t polls = 1;; ++polls) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (polls % 32) continue;
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
@@ -186,14 +217,25 @@ __device__ __forceinline__ bool wait_warp(LinSmem &sm, uint64_t *bar, uint32_t p
     return __all_sync(0xffffffffu, wait(sm, bar, parity));
 }
 
-struct Walk {      // the chunks of this CTA's sequence, in scan order
-    int t0, len, n;
-    __device__ __forceinline__ int start(int c, bool rev) const { return t0 + (rev ? n - 1 - c : c) * kC; }
-    __device__ __forceinline__ int length(int c, bool rev) const {
-        const int i = rev ? n - 1 - c : c;
-        return min(kC, len - i * kC);
+__device__ __forceinline__ bool wait_warp_cluster(LinSmem &sm, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait<true>(sm, bar, parity));
+}
+
+struct Walk {      // the chunks of this CTA's segment, in scan order
+    int t0, len, total;   // the sequence: first token, tokens, chunks
+    int first, n;         // the segment: first chunk in scan order, chunks
+    __device__ __forceinline__ int chunk(int c, bool rev) const {
+        return rev ? total - 1 - (first + c) : first + c;
     }
+    __device__ __forceinline__ int start(int c, bool rev) const { return t0 + chunk(c, rev) * kC; }
+    __device__ __forceinline__ int length(int c, bool rev) const { return min(kC, len - chunk(c, rev) * kC); }
 };
+
+// Column of chunk c's KV: without outputs the P buffers are free, and two chunks alternate.
+template <bool kState>
+__device__ __forceinline__ uint32_t col_kv(int c) {
+    return kState && (c & 1) ? kColP : kColX;
+}
 
 // lam^{i+1} (forward) or lam^{L-1-i} (reverse) as 2^{e + f}, e whole and 0 <= f < 1.
 template <bool kReverse>
@@ -203,25 +245,41 @@ __device__ __forceinline__ void read_power(float g2, int i, int L, float &e, flo
     f = x - e;
 }
 
-template <bool kReverse>
+// kMode 0: outputs and states.  1: outputs summed over the two value heads of a cluster of
+// two CTAs.  2: only the states, of every segment but a sequence's last (their sums are the
+// start states of the segments that a second launch walks at once).
+template <bool kReverse, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_linear_tc(const LinearArgs a, const __grid_constant__ LinMaps maps) {
+    k_linear_tc(const __grid_constant__ LinearArgs a, const __grid_constant__ LinMaps maps) {
+    constexpr bool kPair = kMode == 1, kState = kMode == 2;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     LinSmem &sm = smem_struct<LinSmem>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = blockIdx.x % a.HV;
-    int n = blockIdx.x / a.HV;
-    if (a.N <= kLinearOrder) n = a.order[n];
+    const int hv = blockIdx.x % a.HV, item = blockIdx.x / a.HV;
+    int n = item, seg = 0, nseg = 1;
+    if (a.N <= kLinearOrder) {
+        int x = 0;
+        for (int step = kLinearOrder / 2; step; step >>= 1)   // the last x with seg_first[x] <= item
+            if (x + step < a.N && a.seg_first[x + step] <= item) x += step;
+        n = a.order[x];
+        seg = item - a.seg_first[x];
+        nseg = a.seg_first[x + 1] - a.seg_first[x];
+    }
+    if (kState && seg == nseg - 1) return;
     Walk wk;
     {
         const int t0 = a.cu_dev[n], t1 = a.cu_dev[n + 1];
-        if (t0 < 0 || t1 < t0 || t1 > a.T || t1 - t0 > a.longest) {
+        bool good = t0 >= 0 && t1 >= t0 && t1 <= a.T && t1 - t0 <= a.longest;
+        if (a.N <= kLinearOrder) good = t0 == a.cu[n] && t1 == a.cu[n + 1];
+        if (!good) {
             if (tid == 0 && a.status) atomicOr(a.status, GDN_DEVICE_CU_SEQLENS_MISMATCH);
             return;
         }
         wk.t0 = t0;
         wk.len = t1 - t0;
-        wk.n = (wk.len + kC - 1) / kC;
+        wk.total = (wk.len + kC - 1) / kC;
+        wk.first = seg * a.seg_chunks;
+        wk.n = nseg > 1 ? min(a.seg_chunks, wk.total - wk.first) : wk.total;
     }
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
     const float g2 = g * 1.4426950408889634f;
@@ -230,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&sm.tmem_base, kCols);
         tmem_relinquish();
         if (lane == 0) {
-            tma_prefetch_maps(maps);
+            if (wk.n > 0) tma_prefetch_maps(maps);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sm.full_kv[i], 1);
                 mbar_init(&sm.full_q[i], 1);
@@ -242,11 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.kv_done[i], 1);
                 mbar_init(&sm.o_done[i], 1);
                 mbar_init(&sm.q_free[i], 1);
+                mbar_init(&sm.kv_free[i], kGroupS * 32);
             }
-            mbar_init(&sm.kv_free, kGroupS * 32);
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
-            mbar_init(&sm.o_staged, kGroupS * 32);
+            mbar_init(&sm.o_staged, kGroupS * (kPair ? 16 : 32));
+            mbar_init(&sm.peer_ok, 1);
+            mbar_init(&sm.rx_full, kGroupS * 16);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
@@ -266,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (kPair) cluster_sync();   // the peer's barriers are initialised
     const uint32_t tb = sm.tmem_base;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
 
@@ -275,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3, half = warp >> 2;   // rows 32 quad .., columns 64 half ..
         const int i = quad * 32 + lane;
         const float at = (float)lane, lw = log2f(a.w);   // w > 0
-        for (int c = 0; c < wk.n; ++c) {
+        for (int c = 0; !kState && c < wk.n; ++c) {
             const uint32_t mine = tb + lanes + kColP + 128 * (c & 1) + 64 * half;
             const int L = wk.length(c, kReverse);
             float e, f;
@@ -425,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_up<kRegsState>();
         const int x0 = warp - kGroupP - kGroupW;
         const int r = (warp & 3) * 32 + lane, col = (x0 >> 2) * 64;  // row of S and of O; columns
-        const float *src = a.s0 ? a.s0 + ((size_t)n * a.HV + hv) * kDim * kDim : nullptr;
-        float *dst = a.s1 ? a.s1 + ((size_t)n * a.HV + hv) * kDim * kDim : nullptr;
+        const size_t state = ((size_t)n * a.HV + hv) * kDim * kDim;
+        const float *src = a.s0 ? a.s0 + state : nullptr;
+        float *dst = a.s1 ? a.s1 + state : nullptr;
         if (a.pool) {
             const int slot = a.pool_idx[n];
             if (slot >= a.num_slots && r == 0 && a.pool_status) *a.pool_status = 1;
@@ -435,11 +497,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 src = (!a.pool_resume || a.pool_resume[n]) ? dst : nullptr;
             }
         }
+        float *keep_start = nullptr;
+        bool src_rows = a.s_cs == 1, dst_rows = src_rows;   // row r contiguous
+        if (nseg > 1) {   // inner states of a split sequence: after segment k in record `first + k`
+            float *rec = a.seg_state + ((size_t)item * a.HV + hv) * kDim * kDim;
+            if (seg > 0) {
+                src = kState ? nullptr : rec - (size_t)a.HV * kDim * kDim;
+                src_rows = true;
+            }
+            // a pool slot is written by its last segment's CTA, perhaps before the first one's
+            // starts: the state pass keeps the start state in the last record, which is free
+            float *kept = rec + (size_t)(nseg - 1) * a.HV * kDim * kDim;
+            if (seg == 0 && a.pool && !kState) {
+                src = kept;
+                src_rows = true;
+            }
+            keep_start = seg == 0 && a.pool && kState ? kept : nullptr;
+            if (kState) {
+                dst = rec;
+                dst_rows = true;
+            } else if (seg < nseg - 1) {
+                dst = nullptr;
+            }
+        }
         float st[64];
 #pragma unroll
         for (int j = 0; j < 64; ++j) st[j] = 0.f;
         if (src) {
-            if (a.s_cs == 1) {
+            if (src_rows) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float4 z = *reinterpret_cast<const float4 *>(src + (size_t)r * kDim + col + 4 * j);
@@ -453,6 +538,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 64; ++j) st[j] = src[(size_t)(col + j) * kDim + r];
             }
         }
+        if (keep_start) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                *reinterpret_cast<float4 *>(keep_start + (size_t)r * kDim + col + 4 * j) =
+                    make_float4(st[4 * j], st[4 * j + 1], st[4 * j + 2], st[4 * j + 3]);
+        }
         unsigned char *srow = sm.s + (col >> 6) * kHalf;
         auto publish = [&]() {
             epi::put_row32(srow, r, 0, st);
@@ -460,12 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             mbar_arrive(&sm.s_ready);
         };
-        if (wk.n > 0) publish();
+        if (!kState && wk.n > 0) publish();
         int stores = 0;
         const bool storer = tid == (kGroupP + kGroupW) * 32;
         for (int c = 0; c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (storer && c > 0) {   // the last chunk's output has left its stage's Q tile
+            if (!kState && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
                 tma_store_wait_read();
                 mbar_arrive(&sm.q_free[s ^ 1]);
             }
@@ -475,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x[32];
-                tmem_ld32(tb + lanes + kColX + col + 32 * h, x);
+                tmem_ld32(tb + lanes + col_kv<kState>(c) + col + 32 * h, x);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
@@ -486,19 +577,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive(&sm.kv_free);
+            mbar_arrive(&sm.kv_free[s]);
+            if (kState) continue;
             if (!wait_warp(sm, &sm.o_done[s], (c >> 1) & 1)) break;
             tc_fence_after();
             float e, f;
             read_power<kReverse>(g2, r, L, e, f);
             const float scale = a.so * ex2(f);
             const size_t t = (size_t)wk.start(c, kReverse) + r;
-            const size_t row = (t * a.HV + hv) * kDim + col;
+            const size_t row = (t * a.no + (kPair ? hv >> 1 : hv)) * kDim + col;
             const bool staged = L == kC && !a.part;   // whole chunks of bf16 leave by TMA
-            const bool mine = r < L && in_range(row, 64, (long long)a.T * a.HV * kDim, a.status);
+            const bool mine = r < L && in_range(row, 64, (long long)a.T * a.no * kDim, a.status);
             // the stage's Q tile is free: its readers finished before O did
-            unsigned char *orow = sm.q[s] + (col >> 6) * kHalf + r * 128;
+            unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
             const uint64_t scale2 = pair(scale, scale);
+            const bool keep = !kPair || (col >> 6) == (hv & 1);   // this warp's half is this CTA's to write
+            if (kPair) {
+                if (storer) remote_arrive(&sm.peer_ok, (hv & 1) ^ 1);
+                if (!wait_warp_cluster(sm, keep ? &sm.rx_full : &sm.peer_ok, c & 1)) break;
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x[32];
@@ -514,6 +611,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x[j] = y.x;
                     x[j + 1] = y.y;
                 }
+                if (kPair) {   // 32 columns of row r: a 128-byte row of plane h of the Q tile
+                    const uint32_t plane = smem_u32(sm.q[s] + h * kHalf) + r * 128;
+                    if (!keep) {
+                        const uint32_t there = map_rank(plane, (hv & 1) ^ 1);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            remote_store(there + ((j ^ (r & 7)) << 4), x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + h * kHalf + r * 128 +
+                                                                           ((j ^ (r & 7)) << 4));
+                        // (two terms: the same bits whichever CTA adds)
+                        x[4 * j] += y.x;
+                        x[4 * j + 1] += y.y;
+                        x[4 * j + 2] += y.z;
+                        x[4 * j + 3] += y.w;
+                    }
+                }
                 if (a.part) {
                     if (mine) {
 #pragma unroll
@@ -528,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         y[j] = make_uint4(
                             epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
                             epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
-                    if (staged) {
+                    if (staged) {   // (pair mode: over plane 0's row, which only this thread reads)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             *reinterpret_cast<uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4)) = y[j];
@@ -538,16 +655,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (staged) {
+            if (kPair && !keep) remote_arrive(&sm.rx_full, (hv & 1) ^ 1);
+            if (kPair ? keep : staged) {
                 fence_proxy_async_smem();
                 mbar_arrive(&sm.o_staged);
             }
             if (c + 1 < wk.n) publish();
-            if (staged) {
+            if (kPair || staged) {
                 stores += 1;
-                if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1)) {
-                    for (int h = 0; h < 2; ++h)
-                        tma_store_3d(&maps.o, 64 * h, hv, wk.start(c, kReverse), sm.q[s] + h * kHalf);
+                if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1) && staged) {
+                    for (int h = 0; h < (kPair ? 1 : 2); ++h)
+                        tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv,
+                                     wk.start(c, kReverse), sm.q[s] + h * kHalf);
                     tma_store_commit();
                 }
                 __syncwarp();
@@ -555,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (storer) tma_store_wait_all();
         if (dst && !*(volatile int *)&sm.dead) {
-            if (a.s_cs == 1) {
+            if (dst_rows) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     *reinterpret_cast<float4 *>(dst + (size_t)r * kDim + col + 4 * j) =
@@ -578,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int issued_kv = 0, issued_q = 0;
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1, t = wk.start(c, kReverse);
-                if (c >= 2 && (!wait_warp(sm, &sm.o_done[s], ((c >> 1) - 1) & 1) ||
+                if (c >= 2 && ((!kState && !wait_warp(sm, &sm.o_done[s], ((c >> 1) - 1) & 1)) ||
                                !wait_warp(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
                     break;
                 if (elect_one()) {
@@ -589,6 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 issued_kv = c + 1;
+                if (kState) {
+                    if (c + 2 < wk.n && elect_one()) {
+                        const int t2 = wk.start(c + 2, kReverse);
+                        for (int h = 0; h < 2; ++h) {
+                            tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
+                            tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
+                        }
+                    }
+                    continue;
+                }
                 if (c >= 2 && !wait_warp(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(&sm.full_q[s], kTile);
@@ -615,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------ P = Q K^T
             const uint32_t id = idesc_bf16(128, 128, 0, 0);
             const uint64_t qd0 = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
-            for (int c = 0; c < wk.n; ++c) {
+            for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.full_kv[s], (c >> 1) & 1) || !wait_warp(sm, &sm.full_q[s], (c >> 1) & 1))
                     break;
@@ -634,10 +763,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------ O = [P~ | Q~] [V ; S]
             const uint32_t idv = idesc_bf16(128, 128, 0, 1), ids = idesc_bf16(128, 128, 0, 0);
             const uint64_t vd0 = sdesc(smem_u32(sm.v), kHalf, 1024), sd0 = sdesc(smem_u32(sm.s), 16, 1024);
-            for (int c = 0; c < wk.n; ++c) {
+            for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait_warp(sm, &sm.s_ready, c & 1) ||
-                    !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) || !wait_warp(sm, &sm.kv_free, c & 1))
+                    !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) || !wait_warp(sm, &sm.kv_free[s], (c >> 1) & 1))
                     break;
                 tc_fence_after();
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
@@ -659,7 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int c = 0; c < wk.n && ok; ++c) {
                 const int s = c & 1;
-                if (c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)) break;
+                if (kState ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
+                           : c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1))
+                    break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd) {
@@ -672,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
                             for (int part = 0; part < 3; ++part)
-                                mma_ts(tb + kColX, tb + kColW + 48 * b + 16 * part + 8 * x,
+                                mma_ts(tb + col_kv<kState>(c), tb + kColW + 48 * b + 16 * part + 8 * x,
                                        kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
                         mma_commit(&sm.w_free[b]);
                         if (qd == 3) mma_commit(&sm.kv_done[s]);
@@ -690,16 +821,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();   // neither CTA leaves while the other may still write to it
     if (tid == 0 && sm.dead && a.status) atomicOr(a.status, GDN_DEVICE_WAIT_TIMEOUT);
     if (warp == kWarpLoad) tmem_dealloc(tb, kCols);
+}
+
+// Start states of a split sequence's segments: record k (the state after segment k alone,
+// segment 0's from its true start) becomes the state after segments 0 .. k.
+__global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ LinearArgs a) {
+    const int x = blockIdx.z, hv = blockIdx.y;
+    const int first = a.seg_first[x], nseg = a.seg_first[x + 1] - first;
+    if (nseg < 3) return;
+    const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
+    const double lam = exp((double)g * (double)a.seg_chunks * kC);
+    const float fh = (float)lam, fl = (float)(lam - (double)fh);
+    const size_t step = (size_t)a.HV * kDim * kDim;
+    float4 *p = reinterpret_cast<float4 *>(a.seg_state + ((size_t)first * a.HV + hv) * kDim * kDim) +
+                blockIdx.x * 256 + threadIdx.x;
+    float4 y = *p;
+    for (int k = 1; k < nseg - 1; ++k) {
+        p += step / 4;
+        float4 z = *p;
+        z.x = fmaf(y.x, fh, fmaf(y.x, fl, z.x));
+        z.y = fmaf(y.y, fh, fmaf(y.y, fl, z.y));
+        z.z = fmaf(y.z, fh, fmaf(y.z, fl, z.z));
+        z.w = fmaf(y.w, fh, fmaf(y.w, fl, z.w));
+        *p = z;
+        y = z;
+    }
+}
+
+template <bool kReverse, int kMode>
+cudaError_t launch_mode(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.items * a.HV));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(LinSmem) + 1024;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = kMode == 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_linear_tc<kReverse, kMode>, a, m);
 }
 
 template <bool kReverse>
 cudaError_t launch_dir(const LinearArgs &a, cudaStream_t s) {
     const int smem = (int)sizeof(LinSmem) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k_linear_tc<kReverse>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    // (the call above has made the device's context current, which the encoder needs)
+    cudaError_t e;
+    for (const void *k : {(const void *)k_linear_tc<kReverse, 0>, (const void *)k_linear_tc<kReverse, 1>,
+                          (const void *)k_linear_tc<kReverse, 2>})
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    // (the calls above have made the device's context current, which the encoder needs)
     LinMaps m;
     memset(&m, 0, sizeof(m));
     if (a.T > 0) {
@@ -707,11 +882,16 @@ cudaError_t launch_dir(const LinearArgs &a, cudaStream_t s) {
         if (!encode_rows_bf16(&m.q, a.q, a.nq, a.T, rowb, rowb * a.nq, kC) ||
             !encode_rows_bf16(&m.k, a.k, a.nk, a.T, rowb, rowb * a.nk, kC) ||
             !encode_rows_bf16(&m.v, a.v, a.nv, a.T, rowb, rowb * a.nv, kC) ||
-            (!a.part && !encode_rows_bf16(&m.o, a.o, a.HV, a.T, rowb, rowb * a.HV, kC)))
+            (!a.part && !encode_rows_bf16(&m.o, a.o, a.no, a.T, rowb, rowb * a.no, kC)))
             return cudaErrorInvalidValue;
+        if (a.part) m.o = m.v;   // not used, but fetched with the others
     }
-    k_linear_tc<kReverse><<<(unsigned)(a.N * a.HV), kThreads, smem, s>>>(a, m);
-    return cudaGetLastError();
+    if (a.seg_chunks > 0) {
+        if ((e = launch_mode<kReverse, 2>(a, m, s)) != cudaSuccess) return e;
+        k_linear_stitch<<<dim3(kDim * kDim / 1024, a.HV, a.N), 256, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return a.pair ? launch_mode<kReverse, 1>(a, m, s) : launch_mode<kReverse, 0>(a, m, s);
 }
 
 }  // namespace

@@ -319,9 +319,10 @@ gdn_status gdn_decode_step_gated(int32_t batch, int32_t num_k_heads, int32_t num
  * initial_state[n, hv] (or 0).  log_decay (fp32 [HV], device) is a constant of
  * the layer, <= 0 (0 = no decay, -inf = each token alone); it has no gradient.
  * The packing, the layouts, the conventions and the checks are those of the
- * chunk calls above: gdn_problem describes the pack (beta_dtype and
- * scan_segment_chunks must be valid but are not used), device_status collects
- * GDN_DEVICE_* bits, T == 0 passes the state through.  Within a chunk of tokens
+ * chunk calls above: gdn_problem describes the pack (beta_dtype must be valid but
+ * is not used; scan_segment_chunks plans the scans as above, in chunks of 128
+ * tokens: 0 = the library's plan, -1 = never split, L > 0 = segments of L),
+ * device_status collects GDN_DEVICE_* bits, T == 0 passes the state through.  Within a chunk of tokens
  * a NaN or infinity of one token may reach earlier tokens of the same sequence
  * (its products are masked by zeros); it never reaches another sequence.
  * ------------------------------------------------------------------------- */

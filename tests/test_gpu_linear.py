@@ -93,6 +93,45 @@ def test_backward(i, states):
     assert c.bwd(want_dh0=False)["dh0"] is None
 
 
+SPLITS = [([700], 1, 1, 1), ([700, 0, 129, 1], 1, 2, 2), ([300, 900], 2, 2, 3), ([640], 1, 3, 4), ([385], 1, 4, 1)]
+
+
+@pytest.mark.parametrize("lens, H, HV, seg", SPLITS)
+def test_split_scans(lens, H, HV, seg):
+    c = Case(lens, H, HV, seed=HV)
+    c.check_fwd(*c.fwd(scan_segment_chunks=seg))
+    c.check_bwd(c.bwd(scan_segment_chunks=seg))
+    # without splitting, the same values to the same bounds (checked above): outputs of the
+    # first segment are the same bits
+    whole = c.fwd(scan_segment_chunks=-1)[0]
+    assert torch.equal(c.fwd(scan_segment_chunks=seg)[0][:min(lens[0], 128 * seg)], whole[:min(lens[0], 128 * seg)])
+
+
+def test_the_plan_splits_a_long_sequence():
+    c = Case([5000, 2100], 1, 2)
+    n = [gdn.gdn_linear_attn_workspace_bytes(
+        gdn.make_problem(c.cu, 1, 2, cu_dev_ptr=c.cu_dev.data_ptr(), scan_segment_chunks=x)[0], 0) for x in (0, -1)]
+    assert n[0] > n[1]
+    c.check_fwd(*c.fwd())
+    c.check_bwd(c.bwd())
+
+
+def test_split_paged_prefill_starts_from_the_slot_it_ends_in():
+    c = Case([900, 260], 1, 2)
+    pool = torch.randn(3, 2, 128, 128, device="cuda")
+    c.h0 = pool[1:].transpose(2, 3).contiguous()
+    want, ht = c.fwd(scan_segment_chunks=2)
+    idx = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    o = gdn.linear_attn_prefill_paged(c.q, c.k, c.v, c.g, c.cu, c.cu_dev, pool, idx, scan_segment_chunks=2)
+    assert torch.equal(o, want) and torch.equal(pool[1:].transpose(2, 3), ht)
+
+
+def test_many_sequences():
+    c = Case([3, 0, 130] * 50, 1, 1)
+    c.check_fwd(*c.fwd())
+    c.check_bwd(c.bwd())
+
+
 def test_eight_value_heads_to_a_key_head():
     c = Case([200], 1, 8)
     c.check_fwd(*c.fwd())

@@ -73,7 +73,7 @@ struct LinSmem {
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
     uint64_t full_kv[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
     uint64_t kv_free[2], s_ready, o_free, o_staged, drain[3];
-    uint64_t peer_ok, rx_full;   // pair mode: the peer's Q tile is free; the peer's half of O is here
+    uint64_t peer_ok[2], rx_full[2];   // pair mode: the peer's Q tile is free; the peer's half of O is here
     uint32_t tmem_base;
     int dead;
 };
@@ -300,13 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.kv_done[i], 1);
                 mbar_init(&sm.o_done[i], 1);
                 mbar_init(&sm.q_free[i], 1);
+                mbar_init(&sm.peer_ok[i], 1);
+                mbar_init(&sm.rx_full[i], kGroupS * 16);
                 mbar_init(&sm.kv_free[i], kGroupS * 32);
             }
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
-            mbar_init(&sm.o_staged, kGroupS * (kPair ? 16 : 32));
-            mbar_init(&sm.peer_ok, 1);
-            mbar_init(&sm.rx_full, kGroupS * 16);
+            mbar_init(&sm.o_staged, kGroupS * 32);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
@@ -592,16 +592,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
             const uint64_t scale2 = pair(scale, scale);
             const bool keep = !kPair || (col >> 6) == (hv & 1);   // this warp's half is this CTA's to write
+            uint32_t from = tb + lanes + kColX + col;
             if (kPair) {
-                if (storer) remote_arrive(&sm.peer_ok, (hv & 1) ^ 1);
-                if (!wait_warp_cluster(sm, keep ? &sm.rx_full : &sm.peer_ok, c & 1)) break;
+                // O moves to this chunk's P buffer, which is free until the stage is loaded again:
+                // the exchange must not hold up the next KV
+                const uint32_t to = tb + lanes + kColP + 128 * s + col;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    tmem_ld32(from + 32 * h, x);
+                    tmem_ld_wait();
+                    tmem_st32(to + 32 * h, x);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.o_free);
+                from = to;
+                if (!wait_warp_cluster(sm, keep ? &sm.rx_full[s] : &sm.peer_ok[s], (c >> 1) & 1)) break;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x[32];
-                tmem_ld32(tb + lanes + kColX + col + 32 * h, x);
+                tmem_ld32(from + 32 * h, x);
                 tmem_ld_wait();
-                if (h == 1) {
+                if (!kPair && h == 1) {
                     tc_fence_before();
                     mbar_arrive(&sm.o_free);
                 }
@@ -655,9 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (kPair && !keep) remote_arrive(&sm.rx_full, (hv & 1) ^ 1);
-            if (kPair ? keep : staged) {
+            if (kPair && !keep) remote_arrive(&sm.rx_full[s], (hv & 1) ^ 1);
+            if (kPair || staged) {
                 fence_proxy_async_smem();
+                tc_fence_before();
                 mbar_arrive(&sm.o_staged);
             }
             if (c + 1 < wk.n) publish();
@@ -769,6 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) || !wait_warp(sm, &sm.kv_free[s], (c >> 1) & 1))
                     break;
                 tc_fence_after();
+                // this CTA's Q tile has been read: the peer may put its half of O there
+                if (kPair && elect_one()) remote_arrive(&sm.peer_ok[s], (hv & 1) ^ 1);
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
 #pragma unroll

@@ -71,9 +71,10 @@ struct LinSmem {
     float wtab[2 * kC];   // w lam^{127-x} (forward) or w lam^{x+1} (reverse), zeros above 128
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full_kv[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
+    uint64_t full_v[2], full_kq[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
     uint64_t kv_free[2], s_ready, o_free, o_staged, drain[3];
-    uint64_t peer_ok[2], rx_full[2];   // pair mode: the peer's Q tile is free; the peer's half of O is here
+    // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
+    uint64_t peer_ok[2], rx_full[2], sent[2];
     uint32_t tmem_base;
     int dead;
 };
@@ -172,9 +173,15 @@ __device__ __forceinline__ void remote_arrive(uint64_t *bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
                  : "memory");
 }
-__device__ __forceinline__ void remote_store(uint32_t addr, float a, float b, float c, float d) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
-                 : "memory");
+// Copy `bytes` of this CTA's shared memory to the same kind of place in the peer's; completes
+// on the peer's barrier.
+__device__ __forceinline__ void remote_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                            uint32_t rank) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            map_rank(smem_u32(dst), rank)),
+        "r"(smem_u32(src)), "r"(bytes), "r"(map_rank(smem_u32(bar), rank))
+        : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -290,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             if (wk.n > 0) tma_prefetch_maps(maps);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sm.full_kv[i], 1);
-                mbar_init(&sm.full_q[i], 1);
+                mbar_init(&sm.full_v[i], 1);
+                mbar_init(&sm.full_kq[i], 1);
                 mbar_init(&sm.p_done[i], 1);
                 mbar_init(&sm.pt_ready[i], kGroupP * 32);
                 mbar_init(&sm.v_ok[i], kGroupW * 32);
@@ -301,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.o_done[i], 1);
                 mbar_init(&sm.q_free[i], 1);
                 mbar_init(&sm.peer_ok[i], 1);
-                mbar_init(&sm.rx_full[i], kGroupS * 16);
+                mbar_init(&sm.rx_full[i], 1);
+                mbar_init(&sm.sent[i], 1);
                 mbar_init(&sm.kv_free[i], kGroupS * 32);
             }
             mbar_init(&sm.s_ready, kGroupS * 32);
@@ -419,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (!(ok = wait_warp(sm, &sm.full_kv[s], (c >> 1) & 1))) break;
+            if (!(ok = wait_warp(sm, &sm.full_v[s], (c >> 1) & 1))) break;
             if (L < kC) {
+                if (!(ok = wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1))) break;
                 // rows past the sequence hold the next one's tokens: zeros instead (each half
                 // clears its own quarters of K, which the product of a quarter waits for)
                 for (int x = quad * 32 + lane; x < 2 * 32 * 16; x += kGroupW * 16) {
@@ -592,59 +601,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
             const uint64_t scale2 = pair(scale, scale);
             const bool keep = !kPair || (col >> 6) == (hv & 1);   // this warp's half is this CTA's to write
-            uint32_t from = tb + lanes + kColX + col;
-            if (kPair) {
-                // O moves to this chunk's P buffer, which is free until the stage is loaded again:
-                // the exchange must not hold up the next KV
-                const uint32_t to = tb + lanes + kColP + 128 * s + col;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    tmem_ld32(from + 32 * h, x);
-                    tmem_ld_wait();
-                    tmem_st32(to + 32 * h, x);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&sm.o_free);
-                from = to;
-                if (!wait_warp_cluster(sm, keep ? &sm.rx_full[s] : &sm.peer_ok[s], (c >> 1) & 1)) break;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                tmem_ld32(from + 32 * h, x);
+            // 32 columns of row r, multiplied by its factor
+            auto read = [&](uint32_t from, float (&x)[32]) {
+                tmem_ld32(from, x);
                 tmem_ld_wait();
-                if (!kPair && h == 1) {
-                    tc_fence_before();
-                    mbar_arrive(&sm.o_free);
-                }
+            };
+            auto scaled = [&](float (&x)[32]) {
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     const float2 y = unpair(mul2(scale2, pair(x[j], x[j + 1])));
                     x[j] = y.x;
                     x[j + 1] = y.y;
                 }
-                if (kPair) {   // 32 columns of row r: a 128-byte row of plane h of the Q tile
-                    const uint32_t plane = smem_u32(sm.q[s] + h * kHalf) + r * 128;
-                    if (!keep) {
-                        const uint32_t there = map_rank(plane, (hv & 1) ^ 1);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            remote_store(there + ((j ^ (r & 7)) << 4), x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                        continue;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + h * kHalf + r * 128 +
-                                                                           ((j ^ (r & 7)) << 4));
-                        // (two terms: the same bits whichever CTA adds)
-                        x[4 * j] += y.x;
-                        x[4 * j + 1] += y.y;
-                        x[4 * j + 2] += y.z;
-                        x[4 * j + 3] += y.w;
-                    }
-                }
+            };
+            auto write = [&](int h, const float (&x)[32]) {
                 if (a.part) {
                     if (mine) {
 #pragma unroll
@@ -652,30 +622,106 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4 *>(a.part + row + 32 * h + 4 * j) =
                                 make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
                     }
-                } else {
-                    uint4 y[4];
+                    return;
+                }
+                uint4 y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[j] = make_uint4(
+                        epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
+                        epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
+                if (staged) {   // (pair mode: over plane 0's row, which only this thread reads)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        y[j] = make_uint4(
-                            epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
-                            epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
-                    if (staged) {   // (pair mode: over plane 0's row, which only this thread reads)
+                        *reinterpret_cast<uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4)) = y[j];
+                } else if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4)) = y[j];
-                    } else if (mine) {
+                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.o + row + 32 * h + 8 * j) = y[j];
+                }
+            };
+            const uint32_t from = tb + lanes + kColX + col;
+            if (!kPair) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.o + row + 32 * h + 8 * j) = y[j];
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    read(from + 32 * h, x);
+                    if (h == 1) {
+                        tc_fence_before();
+                        mbar_arrive(&sm.o_free);
+                    }
+                    scaled(x);
+                    write(h, x);
+                }
+                if (staged) {
+                    fence_proxy_async_smem();
+                    mbar_arrive(&sm.o_staged);
+                }
+                if (c + 1 < wk.n) publish();
+            } else {
+                // The exchange must not hold up the next KV.  The half that the peer writes goes to
+                // the stage's K tile, whose products are done, and from there to the peer's Q tile
+                // (rows of 32 columns, two planes); the own half to this chunk's P buffer, which
+                // is free until the stage is loaded again.
+                const uint32_t kept = tb + lanes + kColP + 128 * s + col;
+                const uint32_t peer = (hv & 1) ^ 1;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    read(from + 32 * h, x);
+                    if (keep) {
+                        tmem_st32(kept + 32 * h, x);
+                        continue;
+                    }
+                    if (h == 1) {
+                        tc_fence_before();
+                        mbar_arrive(&sm.o_free);
+                    }
+                    scaled(x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4 *>(sm.k[s] + h * kHalf + r * 128 + ((j ^ (r & 7)) << 4)) =
+                            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                }
+                if (keep) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&sm.o_free);
+                } else {
+                    fence_proxy_async_smem();
+                    if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
+                    if (lane == 0) {   // this warp's 32 rows
+                        for (int h = 0; h < 2; ++h)
+                            remote_copy(sm.q[s] + h * kHalf + (r & ~31) * 128, sm.k[s] + h * kHalf + (r & ~31) * 128,
+                                        32 * 128, &sm.rx_full[s], peer);
+                    }
+                    __syncwarp();
+                }
+                if (c + 1 < wk.n) publish();
+                if (keep) {
+                    if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
+                    if ((warp & 3) == 0 && lane == 0) remote_arrive(&sm.sent[s], peer);
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x[32];
+                        read(kept + 32 * h, x);
+                        scaled(x);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
+                            const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + h * kHalf + r * 128 +
+                                                                               ((j ^ (r & 7)) << 4));
+                            x[4 * j] += y.x;
+                            x[4 * j + 1] += y.y;
+                            x[4 * j + 2] += y.z;
+                            x[4 * j + 3] += y.w;
+                        }
+                        write(h, x);
                     }
                 }
-            }
-            if (kPair && !keep) remote_arrive(&sm.rx_full[s], (hv & 1) ^ 1);
-            if (kPair || staged) {
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(&sm.o_staged);
             }
-            if (c + 1 < wk.n) publish();
             if (kPair || staged) {
                 stores += 1;
                 if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1) && staged) {
@@ -709,60 +755,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (role == 0) {
             // ------------------------------------------------------ loads
             const int hq = hv / (a.HV / a.nq), hk = hv / (a.HV / a.nk), hw = hv / (a.HV / a.nv);
-            int issued_kv = 0, issued_q = 0;
+            int issued_v = 0, issued_kq = 0;
             for (int c = 0; c < wk.n; ++c) {
                 const int s = c & 1, t = wk.start(c, kReverse);
                 if (c >= 2 && ((!kState && !wait_warp(sm, &sm.o_done[s], ((c >> 1) - 1) & 1)) ||
                                !wait_warp(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
                     break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.full_kv[s], 2 * kTile);
-                    for (int h = 0; h < 2; ++h) {
-                        tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full_kv[s]);
-                        tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_kv[s]);
-                    }
-                }
-                issued_kv = c + 1;
-                if (kState) {
-                    if (c + 2 < wk.n && elect_one()) {
-                        const int t2 = wk.start(c + 2, kReverse);
-                        for (int h = 0; h < 2; ++h) {
-                            tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
-                            tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
-                        }
-                    }
-                    continue;
-                }
-                if (c >= 2 && !wait_warp(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.full_q[s], kTile);
+                    mbar_arrive_expect_tx(&sm.full_v[s], kTile);
                     for (int h = 0; h < 2; ++h)
-                        tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_q[s]);
+                        tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_v[s]);
+                }
+                issued_v = c + 1;
+                // the last output of this stage has left its Q tile (and the exchange its K tile)
+                if (!kState && c >= 2 && !wait_warp(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
+                if (kPair && c >= 2 && !wait_warp_cluster(sm, &sm.sent[s], ((c >> 1) - 1) & 1)) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sm.full_kq[s], kState ? kTile : 2 * kTile);
+                    for (int h = 0; h < 2; ++h) {
+                        tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full_kq[s]);
+                        if (!kState) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_kq[s]);
+                    }
                     // the tiles after next start towards L2 while both stages are taken
                     if (c + 2 < wk.n) {
                         const int t2 = wk.start(c + 2, kReverse);
                         for (int h = 0; h < 2; ++h) {
-                            tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
                             tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
-                            tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
+                            tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
+                            if (!kState) tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
                         }
                     }
                 }
-                issued_q = c + 1;
+                issued_kq = c + 1;
             }
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
-            for (int c = max(0, issued_kv - 2); c < issued_kv; ++c)
-                mbar_wait(&sm.full_kv[c & 1], (c >> 1) & 1, kDrainLimitNs);
-            for (int c = max(0, issued_q - 2); c < issued_q; ++c)
-                mbar_wait(&sm.full_q[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            for (int c = max(0, issued_v - 2); c < issued_v; ++c)
+                mbar_wait(&sm.full_v[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            for (int c = max(0, issued_kq - 2); c < issued_kq; ++c)
+                mbar_wait(&sm.full_kq[c & 1], (c >> 1) & 1, kDrainLimitNs);
         } else if (role == 1) {
             // ------------------------------------------------------ P = Q K^T
             const uint32_t id = idesc_bf16(128, 128, 0, 0);
             const uint64_t qd0 = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
             for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
-                if (!wait_warp(sm, &sm.full_kv[s], (c >> 1) & 1) || !wait_warp(sm, &sm.full_q[s], (c >> 1) & 1))
-                    break;
+                if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
                 // (loading this stage waited for O of chunk c - 2, which read this P buffer)
                 tc_fence_after();
                 const uint64_t qd = qd0 + ((s * kTile) >> 4), kd = kd0 + ((s * kTile) >> 4);
@@ -785,7 +822,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 tc_fence_after();
                 // this CTA's Q tile has been read: the peer may put its half of O there
-                if (kPair && elect_one()) remote_arrive(&sm.peer_ok[s], (hv & 1) ^ 1);
+                if (kPair && elect_one()) {
+                    mbar_arrive_expect_tx(&sm.rx_full[s], kTile);
+                    remote_arrive(&sm.peer_ok[s], (hv & 1) ^ 1);
+                }
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
 #pragma unroll
@@ -808,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kState ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
                            : c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1))
                     break;
+                if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd) {

@@ -74,7 +74,7 @@ struct LinSmem {
     uint64_t full_v[2], full_kq[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
     uint64_t kv_free[2], s_ready, o_free, o_staged, drain[3];
     // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
-    uint64_t peer_ok[2], rx_full[2], sent[2];
+    uint64_t peer_ok[2], rx_full[2], sent[2], kept[2], rx_read;
     uint32_t tmem_base;
     int dead;
 };
@@ -252,6 +252,42 @@ __device__ __forceinline__ void read_power(float g2, int i, int L, float &e, flo
     f = x - e;
 }
 
+// 32 columns of output row r: times the row's factor, and out (element `at` of the output, or
+// columns 32 h .. of the swizzled bf16 row `place` in shared memory when staged).
+__device__ __forceinline__ void scale32(float (&x)[32], float scale) {
+    const uint64_t s2 = pair(scale, scale);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float2 y = unpair(mul2(s2, pair(x[j], x[j + 1])));
+        x[j] = y.x;
+        x[j + 1] = y.y;
+    }
+}
+__device__ __forceinline__ void write32(const LinearArgs &a, const float (&x)[32], size_t at, bool mine,
+                                        bool staged, unsigned char *place, int r, int h) {
+    if (a.part) {
+        if (mine) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float4 *>(a.part + at + 4 * j) =
+                    make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        }
+        return;
+    }
+    uint4 y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        y[j] = make_uint4(epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
+                          epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
+    if (staged) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(place + (((4 * h + j) ^ (r & 7)) << 4)) = y[j];
+    } else if (mine) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.o + at + 8 * j) = y[j];
+    }
+}
+
 // kMode 0: outputs and states.  1: outputs summed over the two value heads of a cluster of
 // two CTAs.  2: only the states, of every segment but a sequence's last (their sums are the
 // start states of the segments that a second launch walks at once).
@@ -310,11 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.peer_ok[i], 1);
                 mbar_init(&sm.rx_full[i], 1);
                 mbar_init(&sm.sent[i], 1);
+                mbar_init(&sm.kept[i], kGroupS * 16);
                 mbar_init(&sm.kv_free[i], kGroupS * 32);
             }
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
-            mbar_init(&sm.o_staged, kGroupS * 32);
+            mbar_init(&sm.o_staged, (kPair ? kGroupW : kGroupS) * 32);
+            mbar_init(&sm.rx_read, kGroupW * 32);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
@@ -424,6 +462,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t chunk[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) chunk[x] = (uint32_t)((4 * (quad & 1) + x) ^ (lane & 7)) * 16;
+        // Pair mode: this group, which has the most time to spare, also adds the two
+        // halves of chunk c's outputs and writes them.
+        const int i = quad * 32 + lane;
+        const bool lead = tid == kGroupP * 32;
+        auto finish = [&](int c) -> bool {
+            const int s = c & 1, L = wk.length(c, kReverse), mark = (c >> 1) & 1;
+            if (!wait_warp(sm, &sm.kept[s], mark) || !wait_warp_cluster(sm, &sm.rx_full[s], mark)) return false;
+            if (lead) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
+            tc_fence_after();
+            float x[32];
+            tmem_ld32(tb + lanes + kColP + 128 * s + 64 * (hv & 1) + 32 * half, x);
+            tmem_ld_wait();
+            float e, f;
+            read_power<kReverse>(g2, i, L, e, f);
+            scale32(x, a.so * ex2(f));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
+                const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + half * kHalf + i * 128 +
+                                                                   ((j ^ (i & 7)) << 4));
+                x[4 * j] += y.x;
+                x[4 * j + 1] += y.y;
+                x[4 * j + 2] += y.z;
+                x[4 * j + 3] += y.w;
+            }
+            mbar_arrive(&sm.rx_read);   // the output's rows take plane 0's place
+            if (!wait_warp(sm, &sm.rx_read, c & 1)) return false;
+            const size_t t = (size_t)wk.start(c, kReverse) + i;
+            const size_t out = (t * a.no + (hv >> 1)) * kDim + 64 * (hv & 1) + 32 * half;
+            const bool staged = L == kC && !a.part;
+            const bool mine = i < L && in_range(out, 32, (long long)a.T * a.no * kDim, a.status);
+            write32(a, x, out, mine, staged, sm.q[s] + i * 128, i, half);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(&sm.o_staged);
+            bool ok = true;
+            if (lead && (ok = wait(sm, &sm.o_staged, c & 1))) {
+                if (staged) {
+                    tma_store_3d(&maps.o, 64 * (hv & 1), hv >> 1, wk.start(c, kReverse), sm.q[s]);
+                    tma_store_commit();
+                    tma_store_wait_read();
+                }
+                mbar_arrive(&sm.q_free[s]);
+            }
+            return __all_sync(0xffffffffu, ok);
+        };
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
@@ -489,6 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&sm.w_ready[half]);
             }
+            if (kPair && ok && c > 0) ok = finish(c - 1);
+        }
+        if (kPair) {
+            if (ok && wk.n > 0) finish(wk.n - 1);
+            if (lead) tma_store_wait_all();
         }
     } else if (warp < kWarpLoad) {
         // ---------------------------------------------------------- state and output
@@ -565,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool storer = tid == (kGroupP + kGroupW) * 32;
         for (int c = 0; c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (!kState && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
+            if (kMode == 0 && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
                 tma_store_wait_read();
                 mbar_arrive(&sm.q_free[s ^ 1]);
             }
@@ -593,81 +681,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             float e, f;
             read_power<kReverse>(g2, r, L, e, f);
             const float scale = a.so * ex2(f);
-            const size_t t = (size_t)wk.start(c, kReverse) + r;
-            const size_t row = (t * a.no + (kPair ? hv >> 1 : hv)) * kDim + col;
-            const bool staged = L == kC && !a.part;   // whole chunks of bf16 leave by TMA
-            const bool mine = r < L && in_range(row, 64, (long long)a.T * a.no * kDim, a.status);
-            // the stage's Q tile is free: its readers finished before O did
-            unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
-            const uint64_t scale2 = pair(scale, scale);
-            const bool keep = !kPair || (col >> 6) == (hv & 1);   // this warp's half is this CTA's to write
-            // 32 columns of row r, multiplied by its factor
-            auto read = [&](uint32_t from, float (&x)[32]) {
-                tmem_ld32(from, x);
-                tmem_ld_wait();
-            };
-            auto scaled = [&](float (&x)[32]) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 y = unpair(mul2(scale2, pair(x[j], x[j + 1])));
-                    x[j] = y.x;
-                    x[j + 1] = y.y;
-                }
-            };
-            auto write = [&](int h, const float (&x)[32]) {
-                if (a.part) {
-                    if (mine) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4 *>(a.part + row + 32 * h + 4 * j) =
-                                make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-                    }
-                    return;
-                }
-                uint4 y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    y[j] = make_uint4(
-                        epi::pack_bf2(x[8 * j], x[8 * j + 1]), epi::pack_bf2(x[8 * j + 2], x[8 * j + 3]),
-                        epi::pack_bf2(x[8 * j + 4], x[8 * j + 5]), epi::pack_bf2(x[8 * j + 6], x[8 * j + 7]));
-                if (staged) {   // (pair mode: over plane 0's row, which only this thread reads)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4)) = y[j];
-                } else if (mine) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.o + row + 32 * h + 8 * j) = y[j];
-                }
-            };
             const uint32_t from = tb + lanes + kColX + col;
             if (!kPair) {
+                const size_t row = (((size_t)wk.start(c, kReverse) + r) * a.no + hv) * kDim + col;
+                const bool staged = L == kC && !a.part;   // whole chunks of bf16 leave by TMA
+                const bool mine = r < L && in_range(row, 64, (long long)a.T * a.no * kDim, a.status);
+                // the stage's Q tile is free: its readers finished before O did
+                unsigned char *orow = sm.q[s] + (col >> 6) * kHalf + r * 128;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[32];
-                    read(from + 32 * h, x);
+                    tmem_ld32(from + 32 * h, x);
+                    tmem_ld_wait();
                     if (h == 1) {
                         tc_fence_before();
                         mbar_arrive(&sm.o_free);
                     }
-                    scaled(x);
-                    write(h, x);
+                    scale32(x, scale);
+                    write32(a, x, row + 32 * h, mine, staged, orow, r, h);
                 }
                 if (staged) {
                     fence_proxy_async_smem();
                     mbar_arrive(&sm.o_staged);
                 }
                 if (c + 1 < wk.n) publish();
+                if (staged) {
+                    stores += 1;
+                    if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1)) {
+                        for (int h = 0; h < 2; ++h)
+                            tma_store_3d(&maps.o, 64 * h, hv, wk.start(c, kReverse), sm.q[s] + h * kHalf);
+                        tma_store_commit();
+                    }
+                    __syncwarp();
+                }
             } else {
                 // The exchange must not hold up the next KV.  The half that the peer writes goes to
                 // the stage's K tile, whose products are done, and from there to the peer's Q tile
                 // (rows of 32 columns, two planes); the own half to this chunk's P buffer, which
                 // is free until the stage is loaded again.
                 const uint32_t kept = tb + lanes + kColP + 128 * s + col;
-                const uint32_t peer = (hv & 1) ^ 1;
+                const bool keep = (col >> 6) == (hv & 1);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[32];
-                    read(from + 32 * h, x);
+                    tmem_ld32(from + 32 * h, x);
+                    tmem_ld_wait();
                     if (keep) {
                         tmem_st32(kept + 32 * h, x);
                         continue;
@@ -676,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_before();
                         mbar_arrive(&sm.o_free);
                     }
-                    scaled(x);
+                    scale32(x, scale);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         *reinterpret_cast<float4 *>(sm.k[s] + h * kHalf + r * 128 + ((j ^ (r & 7)) << 4)) =
@@ -686,51 +744,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&sm.o_free);
+                    mbar_arrive(&sm.kept[s]);
                 } else {
                     fence_proxy_async_smem();
                     if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
                     if (lane == 0) {   // this warp's 32 rows
                         for (int h = 0; h < 2; ++h)
                             remote_copy(sm.q[s] + h * kHalf + (r & ~31) * 128, sm.k[s] + h * kHalf + (r & ~31) * 128,
-                                        32 * 128, &sm.rx_full[s], peer);
+                                        32 * 128, &sm.rx_full[s], (hv & 1) ^ 1);
                     }
                     __syncwarp();
                 }
                 if (c + 1 < wk.n) publish();
-                if (keep) {
-                    if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
-                    if ((warp & 3) == 0 && lane == 0) remote_arrive(&sm.sent[s], peer);
-                    tc_fence_after();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float x[32];
-                        read(kept + 32 * h, x);
-                        scaled(x);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
-                            const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + h * kHalf + r * 128 +
-                                                                               ((j ^ (r & 7)) << 4));
-                            x[4 * j] += y.x;
-                            x[4 * j + 1] += y.y;
-                            x[4 * j + 2] += y.z;
-                            x[4 * j + 3] += y.w;
-                        }
-                        write(h, x);
-                    }
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                mbar_arrive(&sm.o_staged);
-            }
-            if (kPair || staged) {
-                stores += 1;
-                if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1) && staged) {
-                    for (int h = 0; h < (kPair ? 1 : 2); ++h)
-                        tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv,
-                                     wk.start(c, kReverse), sm.q[s] + h * kHalf);
-                    tma_store_commit();
-                }
-                __syncwarp();
             }
         }
         if (storer) tma_store_wait_all();

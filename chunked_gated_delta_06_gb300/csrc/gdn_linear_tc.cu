@@ -238,10 +238,12 @@ struct Walk {      // the chunks of this CTA's segment, in scan order
     __device__ __forceinline__ int length(int c, bool rev) const { return min(kC, len - chunk(c, rev) * kC); }
 };
 
-// Column of chunk c's KV: without outputs the P buffers are free, and two chunks alternate.
-template <bool kState>
+// Columns of chunk c's KV.  Mode 0: the P buffer of chunk c - 1, whose readers end with O of
+// that chunk and which chunk c + 1 needs next; so KV waits for no epilogue.  Mode 1 keeps
+// outputs there, so that KV and O take turns in one region.  Mode 2: two regions in turns.
+template <int kMode>
 __device__ __forceinline__ uint32_t col_kv(int c) {
-    return kState && (c & 1) ? kColP : kColX;
+    return kMode == 0 ? kColP + 128 * ((c + 1) & 1) : kMode == 2 && (c & 1) ? kColP : kColX;
 }
 
 // lam^{i+1} (forward) or lam^{L-1-i} (reverse) as 2^{e + f}, e whole and 0 <= f < 1.
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float x[32];
-                tmem_ld32(tb + lanes + col_kv<kState>(c) + col + 32 * h, x);
+                tmem_ld32(tb + lanes + col_kv<kMode>(c) + col + 32 * h, x);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
@@ -826,6 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
                 // (loading this stage waited for O of chunk c - 2, which read this P buffer)
+                if (kMode == 0 && c > 0 && !wait_warp(sm, &sm.kv_free[s ^ 1], ((c - 1) >> 1) & 1)) break;
                 tc_fence_after();
                 const uint64_t qd = qd0 + ((s * kTile) >> 4), kd = kd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
@@ -843,7 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait_warp(sm, &sm.s_ready, c & 1) ||
-                    !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) || !wait_warp(sm, &sm.kv_free[s], (c >> 1) & 1))
+                    !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) ||
+                    (kPair ? !wait_warp(sm, &sm.kv_free[s], (c >> 1) & 1)
+                           : c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)))
                     break;
                 tc_fence_after();
                 // this CTA's Q tile has been read: the peer may put its half of O there
@@ -870,8 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int c = 0; c < wk.n && ok; ++c) {
                 const int s = c & 1;
-                if (kState ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
-                           : c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1))
+                if (kState   ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
+                    : kPair ? c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)
+                            : c > 0 && !wait_warp(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1))
                     break;
                 if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
@@ -886,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
                             for (int part = 0; part < 3; ++part)
-                                mma_ts(tb + col_kv<kState>(c), tb + kColW + 48 * b + 16 * part + 8 * x,
+                                mma_ts(tb + col_kv<kMode>(c), tb + kColW + 48 * b + 16 * part + 8 * x,
                                        kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
                         mma_commit(&sm.w_free[b]);
                         if (qd == 3) mma_commit(&sm.kv_done[s]);

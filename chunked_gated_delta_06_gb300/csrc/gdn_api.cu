@@ -447,8 +447,8 @@ gdn_status decode_impl(int32_t batch, int32_t num_k_heads, int32_t num_v_heads, 
 // How the scans of one problem are run: a CTA walks the 128-token chunks of one (sequence,
 // value head), about as long for each.  Few long sequences leave SMs idle, so a split plan
 // cuts every sequence into segments of `seg` chunks: a pass over the states alone, a stitch,
-// and the full pass over all segments at once.  Costs in chunks of the full pass: 0.45 for a
-// chunk of the state pass, 2.5 for a CTA's start and end, 2 for the two launches more; a
+// and the full pass over all segments at once.  Costs in chunks of the full pass: 0.35 for a
+// chunk of the state pass, 2 for a CTA's start and end, 2 for the two launches more; a
 // launch takes the longer of one CTA and the work over 152 SMs, and half a CTA more when
 // they take turns.  A split has to gain a tenth.  A function of the problem alone.
 struct LinearPlan {
@@ -464,7 +464,7 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
     auto chunks = [&](int n) {
         return (int)(((int64_t)p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n] + 127) / 128);
     };
-    const double start = 2.5, state = 0.45;
+    const double start = 2.0, state = 0.35;
     int longest = 0;
     double work = 0.0;
     for (int n = 0; n < d.N; ++n) {
@@ -502,27 +502,28 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
 // heads, or an odd number, share a key head (summed in order afterwards), and the states
 // between the segments of a split scan.
 struct LinearWs {
-    float *part, *seg_state;
+    float *part[2], *seg_state[2];   // dq, dk; the states of the forward scan and of the reverse ones
 };
 size_t carve_linear(const Dims &d, const LinearPlan &plan, int for_backward, void *base, LinearWs *w) {
     Carver cv(base);
     const int r = d.HV / d.H, no = r % 2 ? d.HV : d.HV / 2;
-    w->part = w->seg_state = nullptr;
-    if (for_backward && no != d.H) w->part = cv.take<float>((size_t)d.T * no * gdn::kDim);
-    if (plan.seg) w->seg_state = cv.take<float>((size_t)plan.items * d.HV * gdn::kDim * gdn::kDim);
+    *w = LinearWs{};
+    for (int i = 0; i <= for_backward; ++i) {
+        if (for_backward && no != d.H) w->part[i] = cv.take<float>((size_t)d.T * no * gdn::kDim);
+        if (plan.seg) w->seg_state[i] = cv.take<float>((size_t)plan.items * d.HV * gdn::kDim * gdn::kDim);
+    }
     return cv.used() > 0 ? cv.used() : kAlign;
 }
 
-gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan, const LinearWs &ws,
+gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan,
                             const float *log_decay) {
     gdn::LinearArgs a{};
     const int32_t *cu = p->cu_seqlens_host;
     a.N = d.N;
     a.T = d.T;
-    a.HV = a.no = d.HV;
+    a.HV = d.HV;
     a.items = plan.items;
     a.seg_chunks = plan.seg;
-    a.seg_state = ws.seg_state;
     for (int n = 0; n < d.N; ++n) a.longest = std::max(a.longest, cu[n + 1] - cu[n]);
     if (d.N <= gdn::kLinearOrder) {
         for (int n = 0; n < d.N; ++n) a.order[n] = (uint16_t)n;
@@ -536,24 +537,27 @@ gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPla
         for (int n = 0; n <= d.N; ++n) a.cu[n] = cu[n];
     }
     a.log_decay = log_decay;
-    a.so = d.scale;
-    a.w = 1.f;
-    a.s_rs = 1;           // K-major states: S[r][c] at c * 128 + r
-    a.s_cs = gdn::kDim;
     a.cu_dev = p->cu_seqlens_dev;
     a.status = p->device_status;
     return a;
 }
 
-// The roles of one scan: output reads q against the state of k and v.
-void linear_roles(gdn::LinearArgs &a, const void *q, int nq, const void *k, int nk, const void *v,
-                  int nv) {
-    a.q = static_cast<const bf16 *>(q);
-    a.k = static_cast<const bf16 *>(k);
-    a.v = static_cast<const bf16 *>(v);
-    a.nq = nq;
-    a.nk = nk;
-    a.nv = nv;
+// One scan: output o reads q against the state of k and v (K-major states hold S by columns).
+gdn::LinearPass linear_pass(const void *q, int nq, const void *k, int nk, const void *v, int nv, void *o,
+                            float so, float w, bool rows) {
+    gdn::LinearPass x{};
+    x.q = static_cast<const bf16 *>(q);
+    x.k = static_cast<const bf16 *>(k);
+    x.v = static_cast<const bf16 *>(v);
+    x.nq = nq;
+    x.nk = nk;
+    x.nv = nv;
+    x.o = static_cast<bf16 *>(o);
+    x.so = so;
+    x.w = w;
+    x.rows = rows;
+    x.seg_rows = 1;
+    return x;
 }
 
 gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, const void *v,
@@ -579,19 +583,20 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
     const LinearPlan plan = plan_linear(p, d);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
     if (ws_size < carve_linear(d, plan, 0, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
-    gdn::LinearArgs a = linear_args(d, p, plan, ws, log_decay);
-    linear_roles(a, q, d.H, k, d.H, v, d.HV);
-    a.o = static_cast<bf16 *>(o);
-    a.s0 = initial_state;
-    a.s1 = final_state;
+    gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
+    a.passes = a.state_passes = 1;
+    gdn::LinearPass &x = a.pass[0];
+    x = linear_pass(q, d.H, k, d.H, v, d.HV, o, d.scale, 1.f, pg != nullptr);   // slots are V-major
+    x.no = d.HV;
+    x.s0 = initial_state;
+    x.s1 = final_state;
+    x.seg_state = ws.seg_state[0];
     if (pg) {
         a.pool = pg->pool;
         a.num_slots = pg->num_slots;
         a.pool_idx = pg->indices;
         a.pool_resume = pg->resume;
         a.pool_status = pg->status;
-        a.s_rs = gdn::kDim;   // V-major slots
-        a.s_cs = 1;
     }
     return cuda_status(gdn::launch_linear_tc(a, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -786,41 +791,28 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
     if (ws_size < carve_linear(d, plan, 1, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    // dq: a forward scan over (d_o, v, k), the state transposed
-    gdn::LinearArgs a = linear_args(d, p, plan, ws, log_decay);
+    gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
+    a.passes = 3;
+    a.state_passes = 2;
+    a.pass[0] = linear_pass(d_o, d.HV, v, d.HV, k, d.H, dq, d.scale, 1.f, true);
+    a.pass[1] = linear_pass(v, d.HV, d_o, d.HV, q, d.H, dk, 1.f, d.scale, true);
+    a.pass[2] = linear_pass(k, d.H, q, d.H, d_o, d.HV, dv, 1.f, d.scale, false);
     const int r = d.HV / d.H;
-    a.pair = r % 2 == 0;   // pairs of value heads are summed inside the scan
-    a.no = a.pair ? d.HV / 2 : d.HV;
-    linear_roles(a, d_o, d.HV, v, d.HV, k, d.H);
-    a.s0 = initial_state;
-    a.s_rs = gdn::kDim;
-    a.s_cs = 1;
-    a.o = static_cast<bf16 *>(dq);
-    a.part = ws.part;
-    if ((e = gdn::launch_linear_tc(a, s)) != cudaSuccess) return cuda_status(e);
-    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, a.no, a.status, s)) != cudaSuccess)
-        return cuda_status(e);
-    // dk: a reverse scan over (v, d_o, q), the state transposed
-    a.reverse = 1;
-    a.s0 = d_final_state;
-    a.so = 1.f;
-    a.w = d.scale;
-    linear_roles(a, v, d.HV, d_o, d.HV, q, d.H);
-    a.o = static_cast<bf16 *>(dk);
-    if ((e = gdn::launch_linear_tc(a, s)) != cudaSuccess) return cuda_status(e);
-    if (ws.part && (e = gdn::launch_linear_heads(ws.part, a.o, d.T, d.H, a.no, a.status, s)) != cudaSuccess)
-        return cuda_status(e);
-    // dv: a reverse scan over (k, q, d_o); it ends with dh0
-    linear_roles(a, k, d.H, q, d.H, d_o, d.HV);
-    a.s_rs = 1;
-    a.s_cs = gdn::kDim;
-    a.o = static_cast<bf16 *>(dv);
-    a.part = nullptr;
-    a.pair = 0;
-    a.no = d.HV;
-    a.s1 = dh0;
-    return cuda_status(gdn::launch_linear_tc(a, s));
+    for (int i = 0; i < 2; ++i) {
+        a.pass[i].pair = r % 2 == 0;   // pairs of value heads are summed inside the scan
+        a.pass[i].no = r % 2 == 0 ? d.HV / 2 : d.HV;
+        a.pass[i].part = ws.part[i];
+    }
+    a.pass[2].no = d.HV;
+    a.pass[0].s0 = initial_state;
+    a.pass[1].s0 = a.pass[2].s0 = d_final_state;
+    a.pass[2].s1 = dh0;
+    a.pass[0].seg_state = ws.seg_state[0];
+    a.pass[1].seg_state = a.pass[2].seg_state = ws.seg_state[1];
+    a.pass[1].seg_rows = 0;   // dv's states, transposed
+    cudaError_t e = gdn::launch_linear_tc(a, s);
+    if (e == cudaSuccess && ws.part[0]) e = gdn::launch_linear_heads(a, d.H, s);
+    return cuda_status(e);
 }
 
 gdn_status gdn_linear_attn_step(int32_t batch, int32_t num_k_heads, int32_t num_v_heads,

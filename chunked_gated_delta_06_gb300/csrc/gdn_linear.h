@@ -11,44 +11,52 @@ constexpr int kLinearOrder = 128;   // packs of at most this many sequences star
 // lam = e^{log_decay[hv]} (rows r = feature of v, columns c = feature of q and k):
 //   forward:  S <- lam S + w v_t k_t^T,  o_t = so S q_t           (t ascending)
 //   reverse:  S <- S + w v_t k_t^T,  o_t = so S q_t,  S <- lam S  (t descending)
-// The forward call is one such scan; the backward is three of them with the roles of
-// the tensors exchanged (see gdn_linear.cu).  A role tensor with n heads is read at
-// head hv / (HV / n).
-struct LinearArgs {
-    int N, T, HV;
-    int longest;              // tokens of the longest sequence (host copy of cu_seqlens)
+// The forward call is one such scan; the backward is three of them with the roles of the
+// tensors exchanged.  With S the state (rows: v, columns: k) and dS the gradient of the state
+// after token t (dS_t = lam dS_{t+1} + scale do_t q_t^T):
+//   dq_t = scale S_t^T do_t     forward scan, (q, k, v) <- (do, v, k), state transposed
+//   dk_t = dS_t^T v_t           reverse scan, (q, k, v) <- (v, do, q), w = scale, transposed
+//   dv_t = dS_t k_t             reverse scan, (q, k, v) <- (k, q, do), w = scale
+// and dh0 is the state that either reverse scan ends with.
+// A role tensor with n heads is read at head hv / (HV / n).
+struct LinearPass {
     const bf16 *q, *k, *v;    // [T, nq | nk | nv, 128]
     int nq, nk, nv;
     bf16 *o;                  // [T, no, 128], or null
     float *part;              // [T, no, 128]: fp32 outputs instead of o (summed by launch_linear_heads)
     int no;                   // output heads: HV, or HV / 2 with pair
     int pair;                 // value heads 2 x and 2 x + 1 are summed into output head x
-    const float *log_decay;   // [HV]
     const float *s0;          // [N, HV, 128, 128] or null (zeros)
     float *s1;                // the same shape, or null
-    int s_rs, s_cs;           // element strides of (r, c) in s0, s1 and the pool's slots
+    int rows;                 // s0, s1 and the pool's slots hold S row by row (else column by column)
+    float *seg_state;         // split scans: [items, HV, 128, 128] states after each inner segment,
+    int seg_rows;             // row by row, or column by column (another scan's transposed states)
+    float so, w;              // output and update factors
+};
+struct LinearArgs {
+    int N, T, HV;
+    int longest;              // tokens of the longest sequence (host copy of cu_seqlens)
+    const float *log_decay;   // [HV]
+    LinearPass pass[3];       // a forward's one scan; a backward's dq, dk, dv
+    int passes, state_passes; // 1 and 1, or 3 and 2 (dk starts its segments from dv's states)
     float *pool;              // [num_slots, HV, V, K] in place of s0 / s1 (paged prefill), or null
     int num_slots;
     const int *pool_idx, *pool_resume;
     int *pool_status;
-    float so, w;              // output and update factors
-    int reverse;
     const int *cu_dev;        // [N + 1]
     int *status;
     // Work items: (sequence, segment), grid order.  seg_chunks > 0 (N <= kLinearOrder only) cuts
     // the sequences into segments of that many chunks, which are walked at once.
     int items, seg_chunks;
-    float *seg_state;              // [items, HV, 128, 128] states after each inner segment
     uint16_t order[kLinearOrder];  // N <= kLinearOrder: sequences by decreasing length,
     int seg_first[kLinearOrder + 1];  // the first item of each, in that order,
-    int cu[kLinearOrder + 1];      // and the host's cu_seqlens, which the device's must equal
+    int cu[kLinearOrder + 1];      // and the host's cu_seqlens
 };
 
-cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t s);
 cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s);
-// out[t][h] = sum of part[t][hv] over the HV / H value heads of key head h, in order, as bf16.
-cudaError_t launch_linear_heads(const float *part, bf16 *out, int T, int H, int HV, int *status,
-                                cudaStream_t s);
+// dq and dk from the scans' fp32 outputs: out[t][h] = sum of part[t][x] over the no / H heads x
+// of key head h, in order, as bf16 (passes 0 and 1 of a).
+cudaError_t launch_linear_heads(const LinearArgs &a, int H, cudaStream_t s);
 
 cudaError_t launch_linear_step(int B, int H, int HV, float scale, const bf16 *q, const bf16 *k,
                                const bf16 *v, const float *log_decay, float *pool, int num_slots,

@@ -34,6 +34,7 @@
 
 #include <initializer_list>
 
+
 #include "gdn_epi.cuh"
 #include "gdn_linear.h"
 #include "gdn_tma.h"
@@ -62,7 +63,8 @@ static_assert((kGroupP + kGroupW) * kRegsWork + kGroupS * kRegsState + 4 * kRegs
 constexpr uint32_t kColP = 0;      // two buffers of 128: P fp32; then, per half h of 64: P~ of tokens
                                    // 64 h .. in 32 columns and Q~ of features 64 h .. in the next 32
 constexpr uint32_t kColX = 256;    // KV of a chunk, then its O
-constexpr uint32_t kColW = 384;    // two buffers of 48: 32 tokens of W, three parts of 16
+constexpr uint32_t kColW = 384;    // two buffers of 48: 32 tokens of W, three parts of 16 (the state
+                                   // pass has two more in the second P buffer)
 constexpr uint32_t kCols = 512;
 
 struct LinSmem {
@@ -71,8 +73,8 @@ struct LinSmem {
     float wtab[2 * kC];   // w lam^{127-x} (forward) or w lam^{x+1} (reverse), zeros above 128
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full_v[2], full_kq[2], p_done[2], pt_ready[2], v_ok[2], w_ready[2], w_free[2], kv_done[2], o_done[2], q_free[2];
-    uint64_t kv_free[2], s_ready, o_free, o_staged, drain[3];
+    uint64_t full_v[2], full_kq[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], q_free[2];
+    uint64_t kv_free[2], s_ready, o_free, o_staged, factors, drain[3];
     // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
     uint64_t peer_ok[2], rx_full[2], sent[2], kept[2], rx_read;
     uint32_t tmem_base;
@@ -82,7 +84,9 @@ static_assert(offsetof(LinSmem, s) % 1024 == 0, "SW128 tiles on 1024-byte bounda
 static_assert(sizeof(LinSmem) + 1024 <= 232448, "one CTA per SM");
 
 struct LinMaps {
-    CUtensorMap q, k, v, o;
+    struct Pass {
+        CUtensorMap q, k, v, o;
+    } pass[3];
 };
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool acc) {
@@ -245,6 +249,7 @@ template <int kMode>
 __device__ __forceinline__ uint32_t col_kv(int c) {
     return kMode == 0 ? kColP + 128 * ((c + 1) & 1) : kMode == 2 && (c & 1) ? kColP : kColX;
 }
+__device__ __forceinline__ uint32_t col_w(int b) { return b < 2 ? kColW + 48 * b : kColP + 128 + 48 * (b - 2); }
 
 // lam^{i+1} (forward) or lam^{L-1-i} (reverse) as 2^{e + f}, e whole and 0 <= f < 1.
 template <bool kReverse>
@@ -265,7 +270,7 @@ __device__ __forceinline__ void scale32(float (&x)[32], float scale) {
         x[j + 1] = y.y;
     }
 }
-__device__ __forceinline__ void write32(const LinearArgs &a, const float (&x)[32], size_t at, bool mine,
+__device__ __forceinline__ void write32(const LinearPass &a, const float (&x)[32], size_t at, bool mine,
                                         bool staged, unsigned char *place, int r, int h) {
     if (a.part) {
         if (mine) {
@@ -290,18 +295,19 @@ __device__ __forceinline__ void write32(const LinearArgs &a, const float (&x)[32
     }
 }
 
-// kMode 0: outputs and states.  1: outputs summed over the two value heads of a cluster of
-// two CTAs.  2: only the states, of every segment but a sequence's last (their sums are the
-// start states of the segments that a second launch walks at once).
+// One scan of one (sequence, value head).  kMode 0: outputs and states.  1: outputs summed
+// over the two value heads of a cluster of two CTAs.  2: only the states, of every segment but
+// a sequence's last (their sums are the start states of the segments that a second launch
+// walks at once).
 template <bool kReverse, int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_linear_tc(const __grid_constant__ LinearArgs a, const __grid_constant__ LinMaps maps) {
+__device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, const LinMaps::Pass &maps,
+                                     const int hv, const int item) {
     constexpr bool kPair = kMode == 1, kState = kMode == 2;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     LinSmem &sm = smem_struct<LinSmem>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = blockIdx.x % a.HV, item = blockIdx.x / a.HV;
     int n = item, seg = 0, nseg = 1;
+    Walk wk;
     if (a.N <= kLinearOrder) {
         int x = 0;
         for (int step = kLinearOrder / 2; step; step >>= 1)   // the last x with seg_first[x] <= item
@@ -309,30 +315,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         n = a.order[x];
         seg = item - a.seg_first[x];
         nseg = a.seg_first[x + 1] - a.seg_first[x];
-    }
-    if (kState && seg == nseg - 1) return;
-    Walk wk;
-    {
-        const int t0 = a.cu_dev[n], t1 = a.cu_dev[n + 1];
-        bool good = t0 >= 0 && t1 >= t0 && t1 <= a.T && t1 - t0 <= a.longest;
-        if (a.N <= kLinearOrder) good = t0 == a.cu[n] && t1 == a.cu[n + 1];
-        if (!good) {
+        // the host's extents are walked; a device copy that differs is flagged
+        wk.t0 = a.cu[n];
+        wk.len = a.cu[n + 1] - wk.t0;
+        if (tid == kThreads - 1 && (a.cu_dev[n] != wk.t0 || a.cu_dev[n + 1] != wk.t0 + wk.len) && a.status)
+            atomicOr(a.status, GDN_DEVICE_CU_SEQLENS_MISMATCH);
+    } else {
+        wk.t0 = a.cu_dev[n];
+        wk.len = a.cu_dev[n + 1] - wk.t0;
+        if (wk.t0 < 0 || wk.len < 0 || wk.t0 > a.T - wk.len || wk.len > a.longest) {
             if (tid == 0 && a.status) atomicOr(a.status, GDN_DEVICE_CU_SEQLENS_MISMATCH);
             return;
         }
-        wk.t0 = t0;
-        wk.len = t1 - t0;
-        wk.total = (wk.len + kC - 1) / kC;
-        wk.first = seg * a.seg_chunks;
-        wk.n = nseg > 1 ? min(a.seg_chunks, wk.total - wk.first) : wk.total;
     }
+    if (kState && seg == nseg - 1) return;
+    wk.total = (wk.len + kC - 1) / kC;
+    wk.first = seg * a.seg_chunks;
+    wk.n = nseg > 1 ? min(a.seg_chunks, wk.total - wk.first) : wk.total;
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
     const float g2 = g * 1.4426950408889634f;
 
+    const int hq = hv / (a.HV / ps.nq), hk = hv / (a.HV / ps.nk), hw = hv / (a.HV / ps.nv);
+    auto load_v = [&](int c) {
+        const int s = c & 1, t = wk.start(c, kReverse);
+        mbar_arrive_expect_tx(&sm.full_v[s], kTile);
+        for (int h = 0; h < 2; ++h) tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_v[s]);
+    };
+    auto load_kq = [&](int c) {
+        const int s = c & 1, t = wk.start(c, kReverse);
+        mbar_arrive_expect_tx(&sm.full_kq[s], kState ? kTile : 2 * kTile);
+        for (int h = 0; h < 2; ++h) {
+            tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full_kq[s]);
+            if (!kState) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_kq[s]);
+        }
+        // the tiles after next start towards L2 while both stages are taken
+        if (c + 2 < wk.n) {
+            const int t2 = wk.start(c + 2, kReverse);
+            for (int h = 0; h < 2; ++h) {
+                tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
+                tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
+                if (!kState) tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
+            }
+        }
+    };
     if (warp == kWarpLoad) {
-        tmem_alloc(&sm.tmem_base, kCols);
-        tmem_relinquish();
-        if (lane == 0) {
+        if (elect_one()) {
             if (wk.n > 0) tma_prefetch_maps(maps);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sm.full_v[i], 1);
@@ -340,8 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.p_done[i], 1);
                 mbar_init(&sm.pt_ready[i], kGroupP * 32);
                 mbar_init(&sm.v_ok[i], kGroupW * 32);
-                mbar_init(&sm.w_ready[i], kGroupW * 16);
-                mbar_init(&sm.w_free[i], 1);
                 mbar_init(&sm.kv_done[i], 1);
                 mbar_init(&sm.o_done[i], 1);
                 mbar_init(&sm.q_free[i], 1);
@@ -351,25 +376,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_init(&sm.kept[i], kGroupS * 16);
                 mbar_init(&sm.kv_free[i], kGroupS * 32);
             }
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&sm.w_ready[i], kGroupW * 16);
+                mbar_init(&sm.w_free[i], 1);
+            }
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
             mbar_init(&sm.o_staged, (kPair ? kGroupW : kGroupS) * 32);
             mbar_init(&sm.rx_read, kGroupW * 32);
+            mbar_init(&sm.factors, 1);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
+            fence_proxy_async_smem();
+            for (int c = 0; c < min(2, wk.n); ++c) {   // both stages, before anything else is set up
+                load_v(c);
+                load_kq(c);
+            }
         }
+        __syncwarp();
+    } else if (warp == kWarpLoad + 1) {
+        tmem_alloc(&sm.tmem_base, kCols);
+        tmem_relinquish();
     }
     if (tid < kC) {
         const int power = kReverse ? tid + 1 : kC - 1 - tid;
-        sm.wtab[tid] = a.w * exp2f(g2 * (float)power);
+        sm.wtab[tid] = ps.w * exp2f(g2 * (float)power);
         sm.wtab[kC + tid] = 0.f;
         if (tid < 32) sm.ptab[tid] = exp2f(g2 * (float)(kReverse ? tid : 31 - tid));
-    } else if (tid == kC || tid == kC + 32) {
-        const int tail = wk.len % kC;
-        const double x = exp((double)g * (double)(tid == kC ? kC : tail));
-        (tid == kC ? sm.full_hi : sm.part_hi) = (float)x;
-        (tid == kC ? sm.full_lo : sm.part_lo) = (float)(x - (double)(float)x);
     }
     tc_fence_before();
     __syncthreads();
@@ -378,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tb = sm.tmem_base;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
 
-    if (warp < kGroupP) {
+    if (!kState && warp < kGroupP) {
         // ---------------------------------------------------------- P~ and Q~
         regs_down<kRegsWork>();
         const int quad = warp & 3, half = warp >> 2;   // rows 32 quad .., columns 64 half ..
         const int i = quad * 32 + lane;
-        const float at = (float)lane, lw = log2f(a.w);   // w > 0
-        for (int c = 0; !kState && c < wk.n; ++c) {
+        const float at = (float)lane, lw = log2f(ps.w);   // w > 0
+        for (int c = 0; c < wk.n; ++c) {
             const uint32_t mine = tb + lanes + kColP + 128 * (c & 1) + 64 * half;
             const int L = wk.length(c, kReverse);
             float e, f;
@@ -455,10 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kGroupP + kGroupW) {
         // ---------------------------------------------------------- W
-        // Half h of the group fills buffer h with the 32-token quarters h and h + 2.
+        // Half h of the group fills buffer h with the 32-token quarters h and h + 2; in the state
+        // pass P's warps take the quarters 2 and 3, with buffers of their own.
         regs_down<kRegsWork>();
-        const int quad = warp & 3, half = (warp - kGroupP) >> 2;
-        const uint32_t buf = tb + lanes + kColW + 48 * half;
+        const int quad = warp & 3, half = warp < kGroupP ? 2 + (warp >> 2) : (warp - kGroupP) >> 2;
+        const uint32_t buf = tb + lanes + col_w(half);
         // this lane's row of the first quarter, and the four 8-feature chunks of the warp in it
         const uint32_t vrow = smem_u32(sm.v[0] + (quad >> 1) * kHalf) + (32 * half + lane) * 128;
         uint32_t chunk[4];
@@ -478,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             float e, f;
             read_power<kReverse>(g2, i, L, e, f);
-            scale32(x, a.so * ex2(f));
+            scale32(x, ps.so * ex2(f));
 #pragma unroll
             for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
                 const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + half * kHalf + i * 128 +
@@ -491,10 +526,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sm.rx_read);   // the output's rows take plane 0's place
             if (!wait_warp(sm, &sm.rx_read, c & 1)) return false;
             const size_t t = (size_t)wk.start(c, kReverse) + i;
-            const size_t out = (t * a.no + (hv >> 1)) * kDim + 64 * (hv & 1) + 32 * half;
-            const bool staged = L == kC && !a.part;
-            const bool mine = i < L && in_range(out, 32, (long long)a.T * a.no * kDim, a.status);
-            write32(a, x, out, mine, staged, sm.q[s] + i * 128, i, half);
+            const size_t out = (t * ps.no + (hv >> 1)) * kDim + 64 * (hv & 1) + 32 * half;
+            const bool staged = L == kC && !ps.part;
+            const bool mine = i < L && in_range(out, 32, (long long)a.T * ps.no * kDim, a.status);
+            write32(ps, x, out, mine, staged, sm.q[s] + i * 128, i, half);
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(&sm.o_staged);
@@ -517,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1))) break;
                 // rows past the sequence hold the next one's tokens: zeros instead (each half
                 // clears its own quarters of K, which the product of a quarter waits for)
-                for (int x = quad * 32 + lane; x < 2 * 32 * 16; x += kGroupW * 16) {
+                for (int x = quad * 32 + lane; x < (kState ? 1 : 2) * 32 * 16; x += kGroupW * 16) {
                     const int y = x >> 4, row = (y >> 5) * 64 + half * 32 + (y & 31), h = (x >> 3) & 1;
                     if (row < L) continue;
                     const uint32_t at = h * kHalf + sw128_off(row, 8 * (x & 7));
@@ -526,12 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
             }
-            mbar_arrive(&sm.v_ok[s]);
+            if (!kState) mbar_arrive(&sm.v_ok[s]);
             const float *wt = sm.wtab + (kReverse ? 0 : kC - L) + 32 * half + 2 * (lane & 3);
             const uint32_t vt = vrow + s * kTile;
 #pragma unroll 1
-            for (int pass = 0; pass < 2; ++pass) {
-                const int use = 2 * c + pass;
+            for (int pass = 0; pass < (kState ? 1 : 2); ++pass) {
+                const int use = kState ? c : 2 * c + pass;
                 uint64_t w2[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w2[k] = pair(wt[64 * pass + 8 * k], wt[64 * pass + 8 * k + 1]);
@@ -586,8 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x0 = warp - kGroupP - kGroupW;
         const int r = (warp & 3) * 32 + lane, col = (x0 >> 2) * 64;  // row of S and of O; columns
         const size_t state = ((size_t)n * a.HV + hv) * kDim * kDim;
-        const float *src = a.s0 ? a.s0 + state : nullptr;
-        float *dst = a.s1 ? a.s1 + state : nullptr;
+        const float *src = ps.s0 ? ps.s0 + state : nullptr;
+        float *dst = ps.s1 ? ps.s1 + state : nullptr;
         if (a.pool) {
             const int slot = a.pool_idx[n];
             if (slot >= a.num_slots && r == 0 && a.pool_status) *a.pool_status = 1;
@@ -597,24 +632,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         float *keep_start = nullptr;
-        bool src_rows = a.s_cs == 1, dst_rows = src_rows;   // row r contiguous
+        bool src_rows = ps.rows, dst_rows = ps.rows;   // row r contiguous, or column c
         if (nseg > 1) {   // inner states of a split sequence: after segment k in record `first + k`
-            float *rec = a.seg_state + ((size_t)item * a.HV + hv) * kDim * kDim;
+            float *rec = ps.seg_state + ((size_t)item * a.HV + hv) * kDim * kDim;
             if (seg > 0) {
                 src = kState ? nullptr : rec - (size_t)a.HV * kDim * kDim;
-                src_rows = true;
+                src_rows = ps.seg_rows;
             }
             // a pool slot is written by its last segment's CTA, perhaps before the first one's
             // starts: the state pass keeps the start state in the last record, which is free
             float *kept = rec + (size_t)(nseg - 1) * a.HV * kDim * kDim;
             if (seg == 0 && a.pool && !kState) {
                 src = kept;
-                src_rows = true;
+                src_rows = ps.seg_rows;
             }
             keep_start = seg == 0 && a.pool && kState ? kept : nullptr;
             if (kState) {
                 dst = rec;
-                dst_rows = true;
+                dst_rows = ps.seg_rows;
             } else if (seg < nseg - 1) {
                 dst = nullptr;
             }
@@ -651,9 +686,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sm.s_ready);
         };
         if (!kState && wk.n > 0) publish();
+        auto store_state = [&]() {
+            if (!dst) return;
+            if (dst_rows) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    *reinterpret_cast<float4 *>(dst + (size_t)r * kDim + col + 4 * j) =
+                        make_float4(st[4 * j], st[4 * j + 1], st[4 * j + 2], st[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) dst[(size_t)(col + j) * kDim + r] = st[j];
+            }
+        };
+        const bool have = wk.n == 0 || wait_warp(sm, &sm.factors, 0);
         int stores = 0;
         const bool storer = tid == (kGroupP + kGroupW) * 32;
-        for (int c = 0; c < wk.n; ++c) {
+        for (int c = 0; have && c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
             if (kMode == 0 && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
                 tma_store_wait_read();
@@ -677,17 +725,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             mbar_arrive(&sm.kv_free[s]);
+            if (c + 1 == wk.n) store_state();   // while the last O runs
             if (kState) continue;
             if (!wait_warp(sm, &sm.o_done[s], (c >> 1) & 1)) break;
             tc_fence_after();
             float e, f;
             read_power<kReverse>(g2, r, L, e, f);
-            const float scale = a.so * ex2(f);
+            const float scale = ps.so * ex2(f);
             const uint32_t from = tb + lanes + kColX + col;
             if (!kPair) {
-                const size_t row = (((size_t)wk.start(c, kReverse) + r) * a.no + hv) * kDim + col;
-                const bool staged = L == kC && !a.part;   // whole chunks of bf16 leave by TMA
-                const bool mine = r < L && in_range(row, 64, (long long)a.T * a.no * kDim, a.status);
+                const size_t row = (((size_t)wk.start(c, kReverse) + r) * ps.no + hv) * kDim + col;
+                const bool staged = L == kC && !ps.part;   // whole chunks of bf16 leave by TMA
+                const bool mine = r < L && in_range(row, 64, (long long)a.T * ps.no * kDim, a.status);
                 // the stage's Q tile is free: its readers finished before O did
                 unsigned char *orow = sm.q[s] + (col >> 6) * kHalf + r * 128;
 #pragma unroll
@@ -700,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(&sm.o_free);
                     }
                     scale32(x, scale);
-                    write32(a, x, row + 32 * h, mine, staged, orow, r, h);
+                    write32(ps, x, row + 32 * h, mine, staged, orow, r, h);
                 }
                 if (staged) {
                     fence_proxy_async_smem();
@@ -761,17 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (storer) tma_store_wait_all();
-        if (dst && !*(volatile int *)&sm.dead) {
-            if (dst_rows) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    *reinterpret_cast<float4 *>(dst + (size_t)r * kDim + col + 4 * j) =
-                        make_float4(st[4 * j], st[4 * j + 1], st[4 * j + 2], st[4 * j + 3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 64; ++j) dst[(size_t)(col + j) * kDim + r] = st[j];
-            }
-        }
+        if (wk.n == 0) store_state();
     } else {
         // ---------------------------------------------------------- issuing warps
         // The whole warp waits and one elected lane issues: the operands stay in uniform
@@ -781,38 +820,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int role = __shfl_sync(0xffffffffu, warp, 0) - kWarpLoad;
         if (role == 0) {
             // ------------------------------------------------------ loads
-            const int hq = hv / (a.HV / a.nq), hk = hv / (a.HV / a.nk), hw = hv / (a.HV / a.nv);
-            int issued_v = 0, issued_kq = 0;
-            for (int c = 0; c < wk.n; ++c) {
-                const int s = c & 1, t = wk.start(c, kReverse);
-                if (c >= 2 && ((!kState && !wait_warp(sm, &sm.o_done[s], ((c >> 1) - 1) & 1)) ||
-                               !wait_warp(sm, &sm.kv_done[s], ((c >> 1) - 1) & 1)))
-                    break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.full_v[s], kTile);
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_v[s]);
-                }
+            int issued_v = min(2, wk.n), issued_kq = issued_v;
+            for (int c = 2; c < wk.n; ++c) {
+                const int s = c & 1, mark = ((c >> 1) - 1) & 1;
+                if ((!kState && !wait_warp(sm, &sm.o_done[s], mark)) || !wait_warp(sm, &sm.kv_done[s], mark)) break;
+                if (elect_one()) load_v(c);
+                __syncwarp();
                 issued_v = c + 1;
                 // the last output of this stage has left its Q tile (and the exchange its K tile)
-                if (!kState && c >= 2 && !wait_warp(sm, &sm.q_free[s], ((c >> 1) - 1) & 1)) break;
-                if (kPair && c >= 2 && !wait_warp_cluster(sm, &sm.sent[s], ((c >> 1) - 1) & 1)) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.full_kq[s], kState ? kTile : 2 * kTile);
-                    for (int h = 0; h < 2; ++h) {
-                        tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full_kq[s]);
-                        if (!kState) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_kq[s]);
-                    }
-                    // the tiles after next start towards L2 while both stages are taken
-                    if (c + 2 < wk.n) {
-                        const int t2 = wk.start(c + 2, kReverse);
-                        for (int h = 0; h < 2; ++h) {
-                            tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
-                            tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
-                            if (!kState) tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
-                        }
-                    }
-                }
+                if (!kState && !wait_warp(sm, &sm.q_free[s], mark)) break;
+                if (kPair && !wait_warp_cluster(sm, &sm.sent[s], mark)) break;
+                if (elect_one()) load_kq(c);
+                __syncwarp();
                 issued_kq = c + 1;
             }
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
@@ -872,6 +891,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------ KV = W^T K
             const uint32_t id = idesc_bf16(128, 128, 0, 1);
             const uint64_t kd0 = sdesc(smem_u32(sm.k), kHalf, 1024);
+            // lam^128 and lam^(partial chunk) to 48 bits, for the state
+            if (lane < 2) {
+                const double x = exp((double)g * (double)(lane == 0 ? kC : wk.len % kC));
+                (lane == 0 ? sm.full_hi : sm.part_hi) = (float)x;
+                (lane == 0 ? sm.full_lo : sm.part_lo) = (float)(x - (double)(float)x);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.factors);
+            __syncwarp();
             bool ok = true;
             for (int c = 0; c < wk.n && ok; ++c) {
                 const int s = c & 1;
@@ -883,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd) {
-                    const int b = qd & 1, use = 2 * c + (qd >> 1);
+                    const int b = kState ? qd : qd & 1, use = kState ? c : 2 * c + (qd >> 1);
                     ok = ok && wait_warp(sm, &sm.w_ready[b], use & 1);
                     if (!ok) break;
                     tc_fence_after();
@@ -892,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
                             for (int part = 0; part < 3; ++part)
-                                mma_ts(tb + col_kv<kMode>(c), tb + kColW + 48 * b + 16 * part + 8 * x,
+                                mma_ts(tb + col_kv<kMode>(c), tb + col_w(b) + 16 * part + 8 * x,
                                        kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
                         mma_commit(&sm.w_free[b]);
                         if (qd == 3) mma_commit(&sm.kv_done[s]);
@@ -912,20 +940,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (kPair) cluster_sync();   // neither CTA leaves while the other may still write to it
     if (tid == 0 && sm.dead && a.status) atomicOr(a.status, GDN_DEVICE_WAIT_TIMEOUT);
-    if (warp == kWarpLoad) tmem_dealloc(tb, kCols);
+    if (warp == kWarpLoad + 1) tmem_dealloc(tb, kCols);
+}
+
+// The scans of a call, work items longest first, the passes of an item and its value heads
+// side by side (the two CTAs of a cluster are two value heads of one pass).
+//   kSet 0: a forward.  1: the state pass.  2, 3: a backward without and with pairs.
+template <int kSet>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_linear_tc(const __grid_constant__ LinearArgs a, const __grid_constant__ LinMaps maps) {
+    const int passes = kSet == 1 ? a.state_passes : a.passes;
+    const int hv = blockIdx.x % a.HV, rest = blockIdx.x / a.HV, item = rest / passes;
+    const int p = rest % passes * (kSet == 1 ? 2 : 1);   // (the state pass takes scans 0 and 2)
+    if (kSet == 0) {
+        scan<false, 0>(a, a.pass[0], maps.pass[0], hv, item);
+    } else if (kSet == 1) {
+        if (p) scan<true, 2>(a, a.pass[2], maps.pass[2], hv, item);
+        else scan<false, 2>(a, a.pass[0], maps.pass[0], hv, item);
+    } else if (kSet == 2) {
+        if (p) scan<true, 0>(a, a.pass[p], maps.pass[p], hv, item);
+        else scan<false, 0>(a, a.pass[0], maps.pass[0], hv, item);
+    } else {
+        if (p == 0) scan<false, 1>(a, a.pass[0], maps.pass[0], hv, item);
+        else if (p == 1) scan<true, 1>(a, a.pass[1], maps.pass[1], hv, item);
+        else scan<true, 0>(a, a.pass[2], maps.pass[2], hv, item);
+    }
 }
 
 // Start states of a split sequence's segments: record k (the state after segment k alone,
 // segment 0's from its true start) becomes the state after segments 0 .. k.
 __global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ LinearArgs a) {
-    const int x = blockIdx.z, hv = blockIdx.y;
+    const int x = blockIdx.z / a.state_passes, hv = blockIdx.y;
     const int first = a.seg_first[x], nseg = a.seg_first[x + 1] - first;
     if (nseg < 3) return;
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
     const double lam = exp((double)g * (double)a.seg_chunks * kC);
     const float fh = (float)lam, fl = (float)(lam - (double)fh);
     const size_t step = (size_t)a.HV * kDim * kDim;
-    float4 *p = reinterpret_cast<float4 *>(a.seg_state + ((size_t)first * a.HV + hv) * kDim * kDim) +
+    float *rec = a.pass[blockIdx.z % a.state_passes * 2].seg_state;
+    float4 *p = reinterpret_cast<float4 *>(rec + ((size_t)first * a.HV + hv) * kDim * kDim) +
                 blockIdx.x * 256 + threadIdx.x;
     float4 y = *p;
     for (int k = 1; k < nseg - 1; ++k) {
@@ -940,10 +993,10 @@ __global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ L
     }
 }
 
-template <bool kReverse, int kMode>
-cudaError_t launch_mode(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
+template <int kSet>
+cudaError_t launch_set(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.items * a.HV));
+    cfg.gridDim = dim3((unsigned)a.items * a.HV * (kSet == 1 ? a.state_passes : a.passes));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(LinSmem) + 1024;
     cfg.stream = s;
@@ -952,41 +1005,40 @@ cudaError_t launch_mode(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
     at[0].val.clusterDim.x = 2;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = kMode == 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_linear_tc<kReverse, kMode>, a, m);
-}
-
-template <bool kReverse>
-cudaError_t launch_dir(const LinearArgs &a, cudaStream_t s) {
-    const int smem = (int)sizeof(LinSmem) + 1024;
-    cudaError_t e;
-    for (const void *k : {(const void *)k_linear_tc<kReverse, 0>, (const void *)k_linear_tc<kReverse, 1>,
-                          (const void *)k_linear_tc<kReverse, 2>})
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    // (the calls above have made the device's context current, which the encoder needs)
-    LinMaps m;
-    memset(&m, 0, sizeof(m));
-    if (a.T > 0) {
-        const uint64_t rowb = kDim * sizeof(bf16);
-        if (!encode_rows_bf16(&m.q, a.q, a.nq, a.T, rowb, rowb * a.nq, kC) ||
-            !encode_rows_bf16(&m.k, a.k, a.nk, a.T, rowb, rowb * a.nk, kC) ||
-            !encode_rows_bf16(&m.v, a.v, a.nv, a.T, rowb, rowb * a.nv, kC) ||
-            (!a.part && !encode_rows_bf16(&m.o, a.o, a.no, a.T, rowb, rowb * a.no, kC)))
-            return cudaErrorInvalidValue;
-        if (a.part) m.o = m.v;   // not used, but fetched with the others
-    }
-    if (a.seg_chunks > 0) {
-        if ((e = launch_mode<kReverse, 2>(a, m, s)) != cudaSuccess) return e;
-        k_linear_stitch<<<dim3(kDim * kDim / 1024, a.HV, a.N), 256, 0, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    return a.pair ? launch_mode<kReverse, 1>(a, m, s) : launch_mode<kReverse, 0>(a, m, s);
+    cfg.numAttrs = kSet == 3 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_linear_tc<kSet>, a, m);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s) {
-    return a.reverse ? launch_dir<true>(a, s) : launch_dir<false>(a, s);
+    LinMaps m;
+    memset(&m, 0, sizeof(m));
+    cudaError_t e = cudaSuccess;
+    for (const void *k : {(const void *)k_linear_tc<0>, (const void *)k_linear_tc<1>, (const void *)k_linear_tc<2>,
+                          (const void *)k_linear_tc<3>})
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)sizeof(LinSmem) + 1024)) != cudaSuccess)
+            return e;
+    // (the calls above have made the device's context current, which the map encoder needs)
+    const uint64_t rowb = kDim * sizeof(bf16);
+    for (int i = 0; i < a.passes && a.T > 0; ++i) {
+        const LinearPass &p = a.pass[i];
+        LinMaps::Pass &x = m.pass[i];
+        if (!encode_rows_bf16(&x.q, p.q, p.nq, a.T, rowb, rowb * p.nq, kC) ||
+            !encode_rows_bf16(&x.k, p.k, p.nk, a.T, rowb, rowb * p.nk, kC) ||
+            !encode_rows_bf16(&x.v, p.v, p.nv, a.T, rowb, rowb * p.nv, kC) ||
+            (!p.part && !encode_rows_bf16(&x.o, p.o, p.no, a.T, rowb, rowb * p.no, kC)))
+            return cudaErrorInvalidValue;
+        if (p.part) x.o = x.v;   // not used, but fetched with the others
+    }
+    if (a.seg_chunks > 0) {
+        if ((e = launch_set<1>(a, m, s)) != cudaSuccess) return e;
+        k_linear_stitch<<<dim3(kDim * kDim / 1024, a.HV, a.N * a.state_passes), 256, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (a.passes == 1) return launch_set<0>(a, m, s);
+    return a.pass[0].pair ? launch_set<3>(a, m, s) : launch_set<2>(a, m, s);
 }
 
 }  // namespace gdn

@@ -20,6 +20,7 @@ from .binding import (GDN_DTYPE_BF16, GDN_DTYPE_F32, GdnError, GdnProblem,  # no
                       GDN_ROPE_SCALE_NONE, GDN_ROPE_SCALE_PARTS,
                       gdn_linear_attn_bwd, gdn_linear_attn_fwd, gdn_linear_attn_prefill_paged,
                       gdn_linear_attn_step, gdn_linear_attn_workspace_bytes, gdn_rope,
-                      gdn_rope_frequencies, linear_attn_bwd, linear_attn_fwd,
-                      linear_attn_prefill_paged, linear_attn_step, rope, rope_frequencies)
+                      gdn_rope_frequencies)
+from .linear import (linear_attn_bwd, linear_attn_fwd, linear_attn_prefill_paged,  # noqa: F401
+                     linear_attn_step, rope, rope_frequencies)
 from .autograd import chunk_gated_delta_rule, linear_attention, rotary  # noqa: E402,F401

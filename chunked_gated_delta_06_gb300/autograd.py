@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import binding
+from . import binding, linear
 
 
 def _function():
@@ -91,7 +91,7 @@ def _linear_function():
             ctx.set_materialize_grads(False)
             ctx.cu, ctx.scale = (cu_host, cu_dev), scale
             ctx.save_for_backward(q, k, v, log_decay, initial_state)
-            return binding.linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=scale,
+            return linear.linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=scale,
                                            initial_state=initial_state,
                                            output_final_state=output_final_state)
 
@@ -100,7 +100,7 @@ def _linear_function():
             q, k, v, log_decay, h0 = ctx.saved_tensors
             if d_o is None:
                 d_o = torch.zeros_like(v)
-            gr = binding.linear_attn_bwd(q, k, v, log_decay, d_o.to(torch.bfloat16).contiguous(), *ctx.cu,
+            gr = linear.linear_attn_bwd(q, k, v, log_decay, d_o.to(torch.bfloat16).contiguous(), *ctx.cu,
                                          scale=ctx.scale, initial_state=h0,
                                          d_final_state=None if d_ht is None else d_ht.float().contiguous(),
                                          want_dh0=h0 is not None)
@@ -117,13 +117,13 @@ def _rotary_function():
         def forward(ctx, q, k, positions, freq, layout, mscale):
             ctx.args = (layout, mscale)
             ctx.save_for_backward(positions, freq)
-            return binding.rope(q, k, positions, freq, layout=layout, mscale=mscale)
+            return linear.rope(q, k, positions, freq, layout=layout, mscale=mscale)
 
         @staticmethod
         def backward(ctx, dq, dk):
             positions, freq = ctx.saved_tensors
             layout, mscale = ctx.args
-            dq, dk = binding.rope(dq.contiguous(), dk.contiguous(), positions, freq, layout=layout,
+            dq, dk = linear.rope(dq.contiguous(), dk.contiguous(), positions, freq, layout=layout,
                                   mscale=mscale, backward=True)
             return dq, dk, None, None, None, None
 
@@ -163,7 +163,7 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
 
 
 def rotary(q, k, positions, freq, layout="half", mscale=1.0):
-    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (binding.rope)."""
+    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (linear.rope)."""
     global _ROTARY
     if _ROTARY is None:
         _ROTARY = _rotary_function()

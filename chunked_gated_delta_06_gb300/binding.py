@@ -132,13 +132,13 @@ def load_library(path):
     L.gdn_chunk_fwd_noalloc.argtypes = [P] + [_vp] * 8 + [_vp]
     L.gdn_chunk_fwd_noalloc.restype = ctypes.c_int
     i32, f32, f64 = ctypes.c_int32, ctypes.c_float, ctypes.c_double
-    L.gdn_linear_attn_workspace_bytes.argtypes = [P, ctypes.c_int]
+    L.gdn_linear_attn_workspace_bytes.argtypes = [_vp, ctypes.c_int]
     L.gdn_linear_attn_workspace_bytes.restype = _sz
-    L.gdn_linear_attn_fwd.argtypes = [P] + [_vp] * 8 + [_sz, _vp]
+    L.gdn_linear_attn_fwd.argtypes = [_vp] + [_vp] * 8 + [_sz, _vp]
     L.gdn_linear_attn_fwd.restype = ctypes.c_int
-    L.gdn_linear_attn_prefill_paged.argtypes = [P] + [_vp] * 5 + [i32] + [_vp] * 5 + [_sz, _vp]
+    L.gdn_linear_attn_prefill_paged.argtypes = [_vp] + [_vp] * 5 + [i32] + [_vp] * 5 + [_sz, _vp]
     L.gdn_linear_attn_prefill_paged.restype = ctypes.c_int
-    L.gdn_linear_attn_bwd.argtypes = [P] + [_vp] * 12 + [_sz, _vp]
+    L.gdn_linear_attn_bwd.argtypes = [_vp] + [_vp] * 12 + [_sz, _vp]
     L.gdn_linear_attn_bwd.restype = ctypes.c_int
     L.gdn_linear_attn_step.argtypes = [i32] * 5 + [f32] + [_vp] * 5 + [i32] + [_vp] * 4
     L.gdn_linear_attn_step.restype = ctypes.c_int
@@ -568,164 +568,3 @@ def chunk_prefill_paged(q, k, v, g, beta, cu_host, cu_dev, state_pool, state_ind
                                  _stream())
     _check(st, "gdn_chunk_prefill_paged")
     return o
-
-
-def _need(t, name, dtype, shape):
-    """Refuse a tensor the kernels would misread: they take dense CUDA tensors of one dtype."""
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous CUDA tensor" % name)
-
-
-def _linear_inputs(q, k, v, log_decay):
-    """(T, H, HV) of a decay-only call after checking its inputs."""
-    import torch
-    if q.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k and v must be [tokens, heads, 128]")
-    T, H, K = q.shape
-    HV = v.shape[1]
-    _need(q, "q", torch.bfloat16, (T, H, K))
-    _need(k, "k", torch.bfloat16, (T, H, K))
-    _need(v, "v", torch.bfloat16, (T, HV, v.shape[2]))
-    _need(log_decay, "log_decay", torch.float32, (HV,))
-    return T, H, HV
-
-
-def _linear_problem(q, v, cu_host, cu_dev, scale, status, scan_segment_chunks=0):
-    import torch
-    cu = np.ascontiguousarray(np.asarray(cu_host, dtype=np.int32))
-    _need(cu_dev, "cu_dev", torch.int32, (len(cu),))
-    if len(cu) == 0 or int(cu[-1]) != q.shape[0]:
-        raise ValueError("cu_host must end with the number of tokens, %d" % q.shape[0])
-    return make_problem(cu, q.shape[1], v.shape[1], q.shape[2], v.shape[2], scale or 0.0,
-                        cu_dev.data_ptr(), device_status_ptr=_ptr(status) or 0,
-                        scan_segment_chunks=scan_segment_chunks)
-
-
-def _linear_workspace(p, mode, workspace, device):
-    import torch
-    n = gdn_linear_attn_workspace_bytes(p, mode)
-    if n == 0:
-        raise GdnError(GDN_ERR_UNSUPPORTED if (p.head_dim_k, p.head_dim_v) != (128, 128)
-                       or p.num_v_heads % p.num_k_heads else GDN_ERR_INVALID_ARG,
-                       "gdn_linear_attn_workspace_bytes")
-    if workspace is None or workspace.numel() < n:
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    return workspace
-
-
-def linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=None, initial_state=None,
-                    output_final_state=True, workspace=None, device_status=None, scan_segment_chunks=0):
-    """gdn_linear_attn_fwd on torch tensors.  Returns (o, final_state or None)."""
-    import torch
-    T, H, HV = _linear_inputs(q, k, v, log_decay)
-    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, device_status, scan_segment_chunks)
-    workspace = _linear_workspace(p, 0, workspace, q.device)
-    shape = (p.num_seqs, HV, 128, 128)
-    if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, shape)
-    o = torch.empty((T, HV, 128), dtype=torch.bfloat16, device=q.device)
-    ht = torch.empty(shape, dtype=torch.float32, device=q.device) if output_final_state else None
-    st = gdn_linear_attn_fwd(p, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
-                             _ptr(o), _ptr(ht), _ptr(workspace), workspace.numel(), _stream())
-    _check(st, "gdn_linear_attn_fwd")
-    return o, ht
-
-
-def linear_attn_prefill_paged(q, k, v, log_decay, cu_host, cu_dev, state_pool, state_indices,
-                              has_initial_state=None, scale=None, device_status=None, workspace=None,
-                              problem_status=None, scan_segment_chunks=0):
-    """gdn_linear_attn_prefill_paged on torch tensors (state_pool updated in place; slots and
-    status words as in chunk_prefill_paged).  Returns o."""
-    import torch
-    T, H, HV = _linear_inputs(q, k, v, log_decay)
-    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, problem_status, scan_segment_chunks)
-    workspace = _linear_workspace(p, 0, workspace, q.device)
-    _need(state_pool, "state_pool", torch.float32, (state_pool.shape[0], HV, 128, 128))
-    _need(state_indices, "state_indices", torch.int32, (p.num_seqs,))
-    if has_initial_state is not None:
-        _need(has_initial_state, "has_initial_state", torch.int32, (p.num_seqs,))
-    o = torch.empty((T, HV, 128), dtype=torch.bfloat16, device=q.device)
-    st = gdn_linear_attn_prefill_paged(p, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state_pool),
-                                       state_pool.shape[0], _ptr(state_indices),
-                                       _ptr(has_initial_state), _ptr(o), _ptr(device_status),
-                                       _ptr(workspace), workspace.numel(), _stream())
-    _check(st, "gdn_linear_attn_prefill_paged")
-    return o
-
-
-def linear_attn_bwd(q, k, v, log_decay, d_o, cu_host, cu_dev, scale=None, initial_state=None,
-                    d_final_state=None, want_dh0=True, workspace=None, device_status=None,
-                    scan_segment_chunks=0):
-    """gdn_linear_attn_bwd on torch tensors.  Returns dict dq, dk, dv, dh0."""
-    import torch
-    T, H, HV = _linear_inputs(q, k, v, log_decay)
-    p, keep = _linear_problem(q, v, cu_host, cu_dev, scale, device_status, scan_segment_chunks)
-    workspace = _linear_workspace(p, 1, workspace, q.device)
-    shape = (p.num_seqs, HV, 128, 128)
-    _need(d_o, "d_o", torch.bfloat16, (T, HV, 128))
-    if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, shape)
-    if d_final_state is not None:
-        _need(d_final_state, "d_final_state", torch.float32, shape)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dh0 = torch.empty(shape, dtype=torch.float32, device=q.device) if want_dh0 else None
-    st = gdn_linear_attn_bwd(p, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
-                             _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dh0),
-                             _ptr(workspace), workspace.numel(), _stream())
-    _check(st, "gdn_linear_attn_bwd")
-    return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
-
-
-def linear_attn_step(q, k, v, log_decay, state_pool, state_indices, scale=None, device_status=None):
-    """gdn_linear_attn_step on torch tensors (state_pool updated in place).  Returns o."""
-    import torch
-    B, H, HV = _linear_inputs(q, k, v, log_decay)
-    _need(state_pool, "state_pool", torch.float32, (state_pool.shape[0], HV, v.shape[2], q.shape[2]))
-    _need(state_indices, "state_indices", torch.int32, (B,))
-    o = torch.empty((B, HV, v.shape[2]), dtype=torch.bfloat16, device=q.device)
-    st = gdn_linear_attn_step(B, H, HV, q.shape[2], v.shape[2], float(scale or 0.0), _ptr(q), _ptr(k),
-                              _ptr(v), _ptr(log_decay), _ptr(state_pool), state_pool.shape[0],
-                              _ptr(state_indices), _ptr(o), _ptr(device_status), _stream())
-    _check(st, "gdn_linear_attn_step")
-    return o
-
-
-_ROPE_SCALING = {"none": GDN_ROPE_SCALE_NONE, "linear": GDN_ROPE_SCALE_LINEAR, "parts": GDN_ROPE_SCALE_PARTS}
-_ROPE_LAYOUT = {"half": GDN_ROPE_HALF, "interleaved": GDN_ROPE_INTERLEAVED}
-
-
-def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, trained_len=0.0, low_turns=1.0,
-                     high_turns=32.0, device=None):
-    """gdn_rope_frequencies as a tensor [2, rot_dim / 2] (turns per position, head and tail),
-    for the `freq` argument of rope; device: where to put it (default: the current CUDA device)."""
-    import torch
-    freq = torch.empty((2, rot_dim // 2), dtype=torch.float32)
-    st = gdn_rope_frequencies(int(rot_dim), float(base), _ROPE_SCALING[scaling], float(factor),
-                              float(trained_len), float(low_turns), float(high_turns), freq.data_ptr())
-    _check(st, "gdn_rope_frequencies")
-    return freq.to("cuda" if device is None else device)
-
-
-def rope(q, k, positions, freq, layout="half", mscale=1.0, backward=False, inplace=False):
-    """gdn_rope on torch tensors: q [T, Hq, D] and k [T, Hk, D] (or None) bf16, positions int32
-    [T], freq as rope_frequencies returns it (2 * freq.shape[1] elements of each head turn).
-    backward: the gradient (the rotation by the negative angle, the same mscale).  Returns
-    (q, k) rotated, new tensors unless inplace."""
-    import torch
-    T, Hq, D = q.shape
-    Hk = 0 if k is None else k.shape[1]
-    _need(q, "q", torch.bfloat16, (T, Hq, D))
-    if k is not None:
-        _need(k, "k", torch.bfloat16, (T, Hk, D))
-    _need(positions, "positions", torch.int32, (T,))
-    _need(freq, "freq", torch.float32, (2, freq.shape[1]))
-    qo = q if inplace else torch.empty_like(q)
-    ko = k if inplace or k is None else torch.empty_like(k)
-    st = gdn_rope(T, Hq, Hk, D, 2 * freq.shape[1], _ROPE_LAYOUT[layout], int(backward), float(mscale),
-                  _ptr(q), _ptr(k), _ptr(positions), _ptr(freq), _ptr(qo), _ptr(ko), _stream())
-    _check(st, "gdn_rope")
-    return qo, ko

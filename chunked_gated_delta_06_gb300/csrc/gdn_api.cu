@@ -512,7 +512,13 @@ size_t carve_linear(const Dims &d, const LinearPlan &plan, int for_backward, voi
         if (for_backward && no != d.H) w->part[i] = cv.take<float>((size_t)d.T * no * gdn::kDim);
         if (plan.seg) w->seg_state[i] = cv.take<float>((size_t)plan.items * d.HV * gdn::kDim * gdn::kDim);
     }
-    return cv.used() > 0 ? cv.used() : kAlign;
+    return cv.used();
+}
+// The decay-only calls take no workspace (NULL, 0 bytes) where the plan needs none.
+gdn_status check_linear_ws(size_t need, const void *workspace, size_t ws_size) {
+    if (!workspace && ws_size == 0) return need > 0 ? GDN_ERR_WORKSPACE_TOO_SMALL : GDN_OK;
+    if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    return ws_size < (need > 0 ? need : kAlign) ? GDN_ERR_WORKSPACE_TOO_SMALL : GDN_OK;
 }
 
 gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan,
@@ -578,11 +584,10 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
     for (const void *x : ptrs)
         if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
     if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
-    if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
     const LinearPlan plan = plan_linear(p, d);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
-    if (ws_size < carve_linear(d, plan, 0, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    if ((st = check_linear_ws(carve_linear(d, plan, 0, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
     a.passes = a.state_passes = 1;
     gdn::LinearPass &x = a.pass[0];
@@ -749,7 +754,8 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward) {
     LinearWs ws;
     if (for_backward < 0 || for_backward > 1) return 0;
     if (check_problem(p, &d) != GDN_OK) return 0;
-    return carve_linear(d, plan_linear(p, d), for_backward, nullptr, &ws);
+    const size_t need = carve_linear(d, plan_linear(p, d), for_backward, nullptr, &ws);
+    return need > 0 ? need : kAlign;
 }
 
 gdn_status gdn_linear_attn_fwd(const gdn_problem *p, const void *q, const void *k, const void *v,
@@ -785,11 +791,10 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     for (const void *x : ptrs)
         if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
     if (dh0 && dh0 == d_final_state) return GDN_ERR_INVALID_ARG;
-    if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
     const LinearPlan plan = plan_linear(p, d);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
-    if (ws_size < carve_linear(d, plan, 1, workspace, &ws)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    if ((st = check_linear_ws(carve_linear(d, plan, 1, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
     a.passes = 3;

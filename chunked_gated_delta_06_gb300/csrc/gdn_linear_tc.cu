@@ -32,8 +32,6 @@
 #include <stddef.h>
 #include <string.h>
 
-#include <initializer_list>
-
 
 #include "gdn_epi.cuh"
 #include "gdn_linear.h"
@@ -1012,33 +1010,56 @@ cudaError_t launch_set(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s) {
+    const int set = a.passes == 1 ? 0 : a.pass[0].pair ? 3 : 2;
+    const void *kernels[] = {(const void *)k_linear_tc<0>, (const void *)k_linear_tc<1>, (const void *)k_linear_tc<2>,
+                             (const void *)k_linear_tc<3>};
+    const int smem = (int)sizeof(LinSmem) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(kernels[set], cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && a.seg_chunks > 0)
+        e = cudaFuncSetAttribute(kernels[1], cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // (the calls above have made the device's context current, which the map encoder needs)
     LinMaps m;
     memset(&m, 0, sizeof(m));
-    cudaError_t e = cudaSuccess;
-    for (const void *k : {(const void *)k_linear_tc<0>, (const void *)k_linear_tc<1>, (const void *)k_linear_tc<2>,
-                          (const void *)k_linear_tc<3>})
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)sizeof(LinSmem) + 1024)) != cudaSuccess)
-            return e;
-    // (the calls above have made the device's context current, which the map encoder needs)
-    const uint64_t rowb = kDim * sizeof(bf16);
+    // a backward's three scans read the same four tensors: each is encoded once
+    const bf16 *known[4];
+    int known_heads[4];
+    const CUtensorMap *map[4];
+    int count = 0;
+    bool ok = true;
+    auto encode = [&](CUtensorMap &x, const bf16 *base, int heads) {
+        const uint64_t rowb = kDim * sizeof(bf16);
+        ok = ok && encode_rows_bf16(&x, base, heads, a.T, rowb, rowb * heads, kC);
+    };
+    auto input = [&](CUtensorMap &x, const bf16 *base, int heads) {
+        for (int i = 0; i < count; ++i)
+            if (known[i] == base && known_heads[i] == heads) {
+                x = *map[i];
+                return;
+            }
+        encode(x, base, heads);
+        if (count < 4) {
+            known[count] = base;
+            known_heads[count] = heads;
+            map[count++] = &x;
+        }
+    };
     for (int i = 0; i < a.passes && a.T > 0; ++i) {
         const LinearPass &p = a.pass[i];
         LinMaps::Pass &x = m.pass[i];
-        if (!encode_rows_bf16(&x.q, p.q, p.nq, a.T, rowb, rowb * p.nq, kC) ||
-            !encode_rows_bf16(&x.k, p.k, p.nk, a.T, rowb, rowb * p.nk, kC) ||
-            !encode_rows_bf16(&x.v, p.v, p.nv, a.T, rowb, rowb * p.nv, kC) ||
-            (!p.part && !encode_rows_bf16(&x.o, p.o, p.no, a.T, rowb, rowb * p.no, kC)))
-            return cudaErrorInvalidValue;
+        input(x.q, p.q, p.nq);
+        input(x.k, p.k, p.nk);
+        input(x.v, p.v, p.nv);
         if (p.part) x.o = x.v;   // not used, but fetched with the others
+        else encode(x.o, p.o, p.no);
     }
+    if (!ok) return cudaErrorInvalidValue;
     if (a.seg_chunks > 0) {
         if ((e = launch_set<1>(a, m, s)) != cudaSuccess) return e;
         k_linear_stitch<<<dim3(kDim * kDim / 1024, a.HV, a.N * a.state_passes), 256, 0, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if (a.passes == 1) return launch_set<0>(a, m, s);
-    return a.pass[0].pair ? launch_set<3>(a, m, s) : launch_set<2>(a, m, s);
+    return set == 0 ? launch_set<0>(a, m, s) : set == 2 ? launch_set<2>(a, m, s) : launch_set<3>(a, m, s);
 }
 
 }  // namespace gdn

@@ -340,7 +340,8 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward);
  *   o              bf16 [T, HV, 128] (out)
  *   final_state    fp32 [N, HV, 128, 128] (out), or NULL; not initial_state
  *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 0), 256-byte
- *                  aligned */
+ *                  aligned; or NULL with ws_bytes 0, which is enough where the
+ *                  plan needs none (GDN_ERR_WORKSPACE_TOO_SMALL where it does) */
 gdn_status gdn_linear_attn_fwd(const gdn_problem *p, const void *q, const void *k, const void *v,
                                const float *log_decay, const float *initial_state, void *o,
                                float *final_state, void *workspace, size_t ws_bytes,
@@ -364,7 +365,7 @@ gdn_status gdn_linear_attn_prefill_paged(const gdn_problem *p, const void *q, co
  *   dv             bf16 [T, HV, 128] (out)
  *   dh0            fp32 [N, HV, 128, 128] (out), or NULL; not d_final_state
  *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 1), 256-byte
- *                  aligned */
+ *                  aligned; or NULL with ws_bytes 0, as in the forward */
 gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *k, const void *v,
                                const float *log_decay, const float *initial_state,
                                const void *d_o, const float *d_final_state, void *dq, void *dk,

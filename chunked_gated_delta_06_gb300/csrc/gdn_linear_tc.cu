@@ -60,7 +60,7 @@ static_assert((kGroupP + kGroupW) * kRegsWork + kGroupS * kRegsState + 4 * kRegs
 // Tensor-memory columns
 constexpr uint32_t kColP = 0;      // two buffers of 128: P fp32; then, per half h of 64: P~ of tokens
                                    // 64 h .. in 32 columns and Q~ of features 64 h .. in the next 32
-constexpr uint32_t kColX = 256;    // KV of a chunk, then its O
+constexpr uint32_t kColX = 256;    // O
 constexpr uint32_t kColW = 384;    // two buffers of 48: 32 tokens of W, three parts of 16 (the state
                                    // pass has two more in the second P buffer)
 constexpr uint32_t kCols = 512;
@@ -74,7 +74,7 @@ struct LinSmem {
     uint64_t full_v[2], full_kq[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], q_free[2];
     uint64_t kv_free[2], s_ready, o_free, o_staged, factors, drain[3];
     // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
-    uint64_t peer_ok[2], rx_full[2], sent[2], kept[2], rx_read;
+    uint64_t peer_ok[2], rx_full[2], sent[2];
     uint32_t tmem_base;
     int dead;
 };
@@ -240,12 +240,12 @@ struct Walk {      // the chunks of this CTA's segment, in scan order
     __device__ __forceinline__ int length(int c, bool rev) const { return min(kC, len - chunk(c, rev) * kC); }
 };
 
-// Columns of chunk c's KV.  Mode 0: the P buffer of chunk c - 1, whose readers end with O of
-// that chunk and which chunk c + 1 needs next; so KV waits for no epilogue.  Mode 1 keeps
-// outputs there, so that KV and O take turns in one region.  Mode 2: two regions in turns.
+// Columns of chunk c's KV: the P buffer of chunk c - 1, whose readers end with O of that chunk
+// and which chunk c + 1 needs next; so KV waits for no epilogue.  The state pass has no outputs
+// and takes two regions in turns.
 template <int kMode>
 __device__ __forceinline__ uint32_t col_kv(int c) {
-    return kMode == 0 ? kColP + 128 * ((c + 1) & 1) : kMode == 2 && (c & 1) ? kColP : kColX;
+    return kMode != 2 ? kColP + 128 * ((c + 1) & 1) : c & 1 ? kColP : kColX;
 }
 __device__ __forceinline__ uint32_t col_w(int b) { return b < 2 ? kColW + 48 * b : kColP + 128 + 48 * (b - 2); }
 
@@ -371,7 +371,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 mbar_init(&sm.peer_ok[i], 1);
                 mbar_init(&sm.rx_full[i], 1);
                 mbar_init(&sm.sent[i], 1);
-                mbar_init(&sm.kept[i], kGroupS * 16);
                 mbar_init(&sm.kv_free[i], kGroupS * 32);
             }
             for (int i = 0; i < 4; ++i) {
@@ -380,8 +379,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             }
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
-            mbar_init(&sm.o_staged, (kPair ? kGroupW : kGroupS) * 32);
-            mbar_init(&sm.rx_read, kGroupW * 32);
+            mbar_init(&sm.o_staged, kGroupS * (kPair ? 16 : 32));
             mbar_init(&sm.factors, 1);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
@@ -497,51 +495,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         uint32_t chunk[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) chunk[x] = (uint32_t)((4 * (quad & 1) + x) ^ (lane & 7)) * 16;
-        // Pair mode: this group, which has the most time to spare, also adds the two
-        // halves of chunk c's outputs and writes them.
-        const int i = quad * 32 + lane;
-        const bool lead = tid == kGroupP * 32;
-        auto finish = [&](int c) -> bool {
-            const int s = c & 1, L = wk.length(c, kReverse), mark = (c >> 1) & 1;
-            if (!wait_warp(sm, &sm.kept[s], mark) || !wait_warp_cluster(sm, &sm.rx_full[s], mark)) return false;
-            if (lead) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
-            tc_fence_after();
-            float x[32];
-            tmem_ld32(tb + lanes + kColP + 128 * s + 64 * (hv & 1) + 32 * half, x);
-            tmem_ld_wait();
-            float e, f;
-            read_power<kReverse>(g2, i, L, e, f);
-            scale32(x, ps.so * ex2(f));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
-                const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + half * kHalf + i * 128 +
-                                                                   ((j ^ (i & 7)) << 4));
-                x[4 * j] += y.x;
-                x[4 * j + 1] += y.y;
-                x[4 * j + 2] += y.z;
-                x[4 * j + 3] += y.w;
-            }
-            mbar_arrive(&sm.rx_read);   // the output's rows take plane 0's place
-            if (!wait_warp(sm, &sm.rx_read, c & 1)) return false;
-            const size_t t = (size_t)wk.start(c, kReverse) + i;
-            const size_t out = (t * ps.no + (hv >> 1)) * kDim + 64 * (hv & 1) + 32 * half;
-            const bool staged = L == kC && !ps.part;
-            const bool mine = i < L && in_range(out, 32, (long long)a.T * ps.no * kDim, a.status);
-            write32(ps, x, out, mine, staged, sm.q[s] + i * 128, i, half);
-            fence_proxy_async_smem();
-            tc_fence_before();
-            mbar_arrive(&sm.o_staged);
-            bool ok = true;
-            if (lead && (ok = wait(sm, &sm.o_staged, c & 1))) {
-                if (staged) {
-                    tma_store_3d(&maps.o, 64 * (hv & 1), hv >> 1, wk.start(c, kReverse), sm.q[s]);
-                    tma_store_commit();
-                    tma_store_wait_read();
-                }
-                mbar_arrive(&sm.q_free[s]);
-            }
-            return __all_sync(0xffffffffu, ok);
-        };
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
@@ -607,11 +560,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 tc_fence_before();
                 mbar_arrive(&sm.w_ready[half]);
             }
-            if (kPair && ok && c > 0) ok = finish(c - 1);
-        }
-        if (kPair) {
-            if (ok && wk.n > 0) finish(wk.n - 1);
-            if (lead) tma_store_wait_all();
         }
     } else if (warp < kWarpLoad) {
         // ---------------------------------------------------------- state and output
@@ -698,10 +646,12 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         };
         const bool have = wk.n == 0 || wait_warp(sm, &sm.factors, 0);
         int stores = 0;
-        const bool storer = tid == (kGroupP + kGroupW) * 32;
+        // pair mode: the warps whose half of O this CTA writes, and those whose half the peer does
+        const bool keep = !kPair || (col >> 6) == (hv & 1);
+        const bool storer = tid == (kGroupP + kGroupW) * 32 + (kPair ? 128 * (hv & 1) : 0);
         for (int c = 0; have && c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (kMode == 0 && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
+            if (!kState && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
                 tma_store_wait_read();
                 mbar_arrive(&sm.q_free[s ^ 1]);
             }
@@ -731,54 +681,20 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             read_power<kReverse>(g2, r, L, e, f);
             const float scale = ps.so * ex2(f);
             const uint32_t from = tb + lanes + kColX + col;
-            if (!kPair) {
-                const size_t row = (((size_t)wk.start(c, kReverse) + r) * ps.no + hv) * kDim + col;
-                const bool staged = L == kC && !ps.part;   // whole chunks of bf16 leave by TMA
-                const bool mine = r < L && in_range(row, 64, (long long)a.T * ps.no * kDim, a.status);
-                // the stage's Q tile is free: its readers finished before O did
-                unsigned char *orow = sm.q[s] + (col >> 6) * kHalf + r * 128;
+            // element (row r, column col) of the output; the pair's sum has half the heads
+            const size_t out = (((size_t)wk.start(c, kReverse) + r) * ps.no + (kPair ? hv >> 1 : hv)) * kDim + col;
+            const bool staged = L == kC && !ps.part;   // whole chunks of bf16 leave by TMA
+            const bool mine = r < L && in_range(out, 64, (long long)a.T * ps.no * kDim, a.status);
+            // the stage's Q tile is free: its readers finished before O did
+            unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
+            if (kPair && !keep) {
+                // the peer writes this half: to the stage's K tile, whose products are done, and from
+                // there to the peer's Q tile (rows of 32 columns, two planes)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[32];
                     tmem_ld32(from + 32 * h, x);
                     tmem_ld_wait();
-                    if (h == 1) {
-                        tc_fence_before();
-                        mbar_arrive(&sm.o_free);
-                    }
-                    scale32(x, scale);
-                    write32(ps, x, row + 32 * h, mine, staged, orow, r, h);
-                }
-                if (staged) {
-                    fence_proxy_async_smem();
-                    mbar_arrive(&sm.o_staged);
-                }
-                if (c + 1 < wk.n) publish();
-                if (staged) {
-                    stores += 1;
-                    if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1)) {
-                        for (int h = 0; h < 2; ++h)
-                            tma_store_3d(&maps.o, 64 * h, hv, wk.start(c, kReverse), sm.q[s] + h * kHalf);
-                        tma_store_commit();
-                    }
-                    __syncwarp();
-                }
-            } else {
-                // The exchange must not hold up the next KV.  The half that the peer writes goes to
-                // the stage's K tile, whose products are done, and from there to the peer's Q tile
-                // (rows of 32 columns, two planes); the own half to this chunk's P buffer, which
-                // is free until the stage is loaded again.
-                const uint32_t kept = tb + lanes + kColP + 128 * s + col;
-                const bool keep = (col >> 6) == (hv & 1);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    tmem_ld32(from + 32 * h, x);
-                    tmem_ld_wait();
-                    if (keep) {
-                        tmem_st32(kept + 32 * h, x);
-                        continue;
-                    }
                     if (h == 1) {
                         tc_fence_before();
                         mbar_arrive(&sm.o_free);
@@ -789,22 +705,60 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                         *reinterpret_cast<float4 *>(sm.k[s] + h * kHalf + r * 128 + ((j ^ (r & 7)) << 4)) =
                             make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
                 }
-                if (keep) {
-                    tmem_st_wait();
+                fence_proxy_async_smem();
+                if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
+                if (lane == 0) {   // this warp's 32 rows
+                    for (int h = 0; h < 2; ++h)
+                        remote_copy(sm.q[s] + h * kHalf + (r & ~31) * 128, sm.k[s] + h * kHalf + (r & ~31) * 128,
+                                    32 * 128, &sm.rx_full[s], (hv & 1) ^ 1);
+                }
+                __syncwarp();
+                if (c + 1 < wk.n) publish();
+                continue;
+            }
+            if (kPair) {
+                if (c + 1 < wk.n) publish();   // while the peer's half comes
+                if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
+                if (storer) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[32];
+                tmem_ld32(from + 32 * h, x);
+                tmem_ld_wait();
+                if (h == 1) {
                     tc_fence_before();
                     mbar_arrive(&sm.o_free);
-                    mbar_arrive(&sm.kept[s]);
-                } else {
-                    fence_proxy_async_smem();
-                    if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
-                    if (lane == 0) {   // this warp's 32 rows
-                        for (int h = 0; h < 2; ++h)
-                            remote_copy(sm.q[s] + h * kHalf + (r & ~31) * 128, sm.k[s] + h * kHalf + (r & ~31) * 128,
-                                        32 * 128, &sm.rx_full[s], (hv & 1) ^ 1);
-                    }
-                    __syncwarp();
                 }
-                if (c + 1 < wk.n) publish();
+                scale32(x, scale);
+                if (kPair) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
+                        const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + h * kHalf + r * 128 +
+                                                                           ((j ^ (r & 7)) << 4));
+                        x[4 * j] += y.x;
+                        x[4 * j + 1] += y.y;
+                        x[4 * j + 2] += y.z;
+                        x[4 * j + 3] += y.w;
+                    }
+                }
+                // (pair mode: over plane 0's row, which only this thread reads)
+                write32(ps, x, out + 32 * h, mine, staged, orow, r, h);
+            }
+            if (kPair || staged) {
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.o_staged);
+            }
+            if (!kPair && c + 1 < wk.n) publish();
+            if (kPair || staged) {
+                stores += 1;
+                if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1) && staged) {
+                    for (int h = 0; h < (kPair ? 1 : 2); ++h)
+                        tma_store_3d(&maps.o, kPair ? col : 64 * h, kPair ? hv >> 1 : hv, wk.start(c, kReverse),
+                                     sm.q[s] + h * kHalf);
+                    tma_store_commit();
+                }
+                __syncwarp();
             }
         }
         if (storer) tma_store_wait_all();
@@ -845,7 +799,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
                 // (loading this stage waited for O of chunk c - 2, which read this P buffer)
-                if (kMode == 0 && c > 0 && !wait_warp(sm, &sm.kv_free[s ^ 1], ((c - 1) >> 1) & 1)) break;
+                if (c > 0 && !wait_warp(sm, &sm.kv_free[s ^ 1], ((c - 1) >> 1) & 1)) break;
                 tc_fence_after();
                 const uint64_t qd = qd0 + ((s * kTile) >> 4), kd = kd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
@@ -864,8 +818,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait_warp(sm, &sm.s_ready, c & 1) ||
                     !wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1) ||
-                    (kPair ? !wait_warp(sm, &sm.kv_free[s], (c >> 1) & 1)
-                           : c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)))
+                    (c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)))
                     break;
                 tc_fence_after();
                 // this CTA's Q tile has been read: the peer may put its half of O there
@@ -901,9 +854,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             bool ok = true;
             for (int c = 0; c < wk.n && ok; ++c) {
                 const int s = c & 1;
-                if (kState   ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
-                    : kPair ? c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)
-                            : c > 0 && !wait_warp(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1))
+                if (kState ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
+                           : c > 0 && !wait_warp(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1))
                     break;
                 if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
@@ -947,9 +899,16 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
 template <int kSet>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ LinearArgs a, const __grid_constant__ LinMaps maps) {
-    const int passes = kSet == 1 ? a.state_passes : a.passes;
-    const int hv = blockIdx.x % a.HV, rest = blockIdx.x / a.HV, item = rest / passes;
-    const int p = rest % passes * (kSet == 1 ? 2 : 1);   // (the state pass takes scans 0 and 2)
+    const int hv = blockIdx.x % a.HV, rest = blockIdx.x / a.HV;
+    int item, p;
+    if (kSet >= 2 && rest >= 2 * a.items) {   // dv's scans, the shortest, fill in at the end
+        item = rest - 2 * a.items;
+        p = 2;
+    } else {
+        const int sides = kSet == 0 ? 1 : kSet == 1 ? a.state_passes : 2;
+        item = rest / sides;
+        p = rest % sides * (kSet == 1 ? 2 : 1);   // (the state pass takes scans 0 and 2)
+    }
     if (kSet == 0) {
         scan<false, 0>(a, a.pass[0], maps.pass[0], hv, item);
     } else if (kSet == 1) {

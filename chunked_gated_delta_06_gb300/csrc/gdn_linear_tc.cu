@@ -29,6 +29,7 @@
 // CTA's warps run as a pipeline over chunks: 8 warps turn P into P~ and build Q~, 8 warps
 // build W, 8 warps hold the state, publish its bf16 copy and write O, and one thread each
 // issues the loads and the three products.
+#include <cuda_fp16.h>
 #include <stddef.h>
 #include <string.h>
 
@@ -52,9 +53,10 @@ constexpr int kThreads = (kWarpLoad + 4) * 32;
 
 // Registers a thread: the state's warps hold 64 floats each.  The groups' shares must not
 // exceed what the launch gives (kThreads * kRegsLaunch), or the increase would never end.
-constexpr int kRegsLaunch = 72, kRegsWork = 56, kRegsState = 120, kRegsIssue = 40;
-static_assert((kGroupP + kGroupW) * kRegsWork + kGroupS * kRegsState + 4 * kRegsIssue <=
-                  (kWarpLoad + 4) * kRegsLaunch,
+constexpr int kRegsLaunch = 72, kRegsP = 80, kRegsW = 48, kRegsState = 104, kRegsIssue = 40;
+static_assert(kGroupP * kRegsP + kGroupW * kRegsW + kGroupS * kRegsState + 4 * kRegsIssue <=
+                      (kWarpLoad + 4) * kRegsLaunch &&
+                  kRegsW <= kRegsP,   // in the state pass P's warps do W's work, with W's share
               "register shares");
 
 // Tensor-memory columns
@@ -68,10 +70,10 @@ constexpr uint32_t kCols = 512;
 struct LinSmem {
     unsigned char q[2][kTile], k[2][kTile], v[2][kTile];  // TMA tiles, two stages
     unsigned char s[kTile];                               // bf16 copy of S, row r K-major
-    float wtab[2 * kC];   // w lam^{127-x} (forward) or w lam^{x+1} (reverse), zeros above 128
+    bf16 wtab[2][3][kC];  // weights of a whole and of the partial chunk's tokens, three parts each
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full_v[2], full_kq[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], q_free[2];
+    uint64_t full_v[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], q_free[2];
     uint64_t kv_free[2], s_ready, o_free, o_staged, factors, drain[3];
     // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
     uint64_t peer_ok[2], rx_full[2], sent[2];
@@ -141,6 +143,11 @@ __device__ __forceinline__ uint64_t keep_tops(float2 x) {
                 __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
 }
 
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 t = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+
 // Four 8 x 8 bf16 matrices of shared rows, each transposed: register m of lane l holds
 // (row 2 (l % 4) + {0, 1}, column l / 4) of matrix m, whose rows lanes 8 m .. 8 m + 7 point at.
 __device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
@@ -149,19 +156,13 @@ __device__ __forceinline__ void ldmatrix4t(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-// 16 lanes x 16 columns: register 2 k + e of lane t goes to lane t / 4 + 8 e, column 4 k + t % 4.
-__device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t (&u)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+// 16 lanes x 8 columns: register 2 k + e of lane t goes to lane t / 4 + 8 e, column 4 k + t % 4.
+__device__ __forceinline__ void tmem_st16x128_x2(uint32_t taddr, const uint32_t (&u)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3])
                  : "memory");
 }
 
-// One lane of a converged warp, always the same.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
 // ---- the other CTA of a cluster
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -194,6 +195,12 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
+}
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -247,7 +254,7 @@ template <int kMode>
 __device__ __forceinline__ uint32_t col_kv(int c) {
     return kMode != 2 ? kColP + 128 * ((c + 1) & 1) : c & 1 ? kColP : kColX;
 }
-__device__ __forceinline__ uint32_t col_w(int b) { return b < 2 ? kColW + 48 * b : kColP + 128 + 48 * (b - 2); }
+__device__ __forceinline__ uint32_t col_w(int b) { return b < 2 ? kColW + 64 * b : kColP + 128 + 64 * (b - 2); }
 
 // lam^{i+1} (forward) or lam^{L-1-i} (reverse) as 2^{e + f}, e whole and 0 <= f < 1.
 template <bool kReverse>
@@ -334,18 +341,17 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
     const float g2 = g * 1.4426950408889634f;
 
     const int hq = hv / (a.HV / ps.nq), hk = hv / (a.HV / ps.nk), hw = hv / (a.HV / ps.nv);
-    auto load_v = [&](int c) {
-        const int s = c & 1, t = wk.start(c, kReverse);
-        mbar_arrive_expect_tx(&sm.full_v[s], kTile);
-        for (int h = 0; h < 2; ++h) tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_v[s]);
+    // A stage's tiles come in two batches, by when their places are free: V and K after the
+    // products of the chunk that held them, Q (in pair mode K too) after its output has left.
+    auto load_k = [&](int c, uint64_t *bar) {
+        for (int h = 0; h < 2; ++h)
+            tma_load_3d(sm.k[c & 1] + h * kHalf, &maps.k, 64 * h, hk, wk.start(c, kReverse), bar);
     };
-    auto load_kq = [&](int c) {
+    auto load_first = [&](int c) {
         const int s = c & 1, t = wk.start(c, kReverse);
-        mbar_arrive_expect_tx(&sm.full_kq[s], kState ? kTile : 2 * kTile);
-        for (int h = 0; h < 2; ++h) {
-            tma_load_3d(sm.k[s] + h * kHalf, &maps.k, 64 * h, hk, t, &sm.full_kq[s]);
-            if (!kState) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_kq[s]);
-        }
+        mbar_arrive_expect_tx(&sm.full_v[s], kPair ? kTile : 2 * kTile);
+        for (int h = 0; h < 2; ++h) tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_v[s]);
+        if (!kPair) load_k(c, &sm.full_v[s]);
         // the tiles after next start towards L2 while both stages are taken
         if (c + 2 < wk.n) {
             const int t2 = wk.start(c + 2, kReverse);
@@ -356,12 +362,18 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             }
         }
     };
+    auto load_second = [&](int c) {
+        const int s = c & 1, t = wk.start(c, kReverse);
+        mbar_arrive_expect_tx(&sm.full_q[s], kPair ? 2 * kTile : kTile);
+        for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_q[s]);
+        if (kPair) load_k(c, &sm.full_q[s]);
+    };
     if (warp == kWarpLoad) {
         if (elect_one()) {
             if (wk.n > 0) tma_prefetch_maps(maps);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sm.full_v[i], 1);
-                mbar_init(&sm.full_kq[i], 1);
+                mbar_init(&sm.full_q[i], 1);
                 mbar_init(&sm.p_done[i], 1);
                 mbar_init(&sm.pt_ready[i], kGroupP * 32);
                 mbar_init(&sm.v_ok[i], kGroupW * 32);
@@ -379,15 +391,15 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             }
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
-            mbar_init(&sm.o_staged, kGroupS * (kPair ? 16 : 32));
+            mbar_init(&sm.o_staged, kGroupS * 32);
             mbar_init(&sm.factors, 1);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
             fence_proxy_async_smem();
             for (int c = 0; c < min(2, wk.n); ++c) {   // both stages, before anything else is set up
-                load_v(c);
-                load_kq(c);
+                load_first(c);
+                if (!kState) load_second(c);
             }
         }
         __syncwarp();
@@ -395,10 +407,14 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         tmem_alloc(&sm.tmem_base, kCols);
         tmem_relinquish();
     }
-    if (tid < kC) {
-        const int power = kReverse ? tid + 1 : kC - 1 - tid;
-        sm.wtab[tid] = ps.w * exp2f(g2 * (float)power);
-        sm.wtab[kC + tid] = 0.f;
+    if (tid < 2 * kC) {
+        const int part = tid >> 7, t = tid & (kC - 1), L = part ? wk.len % kC : kC;
+        float w = t < L ? ps.w * exp2f(g2 * (float)(kReverse ? t + 1 : L - 1 - t)) : 0.f;
+        for (int x = 0; x < 3; ++x) {
+            const bf16 y = f2bf(w);
+            sm.wtab[part][x][t] = y;
+            w -= bf2f(y);
+        }
         if (tid < 32) sm.ptab[tid] = exp2f(g2 * (float)(kReverse ? tid : 31 - tid));
     }
     tc_fence_before();
@@ -410,7 +426,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
 
     if (!kState && warp < kGroupP) {
         // ---------------------------------------------------------- P~ and Q~
-        regs_down<kRegsWork>();
+        regs_up<kRegsP>();
         const int quad = warp & 3, half = warp >> 2;   // rows 32 quad .., columns 64 half ..
         const int i = quad * 32 + lane;
         const float at = (float)lane, lw = log2f(ps.w);   // w > 0
@@ -419,6 +435,22 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             const int L = wk.length(c, kReverse);
             float e, f;
             read_power<kReverse>(g2, i, L, e, f);
+            // Q~ first, while P is formed; it waits in registers for its columns
+            if (!wait_warp(sm, &sm.full_q[c & 1], (c >> 1) & 1)) break;
+            const unsigned char *qt = sm.q[c & 1] + half * kHalf;
+            const __nv_bfloat162 pw = __float2bfloat162_rn(
+                e < -120.f ? 0.f : __int_as_float(((int)e + 127) << 23));
+            float q[32];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const uint4 z = *reinterpret_cast<const uint4 *>(qt + sw128_off(i, 8 * p));
+                const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&zz[y]), pw);
+                    q[4 * p + y] = __uint_as_float(*reinterpret_cast<const uint32_t *>(&t));
+                }
+            }
             if (!wait_warp(sm, &sm.p_done[c & 1], (c >> 1) & 1)) break;
             tc_fence_after();
 #pragma unroll 1
@@ -463,22 +495,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 }
                 tmem_st16(mine + 16 * b2, x);   // over columns that this warp has read
             }
-            const unsigned char *qt = sm.q[c & 1] + half * kHalf;
-            const __nv_bfloat162 pw = __float2bfloat162_rn(
-                e < -120.f ? 0.f : __int_as_float(((int)e + 127) << 23));
-            float x[32];
-            uint32_t *u = reinterpret_cast<uint32_t *>(x);
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const uint4 z = *reinterpret_cast<const uint4 *>(qt + sw128_off(i, 8 * p));
-                const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&zz[y]), pw);
-                    u[4 * p + y] = *reinterpret_cast<const uint32_t *>(&t);
-                }
-            }
-            tmem_st32(mine + 32, x);
+            tmem_st32(mine + 32, q);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.pt_ready[c & 1]);
@@ -487,20 +504,23 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         // ---------------------------------------------------------- W
         // Half h of the group fills buffer h with the 32-token quarters h and h + 2; in the state
         // pass P's warps take the quarters 2 and 3, with buffers of their own.
-        regs_down<kRegsWork>();
+        regs_down<kRegsW>();
         const int quad = warp & 3, half = warp < kGroupP ? 2 + (warp >> 2) : (warp - kGroupP) >> 2;
         const uint32_t buf = tb + lanes + col_w(half);
         // this lane's row of the first quarter, and the four 8-feature chunks of the warp in it
-        const uint32_t vrow = smem_u32(sm.v[0] + (quad >> 1) * kHalf) + (32 * half + lane) * 128;
-        uint32_t chunk[4];
+        // (rows: 8 tokens of the first or second half of 16; chunks: the first or last 16 features)
+        const uint32_t vrow = smem_u32(sm.v[0] + (quad >> 1) * kHalf) +
+                              (32 * half + 8 * ((lane >> 3) & 1) + (lane & 7)) * 128;
+        uint32_t chunk[2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) chunk[x] = (uint32_t)((4 * (quad & 1) + x) ^ (lane & 7)) * 16;
+        for (int x = 0; x < 2; ++x)
+            chunk[x] = (uint32_t)((4 * (quad & 1) + 2 * x + (lane >> 4)) ^ (lane & 7)) * 16;
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
             if (!(ok = wait_warp(sm, &sm.full_v[s], (c >> 1) & 1))) break;
             if (L < kC) {
-                if (!(ok = wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1))) break;
+                if (kPair && !(ok = wait_warp(sm, &sm.full_q[s], (c >> 1) & 1))) break;
                 // rows past the sequence hold the next one's tokens: zeros instead (each half
                 // clears its own quarters of K, which the product of a quarter waits for)
                 for (int x = quad * 32 + lane; x < (kState ? 1 : 2) * 32 * 16; x += kGroupW * 16) {
@@ -513,48 +533,53 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 fence_proxy_async_smem();
             }
             if (!kState) mbar_arrive(&sm.v_ok[s]);
-            const float *wt = sm.wtab + (kReverse ? 0 : kC - L) + 32 * half + 2 * (lane & 3);
+            const bf16 *wt = sm.wtab[L < kC][0] + 32 * half + 2 * (lane & 3);
             const uint32_t vt = vrow + s * kTile;
 #pragma unroll 1
             for (int pass = 0; pass < (kState ? 1 : 2); ++pass) {
                 const int use = kState ? c : 2 * c + pass;
-                uint64_t w2[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w2[k] = pair(wt[64 * pass + 8 * k], wt[64 * pass + 8 * k + 1]);
                 if (use > 0 && !(ok = wait_warp(sm, &sm.w_free[half], (use - 1) & 1))) break;
                 tc_fence_after();
+#pragma unroll 1
+                for (int k16 = 0; k16 < 2; ++k16) {   // 16 tokens
+                    __nv_bfloat162 w[2][3];
 #pragma unroll
-                for (int g16 = 0; g16 < 2; ++g16) {   // features 32 quad + 16 g16 ..
-                    uint32_t in[2][4], hi[8], mid[8], lo[8];
-                    ldmatrix4t(vt + pass * 64 * 128 + chunk[2 * g16], in[0]);
-                    ldmatrix4t(vt + pass * 64 * 128 + chunk[2 * g16 + 1], in[1]);
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int x = 0; x < 3; ++x)
+                            w[k][x] = *reinterpret_cast<const __nv_bfloat162 *>(wt + x * kC + 64 * pass + 16 * k16 + 8 * k);
+                    uint32_t in[2][4];
+                    ldmatrix4t(vt + (64 * pass + 16 * k16) * 128 + chunk[0], in[0]);
+                    ldmatrix4t(vt + (64 * pass + 16 * k16) * 128 + chunk[1], in[1]);
                     if (L < kC) {   // tokens past the sequence
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int left = L - (64 * pass + 32 * half + 8 * k + 2 * (lane & 3));
+                        for (int k = 0; k < 2; ++k) {
+                            const int left = L - (64 * pass + 32 * half + 16 * k16 + 8 * k + 2 * (lane & 3));
                             const uint32_t keep = left > 1 ? 0xffffffffu : left > 0 ? 0xffffu : 0u;
-                            in[0][k] &= keep;
-                            in[1][k] &= keep;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) in[x >> 1][k + 2 * (x & 1)] &= keep;
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int g16 = 0; g16 < 2; ++g16) {   // features 32 quad + 16 g16 ..
+                        uint32_t part[4][4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t v2 = in[e][k];
-                            const float2 x = unpair(mul2(w2[k], pair(__uint_as_float(v2 << 16),
-                                                                     __uint_as_float(v2 & 0xffff0000u))));
-                            const float2 y = unpair(sub2(pair(x.x, x.y), keep_tops(x)));
-                            const float2 z = unpair(sub2(pair(y.x, y.y), keep_tops(y)));
-                            hi[2 * k + e] = tops(x);
-                            mid[2 * k + e] = tops(y);
-                            lo[2 * k + e] = tops(z);
+                        for (int x = 0; x < 4; ++x) {   // 8 tokens x & 1, features 8 (x >> 1) ..
+                            const __nv_bfloat162 *wx = w[x & 1];
+                            const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162 *>(&in[g16][x]);
+                            const __nv_bfloat162 h = __hmul2(wx[0], v2), l = __hfma2(wx[0], v2, __hneg2(h));
+                            const __nv_bfloat162 p = __hmul2(wx[1], v2);
+                            const __nv_bfloat162 r = __hfma2(wx[2], v2, __hfma2(wx[1], v2, __hneg2(p)));
+                            const int at = 2 * (x & 1) + (x >> 1);
+                            part[0][at] = *reinterpret_cast<const uint32_t *>(&h);
+                            part[1][at] = *reinterpret_cast<const uint32_t *>(&l);
+                            part[2][at] = *reinterpret_cast<const uint32_t *>(&p);
+                            part[3][at] = *reinterpret_cast<const uint32_t *>(&r);
                         }
+                        const uint32_t at = buf + ((uint32_t)(16 * g16) << 16) + 8 * k16;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) tmem_st16x128_x2(at + 16 * y, part[y]);
                     }
-                    const uint32_t at = buf + ((uint32_t)(16 * g16) << 16);
-                    tmem_st16x128_x4(at, hi);
-                    tmem_st16x128_x4(at + 16, mid);
-                    tmem_st16x128_x4(at + 32, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -646,9 +671,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         };
         const bool have = wk.n == 0 || wait_warp(sm, &sm.factors, 0);
         int stores = 0;
-        // pair mode: the warps whose half of O this CTA writes, and those whose half the peer does
-        const bool keep = !kPair || (col >> 6) == (hv & 1);
-        const bool storer = tid == (kGroupP + kGroupW) * 32 + (kPair ? 128 * (hv & 1) : 0);
+        const bool storer = tid == (kGroupP + kGroupW) * 32;
         for (int c = 0; have && c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
             if (!kState && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
@@ -681,15 +704,68 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             read_power<kReverse>(g2, r, L, e, f);
             const float scale = ps.so * ex2(f);
             const uint32_t from = tb + lanes + kColX + col;
-            // element (row r, column col) of the output; the pair's sum has half the heads
-            const size_t out = (((size_t)wk.start(c, kReverse) + r) * ps.no + (kPair ? hv >> 1 : hv)) * kDim + col;
+            const int first = kPair ? 64 * (hv & 1) + (col >> 1) : col;   // this warp's first column to write
+            const size_t out = (((size_t)wk.start(c, kReverse) + r) * ps.no + (kPair ? hv >> 1 : hv)) * kDim + first;
             const bool staged = L == kC && !ps.part;   // whole chunks of bf16 leave by TMA
-            const bool mine = r < L && in_range(out, 64, (long long)a.T * ps.no * kDim, a.status);
+            const bool mine = r < L && in_range(out, kPair ? 32 : 64, (long long)a.T * ps.no * kDim, a.status);
             // the stage's Q tile is free: its readers finished before O did
             unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
-            if (kPair && !keep) {
-                // the peer writes this half: to the stage's K tile, whose products are done, and from
-                // there to the peer's Q tile (rows of 32 columns, two planes)
+            if (kPair) {
+                // Each CTA writes 64 columns of the pair's sum; the other 64 go to the peer as fp16
+                // times a power of two for each 32 of a row (2^-12 of the largest at most, where the
+                // output is rounded at 2^-9): from the stage's K tile, whose products are done, to
+                // the peer's Q tile, rows in plane 0 and their factors in plane 1.
+                if ((col >> 6) != (hv & 1)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x[32];
+                        tmem_ld32(from + 32 * h, x);
+                        tmem_ld_wait();
+                        float big = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(x[j]));
+                        // 2^e <= big < 2^{e+1}, within the normal numbers (infinities stay infinite)
+                        const uint32_t e = min(max(__float_as_uint(big) & 0x7f800000u, 1u << 23), 253u << 23);
+                        scale32(x, __uint_as_float((254u << 23) - e));
+                        reinterpret_cast<float *>(sm.k[s] + kHalf)[2 * r + h] = scale * __uint_as_float(e);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(sm.k[s] + r * 128 + (((4 * h + j) ^ (r & 7)) << 4)) = make_uint4(
+                                pack_half2(x[8 * j], x[8 * j + 1]), pack_half2(x[8 * j + 2], x[8 * j + 3]),
+                                pack_half2(x[8 * j + 4], x[8 * j + 5]), pack_half2(x[8 * j + 6], x[8 * j + 7]));
+                    }
+                    fence_proxy_async_smem();
+                    if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
+                    if (lane == 0) {   // this warp's 32 rows
+                        const uint32_t peer = (hv & 1) ^ 1;
+                        remote_copy(sm.q[s] + r * 128, sm.k[s] + r * 128, 32 * 128, &sm.rx_full[s], peer);
+                        remote_copy(sm.q[s] + kHalf + r * 8, sm.k[s] + kHalf + r * 8, 32 * 8, &sm.rx_full[s], peer);
+                    }
+                    __syncwarp();
+                }
+                if (c + 1 < wk.n) publish();   // while the peer's half comes
+                if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
+                if (storer) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
+                const int h = col >> 6;
+                float x[32];
+                tmem_ld32(tb + lanes + kColX + first, x);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(&sm.o_free);
+                const float theirs = reinterpret_cast<const float *>(sm.q[s] + kHalf)[2 * r + h];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {   // (two terms: the same sum whichever CTA adds)
+                    const uint4 y = *reinterpret_cast<const uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4));
+                    const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&yy[i]));
+                        x[8 * j + 2 * i] = fmaf(theirs, z.x, scale * x[8 * j + 2 * i]);
+                        x[8 * j + 2 * i + 1] = fmaf(theirs, z.y, scale * x[8 * j + 2 * i + 1]);
+                    }
+                }
+                write32(ps, x, out, mine, staged, orow, r, h);   // (over the 16 bytes it has read)
+            } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[32];
@@ -700,66 +776,24 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                         mbar_arrive(&sm.o_free);
                     }
                     scale32(x, scale);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<float4 *>(sm.k[s] + h * kHalf + r * 128 + ((j ^ (r & 7)) << 4)) =
-                            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                    write32(ps, x, out + 32 * h, mine, staged, orow, r, h);
                 }
-                fence_proxy_async_smem();
-                if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
-                if (lane == 0) {   // this warp's 32 rows
-                    for (int h = 0; h < 2; ++h)
-                        remote_copy(sm.q[s] + h * kHalf + (r & ~31) * 128, sm.k[s] + h * kHalf + (r & ~31) * 128,
-                                    32 * 128, &sm.rx_full[s], (hv & 1) ^ 1);
-                }
-                __syncwarp();
-                if (c + 1 < wk.n) publish();
-                continue;
-            }
-            if (kPair) {
-                if (c + 1 < wk.n) publish();   // while the peer's half comes
-                if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
-                if (storer) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float x[32];
-                tmem_ld32(from + 32 * h, x);
-                tmem_ld_wait();
-                if (h == 1) {
-                    tc_fence_before();
-                    mbar_arrive(&sm.o_free);
-                }
-                scale32(x, scale);
-                if (kPair) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {   // (two terms: the same bits whichever CTA adds)
-                        const float4 y = *reinterpret_cast<const float4 *>(sm.q[s] + h * kHalf + r * 128 +
-                                                                           ((j ^ (r & 7)) << 4));
-                        x[4 * j] += y.x;
-                        x[4 * j + 1] += y.y;
-                        x[4 * j + 2] += y.z;
-                        x[4 * j + 3] += y.w;
-                    }
-                }
-                // (pair mode: over plane 0's row, which only this thread reads)
-                write32(ps, x, out + 32 * h, mine, staged, orow, r, h);
             }
             if (kPair || staged) {
                 fence_proxy_async_smem();
                 mbar_arrive(&sm.o_staged);
             }
-            if (!kPair && c + 1 < wk.n) publish();
             if (kPair || staged) {
                 stores += 1;
                 if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1) && staged) {
                     for (int h = 0; h < (kPair ? 1 : 2); ++h)
-                        tma_store_3d(&maps.o, kPair ? col : 64 * h, kPair ? hv >> 1 : hv, wk.start(c, kReverse),
+                        tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv, wk.start(c, kReverse),
                                      sm.q[s] + h * kHalf);
                     tma_store_commit();
                 }
                 __syncwarp();
             }
+            if (!kPair && c + 1 < wk.n) publish();
         }
         if (storer) tma_store_wait_all();
         if (wk.n == 0) store_state();
@@ -772,32 +806,33 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         const int role = __shfl_sync(0xffffffffu, warp, 0) - kWarpLoad;
         if (role == 0) {
             // ------------------------------------------------------ loads
-            int issued_v = min(2, wk.n), issued_kq = issued_v;
+            int issued_v = min(2, wk.n), issued_q = kState ? 0 : issued_v;
             for (int c = 2; c < wk.n; ++c) {
                 const int s = c & 1, mark = ((c >> 1) - 1) & 1;
                 if ((!kState && !wait_warp(sm, &sm.o_done[s], mark)) || !wait_warp(sm, &sm.kv_done[s], mark)) break;
-                if (elect_one()) load_v(c);
+                if (elect_one()) load_first(c);
                 __syncwarp();
                 issued_v = c + 1;
+                if (kState) continue;
                 // the last output of this stage has left its Q tile (and the exchange its K tile)
-                if (!kState && !wait_warp(sm, &sm.q_free[s], mark)) break;
+                if (!wait_warp(sm, &sm.q_free[s], mark)) break;
                 if (kPair && !wait_warp_cluster(sm, &sm.sent[s], mark)) break;
-                if (elect_one()) load_kq(c);
+                if (elect_one()) load_second(c);
                 __syncwarp();
-                issued_kq = c + 1;
+                issued_q = c + 1;
             }
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
             for (int c = max(0, issued_v - 2); c < issued_v; ++c)
                 mbar_wait(&sm.full_v[c & 1], (c >> 1) & 1, kDrainLimitNs);
-            for (int c = max(0, issued_kq - 2); c < issued_kq; ++c)
-                mbar_wait(&sm.full_kq[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            for (int c = max(0, issued_q - 2); c < issued_q; ++c)
+                mbar_wait(&sm.full_q[c & 1], (c >> 1) & 1, kDrainLimitNs);
         } else if (role == 1) {
             // ------------------------------------------------------ P = Q K^T
             const uint32_t id = idesc_bf16(128, 128, 0, 0);
             const uint64_t qd0 = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
             for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
-                if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
+                if (!wait_warp(sm, &sm.full_v[s], (c >> 1) & 1) || !wait_warp(sm, &sm.full_q[s], (c >> 1) & 1)) break;
                 // (loading this stage waited for O of chunk c - 2, which read this P buffer)
                 if (c > 0 && !wait_warp(sm, &sm.kv_free[s ^ 1], ((c - 1) >> 1) & 1)) break;
                 tc_fence_after();
@@ -823,7 +858,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 tc_fence_after();
                 // this CTA's Q tile has been read: the peer may put its half of O there
                 if (kPair && elect_one()) {
-                    mbar_arrive_expect_tx(&sm.rx_full[s], kTile);
+                    mbar_arrive_expect_tx(&sm.rx_full[s], kHalf + kC * 8);
                     remote_arrive(&sm.peer_ok[s], (hv & 1) ^ 1);
                 }
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
@@ -857,7 +892,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 if (kState ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
                            : c > 0 && !wait_warp(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1))
                     break;
-                if (!wait_warp(sm, &sm.full_kq[s], (c >> 1) & 1)) break;
+                if (!wait_warp(sm, kPair ? &sm.full_q[s] : &sm.full_v[s], (c >> 1) & 1)) break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd) {
@@ -869,7 +904,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
-                            for (int part = 0; part < 3; ++part)
+                            for (int part = 0; part < 4; ++part)
                                 mma_ts(tb + col_kv<kMode>(c), tb + col_w(b) + 16 * part + 8 * x,
                                        kd + 128 * (2 * qd + x), id, qd > 0 || x > 0 || part > 0);
                         mma_commit(&sm.w_free[b]);

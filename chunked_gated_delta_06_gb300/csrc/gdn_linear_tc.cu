@@ -73,8 +73,8 @@ struct LinSmem {
     bf16 wtab[2][3][kC];  // weights of a whole and of the partial chunk's tokens, three parts each
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full_v[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], q_free[2];
-    uint64_t kv_free[2], s_ready, o_free, o_staged, factors, drain[3];
+    uint64_t full_v[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], o_staged[2];
+    uint64_t kv_free[2], s_ready, o_free, factors, drain[3];
     // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
     uint64_t peer_ok[2], rx_full[2], sent[2];
     uint32_t tmem_base;
@@ -379,7 +379,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 mbar_init(&sm.v_ok[i], kGroupW * 32);
                 mbar_init(&sm.kv_done[i], 1);
                 mbar_init(&sm.o_done[i], 1);
-                mbar_init(&sm.q_free[i], 1);
+                mbar_init(&sm.o_staged[i], kGroupS * 32);
                 mbar_init(&sm.peer_ok[i], 1);
                 mbar_init(&sm.rx_full[i], 1);
                 mbar_init(&sm.sent[i], 1);
@@ -391,7 +391,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             }
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
-            mbar_init(&sm.o_staged, kGroupS * 32);
             mbar_init(&sm.factors, 1);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
@@ -670,14 +669,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             }
         };
         const bool have = wk.n == 0 || wait_warp(sm, &sm.factors, 0);
-        int stores = 0;
-        const bool storer = tid == (kGroupP + kGroupW) * 32;
         for (int c = 0; have && c < wk.n; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (!kState && storer && c > 0) {   // the last chunk's output has left its stage's Q tile
-                tma_store_wait_read();
-                mbar_arrive(&sm.q_free[s ^ 1]);
-            }
             const float fh = L < kC ? sm.part_hi : sm.full_hi, fl = L < kC ? sm.part_lo : sm.full_lo;
             if (!wait_warp(sm, &sm.kv_done[s], (c >> 1) & 1)) break;
             tc_fence_after();
@@ -745,7 +738,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 }
                 if (c + 1 < wk.n) publish();   // while the peer's half comes
                 if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
-                if (storer) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
+                if (warp == kGroupP + kGroupW && lane == 0) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
                 const int h = col >> 6;
                 float x[32];
                 tmem_ld32(tb + lanes + kColX + first, x);
@@ -779,23 +772,10 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     write32(ps, x, out + 32 * h, mine, staged, orow, r, h);
                 }
             }
-            if (kPair || staged) {
-                fence_proxy_async_smem();
-                mbar_arrive(&sm.o_staged);
-            }
-            if (kPair || staged) {
-                stores += 1;
-                if (storer && wait(sm, &sm.o_staged, (stores - 1) & 1) && staged) {
-                    for (int h = 0; h < (kPair ? 1 : 2); ++h)
-                        tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv, wk.start(c, kReverse),
-                                     sm.q[s] + h * kHalf);
-                    tma_store_commit();
-                }
-                __syncwarp();
-            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sm.o_staged[s]);
             if (!kPair && c + 1 < wk.n) publish();
         }
-        if (storer) tma_store_wait_all();
         if (wk.n == 0) store_state();
     } else {
         // ---------------------------------------------------------- issuing warps
@@ -807,20 +787,42 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         if (role == 0) {
             // ------------------------------------------------------ loads
             int issued_v = min(2, wk.n), issued_q = kState ? 0 : issued_v;
-            for (int c = 2; c < wk.n; ++c) {
+            // The output of chunk c leaves its stage's Q tile (a partial chunk's has been written).
+            auto store = [&](int c) {
+                const int s = c & 1;
+                if (!wait_warp(sm, &sm.o_staged[s], (c >> 1) & 1)) return false;
+                if (wk.length(c, kReverse) == kC && !ps.part && elect_one()) {
+                    for (int h = 0; h < (kPair ? 1 : 2); ++h)
+                        tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv,
+                                     wk.start(c, kReverse), sm.q[s] + h * kHalf);
+                    tma_store_commit();
+                    tma_store_wait_read();
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = true;
+            for (int c = 2; c < wk.n && ok; ++c) {
                 const int s = c & 1, mark = ((c >> 1) - 1) & 1;
+                ok = false;
                 if ((!kState && !wait_warp(sm, &sm.o_done[s], mark)) || !wait_warp(sm, &sm.kv_done[s], mark)) break;
                 if (elect_one()) load_first(c);
                 __syncwarp();
                 issued_v = c + 1;
+                ok = true;
                 if (kState) continue;
-                // the last output of this stage has left its Q tile (and the exchange its K tile)
-                if (!wait_warp(sm, &sm.q_free[s], mark)) break;
+                ok = false;
+                // the last output of this stage leaves its Q tile (and the exchange its K tile)
+                if (!store(c - 2)) break;
                 if (kPair && !wait_warp_cluster(sm, &sm.sent[s], mark)) break;
                 if (elect_one()) load_second(c);
                 __syncwarp();
                 issued_q = c + 1;
+                ok = true;
             }
+            for (int c = max(0, wk.n - 2); !kState && ok && c < wk.n; ++c) ok = store(c);
+            if (elect_one()) tma_store_wait_all();
+            __syncwarp();
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
             for (int c = max(0, issued_v - 2); c < issued_v; ++c)
                 mbar_wait(&sm.full_v[c & 1], (c >> 1) & 1, kDrainLimitNs);

@@ -479,7 +479,7 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
         return best;
     }
     double t = 0.9 * launch_cost(longest + start, work);
-    for (int seg : {4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256}) {
+    for (int seg : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256}) {
         double work1 = 0.0, work2 = 0.0;
         int64_t items = 0;
         for (int n = 0; n < d.N; ++n) {

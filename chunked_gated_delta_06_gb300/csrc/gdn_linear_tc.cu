@@ -970,20 +970,26 @@ __global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ L
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
     const double lam = exp((double)g * (double)a.seg_chunks * kC);
     const float fh = (float)lam, fl = (float)(lam - (double)fh);
-    const size_t step = (size_t)a.HV * kDim * kDim;
+    const size_t step4 = (size_t)a.HV * kDim * kDim / 4;
     float *rec = a.pass[blockIdx.z % a.state_passes * 2].seg_state;
     float4 *p = reinterpret_cast<float4 *>(rec + ((size_t)first * a.HV + hv) * kDim * kDim) +
                 blockIdx.x * 256 + threadIdx.x;
     float4 y = *p;
-    for (int k = 1; k < nseg - 1; ++k) {
-        p += step / 4;
-        float4 z = *p;
-        z.x = fmaf(y.x, fh, fmaf(y.x, fl, z.x));
-        z.y = fmaf(y.y, fh, fmaf(y.y, fl, z.y));
-        z.z = fmaf(y.z, fh, fmaf(y.z, fl, z.z));
-        z.w = fmaf(y.w, fh, fmaf(y.w, fl, z.w));
-        *p = z;
-        y = z;
+    for (int k = 1; k < nseg - 1; k += 8) {   // eight records on their way at once
+        float4 z[8];
+        const int m = min(8, nseg - 1 - k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < m) z[j] = p[(size_t)(k + j) * step4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < m) {
+                y.x = fmaf(y.x, fh, fmaf(y.x, fl, z[j].x));
+                y.y = fmaf(y.y, fh, fmaf(y.y, fl, z[j].y));
+                y.z = fmaf(y.z, fh, fmaf(y.z, fl, z[j].z));
+                y.w = fmaf(y.w, fh, fmaf(y.w, fl, z[j].w));
+                p[(size_t)(k + j) * step4] = y;
+            }
     }
 }
 

@@ -8,6 +8,8 @@
 // position: pos is split into two parts that fp32 holds exactly, each part's product loses
 // its whole turns inside one fused multiply-add (rounded once), and only a fraction of a
 // turn reaches sincospif.  An fp32 angle would be off by 2^-24 pos radians instead.
+#include <algorithm>
+
 #include "gdn_linear.h"
 
 namespace gdn {
@@ -96,7 +98,12 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a, int tokens)
 
 template <int V>
 cudaError_t launch_width(const RopeArgs &a, cudaStream_t s) {
-    const int tokens = 1;
+    // Up to four tokens a block, for about four units a thread, once every SM has blocks for its
+    // eight places all the same (32768 tokens of 32 heads of 128: 97 us with one, 87 with four;
+    // 16384 tokens of 36 heads of 256, nine units a thread with four: 97 and 101).  A decoding
+    // step keeps one, to spread over the SMs (256 tokens: 9 us, 11 with four).
+    const int units = (a.Hq + a.Hk) * (a.D / (2 * V)), places = 8 * 152;
+    const int tokens = std::max(1, std::min({4, 4 * kThreads / units, a.T / places}));
     const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);
     const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
     if (a.interleaved) k_rope<V, true><<<grid, kThreads, smem, s>>>(a, tokens);

@@ -339,6 +339,16 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
     wk.n = nseg > 1 ? min(a.seg_chunks, wk.total - wk.first) : wk.total;
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
     const float g2 = g * 1.4426950408889634f;
+    bool cut = false;
+    if (kState && g2 * (float)(wk.n * kC) < -150.f) {
+        // tokens whose weight at the segment's end is below 2^-150, which is zero in fp32
+        const int need = (int)ceilf(-150.f / (g2 * kC));
+        cut = need < wk.n;
+        if (cut) {
+            wk.first += wk.n - need;
+            wk.n = need;
+        }
+    }
 
     const int hq = hv / (a.HV / ps.nq), hk = hv / (a.HV / ps.nk), hw = hv / (a.HV / ps.nv);
     // A stage's tiles come in two batches, by when their places are free: V and K after the
@@ -647,6 +657,10 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             for (int j = 0; j < 16; ++j)
                 *reinterpret_cast<float4 *>(keep_start + (size_t)r * kDim + col + 4 * j) =
                     make_float4(st[4 * j], st[4 * j + 1], st[4 * j + 2], st[4 * j + 3]);
+        }
+        if (cut) {   // the start state too
+#pragma unroll
+            for (int j = 0; j < 64; ++j) st[j] = 0.f;
         }
         unsigned char *srow = sm.s + (col >> 6) * kHalf;
         auto publish = [&]() {

@@ -447,16 +447,20 @@ gdn_status decode_impl(int32_t batch, int32_t num_k_heads, int32_t num_v_heads, 
 // How the scans of one problem are run: a CTA walks the 128-token chunks of one (sequence,
 // value head), about as long for each.  Few long sequences leave SMs idle, so a split plan
 // cuts every sequence into segments of `seg` chunks: a pass over the states alone, a stitch,
-// and the full pass over all segments at once.  Costs in chunks of the full pass: 0.35 for a
-// chunk of the state pass, 2 for a CTA's start and end, 2 for the two launches more; a
-// launch takes the longer of one CTA and the work over 152 SMs, and half a CTA more when
-// they take turns.  A split has to gain a tenth.  A function of the problem alone.
+// and the full pass over all segments at once.  Costs in chunks of a forward: 0.35 for a
+// chunk of the state pass, 1.3 for one of dq and dk in pairs, 2 for a CTA's start and end, 2 for
+// the two launches more; a launch takes the longer of one CTA and the work over 152 SMs, and
+// half a CTA more when they take turns.  A split has to gain a tenth.  (1 x 65536 tokens, 64
+// heads: segments of 16, 32, 64 chunks and none take 1.10, 0.94, 0.96 and 1.36 ms.)  A function of the problem alone.
 struct LinearPlan {
     int seg, items;
 };
-LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
+LinearPlan plan_linear(const gdn_problem *p, const Dims &d, int backward) {
     LinearPlan best{0, d.N};
     if (d.N > gdn::kLinearOrder || p->scan_segment_chunks < 0) return best;
+    const bool pair = backward && d.HV / d.H % 2 == 0;
+    const double one = pair ? 1.3 : 1.0;                       // a chunk of the longest scan
+    const double all = !backward ? 1.0 : pair ? 3.6 : 3.0;     // of all the scans
     auto launch_cost = [&](double cta, double work) {
         const double area = work * d.HV / 152.0;
         return area <= cta ? cta : area + 0.5 * cta;
@@ -478,7 +482,7 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
         if (items > d.N && items * d.HV <= 16384) best = {seg, (int)items};
         return best;
     }
-    double t = 0.9 * launch_cost(longest + start, work);
+    double t = 0.9 * launch_cost(one * longest + start, all * work);
     for (int seg : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256}) {
         double work1 = 0.0, work2 = 0.0;
         int64_t items = 0;
@@ -489,7 +493,8 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d) {
             items += k;
         }
         if (items == d.N || items * d.HV > 16384) continue;  // 1 GiB of states at most
-        const double cost = launch_cost(state * seg + start, work1) + launch_cost(seg + start, work2) + 2.0;
+        const double cost = launch_cost(state * seg + start, (backward ? 2.0 : 1.0) * work1) +
+                            launch_cost(one * seg + start, all * work2) + 2.0;
         if (cost < t) {
             t = cost;
             best = {seg, (int)items};
@@ -585,7 +590,7 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
         if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
     if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
-    const LinearPlan plan = plan_linear(p, d);
+    const LinearPlan plan = plan_linear(p, d, 0);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
     if ((st = check_linear_ws(carve_linear(d, plan, 0, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
@@ -754,7 +759,7 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward) {
     LinearWs ws;
     if (for_backward < 0 || for_backward > 1) return 0;
     if (check_problem(p, &d) != GDN_OK) return 0;
-    const size_t need = carve_linear(d, plan_linear(p, d), for_backward, nullptr, &ws);
+    const size_t need = carve_linear(d, plan_linear(p, d, for_backward), for_backward, nullptr, &ws);
     return need > 0 ? need : kAlign;
 }
 
@@ -792,7 +797,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
         if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
     if (dh0 && dh0 == d_final_state) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
-    const LinearPlan plan = plan_linear(p, d);
+    const LinearPlan plan = plan_linear(p, d, 1);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
     if ((st = check_linear_ws(carve_linear(d, plan, 1, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -591,7 +591,7 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
     if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
     const LinearPlan plan = plan_linear(p, d, 0);
-    if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)plan.items * d.HV > 0x7fffffffLL / 3) return GDN_ERR_INVALID_ARG;
     if ((st = check_linear_ws(carve_linear(d, plan, 0, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
     a.passes = a.state_passes = 1;
@@ -798,7 +798,7 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     if (dh0 && dh0 == d_final_state) return GDN_ERR_INVALID_ARG;
     LinearWs ws;
     const LinearPlan plan = plan_linear(p, d, 1);
-    if ((int64_t)plan.items * d.HV > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if ((int64_t)plan.items * d.HV > 0x7fffffffLL / 3) return GDN_ERR_INVALID_ARG;
     if ((st = check_linear_ws(carve_linear(d, plan, 1, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);

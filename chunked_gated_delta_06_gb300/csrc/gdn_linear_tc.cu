@@ -19,20 +19,33 @@
 // own rounding.  A row factor on the state's part alone would cost a second accumulator or
 // a round trip of O; a rounded Q~ a second rounding.
 //
-// The state is held in fp32 registers.  W = w lam^{..} v is split exactly into three bf16
-// parts (8 + 8 + 8 bits of the fp32 product), so that KV has fp32 accuracy: two parts leave
-// 2^-18, which shows in the fp32 states.  KV is formed alone for each chunk and added in the
-// registers with one rounding: accumulating in tensor memory over a long sequence would add
-// up the tensor core's truncations.  lam^L is kept to 48 bits, for the same reason.
+// The state is held in fp32 registers, and W = w lam^{..} v has fp32 accuracy: the weight is
+// split into bf16 numbers w1 + w2 + w3 (8 bits each), and
+//   w v = h + l + p + r,   h = bf16(w1 v),  l = w1 v - h,  p = bf16(w2 v),
+//                          r = bf16(w3 v + (w2 v - p)),
+// where l and w2 v - p are exact in bf16 (a 16-bit product less its upper half).  Each part is
+// one or two packed bf16 instructions for two tokens, and KV is four products.  (Two parts
+// leave 2^-17, which shows in the fp32 states.)  KV is formed alone for each chunk and added
+// in the registers with one rounding: accumulating in tensor memory over a long sequence would
+// add up the tensor core's truncations.  lam^L is kept to 48 bits, for the same reason.
 //
-// Since the products of a chunk never wait for the state (only the S rows of O do), the
-// CTA's warps run as a pipeline over chunks: 8 warps turn P into P~ and build Q~, 8 warps
-// build W, 8 warps hold the state, publish its bf16 copy and write O, and one thread each
-// issues the loads and the three products.
+// No product waits for another chunk's epilogue but through the buffers it needs, so the warps
+// run as a pipeline over chunks: 8 warps turn P into P~ and build Q~, 8 build W, 8 hold the
+// state, publish its bf16 copy and write O, and four issue the loads, the stores and the three
+// products.  Tensor memory holds two P buffers, O and W; KV takes the P buffer that the chunk
+// before has finished with.
+//
+// What bounds it (4 x 4096 tokens, 16 / 32 heads: 107 us, 3.9 TB/s or 0.57 of the measured copy
+// rate): shared memory.  A chunk takes 5600 cycles; the tensor pipe works for 3584 of them (QK 8
+// products of 64 cycles, O 16, KV 32), and the SM's data path, which the products' operands
+// (256 KB a chunk), the tiles' arrival and the warps' own accesses share, is busy for about
+// 4/5.  What was tried and changed nothing, for that reason: three parts for W (by truncation
+// or by error-free sums), finer W buffers, W computed ahead of its buffer, arrivals once a warp.
 #include <cuda_fp16.h>
 #include <stddef.h>
 #include <string.h>
 
+#include <initializer_list>
 
 #include "gdn_epi.cuh"
 #include "gdn_linear.h"
@@ -51,8 +64,9 @@ constexpr int kGroupP = 8, kGroupW = 8, kGroupS = 8;  // warps of the three grou
 constexpr int kWarpLoad = kGroupP + kGroupW + kGroupS;
 constexpr int kThreads = (kWarpLoad + 4) * 32;
 
-// Registers a thread: the state's warps hold 64 floats each.  The groups' shares must not
-// exceed what the launch gives (kThreads * kRegsLaunch), or the increase would never end.
+// Registers a thread: the state's warps hold 64 floats each, P's a row of Q~.  The groups' shares
+// must not exceed what the launch gives (kThreads * kRegsLaunch, checked there too), or the
+// increase would never end.
 constexpr int kRegsLaunch = 72, kRegsP = 80, kRegsW = 48, kRegsState = 104, kRegsIssue = 40;
 static_assert(kGroupP * kRegsP + kGroupW * kRegsW + kGroupS * kRegsState + 4 * kRegsIssue <=
                       (kWarpLoad + 4) * kRegsLaunch &&
@@ -63,7 +77,7 @@ static_assert(kGroupP * kRegsP + kGroupW * kRegsW + kGroupS * kRegsState + 4 * k
 constexpr uint32_t kColP = 0;      // two buffers of 128: P fp32; then, per half h of 64: P~ of tokens
                                    // 64 h .. in 32 columns and Q~ of features 64 h .. in the next 32
 constexpr uint32_t kColX = 256;    // O
-constexpr uint32_t kColW = 384;    // two buffers of 48: 32 tokens of W, three parts of 16 (the state
+constexpr uint32_t kColW = 384;    // two buffers of 64: 32 tokens of W, four parts of 16 (the state
                                    // pass has two more in the second P buffer)
 constexpr uint32_t kCols = 512;
 
@@ -73,7 +87,8 @@ struct LinSmem {
     bf16 wtab[2][3][kC];  // weights of a whole and of the partial chunk's tokens, three parts each
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full_v[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2], o_done[2], o_staged[2];
+    uint64_t full_v[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2],
+        o_done[2], o_staged[2];
     uint64_t kv_free[2], s_ready, o_free, factors, drain[3];
     // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
     uint64_t peer_ok[2], rx_full[2], sent[2];
@@ -124,25 +139,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
     return x;
 }
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-    uint64_t x;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
-    return x;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t x;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
     return x;
 }
-// The upper 16 bits of both halves: a bf16 pair by truncation (the even token in the low half).
-__device__ __forceinline__ uint32_t tops(float2 x) {
-    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-}
-__device__ __forceinline__ uint64_t keep_tops(float2 x) {
-    return pair(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
-                __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 t = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&t);
@@ -1030,6 +1031,12 @@ cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s) {
     const void *kernels[] = {(const void *)k_linear_tc<0>, (const void *)k_linear_tc<1>, (const void *)k_linear_tc<2>,
                              (const void *)k_linear_tc<3>};
     const int smem = (int)sizeof(LinSmem) + 1024;
+    for (int k : {set, a.seg_chunks > 0 ? 1 : set}) {   // the groups' register shares rely on it
+        cudaFuncAttributes fa;
+        const cudaError_t err = cudaFuncGetAttributes(&fa, kernels[k]);
+        if (err != cudaSuccess) return err;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    }
     cudaError_t e = cudaFuncSetAttribute(kernels[set], cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess && a.seg_chunks > 0)
         e = cudaFuncSetAttribute(kernels[1], cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -260,6 +260,24 @@ def test_step_continues_a_prefill():
     ref.check("state", pool[1:].transpose(2, 3), rh, ref.state_bound(mh))
 
 
+def test_many_steps_of_a_slow_decay():
+    # lam in fp32 would be off by up to 2^-25 each step, 2^-15 after 1024
+    n, g = 1024, -3e-4
+    rng = np.random.default_rng(3)
+    q, k, v = (_bf(rng.standard_normal((n, 1, 128))) for _ in range(3))
+    gd = torch.full((1,), g, device="cuda")
+    pool = torch.randn(2, 1, 128, 128, device="cuda")
+    s0 = _f64(pool[1, 0])
+    idx = torch.ones(1, dtype=torch.int32, device="cuda")
+    for t in range(n):
+        gdn.linear_attn_step(q[t:t + 1], k[t:t + 1], v[t:t + 1], gd, pool, idx)
+    w = np.exp(np.float64(np.float32(g)) * np.arange(n, -1, -1))
+    kk, vv = _f64(k)[:, 0], _f64(v)[:, 0]
+    want = (vv * w[1:, None]).T @ kk + w[0] * s0
+    mag = (np.abs(vv) * w[1:, None]).T @ np.abs(kk) + w[0] * np.abs(s0)
+    ref.check("slot", pool[1, 0], want, ref.state_bound(mag))
+
+
 def test_autograd():
     c = Case([100, 61], 2, 4)
     q, k, v = (x.clone().requires_grad_() for x in (c.q, c.k, c.v))
@@ -272,6 +290,18 @@ def test_autograd():
         assert torch.equal(t.grad, gr[n])
     with pytest.raises(ValueError):
         gdn.linear_attention(q, k, v, c.g.clone().requires_grad_())
+
+
+def test_bounds_checked_build():
+    from chunked_gated_delta_06_gb300 import binding, build
+    c = Case([130, 1, 300], 2, 4)
+    want, gr = c.fwd(), c.bwd()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with binding.use_library(build.build(checked=True)):
+        o, ht = c.fwd(device_status=status)
+        ck = c.bwd(device_status=status)
+    assert int(status) == 0 and torch.equal(o, want[0]) and torch.equal(ht, want[1])
+    assert all(torch.equal(ck[n], gr[n]) for n in gr)
 
 
 def test_device_offsets_that_disagree_are_flagged():

@@ -1,5 +1,7 @@
 // gdn_linear.cu -- linear attention with a decay for each head: the sum over the value heads
 // of a key head, and the single-token step (the scans are in gdn_linear_tc.cu).
+#include <type_traits>
+
 #include "gdn_linear.h"
 
 namespace gdn {
@@ -66,17 +68,21 @@ __global__ void __launch_bounds__(kStepWarps * 32)
     const float lam = slow ? expm1f(g) : expf(g);
     const bf16 *vrow = v + ((size_t)b * HV + hv) * kDim + r0;
     float mine = 0.f;
+    auto rows = [&](auto near_one) {
 #pragma unroll
-    for (int j = 0; j < kStepRows; ++j) {
-        const float vj = bf2f(vrow[j]);
-        s[j].x = fmaf(lam, s[j].x, fmaf(vj, kv[0], slow ? s[j].x : 0.f));
-        s[j].y = fmaf(lam, s[j].y, fmaf(vj, kv[1], slow ? s[j].y : 0.f));
-        s[j].z = fmaf(lam, s[j].z, fmaf(vj, kv[2], slow ? s[j].z : 0.f));
-        s[j].w = fmaf(lam, s[j].w, fmaf(vj, kv[3], slow ? s[j].w : 0.f));
-        __stcs(reinterpret_cast<float4 *>(S + (size_t)(r0 + j) * kDim + lane * 4), s[j]);
-        const float dot = warp_sum(s[j].x * qv[0] + s[j].y * qv[1] + s[j].z * qv[2] + s[j].w * qv[3]);
-        if (lane == j) mine = dot;
-    }
+        for (int j = 0; j < kStepRows; ++j) {
+            const float vj = bf2f(vrow[j]);
+            s[j].x = fmaf(lam, s[j].x, near_one ? fmaf(vj, kv[0], s[j].x) : vj * kv[0]);
+            s[j].y = fmaf(lam, s[j].y, near_one ? fmaf(vj, kv[1], s[j].y) : vj * kv[1]);
+            s[j].z = fmaf(lam, s[j].z, near_one ? fmaf(vj, kv[2], s[j].z) : vj * kv[2]);
+            s[j].w = fmaf(lam, s[j].w, near_one ? fmaf(vj, kv[3], s[j].w) : vj * kv[3]);
+            __stcs(reinterpret_cast<float4 *>(S + (size_t)(r0 + j) * kDim + lane * 4), s[j]);
+            const float dot = warp_sum(s[j].x * qv[0] + s[j].y * qv[1] + s[j].z * qv[2] + s[j].w * qv[3]);
+            if (lane == j) mine = dot;
+        }
+    };
+    if (slow) rows(std::true_type());
+    else rows(std::false_type());
     if (lane < kStepRows) orow[r0 + lane] = f2bf(mine);
 }
 

@@ -866,6 +866,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             // ------------------------------------------------------ O = [P~ | Q~] [V ; S]
             const uint32_t idv = idesc_bf16(128, 128, 0, 1), ids = idesc_bf16(128, 128, 0, 0);
             const uint64_t vd0 = sdesc(smem_u32(sm.v), kHalf, 1024), sd0 = sdesc(smem_u32(sm.s), 16, 1024);
+            int armed = 0;   // chunks whose half of O from the peer may be on its way
             for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait_warp(sm, &sm.s_ready, c & 1) ||
@@ -878,6 +879,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     mbar_arrive_expect_tx(&sm.rx_full[s], kHalf + kC * 8);
                     remote_arrive(&sm.peer_ok[s], (hv & 1) ^ 1);
                 }
+                armed = c + 1;
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
 #pragma unroll
@@ -890,6 +892,9 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 }
                 __syncwarp();
             }
+            if (kPair && *(volatile int *)&sm.dead)   // the peer's copies write this CTA's tiles (bounded)
+                for (int c = max(0, armed - 2); c < armed; ++c)
+                    mbar_wait(&sm.rx_full[c & 1], (c >> 1) & 1, kDrainLimitNs);
         } else {
             // ------------------------------------------------------ KV = W^T K
             const uint32_t id = idesc_bf16(128, 128, 0, 1);

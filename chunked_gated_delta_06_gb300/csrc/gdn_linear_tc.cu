@@ -35,12 +35,20 @@
 // products.  Tensor memory holds two P buffers, O and W; KV takes the P buffer that the chunk
 // before has finished with.
 //
-// What bounds it (4 x 4096 tokens, 16 / 32 heads: 107 us, 3.9 TB/s or 0.57 of the measured copy
-// rate): shared memory.  A chunk takes 5600 cycles; the tensor pipe works for 3584 of them (QK 8
-// products of 64 cycles, O 16, KV 32), and the SM's data path, which the products' operands
-// (256 KB a chunk), the tiles' arrival and the warps' own accesses share, is busy for about
-// 4/5.  What was tried and changed nothing, for that reason: three parts for W (by truncation
-// or by error-free sums), finer W buffers, W computed ahead of its buffer, arrivals once a warp.
+// Shared memory: K and V have two stages; Q has one tile, free again once Q~ is in tensor memory
+// (P was formed before), and the output a tile of its own, so that no tile waits for an output to
+// leave.  (Q in two stages, its tile taking the output: 109 instead of 105 us for the forward
+// below, 396 instead of 352 us for the backward of 4 x 4096 tokens.)
+//
+// What bounds it (4 x 4096 tokens, 16 / 32 heads: 105 us, 3.8 TB/s or 0.56 of the measured copy
+// rate): the steps of a chunk that wait on each other.  A chunk takes 5300 cycles, of which the
+// tensor pipe works for 3584 (QK 8 products of 64 cycles, O 16, KV 32).  Over two chunks O(c - 1)
+// frees the buffer for KV(c), whose end frees it for P(c + 1), from which P~ and then O(c + 1)
+// follow; each hand-over crosses tensor memory, and every step shares the SM's one data path with
+// the products' operands (256 KB a chunk) and the tiles' arrival.  Without effect: two or three
+// parts for W (by truncation or by error-free sums), also with all of a chunk's W ahead of KV;
+// finer W buffers; arrivals once a warp; P's factors in registers.  Slower: rows of O written
+// straight from registers (126 us), Q's tile freed before P is formed (113 us).
 #include <cuda_fp16.h>
 #include <stddef.h>
 #include <string.h>
@@ -82,16 +90,20 @@ constexpr uint32_t kColW = 384;    // two buffers of 64: 32 tokens of W, four pa
 constexpr uint32_t kCols = 512;
 
 struct LinSmem {
-    unsigned char q[2][kTile], k[2][kTile], v[2][kTile];  // TMA tiles, two stages
+    unsigned char k[2][kTile], v[2][kTile];               // TMA tiles, two stages
+    unsigned char q[kTile];                               // free again once P is formed and Q~ read
+    unsigned char x[kTile];                               // the output on its way (pair mode: half of it to
+                                                          // the peer in plane 0, the rest in plane 1)
     unsigned char s[kTile];                               // bf16 copy of S, row r K-major
-    bf16 wtab[2][3][kC];  // weights of a whole and of the partial chunk's tokens, three parts each
+    bf16 wtab[3][kC];     // weights of a whole chunk's tokens, three parts
+    unsigned char to_peer[kC][2], from_peer[kC][2];  // pair mode: exponents of the exchanged halves' rows
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
-    uint64_t full_v[2], full_q[2], p_done[2], pt_ready[2], v_ok[2], w_ready[4], w_free[4], kv_done[2],
-        o_done[2], o_staged[2];
-    uint64_t kv_free[2], s_ready, o_free, factors, drain[3];
-    // pair mode: the peer's Q tile is free; the peer's half of O is here; this CTA's has arrived
-    uint64_t peer_ok[2], rx_full[2], sent[2];
+    uint64_t full_vk[2], v_ok[2], p_done[2], pt_ready[2], w_ready[4], w_free[4], kv_done[2], kv_free[2], o_done[2];
+    uint64_t full_q, s_ready, o_free, o_staged, x_free, factors, drain[3];
+    // pair mode: the peer's half of the exchange tile is free; the peer's half of O is here; this
+    // CTA's half has arrived
+    uint64_t peer_ok, rx_full, sent;
     uint32_t tmem_base;
     int dead;
 };
@@ -352,64 +364,59 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
     }
 
     const int hq = hv / (a.HV / ps.nq), hk = hv / (a.HV / ps.nk), hw = hv / (a.HV / ps.nv);
-    // A stage's tiles come in two batches, by when their places are free: V and K after the
-    // products of the chunk that held them, Q (in pair mode K too) after its output has left.
-    auto load_k = [&](int c, uint64_t *bar) {
-        for (int h = 0; h < 2; ++h)
-            tma_load_3d(sm.k[c & 1] + h * kHalf, &maps.k, 64 * h, hk, wk.start(c, kReverse), bar);
+    auto load = [&](const CUtensorMap *map, unsigned char *to, int head, int t, uint64_t *bar) {
+        for (int h = 0; h < 2; ++h) tma_load_3d(to + h * kHalf, map, 64 * h, head, t, bar);
     };
-    auto load_first = [&](int c) {
+    auto load_vk = [&](int c) {
         const int s = c & 1, t = wk.start(c, kReverse);
-        mbar_arrive_expect_tx(&sm.full_v[s], kPair ? kTile : 2 * kTile);
-        for (int h = 0; h < 2; ++h) tma_load_3d(sm.v[s] + h * kHalf, &maps.v, 64 * h, hw, t, &sm.full_v[s]);
-        if (!kPair) load_k(c, &sm.full_v[s]);
+        mbar_arrive_expect_tx(&sm.full_vk[s], 2 * kTile);
+        load(&maps.v, sm.v[s], hw, t, &sm.full_vk[s]);
+        load(&maps.k, sm.k[s], hk, t, &sm.full_vk[s]);
         // the tiles after next start towards L2 while both stages are taken
-        if (c + 2 < wk.n) {
-            const int t2 = wk.start(c + 2, kReverse);
-            for (int h = 0; h < 2; ++h) {
-                tma_prefetch_3d(&maps.v, 64 * h, hw, t2);
-                tma_prefetch_3d(&maps.k, 64 * h, hk, t2);
-                if (!kState) tma_prefetch_3d(&maps.q, 64 * h, hq, t2);
+        for (int h = 0; h < 2; ++h) {
+            if (c + 2 < wk.n) {
+                tma_prefetch_3d(&maps.v, 64 * h, hw, wk.start(c + 2, kReverse));
+                tma_prefetch_3d(&maps.k, 64 * h, hk, wk.start(c + 2, kReverse));
             }
+            if (!kState && c + 1 < wk.n) tma_prefetch_3d(&maps.q, 64 * h, hq, wk.start(c + 1, kReverse));
         }
     };
-    auto load_second = [&](int c) {
-        const int s = c & 1, t = wk.start(c, kReverse);
-        mbar_arrive_expect_tx(&sm.full_q[s], kPair ? 2 * kTile : kTile);
-        for (int h = 0; h < 2; ++h) tma_load_3d(sm.q[s] + h * kHalf, &maps.q, 64 * h, hq, t, &sm.full_q[s]);
-        if (kPair) load_k(c, &sm.full_q[s]);
+    auto load_q = [&](int c) {
+        mbar_arrive_expect_tx(&sm.full_q, kTile);
+        load(&maps.q, sm.q, hq, wk.start(c, kReverse), &sm.full_q);
     };
     if (warp == kWarpLoad) {
         if (elect_one()) {
             if (wk.n > 0) tma_prefetch_maps(maps);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&sm.full_v[i], 1);
-                mbar_init(&sm.full_q[i], 1);
+                mbar_init(&sm.full_vk[i], 1);
+                mbar_init(&sm.v_ok[i], kGroupW * 32);
                 mbar_init(&sm.p_done[i], 1);
                 mbar_init(&sm.pt_ready[i], kGroupP * 32);
-                mbar_init(&sm.v_ok[i], kGroupW * 32);
                 mbar_init(&sm.kv_done[i], 1);
-                mbar_init(&sm.o_done[i], 1);
-                mbar_init(&sm.o_staged[i], kGroupS * 32);
-                mbar_init(&sm.peer_ok[i], 1);
-                mbar_init(&sm.rx_full[i], 1);
-                mbar_init(&sm.sent[i], 1);
                 mbar_init(&sm.kv_free[i], kGroupS * 32);
+                mbar_init(&sm.o_done[i], 1);
             }
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&sm.w_ready[i], kGroupW * 16);
                 mbar_init(&sm.w_free[i], 1);
             }
+            mbar_init(&sm.full_q, 1);
             mbar_init(&sm.s_ready, kGroupS * 32);
             mbar_init(&sm.o_free, kGroupS * 32);
+            mbar_init(&sm.o_staged, kGroupS * 32);
+            mbar_init(&sm.x_free, 1);
             mbar_init(&sm.factors, 1);
+            mbar_init(&sm.peer_ok, 1);
+            mbar_init(&sm.rx_full, 1);
+            mbar_init(&sm.sent, 1);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
             fence_proxy_async_smem();
-            for (int c = 0; c < min(2, wk.n); ++c) {   // both stages, before anything else is set up
-                load_first(c);
-                if (!kState) load_second(c);
+            for (int c = 0; c < min(2, wk.n); ++c) {   // before anything else is set up
+                load_vk(c);
+                if (!kState && c == 0) load_q(c);
             }
         }
         __syncwarp();
@@ -417,12 +424,11 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         tmem_alloc(&sm.tmem_base, kCols);
         tmem_relinquish();
     }
-    if (tid < 2 * kC) {
-        const int part = tid >> 7, t = tid & (kC - 1), L = part ? wk.len % kC : kC;
-        float w = t < L ? ps.w * exp2f(g2 * (float)(kReverse ? t + 1 : L - 1 - t)) : 0.f;
+    if (tid < kC) {
+        float w = ps.w * exp2f(g2 * (float)(kReverse ? tid + 1 : kC - 1 - tid));
         for (int x = 0; x < 3; ++x) {
             const bf16 y = f2bf(w);
-            sm.wtab[part][x][t] = y;
+            sm.wtab[x][tid] = y;
             w -= bf2f(y);
         }
         if (tid < 32) sm.ptab[tid] = exp2f(g2 * (float)(kReverse ? tid : 31 - tid));
@@ -446,8 +452,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             float e, f;
             read_power<kReverse>(g2, i, L, e, f);
             // Q~ first, while P is formed; it waits in registers for its columns
-            if (!wait_warp(sm, &sm.full_q[c & 1], (c >> 1) & 1)) break;
-            const unsigned char *qt = sm.q[c & 1] + half * kHalf;
+            if (!wait_warp(sm, &sm.full_q, c & 1)) break;
+            const unsigned char *qt = sm.q + half * kHalf;
             const __nv_bfloat162 pw = __float2bfloat162_rn(
                 e < -120.f ? 0.f : __int_as_float(((int)e + 127) << 23));
             float q[32];
@@ -528,9 +534,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         bool ok = true;
         for (int c = 0; c < wk.n && ok; ++c) {
             const int s = c & 1, L = wk.length(c, kReverse);
-            if (!(ok = wait_warp(sm, &sm.full_v[s], (c >> 1) & 1))) break;
+            if (!(ok = wait_warp(sm, &sm.full_vk[s], (c >> 1) & 1))) break;
             if (L < kC) {
-                if (kPair && !(ok = wait_warp(sm, &sm.full_q[s], (c >> 1) & 1))) break;
                 // rows past the sequence hold the next one's tokens: zeros instead (each half
                 // clears its own quarters of K, which the product of a quarter waits for)
                 for (int x = quad * 32 + lane; x < (kState ? 1 : 2) * 32 * 16; x += kGroupW * 16) {
@@ -543,7 +548,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 fence_proxy_async_smem();
             }
             if (!kState) mbar_arrive(&sm.v_ok[s]);
-            const bf16 *wt = sm.wtab[L < kC][0] + 32 * half + 2 * (lane & 3);
+            // a forward scan's partial chunk ends with the same weights as a whole one
+            const int first = 32 * half + 2 * (lane & 3), shift = kReverse ? 0 : kC - L;
             const uint32_t vt = vrow + s * kTile;
 #pragma unroll 1
             for (int pass = 0; pass < (kState ? 1 : 2); ++pass) {
@@ -557,7 +563,13 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int x = 0; x < 3; ++x)
-                            w[k][x] = *reinterpret_cast<const __nv_bfloat162 *>(wt + x * kC + 64 * pass + 16 * k16 + 8 * k);
+                        {
+                            const int t = first + 64 * pass + 16 * k16 + 8 * k + shift;   // (past the sequence: any)
+                            if (shift & 1)
+                                w[k][x] = __nv_bfloat162(sm.wtab[x][min(t, kC - 1)], sm.wtab[x][min(t + 1, kC - 1)]);
+                            else
+                                w[k][x] = *reinterpret_cast<const __nv_bfloat162 *>(&sm.wtab[x][min(t, kC - 2)]);
+                        }
                     uint32_t in[2][4];
                     ldmatrix4t(vt + (64 * pass + 16 * k16) * 128 + chunk[0], in[0]);
                     ldmatrix4t(vt + (64 * pass + 16 * k16) * 128 + chunk[1], in[1]);
@@ -577,7 +589,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                         for (int x = 0; x < 4; ++x) {   // 8 tokens x & 1, features 8 (x >> 1) ..
                             const __nv_bfloat162 *wx = w[x & 1];
                             const __nv_bfloat162 v2 = *reinterpret_cast<const __nv_bfloat162 *>(&in[g16][x]);
-                            const __nv_bfloat162 h = __hmul2(wx[0], v2), l = __hfma2(wx[0], v2, __hneg2(h));
+                            const __nv_bfloat162 h = __hmul2(wx[0], v2);
+                            const __nv_bfloat162 l = __hfma2(wx[0], v2, __hneg2(h));
                             const __nv_bfloat162 p = __hmul2(wx[1], v2);
                             const __nv_bfloat162 r = __hfma2(wx[2], v2, __hfma2(wx[1], v2, __hneg2(p)));
                             const int at = 2 * (x & 1) + (x >> 1);
@@ -716,14 +729,13 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             const size_t out = (((size_t)wk.start(c, kReverse) + r) * ps.no + (kPair ? hv >> 1 : hv)) * kDim + first;
             const bool staged = L == kC && !ps.part;   // whole chunks of bf16 leave by TMA
             const bool mine = r < L && in_range(out, kPair ? 32 : 64, (long long)a.T * ps.no * kDim, a.status);
-            // the stage's Q tile is free: its readers finished before O did
-            unsigned char *orow = sm.q[s] + (kPair ? 0 : (col >> 6) * kHalf) + r * 128;
+            unsigned char *orow = sm.x + (kPair ? kHalf : (col >> 6) * kHalf) + r * 128;
             if (kPair) {
                 // Each CTA writes 64 columns of the pair's sum; the other 64 go to the peer as fp16
                 // times a power of two for each 32 of a row (2^-12 of the largest at most, where the
-                // output is rounded at 2^-9): from the stage's K tile, whose products are done, to
-                // the peer's Q tile, rows in plane 0 and their factors in plane 1.
+                // output is rounded at 2^-9).
                 if ((col >> 6) != (hv & 1)) {
+                    if (c > 0 && !wait_warp_cluster(sm, &sm.sent, (c - 1) & 1)) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float x[32];
@@ -732,35 +744,35 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                         float big = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(x[j]));
-                        // 2^e <= big < 2^{e+1}, within the normal numbers (infinities stay infinite)
-                        const uint32_t e = min(max(__float_as_uint(big) & 0x7f800000u, 1u << 23), 253u << 23);
-                        scale32(x, __uint_as_float((254u << 23) - e));
-                        reinterpret_cast<float *>(sm.k[s] + kHalf)[2 * r + h] = scale * __uint_as_float(e);
+                        // 2^e <= scale * big < 2^{e+1}, within the normal numbers (infinities stay infinite)
+                        const uint32_t e = min(max((__float_as_uint(scale * big) >> 23) & 0xff, 1u), 253u);
+                        scale32(x, scale * __uint_as_float((254u - e) << 23));
+                        sm.to_peer[r][h] = (unsigned char)e;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4 *>(sm.k[s] + r * 128 + (((4 * h + j) ^ (r & 7)) << 4)) = make_uint4(
+                            *reinterpret_cast<uint4 *>(sm.x + r * 128 + (((4 * h + j) ^ (r & 7)) << 4)) = make_uint4(
                                 pack_half2(x[8 * j], x[8 * j + 1]), pack_half2(x[8 * j + 2], x[8 * j + 3]),
                                 pack_half2(x[8 * j + 4], x[8 * j + 5]), pack_half2(x[8 * j + 6], x[8 * j + 7]));
                     }
                     fence_proxy_async_smem();
-                    if (!wait_warp_cluster(sm, &sm.peer_ok[s], (c >> 1) & 1)) break;
+                    if (!wait_warp_cluster(sm, &sm.peer_ok, c & 1)) break;
                     if (lane == 0) {   // this warp's 32 rows
                         const uint32_t peer = (hv & 1) ^ 1;
-                        remote_copy(sm.q[s] + r * 128, sm.k[s] + r * 128, 32 * 128, &sm.rx_full[s], peer);
-                        remote_copy(sm.q[s] + kHalf + r * 8, sm.k[s] + kHalf + r * 8, 32 * 8, &sm.rx_full[s], peer);
+                        remote_copy(sm.x + kHalf + r * 128, sm.x + r * 128, 32 * 128, &sm.rx_full, peer);
+                        remote_copy(sm.from_peer[r], sm.to_peer[r], 32 * 2, &sm.rx_full, peer);
                     }
                     __syncwarp();
                 }
                 if (c + 1 < wk.n) publish();   // while the peer's half comes
-                if (!wait_warp_cluster(sm, &sm.rx_full[s], (c >> 1) & 1)) break;
-                if (warp == kGroupP + kGroupW && lane == 0) remote_arrive(&sm.sent[s], (hv & 1) ^ 1);
+                if (!wait_warp_cluster(sm, &sm.rx_full, c & 1)) break;
+                if (warp == kGroupP + kGroupW && lane == 0) remote_arrive(&sm.sent, (hv & 1) ^ 1);
                 const int h = col >> 6;
                 float x[32];
                 tmem_ld32(tb + lanes + kColX + first, x);
                 tmem_ld_wait();
                 tc_fence_before();
                 mbar_arrive(&sm.o_free);
-                const float theirs = reinterpret_cast<const float *>(sm.q[s] + kHalf)[2 * r + h];
+                const float theirs = __uint_as_float((uint32_t)sm.from_peer[r][h] << 23);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {   // (two terms: the same sum whichever CTA adds)
                     const uint4 y = *reinterpret_cast<const uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4));
@@ -774,6 +786,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 }
                 write32(ps, x, out, mine, staged, orow, r, h);   // (over the 16 bytes it has read)
             } else {
+                if (c > 0 && !wait_warp(sm, &sm.x_free, (c - 1) & 1)) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[32];
@@ -788,7 +801,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&sm.o_staged[s]);
+            mbar_arrive(&sm.o_staged);
             if (!kPair && c + 1 < wk.n) publish();
         }
         if (wk.n == 0) store_state();
@@ -801,59 +814,60 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         const int role = __shfl_sync(0xffffffffu, warp, 0) - kWarpLoad;
         if (role == 0) {
             // ------------------------------------------------------ loads
-            int issued_v = min(2, wk.n), issued_q = kState ? 0 : issued_v;
-            // The output of chunk c leaves its stage's Q tile (a partial chunk's has been written).
-            auto store = [&](int c) {
-                const int s = c & 1;
-                if (!wait_warp(sm, &sm.o_staged[s], (c >> 1) & 1)) return false;
-                if (wk.length(c, kReverse) == kC && !ps.part && elect_one()) {
-                    for (int h = 0; h < (kPair ? 1 : 2); ++h)
-                        tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv,
-                                     wk.start(c, kReverse), sm.q[s] + h * kHalf);
-                    tma_store_commit();
-                    tma_store_wait_read();
+            // pair mode: the exchange tile's second plane may take the peer's half of chunk c's output
+            auto arm = [&](int c) {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sm.rx_full, kHalf + kC * 2);
+                    remote_arrive(&sm.peer_ok, (hv & 1) ^ 1);
                 }
                 __syncwarp();
-                return true;
             };
-            bool ok = true;
-            for (int c = 2; c < wk.n && ok; ++c) {
-                const int s = c & 1, mark = ((c >> 1) - 1) & 1;
-                ok = false;
-                if ((!kState && !wait_warp(sm, &sm.o_done[s], mark)) || !wait_warp(sm, &sm.kv_done[s], mark)) break;
-                if (elect_one()) load_first(c);
-                __syncwarp();
-                issued_v = c + 1;
-                ok = true;
+            int issued = min(2, wk.n), armed = min(1, wk.n);
+            if (kPair && armed) arm(0);
+            for (int c = 0; c < wk.n; ++c) {
+                const int s = c & 1, mark = (c >> 1) & 1;
+                if (c + 2 < wk.n) {
+                    if ((!kState && !wait_warp(sm, &sm.o_done[s], mark)) || !wait_warp(sm, &sm.kv_done[s], mark)) break;
+                    if (elect_one()) load_vk(c + 2);
+                    __syncwarp();
+                    issued = c + 3;
+                }
                 if (kState) continue;
-                ok = false;
-                // the last output of this stage leaves its Q tile (and the exchange its K tile)
-                if (!store(c - 2)) break;
-                if (kPair && !wait_warp_cluster(sm, &sm.sent[s], mark)) break;
-                if (elect_one()) load_second(c);
+                if (!wait_warp(sm, &sm.o_staged, c & 1)) break;
+                if (elect_one()) {   // (a partial chunk's output has been written)
+                    if (wk.length(c, kReverse) == kC && !ps.part) {
+                        for (int h = kPair ? 1 : 0; h < 2; ++h)
+                            tma_store_3d(&maps.o, kPair ? 64 * (hv & 1) : 64 * h, kPair ? hv >> 1 : hv,
+                                         wk.start(c, kReverse), sm.x + h * kHalf);
+                        tma_store_commit();
+                        tma_store_wait_read();
+                    }
+                    mbar_arrive(&sm.x_free);
+                }
                 __syncwarp();
-                issued_q = c + 1;
-                ok = true;
+                if (kPair && c + 1 < wk.n) {
+                    arm(c + 1);
+                    armed = c + 2;
+                }
             }
-            for (int c = max(0, wk.n - 2); !kState && ok && c < wk.n; ++c) ok = store(c);
             if (elect_one()) tma_store_wait_all();
             __syncwarp();
             // copies still in flight write this CTA's shared memory: wait for them (bounded)
-            for (int c = max(0, issued_v - 2); c < issued_v; ++c)
-                mbar_wait(&sm.full_v[c & 1], (c >> 1) & 1, kDrainLimitNs);
-            for (int c = max(0, issued_q - 2); c < issued_q; ++c)
-                mbar_wait(&sm.full_q[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            for (int c = max(0, issued - 2); c < issued; ++c)
+                mbar_wait(&sm.full_vk[c & 1], (c >> 1) & 1, kDrainLimitNs);
+            if (kPair && armed) mbar_wait(&sm.rx_full, (armed - 1) & 1, kDrainLimitNs);
         } else if (role == 1) {
             // ------------------------------------------------------ P = Q K^T
             const uint32_t id = idesc_bf16(128, 128, 0, 0);
-            const uint64_t qd0 = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
+            const uint64_t qd = sdesc(smem_u32(sm.q), 16, 1024), kd0 = sdesc(smem_u32(sm.k), 16, 1024);
+            int issued = kState ? 0 : min(1, wk.n);
             for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
-                if (!wait_warp(sm, &sm.full_v[s], (c >> 1) & 1) || !wait_warp(sm, &sm.full_q[s], (c >> 1) & 1)) break;
-                // (loading this stage waited for O of chunk c - 2, which read this P buffer)
+                if (!wait_warp(sm, &sm.full_vk[s], (c >> 1) & 1) || !wait_warp(sm, &sm.full_q, c & 1)) break;
+                // (KV of chunk c - 1 took this P buffer after O of chunk c - 2)
                 if (c > 0 && !wait_warp(sm, &sm.kv_free[s ^ 1], ((c - 1) >> 1) & 1)) break;
                 tc_fence_after();
-                const uint64_t qd = qd0 + ((s * kTile) >> 4), kd = kd0 + ((s * kTile) >> 4);
+                const uint64_t kd = kd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
@@ -861,12 +875,20 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     mma_commit(&sm.p_done[s]);
                 }
                 __syncwarp();
+                // The next Q, once this one is in P and Q~.  (P's warps arrive after Q~ is stored, which
+                // took the tile's data: an arrival right after the reads was seen to come before them.)
+                if (c + 1 < wk.n) {
+                    if (!wait_warp(sm, &sm.pt_ready[s], (c >> 1) & 1)) break;
+                    if (elect_one()) load_q(c + 1);
+                    __syncwarp();
+                    issued = c + 2;
+                }
             }
+            if (issued > 0) mbar_wait(&sm.full_q, (issued - 1) & 1, kDrainLimitNs);
         } else if (role == 2) {
             // ------------------------------------------------------ O = [P~ | Q~] [V ; S]
             const uint32_t idv = idesc_bf16(128, 128, 0, 1), ids = idesc_bf16(128, 128, 0, 0);
             const uint64_t vd0 = sdesc(smem_u32(sm.v), kHalf, 1024), sd0 = sdesc(smem_u32(sm.s), 16, 1024);
-            int armed = 0;   // chunks whose half of O from the peer may be on its way
             for (int c = 0; !kState && c < wk.n; ++c) {
                 const int s = c & 1;
                 if (!wait_warp(sm, &sm.v_ok[s], (c >> 1) & 1) || !wait_warp(sm, &sm.s_ready, c & 1) ||
@@ -874,12 +896,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     (c > 0 && !wait_warp(sm, &sm.o_free, (c - 1) & 1)))
                     break;
                 tc_fence_after();
-                // this CTA's Q tile has been read: the peer may put its half of O there
-                if (kPair && elect_one()) {
-                    mbar_arrive_expect_tx(&sm.rx_full[s], kHalf + kC * 8);
-                    remote_arrive(&sm.peer_ok[s], (hv & 1) ^ 1);
-                }
-                armed = c + 1;
                 const uint64_t vd = vd0 + ((s * kTile) >> 4);
                 if (elect_one()) {
 #pragma unroll
@@ -892,9 +908,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 }
                 __syncwarp();
             }
-            if (kPair && *(volatile int *)&sm.dead)   // the peer's copies write this CTA's tiles (bounded)
-                for (int c = max(0, armed - 2); c < armed; ++c)
-                    mbar_wait(&sm.rx_full[c & 1], (c >> 1) & 1, kDrainLimitNs);
         } else {
             // ------------------------------------------------------ KV = W^T K
             const uint32_t id = idesc_bf16(128, 128, 0, 1);
@@ -914,7 +927,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 if (kState ? c > 1 && !wait_warp(sm, &sm.kv_free[s], ((c >> 1) - 1) & 1)
                            : c > 0 && !wait_warp(sm, &sm.o_done[s ^ 1], ((c - 1) >> 1) & 1))
                     break;
-                if (!wait_warp(sm, kPair ? &sm.full_q[s] : &sm.full_v[s], (c >> 1) & 1)) break;
+                if (!wait_warp(sm, &sm.full_vk[s], (c >> 1) & 1)) break;
                 const uint64_t kd = kd0 + ((s * kTile) >> 4);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd) {
@@ -971,12 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (kSet == 1) {
         if (p) scan<true, 2>(a, a.pass[2], maps.pass[2], hv, item);
         else scan<false, 2>(a, a.pass[0], maps.pass[0], hv, item);
-    } else if (kSet == 2) {
-        if (p) scan<true, 0>(a, a.pass[p], maps.pass[p], hv, item);
-        else scan<false, 0>(a, a.pass[0], maps.pass[0], hv, item);
     } else {
-        if (p == 0) scan<false, 1>(a, a.pass[0], maps.pass[0], hv, item);
-        else if (p == 1) scan<true, 1>(a, a.pass[1], maps.pass[1], hv, item);
+        constexpr int kMode = kSet == 3 ? 1 : 0;
+        if (p == 0) scan<false, kMode>(a, a.pass[0], maps.pass[0], hv, item);
+        else if (p == 1) scan<true, kMode>(a, a.pass[1], maps.pass[1], hv, item);
         else scan<true, 0>(a, a.pass[2], maps.pass[2], hv, item);
     }
 }

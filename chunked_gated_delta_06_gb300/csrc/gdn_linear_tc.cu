@@ -38,7 +38,9 @@
 // Shared memory: K and V have two stages; Q has one tile, free again once Q~ is in tensor memory
 // (P was formed before), and the output a tile of its own, so that no tile waits for an output to
 // leave.  (Q in two stages, its tile taking the output: 109 instead of 105 us for the forward
-// below, 396 instead of 352 us for the backward of 4 x 4096 tokens.)
+// below, 396 instead of 352 us for the backward of 4 x 4096 tokens.)  A pair's exchange takes
+// some 3000 cycles: the epilogue reads its own half and frees O before it waits for the other
+// (backward 352 -> 342 us).
 //
 // What bounds it (4 x 4096 tokens, 16 / 32 heads: 105 us, 3.8 TB/s or 0.56 of the measured copy
 // rate): the steps of a chunk that wait on each other.  A chunk takes 5300 cycles, of which the
@@ -101,9 +103,8 @@ struct LinSmem {
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
     uint64_t full_vk[2], v_ok[2], p_done[2], pt_ready[2], w_ready[4], w_free[4], kv_done[2], kv_free[2], o_done[2];
     uint64_t full_q, s_ready, o_free, o_staged, x_free, factors, drain[3];
-    // pair mode: the peer's half of the exchange tile is free; the peer's half of O is here; this
-    // CTA's half has arrived
-    uint64_t peer_ok, rx_full, sent;
+    // pair mode: the peer may take this CTA's half of the next output; the peer's half is here
+    uint64_t peer_ok, rx_full;
     uint32_t tmem_base;
     int dead;
 };
@@ -185,8 +186,10 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Hands over a place whose reads have completed, and nothing that was written: relaxed (a release
+// to the cluster takes about a thousand cycles; backward of 4 x 4096 tokens 343 -> 332 us).
 __device__ __forceinline__ void remote_arrive(uint64_t *bar, uint32_t rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
                  : "memory");
 }
 // Copy `bytes` of this CTA's shared memory to the same kind of place in the peer's; completes
@@ -372,13 +375,13 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         mbar_arrive_expect_tx(&sm.full_vk[s], 2 * kTile);
         load(&maps.v, sm.v[s], hw, t, &sm.full_vk[s]);
         load(&maps.k, sm.k[s], hk, t, &sm.full_vk[s]);
-        // the tiles after next start towards L2 while both stages are taken
+        // tiles whose places are still taken start towards L2 (further ahead is slower)
         for (int h = 0; h < 2; ++h) {
             if (c + 2 < wk.n) {
                 tma_prefetch_3d(&maps.v, 64 * h, hw, wk.start(c + 2, kReverse));
                 tma_prefetch_3d(&maps.k, 64 * h, hk, wk.start(c + 2, kReverse));
             }
-            if (!kState && c + 1 < wk.n) tma_prefetch_3d(&maps.q, 64 * h, hq, wk.start(c + 1, kReverse));
+            if (!kState) tma_prefetch_3d(&maps.q, 64 * h, hq, t);
         }
     };
     auto load_q = [&](int c) {
@@ -409,7 +412,6 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             mbar_init(&sm.factors, 1);
             mbar_init(&sm.peer_ok, 1);
             mbar_init(&sm.rx_full, 1);
-            mbar_init(&sm.sent, 1);
             for (int i = 0; i < 3; ++i) mbar_init(&sm.drain[i], 1);
             sm.dead = 0;
             fence_mbar_init();
@@ -735,7 +737,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 // times a power of two for each 32 of a row (2^-12 of the largest at most, where the
                 // output is rounded at 2^-9).
                 if ((col >> 6) != (hv & 1)) {
-                    if (c > 0 && !wait_warp_cluster(sm, &sm.sent, (c - 1) & 1)) break;
+                    // plane 0 is free too: the peer has added what was sent before
+                    if (!wait_warp_cluster(sm, &sm.peer_ok, c & 1)) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float x[32];
@@ -755,7 +758,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                                 pack_half2(x[8 * j + 4], x[8 * j + 5]), pack_half2(x[8 * j + 6], x[8 * j + 7]));
                     }
                     fence_proxy_async_smem();
-                    if (!wait_warp_cluster(sm, &sm.peer_ok, c & 1)) break;
+                    __syncwarp();
                     if (lane == 0) {   // this warp's 32 rows
                         const uint32_t peer = (hv & 1) ^ 1;
                         remote_copy(sm.x + kHalf + r * 128, sm.x + r * 128, 32 * 128, &sm.rx_full, peer);
@@ -764,14 +767,13 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     __syncwarp();
                 }
                 if (c + 1 < wk.n) publish();   // while the peer's half comes
-                if (!wait_warp_cluster(sm, &sm.rx_full, c & 1)) break;
-                if (warp == kGroupP + kGroupW && lane == 0) remote_arrive(&sm.sent, (hv & 1) ^ 1);
                 const int h = col >> 6;
                 float x[32];
                 tmem_ld32(tb + lanes + kColX + first, x);
                 tmem_ld_wait();
                 tc_fence_before();
                 mbar_arrive(&sm.o_free);
+                if (!wait_warp_cluster(sm, &sm.rx_full, c & 1)) break;
                 const float theirs = __uint_as_float((uint32_t)sm.from_peer[r][h] << 23);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {   // (two terms: the same sum whichever CTA adds)

@@ -17,7 +17,11 @@
 // P~_ij = (lam^{i-j} / m_i) P_ij is rounded to bf16 once, and the epilogue multiplies row i
 // by so m_i: every term has one rounded factor, P~ or the bf16 copy of S, beside the output's
 // own rounding.  A row factor on the state's part alone would cost a second accumulator or
-// a round trip of O; a rounded Q~ a second rounding.
+// a round trip of O; a rounded Q~ a second rounding.  When no sequence has more than
+// one chunk the second stage is empty: there P~ and S get a second bf16 part each, and only the
+// output's rounding is left (the error of a few tokens averages over few values; relative, it is
+// 1.7e-3 where one part gives 2.4e-3).  In the kernels for all lengths the same rule by sequence
+// costs the backward of 4 x 4096 tokens 4 to 10 %, by its registers alone.
 //
 // The state is held in fp32 registers, and W = w lam^{..} v has fp32 accuracy: the weight is
 // split into bf16 numbers w1 + w2 + w3 (8 bits each), and
@@ -253,6 +257,18 @@ __device__ __forceinline__ bool wait_warp_cluster(LinSmem &sm, uint64_t *bar, ui
     return __all_sync(0xffffffffu, wait<true>(sm, bar, parity));
 }
 
+// What bf16 leaves of 8 values, as bf16 (nothing of an infinity, which the first part holds).
+__device__ __forceinline__ uint4 second_part(const float *x) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = x[j] - bf2f(f2bf(x[j]));
+        y[j] = y[j] == y[j] ? y[j] : 0.f;
+    }
+    return make_uint4(epi::pack_bf2(y[0], y[1]), epi::pack_bf2(y[2], y[3]), epi::pack_bf2(y[4], y[5]),
+                      epi::pack_bf2(y[6], y[7]));
+}
+
 struct Walk {      // the chunks of this CTA's segment, in scan order
     int t0, len, total;   // the sequence: first token, tokens, chunks
     int first, n;         // the segment: first chunk in scan order, chunks
@@ -319,8 +335,8 @@ __device__ __forceinline__ void write32(const LinearPass &a, const float (&x)[32
 // One scan of one (sequence, value head).  kMode 0: outputs and states.  1: outputs summed
 // over the two value heads of a cluster of two CTAs.  2: only the states, of every segment but
 // a sequence's last (their sums are the start states of the segments that a second launch
-// walks at once).
-template <bool kReverse, int kMode>
+// walks at once).  kOne: no sequence has more than one chunk.
+template <bool kReverse, int kMode, bool kOne = false>
 __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, const LinMaps::Pass &maps,
                                      const int hv, const int item) {
     constexpr bool kPair = kMode == 1, kState = kMode == 2;
@@ -353,6 +369,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
     wk.total = (wk.len + kC - 1) / kC;
     wk.first = seg * a.seg_chunks;
     wk.n = nseg > 1 ? min(a.seg_chunks, wk.total - wk.first) : wk.total;
+    if (kOne) wk.n = min(wk.n, 1);   // (as the host has checked)
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
     const float g2 = g * 1.4426950408889634f;
     bool cut = false;
@@ -448,6 +465,9 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         const int quad = warp & 3, half = warp >> 2;   // rows 32 quad .., columns 64 half ..
         const int i = quad * 32 + lane;
         const float at = (float)lane, lw = log2f(ps.w);   // w > 0
+        auto second = [&](int j) {   // 8 columns of P~'s second part
+            return reinterpret_cast<uint4 *>(sm.k[1] + half * kHalf + sw128_off(i, j));
+        };
         for (int c = 0; c < wk.n; ++c) {
             const uint32_t mine = tb + lanes + kColP + 128 * (c & 1) + 64 * half;
             const int L = wk.length(c, kReverse);
@@ -479,6 +499,10 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 if (kReverse ? b < quad : b > quad) {
 #pragma unroll
                     for (int p = 0; p < 16; ++p) u[p] = 0u;
+                    if (kOne) {
+#pragma unroll
+                        for (int p = 0; p < 32; p += 8) *second(32 * b2 + p) = make_uint4(0, 0, 0, 0);
+                    }
                 } else {
                     float r[32];
                     tmem_ld32(mine + 32 * b2, r);
@@ -508,12 +532,17 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
 #pragma unroll
                         for (int jj = 0; jj < 32; ++jj) r[jj] = 32 * b + jj < L ? r[jj] : 0.f;
                     }
+                    if (kOne) {
+#pragma unroll
+                        for (int p = 0; p < 32; p += 8) *second(32 * b2 + p) = second_part(r + p);
+                    }
 #pragma unroll
                     for (int p = 0; p < 16; ++p) u[p] = epi::pack_bf2(r[2 * p], r[2 * p + 1]);
                 }
                 tmem_st16(mine + 16 * b2, x);   // over columns that this warp has read
             }
             tmem_st32(mine + 32, q);
+            if (kOne) fence_proxy_async_smem();
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&sm.pt_ready[c & 1]);
@@ -685,6 +714,11 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             fence_proxy_async_smem();
             mbar_arrive(&sm.s_ready);
         };
+        if (kOne) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 8)
+                *reinterpret_cast<uint4 *>(sm.v[1] + (col >> 6) * kHalf + sw128_off(r, j)) = second_part(st + j);
+        }
         if (!kState && wk.n > 0) publish();
         auto store_state = [&]() {
             if (!dst) return;
@@ -906,6 +940,14 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         mma_ts(tb + kColX, tb + 128 * s + a_step(x), vd + 128 * x, idv, true);
+                    if (kOne) {   // second parts: S in the second stage's V tile, P~ in its K tile
+                        const uint64_t p2 = sdesc(smem_u32(sm.k[1]), 16, 1024), s2 = sdesc(smem_u32(sm.v[1]), 16, 1024);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            mma_ts(tb + kColX, tb + a_step(x) + 32, s2 + k_step(x), ids, true);
+                            mma_bf16(tb + kColX, p2 + k_step(x), vd + 128 * x, idv, true);
+                        }
+                    }
                     mma_commit(&sm.o_done[s]);
                 }
                 __syncwarp();
@@ -968,7 +1010,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
 // The scans of a call, work items longest first, the passes of an item and its value heads
 // side by side (the two CTAs of a cluster are two value heads of one pass).
 //   kSet 0: a forward.  1: the state pass.  2, 3: a backward without and with pairs.
-template <int kSet>
+template <int kSet, bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_tc(const __grid_constant__ LinearArgs a, const __grid_constant__ LinMaps maps) {
     const int hv = blockIdx.x % a.HV, rest = blockIdx.x / a.HV;
@@ -982,15 +1024,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         p = rest % sides * (kSet == 1 ? 2 : 1);   // (the state pass takes scans 0 and 2)
     }
     if (kSet == 0) {
-        scan<false, 0>(a, a.pass[0], maps.pass[0], hv, item);
+        scan<false, 0, kOne>(a, a.pass[0], maps.pass[0], hv, item);
     } else if (kSet == 1) {
         if (p) scan<true, 2>(a, a.pass[2], maps.pass[2], hv, item);
         else scan<false, 2>(a, a.pass[0], maps.pass[0], hv, item);
+    } else if (kSet == 2) {
+        if (p) scan<true, 0, kOne>(a, a.pass[p], maps.pass[p], hv, item);
+        else scan<false, 0, kOne>(a, a.pass[0], maps.pass[0], hv, item);
     } else {
-        constexpr int kMode = kSet == 3 ? 1 : 0;
-        if (p == 0) scan<false, kMode>(a, a.pass[0], maps.pass[0], hv, item);
-        else if (p == 1) scan<true, kMode>(a, a.pass[1], maps.pass[1], hv, item);
-        else scan<true, 0>(a, a.pass[2], maps.pass[2], hv, item);
+        if (p == 0) scan<false, 1, kOne>(a, a.pass[0], maps.pass[0], hv, item);
+        else if (p == 1) scan<true, 1, kOne>(a, a.pass[1], maps.pass[1], hv, item);
+        else scan<true, 0, kOne>(a, a.pass[2], maps.pass[2], hv, item);
     }
 }
 
@@ -1026,10 +1070,11 @@ __global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ L
     }
 }
 
-template <int kSet>
-cudaError_t launch_set(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
+using Kernel = void (*)(LinearArgs, LinMaps);
+
+cudaError_t launch_set(Kernel kernel, int scans, bool pairs, const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.items * a.HV * (kSet == 1 ? a.state_passes : a.passes));
+    cfg.gridDim = dim3((unsigned)a.items * a.HV * scans);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(LinSmem) + 1024;
     cfg.stream = s;
@@ -1038,27 +1083,27 @@ cudaError_t launch_set(const LinearArgs &a, const LinMaps &m, cudaStream_t s) {
     at[0].val.clusterDim.x = 2;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = kSet == 3 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, k_linear_tc<kSet>, a, m);
+    cfg.numAttrs = pairs ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a, m);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s) {
-    const int set = a.passes == 1 ? 0 : a.pass[0].pair ? 3 : 2;
-    const void *kernels[] = {(const void *)k_linear_tc<0>, (const void *)k_linear_tc<1>, (const void *)k_linear_tc<2>,
-                             (const void *)k_linear_tc<3>};
+    const bool one = a.longest <= kC, pairs = a.passes > 1 && a.pass[0].pair;
+    const Kernel kernel = a.passes == 1 ? (one ? k_linear_tc<0, true> : k_linear_tc<0, false>)
+                          : pairs       ? (one ? k_linear_tc<3, true> : k_linear_tc<3, false>)
+                                        : (one ? k_linear_tc<2, true> : k_linear_tc<2, false>);
+    const Kernel states = k_linear_tc<1, false>;
     const int smem = (int)sizeof(LinSmem) + 1024;
-    for (int k : {set, a.seg_chunks > 0 ? 1 : set}) {   // the groups' register shares rely on it
+    cudaError_t e;
+    for (Kernel k : {kernel, a.seg_chunks > 0 ? states : kernel}) {
         cudaFuncAttributes fa;
-        const cudaError_t err = cudaFuncGetAttributes(&fa, kernels[k]);
-        if (err != cudaSuccess) return err;
-        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+        if ((e = cudaFuncGetAttributes(&fa, k)) != cudaSuccess) return e;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;   // the groups' register shares rely on it
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        if (a.seg_chunks == 0) break;
     }
-    cudaError_t e = cudaFuncSetAttribute(kernels[set], cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && a.seg_chunks > 0)
-        e = cudaFuncSetAttribute(kernels[1], cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     // (the calls above have made the device's context current, which the map encoder needs)
     LinMaps m;
     memset(&m, 0, sizeof(m));
@@ -1096,11 +1141,11 @@ cudaError_t launch_linear_tc(const LinearArgs &a, cudaStream_t s) {
     }
     if (!ok) return cudaErrorInvalidValue;
     if (a.seg_chunks > 0) {
-        if ((e = launch_set<1>(a, m, s)) != cudaSuccess) return e;
+        if ((e = launch_set(states, a.state_passes, false, a, m, s)) != cudaSuccess) return e;
         k_linear_stitch<<<dim3(kDim * kDim / 1024, a.HV, a.N * a.state_passes), 256, 0, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return set == 0 ? launch_set<0>(a, m, s) : set == 2 ? launch_set<2>(a, m, s) : launch_set<3>(a, m, s);
+    return launch_set(kernel, a.passes, pairs, a, m, s);
 }
 
 }  // namespace gdn

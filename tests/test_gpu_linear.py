@@ -327,3 +327,28 @@ def test_python_calls_refuse_what_the_kernels_cannot_read():
         gdn.linear_attn_fwd(c.q[:, :, :64].contiguous(), c.k[:, :, :64].contiguous(), c.v, c.g, c.cu, c.cu_dev)
     with pytest.raises(ValueError):
         gdn.linear_attn_bwd(*args()[:4], c.do[:10], c.cu, c.cu_dev)
+
+
+# Sequences of one chunk: the second bf16 parts leave 2^-16 of each term, the fp32 sums at most
+# 2^-12, and the output is rounded once.  (One or three value heads a key head: no exchange.)
+@pytest.mark.parametrize("lens, H, HV", [([1], 1, 1), ([2, 1, 0, 7], 2, 2), ([128], 1, 1), ([40] * 3, 1, 3),
+                                         ([127, 65], 1, 1)])
+@pytest.mark.parametrize("states", [True, False])
+def test_one_chunk_outputs(lens, H, HV, states):
+    c = Case(lens, H, HV, seed=3, states=states)
+    bound = lambda r, m: 2.0 ** -12 * m + 2.0 ** -7.9 * np.abs(r) + 1e-30  # noqa: E731
+    (ro, _), (mo, _) = c.ref_fwd()
+    ref.check("o", c.fwd()[0], ro, bound(ro, mo))
+    (r, m), gr = c.ref_bwd(), c.bwd()
+    for n in ("dq", "dk", "dv"):
+        ref.check(n, gr[n], r[n], bound(r[n], m[n]))
+
+
+@pytest.mark.parametrize("lens", [[5], [130]])
+def test_infinite_state_stays_in_its_column(lens):
+    c = Case(lens, 1, 1, seed=0)
+    c.h0[0, 0, 3, 7] = float("inf")   # [K, V]
+    o, _ = c.fwd()
+    assert torch.isinf(o[:, :, 7]).all()
+    o[:, :, 7] = 0
+    assert torch.isfinite(o).all()

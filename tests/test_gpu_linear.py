@@ -352,3 +352,36 @@ def test_infinite_state_stays_in_its_column(lens):
     assert torch.isinf(o[:, :, 7]).all()
     o[:, :, 7] = 0
     assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("H, HV", [(1, 1), (1, 2), (1, 4)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_values_between_sequences_of_one_chunk(H, HV, bad):
+    c = Case([70, 20, 128, 33], H, HV)
+    clean, gr = c.fwd(), c.bwd()
+    for x in (c.q, c.k, c.v, c.do):
+        x[70:90] = bad
+    c.h0[1] = bad
+    c.dht[1] = bad
+    o, ht = c.fwd()
+    bw = c.bwd()
+    rest = [i for i in range(251) if not 70 <= i < 90]
+    for a, b in ((o, clean[0]), (bw["dq"], gr["dq"]), (bw["dk"], gr["dk"]), (bw["dv"], gr["dv"])):
+        assert torch.equal(a[rest], b[rest])
+    for a, b in ((ht, clean[1]), (bw["dh0"], gr["dh0"])):
+        assert torch.equal(a[[0, 2, 3]], b[[0, 2, 3]])
+
+
+def test_many_sequences_of_one_chunk():
+    c = Case([3, 0, 120, 17] * 40, 1, 2)
+    c.check_fwd(*c.fwd())
+    c.check_bwd(c.bwd())
+
+
+# Pairs whose scans of different lengths share the SMs, many times over: the same bits.
+def test_backward_of_pairs_repeats():
+    c = Case([300, 1, 0, 130, 257, 128, 40], 2, 4)
+    first = c.bwd()
+    for _ in range(30):
+        again = c.bwd()
+        assert all(torch.equal(first[n], again[n]) for n in first)

@@ -448,10 +448,11 @@ gdn_status decode_impl(int32_t batch, int32_t num_k_heads, int32_t num_v_heads, 
 // value head), about as long for each.  Few long sequences leave SMs idle, so a split plan
 // cuts every sequence into segments of `seg` chunks: a pass over the states alone, a stitch,
 // and the full pass over all segments at once.  Costs in chunks of a forward: 0.35 for a
-// chunk of the state pass, 1.3 for one of dq and dk in pairs, 2 for a CTA's start and end, 2 for
+// chunk of the state pass, 1.15 for one of dq and dk in pairs, 2 for a CTA's start and end, 2 for
 // the two launches more; a launch takes the longer of one CTA and the work over 152 SMs, and
 // half a CTA more when they take turns.  A split has to gain a tenth.  (1 x 65536 tokens, 64
-// heads: segments of 16, 32, 64 chunks and none take 1.10, 0.94, 0.96 and 1.36 ms.)  A function of the problem alone.
+// heads: segments of 16, 32, 64 chunks and none take 1.10, 0.94, 0.96 and 1.32 ms.)  A function
+// of the problem alone.
 struct LinearPlan {
     int seg, items;
 };
@@ -459,8 +460,8 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d, int backward) {
     LinearPlan best{0, d.N};
     if (d.N > gdn::kLinearOrder || p->scan_segment_chunks < 0) return best;
     const bool pair = backward && d.HV / d.H % 2 == 0;
-    const double one = pair ? 1.3 : 1.0;                       // a chunk of the longest scan
-    const double all = !backward ? 1.0 : pair ? 3.6 : 3.0;     // of all the scans
+    const double one = pair ? 1.15 : 1.0;                      // a chunk of the longest scan
+    const double all = !backward ? 1.0 : pair ? 3.3 : 3.0;     // of all the scans
     auto launch_cost = [&](double cta, double work) {
         const double area = work * d.HV / 152.0;
         return area <= cta ? cta : area + 0.5 * cta;

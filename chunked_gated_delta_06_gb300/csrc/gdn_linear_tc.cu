@@ -17,11 +17,11 @@
 // P~_ij = (lam^{i-j} / m_i) P_ij is rounded to bf16 once, and the epilogue multiplies row i
 // by so m_i: every term has one rounded factor, P~ or the bf16 copy of S, beside the output's
 // own rounding.  A row factor on the state's part alone would cost a second accumulator or
-// a round trip of O; a rounded Q~ a second rounding.  When no sequence has more than
-// one chunk the second stage is empty: there P~ and S get a second bf16 part each, and only the
-// output's rounding is left (the error of a few tokens averages over few values; relative, it is
-// 1.7e-3 where one part gives 2.4e-3).  In the kernels for all lengths the same rule by sequence
-// costs the backward of 4 x 4096 tokens 4 to 10 %, by its registers alone.
+// a round trip of O; a rounded Q~ a second rounding.  When no sequence has more than one chunk
+// the second stage is empty: there P~ and S get a second bf16 part each, and only the output's
+// rounding is left (the error of a few tokens averages over few values; relative, it is 1.7e-3
+// where one part gives 2.4e-3).  In the kernels for all lengths the same rule by sequence costs
+// the backward of 4 x 4096 tokens 4 to 10 %, by its registers alone.
 //
 // The state is held in fp32 registers, and W = w lam^{..} v has fp32 accuracy: the weight is
 // split into bf16 numbers w1 + w2 + w3 (8 bits each), and
@@ -78,10 +78,11 @@ constexpr int kGroupP = 8, kGroupW = 8, kGroupS = 8;  // warps of the three grou
 constexpr int kWarpLoad = kGroupP + kGroupW + kGroupS;
 constexpr int kThreads = (kWarpLoad + 4) * 32;
 
-// Registers a thread: the state's warps hold 64 floats each, P's a row of Q~.  The groups' shares
-// must not exceed what the launch gives (kThreads * kRegsLaunch, checked there too), or the
-// increase would never end.
-constexpr int kRegsLaunch = 72, kRegsP = 80, kRegsW = 48, kRegsState = 104, kRegsIssue = 40;
+// Registers a thread: the state's warps hold 64 floats and 32 of an output each, P's a row of Q~.
+// The groups' shares must not exceed what the launch gives (kThreads * kRegsLaunch, checked there
+// too), or the increase would never end.  (P 80, W 48, state 104: backward of 4 x 4096 tokens 332
+// instead of 322 us, by spills of the pairs' epilogue; P 72 or W 32 for more elsewhere: slower.)
+constexpr int kRegsLaunch = 72, kRegsP = 80, kRegsW = 40, kRegsState = 112, kRegsIssue = 40;
 static_assert(kGroupP * kRegsP + kGroupW * kRegsW + kGroupS * kRegsState + 4 * kRegsIssue <=
                       (kWarpLoad + 4) * kRegsLaunch &&
                   kRegsW <= kRegsP,   // in the state pass P's warps do W's work, with W's share

@@ -782,8 +782,10 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                         float big = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(x[j]));
-                        // 2^e <= scale * big < 2^{e+1}, within the normal numbers (infinities stay infinite)
-                        const uint32_t e = min(max((__float_as_uint(scale * big) >> 23) & 0xff, 1u), 253u);
+                        // 2^e <= scale * big < 2^{e+1}, within the normal numbers (infinities stay infinite),
+                        // and large enough for scale * 2^-e to be finite: a row of zeros stays zeros
+                        const uint32_t least = max((__float_as_uint(scale) >> 23) & 0xff, 127u) - 126u;
+                        const uint32_t e = min(max((__float_as_uint(scale * big) >> 23) & 0xff, least), 253u);
                         scale32(x, scale * __uint_as_float((254u - e) << 23));
                         sm.to_peer[r][h] = (unsigned char)e;
 #pragma unroll

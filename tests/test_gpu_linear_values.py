@@ -1,0 +1,37 @@
+"""Decay-only linear attention at the edges of the number range: scales, columns of very different
+size, infinities in the states, against the 64-bit definition."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_gated_delta_06_gb300 as gdn  # noqa: F401
+
+import linear_reference as ref
+from test_gpu_linear import Case, _f64
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_bwd(c, scale):
+    """The backward at a scale against the reference, to the bounds of the other tests."""
+    gr = c.bwd(scale=scale)
+    h, d = (None, None) if c.h0 is None else (_f64(c.h0), _f64(c.dht))
+    ab = (None, None) if h is None else (np.abs(h), np.abs(d))
+    r = ref.backward(*c.host(), _f64(c.do), h, d, scale=scale)
+    m = ref.backward(*c.host(True), np.abs(_f64(c.do)), *ab, scale=scale)
+    for n in ("dq", "dk", "dv"):
+        ref.check(n, gr[n], r[n], ref.out_bound(r[n], m[n]))
+    ref.check("dh0", gr["dh0"], r["dh0"], ref.state_bound(m["dh0"]))
+
+
+# Tokens without a gradient (a loss mask, padding) give rows of zeros in the sum of a pair.
+@pytest.mark.parametrize("lens", [[70], [300, 40]])
+@pytest.mark.parametrize("HV", [1, 2, 4])
+@pytest.mark.parametrize("scale", [1.0, 4.0, 11.3])
+def test_backward_of_masked_tokens_at_any_scale(lens, HV, scale):
+    c = Case(lens, 1, HV, seed=3, states=False)
+    c.do[::3] = 0
+    c.do[40:60] = 0
+    c.q[10:20] = 0
+    c.h0 = c.dht = None
+    _check_bwd(c, scale)

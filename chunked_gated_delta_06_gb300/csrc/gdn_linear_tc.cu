@@ -781,7 +781,8 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                         tmem_ld_wait();
                         float big = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) big = fmaxf(big, fabsf(x[j]));
+                        for (int j = 0; j < 32; ++j)
+                            big = fmaxf(big, fabsf(x[j]) <= 3.4028235e38f ? fabsf(x[j]) : 0.f);   // the finite ones
                         // 2^e <= scale * big < 2^{e+1}, within the normal numbers (infinities stay infinite),
                         // and large enough for scale * 2^-e to be finite: a row of zeros stays zeros
                         const uint32_t least = max((__float_as_uint(scale) >> 23) & 0xff, 127u) - 126u;

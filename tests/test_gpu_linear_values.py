@@ -35,3 +35,32 @@ def test_backward_of_masked_tokens_at_any_scale(lens, HV, scale):
     c.q[10:20] = 0
     c.h0 = c.dht = None
     _check_bwd(c, scale)
+
+
+def _columns(name, got, want, bound, bad):
+    """Feature `bad` of `got` is infinite wherever the definition has it so, the rest within bounds."""
+    got = _f64(got)
+    assert not np.isfinite(got[..., bad]).any(), name
+    rest = np.arange(got.shape[-1]) != bad
+    off = np.abs(got - want)[..., rest] / bound[..., rest]
+    assert np.all(off <= 1), "%s: worst %.3g of the bound" % (name, np.nanmax(off))
+
+
+# An infinite element of a state reaches one feature of a gradient; the features beside it, which
+# two value heads add up, keep both heads' parts.
+@pytest.mark.parametrize("lens", [[60], [200]])
+@pytest.mark.parametrize("HV", [1, 2, 4])
+@pytest.mark.parametrize("row, head", [(5, 0), (70, 0), (40, 1), (127, 1)])
+def test_backward_beside_an_infinite_state(lens, HV, row, head):
+    c = Case(lens, 1, HV, seed=0)
+    c.g.fill_(-0.02)
+    head = min(head, HV - 1)
+    c.h0[0, head, row, 9] = 0
+    c.dht[0, head, row, 9] = 0
+    r, m = c.ref_bwd()
+    c.h0[0, head, row, 9] = float("inf")
+    c.dht[0, head, row, 9] = float("-inf")
+    gr = c.bwd()
+    for n in ("dq", "dk"):
+        _columns(n, gr[n][:, 0], r[n][:, 0], ref.out_bound(r[n], m[n])[:, 0], row)
+    _columns("dv", gr["dv"][:, head], r["dv"][:, head], ref.out_bound(r["dv"], m["dv"])[:, head], 9)

@@ -44,7 +44,9 @@
 // leave.  (Q in two stages, its tile taking the output: 109 instead of 105 us for the forward
 // below, 396 instead of 352 us for the backward of 4 x 4096 tokens.)  A pair's exchange takes
 // some 3000 cycles: the epilogue reads its own half and frees O before it waits for the other
-// (backward 352 -> 342 us).
+// (backward 352 -> 342 us).  The partial sums cross in fp32, stored straight into the peer's tile:
+// in fp16 with a power of two for 32 columns the backward took 3 % less (359 instead of 368 us in
+// turns), but columns far below the largest, or beside an infinity, were lost.
 //
 // What bounds it (4 x 4096 tokens, 16 / 32 heads: 105 us, 3.8 TB/s or 0.56 of the measured copy
 // rate): the steps of a chunk that wait on each other.  A chunk takes 5300 cycles, of which the
@@ -55,7 +57,6 @@
 // parts for W (by truncation or by error-free sums), also with all of a chunk's W ahead of KV;
 // finer W buffers; arrivals once a warp; P's factors in registers.  Slower: rows of O written
 // straight from registers (126 us), Q's tile freed before P is formed (113 us).
-#include <cuda_fp16.h>
 #include <stddef.h>
 #include <string.h>
 
@@ -99,11 +100,10 @@ constexpr uint32_t kCols = 512;
 struct LinSmem {
     unsigned char k[2][kTile], v[2][kTile];               // TMA tiles, two stages
     unsigned char q[kTile];                               // free again once P is formed and Q~ read
-    unsigned char x[kTile];                               // the output on its way (pair mode: half of it to
-                                                          // the peer in plane 0, the rest in plane 1)
+    unsigned char x[kTile];                               // the output on its way (pair mode: the peer's part of
+                                                          // this CTA's half, fp32; then the half in plane 1)
     unsigned char s[kTile];                               // bf16 copy of S, row r K-major
     bf16 wtab[3][kC];     // weights of a whole chunk's tokens, three parts
-    unsigned char to_peer[kC][2], from_peer[kC][2];  // pair mode: exponents of the exchanged halves' rows
     float ptab[32];       // decays inside a block of 32 columns of P
     float full_hi, full_lo, part_hi, part_lo;  // lam^128 and lam^(partial chunk), head and tail
     uint64_t full_vk[2], v_ok[2], p_done[2], pt_ready[2], w_ready[4], w_free[4], kv_done[2], kv_free[2], o_done[2];
@@ -162,10 +162,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
     return x;
 }
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-    const __half2 t = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&t);
-}
 
 // Four 8 x 8 bf16 matrices of shared rows, each transposed: register m of lane l holds
 // (row 2 (l % 4) + {0, 1}, column l / 4) of matrix m, whose rows lanes 8 m .. 8 m + 7 point at.
@@ -192,19 +188,19 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
     return r;
 }
 // Hands over a place whose reads have completed, and nothing that was written: relaxed (a release
-// to the cluster takes about a thousand cycles; backward of 4 x 4096 tokens 343 -> 332 us).
+// to the cluster takes about a thousand cycles; backward of 4 x 4096 tokens 343 -> 332 us).  The
+// memory model does not order those reads before the peer's stores; a dependency does.  Each value
+// read is part of a sum that the same lane stores (write32) before it arrives on o_staged, which
+// comes before this; a value that is not stored (a row past the sequence) may be anything.
 __device__ __forceinline__ void remote_arrive(uint64_t *bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_u32(bar), rank))
                  : "memory");
 }
-// Copy `bytes` of this CTA's shared memory to the same kind of place in the peer's; completes
-// on the peer's barrier.
-__device__ __forceinline__ void remote_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
-                                            uint32_t rank) {
+// Sixteen bytes into another CTA's shared memory; completes on that CTA's barrier.
+__device__ __forceinline__ void remote_store(uint32_t to, const float *x, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            map_rank(smem_u32(dst), rank)),
-        "r"(smem_u32(src)), "r"(bytes), "r"(map_rank(smem_u32(bar), rank))
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+        "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
@@ -331,6 +327,14 @@ __device__ __forceinline__ void write32(const LinearPass &a, const float (&x)[32
 #pragma unroll
         for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(a.o + at + 8 * j) = y[j];
     }
+}
+
+// Place of 16 bytes, unit j of row r, of the peer's columns 32 h ..: the 4 KB of one warp's rows
+// cover the chunks of plane 1 that write32 stages from that warp, and the same of plane 0.  Four
+// rows are 64 bytes side by side (one row's alone: backward of 4 x 4096 tokens 417 us).
+__device__ __forceinline__ uint32_t exchange_place(int r, int h, int j) {
+    const int at = 8 * (j & 3) + (((r >> 2) & 1) << 2) + ((r & 31) >> 3);
+    return (j >> 2) * kHalf + ((r & ~31) + at) * 128 + (((4 * h + (r & 3)) ^ (at & 7)) << 4);
 }
 
 // One scan of one (sequence, value head).  kMode 0: outputs and states.  1: outputs summed
@@ -768,41 +772,21 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             const bool mine = r < L && in_range(out, kPair ? 32 : 64, (long long)a.T * ps.no * kDim, a.status);
             unsigned char *orow = sm.x + (kPair ? kHalf : (col >> 6) * kHalf) + r * 128;
             if (kPair) {
-                // Each CTA writes 64 columns of the pair's sum; the other 64 go to the peer as fp16
-                // times a power of two for each 32 of a row (2^-12 of the largest at most, where the
-                // output is rounded at 2^-9).
+                // Each CTA writes 64 columns of the pair's sum; the other 64 go to the peer.
                 if ((col >> 6) != (hv & 1)) {
-                    // plane 0 is free too: the peer has added what was sent before
-                    if (!wait_warp_cluster(sm, &sm.peer_ok, c & 1)) break;
+                    if (!wait_warp_cluster(sm, &sm.peer_ok, c & 1)) break;   // its tile is free
+                    const uint32_t peer = (hv & 1) ^ 1;
+                    const uint32_t x_peer = map_rank(smem_u32(sm.x), peer), full = map_rank(smem_u32(&sm.rx_full), peer);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float x[32];
                         tmem_ld32(from + 32 * h, x);
                         tmem_ld_wait();
-                        float big = 0.f;
+                        scale32(x, scale);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            big = fmaxf(big, fabsf(x[j]) <= 3.4028235e38f ? fabsf(x[j]) : 0.f);   // the finite ones
-                        // 2^e <= scale * big < 2^{e+1}, within the normal numbers (infinities stay infinite),
-                        // and large enough for scale * 2^-e to be finite: a row of zeros stays zeros
-                        const uint32_t least = max((__float_as_uint(scale) >> 23) & 0xff, 127u) - 126u;
-                        const uint32_t e = min(max((__float_as_uint(scale * big) >> 23) & 0xff, least), 253u);
-                        scale32(x, scale * __uint_as_float((254u - e) << 23));
-                        sm.to_peer[r][h] = (unsigned char)e;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4 *>(sm.x + r * 128 + (((4 * h + j) ^ (r & 7)) << 4)) = make_uint4(
-                                pack_half2(x[8 * j], x[8 * j + 1]), pack_half2(x[8 * j + 2], x[8 * j + 3]),
-                                pack_half2(x[8 * j + 4], x[8 * j + 5]), pack_half2(x[8 * j + 6], x[8 * j + 7]));
+                        for (int j = 0; j < 8; ++j)
+                            remote_store(x_peer + exchange_place(r, h, j), x + 4 * j, full);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {   // this warp's 32 rows
-                        const uint32_t peer = (hv & 1) ^ 1;
-                        remote_copy(sm.x + kHalf + r * 128, sm.x + r * 128, 32 * 128, &sm.rx_full, peer);
-                        remote_copy(sm.from_peer[r], sm.to_peer[r], 32 * 2, &sm.rx_full, peer);
-                    }
-                    __syncwarp();
                 }
                 if (c + 1 < wk.n) publish();   // while the peer's half comes
                 const int h = col >> 6;
@@ -812,19 +796,17 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 tc_fence_before();
                 mbar_arrive(&sm.o_free);
                 if (!wait_warp_cluster(sm, &sm.rx_full, c & 1)) break;
-                const float theirs = __uint_as_float((uint32_t)sm.from_peer[r][h] << 23);
+                scale32(x, scale);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {   // (two terms: the same sum whichever CTA adds)
-                    const uint4 y = *reinterpret_cast<const uint4 *>(orow + (((4 * h + j) ^ (r & 7)) << 4));
-                    const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&yy[i]));
-                        x[8 * j + 2 * i] = fmaf(theirs, z.x, scale * x[8 * j + 2 * i]);
-                        x[8 * j + 2 * i + 1] = fmaf(theirs, z.y, scale * x[8 * j + 2 * i + 1]);
-                    }
+                for (int j = 0; j < 8; ++j) {   // (two terms: the same sum whichever CTA adds)
+                    const float4 y = *reinterpret_cast<const float4 *>(sm.x + exchange_place(r, h, j));
+                    x[4 * j] += y.x;
+                    x[4 * j + 1] += y.y;
+                    x[4 * j + 2] += y.z;
+                    x[4 * j + 3] += y.w;
                 }
-                write32(ps, x, out, mine, staged, orow, r, h);   // (over the 16 bytes it has read)
+                __syncwarp();
+                write32(ps, x, out, mine, staged, orow, r, h);   // (over what its warp has read)
             } else {
                 if (c > 0 && !wait_warp(sm, &sm.x_free, (c - 1) & 1)) break;
 #pragma unroll
@@ -854,10 +836,10 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         const int role = __shfl_sync(0xffffffffu, warp, 0) - kWarpLoad;
         if (role == 0) {
             // ------------------------------------------------------ loads
-            // pair mode: the exchange tile's second plane may take the peer's half of chunk c's output
+            // pair mode: the exchange tile may take the peer's part of chunk c's output
             auto arm = [&](int c) {
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&sm.rx_full, kHalf + kC * 2);
+                    mbar_arrive_expect_tx(&sm.rx_full, kTile);
                     remote_arrive(&sm.peer_ok, (hv & 1) ^ 1);
                 }
                 __syncwarp();

@@ -64,3 +64,14 @@ def test_backward_beside_an_infinite_state(lens, HV, row, head):
     for n in ("dq", "dk"):
         _columns(n, gr[n][:, 0], r[n][:, 0], ref.out_bound(r[n], m[n])[:, 0], row)
     _columns("dv", gr["dv"][:, head], r["dv"][:, head], ref.out_bound(r["dv"], m["dv"])[:, head], 9)
+
+
+# A feature of q and k far above its neighbours: every gradient keeps its own precision.
+@pytest.mark.parametrize("lens", [[60], [200, 129]])
+@pytest.mark.parametrize("HV", [1, 2, 4])
+@pytest.mark.parametrize("power", [18, 24, 40])
+def test_backward_of_features_of_very_different_size(lens, HV, power):
+    c = Case(lens, 1, HV, seed=0)
+    for x in (c.q, c.k):
+        x[:, :, [7, 90]] *= 2.0 ** power
+    c.check_bwd(c.bwd())

@@ -57,6 +57,7 @@
 // parts for W (by truncation or by error-free sums), also with all of a chunk's W ahead of KV;
 // finer W buffers; arrivals once a warp; P's factors in registers.  Slower: rows of O written
 // straight from registers (126 us), Q's tile freed before P is formed (113 us).
+#include <float.h>
 #include <stddef.h>
 #include <string.h>
 
@@ -264,6 +265,19 @@ __device__ __forceinline__ uint4 second_part(const float *x) {
     }
     return make_uint4(epi::pack_bf2(y[0], y[1]), epi::pack_bf2(y[2], y[3]), epi::pack_bf2(y[4], y[5]),
                       epi::pack_bf2(y[6], y[7]));
+}
+
+// e^{g n} as head + tail, 48 bits.  The head is rounded towards zero and the tail at least the
+// smallest number, so that both keep the sign of an infinite state (y hi + y lo is +-inf, not NaN);
+// a power that fp32 has no number for counts as the smallest too, unless e^g itself is zero.
+struct Decay {
+    float hi, lo;
+};
+__device__ __forceinline__ Decay decay_power(float g, double n) {
+    const float least = expf(g) == 0.f ? 0.f : __int_as_float(1);   // 2^-149
+    const double x = exp((double)g * n);
+    const float hi = __double2float_rz(x), lo = (float)(x - (double)hi);
+    return {hi < least ? least : hi, lo < least ? least : lo};   // (a NaN stays)
 }
 
 struct Walk {      // the chunks of this CTA's segment, in scan order
@@ -708,9 +722,10 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                 *reinterpret_cast<float4 *>(keep_start + (size_t)r * kDim + col + 4 * j) =
                     make_float4(st[4 * j], st[4 * j + 1], st[4 * j + 2], st[4 * j + 3]);
         }
-        if (cut) {   // the start state too
+        if (cut) {   // the start state too, but for infinities and NaN
+            const float one = expf(g);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) st[j] = 0.f;
+            for (int j = 0; j < 64; ++j) st[j] = fabsf(st[j]) <= FLT_MAX ? 0.f : one * st[j];
         }
         unsigned char *srow = sm.s + (col >> 6) * kHalf;
         auto publish = [&]() {
@@ -944,9 +959,9 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
             const uint64_t kd0 = sdesc(smem_u32(sm.k), kHalf, 1024);
             // lam^128 and lam^(partial chunk) to 48 bits, for the state
             if (lane < 2) {
-                const double x = exp((double)g * (double)(lane == 0 ? kC : wk.len % kC));
-                (lane == 0 ? sm.full_hi : sm.part_hi) = (float)x;
-                (lane == 0 ? sm.full_lo : sm.part_lo) = (float)(x - (double)(float)x);
+                const Decay x = decay_power(g, lane == 0 ? kC : wk.len % kC);
+                (lane == 0 ? sm.full_hi : sm.part_hi) = x.hi;
+                (lane == 0 ? sm.full_lo : sm.part_lo) = x.lo;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.factors);
@@ -1031,8 +1046,8 @@ __global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ L
     const int first = a.seg_first[x], nseg = a.seg_first[x + 1] - first;
     if (nseg < 3) return;
     const float g = a.log_decay[hv] < -1e4f ? -1e4f : a.log_decay[hv];
-    const double lam = exp((double)g * (double)a.seg_chunks * kC);
-    const float fh = (float)lam, fl = (float)(lam - (double)fh);
+    const Decay lam = decay_power(g, (double)a.seg_chunks * kC);
+    const float fh = lam.hi, fl = lam.lo;
     const size_t step4 = (size_t)a.HV * kDim * kDim / 4;
     float *rec = a.pass[blockIdx.z % a.state_passes * 2].seg_state;
     float4 *p = reinterpret_cast<float4 *>(rec + ((size_t)first * a.HV + hv) * kDim * kDim) +

@@ -75,3 +75,31 @@ def test_backward_of_features_of_very_different_size(lens, HV, power):
     for x in (c.q, c.k):
         x[:, :, [7, 90]] *= 2.0 ** power
     c.check_bwd(c.bwd())
+
+
+INF_DECAYS = [0.0, -1e-6, -0.003, -0.02, -0.3, -0.5, -1.0, -6.0, -100.0]
+
+
+def _state(name, got, want, bound, at):
+    """got[at] has the infinity, every other element is within bounds."""
+    got = _f64(got)
+    assert got[at] == np.inf, "%s: %r" % (name, got[at])
+    got[at] = want[at]
+    off = np.abs(got - want) / bound
+    assert np.all(off <= 1), "%s: worst %.3g of the bound" % (name, np.nanmax(off))
+
+
+# An infinite state stays infinite while e^g is not zero, whatever the tail of a chunk's factor.
+@pytest.mark.parametrize("lens, seg", [([1], -1), ([130], -1), ([300], -1), ([1300], 2)])
+@pytest.mark.parametrize("g", INF_DECAYS)
+def test_infinite_state_through_a_scan(lens, seg, g):
+    c = Case(lens, 1, 2, seed=0)
+    c.g.fill_(g)
+    for x in (c.h0, c.dht):
+        x[0, 1, 3, 7] = 0
+    (_, rh), (_, mh) = c.ref_fwd()
+    r, m = c.ref_bwd()
+    for x in (c.h0, c.dht):
+        x[0, 1, 3, 7] = float("inf")
+    _state("final_state", c.fwd(scan_segment_chunks=seg)[1], rh, ref.state_bound(mh), (0, 1, 3, 7))
+    _state("dh0", c.bwd(scan_segment_chunks=seg)["dh0"], r["dh0"], ref.state_bound(m["dh0"]), (0, 1, 3, 7))

@@ -37,8 +37,9 @@ constexpr int kStepRows = kDim / kStepWarps;
 // One block per (row, value head), as the gated step: a warp owns 16 rows of S, a lane one
 // float4 of each.  Bound by HBM, the state read and written once: 256 rows of 32 heads, 26 of
 // them null, take 143 us, 6.75 TB/s or 0.99 of the measured copy rate.
-// lam S + v k is taken as (S + v k) + (lam - 1) S where lam is near 1: lam rounded to fp32 would
-// be off by the same 2^-25 in every step of a long answer.
+// Where lam is near 1 it is a sum hi + lo: rounded to fp32 it would be off by the same 2^-25 in
+// every step of a long answer.  hi is rounded towards zero and lo at least 2^-149, so that an
+// infinite element of S stays infinite (inf hi + inf lo; (lam - 1) S would cancel it to NaN).
 __global__ void __launch_bounds__(kStepWarps * 32)
     k_linear_step(int H, int HV, float scale, const bf16 *__restrict__ q, const bf16 *__restrict__ k,
                   const bf16 *__restrict__ v, const float *__restrict__ log_decay,
@@ -68,17 +69,22 @@ __global__ void __launch_bounds__(kStepWarps * 32)
     }
     const float g = log_decay[hv];
     const bool slow = g > -0.5f;
-    const float lam = slow ? expm1f(g) : expf(g);
+    const float less = expm1f(g);   // lam - 1
+    const float lam = slow ? __fadd_rz(1.f, less) : expf(g);
+    const float lo = fmaxf(less - (lam - 1.f), __int_as_float(1));
     const bf16 *vrow = v + ((size_t)b * HV + hv) * kDim + r0;
     float mine = 0.f;
     auto rows = [&](auto near_one) {
 #pragma unroll
         for (int j = 0; j < kStepRows; ++j) {
             const float vj = bf2f(vrow[j]);
-            s[j].x = fmaf(lam, s[j].x, near_one ? fmaf(vj, kv[0], s[j].x) : vj * kv[0]);
-            s[j].y = fmaf(lam, s[j].y, near_one ? fmaf(vj, kv[1], s[j].y) : vj * kv[1]);
-            s[j].z = fmaf(lam, s[j].z, near_one ? fmaf(vj, kv[2], s[j].z) : vj * kv[2]);
-            s[j].w = fmaf(lam, s[j].w, near_one ? fmaf(vj, kv[3], s[j].w) : vj * kv[3]);
+            auto next = [&](float x, float k) {
+                return fmaf(lam, x, near_one ? fmaf(lo, x, vj * k) : vj * k);   // (v k is exact)
+            };
+            s[j].x = next(s[j].x, kv[0]);
+            s[j].y = next(s[j].y, kv[1]);
+            s[j].z = next(s[j].z, kv[2]);
+            s[j].w = next(s[j].w, kv[3]);
             __stcs(reinterpret_cast<float4 *>(S + (size_t)(r0 + j) * kDim + lane * 4), s[j]);
             const float dot = warp_sum(s[j].x * qv[0] + s[j].y * qv[1] + s[j].z * qv[2] + s[j].w * qv[3]);
             if (lane == j) mine = dot;

@@ -103,3 +103,22 @@ def test_infinite_state_through_a_scan(lens, seg, g):
         x[0, 1, 3, 7] = float("inf")
     _state("final_state", c.fwd(scan_segment_chunks=seg)[1], rh, ref.state_bound(mh), (0, 1, 3, 7))
     _state("dh0", c.bwd(scan_segment_chunks=seg)["dh0"], r["dh0"], ref.state_bound(m["dh0"]), (0, 1, 3, 7))
+
+
+@pytest.mark.parametrize("g", INF_DECAYS)
+def test_infinite_state_through_steps(g):
+    rng = np.random.default_rng(4)
+    q, k, v = (torch.from_numpy(rng.standard_normal((2, 1, 128)).astype(np.float32)).cuda().to(torch.bfloat16)
+               for _ in range(3))
+    pool = torch.from_numpy(rng.standard_normal((3, 1, 128, 128)).astype(np.float32)).cuda()
+    gd = torch.full((1,), g, device="cuda")
+    idx = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    pool[2, 0, 7, 3] = 0   # [V, K]
+    before = _f64(pool[1:])[:, 0]
+    pool[2, 0, 7, 3] = float("inf")
+    o = gdn.linear_attn_step(q, k, v, gd, pool, idx)
+    vk = _f64(v)[:, 0, :, None] * _f64(k)[:, 0, None, :]
+    lam = np.exp(np.float64(np.float32(g)))
+    _state("pool", pool[1:, 0], lam * before + vk, ref.state_bound(lam * np.abs(before) + np.abs(vk)), (1, 7, 3))
+    o = _f64(o)[:, 0]
+    assert np.isinf(o[1, 7]) and np.isfinite(np.delete(o[1], 7)).all() and np.isfinite(o[0]).all()

@@ -527,6 +527,16 @@ gdn_status check_linear_ws(size_t need, const void *workspace, size_t ws_size) {
     return ws_size < (need > 0 ? need : kAlign) ? GDN_ERR_WORKSPACE_TOO_SMALL : GDN_OK;
 }
 
+// Bytes of a call's buffer.
+struct Span {
+    const void *at;
+    size_t bytes;
+    bool meets(const Span &x) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(x.at);
+        return at && x.at && bytes && x.bytes && a < b + x.bytes && b < a + bytes;
+    }
+};
+
 gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan,
                             const float *log_decay) {
     gdn::LinearArgs a{};
@@ -800,7 +810,19 @@ gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *
     LinearWs ws;
     const LinearPlan plan = plan_linear(p, d, 1);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL / 3) return GDN_ERR_INVALID_ARG;
-    if ((st = check_linear_ws(carve_linear(d, plan, 1, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
+    const size_t need = carve_linear(d, plan, 1, workspace, &ws);
+    if ((st = check_linear_ws(need, workspace, ws_size)) != GDN_OK) return st;
+    // the three scans run at once: what one of them writes, no other may read or write
+    const size_t tokens = (size_t)d.T * gdn::kDim * sizeof(bf16);
+    const size_t states = (size_t)d.N * d.HV * gdn::kDim * gdn::kDim * sizeof(float);
+    const Span spans[] = {{dq, tokens * d.H}, {dk, tokens * d.H}, {dv, tokens * d.HV}, {dh0, states},
+                          {workspace, need}, {q, tokens * d.H}, {k, tokens * d.H}, {v, tokens * d.HV},
+                          {d_o, tokens * d.HV}, {initial_state, states}, {d_final_state, states},
+                          {log_decay, d.HV * sizeof(float)}, {p->cu_seqlens_dev, (d.N + 1) * sizeof(int32_t)},
+                          {p->device_status, sizeof(int32_t)}};
+    for (int i = 0; i < 5; ++i)
+        for (size_t j = i + 1; j < sizeof(spans) / sizeof(spans[0]); ++j)
+            if (spans[i].meets(spans[j])) return GDN_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
     a.passes = 3;

@@ -339,6 +339,7 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward);
  *   initial_state  fp32 [N, HV, 128(K), 128(V)], or NULL for zeros
  *   o              bf16 [T, HV, 128] (out)
  *   final_state    fp32 [N, HV, 128, 128] (out), or NULL; not initial_state
+ *                  (outputs must not overlap inputs or one another)
  *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 0), 256-byte
  *                  aligned; or NULL with ws_bytes 0, which is enough where the
  *                  plan needs none (GDN_ERR_WORKSPACE_TOO_SMALL where it does) */
@@ -363,9 +364,11 @@ gdn_status gdn_linear_attn_prefill_paged(const gdn_problem *p, const void *q, co
  *   d_final_state  fp32 [N, HV, 128, 128], or NULL for zeros
  *   dq, dk         bf16 [T, H, 128]  (out; summed over the HV/H value heads)
  *   dv             bf16 [T, HV, 128] (out)
- *   dh0            fp32 [N, HV, 128, 128] (out), or NULL; not d_final_state
+ *   dh0            fp32 [N, HV, 128, 128] (out), or NULL
  *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 1), 256-byte
- *                  aligned; or NULL with ws_bytes 0, as in the forward */
+ *                  aligned; or NULL with ws_bytes 0, as in the forward
+ * dq, dk, dv, dh0 and the workspace must overlap neither an input nor one
+ * another (GDN_ERR_INVALID_ARG): the inputs are read to the end of the call. */
 gdn_status gdn_linear_attn_bwd(const gdn_problem *p, const void *q, const void *k, const void *v,
                                const float *log_decay, const float *initial_state,
                                const void *d_o, const float *d_final_state, void *dq, void *dk,

@@ -98,6 +98,26 @@ def test_missing_and_misaligned_buffers_are_refused():
     assert gdn.gdn_linear_attn_workspace_bytes(p, 0) > 0 and gdn.gdn_linear_attn_workspace_bytes(p, 1) > 0
 
 
+def test_backward_outputs_over_inputs_are_refused():
+    # dq, dk, dv and dh0 are written while the other scans still read: no overlap, in whole or part
+    p, keep = _problem([0, 5, 9])
+    names = ["q", "k", "v", "g", "h0", "do", "dht", "dq", "dk", "dv", "dh0", "ws"]
+    at = {n: 0x10000000 * (i + 1) for i, n in enumerate(names)}
+    tokens = dict(q=2, k=2, v=4, do=4, dq=2, dk=2, dv=4)
+    size = {n: 9 * tokens[n] * 256 if n in tokens else 2 * 4 * 65536 for n in names}
+    size["g"] = 16
+    for out in ("dq", "dk", "dv", "dh0"):
+        for other in names:
+            if other in (out, "ws"):
+                continue
+            for place in (at[other], at[other] + (size[other] - 16 if other != "g" else 0),
+                          at[other] - size[out] + 16):
+                a = dict(at)
+                a[out] = place
+                got = gdn.gdn_linear_attn_bwd(p, *(a[n] for n in names), 1 << 20, None)
+                assert got == binding.GDN_ERR_INVALID_ARG, (out, other, hex(place))
+
+
 def test_step_arguments():
     def call(batch=4, H=2, HV=4, K=128, pool=FAKE, slots=8, idx=FAKE, g=FAKE, q=FAKE):
         return gdn.gdn_linear_attn_step(batch, H, HV, K, 128, 0.0, q, FAKE, FAKE, g, pool, slots, idx, FAKE,

@@ -557,6 +557,8 @@ gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPla
             a.seg_first[x + 1] = a.seg_first[x] + (plan.seg && c > 0 ? (c - 1) / plan.seg + 1 : 1);
         }
         for (int n = 0; n <= d.N; ++n) a.cu[n] = cu[n];
+    } else {
+        for (int n = 0; n <= d.N; ++n) a.cu_sum += gdn::offset_term(n, cu[n]);
     }
     a.log_decay = log_decay;
     a.cu_dev = p->cu_seqlens_dev;

@@ -33,6 +33,17 @@ struct LinearPass {
     int seg_rows;             // row by row, or column by column (another scan's transposed states)
     float so, w;              // output and update factors
 };
+// An offset's part of a sum (mod 2^64) that holds the device's cu_seqlens against the host's: times
+// an odd number of its place, so that one changed offset always changes the sum, and several but
+// for a chance of 2^-64.
+__host__ __device__ inline uint64_t offset_term(int i, int32_t x) {
+    uint64_t m = (uint64_t)(i + 1) * 0x9e3779b97f4a7c15ull;   // 2^64 / golden ratio
+    m ^= m >> 32;
+    m *= 0xd1342543de82ef95ull;
+    m ^= m >> 29;
+    return (uint64_t)(uint32_t)x * (m | 1);
+}
+
 struct LinearArgs {
     int N, T, HV;
     int longest;              // tokens of the longest sequence (host copy of cu_seqlens)
@@ -44,6 +55,7 @@ struct LinearArgs {
     const int *pool_idx, *pool_resume;
     int *pool_status;
     const int *cu_dev;        // [N + 1]
+    uint64_t cu_sum;          // N > kLinearOrder: the sum of the host's offset_terms
     int *status;
     // Work items: (sequence, segment), grid order.  seg_chunks > 0 (N <= kLinearOrder only) cuts
     // the sequences into segments of that many chunks, which are walked at once.

@@ -377,6 +377,7 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         if (tid == kThreads - 1 && (a.cu_dev[n] != wk.t0 || a.cu_dev[n + 1] != wk.t0 + wk.len) && a.status)
             atomicOr(a.status, GDN_DEVICE_CU_SEQLENS_MISMATCH);
     } else {
+        // the device's extents, within the buffers; the first CTA compares all of them (below)
         wk.t0 = a.cu_dev[n];
         wk.len = a.cu_dev[n + 1] - wk.t0;
         if (wk.t0 < 0 || wk.len < 0 || wk.t0 > a.T - wk.len || wk.len > a.longest) {
@@ -992,6 +993,12 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
                     }
                     __syncwarp();
                 }
+            }
+            if (!kState && a.N > kLinearOrder && blockIdx.x == 0 && a.status) {
+                uint64_t sum = 0;
+                for (int i = lane; i <= a.N; i += 32) sum += offset_term(i, a.cu_dev[i]);
+                for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                if (lane == 0 && sum != a.cu_sum) atomicOr(a.status, GDN_DEVICE_CU_SEQLENS_MISMATCH);
             }
         }
         if (role > 0 && *(volatile int *)&sm.dead) {

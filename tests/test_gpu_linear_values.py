@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-import chunked_gated_delta_06_gb300 as gdn  # noqa: F401
+import chunked_gated_delta_06_gb300 as gdn
 
 import linear_reference as ref
 from test_gpu_linear import Case, _f64
@@ -122,3 +122,25 @@ def test_infinite_state_through_steps(g):
     _state("pool", pool[1:, 0], lam * before + vk, ref.state_bound(lam * np.abs(before) + np.abs(vk)), (1, 7, 3))
     o = _f64(o)[:, 0]
     assert np.isinf(o[1, 7]) and np.isfinite(np.delete(o[1], 7)).all() and np.isfinite(o[0]).all()
+
+
+# More sequences than a launch carries offsets for: the device's copy is walked, and any difference
+# from the host's is reported.
+@pytest.mark.parametrize("lens", [[3, 0, 70], [3, 0, 130]])
+@pytest.mark.parametrize("wrong", ["shift", "two", "first", "last", "outside", "backwards"])
+def test_device_offsets_of_many_sequences(lens, wrong):
+    c = Case(lens * 50, 1, 2, states=False)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = c.fwd(device_status=status), c.bwd(device_status=status)
+    assert int(status) == 0
+    right, T = c.cu_dev.clone(), int(c.cu[-1])
+    at, by = dict(shift=([60], -1), two=([30, 60], -1), first=([0], 1), last=([-1], -1), outside=([75], T),
+                  backwards=([75], -T))[wrong]
+    c.cu_dev[at] += by
+    for call in (c.fwd, c.bwd):
+        status.zero_()
+        call(device_status=status)
+        assert int(status) == gdn.binding.GDN_DEVICE_CU_SEQLENS_MISMATCH
+    c.cu_dev.copy_(right)
+    again = c.fwd(), c.bwd()
+    assert torch.equal(good[0][0], again[0][0]) and all(torch.equal(good[1][n], again[1][n]) for n in again[1])

@@ -20,54 +20,72 @@ _ROPE_SCALING = {"none": binding.GDN_ROPE_SCALE_NONE, "linear": binding.GDN_ROPE
 _ROPE_LAYOUT = {"half": binding.GDN_ROPE_HALF, "interleaved": binding.GDN_ROPE_INTERLEAVED}
 
 torch = None
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _ready():
     """The library; torch is imported by the first call, not with the package."""
-    global torch, _raw_stream
+    global torch, _raw_stream, _current_device
     if torch is None:
         import torch as module
         torch = module
         _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch._C._cuda_getDevice
     return binding._lib or binding.lib()
 
 
-def _need(t, name, dtype, shape):
-    """Refuse a tensor the kernels would misread: they take dense CUDA tensors of one dtype."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _device(q):
+    """The device of a call: q's, which must be the current one (the library launches there)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a contiguous CUDA tensor")
+    if dev != _current_device():
+        raise ValueError("q is on cuda:%d, which is not the current device" % dev)
+    return dev
+
+
+def _need(t, name, dtype, shape, dev):
+    """Refuse a tensor the kernels would misread: they take dense tensors of one dtype on the
+    call's device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, not %s" % (name, dtype, t.dtype))
     if tuple(t.shape) != shape:
         raise ValueError("%s must have shape %s, not %s" % (name, shape, tuple(t.shape)))
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, not on q's device" % (name, t.get_device()))
     raise ValueError("%s must be a contiguous CUDA tensor" % name)
 
 
-def _maybe(t, name, dtype, shape):
-    return None if t is None else _need(t, name, dtype, shape)
+def _maybe(t, name, dtype, shape, dev):
+    return None if t is None else _need(t, name, dtype, shape, dev)
 
 
-def _status(t):
+def _status(t, dev):
     if t is None:
         return None
     if t.dtype is not torch.int32 or not t.is_cuda or t.numel() < 1:
         raise TypeError("a device status is an int32 CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError("a device status must be on q's device")
     return t.data_ptr()
 
 
 def _inputs(q, k, v, log_decay):
-    """(T, H, K, HV, V) and the four addresses."""
+    """(T, H, K, HV, V), the four addresses and the device."""
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [tokens, heads, 128]")
     bf = torch.bfloat16
     T, H, K = shape = q.shape
     _, HV, V = v.shape
-    return (T, H, K, HV, V), (_need(q, "q", bf, shape), _need(k, "k", bf, shape), _need(v, "v", bf, (T, HV, V)),
-                              _need(log_decay, "log_decay", torch.float32, (HV,)))
+    dev = _device(q)
+    return (T, H, K, HV, V), (_need(q, "q", bf, shape, dev), _need(k, "k", bf, shape, dev),
+                              _need(v, "v", bf, (T, HV, V), dev),
+                              _need(log_decay, "log_decay", torch.float32, (HV,), dev)), dev
 
 
-def _problem(dims, cu_host, cu_dev, scale, status, segments):
+def _problem(dims, cu_host, cu_dev, scale, status, segments, dev):
     """gdn_problem as bytes, the array it points at (to be kept alive), and N."""
     T, H, K, HV, V = dims
     cu = cu_host
@@ -77,20 +95,22 @@ def _problem(dims, cu_host, cu_dev, scale, status, segments):
     if N < 1 or cu[N] != T:
         raise ValueError("cu_host must end with the number of tokens, %d" % T)
     return _PROBLEM.pack(N, T, H, HV, K, V, scale or 0.0, 0, cu.__array_interface__["data"][0],
-                         _need(cu_dev, "cu_dev", torch.int32, (N + 1,)), _status(status) or 0, segments), cu, N
+                         _need(cu_dev, "cu_dev", torch.int32, (N + 1,), dev), _status(status, dev) or 0, segments), cu, N
 
 
-def _call(fn, name, problem, mode, args, workspace, q):
+def _call(fn, name, problem, mode, args, workspace, dev):
     """fn(problem, *args, workspace, bytes, stream): without a workspace first, which most short
     calls do not need."""
-    stream = _raw_stream(q.get_device())
+    stream = _raw_stream(dev)
     if workspace is None:
         st = fn(problem, *args, None, 0, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
     else:
-        st = fn(problem, *args, workspace.data_ptr(), workspace.numel(), stream)
+        st = fn(problem, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream)
     if st == GDN_ERR_WORKSPACE_TOO_SMALL:
         n = binding._lib.gdn_linear_attn_workspace_bytes(problem, mode)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         st = fn(problem, *args, workspace.data_ptr(), n, stream)
     if st != GDN_OK:
         raise GdnError(st, name)
@@ -104,14 +124,14 @@ def linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=None, initial_sta
     int32 sequence boundaries on the host and on the device; states fp32 [N, HV, K, V].
     scan_segment_chunks: the problem field of that name, in chunks of 128 tokens."""
     L = _ready()
-    dims, inputs = _inputs(q, k, v, log_decay)
-    p, keep, N = _problem(dims, cu_host, cu_dev, scale, device_status, scan_segment_chunks)
+    dims, inputs, dev = _inputs(q, k, v, log_decay)
+    p, keep, N = _problem(dims, cu_host, cu_dev, scale, device_status, scan_segment_chunks, dev)
     shape = (N, dims[3], 128, 128)
-    h0 = _maybe(initial_state, "initial_state", torch.float32, shape)
+    h0 = _maybe(initial_state, "initial_state", torch.float32, shape, dev)
     o = torch.empty_like(v)
     ht = torch.empty(shape, dtype=torch.float32, device=q.device) if output_final_state else None
     _call(L.gdn_linear_attn_fwd, "gdn_linear_attn_fwd", p, 0,
-          (*inputs, h0, o.data_ptr(), None if ht is None else ht.data_ptr()), workspace, q)
+          (*inputs, h0, o.data_ptr(), None if ht is None else ht.data_ptr()), workspace, dev)
     return o, ht
 
 
@@ -121,15 +141,15 @@ def linear_attn_prefill_paged(q, k, v, log_decay, cu_host, cu_dev, state_pool, s
     """gdn_linear_attn_prefill_paged on torch tensors (state_pool updated in place; slots and
     status words as in chunk_prefill_paged).  Returns o."""
     L = _ready()
-    dims, inputs = _inputs(q, k, v, log_decay)
-    p, keep, N = _problem(dims, cu_host, cu_dev, scale, problem_status, scan_segment_chunks)
+    dims, inputs, dev = _inputs(q, k, v, log_decay)
+    p, keep, N = _problem(dims, cu_host, cu_dev, scale, problem_status, scan_segment_chunks, dev)
     slots = state_pool.shape[0]
-    pool = _need(state_pool, "state_pool", torch.float32, (slots, dims[3], 128, 128))
-    idx = _need(state_indices, "state_indices", torch.int32, (N,))
-    resume = _maybe(has_initial_state, "has_initial_state", torch.int32, (N,))
+    pool = _need(state_pool, "state_pool", torch.float32, (slots, dims[3], 128, 128), dev)
+    idx = _need(state_indices, "state_indices", torch.int32, (N,), dev)
+    resume = _maybe(has_initial_state, "has_initial_state", torch.int32, (N,), dev)
     o = torch.empty_like(v)
     _call(L.gdn_linear_attn_prefill_paged, "gdn_linear_attn_prefill_paged", p, 0,
-          (*inputs, pool, slots, idx, resume, o.data_ptr(), _status(device_status)), workspace, q)
+          (*inputs, pool, slots, idx, resume, o.data_ptr(), _status(device_status, dev)), workspace, dev)
     return o
 
 
@@ -138,17 +158,17 @@ def linear_attn_bwd(q, k, v, log_decay, d_o, cu_host, cu_dev, scale=None, initia
                     scan_segment_chunks=0):
     """gdn_linear_attn_bwd on torch tensors.  Returns dict dq, dk, dv, dh0."""
     L = _ready()
-    dims, inputs = _inputs(q, k, v, log_decay)
-    p, keep, N = _problem(dims, cu_host, cu_dev, scale, device_status, scan_segment_chunks)
+    dims, inputs, dev = _inputs(q, k, v, log_decay)
+    p, keep, N = _problem(dims, cu_host, cu_dev, scale, device_status, scan_segment_chunks, dev)
     shape = (N, dims[3], 128, 128)
-    do = _need(d_o, "d_o", torch.bfloat16, v.shape)
-    h0 = _maybe(initial_state, "initial_state", torch.float32, shape)
-    dht = _maybe(d_final_state, "d_final_state", torch.float32, shape)
+    do = _need(d_o, "d_o", torch.bfloat16, v.shape, dev)
+    h0 = _maybe(initial_state, "initial_state", torch.float32, shape, dev)
+    dht = _maybe(d_final_state, "d_final_state", torch.float32, shape, dev)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dh0 = torch.empty(shape, dtype=torch.float32, device=q.device) if want_dh0 else None
     _call(L.gdn_linear_attn_bwd, "gdn_linear_attn_bwd", p, 1,
           (*inputs, h0, do, dht, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if dh0 is None else dh0.data_ptr()),
-          workspace, q)
+          workspace, dev)
     return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
 
 
@@ -156,13 +176,13 @@ def linear_attn_step(q, k, v, log_decay, state_pool, state_indices, scale=None, 
     """gdn_linear_attn_step on torch tensors (state_pool updated in place): row b is one token of
     the sequence in slot state_indices[b].  Returns o."""
     L = _ready()
-    (B, H, K, HV, V), (qp, kp, vp, gp) = _inputs(q, k, v, log_decay)
+    (B, H, K, HV, V), (qp, kp, vp, gp), dev = _inputs(q, k, v, log_decay)
     slots = state_pool.shape[0]
-    pool = _need(state_pool, "state_pool", torch.float32, (slots, HV, V, K))
-    idx = _need(state_indices, "state_indices", torch.int32, (B,))
+    pool = _need(state_pool, "state_pool", torch.float32, (slots, HV, V, K), dev)
+    idx = _need(state_indices, "state_indices", torch.int32, (B,), dev)
     o = torch.empty_like(v)
     st = L.gdn_linear_attn_step(B, H, HV, K, V, scale or 0.0, qp, kp, vp, gp, pool, slots, idx, o.data_ptr(),
-                                _status(device_status), _raw_stream(q.get_device()))
+                                _status(device_status, dev), _raw_stream(dev))
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_attn_step")
     return o
@@ -190,21 +210,22 @@ def rope(q, k, positions, freq, layout="half", mscale=1.0, backward=False, inpla
     bf = torch.bfloat16
     T, Hq, D = q.shape
     pairs = freq.shape[1]
-    qp = qo = _need(q, "q", bf, (T, Hq, D))
+    dev = _device(q)
+    qp = qo = _need(q, "q", bf, (T, Hq, D), dev)
     kp = ko = None
     Hk, qt, kt = 0, q, k
     if k is not None:
         Hk = k.shape[1]
-        kp = ko = _need(k, "k", bf, (T, Hk, D))
+        kp = ko = _need(k, "k", bf, (T, Hk, D), dev)
+    pos, turns = _need(positions, "positions", torch.int32, (T,), dev), _need(freq, "freq", torch.float32, (2, pairs), dev)
     if not inplace:
         qt = torch.empty_like(q)
         qo = qt.data_ptr()
         if k is not None:
             kt = torch.empty_like(k)
             ko = kt.data_ptr()
-    st = L.gdn_rope(T, Hq, Hk, D, 2 * pairs, _ROPE_LAYOUT[layout], 1 if backward else 0, mscale, qp, kp,
-                    _need(positions, "positions", torch.int32, (T,)), _need(freq, "freq", torch.float32, (2, pairs)),
-                    qo, ko, _raw_stream(q.get_device()))
+    st = L.gdn_rope(T, Hq, Hk, D, 2 * pairs, _ROPE_LAYOUT[layout], 1 if backward else 0, mscale, qp, kp, pos, turns,
+                    qo, ko, _raw_stream(dev))
     if st != GDN_OK:
         raise GdnError(st, "gdn_rope")
     return qt, kt

@@ -4,9 +4,10 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import chunked_gated_delta_06_gb300 as gdn
-from chunked_gated_delta_06_gb300 import binding, build
+from chunked_gated_delta_06_gb300 import binding, build, linear
 
 import linear_reference as ref
 
@@ -160,3 +161,74 @@ def test_rope_frequencies(rot):
         == binding.GDN_ERR_INVALID_ARG
     assert gdn.gdn_rope_frequencies(4, 1e4, 3, 1.0, 0.0, 1.0, 32.0, (ctypes.c_float * 4)()) \
         == binding.GDN_ERR_INVALID_ARG
+
+
+class _Elsewhere:
+    """What the calls look at of a CUDA tensor, with a device of its own; nothing is launched."""
+
+    def __init__(self, dtype, shape, device=0):
+        self.dtype, self.shape, self.device, self.is_cuda = dtype, torch.Size(shape), device, device >= 0
+
+    def get_device(self):
+        return self.device
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def element_size(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+def _calls():
+    """Every call's tensors by argument name."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    cu = np.array([0, 6], np.int32)
+    seq = dict(q=(bf, (6, 2, 128)), k=(bf, (6, 2, 128)), v=(bf, (6, 4, 128)), log_decay=(f32, (4,)),
+               cu_dev=(i32, (2,)), device_status=(i32, (1,)))
+    state = (f32, (1, 4, 128, 128))
+    pool = dict(state_pool=(f32, (3, 4, 128, 128)), state_indices=(i32, (1,)))
+    step = {n: seq[n] for n in ("q", "k", "v", "log_decay", "device_status")}
+    yield gdn.linear_attn_fwd, dict(seq, initial_state=state, workspace=(torch.uint8, (64,))), dict(cu_host=cu)
+    yield gdn.linear_attn_bwd, dict(seq, d_o=(bf, (6, 4, 128)), initial_state=state, d_final_state=state,
+                                    workspace=(torch.uint8, (64,))), dict(cu_host=cu)
+    yield gdn.linear_attn_prefill_paged, dict(seq, **pool, has_initial_state=(i32, (1,)), problem_status=(i32, (1,)),
+                                              workspace=(torch.uint8, (64,))), dict(cu_host=cu)
+    yield gdn.linear_attn_step, dict(step, state_pool=(f32, (3, 4, 128, 128)), state_indices=(i32, (6,))), {}
+    yield gdn.rope, dict(q=(bf, (6, 2, 128)), k=(bf, (6, 2, 128)), positions=(i32, (6,)), freq=(f32, (2, 32))), {}
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    class Refused(Exception):
+        pass
+
+    class Library:
+        def __getattr__(self, name):
+            def launch(*args):
+                raise Refused(name)
+            return launch
+
+    linear._ready()
+    monkeypatch.setattr(binding, "_lib", Library())
+    monkeypatch.setattr(linear, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(linear, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(torch, "empty_like", lambda t: t)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: _Elsewhere(torch.float32, a[0]))
+    for call, tensors, rest in _calls():
+        with pytest.raises(Refused):   # all on the current device: the call goes through
+            call(**{n: _Elsewhere(*x) for n, x in tensors.items()}, **rest)
+        for other in tensors:
+            for device in (1, -1):
+                with pytest.raises((ValueError, TypeError), match="device|CUDA"):
+                    call(**{n: _Elsewhere(*x, device=device if n == other else 0) for n, x in tensors.items()},
+                         **rest)
+        with pytest.raises(ValueError, match="device"):   # all of them on one that is not current
+            call(**{n: _Elsewhere(*x, device=1) for n, x in tensors.items()}, **rest)

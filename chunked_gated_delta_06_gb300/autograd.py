@@ -14,6 +14,29 @@ import numpy as np
 from . import binding, linear
 
 
+def _final(name, grads, inputs):
+    """The gradients of a fused backward, which are not differentiable themselves: where the caller
+    records a graph of them (create_graph), differentiating it raises instead of taking them for
+    constants.  inputs: what they depend on."""
+    import torch
+    inputs = [x for x in inputs if x is not None and x.requires_grad]
+    if not torch.is_grad_enabled() or not inputs:
+        return grads
+
+    class Final(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, count, *tensors):
+            return tensors[:count]
+
+        @staticmethod
+        def backward(ctx, *unused):
+            raise RuntimeError("the gradients of %s cannot be differentiated once more" % name)
+
+    there = [x for x in grads if x is not None]
+    marked = iter(Final.apply(len(there), *there, *inputs))
+    return tuple(None if x is None else next(marked) for x in grads)
+
+
 def _function():
     import torch
 
@@ -40,8 +63,9 @@ def _function():
             gr = binding.chunk_bwd(ctx.gdn, q, k, v, g, beta, d_o.to(torch.bfloat16).contiguous(),
                                    d_final_state=None if d_ht is None else d_ht.float().contiguous(),
                                    initial_state=h0, want_dh0=ctx.has_h0)
-            return (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dbeta"], gr["dh0"], None, None, None,
-                    None, None)
+            grads = _final("chunk_gated_delta_rule", [gr[n] for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")],
+                           (q, k, v, g, beta, h0, d_o, d_ht))
+            return (*grads, None, None, None, None, None)
 
     return ChunkGatedDeltaRule
 
@@ -104,7 +128,9 @@ def _linear_function():
                                          scale=ctx.scale, initial_state=h0,
                                          d_final_state=None if d_ht is None else d_ht.float().contiguous(),
                                          want_dh0=h0 is not None)
-            return gr["dq"], gr["dk"], gr["dv"], None, gr["dh0"], None, None, None, None
+            dq, dk, dv, dh0 = _final("linear_attention", [gr[n] for n in ("dq", "dk", "dv", "dh0")],
+                                     (q, k, v, h0, d_o, d_ht))
+            return dq, dk, dv, None, dh0, None, None, None, None
 
     return LinearAttention
 
@@ -114,18 +140,18 @@ def _rotary_function():
 
     class Rotary(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, q, k, positions, freq, layout, mscale):
-            ctx.args = (layout, mscale)
+        def forward(ctx, q, k, positions, freq, layout, mscale, transposed):
+            ctx.args = (layout, mscale, transposed)
             ctx.save_for_backward(positions, freq)
-            return linear.rope(q, k, positions, freq, layout=layout, mscale=mscale)
+            return linear.rope(q, k, positions, freq, layout=layout, mscale=mscale, backward=transposed)
 
         @staticmethod
         def backward(ctx, dq, dk):
-            positions, freq = ctx.saved_tensors
-            layout, mscale = ctx.args
-            dq, dk = linear.rope(dq.contiguous(), dk.contiguous(), positions, freq, layout=layout,
-                                  mscale=mscale, backward=True)
-            return dq, dk, None, None, None, None
+            # the other direction of the same operator, so that it has a gradient of its own
+            layout, mscale, transposed = ctx.args
+            dq, dk = Rotary.apply(dq.contiguous(), dk.contiguous(), *ctx.saved_tensors, layout, mscale,
+                                  not transposed)
+            return dq, dk, None, None, None, None, None
 
     return Rotary
 
@@ -138,7 +164,8 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
     """Differentiable linear attention with a decay for each head, in the call shape of
     chunk_gated_delta_rule: o (and the final state [N, HV, K, V] when output_final_state).
 
-    log_decay: fp32 [HV], <= 0, a constant of the layer: asking for its gradient is refused."""
+    log_decay: fp32 [HV], <= 0, a constant of the layer: asking for its gradient is refused, as is
+    differentiating the gradients once more."""
     global _LINEAR
     if log_decay.requires_grad:
         raise ValueError("log_decay has no gradient: pass it detached")
@@ -163,8 +190,8 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
 
 
 def rotary(q, k, positions, freq, layout="half", mscale=1.0):
-    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (linear.rope)."""
+    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (linear.rope), to any order."""
     global _ROTARY
     if _ROTARY is None:
         _ROTARY = _rotary_function()
-    return _ROTARY.apply(q.contiguous(), k.contiguous(), positions, freq, layout, mscale)
+    return _ROTARY.apply(q.contiguous(), k.contiguous(), positions, freq, layout, mscale, False)

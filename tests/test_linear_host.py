@@ -232,3 +232,46 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                          **rest)
         with pytest.raises(ValueError, match="device"):   # all of them on one that is not current
             call(**{n: _Elsewhere(*x, device=1) for n, x in tensors.items()}, **rest)
+
+
+def _torch_rope(q, k, positions, freq, layout="half", mscale=1.0, backward=False, inplace=False):
+    """gdn.rope in torch operations (half layout), as opaque to autograd as the kernel."""
+    def turn(x):
+        a = 2 * np.pi * positions.double()[:, None] * freq.double().sum(0)
+        c, s = (mscale * f(a)[:, None].to(x.dtype) for f in (torch.cos, torch.sin))
+        half = freq.shape[1]
+        one, two, rest = x[..., :half], x[..., half:2 * half], x[..., 2 * half:]
+        s = -s if backward else s
+        return torch.cat([one * c - two * s, two * c + one * s, rest], -1)
+    with torch.no_grad():
+        return turn(q), None if k is None else turn(k)
+
+
+def test_rotary_has_a_second_derivative(monkeypatch):
+    # a penalty on a gradient that passed the rotation keeps its own gradient
+    monkeypatch.setattr(linear, "rope", _torch_rope)
+    rng = torch.Generator().manual_seed(1)
+    q, k = (torch.randn(5, h, 8, generator=rng, dtype=torch.float64, requires_grad=True) for h in (2, 1))
+    pos, freq = torch.arange(5, dtype=torch.int32), torch.rand(2, 3, generator=rng)
+    assert torch.autograd.gradcheck(lambda x, y: gdn.rotary(x, y, pos, freq, mscale=1.25), (q, k))
+    assert torch.autograd.gradgradcheck(lambda x, y: gdn.rotary(x, y, pos, freq, mscale=1.25), (q, k))
+
+
+@pytest.mark.parametrize("which", ["linear_attention", "chunk_gated_delta_rule"])
+def test_second_derivatives_that_do_not_exist_are_refused(monkeypatch, which):
+    # the gradients of a fused backward are not differentiable: a loss on them must not lose its term
+    x = torch.randn(4, 1, 128, requires_grad=True)
+    zeros = {n: torch.zeros(4, 1, 128) for n in ("dq", "dk", "dv")}
+    if which == "linear_attention":
+        monkeypatch.setattr(linear, "linear_attn_fwd", lambda *a, **kw: (a[2] * 2.0, None))
+        monkeypatch.setattr(linear, "linear_attn_bwd", lambda *a, **kw: dict(zeros, dh0=None))
+        o, _ = gdn.linear_attention(x, x, x, torch.zeros(1), cu_seqlens=torch.tensor([0, 4]))
+    else:
+        monkeypatch.setattr(binding, "chunk_fwd", lambda *a, **kw: (a[2] * 2.0, None, None))
+        monkeypatch.setattr(binding, "chunk_bwd", lambda *a, **kw: dict(zeros, dg=torch.zeros(4, 1),
+                                                                        dbeta=torch.zeros(4, 1), dh0=None))
+        g = torch.zeros(4, 1, requires_grad=True)
+        o, _ = gdn.chunk_gated_delta_rule(x, x, x, g, g, cu_seqlens=torch.tensor([0, 4]))
+    (dx,) = torch.autograd.grad(o.float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once more"):
+        (dx.square().sum() + o.sum()).backward()

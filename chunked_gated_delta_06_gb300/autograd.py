@@ -190,8 +190,11 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
 
 
 def rotary(q, k, positions, freq, layout="half", mscale=1.0):
-    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (linear.rope), to any order."""
+    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (linear.rope), to any order.
+    freq is a constant of the model: asking for its gradient is refused."""
     global _ROTARY
+    if freq.requires_grad:
+        raise ValueError("freq has no gradient: pass it detached")
     if _ROTARY is None:
         _ROTARY = _rotary_function()
     return _ROTARY.apply(q.contiguous(), k.contiguous(), positions, freq, layout, mscale, False)

@@ -275,3 +275,10 @@ def test_second_derivatives_that_do_not_exist_are_refused(monkeypatch, which):
     (dx,) = torch.autograd.grad(o.float().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once more"):
         (dx.square().sum() + o.sum()).backward()
+
+
+def test_rotary_refuses_a_gradient_of_the_frequencies(monkeypatch):
+    monkeypatch.setattr(linear, "rope", _torch_rope)
+    q = torch.randn(5, 2, 8, requires_grad=True)
+    with pytest.raises(ValueError, match="freq"):
+        gdn.rotary(q, q, torch.arange(5, dtype=torch.int32), torch.rand(2, 3, requires_grad=True))

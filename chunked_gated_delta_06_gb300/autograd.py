@@ -149,8 +149,8 @@ def _rotary_function():
         def backward(ctx, dq, dk):
             # the other direction of the same operator, so that it has a gradient of its own
             layout, mscale, transposed = ctx.args
-            dq, dk = Rotary.apply(dq.contiguous(), dk.contiguous(), *ctx.saved_tensors, layout, mscale,
-                                  not transposed)
+            dq, dk = Rotary.apply(dq.contiguous(), None if dk is None else dk.contiguous(), *ctx.saved_tensors,
+                                  layout, mscale, not transposed)
             return dq, dk, None, None, None, None, None
 
     return Rotary
@@ -190,11 +190,12 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
 
 
 def rotary(q, k, positions, freq, layout="half", mscale=1.0):
-    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] (linear.rope), to any order.
-    freq is a constant of the model: asking for its gradient is refused."""
+    """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] or None (linear.rope), to
+    any order.  freq is a constant of the model: asking for its gradient is refused."""
     global _ROTARY
     if freq.requires_grad:
         raise ValueError("freq has no gradient: pass it detached")
     if _ROTARY is None:
         _ROTARY = _rotary_function()
-    return _ROTARY.apply(q.contiguous(), k.contiguous(), positions, freq, layout, mscale, False)
+    return _ROTARY.apply(q.contiguous(), None if k is None else k.contiguous(), positions, freq, layout, mscale,
+                         False)

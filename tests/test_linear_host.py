@@ -282,3 +282,14 @@ def test_rotary_refuses_a_gradient_of_the_frequencies(monkeypatch):
     q = torch.randn(5, 2, 8, requires_grad=True)
     with pytest.raises(ValueError, match="freq"):
         gdn.rotary(q, q, torch.arange(5, dtype=torch.int32), torch.rand(2, 3, requires_grad=True))
+
+
+def test_rotary_without_k(monkeypatch):
+    monkeypatch.setattr(linear, "rope", _torch_rope)
+    q = torch.randn(5, 2, 8, requires_grad=True)
+    pos, freq = torch.arange(5, dtype=torch.int32), torch.rand(2, 3)
+    y, none = gdn.rotary(q, None, pos, freq)
+    both, _ = gdn.rotary(q, q, pos, freq)
+    assert none is None and torch.equal(y, both)
+    (dq,) = torch.autograd.grad(y, q, torch.ones_like(y))
+    assert torch.equal(dq, _torch_rope(torch.ones_like(y), None, pos, freq, backward=True)[0])

@@ -193,7 +193,8 @@ def rotary(q, k, positions, freq, layout="half", mscale=1.0):
     """Differentiable rotary positions of q [T, Hq, D] and k [T, Hk, D] or None (linear.rope), to
     any order.  freq is a constant of the model: asking for its gradient is refused."""
     global _ROTARY
-    if freq.requires_grad:
+    import torch
+    if freq.requires_grad and torch.is_grad_enabled():
         raise ValueError("freq has no gradient: pass it detached")
     if _ROTARY is None:
         _ROTARY = _rotary_function()

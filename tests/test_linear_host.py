@@ -282,6 +282,8 @@ def test_rotary_refuses_a_gradient_of_the_frequencies(monkeypatch):
     q = torch.randn(5, 2, 8, requires_grad=True)
     with pytest.raises(ValueError, match="freq"):
         gdn.rotary(q, q, torch.arange(5, dtype=torch.int32), torch.rand(2, 3, requires_grad=True))
+    with torch.no_grad():
+        gdn.rotary(q, q, torch.arange(5, dtype=torch.int32), torch.rand(2, 3, requires_grad=True))
 
 
 def test_rotary_without_k(monkeypatch):

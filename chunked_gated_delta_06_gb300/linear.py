@@ -205,7 +205,8 @@ def rope(q, k, positions, freq, layout="half", mscale=1.0, backward=False, inpla
     """gdn_rope on torch tensors: q [T, Hq, D] and k [T, Hk, D] (or None) bf16, positions int32
     [T], freq as rope_frequencies returns it (2 * freq.shape[1] elements of each head turn).
     backward: the gradient (the rotation by the negative angle, the same mscale).  Returns
-    (q, k) rotated, new tensors unless inplace."""
+    (q, k) rotated, new tensors unless inplace.  No gradient is recorded (rotary does that): in
+    place, tensors that ask for one are refused."""
     L = _ready()
     bf = torch.bfloat16
     T, Hq, D = q.shape
@@ -218,7 +219,10 @@ def rope(q, k, positions, freq, layout="half", mscale=1.0, backward=False, inpla
         Hk = k.shape[1]
         kp = ko = _need(k, "k", bf, (T, Hk, D), dev)
     pos, turns = _need(positions, "positions", torch.int32, (T,), dev), _need(freq, "freq", torch.float32, (2, pairs), dev)
-    if not inplace:
+    if inplace:
+        if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+            raise ValueError("rope in place has no gradient: use rotary, or no_grad")
+    else:
         qt = torch.empty_like(q)
         qo = qt.data_ptr()
         if k is not None:
@@ -228,4 +232,8 @@ def rope(q, k, positions, freq, layout="half", mscale=1.0, backward=False, inpla
                     qo, ko, _raw_stream(dev))
     if st != GDN_OK:
         raise GdnError(st, "gdn_rope")
+    if inplace:   # written through their addresses: tell autograd
+        for t in (q, k):
+            if t is not None and not t.is_inference():
+                torch.autograd.graph.increment_version(t)
     return qt, kt

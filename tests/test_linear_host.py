@@ -295,3 +295,36 @@ def test_rotary_without_k(monkeypatch):
     assert none is None and torch.equal(y, both)
     (dq,) = torch.autograd.grad(y, q, torch.ones_like(y))
     assert torch.equal(dq, _torch_rope(torch.ones_like(y), None, pos, freq, backward=True)[0])
+
+
+def test_rope_in_place_shows_itself_to_autograd(monkeypatch):
+    class Library:
+        def gdn_rope(self, *args):
+            return binding.GDN_OK
+
+    linear._ready()
+    monkeypatch.setattr(binding, "_lib", Library())
+    monkeypatch.setattr(linear, "_device", lambda q: -1)   # host tensors stand in; nothing is launched
+    monkeypatch.setattr(linear, "_raw_stream", lambda device: 0)
+    q, k = (torch.zeros(3, h, 8, dtype=torch.bfloat16) for h in (2, 1))
+    pos, freq = torch.zeros(3, dtype=torch.int32), torch.zeros(2, 4)
+    before = q._version, k._version
+    gdn.rope(q, k, pos, freq)
+    assert (q._version, k._version) == before
+    gdn.rope(q, k, pos, freq, inplace=True)
+    assert q._version > before[0] and k._version > before[1]
+    # a tensor that a graph has saved cannot change unseen
+    w = torch.ones(8, dtype=torch.bfloat16, requires_grad=True)
+    loss = (q * w).sum()
+    gdn.rope(q, None, pos, freq, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # nor one whose gradient is asked for, unless none is recorded
+    x = q.clone().requires_grad_()
+    for args in ((x, None), (q, k.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="gradient"):
+            gdn.rope(*args, pos, freq, inplace=True)
+        with torch.no_grad():
+            gdn.rope(*args, pos, freq, inplace=True)
+    with torch.inference_mode():
+        gdn.rope(torch.zeros(3, 2, 8, dtype=torch.bfloat16), None, pos, freq, inplace=True)

@@ -113,19 +113,19 @@ def _linear_function():
         @staticmethod
         def forward(ctx, q, k, v, log_decay, initial_state, cu_host, cu_dev, scale, output_final_state):
             ctx.set_materialize_grads(False)
-            ctx.cu, ctx.scale = (cu_host, cu_dev), scale
-            ctx.save_for_backward(q, k, v, log_decay, initial_state)
+            ctx.cu_host, ctx.scale = cu_host.copy(), scale   # (the caller may reuse its buffer)
+            ctx.save_for_backward(q, k, v, log_decay, initial_state, cu_dev)
             return linear.linear_attn_fwd(q, k, v, log_decay, cu_host, cu_dev, scale=scale,
                                            initial_state=initial_state,
                                            output_final_state=output_final_state)
 
         @staticmethod
         def backward(ctx, d_o, d_ht):
-            q, k, v, log_decay, h0 = ctx.saved_tensors
+            q, k, v, log_decay, h0, cu_dev = ctx.saved_tensors
             if d_o is None:
                 d_o = torch.zeros_like(v)
-            gr = linear.linear_attn_bwd(q, k, v, log_decay, d_o.to(torch.bfloat16).contiguous(), *ctx.cu,
-                                         scale=ctx.scale, initial_state=h0,
+            gr = linear.linear_attn_bwd(q, k, v, log_decay, d_o.to(torch.bfloat16).contiguous(), ctx.cu_host,
+                                         cu_dev, scale=ctx.scale, initial_state=h0,
                                          d_final_state=None if d_ht is None else d_ht.float().contiguous(),
                                          want_dh0=h0 is not None)
             dq, dk, dv, dh0 = _final("linear_attention", [gr[n] for n in ("dq", "dk", "dv", "dh0")],

@@ -328,3 +328,22 @@ def test_rope_in_place_shows_itself_to_autograd(monkeypatch):
             gdn.rope(*args, pos, freq, inplace=True)
     with torch.inference_mode():
         gdn.rope(torch.zeros(3, 2, 8, dtype=torch.bfloat16), None, pos, freq, inplace=True)
+
+
+def test_offsets_changed_before_the_backward(monkeypatch):
+    # a loop that reuses its offset buffers: the backward has the forward's host copy, and a device
+    # copy that changed in place is an error
+    seen = []
+    monkeypatch.setattr(linear, "linear_attn_fwd", lambda *a, **kw: (a[2] * 2.0, None))
+    monkeypatch.setattr(linear, "linear_attn_bwd", lambda q, k, v, g, do, cu, cu_dev, **kw: (
+        seen.append(cu.copy()), dict(dq=q * 0, dk=k * 0, dv=v * 0, dh0=None))[1])
+    x = torch.randn(4, 1, 128, requires_grad=True)
+    host, dev = torch.tensor([0, 1, 4], dtype=torch.int32), torch.tensor([0, 1, 4], dtype=torch.int32)
+    o, _ = gdn.linear_attention(x, x, x, torch.zeros(1), cu_seqlens=dev, cu_seqlens_cpu=host)
+    host[1] = 3
+    o.float().sum().backward()
+    assert seen[0].tolist() == [0, 1, 4]
+    o, _ = gdn.linear_attention(x, x, x, torch.zeros(1), cu_seqlens=dev, cu_seqlens_cpu=host)
+    dev[1] = 3
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.float().sum().backward()

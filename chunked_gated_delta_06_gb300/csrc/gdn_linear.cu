@@ -17,7 +17,9 @@ __global__ void k_linear_heads(const __grid_constant__ LinearArgs a, int H) {
     if (i >= (size_t)a.T * H * (kDim / 4)) return;
     const size_t row = i / (kDim / 4), d = i % (kDim / 4) * 4;
     const float *src = p.part + row * r * kDim + d;
-    if (!in_range(src - p.part, (long long)(r - 1) * kDim + 4, (long long)a.T * p.no * kDim, a.status)) return;
+    if (!in_range(src - p.part, (long long)(r - 1) * kDim + 4, (long long)a.T * p.no * kDim, a.status) ||
+        !in_range(row * kDim + d, 4, (long long)a.T * H * kDim, a.status))
+        return;
     float4 x = *reinterpret_cast<const float4 *>(src);
     for (int j = 1; j < r; ++j) {
         const float4 y = *reinterpret_cast<const float4 *>(src + (size_t)j * kDim);
@@ -55,6 +57,11 @@ __global__ void __launch_bounds__(kStepWarps * 32)
         return;
     }
     const int h = hv / (HV / H), r0 = warp * kStepRows;
+    if (!in_range(((long long)slot * HV + hv) * kDim * kDim, kDim * kDim, (long long)num_slots * HV * kDim * kDim,
+                  status) ||
+        !in_range(((long long)b * H + h) * kDim, kDim, (long long)(gridDim.x / HV) * H * kDim, status) ||
+        !in_range(orow - o, kDim, (long long)gridDim.x * kDim, status))   // (v's rows too)
+        return;
     float *S = pool + ((size_t)slot * HV + hv) * kDim * kDim;
     float4 s[kStepRows];
 #pragma unroll

@@ -665,35 +665,38 @@ __device__ __forceinline__ void scan(const LinearArgs &a, const LinearPass &ps, 
         regs_up<kRegsState>();
         const int x0 = warp - kGroupP - kGroupW;
         const int r = (warp & 3) * 32 + lane, col = (x0 >> 2) * 64;  // row of S and of O; columns
-        const size_t state = ((size_t)n * a.HV + hv) * kDim * kDim;
-        const float *src = ps.s0 ? ps.s0 + state : nullptr;
-        float *dst = ps.s1 ? ps.s1 + state : nullptr;
+        // state x of `of`, or none where the checked build finds it outside
+        auto state_of = [&](float *base, long long x, long long of) {
+            const bool in = base && in_range((x * a.HV + hv) * kDim * kDim, kDim * kDim, of * a.HV * kDim * kDim, a.status);
+            return in ? base + ((size_t)x * a.HV + hv) * kDim * kDim : nullptr;
+        };
+        const float *src = state_of(const_cast<float *>(ps.s0), n, a.N);
+        float *dst = state_of(ps.s1, n, a.N);
         if (a.pool) {
             const int slot = a.pool_idx[n];
             if (slot >= a.num_slots && r == 0 && a.pool_status) *a.pool_status = 1;
             if (slot > 0 && slot < a.num_slots) {
-                dst = a.pool + ((size_t)slot * a.HV + hv) * kDim * kDim;
+                dst = state_of(a.pool, slot, a.num_slots);
                 src = (!a.pool_resume || a.pool_resume[n]) ? dst : nullptr;
             }
         }
         float *keep_start = nullptr;
         bool src_rows = ps.rows, dst_rows = ps.rows;   // row r contiguous, or column c
         if (nseg > 1) {   // inner states of a split sequence: after segment k in record `first + k`
-            float *rec = ps.seg_state + ((size_t)item * a.HV + hv) * kDim * kDim;
             if (seg > 0) {
-                src = kState ? nullptr : rec - (size_t)a.HV * kDim * kDim;
+                src = kState ? nullptr : state_of(ps.seg_state, item - 1, a.items);
                 src_rows = ps.seg_rows;
             }
             // a pool slot is written by its last segment's CTA, perhaps before the first one's
             // starts: the state pass keeps the start state in the last record, which is free
-            float *kept = rec + (size_t)(nseg - 1) * a.HV * kDim * kDim;
+            float *kept = seg == 0 && a.pool ? state_of(ps.seg_state, item + nseg - 1, a.items) : nullptr;
             if (seg == 0 && a.pool && !kState) {
                 src = kept;
                 src_rows = ps.seg_rows;
             }
-            keep_start = seg == 0 && a.pool && kState ? kept : nullptr;
+            keep_start = kState ? kept : nullptr;
             if (kState) {
-                dst = rec;
+                dst = state_of(ps.seg_state, item, a.items);
                 dst_rows = ps.seg_rows;
             } else if (seg < nseg - 1) {
                 dst = nullptr;
@@ -1057,6 +1060,9 @@ __global__ void __launch_bounds__(256) k_linear_stitch(const __grid_constant__ L
     const float fh = lam.hi, fl = lam.lo;
     const size_t step4 = (size_t)a.HV * kDim * kDim / 4;
     float *rec = a.pass[blockIdx.z % a.state_passes * 2].seg_state;
+    if (!in_range(((long long)first * a.HV + hv) * kDim * kDim, ((long long)(nseg - 2) * a.HV + 1) * kDim * kDim,
+                  (long long)a.items * a.HV * kDim * kDim, a.status))
+        return;
     float4 *p = reinterpret_cast<float4 *>(rec + ((size_t)first * a.HV + hv) * kDim * kDim) +
                 blockIdx.x * 256 + threadIdx.x;
     float4 y = *p;

@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a, int tokens)
         const bool is_q = h < a.Hq;
         const size_t row = is_q ? ((size_t)(t0 + t) * a.Hq + h) * a.D
                                 : ((size_t)(t0 + t) * a.Hk + (h - a.Hq)) * a.D;
+        if (!in_range(row, a.D, (long long)a.T * (is_q ? a.Hq : a.Hk) * a.D, nullptr)) continue;
         const bf16 *src = (is_q ? a.q : a.k) + row;
         bf16 *dst = (is_q ? a.qo : a.ko) + row;
         const bool turned = j * V < half;

@@ -7,6 +7,7 @@ the library says that the call needs one.
 """
 from __future__ import annotations
 
+import ctypes
 import struct
 
 import numpy as np
@@ -14,7 +15,15 @@ import numpy as np
 from . import binding
 from .binding import GDN_ERR_WORKSPACE_TOO_SMALL, GDN_OK, GdnError
 
-_PROBLEM = struct.Struct("@iqiiiifiPPPi4x")   # gdn_problem
+
+
+def _struct_of(layout):
+    """A ctypes structure's fields, in their order, to be packed in one go."""
+    codes = "".join(t._type_ if isinstance(t._type_, str) else "P" for _, t in layout._fields_)
+    return struct.Struct("@%s%dx" % (codes, ctypes.sizeof(layout) - struct.calcsize("@" + codes)))
+
+
+_PROBLEM = _struct_of(binding.GdnProblem)
 _ROPE_SCALING = {"none": binding.GDN_ROPE_SCALE_NONE, "linear": binding.GDN_ROPE_SCALE_LINEAR,
                  "parts": binding.GDN_ROPE_SCALE_PARTS}
 _ROPE_LAYOUT = {"half": binding.GDN_ROPE_HALF, "interleaved": binding.GDN_ROPE_INTERLEAVED}
@@ -94,6 +103,7 @@ def _problem(dims, cu_host, cu_dev, scale, status, segments, dev):
     N = len(cu) - 1
     if N < 1 or cu[N] != T:
         raise ValueError("cu_host must end with the number of tokens, %d" % T)
+    # (in the order of GdnProblem)
     return _PROBLEM.pack(N, T, H, HV, K, V, scale or 0.0, 0, cu.__array_interface__["data"][0],
                          _need(cu_dev, "cu_dev", torch.int32, (N + 1,), dev), _status(status, dev) or 0, segments), cu, N
 

@@ -347,3 +347,21 @@ def test_offsets_changed_before_the_backward(monkeypatch):
     dev[1] = 3
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         o.float().sum().backward()
+
+
+def test_packed_problem_is_the_structure(monkeypatch):
+    linear._ready()
+    cu = np.array([0, 2, 6], np.int32)
+    tensors = [_Elsewhere(torch.int32, (3,)), _Elsewhere(torch.int32, (1,))]
+    tensors[1].data_ptr = lambda: FAKE + 4
+    raw, keep, N = linear._problem((6, 2, 128, 4, 128), cu, tensors[0], 0.5, tensors[1], 7, 0)
+    p = binding.GdnProblem.from_buffer_copy(raw)
+    assert len(raw) == ctypes.sizeof(binding.GdnProblem) and N == 2 and keep is cu
+    got = {n: getattr(p, n) for n, _ in binding.GdnProblem._fields_ if n != "cu_seqlens_host"}
+    assert got == dict(num_seqs=2, total_tokens=6, num_k_heads=2, num_v_heads=4, head_dim_k=128, head_dim_v=128,
+                       scale=0.5, beta_dtype=0, cu_seqlens_dev=FAKE, device_status=FAKE + 4, scan_segment_chunks=7)
+    assert ctypes.addressof(p.cu_seqlens_host.contents) == cu.ctypes.data
+    # a further field would change the format, and the packing would raise
+    class Longer(ctypes.Structure):
+        _fields_ = binding.GdnProblem._fields_ + [("more", ctypes.c_int32)]
+    assert linear._struct_of(Longer).format != linear._PROBLEM.format

@@ -111,7 +111,7 @@ cudaError_t launch_width(const RopeArgs &a, cudaStream_t s) {
     const int units = (a.Hq + a.Hk) * (a.D / (2 * V)), places = 8 * 152;
     const int tokens = std::max(1, std::min({4, 4 * kThreads / units, a.T / places}));
     const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);
-    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
+    const unsigned grid = ((unsigned)a.T + tokens - 1) / tokens;   // (T < 2^31)
     if (a.interleaved) k_rope<V, true><<<grid, kThreads, smem, s>>>(a, tokens);
     else k_rope<V, false><<<grid, kThreads, smem, s>>>(a, tokens);
     return cudaGetLastError();

@@ -97,3 +97,17 @@ def test_no_tokens_and_refusals():
         gdn.rope(q, k, pos, torch.zeros(2, 65, device="cuda"))
     with pytest.raises(KeyError):
         gdn.rope(q, k, pos, freq, layout="other")
+
+
+def test_the_most_tokens():
+    # 2^31 - 1 tokens of one pair: the number of blocks does not pass 32 bits on its way (17 GB)
+    T = 2 ** 31 - 1
+    q = torch.empty(T, 1, 2, device="cuda", dtype=torch.bfloat16)
+    pos = torch.empty(T, device="cuda", dtype=torch.int32)
+    freq = gdn.rope_frequencies(2)
+    rows = torch.tensor([0, 1, 2 ** 30 + 1, T - 2, T - 1], device="cuda")
+    q[rows] = torch.randn(5, 1, 2, device="cuda").to(torch.bfloat16)
+    pos[rows] = torch.tensor([3, 70000, -5, 11, 2 ** 31 - 1], device="cuda", dtype=torch.int32)
+    x = q[rows]
+    gdn.rope(q, None, pos, freq, inplace=True)
+    _check(x, q[rows], pos[rows], freq, "half")

@@ -493,7 +493,7 @@ LinearPlan plan_linear(const gdn_problem *p, const Dims &d, int backward) {
             work2 += c + k * start;
             items += k;
         }
-        if (items == d.N || items * d.HV > 16384) continue;  // 1 GiB of states at most
+        if (items == d.N || items * d.HV > 16384) continue;  // 1 GiB of states each way at most
         const double cost = launch_cost(state * seg + start, (backward ? 2.0 : 1.0) * work1) +
                             launch_cost(one * seg + start, all * work2) + 2.0;
         if (cost < t) {

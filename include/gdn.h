@@ -321,10 +321,22 @@ gdn_status gdn_decode_step_gated(int32_t batch, int32_t num_k_heads, int32_t num
  * The packing, the layouts, the conventions and the checks are those of the
  * chunk calls above: gdn_problem describes the pack (beta_dtype must be valid but
  * is not used; scan_segment_chunks plans the scans as above, in chunks of 128
- * tokens: 0 = the library's plan, -1 = never split, L > 0 = segments of L),
- * device_status collects GDN_DEVICE_* bits, T == 0 passes the state through.  Within a chunk of tokens
- * a NaN or infinity of one token may reach earlier tokens of the same sequence
- * (its products are masked by zeros); it never reaches another sequence.
+ * tokens: 0 = the library's plan, -1 = never split, L > 0 = segments of L, and
+ * no split where segments x HV would pass 16384 or N passes 128), device_status
+ * collects GDN_DEVICE_* bits, T == 0 passes the state through.
+ * What a sequence's values depend on beside its own inputs: a call whose
+ * sequences all have at most 128 tokens carries more bits through its products,
+ * and a plan's segments come from the whole pack.  The same sequence in another
+ * pack may so give values that differ by their rounding; the same call gives the
+ * same bits every time.
+ * Infinities and NaN never reach another sequence or another key head's results.
+ * An infinite element of a state stays infinite for as long as
+ * e^log_decay is not 0 in fp32.  An infinite element of q, k, v or d_o makes what
+ * the recurrence makes of it not finite, but NaN where that has an infinity (the
+ * products come in parts, some of them zero), and within a chunk of 128 tokens
+ * that may reach the same feature of tokens on its other side too (their products
+ * are masked by zeros).  A pass over split sequences leaves out tokens whose weight
+ * at a segment's end is below 2^-150, their infinities and NaN included.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of scratch of gdn_linear_attn_fwd and gdn_linear_attn_prefill_paged

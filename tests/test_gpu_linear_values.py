@@ -144,3 +144,20 @@ def test_device_offsets_of_many_sequences(lens, wrong):
     c.cu_dev.copy_(right)
     again = c.fwd(), c.bwd()
     assert torch.equal(good[0][0], again[0][0]) and all(torch.equal(good[1][n], again[1][n]) for n in again[1])
+
+
+# An infinite token: its feature of the outputs from there on and of the state is not finite, the
+# other features, the tokens of earlier chunks and the other sequences keep their values.
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("g", [0.0, -0.02])
+def test_infinite_token_stays_in_its_feature(bad, g):
+    c = Case([300, 40], 1, 2, seed=0)
+    c.g.fill_(g)
+    (ro, rh), (mo, mh) = c.ref_fwd()
+    c.v[150, 1, 9] = bad
+    o, ht = (_f64(x) for x in c.fwd())
+    assert not np.isfinite(o[150:300, 1, 9]).any() and not np.isfinite(ht[0, 1, :, 9]).any()
+    for got, want, bound, hit in ((o, ro, ref.out_bound(ro, mo), np.s_[128:300, 1, 9]),
+                                  (ht, rh, ref.state_bound(mh), np.s_[0, 1, :, 9])):
+        got[hit] = want[hit]
+        assert np.all(np.abs(got - want) <= bound)

@@ -45,11 +45,12 @@
 // below, 396 instead of 352 us for the backward of 4 x 4096 tokens.)  A pair's exchange takes
 // some 3000 cycles: the epilogue reads its own half and frees O before it waits for the other
 // (backward 352 -> 342 us).  The partial sums cross in fp32, stored straight into the peer's tile:
-// in fp16 with a power of two for 32 columns the backward took 3 % less (359 instead of 368 us in
-// turns), but columns far below the largest, or beside an infinity, were lost.
+// in fp16 with a power of two for 32 columns the backward took as long (322 us alone after a flush,
+// now 316; among other passes, at the clock that the load leaves, 328 and 337), and columns far below
+// the largest, or beside an infinity, were lost.
 //
-// What bounds it (4 x 4096 tokens, 16 / 32 heads: 105 us, 3.8 TB/s or 0.56 of the measured copy
-// rate): the steps of a chunk that wait on each other.  A chunk takes 5300 cycles, of which the
+// What bounds it (4 x 4096 tokens, 16 / 32 heads: 106 us among other passes, with the states 3.9 TB/s
+// or 0.58 of the measured copy rate): the steps of a chunk that wait on each other.  A chunk takes 5300 cycles, of which the
 // tensor pipe works for 3584 (QK 8 products of 64 cycles, O 16, KV 32).  Over two chunks O(c - 1)
 // frees the buffer for KV(c), whose end frees it for P(c + 1), from which P~ and then O(c + 1)
 // follow; each hand-over crosses tensor memory, and every step shares the SM's one data path with

@@ -10,9 +10,9 @@
 // turn reaches sincospif.  An fp32 angle would be off by 2^-24 pos radians instead.
 //
 // Bound by HBM: every element is read and written once, the cosines and sines of a token are formed
-// once for all of its heads.  32768 tokens of 16 + 16 heads take 84 us, 6.4 TB/s or 0.94 of the
-// measured copy rate; the gradient of 16384 tokens of 32 + 4 heads of 256, 94 us, 0.95 of it.  256
-// tokens take 3 us on the GPU, which the launch hides.
+// once for all of its heads.  Among other passes, 32768 tokens of 16 + 16 heads take 84 us, 6.4 TB/s
+// or 0.94 of the measured copy rate; the gradient of 16384 tokens of 32 + 4 heads of 256, 94 us, 0.95
+// of it.  256 tokens take 3 us on the GPU, which the launch hides.
 #include <algorithm>
 
 #include "gdn_linear.h"
@@ -105,9 +105,10 @@ __global__ void __launch_bounds__(kThreads) k_rope(const RopeArgs a, int tokens)
 template <int V>
 cudaError_t launch_width(const RopeArgs &a, cudaStream_t s) {
     // Up to four tokens a block, for about four units a thread, once every SM has blocks for its
-    // eight places all the same (32768 tokens of 32 heads of 128: 97 us with one, 87 with four;
-    // 16384 tokens of 36 heads of 256, nine units a thread with four: 97 and 101).  A decoding
-    // step keeps one, to spread over the SMs (256 tokens: 9 us, 11 with four).
+    // eight places all the same (one call alone, by events, its launch included: 32768 tokens of 32
+    // heads of 128, 97 us with one, 87 with four; 16384 tokens of 36 heads of 256, nine units a thread
+    // with four, 97 and 101).  A decoding step keeps one, to spread over the SMs (256 tokens: 9 us, 11
+    // with four).
     const int units = (a.Hq + a.Hk) * (a.D / (2 * V)), places = 8 * 152;
     const int tokens = std::max(1, std::min({4, 4 * kThreads / units, a.T / places}));
     const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);

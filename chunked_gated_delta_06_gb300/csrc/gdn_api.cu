@@ -535,6 +535,7 @@ struct Span {
         const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(x.at);
         return at && x.at && bytes && x.bytes && a < b + x.bytes && b < a + bytes;
     }
+    bool same(const Span &x) const { return at == x.at && bytes == x.bytes; }
 };
 
 gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan,
@@ -605,7 +606,22 @@ gdn_status linear_fwd_impl(const gdn_problem *p, const void *q, const void *k, c
     LinearWs ws;
     const LinearPlan plan = plan_linear(p, d, 0);
     if ((int64_t)plan.items * d.HV > 0x7fffffffLL / 3) return GDN_ERR_INVALID_ARG;
-    if ((st = check_linear_ws(carve_linear(d, plan, 0, workspace, &ws), workspace, ws_size)) != GDN_OK) return st;
+    const size_t need = carve_linear(d, plan, 0, workspace, &ws);
+    if ((st = check_linear_ws(need, workspace, ws_size)) != GDN_OK) return st;
+    // Sequences, value heads and segments are walked at once: what one of them writes, no other may
+    // touch.  (o as one of q, k, v itself is fine: a CTA has read a chunk of its head when it writes it.)
+    const size_t tokens = (size_t)d.T * gdn::kDim * sizeof(bf16);
+    const size_t state = (size_t)d.HV * gdn::kDim * gdn::kDim * sizeof(float), each = d.N * sizeof(int32_t);
+    const Span spans[] = {{o, tokens * d.HV}, {final_state, state * d.N}, {pg ? pg->pool : nullptr, pg ? state * pg->num_slots : 0},
+                          {workspace, need}, {q, tokens * d.H}, {k, tokens * d.H}, {v, tokens * d.HV},
+                          {initial_state, state * d.N}, {log_decay, d.HV * sizeof(float)},
+                          {p->cu_seqlens_dev, each + sizeof(int32_t)}, {p->device_status, sizeof(int32_t)},
+                          {pg ? pg->indices : nullptr, each}, {pg ? pg->resume : nullptr, each},
+                          {pg ? pg->status : nullptr, sizeof(int32_t)}};
+    for (int i = 0; i < 4; ++i)
+        for (size_t j = i + 1; j < sizeof(spans) / sizeof(spans[0]); ++j)
+            if (spans[i].meets(spans[j]) && !(i == 0 && j >= 4 && j <= 6 && spans[i].same(spans[j])))
+                return GDN_ERR_INVALID_ARG;
     gdn::LinearArgs a = linear_args(d, p, plan, log_decay);
     a.passes = a.state_passes = 1;
     gdn::LinearPass &x = a.pass[0];

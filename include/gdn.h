@@ -351,7 +351,8 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_problem *p, int for_backward);
  *   initial_state  fp32 [N, HV, 128(K), 128(V)], or NULL for zeros
  *   o              bf16 [T, HV, 128] (out)
  *   final_state    fp32 [N, HV, 128, 128] (out), or NULL; not initial_state
- *                  (outputs must not overlap inputs or one another)
+ *                  (outputs and workspace must overlap neither inputs nor
+ *                  one another: GDN_ERR_INVALID_ARG)
  *   workspace      ws_bytes >= gdn_linear_attn_workspace_bytes(p, 0), 256-byte
  *                  aligned; or NULL with ws_bytes 0, which is enough where the
  *                  plan needs none (GDN_ERR_WORKSPACE_TOO_SMALL where it does) */

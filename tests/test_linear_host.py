@@ -119,6 +119,35 @@ def test_backward_outputs_over_inputs_are_refused():
                 assert got == binding.GDN_ERR_INVALID_ARG, (out, other, hex(place))
 
 
+@pytest.mark.parametrize("H", [2, 4])
+def test_forward_outputs_over_inputs_are_refused(H):
+    # o, the final state and the pool over anything else in part, or over a tensor of another shape:
+    # value heads and sequences are walked at once.  (o as one of q, k, v itself is read before it is written.)
+    p, keep = _problem([0, 5, 9], H=H)
+    fwd = ["q", "k", "v", "g", "h0", "o", "ht", "ws"]
+    paged = ["q", "k", "v", "g", "pool", "idx", "resume", "o", "status", "ws"]
+    heads = dict(q=H, k=H, v=4, o=4)
+    size = {n: 9 * heads[n] * 256 if n in heads else 2 * 4 * 65536 for n in fwd}
+    size.update(g=16, pool=3 * 4 * 65536, idx=8, resume=8, status=4)
+    for names, outs in ((fwd, ("o", "ht")), (paged, ("o", "pool"))):
+        at = {n: 0x10000000 * (i + 1) for i, n in enumerate(names)}
+        for out in outs:
+            for other in names:
+                if other in (out, "ws"):
+                    continue
+                for shift in (0, (size[other] - 1) // 16 * 16, 16 - size[out]):
+                    if shift == 0 and out == "o" and other in heads and size[other] == size["o"]:
+                        continue
+                    a = dict(at)
+                    a[out] = at[other] + shift
+                    if names is fwd:
+                        got = gdn.gdn_linear_attn_fwd(p, *(a[n] for n in names), 1 << 20, None)
+                    else:
+                        args = [a[n] for n in names]
+                        got = gdn.gdn_linear_attn_prefill_paged(p, *args[:5], 3, *args[5:], 1 << 20, None)
+                    assert got == binding.GDN_ERR_INVALID_ARG, (out, other, shift)
+
+
 def test_step_arguments():
     def call(batch=4, H=2, HV=4, K=128, pool=FAKE, slots=8, idx=FAKE, g=FAKE, q=FAKE):
         return gdn.gdn_linear_attn_step(batch, H, HV, K, 128, 0.0, q, FAKE, FAKE, g, pool, slots, idx, FAKE,

@@ -330,8 +330,8 @@ gdn_status gdn_decode_step_gated(int32_t batch, int32_t num_k_heads, int32_t num
  * pack may so give values that differ by their rounding; the same call gives the
  * same bits every time.
  * Infinities and NaN never reach another sequence or another key head's results.
- * An infinite element of a state stays infinite for as long as
- * e^log_decay is not 0 in fp32.  An infinite element of q, k, v or d_o makes what
+ * An infinite element of a state stays infinite for as long as e^log_decay is not
+ * 0 in fp32 (outputs that read it are infinite or NaN).  An infinite element of q, k, v or d_o makes what
  * the recurrence makes of it not finite, but NaN where that has an infinity (the
  * products come in parts, some of them zero), and within a chunk of 128 tokens
  * that may reach the same feature of tokens on its other side too (their products

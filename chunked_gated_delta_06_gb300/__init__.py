@@ -23,4 +23,8 @@ from .binding import (GDN_DTYPE_BF16, GDN_DTYPE_F32, GdnError, GdnProblem,  # no
                       gdn_rope_frequencies)
 from .linear import (linear_attn_bwd, linear_attn_fwd, linear_attn_prefill_paged,  # noqa: F401
                      linear_attn_step, rope, rope_frequencies)
-from .autograd import chunk_gated_delta_rule, linear_attention, rotary  # noqa: E402,F401
+from .mixer import (rms_norm_bwd, rms_norm_fwd, selective_scan_bwd, selective_scan_fwd,  # noqa: F401
+                    selective_scan_prefill_paged, selective_scan_step, short_conv_bwd, short_conv_fwd,
+                    short_conv_prefill_paged, short_conv_step)
+from .autograd import (chunk_gated_delta_rule, linear_attention, rms_norm, rotary,  # noqa: E402,F401
+                       selective_scan, short_conv)

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import binding, linear
+from . import binding, linear, mixer
 
 
 def _final(name, grads, inputs):
@@ -200,3 +200,151 @@ def rotary(q, k, positions, freq, layout="half", mscale=1.0):
         _ROTARY = _rotary_function()
     return _ROTARY.apply(q.contiguous(), None if k is None else k.contiguous(), positions, freq, layout, mscale,
                          False)
+
+
+def _mixer_functions():
+    import torch
+
+    class ShortConv(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, initial_state, cu_host, cu_dev, activation, output_final_state):
+            ctx.set_materialize_grads(False)
+            ctx.cu_host, ctx.activation = cu_host.copy(), activation
+            ctx.save_for_backward(x, weight, bias, initial_state, cu_dev)
+            return mixer.short_conv_fwd(x, weight, cu_host, cu_dev, bias=bias, activation=activation,
+                                        initial_state=initial_state, output_final_state=output_final_state)
+
+        @staticmethod
+        def backward(ctx, dy, dht):
+            x, weight, bias, h0, cu_dev = ctx.saved_tensors
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy
+            gr = mixer.short_conv_bwd(x, weight, dy.contiguous(), ctx.cu_host, cu_dev, bias=bias,
+                                      activation=ctx.activation, initial_state=h0,
+                                      d_final_state=None if dht is None else dht.contiguous(), want_dh0=h0 is not None)
+            grads = _final("short_conv", [gr[n] for n in ("dx", "dw", "dbias", "dh0")],
+                           (x, weight, bias, h0, dy, dht))
+            return (*grads, None, None, None, None)
+
+    class SelectiveScan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, dt, A_log, B, C, D, z, dt_bias, initial_state, cu_host, cu_dev, output_final_state):
+            ctx.set_materialize_grads(False)
+            ctx.cu_host = cu_host.copy()
+            ctx.save_for_backward(x, dt, A_log, B, C, D, z, dt_bias, initial_state, cu_dev)
+            return mixer.selective_scan_fwd(x, dt, A_log, B, C, cu_host, cu_dev, D=D, z=z, dt_bias=dt_bias,
+                                            initial_state=initial_state, output_final_state=output_final_state)
+
+        @staticmethod
+        def backward(ctx, dy, dht):
+            *inputs, cu_dev = ctx.saved_tensors
+            x, dt, A_log, B, C, D, z, dt_bias, h0 = inputs
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy
+            gr = mixer.selective_scan_bwd(x, dt, A_log, B, C, dy.contiguous(), ctx.cu_host, cu_dev, D=D, z=z,
+                                          dt_bias=dt_bias, initial_state=h0,
+                                          d_final_state=None if dht is None else dht.contiguous(),
+                                          want_dh0=h0 is not None)
+            names = ("dx", "ddt", "dA_log", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
+            grads = _final("selective_scan", [gr[n] for n in names], (*inputs, dy, dht))
+            return (*grads, None, None, None)
+
+    class RmsNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, z, residual, scale, gate, eps, offset):
+            ctx.set_materialize_grads(False)
+            y, h = mixer.rms_norm_fwd(x, weight, z=z, residual=residual, scale=scale, gate=gate, eps=eps, offset=offset)
+            ctx.args, ctx.kind = dict(gate=gate, eps=eps, offset=offset, residual=residual is not None), x.dtype
+            ctx.save_for_backward(x if h is None else h, weight, z, scale, x if scale is not None else None)
+            return y, h
+
+        @staticmethod
+        def backward(ctx, dy, dh):
+            h, weight, z, scale, x = ctx.saved_tensors
+            dy = torch.zeros(h.shape, dtype=ctx.kind, device=h.device) if dy is None else dy
+            gr = mixer.rms_norm_bwd(h, weight, dy.contiguous(), z=z, dh=None if dh is None else dh.contiguous(),
+                                    scale=scale, x=x, **ctx.args)
+            grads = _final("rms_norm", [gr[n] for n in ("dx", "dweight", "dz", "dresidual", "dscale")],
+                           (h, weight, z, scale, x, dy, dh))
+            return (*grads, None, None, None)
+
+    return ShortConv, SelectiveScan, RmsNorm
+
+
+_MIXER = None
+
+
+def _mixer(which):
+    global _MIXER
+    if _MIXER is None:
+        _MIXER = _mixer_functions()
+    return _MIXER[which]
+
+
+def _dense_rows(t):
+    """t, or a copy of it whose rows are dense."""
+    if t is None or t.is_contiguous():
+        return t
+    width = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != width:
+            return t.contiguous()
+        width *= n
+    return t if t.stride(0) >= width else t.contiguous()
+
+
+def _offsets(T, device, cu_seqlens, cu_seqlens_cpu):
+    import torch
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=device)
+        cu_seqlens_cpu = np.array([0, T], dtype=np.int32)
+    if cu_seqlens_cpu is None:
+        cu_seqlens_cpu = cu_seqlens.cpu()
+    cu_host = np.asarray(cu_seqlens_cpu.cpu() if hasattr(cu_seqlens_cpu, "cpu") else cu_seqlens_cpu, dtype=np.int32)
+    return cu_host, cu_seqlens.to(torch.int32).contiguous()
+
+
+def _one_batch(*tensors):
+    if tensors[0].shape[0] != 1:
+        raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
+    return [None if t is None else t[0] for t in tensors]
+
+
+def _float(t):
+    return None if t is None else t.float().contiguous()
+
+
+def short_conv(x, weight, bias=None, activation="silu", initial_state=None, output_final_state=False,
+               cu_seqlens=None, cu_seqlens_cpu=None):
+    """Differentiable short causal convolution of packed sequences: y like x (and the final state [N, C,
+    W - 1] when output_final_state).  x: [T, C] or [1, T, C], bf16 or fp32, rows may lie apart; weight [C, W]
+    and bias [C] of any floating type (computed with in fp32); activation: "silu" or None."""
+    batched = x.dim() == 3
+    if batched:
+        (x,) = _one_batch(x)
+    cu_host, cu_dev = _offsets(x.shape[0], x.device, cu_seqlens, cu_seqlens_cpu)
+    y, ht = _mixer(0).apply(_dense_rows(x), _float(weight), _float(bias), initial_state, cu_host, cu_dev, activation,
+                            output_final_state)
+    return (y.unsqueeze(0) if batched else y), ht
+
+
+def selective_scan(x, dt, A_log, B, C, D=None, z=None, dt_bias=None, initial_state=None, output_final_state=False,
+                   cu_seqlens=None, cu_seqlens_cpu=None):
+    """Differentiable selective state space scan of packed sequences: y like x (and the final state fp32
+    [N, channels, state_dim] when output_final_state).  x, dt, z: [T, channels] or [1, T, channels]; B, C:
+    [.., T, groups, state_dim]; rows may lie apart; A_log [channels, state_dim], D and dt_bias [channels] of
+    any floating type (computed with in fp32)."""
+    batched = x.dim() == 3
+    if batched:
+        x, dt, B, C, z = _one_batch(x, dt, B, C, z)
+    cu_host, cu_dev = _offsets(x.shape[0], x.device, cu_seqlens, cu_seqlens_cpu)
+    y, ht = _mixer(1).apply(_dense_rows(x), _dense_rows(dt), _float(A_log), _dense_rows(B), _dense_rows(C), _float(D),
+                            _dense_rows(z), _float(dt_bias), initial_state, cu_host, cu_dev, output_final_state)
+    return (y.unsqueeze(0) if batched else y), ht
+
+
+def rms_norm(x, weight, z=None, residual=None, scale=None, gate="silu", eps=1e-6, offset=0.0):
+    """Differentiable norm of rows with its gate and residual: y = h / rms(h) (offset + weight) act(z), with
+    h = residual + scale x returned as well, (y, h), where there is a residual.  x, z, residual: [..., dim];
+    weight and scale [dim] of any floating type (computed with in fp32)."""
+    dense = lambda t: None if t is None else t.contiguous()  # noqa: E731
+    y, h = _mixer(2).apply(dense(x), _float(weight), dense(z), dense(residual), _float(scale), gate, eps, offset)
+    return y if residual is None else (y, h)

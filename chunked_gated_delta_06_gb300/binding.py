@@ -25,6 +25,9 @@ GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE_TOO_SMALL, G
 GDN_DTYPE_BF16, GDN_DTYPE_F32 = 0, 1
 GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 GDN_ROPE_SCALE_NONE, GDN_ROPE_SCALE_LINEAR, GDN_ROPE_SCALE_PARTS = 0, 1, 2
+GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
+GDN_NO_RESIDUAL = -1
+GDN_GATE_NONE, GDN_GATE_SILU, GDN_GATE_SIGMOID = 0, 1, 2
 GDN_DEVICE_CU_SEQLENS_MISMATCH, GDN_DEVICE_WAIT_TIMEOUT, GDN_DEVICE_INDEX_OUT_OF_RANGE = 1, 2, 4
 
 
@@ -58,6 +61,31 @@ class GdnProblem(ctypes.Structure):
         ("cu_seqlens_dev", ctypes.c_void_p),
         ("device_status", ctypes.c_void_p),
         ("scan_segment_chunks", ctypes.c_int32),
+    ]
+
+
+class GdnPack(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64),
+        ("cu_seqlens_host", ctypes.POINTER(ctypes.c_int32)),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p),
+    ]
+
+
+class GdnScanShape(ctypes.Structure):
+    _fields_ = [
+        ("channels", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("state_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("dt_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64),
+        ("b_stride", ctypes.c_int64),
+        ("c_stride", ctypes.c_int64),
+        ("segment_tokens", ctypes.c_int32),
     ]
 
 
@@ -146,6 +174,26 @@ def load_library(path):
     L.gdn_rope_frequencies.restype = ctypes.c_int
     L.gdn_rope.argtypes = [ctypes.c_int64] + [i32] * 6 + [f32] + [_vp] * 7
     L.gdn_rope.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    conv = [i32] * 4 + [_vp, i64, _vp, _vp]   # channels, width, activation, dtype, x, x_stride, weight, bias
+    L.gdn_short_conv_fwd.argtypes = [_vp] + conv + [_vp] * 4
+    L.gdn_short_conv_prefill_paged.argtypes = [_vp] + conv + [_vp, i32] + [_vp] * 5
+    L.gdn_short_conv_workspace_bytes.argtypes = [_vp, i32, i32]
+    L.gdn_short_conv_bwd.argtypes = [_vp] + conv + [_vp] * 8 + [_sz, _vp]
+    L.gdn_short_conv_step.argtypes = [i32] + conv + [_vp, i32] + [_vp] * 4
+    L.gdn_selective_scan_workspace_bytes.argtypes = [_vp, _vp, ctypes.c_int]
+    L.gdn_selective_scan_fwd.argtypes = [_vp] * 14 + [_sz, _vp]
+    L.gdn_selective_scan_prefill_paged.argtypes = [_vp] * 11 + [i32] + [_vp] * 5 + [_sz, _vp]
+    L.gdn_selective_scan_bwd.argtypes = [_vp] * 23 + [_sz, _vp]
+    L.gdn_selective_scan_step.argtypes = [i32] + [_vp] * 10 + [i32] + [_vp] * 4
+    norm = [i64] + [i32] * 4 + [f32, f32]     # rows, dim, dtype, residual_dtype, gate, eps, offset
+    L.gdn_rms_norm_fwd.argtypes = norm + [_vp] * 8
+    L.gdn_rms_norm_workspace_bytes.argtypes = [i64] + [i32] * 3
+    L.gdn_rms_norm_bwd.argtypes = norm + [_vp] * 13 + [_sz, _vp]
+    for name in ("short_conv", "selective_scan", "rms_norm"):
+        getattr(L, "gdn_%s_workspace_bytes" % name).restype = _sz
+        for form in ("fwd", "prefill_paged", "bwd", "step") if name != "rms_norm" else ("fwd", "bwd"):
+            getattr(L, "gdn_%s_%s" % (name, form)).restype = ctypes.c_int
     L.gdn_check_indices.argtypes = [_vp, ctypes.c_int32, ctypes.c_int32, _vp]
     L.gdn_check_indices.restype = ctypes.c_int
     L.gdn_selftest_bounded_wait.argtypes = [_vp, ctypes.c_uint64, _vp]

@@ -8,29 +8,19 @@
 #include <algorithm>
 
 #include "../../include/gdn.h"
+#include "gdn_host.h"
 #include "gdn_kernels.h"
 #include "gdn_linear.h"
 
 namespace {
 
+using gdn::aligned16;
+using gdn::aligned_to;
 using gdn::bf16;
-constexpr size_t kAlign = 256;
-
-// Sequential sub-allocator over a caller buffer; with base == nullptr it only counts.
-struct Carver {
-    char *base;
-    size_t off = 0;
-    explicit Carver(void *b) : base(static_cast<char *>(b)) {}
-    template <typename T>
-    T *take(size_t count) {
-        off = (off + kAlign - 1) / kAlign * kAlign;
-        T *p = base ? reinterpret_cast<T *>(base + off) : nullptr;
-        off += count * sizeof(T);
-        return p;
-    }
-    size_t used() const { return (off + kAlign - 1) / kAlign * kAlign; }
-};
-
+using gdn::Carver;
+using gdn::cuda_status;
+using gdn::kAlign;
+using gdn::Span;
 struct Dims {
     int N, T, H, HV, C;  // C = chunk count
     int longest;         // chunks of the longest sequence
@@ -106,9 +96,6 @@ void plan_segments(const gdn_problem *p, Dims *d) {
         }
     }
 }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 gdn_status check_problem(const gdn_problem *p, Dims *d) {
     if (!p) return GDN_ERR_INVALID_ARG;
@@ -237,8 +224,6 @@ void fill_common(gdn::ChunkArgs &a, const Dims &d, const gdn_problem *p, const v
     a.cu_dev = p->cu_seqlens_dev;
     a.status = p->device_status;
 }
-
-gdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 // Fused-gating arguments of the *_gated entry points (all null otherwise).
 struct Gate {
@@ -526,17 +511,6 @@ gdn_status check_linear_ws(size_t need, const void *workspace, size_t ws_size) {
     if (!workspace || !aligned_to(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     return ws_size < (need > 0 ? need : kAlign) ? GDN_ERR_WORKSPACE_TOO_SMALL : GDN_OK;
 }
-
-// Bytes of a call's buffer.
-struct Span {
-    const void *at;
-    size_t bytes;
-    bool meets(const Span &x) const {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(x.at);
-        return at && x.at && bytes && x.bytes && a < b + x.bytes && b < a + bytes;
-    }
-    bool same(const Span &x) const { return at == x.at && bytes == x.bytes; }
-};
 
 gdn::LinearArgs linear_args(const Dims &d, const gdn_problem *p, const LinearPlan &plan,
                             const float *log_decay) {

@@ -1,0 +1,477 @@
+// gdn_scan_bwd.cu -- gradient of the selective scan (gdn_scan.cuh has the forward's formulas).
+//
+// With o_t = dy_t silu(z_t), G_t the gradient of h_t and p_t = G_t e^{d_t A} h_{t-1}:
+//   G_t = e^{d_{t+1} A} G_{t+1} + C_t o_t
+//   dC_t = sum over the group's channels of o_t h_t,      dB_t = the same of G_t d_t x_t
+//   dx_t = d_t sum_n G_t B_t + D o_t,                     dd_t = sum_n p_t A + x_t sum_n G_t B_t
+//   ddt_t = dd_t softplus'(u_t),                          dA_log = A sum_t p_t d_t
+//   dz_t = dy_t (sum_n C_t h_t + D x_t) silu'(z_t)
+//
+// A block walks its segment forward once for the states ahead of each tile (the marks, kept in
+// the workspace), then the tiles backwards: the states of a tile are formed again and wait in shared
+// memory as e^{dA} h_{t-1}, 32 bytes a thread and token, and each is replaced by the thread's
+// dC and dB as the walk back reads it, which the block then adds over its channels.
+#include "gdn_scan.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kMarkTile = 8;   // tokens of a tile
+constexpr int kEV = 4;
+
+__device__ __forceinline__ long long first_mark(const ScanArgs &a, const ScanPlace &w) {
+    // (the marks of a sequence follow n + s / tile, as the items of a scan do; a segment is whole tiles)
+    return (long long)w.n + w.s / kMarkTile + (w.b - w.s) / kMarkTile;
+}
+
+template <int TT, int CB, typename V>
+__device__ __forceinline__ void keep_inputs(const ScanPlace &w, int t, int k, int row, int col, const V &x, const V &dt,
+                                            const float *bias, float (&d)[kEV], float4 (*dd)[CB / 2]) {
+#pragma unroll
+    for (int i = 0; i < kEV; ++i)
+        d[i] = t + row < w.f && w.c0 + col + i < w.cend ? softplus_of(as_float(dt.x[i]) + bias[col + i]) : 0.f;
+    if (row >= TT) return;
+#pragma unroll
+    for (int i = 0; i < kEV; i += 2)
+        dd[row][unit_at((col + i) / 2)] = make_float4(d[i], d[i] * as_float(x.x[i]), d[i + 1], d[i + 1] * as_float(x.x[i + 1]));
+}
+
+// The gradient at the start of each segment but a sequence's first, from nothing behind it (for
+// the last segment, from the final state's gradient).
+template <typename T, int NS, bool kWide>
+__global__ void __launch_bounds__(kScanThreads) k_scan_starts(const __grid_constant__ ScanArgs a) {
+    constexpr int CB = ScanShape<NS>::CB, TT = 16;
+    using Tile = TileOf<T, CB, TT, kEV, kWide>;
+    using Rows = RowsOf<T, NS, TT, kWide>;
+    __shared__ float ds[TT][CB], os[TT][CB];
+    __shared__ float Cs[TT][NS];
+    __shared__ float bias[CB];
+    ScanPlace w;
+    if (!scan_place<NS>(a, blockIdx.x, &w) || w.seg == 0) return;
+    for (int i = threadIdx.x; i < CB; i += kScanThreads)
+        bias[i] = w.c0 + i < w.cend && a.dt_bias && in_range(w.c0 + i, 1, a.C, a.pack.status) ? a.dt_bias[w.c0 + i] : 0.f;
+    const ScanLane<NS> lane(a, w);
+    float2 g[2][2];
+    lane.load(a.ds1, a.ds1 && w.seg == w.segs - 1 ? w.n : -1, a.pack.N, a, w, g);
+    const T *dt = static_cast<const T *>(a.dt), *z = static_cast<const T *>(a.z), *dy = static_cast<const T *>(a.dy);
+    typename Tile::V dn[Tile::NV], zn[Tile::NV], on[Tile::NV];
+    typename Rows::V cn[Rows::NU];
+    auto fetch = [&](int t) {
+        Tile::load(dt, a.dts, a, w, t, w.f, dn);
+        Tile::load(dy, a.C, a, w, t, w.f, on);
+        if (z) Tile::load(z, a.zs, a, w, t, w.f, zn);
+        Rows::load(static_cast<const T *>(a.Cm), a.cs, a, w, t, w.f, cn);
+    };
+    __syncthreads();
+    const int tiles = (w.f - w.b + TT - 1) / TT;
+    if (tiles > 0) fetch(w.b + (tiles - 1) * TT);
+    for (int i = tiles - 1; i >= 0; --i) {
+        const int t = w.b + i * TT;
+#pragma unroll
+        for (int k = 0; k < Tile::NV; ++k) {
+            const int row = Tile::row(k), col = Tile::col();
+            if (row >= TT) break;
+#pragma unroll
+            for (int j = 0; j < kEV; ++j) {
+                const bool there = t + row < w.f && w.c0 + col + j < w.cend;
+                float o = as_float(on[k].x[j]);
+                if (z) {
+                    const float zj = as_float(zn[k].x[j]);
+                    o *= zj * sigmoid_of(zj);
+                }
+                ds[row][col + j] = there ? softplus_of(as_float(dn[k].x[j]) + bias[col + j]) : 0.f;
+                os[row][col + j] = there ? o : 0.f;
+            }
+        }
+        Rows::keep(cn, Cs);
+        __syncthreads();
+        if (i > 0) fetch(t - TT);
+#pragma unroll 4
+        for (int j = TT - 1; j >= 0; --j) {
+            const float2 d = *reinterpret_cast<const float2 *>(&ds[j][2 * lane.pair]);
+            const float2 o = *reinterpret_cast<const float2 *>(&os[j][2 * lane.pair]);
+            const float4 c = *reinterpret_cast<const float4 *>(&Cs[j][4 * lane.q]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float2 decay[2];
+                lane.decays(p, p ? d.y : d.x, decay);
+                const float2 op = both(p ? o.y : o.x);
+                g[p][0] = mul2(decay[0], fma2(make_float2(c.x, c.y), op, g[p][0]));
+                g[p][1] = mul2(decay[1], fma2(make_float2(c.z, c.w), op, g[p][1]));
+            }
+        }
+        __syncthreads();
+    }
+    lane.store(a.rec_g, w.item, a.pack.N + (long long)(a.pack.T / a.seg), a, w, g);
+}
+
+template <typename T, int NS, bool kWide>
+__global__ void __launch_bounds__(kScanThreads) k_scan_bwd(const __grid_constant__ ScanArgs a) {
+    constexpr int CB = ScanShape<NS>::CB, L = ScanShape<NS>::L, TT = kMarkTile, BT = L < 4 ? L : 4;
+    constexpr int kPairs = ScanShape<NS>::kPairs;
+    using Tile = TileOf<T, CB, TT, kEV, kWide>;
+    using Rows = RowsOf<T, NS, TT, kWide>;
+    extern __shared__ float4 smem[];
+    float4 (*us)[kScanThreads][2] = reinterpret_cast<float4 (*)[kScanThreads][2]>(smem);   // [TT]
+    float4 (*dd)[CB / 2] = reinterpret_cast<float4 (*)[CB / 2]>(us + TT);                   // [TT]
+    float (*os)[CB] = reinterpret_cast<float (*)[CB]>(dd + TT);                             // [TT]
+    float (*Bs)[NS] = reinterpret_cast<float (*)[NS]>(os + TT);                             // [TT]
+    float (*Cs)[NS] = Bs + TT;                                                              // [TT]
+    float *bias = reinterpret_cast<float *>(Cs + TT), *skip = bias + CB;
+
+    ScanPlace w;
+    const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
+    if (!scan_place<NS>(a, blockIdx.x, &w)) {
+        if (a.pack.status && w.item == items) check_offsets(a.pack);
+        return;
+    }
+    for (int i = threadIdx.x; i < CB; i += kScanThreads) {
+        const bool there = w.c0 + i < w.cend && in_range(w.c0 + i, 1, a.C, a.pack.status);
+        bias[i] = there && a.dt_bias ? a.dt_bias[w.c0 + i] : 0.f;
+        skip[i] = there && a.D ? a.D[w.c0 + i] : 0.f;
+    }
+    const ScanLane<NS> lane(a, w);
+    const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
+    const int tiles = (w.f - w.b + TT - 1) / TT;
+    const T *x = static_cast<const T *>(a.x), *dt = static_cast<const T *>(a.dt), *z = static_cast<const T *>(a.z);
+    const T *dy = static_cast<const T *>(a.dy), *B = static_cast<const T *>(a.B), *Cm = static_cast<const T *>(a.Cm);
+
+    // Forward: the states ahead of the tiles.
+    float2 h[2][2];
+    if (w.seg == 0) {
+        lane.load(a.s0, a.s0 ? w.n : -1, a.pack.N, a, w, h);
+    } else {
+        lane.load(a.rec_h, w.item - w.seg, items, a, w, h);
+        for (int i = w.item - w.seg + 1; i < w.item; ++i) lane.join(a, w, a.rec_h, i, h);
+    }
+    typename Tile::V xn[Tile::NV], dn[Tile::NV], zn[Tile::NV], on[Tile::NV];
+    typename Rows::V bn[Rows::NU], cn[Rows::NU];
+    auto fetch = [&](int t) {
+        Tile::load(x, a.xs, a, w, t, w.f, xn);
+        Tile::load(dt, a.dts, a, w, t, w.f, dn);
+        Rows::load(B, a.bs, a, w, t, w.f, bn);
+    };
+    auto fetch_more = [&](int t) {
+        Tile::load(dy, a.C, a, w, t, w.f, on);
+        if (z) Tile::load(z, a.zs, a, w, t, w.f, zn);
+        Rows::load(Cm, a.cs, a, w, t, w.f, cn);
+    };
+    if (tiles > 0) fetch(w.b);
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        lane.store(a.marks, mark + i, marks, a, w, h);
+        if (i == tiles - 1) break;   // (its last tile's end is nobody's start)
+        const int t = w.b + i * TT;
+#pragma unroll
+        for (int k = 0; k < Tile::NV; ++k) {
+            float d[kEV];
+            keep_inputs<TT, CB>(w, t, k, Tile::row(k), Tile::col(), xn[k], dn[k], bias, d, dd);
+        }
+        Rows::keep(bn, Bs);
+        __syncthreads();
+        fetch(t + TT);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const float4 in = dd[j][unit_at(lane.pair)];
+            const float4 b = *reinterpret_cast<const float4 *>(&Bs[j][4 * lane.q]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float2 decay[2];
+                lane.decays(p, p ? in.z : in.x, decay);
+                const float2 dx = both(p ? in.w : in.y);
+                h[p][0] = fma2(decay[0], h[p][0], mul2(dx, make_float2(b.x, b.y)));
+                h[p][1] = fma2(decay[1], h[p][1], mul2(dx, make_float2(b.z, b.w)));
+            }
+        }
+        __syncthreads();
+    }
+
+    // Backward.  g holds e^{d A} G of the token behind.
+    float2 g[2][2], dA[2][2] = {};
+    lane.load(w.segs > 1 && w.seg < w.segs - 1 ? nullptr : a.ds1, w.n, a.pack.N, a, w, g);
+    if (w.seg < w.segs - 1) {
+        const int last = w.item - w.seg + w.segs - 1;
+        lane.load(a.rec_g, last, items, a, w, g);
+        for (int i = last - 1; i > w.item; --i) lane.join(a, w, a.rec_g, i, g);
+    }
+    float dD[kEV] = {}, db[kEV] = {};
+    const float ln2 = 0.693147180559945309f;
+    if (tiles > 0) {
+        fetch(w.b + (tiles - 1) * TT);
+        fetch_more(w.b + (tiles - 1) * TT);
+    }
+    for (int i = tiles - 1; i >= 0; --i) {
+        const int t = w.b + i * TT;
+        typename Tile::V xc[Tile::NV], zc[Tile::NV], oc[Tile::NV], uc[Tile::NV];
+        float d[Tile::NV][kEV];
+#pragma unroll
+        for (int k = 0; k < Tile::NV; ++k) {
+            const int row = Tile::row(k), col = Tile::col();
+            keep_inputs<TT, CB>(w, t, k, row, col, xn[k], dn[k], bias, d[k], dd);
+            if (row < TT) {
+                float o[kEV];
+#pragma unroll
+                for (int j = 0; j < kEV; ++j) {
+                    o[j] = as_float(on[k].x[j]);
+                    if (z) {
+                        const float zj = as_float(zn[k].x[j]);
+                        o[j] *= zj * sigmoid_of(zj);
+                    }
+                }
+                *reinterpret_cast<float4 *>(&os[row][col]) = make_float4(o[0], o[1], o[2], o[3]);
+            }
+            xc[k] = xn[k];
+            uc[k] = dn[k];
+            zc[k] = zn[k];
+            oc[k] = on[k];
+        }
+        Rows::keep(bn, Bs);
+        Rows::keep(cn, Cs);
+        lane.load(a.marks, mark + i, marks, a, w, h);
+        __syncthreads();
+        if (i > 0) {
+            fetch(t - TT);
+            fetch_more(t - TT);
+        }
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const float4 in = dd[j][unit_at(lane.pair)];
+            const float4 b = *reinterpret_cast<const float4 *>(&Bs[j][4 * lane.q]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float2 decay[2];
+                lane.decays(p, p ? in.z : in.x, decay);
+                const float2 dx = both(p ? in.w : in.y);
+                const float2 u0 = mul2(decay[0], h[p][0]), u1 = mul2(decay[1], h[p][1]);
+                us[j][threadIdx.x][p ^ (threadIdx.x >> 2 & 1)] = make_float4(u0.x, u0.y, u1.x, u1.y);
+                h[p][0] = fma2(dx, make_float2(b.x, b.y), u0);
+                h[p][1] = fma2(dx, make_float2(b.z, b.w), u1);
+            }
+        }
+        float2 tileA[2][2] = {};
+#pragma unroll
+        for (int j0 = TT - BT; j0 >= 0; j0 -= BT) {
+            float part[BT][6];   // of each token: sum G B, sum p A / ln 2, sum C h of the two channels
+#pragma unroll
+            for (int jj = BT - 1; jj >= 0; --jj) {
+                const int j = j0 + jj;
+                const float4 in = dd[j][unit_at(lane.pair)];
+                const float2 o = *reinterpret_cast<const float2 *>(&os[j][2 * lane.pair]);
+                const float4 bb = *reinterpret_cast<const float4 *>(&Bs[j][4 * lane.q]);
+                const float4 cc = *reinterpret_cast<const float4 *>(&Cs[j][4 * lane.q]);
+                const float2 b[2] = {make_float2(bb.x, bb.y), make_float2(bb.z, bb.w)};
+                const float2 c[2] = {make_float2(cc.x, cc.y), make_float2(cc.z, cc.w)};
+                float2 dC[2], dB[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float dp = p ? in.z : in.x;
+                    const float2 dx = both(p ? in.w : in.y), op = both(p ? o.y : o.x);
+                    const float4 uu = us[j][threadIdx.x][p ^ (threadIdx.x >> 2 & 1)];
+                    const float2 u[2] = {make_float2(uu.x, uu.y), make_float2(uu.z, uu.w)};
+                    float2 decay[2], sB, sA, sC;
+                    lane.decays(p, dp, decay);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 hk = fma2(dx, b[k], u[k]);
+                        const float2 G = fma2(c[k], op, g[p][k]);
+                        const float2 pk = mul2(G, u[k]);
+                        dC[k] = p ? fma2(op, hk, dC[k]) : mul2(op, hk);
+                        dB[k] = p ? fma2(dx, G, dB[k]) : mul2(dx, G);
+                        sB = k ? fma2(G, b[k], sB) : mul2(G, b[k]);
+                        sA = k ? fma2(pk, lane.A[p][k], sA) : mul2(pk, lane.A[p][k]);
+                        sC = k ? fma2(c[k], hk, sC) : mul2(c[k], hk);
+                        tileA[p][k] = fma2(pk, both(dp), tileA[p][k]);
+                        g[p][k] = mul2(decay[k], G);
+                    }
+                    part[jj][p] = sB.x + sB.y;
+                    part[jj][2 + p] = sA.x + sA.y;
+                    part[jj][4 + p] = sC.x + sC.y;
+                }
+                us[j][threadIdx.x][threadIdx.x >> 2 & 1] = make_float4(dC[0].x, dC[0].y, dC[1].x, dC[1].y);
+                us[j][threadIdx.x][1 ^ (threadIdx.x >> 2 & 1)] = make_float4(dB[0].x, dB[0].y, dB[1].x, dB[1].y);
+            }
+            pair_sums<L, BT, 6>(part, lane.q);
+            // (the pair's threads, all of this warp, have read what this takes the place of)
+            __syncwarp();
+            if (lane.q < BT) {
+                dd[j0 + lane.q][unit_at(lane.pair)] = make_float4(part[0][0], part[0][2], part[0][1], part[0][3]);
+                *reinterpret_cast<float2 *>(&os[j0 + lane.q][2 * lane.pair]) = make_float2(part[0][4], part[0][5]);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) dA[p][k] = add2(dA[p][k], tileA[p][k]);
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < Tile::NV; ++k) {
+            const int row = Tile::row(k), col = Tile::col();
+            if (row >= TT) break;
+            typename Tile::V dxv, ddv, dzv;
+            float sums[kEV][2];   // sum G B, sum p A / ln 2
+#pragma unroll
+            for (int j = 0; j < kEV; j += 2) {
+                const float4 v = dd[row][unit_at((col + j) / 2)];
+                sums[j][0] = v.x;
+                sums[j][1] = v.y;
+                sums[j + 1][0] = v.z;
+                sums[j + 1][1] = v.w;
+            }
+#pragma unroll
+            for (int j = 0; j < kEV; ++j) {
+                const bool there = t + row < w.f && w.c0 + col + j < w.cend;
+                const float xj = as_float(xc[k].x[j]), dyj = as_float(oc[k].x[j]);
+                float o = dyj;
+                if (z) {
+                    const float zj = as_float(zc[k].x[j]), sig = sigmoid_of(zj);
+                    o *= zj * sig;
+                    dzv.x[j] = as_type<T>(dyj * fmaf(skip[col + j], xj, os[row][col + j]) * fmaf(zj * sig, 1.f - sig, sig));
+                }
+                dxv.x[j] = as_type<T>(fmaf(sums[j][0], d[k][j], skip[col + j] * o));
+                const float u = as_float(uc[k].x[j]) + bias[col + j];
+                const float du = fmaf(sums[j][1], ln2, sums[j][0] * xj) * sigmoid_of(u);
+                ddv.x[j] = as_type<T>(du);
+                if (there) {
+                    dD[j] = fmaf(o, xj, dD[j]);
+                    db[j] += du;
+                }
+            }
+            Tile::store(static_cast<T *>(a.dx), a, w, t, w.f, k, dxv);
+            Tile::store(static_cast<T *>(a.ddt), a, w, t, w.f, k, ddv);
+            if (z) Tile::store(static_cast<T *>(a.dz), a, w, t, w.f, k, dzv);
+        }
+        // dC and dB of the tile over the block's channels: four states of one of them a thread
+        const int blocks = (a.C / a.G + CB - 1) / CB, mine = (w.c0 - w.g * (a.C / a.G)) / CB;
+        for (int v = threadIdx.x; v < TT * L * 2; v += kScanThreads) {
+            const int j = v / (2 * L), which = v % (2 * L) / L, q = v % L;
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll 8
+            for (int p = 0; p < kPairs; ++p) {
+                const int th = p * L + q;
+                const float4 u = us[j][th][which ^ (th >> 2 & 1)];
+                s0 = add2(s0, make_float2(u.x, u.y));
+                s1 = add2(s1, make_float2(u.z, u.w));
+            }
+            if (t + j < w.f) {
+                const long long at = (((long long)mine * a.pack.T + t + j) * a.G + w.g) * 2 * NS + which * NS + 4 * q;
+                if (in_range(at, 4, (long long)blocks * a.pack.T * a.G * 2 * NS, a.pack.status))
+                    *reinterpret_cast<float4 *>(a.part_bc + at) = make_float4(s0.x, s0.y, s1.x, s1.y);
+            }
+        }
+        __syncthreads();
+    }
+    if (w.seg == 0 && a.ds0) lane.store(a.ds0, w.n, a.pack.N, a, w, g);
+    // the segment's sums for the parameters, [items, C, NS + 2]
+    const long long extent = items * a.C * (NS + 2);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const long long at = ((long long)w.item * a.C + lane.c + p) * (NS + 2) + 4 * lane.q;
+        if (lane.c + p >= w.cend || !in_range(at, 4, extent, a.pack.status)) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            a.part_c[at + 2 * k] = dA[p][k].x * lane.A[p][k].x * ln2;
+            a.part_c[at + 2 * k + 1] = dA[p][k].y * lane.A[p][k].y * ln2;
+        }
+    }
+    float (*rows)[CB][2] = reinterpret_cast<float (*)[CB][2]>(smem);   // the rows of threads, in order
+    constexpr int kRows = kScanThreads / Tile::kCols;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEV; ++j) {
+        rows[threadIdx.x / Tile::kCols][Tile::col() + j][0] = dD[j];
+        rows[threadIdx.x / Tile::kCols][Tile::col() + j][1] = db[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < CB; i += kScanThreads) {
+        float s[2] = {};
+        for (int r = 0; r < kRows; ++r) {
+            s[0] += rows[r][i][0];
+            s[1] += rows[r][i][1];
+        }
+        const long long at = ((long long)w.item * a.C + w.c0 + i) * (NS + 2) + NS;
+        if (w.c0 + i < w.cend && in_range(at, 2, extent, a.pack.status)) {
+            a.part_c[at] = s[0];
+            a.part_c[at + 1] = s[1];
+        }
+    }
+}
+
+// dB and dC: the blocks' sums in their order, rounded once.
+template <typename T, int NS>
+__global__ void __launch_bounds__(256) k_scan_bc(const __grid_constant__ ScanArgs a, int blocks) {
+    const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4, n = (long long)a.pack.T * a.G * 2 * NS;
+    if (i >= n) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int b = 0; b < blocks; ++b) {
+        const Vec<float, 4> v = load_vec<4>(a.part_bc, b * n + i, blocks * n, a.pack.status);
+        s.x += v.x[0];
+        s.y += v.x[1];
+        s.z += v.x[2];
+        s.w += v.x[3];
+    }
+    const long long row = i / (2 * NS);
+    const int k = (int)(i % (2 * NS));
+    T *out = static_cast<T *>(k < NS ? a.dC : a.dB);
+    store_vec<4>(out, row * NS + k % NS, (long long)a.pack.T * a.G * NS, a.pack.status,
+                 Vec<T, 4>{{as_type<T>(s.x), as_type<T>(s.y), as_type<T>(s.z), as_type<T>(s.w)}});
+}
+
+// dA_log, dD and ddt_bias: the segments' sums in their order (idle items have none).
+__global__ void __launch_bounds__(256) k_scan_params(const __grid_constant__ ScanArgs a) {
+    const int per = a.Ns + 2;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, n = (long long)a.C * per;
+    if (i >= n) return;
+    const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
+    float s = 0.f;
+    for (int q = 0; q < a.pack.N; ++q) {
+        const int b = offset_of(a.pack, q), e = max(b, offset_of(a.pack, q + 1));
+        const int segs = max(1, (int)(((long long)e - b + a.seg - 1) / a.seg)), first = first_item(a, q);
+#pragma unroll 4
+        for (int k = 0; k < segs; ++k)
+            if (in_range((first + k) * n + i, 1, items * n, a.pack.status)) s += a.part_c[(first + k) * n + i];
+    }
+    const int c = (int)(i / per), k = (int)(i % per);
+    if (k < a.Ns) a.dA_log[(long long)c * a.Ns + k] = s;
+    else if (k == a.Ns && a.dD) a.dD[c] = s;
+    else if (k == a.Ns + 1 && a.ddt_bias) a.ddt_bias[c] = s;
+}
+
+template <typename T, int NS, bool kWide>
+cudaError_t bwd(const ScanArgs &a, cudaStream_t s) {
+    constexpr int CB = ScanShape<NS>::CB, TT = kMarkTile;
+    constexpr size_t bytes = (size_t)TT * (kScanThreads * 32 + CB * 8 + CB * 4 + NS * 8) + CB * 8;
+    static_assert(bytes <= 48 * 1024, "no more than a kernel has without asking");
+    static_assert(kScanThreads / (CB / kEV) * CB * 8 <= TT * kScanThreads * 32, "the last sums fit the states' place");
+    const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<NS>(a);
+    if (a.seg <= a.pack.T) k_scan_starts<T, NS, kWide><<<(unsigned)blocks, kScanThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    k_scan_bwd<T, NS, kWide><<<(unsigned)(blocks + (a.pack.status ? 1 : 0)), kScanThreads, bytes, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long long units = (long long)a.pack.T * a.G * 2 * NS / 4;
+    if (units > 0) k_scan_bc<T, NS><<<(unsigned)((units + 255) / 256), 256, 0, s>>>(a, (a.C / a.G + CB - 1) / CB);
+    k_scan_params<<<(unsigned)(((long long)a.C * (NS + 2) + 255) / 256), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int NS>
+cudaError_t bwd_of(const ScanArgs &a, cudaStream_t s) {
+    return scan_wide(a, kEV) ? bwd<T, NS, true>(a, s) : bwd<T, NS, false>(a, s);
+}
+
+}  // namespace
+
+int scan_mark_tile() { return kMarkTile; }
+
+cudaError_t launch_scan_bwd(const ScanArgs &a, cudaStream_t s) {
+    if (a.seg <= a.pack.T) {
+        const cudaError_t e = launch_scan_ends(a, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.f32) return a.Ns == 8 ? bwd_of<float, 8>(a, s) : a.Ns == 16 ? bwd_of<float, 16>(a, s) : bwd_of<float, 32>(a, s);
+    return a.Ns == 8 ? bwd_of<bf16, 8>(a, s) : a.Ns == 16 ? bwd_of<bf16, 16>(a, s) : bwd_of<bf16, 32>(a, s);
+}
+
+}  // namespace gdn

@@ -439,6 +439,194 @@ gdn_status gdn_rope(int64_t total_tokens, int32_t num_q_heads, int32_t num_k_hea
                     float mscale, const void *q, const void *k, const int32_t *positions,
                     const float *freq, void *q_out, void *k_out, gdn_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * What stands around the recurrences in a layer: the short causal convolution,
+ * the selective state space scan, and norms with their gate and residual.
+ * Tensors of these calls are bf16 or fp32 as `dtype` (GDN_DTYPE_*) says; all sums,
+ * states of the scan and parameters are fp32.  Outputs and workspaces must
+ * overlap neither inputs nor one another (GDN_ERR_INVALID_ARG); tensors start on
+ * 16 bytes, indices, parameters and rows that are not dense on their element's
+ * size, workspaces on 256.  Packed calls with T == 0 pass the states through.
+ * ------------------------------------------------------------------------- */
+
+/* Packed sequences of any width.  total_tokens <= 2^31 - 65536. */
+typedef struct {
+    int32_t num_seqs;                 /* N >= 1 */
+    int64_t total_tokens;             /* T >= 0, T == cu[N] */
+    const int32_t *cu_seqlens_host;   /* host [N+1]: 0 = c0 <= c1 <= ... <= cN = T */
+    const int32_t *cu_seqlens_dev;    /* device [N+1], the same values */
+    int32_t *device_status;           /* device int32, or NULL: GDN_DEVICE_* bits */
+} gdn_pack;
+
+#define GDN_ACT_NONE 0
+#define GDN_ACT_SILU 1   /* u sigmoid(u) */
+
+/* Short causal convolution, one filter of `width` (2, 3 or 4) weights a channel:
+ *     u[t, c] = bias[c] + sum_j weight[c, j] x[t - (width - 1) + j, c],  y = act(u)
+ * Inputs ahead of a sequence come from its state, the last width - 1 inputs,
+ * oldest first ([.., channels, width - 1] in the type of x; "C6: GDN decode-step
+ * goldens and recurrent/conv state contract", State contract).
+ *   x              [T, channels], rows x_stride elements apart (>= channels)
+ *   weight, bias   fp32 [channels, width], fp32 [channels] or NULL
+ *   initial_state  [N, channels, width - 1], or NULL for zeros
+ *   y              [T, channels] (out)
+ *   final_state    [N, channels, width - 1] (out), or NULL */
+gdn_status gdn_short_conv_fwd(const gdn_pack *p, int32_t channels, int32_t width, int32_t activation,
+                              int32_t dtype, const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, const void *initial_state, void *y,
+                              void *final_state, gdn_stream_t stream);
+
+/* The forward over the slots of a pool, in place: conv_pool [num_slots, channels,
+ * width - 1]; num_slots, state_indices, has_initial_state and device_status as in
+ * gdn_chunk_prefill_paged. */
+gdn_status gdn_short_conv_prefill_paged(const gdn_pack *p, int32_t channels, int32_t width,
+                                        int32_t activation, int32_t dtype, const void *x,
+                                        int64_t x_stride, const float *weight, const float *bias,
+                                        void *conv_pool, int32_t num_slots,
+                                        const int32_t *state_indices,
+                                        const int32_t *has_initial_state, void *y,
+                                        int32_t *device_status, gdn_stream_t stream);
+
+/* Bytes of scratch of gdn_short_conv_bwd; 0 for invalid arguments. */
+size_t gdn_short_conv_workspace_bytes(const gdn_pack *p, int32_t channels, int32_t width);
+
+/* Backward, from the forward's inputs.
+ *   d_y             [T, channels]
+ *   d_final_state   [N, channels, width - 1], or NULL for zeros
+ *   dx              [T, channels] (out, dense)
+ *   dweight, dbias  fp32 [channels, width] (out), fp32 [channels] (out) or NULL
+ *   d_initial_state [N, channels, width - 1] (out), or NULL */
+gdn_status gdn_short_conv_bwd(const gdn_pack *p, int32_t channels, int32_t width, int32_t activation,
+                              int32_t dtype, const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, const void *initial_state, const void *d_y,
+                              const void *d_final_state, void *dx, float *dweight, float *dbias,
+                              void *d_initial_state, void *workspace, size_t ws_bytes,
+                              gdn_stream_t stream);
+
+/* One token per row: x, y [batch, channels], row b's state in slot
+ * state_indices[b] of conv_pool, advanced in place (slots as in gdn_decode_step). */
+gdn_status gdn_short_conv_step(int32_t batch, int32_t channels, int32_t width, int32_t activation,
+                               int32_t dtype, const void *x, int64_t x_stride, const float *weight,
+                               const float *bias, void *conv_pool, int32_t num_slots,
+                               const int32_t *state_indices, void *y, int32_t *device_status,
+                               gdn_stream_t stream);
+
+/* Selective state space scan.  Channel c belongs to group c / (channels / groups);
+ * with d = softplus(dt + dt_bias) and A = -e^{A_log}:
+ *     h_t[c, n] = e^{d_t[c] A[c, n]} h_{t-1}[c, n] + d_t[c] x_t[c] B_t[group, n]
+ *     y_t[c] = (sum_n C_t[group, n] h_t[c, n] + D[c] x_t[c]) silu(z_t[c])
+ * A call may cut long sequences into segments that are walked at once (their
+ * states joined by the segments' whole decays): by the call's sizes alone, so that
+ * the same call gives the same bits.  A state that is not finite stays so, but may
+ * turn from infinite to NaN.  Infinities and NaN reach neither another sequence
+ * nor, but through dB and dC, another channel. */
+typedef struct {
+    int32_t channels;                 /* >= 1 */
+    int32_t groups;                   /* >= 1, a divisor of channels */
+    int32_t state_dim;                /* 8, 16 or 32 */
+    int32_t dtype;                    /* of x, dt, z, B, C, y and their gradients */
+    int64_t x_stride, dt_stride, z_stride;   /* elements from token to token, 0 = dense */
+    int64_t b_stride, c_stride;
+    int32_t segment_tokens;           /* 0: the library's plan, -1: never split, L > 0:
+                                         segments of L tokens (rounded up to 32) */
+} gdn_scan_shape;
+
+/* Bytes of scratch of gdn_selective_scan_fwd and _prefill_paged (for_backward = 0;
+ * may be small) or _bwd (1); never 0 for valid arguments, 0 otherwise. */
+size_t gdn_selective_scan_workspace_bytes(const gdn_pack *p, const gdn_scan_shape *s, int for_backward);
+
+/* Forward.
+ *   x, dt, z       [T, channels]; z NULL: no gate
+ *   B, C           [T, groups, state_dim]
+ *   A_log          fp32 [channels, state_dim]
+ *   D, dt_bias     fp32 [channels], or NULL for zeros
+ *   initial_state  fp32 [N, channels, state_dim], or NULL for zeros
+ *   y              [T, channels] (out)
+ *   final_state    fp32 [N, channels, state_dim] (out), or NULL
+ *   workspace      or NULL with ws_bytes 0, which is enough for a call that is not
+ *                  split (GDN_ERR_WORKSPACE_TOO_SMALL for one that is) */
+gdn_status gdn_selective_scan_fwd(const gdn_pack *p, const gdn_scan_shape *s, const void *x,
+                                  const void *dt, const float *A_log, const void *B, const void *C,
+                                  const float *D, const void *z, const float *dt_bias,
+                                  const float *initial_state, void *y, float *final_state,
+                                  void *workspace, size_t ws_bytes, gdn_stream_t stream);
+
+/* The forward over the slots of a pool fp32 [num_slots, channels, state_dim], in
+ * place; slots as in gdn_chunk_prefill_paged. */
+gdn_status gdn_selective_scan_prefill_paged(const gdn_pack *p, const gdn_scan_shape *s,
+                                            const void *x, const void *dt, const float *A_log,
+                                            const void *B, const void *C, const float *D,
+                                            const void *z, const float *dt_bias, float *state_pool,
+                                            int32_t num_slots, const int32_t *state_indices,
+                                            const int32_t *has_initial_state, void *y,
+                                            int32_t *device_status, void *workspace,
+                                            size_t ws_bytes, gdn_stream_t stream);
+
+/* Backward, from the forward's inputs (the states are rebuilt).
+ *   d_y                  [T, channels]
+ *   d_final_state        fp32 [N, channels, state_dim], or NULL for zeros
+ *   dx, ddt, dz          [T, channels] (out, dense; dz with z only)
+ *   dB, dC               [T, groups, state_dim] (out, dense)
+ *   dA_log               fp32 [channels, state_dim] (out)
+ *   dD, ddt_bias         fp32 [channels] (out), or NULL
+ *   d_initial_state      fp32 [N, channels, state_dim] (out), or NULL */
+gdn_status gdn_selective_scan_bwd(const gdn_pack *p, const gdn_scan_shape *s, const void *x,
+                                  const void *dt, const float *A_log, const void *B, const void *C,
+                                  const float *D, const void *z, const float *dt_bias,
+                                  const float *initial_state, const void *d_y,
+                                  const float *d_final_state, void *dx, void *ddt, float *dA_log,
+                                  void *dB, void *dC, float *dD, void *dz, float *ddt_bias,
+                                  float *d_initial_state, void *workspace, size_t ws_bytes,
+                                  gdn_stream_t stream);
+
+/* One token per row: x, dt, z, y [batch, channels], B, C [batch, groups, state_dim],
+ * row b's state in slot state_indices[b] of state_pool, advanced in place (slots as
+ * in gdn_decode_step). */
+gdn_status gdn_selective_scan_step(int32_t batch, const gdn_scan_shape *s, const void *x,
+                                   const void *dt, const float *A_log, const void *B,
+                                   const void *C, const float *D, const void *z,
+                                   const float *dt_bias, float *state_pool, int32_t num_slots,
+                                   const int32_t *state_indices, void *y, int32_t *device_status,
+                                   gdn_stream_t stream);
+
+/* Norm of rows, with what stands ahead of it and behind it in a block:
+ *     h = residual + scale x, rounded to the residual's type   (no residual: h = x)
+ *     y = h / sqrt(mean(h^2) + eps) (offset + weight) act(z)
+ *   x, z, y          [rows, dim] in `dtype`; z NULL: no gate
+ *   residual, h      [rows, dim] in residual_dtype (h out): the residual stream ahead of
+ *                    and behind the branch x; both NULL with GDN_NO_RESIDUAL.  A bf16
+ *                    or fp32 stream for bf16, an fp32 one for fp32
+ *   scale            fp32 [dim], or NULL for 1 (with a residual only)
+ *   weight           fp32 [dim]; offset 1 for weights kept around zero
+ *   gate             GDN_GATE_*
+ * dim 1 .. 8192, eps >= 0 and finite, offset finite. */
+#define GDN_NO_RESIDUAL (-1)
+#define GDN_GATE_NONE 0
+#define GDN_GATE_SILU 1
+#define GDN_GATE_SIGMOID 2
+gdn_status gdn_rms_norm_fwd(int64_t rows, int32_t dim, int32_t dtype, int32_t residual_dtype,
+                            int32_t gate, float eps, float offset, const void *x,
+                            const void *residual, const float *scale, const float *weight,
+                            const void *z, void *y, void *h, gdn_stream_t stream);
+
+/* Bytes of scratch of gdn_rms_norm_bwd; 0 for invalid arguments. */
+size_t gdn_rms_norm_workspace_bytes(int64_t rows, int32_t dim, int32_t dtype, int32_t with_scale);
+
+/* Backward.
+ *   h          the forward's h (x where there is no residual)
+ *   x          the forward's x, with a scale only (for dscale); else NULL
+ *   d_y, d_h   [rows, dim]; d_h in residual_dtype, or NULL for zeros
+ *   dx, dz     [rows, dim] (out); dz with z only
+ *   dresidual  [rows, dim] in residual_dtype (out), or NULL where the caller takes dx
+ *              for it (the same numbers without a scale in one type)
+ *   dweight    fp32 [dim] (out);  dscale fp32 [dim] (out, with a scale only) */
+gdn_status gdn_rms_norm_bwd(int64_t rows, int32_t dim, int32_t dtype, int32_t residual_dtype,
+                            int32_t gate, float eps, float offset, const void *h, const void *x,
+                            const float *scale, const float *weight, const void *z,
+                            const void *d_y, const void *d_h, void *dx, void *dresidual, void *dz,
+                            float *dweight, float *dscale, void *workspace, size_t ws_bytes,
+                            gdn_stream_t stream);
+
 /* Optional per-kernel timing, for profiling tools and benchmarks.  The caller
  * creates `capacity` pairs of CUDA events (cudaEvent_t, passed as void*) and
  * passes the struct to a *_timed entry point; the library records

@@ -35,9 +35,22 @@ __device__ __forceinline__ void store_vec(T *p, long long i, long long n, int *s
     if (in_range(i, V, n, status)) *reinterpret_cast<Vec<T, V> *>(p + i) = v;
 }
 
-// 1 / (1 + e^-x) from the hardware's exponential and reciprocal: good to about 2^-21 for |x| < 10
-// (2^-24 |x| beyond), which a result in bf16 does not see and one in fp32 bears.
-__device__ __forceinline__ float sigmoid_of(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// The hardware's 2^x and 1 / x (2^-22 each), denormal numbers taken for 0: one instruction each, where
+// __expf and __fdividef keep denormals and extreme divisors for some more.
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float exp_of(float x) { return exp2_of(x * 1.44269504088896341f); }
+__device__ __forceinline__ float reciprocal_of(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + e^-x): good to about 2^-21 for |x| < 10 (2^-24 |x| beyond), which a result in bf16 does
+// not see and one in fp32 bears.
+__device__ __forceinline__ float sigmoid_of(float x) { return reciprocal_of(1.f + exp_of(-x)); }
 
 // The sequence of token t: the last n with cu[n] <= t.
 __device__ __forceinline__ int sequence_of(const PackArgs &p, int t) {

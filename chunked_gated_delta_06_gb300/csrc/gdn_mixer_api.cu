@@ -166,9 +166,12 @@ gdn_status check_scan(const gdn_scan_shape *s, ScanWidth *w) {
     return GDN_OK;
 }
 
-int scan_block(const gdn_scan_shape *s) { return 1024 / s->state_dim; }   // channels of a block
-int64_t scan_across(const gdn_scan_shape *s) {
-    const int64_t per = s->channels / s->groups, cb = scan_block(s);
+// Blocks of a segment; a block's channels are the kernels' (forward: 128 threads of up to 16 states).
+int scan_block(const gdn_scan_shape *s, int for_backward) {
+    return for_backward ? 1024 / s->state_dim : s->state_dim == 32 ? 64 : 128;
+}
+int64_t scan_across(const gdn_scan_shape *s, int for_backward) {
+    const int64_t per = s->channels / s->groups, cb = scan_block(s, for_backward);
     return s->groups * ((per + cb - 1) / cb);
 }
 
@@ -176,9 +179,14 @@ constexpr int kSegment = 32;   // segments are whole tiles of every kernel that 
 constexpr int kNoSplit = 0x7fffffff;
 
 // Tokens of a segment (kNoSplit: none).  A block walks its tokens one after another, so a few long
-// sequences leave SMs idle.  In units of a token's time in a block: a walk takes as long as its
-// longest chain or as all its blocks' tokens over the blocks that run at once; a split scan walks
-// the segments once for their ends (about two thirds of the work) and once for the outputs.
+// sequences leave SMs idle.  In units of a token's time in a block that has its SM for itself (forward
+// 90 ns, backward 300 ns), a walk takes as long as its longest chain, a fifth more for the blocks that
+// share its SM, or as all its blocks' tokens over the SMs (which a second block on an SM makes worth 1.08
+// or 1.4) and half a segment for the last ones; a split scan walks its segments for their ends first
+// (0.66 of a forward, 0.3 of a backward), and costs about 60 tokens for the launches and two for each
+// record that a block joins.  Forward of 4 x 4096 tokens of 4096 channels: 365 us, split 510; of 65536
+// tokens of 2048: 5710 us, split 1004.  Backward: 1699 and 1918, of 11 sequences up to 6969 tokens 2357
+// and 1958.
 int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &pack, int for_backward) {
     if (s->segment_tokens < 0) return kNoSplit;
     if (s->segment_tokens > 0) {
@@ -186,13 +194,13 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         return seg <= pack.T ? (int)seg : kNoSplit;
     }
     const int32_t *cu = p->cu_seqlens_host;
-    const double places = 3.0 * 152.0, across = (double)scan_across(s);
+    const double places = (for_backward ? 1.4 : 1.08) * 152.0, first = for_backward ? 0.3 : 0.66;
+    const double across = (double)scan_across(s, for_backward);
     int longest = 0;
     for (int n = 0; n < pack.N; ++n) longest = std::max(longest, cu[n + 1] - cu[n]);
-    if (longest < 512) return kNoSplit;
-    double best = 0.9 * std::max((double)longest, pack.T * across / places);
+    double best = std::max(1.2 * longest, pack.T * across / places);
     int seg = kNoSplit;
-    for (int L = 256; L < longest; L *= 2) {
+    for (int L = 64; L < longest; L *= 2) {
         double ends = 0.0;
         for (int n = 0; n < pack.N; ++n) {
             const int len = cu[n + 1] - cu[n];
@@ -200,8 +208,8 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         }
         const double bytes = 4.0 * (pack.N + pack.T / L) * s->channels * (2.0 * s->state_dim + 1.0);
         if (bytes > 1073741824.0) continue;
-        const double pass = (for_backward ? 0.5 : 0.65) * std::max((double)L, ends * across / places);
-        const double t = pass + std::max((double)L, pack.T * across / places) + 32.0;
+        auto walk = [&](double tokens) { return std::max((double)L, tokens * across / places + 0.5 * L); };
+        const double t = first * walk(ends) + walk(pack.T) + 60.0 + 2.0 * (longest / L);
         if (t < best) {
             best = t;
             seg = L;
@@ -219,7 +227,7 @@ size_t carve_scan(const gdn_scan_shape *s, gdn::ScanArgs &a, int for_backward, v
         if (for_backward) a.rec_g = c.take<float>(items * C * NS);
     }
     if (for_backward) {
-        const size_t per = C / s->groups, blocks = (per + scan_block(s) - 1) / scan_block(s);
+        const size_t per = C / s->groups, blocks = (per + scan_block(s, 1) - 1) / scan_block(s, 1);
         a.marks = c.take<float>(((size_t)a.pack.N + a.pack.T / gdn::scan_mark_tile()) * C * NS);
         a.part_bc = c.take<float>(blocks * (size_t)a.pack.T * s->groups * 2 * NS);
         a.part_c = c.take<float>(items * C * (NS + 2));
@@ -229,7 +237,7 @@ size_t carve_scan(const gdn_scan_shape *s, gdn::ScanArgs &a, int for_backward, v
 
 bool scan_grid_fits(const gdn_scan_shape *s, const gdn::ScanArgs &a) {
     const int64_t bc = (int64_t)a.pack.T * s->groups * s->state_dim / 512, par = (int64_t)s->channels * 34 / 256;
-    return (gdn::scan_items(a.pack.N, a.pack.T, a.seg) + 1) * scan_across(s) < kGrid && bc + 1 < kGrid && par + 1 < kGrid;
+    return (gdn::scan_items(a.pack.N, a.pack.T, a.seg) + 1) * scan_across(s, 1) < kGrid && bc + 1 < kGrid && par + 1 < kGrid;
 }
 
 gdn::ScanArgs scan_args(const gdn::PackArgs &pack, const gdn_scan_shape *s, const ScanWidth &w, const void *x,

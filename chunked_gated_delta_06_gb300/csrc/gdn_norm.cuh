@@ -38,7 +38,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int turn) {
 
 // The gate's factor and its slope at z.
 __device__ __forceinline__ float gate_of(int gate, float z, float *slope) {
-    const float e = __expf(-z), sig = __fdividef(1.f, 1.f + e);
+    const float e = exp_of(-z), sig = reciprocal_of(1.f + e);
     const float rest = z > 0.f ? e * sig : 1.f - sig;   // 1 - sig, which a sig near 1 has lost
     if (gate == GDN_GATE_SIGMOID) {
         if (slope) *slope = sig * rest;

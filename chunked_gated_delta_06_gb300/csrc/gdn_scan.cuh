@@ -3,26 +3,16 @@
 // Per channel c (of group g) and state n, with d_t = softplus(dt_t + dt_bias), A = -e^{A_log}:
 //   h_t = e^{d_t A} h_{t-1} + d_t x_t B_t[n],   y_t = (sum_n C_t[n] h_t + D x_t) silu(z_t)
 //
-// A block of 128 threads walks a segment of one sequence for CB channels of one group, a tile of
-// tokens at a time.  What is the same for all states of a channel (d, d x, the gate) is formed once,
-// element by element over the whole block, and passes through shared memory; in the walk itself a
-// thread has two neighbouring channels of four states each, so that a token costs it one 16-byte
-// read of (d, d x), one of B and one of C for eight states, and pairs of states are one packed
-// product or multiply-add.  The decay is the hardware's 2^x, d (A / ln 2) rounded once.
+// A block walks a segment of one sequence for CB channels of one group, a tile of tokens at a time.
+// What is the same for all states of a channel (d, d x, the gate) is formed once, element by element
+// over many threads, and passes through shared memory to the threads that walk the states.  Pairs
+// of states are one packed product or multiply-add; the decay is the hardware's 2^x, d (A / ln 2)
+// rounded once.
 #pragma once
 
 #include "gdn_mixer.cuh"
 
 namespace gdn {
-
-constexpr int kScanThreads = 128;
-
-template <int NS>
-struct ScanShape {
-    static constexpr int L = NS / 4;                    // threads of a channel pair
-    static constexpr int kPairs = kScanThreads / L;     // channel pairs of a block
-    static constexpr int CB = 2 * kPairs;
-};
 
 __device__ __forceinline__ unsigned long long as_bits(float2 x) { return *reinterpret_cast<unsigned long long *>(&x); }
 __device__ __forceinline__ float2 as_pair(unsigned long long x) { return *reinterpret_cast<float2 *>(&x); }
@@ -42,18 +32,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return as_pair(d);
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float exp2_of(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float2 exp2_of(float2 x) { return make_float2(exp2_of(x.x), exp2_of(x.y)); }
 
 // softplus(u) = max(u, 0) + log(1 + e^-|u|), the logarithm as 2 artanh(e / (2 + e)): its series in
 // s = e / (2 + e) <= 1/3 up to s^13 is good to 2^-23, for a small e as well (where log(1 + e) from
 // a rounded 1 + e would keep nothing of it).
 __device__ __forceinline__ float softplus_of(float u) {
-    const float e = __expf(-fabsf(u)), s = __fdividef(e, 2.f + e), q = s * s;
+    const float e = exp_of(-fabsf(u)), s = e * reciprocal_of(2.f + e), q = s * s;
     float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
     p = fmaf(q, p, 1.f / 9.f);
     p = fmaf(q, p, 1.f / 7.f);
@@ -62,6 +47,38 @@ __device__ __forceinline__ float softplus_of(float u) {
     p = fmaf(q, p, 1.f);
     return fmaxf(u, 0.f) + 2.f * s * p;
 }
+
+// Of two numbers at once, without the larger of the number and 0 (to be added last).
+__device__ __forceinline__ float2 softplus_rest(float2 u) {
+    const float2 e = make_float2(exp_of(-fabsf(u.x)), exp_of(-fabsf(u.y)));
+    const float2 n = add2(e, both(2.f));
+    const float2 s = mul2(e, make_float2(reciprocal_of(n.x), reciprocal_of(n.y))), q = mul2(s, s);
+    float2 p = fma2(q, both(1.f / 13.f), both(1.f / 11.f));
+    p = fma2(q, p, both(1.f / 9.f));
+    p = fma2(q, p, both(1.f / 7.f));
+    p = fma2(q, p, both(1.f / 5.f));
+    p = fma2(q, p, both(1.f / 3.f));
+    p = fma2(q, p, both(1.f));
+    return mul2(add2(s, s), p);
+}
+__device__ __forceinline__ float2 softplus_of(float2 u) {
+    return add2(softplus_rest(u), make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
+}
+__device__ __forceinline__ float2 silu_of(float2 z) {
+    return mul2(z, make_float2(sigmoid_of(z.x), sigmoid_of(z.y)));
+}
+
+// Asynchronous copies of `bytes` (4, 8 or 16) into shared memory; zeros instead where there is nothing.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *to, const void *from, bool there) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    const int n = there ? kBytes : 0;
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(kBytes), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
 
 // Where a block works.
 struct ScanPlace {
@@ -73,9 +90,8 @@ struct ScanPlace {
 
 __device__ __forceinline__ int first_item(const ScanArgs &a, int n) { return n + offset_of(a.pack, n) / a.seg; }
 
-template <int NS>
+template <int CB>   // channels of a block
 __device__ __forceinline__ bool scan_place(const ScanArgs &a, long long block, ScanPlace *p) {
-    constexpr int CB = ScanShape<NS>::CB;
     const int per_group = a.C / a.G, blocks = (per_group + CB - 1) / CB, across = a.G * blocks;
     const int col = (int)(block % across);
     p->item = (int)(block / across);
@@ -98,14 +114,15 @@ __device__ __forceinline__ bool scan_place(const ScanArgs &a, long long block, S
     return p->seg >= 0 && p->seg < p->segs;
 }
 
-// A tile's elements of a [T, C] tensor, spread over the block: EV channels of a row in a vector.
-template <typename T, int CB, int TT, int EV, bool kWide>
+// A tile's elements of a [T, C] tensor, spread over N threads: EV channels of a row in a vector.
+template <typename T, int CB, int TT, int EV, int N, bool kWide>
 struct TileOf {
-    static constexpr int kCols = CB / EV, kVecs = TT * kCols, NV = (kVecs + kScanThreads - 1) / kScanThreads;
-    static_assert(kScanThreads % kCols == 0, "a thread's vectors have the same channels");
+    static constexpr int kCols = CB / EV, kVecs = TT * kCols, NV = (kVecs + N - 1) / N;
+    static_assert(N % kCols == 0, "a thread's vectors have the same channels");
     using V = Vec<T, EV>;
-    static __device__ int row(int k) { return ((int)threadIdx.x + k * kScanThreads) / kCols; }
-    static __device__ int col() { return (int)threadIdx.x % kCols * EV; }
+    static __device__ int thread() { return (int)threadIdx.x % N; }
+    static __device__ int row(int k) { return (thread() + k * N) / kCols; }
+    static __device__ int col() { return thread() % kCols * EV; }
     // rows [t, end) of the tile that starts at token t; zeros elsewhere
     static __device__ void load(const T *p, long long stride, const ScanArgs &a, const ScanPlace &w, int t, int end, V (&v)[NV]) {
         const int c = w.c0 + col();
@@ -144,15 +161,15 @@ struct TileOf {
 };
 
 // A tile's rows of B or C ([T, G, NS]), four elements a unit.
-template <typename T, int NS, int TT, bool kWide>
+template <typename T, int NS, int TT, int N, bool kWide>
 struct RowsOf {
-    static constexpr int kUnits = TT * NS / 4, NU = (kUnits + kScanThreads - 1) / kScanThreads;
+    static constexpr int kUnits = TT * NS / 4, NU = (kUnits + N - 1) / N;
     using V = Vec<T, 4>;
     static __device__ void load(const T *p, long long stride, const ScanArgs &a, const ScanPlace &w, int t, int end, V (&v)[NU]) {
         const long long extent = (a.pack.T - 1) * stride + (long long)a.G * NS;
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
-            const int u = (int)threadIdx.x + k * kScanThreads, at = t + u / (NS / 4), i = u % (NS / 4) * 4;
+            const int u = (int)threadIdx.x % N + k * N, at = t + u / (NS / 4), i = u % (NS / 4) * 4;
             const long long from = at * stride + w.g * NS + i;
             const bool there = u < kUnits && at < end;
             if (kWide && there) {
@@ -164,10 +181,19 @@ struct RowsOf {
             }
         }
     }
+    static __device__ void keep_copied(const V *v, float (*rows)[NS]) {
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+            const int u = (int)threadIdx.x % N + k * N;
+            if (u >= kUnits) break;
+            *reinterpret_cast<float4 *>(&rows[u / (NS / 4)][u % (NS / 4) * 4]) =
+                make_float4(as_float(v[u].x[0]), as_float(v[u].x[1]), as_float(v[u].x[2]), as_float(v[u].x[3]));
+        }
+    }
     static __device__ void keep(const V (&v)[NU], float (*rows)[NS]) {
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
-            const int u = (int)threadIdx.x + k * kScanThreads;
+            const int u = (int)threadIdx.x % N + k * N;
             if (u >= kUnits) break;
             *reinterpret_cast<float4 *>(&rows[u / (NS / 4)][u % (NS / 4) * 4]) =
                 make_float4(as_float(v[k].x[0]), as_float(v[k].x[1]), as_float(v[k].x[2]), as_float(v[k].x[3]));
@@ -175,74 +201,162 @@ struct RowsOf {
     }
 };
 
-// (d, d x) of two neighbouring channels are one 16-byte unit of a row.  Units are permuted within
-// runs of 8, so that threads that write the four units of eight channels meet no bank twice.
-__device__ __forceinline__ int unit_at(int unit) { return unit ^ (unit >> 3 & 3); }
+// Copies tile after tile of a tensor into the thread's own places to[thread + k N] of shared memory.
+template <typename Tile, typename T, int N, bool kWide>
+struct FeedOf {
+    const T *p, *at;
+    long long step, apart, extent;
+    int left;            // tokens that the segment has from the next tile on
+    bool there;
+    __device__ FeedOf(const T *from, long long stride, const ScanArgs &a, const ScanPlace &w, int tokens) {
+        const int c = w.c0 + Tile::col();
+        p = from;
+        step = tokens * stride;
+        apart = (long long)(N / Tile::kCols) * stride;
+        extent = (a.pack.T - 1) * stride + a.C;
+        left = w.f - w.b;
+        there = from != nullptr && c < w.cend;
+        at = from + (long long)(w.b + Tile::row(0)) * stride + c;
+    }
+    // on to the tile `tokens` on, to walk back from there
+    __device__ void turn(int tokens, int tile) {
+        at += step / tile * tokens;
+        left -= tokens;
+        step = -step;
+    }
+    // tokens: of a tile, negative for a walk back
+    __device__ void next(typename Tile::V *to, const ScanArgs &a, const ScanPlace &w, int tokens) {
+        // (in a walk forward or back every row of a tile is one of its `tokens`)
+        constexpr int E = sizeof(to->x) / sizeof(T), kBytes = (int)sizeof(to->x) > 16 ? 16 : (int)sizeof(to->x);
+        constexpr int kE = kBytes / (int)sizeof(T);
+#pragma unroll
+        for (int k = 0; k < Tile::NV; ++k) {
+            if (Tile::thread() + k * N >= Tile::kVecs) break;   // (the tile has fewer vectors than there are threads)
+            const T *from = at + k * apart;
+            typename Tile::V *place = to + Tile::thread() + k * N;
+            const bool row = there && Tile::row(k) < left;
+            if (kWide) {
+                const bool ok = row && in_range(from - p, E, extent, a.pack.status);
+#pragma unroll
+                for (int i = 0; i < E; i += kE) copy_async<kBytes>(place->x + i, ok ? from + i : p, ok);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    place->x[i] = row && w.c0 + Tile::col() + i < w.cend && in_range(from - p + i, 1, extent, a.pack.status)
+                                      ? from[i]
+                                      : as_type<T>(0.f);
+            }
+        }
+        at += step;
+        left -= tokens;
+    }
+};
+// The same for the rows of B or C, four elements a unit.
+template <typename Rows, typename T, int NS, int N, bool kWide>
+struct RowFeedOf {
+    const T *p, *at;
+    long long step, apart, extent;
+    int left;
+    __device__ RowFeedOf(const T *from, long long stride, const ScanArgs &a, const ScanPlace &w, int tokens) {
+        const int u = (int)threadIdx.x % N;
+        p = from;
+        step = tokens * stride;
+        apart = (long long)(N / (NS / 4)) * stride;
+        extent = (a.pack.T - 1) * stride + (long long)a.G * NS;
+        left = w.f - w.b;
+        at = from + (long long)(w.b + u / (NS / 4)) * stride + w.g * NS + u % (NS / 4) * 4;
+    }
+    __device__ void turn(int tokens, int tile) {
+        at += step / tile * tokens;
+        left -= tokens;
+        step = -step;
+    }
+    __device__ void next(typename Rows::V *to, const ScanArgs &a, int tokens) {
+        static_assert(N % (NS / 4) == 0, "a thread's units are of the same states");
+#pragma unroll
+        for (int k = 0; k < Rows::NU; ++k) {
+            const int u = (int)threadIdx.x % N + k * N;
+            if (u >= Rows::kUnits) break;
+            const T *from = at + k * apart;
+            const bool ok = u / (NS / 4) < left && in_range(from - p, 4, extent, a.pack.status);
+            if (kWide) {
+                copy_async<4 * (int)sizeof(T)>(to + u, ok ? from : p, ok);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[u].x[i] = ok ? from[i] : as_type<T>(0.f);
+            }
+        }
+        at += step;
+        left -= tokens;
+    }
+};
 
-// A thread's part of the walk: channels c and c + 1, states 4 q .. 4 q + 3 of each.
-template <int NS>
+// A thread's part of a walk: channels c .. c + P - 1, states S q .. S q + S - 1 of each.
+template <int NS, int P, int S, int kFirst = 0>   // kFirst: the first thread that walks
 struct ScanLane {
-    int pair, q, c;
-    float2 A[2][2];      // rates / ln 2, <= 0 and finite (a token without an input has d = 0)
+    static constexpr int L = NS / S, H = S / 2;
+    using States = float2[P][H];
+    int at, q, c;        // its group of P channels in the block, its part of the states, its first channel
+    float2 A[P][H];      // rates / ln 2, <= 0 and finite (a token without an input has d = 0)
     __device__ ScanLane(const ScanArgs &a, const ScanPlace &w) {
-        pair = (int)threadIdx.x / ScanShape<NS>::L;
-        q = (int)threadIdx.x % ScanShape<NS>::L;
-        c = w.c0 + 2 * pair;
+        at = ((int)threadIdx.x - kFirst) / L;
+        q = ((int)threadIdx.x - kFirst) % L;
+        c = w.c0 + P * at;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const long long at = (long long)(c + i) * NS + 4 * q;
-            float r[4] = {};
-            if (c + i < w.cend && in_range(at, 4, (long long)a.C * NS, a.pack.status))
+        for (int i = 0; i < P; ++i) {
+            const long long from = (long long)(c + i) * NS + S * q;
+            const bool there = c + i < w.cend && in_range(from, S, (long long)a.C * NS, a.pack.status);
+            auto rate = [&](int j) {
+                return there ? fmaxf(-1.44269504088896341f * expf(a.A_log[from + j]), -3e38f) : 0.f;
+            };
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = fmaxf(-1.44269504088896341f * expf(a.A_log[at + j]), -3e38f);
-            A[i][0] = make_float2(r[0], r[1]);
-            A[i][1] = make_float2(r[2], r[3]);
+            for (int k = 0; k < H; ++k) A[i][k] = make_float2(rate(2 * k), rate(2 * k + 1));
         }
     }
     // the thread's states of a row of [rows, C, NS]
-    __device__ void load(const float *p, long long row, long long rows, const ScanArgs &a, const ScanPlace &w, float2 (&h)[2][2]) const {
+    __device__ void load(const float *p, long long row, long long rows, const ScanArgs &a, const ScanPlace &w, States &h) const {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            const long long at = (row * a.C + c + i) * NS + 4 * q;
-            if (p && row >= 0 && c + i < w.cend && in_range(at, 4, rows * a.C * NS, a.pack.status))
-                v = *reinterpret_cast<const float4 *>(p + at);
-            h[i][0] = make_float2(v.x, v.y);
-            h[i][1] = make_float2(v.z, v.w);
-        }
-    }
-    __device__ void store(float *p, long long row, long long rows, const ScanArgs &a, const ScanPlace &w, const float2 (&h)[2][2]) const {
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const long long at = (row * a.C + c + i) * NS + 4 * q;
-            if (p && row >= 0 && c + i < w.cend && in_range(at, 4, rows * a.C * NS, a.pack.status))
-                *reinterpret_cast<float4 *>(p + at) = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
-        }
+            for (int k = 0; k < H; k += 2) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                const long long from = (row * a.C + c + i) * NS + S * q + 2 * k;
+                if (p && row >= 0 && c + i < w.cend && in_range(from, 4, rows * a.C * NS, a.pack.status))
+                    v = *reinterpret_cast<const float4 *>(p + from);
+                h[i][k] = make_float2(v.x, v.y);
+                h[i][k + 1] = make_float2(v.z, v.w);
+            }
     }
-    __device__ void decays(int i, float d, float2 (&out)[2]) const {
-        out[0] = exp2_of(mul2(A[i][0], both(d)));
-        out[1] = exp2_of(mul2(A[i][1], both(d)));
+    __device__ void store(float *p, long long row, long long rows, const ScanArgs &a, const ScanPlace &w, const States &h) const {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+            for (int k = 0; k < H; k += 2) {
+                const long long to = (row * a.C + c + i) * NS + S * q + 2 * k;
+                if (p && row >= 0 && c + i < w.cend && in_range(to, 4, rows * a.C * NS, a.pack.status))
+                    *reinterpret_cast<float4 *>(p + to) = make_float4(h[i][k].x, h[i][k].y, h[i][k + 1].x, h[i][k + 1].y);
+            }
     }
+    __device__ float2 decay(int i, int k, float2 d) const { return exp2_of(mul2(A[i][k], d)); }
     // h <- e^{A sum of d} h + the record of segment `item`
-    __device__ void join(const ScanArgs &a, const ScanPlace &w, const float *rec, int item, float2 (&h)[2][2]) const {
+    __device__ void join(const ScanArgs &a, const ScanPlace &w, const float *rec, int item, States &h) const {
         const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
-        float2 end[2][2], decay[2];
+        States end;
         load(rec, item, items, a, w, end);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const long long at = (long long)item * a.C + c + i;
-            const float d = c + i < w.cend && in_range(at, 1, items * a.C, a.pack.status) ? a.rec_d[at] : 0.f;
-            decays(i, d, decay);
-            h[i][0] = fma2(decay[0], h[i][0], end[i][0]);
-            h[i][1] = fma2(decay[1], h[i][1], end[i][1]);
+        for (int i = 0; i < P; ++i) {
+            const long long from = (long long)item * a.C + c + i;
+            const float d = c + i < w.cend && in_range(from, 1, items * a.C, a.pack.status) ? a.rec_d[from] : 0.f;
+#pragma unroll
+            for (int k = 0; k < H; ++k) h[i][k] = fma2(decay(i, k, both(d)), h[i][k], end[i][k]);
         }
     }
 };
 
-// Sums over the L threads of a channel pair: K values of each of BT = min(L, 4) tokens come in, and
-// thread q has those of token q % BT in v[0].
+// Sums over the L threads that share channels: K values of each of BT <= L tokens come in, and thread
+// q has those of token q % BT in v[0].
 template <int L, int BT, int K>
-__device__ __forceinline__ void pair_sums(float (&v)[BT][K], int q) {
+__device__ __forceinline__ void lane_sums(float (&v)[BT][K], int q) {
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) {
         if (o >= BT) {
@@ -281,9 +395,9 @@ inline bool scan_wide(const ScanArgs &a, int elements) {
            ok(a.dx, a.C, elements) && ok(a.ddt, a.C, elements) && ok(a.dz, a.C, elements);
 }
 
-template <int NS>
+template <int CB>
 long long scan_across(const ScanArgs &a) {
-    return (long long)a.G * ((a.C / a.G + ScanShape<NS>::CB - 1) / ScanShape<NS>::CB);
+    return (long long)a.G * ((a.C / a.G + CB - 1) / CB);
 }
 
 // end states (and sums of d) of every segment but the last of each sequence

@@ -16,6 +16,21 @@
 namespace gdn {
 namespace {
 
+constexpr int kScanThreads = 128;
+
+// A thread walks two neighbouring channels of four states each.
+template <int NS>
+struct PairShape {
+    static constexpr int L = NS / 4, kPairs = kScanThreads / L, CB = 2 * kPairs;
+    static_assert(CB == 1024 / NS, "as the host counts them");
+};
+template <int NS, int kFirst = 0>
+using PairLane = ScanLane<NS, 2, 4, kFirst>;
+
+// (d, d x) of two neighbouring channels are one 16-byte unit of a row.  Units are permuted within
+// runs of 8, so that threads that write the four units of eight channels meet no bank twice.
+__device__ __forceinline__ int unit_at(int unit) { return unit ^ (unit >> 3 & 3); }
+
 constexpr int kMarkTile = 8;   // tokens of a tile
 constexpr int kEV = 4;
 
@@ -24,33 +39,21 @@ __device__ __forceinline__ long long first_mark(const ScanArgs &a, const ScanPla
     return (long long)w.n + w.s / kMarkTile + (w.b - w.s) / kMarkTile;
 }
 
-template <int TT, int CB, typename V>
-__device__ __forceinline__ void keep_inputs(const ScanPlace &w, int t, int k, int row, int col, const V &x, const V &dt,
-                                            const float *bias, float (&d)[kEV], float4 (*dd)[CB / 2]) {
-#pragma unroll
-    for (int i = 0; i < kEV; ++i)
-        d[i] = t + row < w.f && w.c0 + col + i < w.cend ? softplus_of(as_float(dt.x[i]) + bias[col + i]) : 0.f;
-    if (row >= TT) return;
-#pragma unroll
-    for (int i = 0; i < kEV; i += 2)
-        dd[row][unit_at((col + i) / 2)] = make_float4(d[i], d[i] * as_float(x.x[i]), d[i + 1], d[i + 1] * as_float(x.x[i + 1]));
-}
-
 // The gradient at the start of each segment but a sequence's first, from nothing behind it (for
 // the last segment, from the final state's gradient).
 template <typename T, int NS, bool kWide>
 __global__ void __launch_bounds__(kScanThreads) k_scan_starts(const __grid_constant__ ScanArgs a) {
-    constexpr int CB = ScanShape<NS>::CB, TT = 16;
-    using Tile = TileOf<T, CB, TT, kEV, kWide>;
-    using Rows = RowsOf<T, NS, TT, kWide>;
+    constexpr int CB = PairShape<NS>::CB, TT = 16;
+    using Tile = TileOf<T, CB, TT, kEV, kScanThreads, kWide>;
+    using Rows = RowsOf<T, NS, TT, kScanThreads, kWide>;
     __shared__ float ds[TT][CB], os[TT][CB];
     __shared__ float Cs[TT][NS];
     __shared__ float bias[CB];
     ScanPlace w;
-    if (!scan_place<NS>(a, blockIdx.x, &w) || w.seg == 0) return;
+    if (!scan_place<PairShape<NS>::CB>(a, blockIdx.x, &w) || w.seg == 0) return;
     for (int i = threadIdx.x; i < CB; i += kScanThreads)
         bias[i] = w.c0 + i < w.cend && a.dt_bias && in_range(w.c0 + i, 1, a.C, a.pack.status) ? a.dt_bias[w.c0 + i] : 0.f;
-    const ScanLane<NS> lane(a, w);
+    const PairLane<NS> lane(a, w);
     float2 g[2][2];
     lane.load(a.ds1, a.ds1 && w.seg == w.segs - 1 ? w.n : -1, a.pack.N, a, w, g);
     const T *dt = static_cast<const T *>(a.dt), *z = static_cast<const T *>(a.z), *dy = static_cast<const T *>(a.dy);
@@ -88,13 +91,12 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_starts(const __grid_const
         if (i > 0) fetch(t - TT);
 #pragma unroll 4
         for (int j = TT - 1; j >= 0; --j) {
-            const float2 d = *reinterpret_cast<const float2 *>(&ds[j][2 * lane.pair]);
-            const float2 o = *reinterpret_cast<const float2 *>(&os[j][2 * lane.pair]);
+            const float2 d = *reinterpret_cast<const float2 *>(&ds[j][2 * lane.at]);
+            const float2 o = *reinterpret_cast<const float2 *>(&os[j][2 * lane.at]);
             const float4 c = *reinterpret_cast<const float4 *>(&Cs[j][4 * lane.q]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float2 decay[2];
-                lane.decays(p, p ? d.y : d.x, decay);
+                const float2 dp_ = both(p ? d.y : d.x), decay[2] = {lane.decay(p, 0, dp_), lane.decay(p, 1, dp_)};
                 const float2 op = both(p ? o.y : o.x);
                 g[p][0] = mul2(decay[0], fma2(make_float2(c.x, c.y), op, g[p][0]));
                 g[p][1] = mul2(decay[1], fma2(make_float2(c.z, c.w), op, g[p][1]));
@@ -105,37 +107,249 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_starts(const __grid_const
     lane.store(a.rec_g, w.item, a.pack.N + (long long)(a.pack.T / a.seg), a, w, g);
 }
 
+template <typename T, int NS>
+struct BackTiles {
+    static constexpr int CB = PairShape<NS>::CB, TT = kMarkTile, kRing = 4;
+    float4 us[2][TT][kScanThreads][2];   // e^{dA} h of a walker's two channels, then its dC and dB
+    float4 dd[2][TT][CB / 2];            // d, d x of two channels, at unit_at; then sum G B, sum p A / ln 2
+    float os[2][TT][CB];                 // o, then sum C h
+    float B[2][TT][NS], C[2][TT][NS];
+    float bias[CB], skip[CB];
+    alignas(16) T x[kRing][TT * CB], dt[kRing][TT * CB], z[kRing][TT * CB], dy[kRing][TT * CB];
+    alignas(16) T rB[kRing][TT * NS], rC[kRing][TT * NS];
+};
+
+// As in the forward, half of the threads are formers and half are walkers, a tile apart.
 template <typename T, int NS, bool kWide>
-__global__ void __launch_bounds__(kScanThreads) k_scan_bwd(const __grid_constant__ ScanArgs a) {
-    constexpr int CB = ScanShape<NS>::CB, L = ScanShape<NS>::L, TT = kMarkTile, BT = L < 4 ? L : 4;
-    constexpr int kPairs = ScanShape<NS>::kPairs;
-    using Tile = TileOf<T, CB, TT, kEV, kWide>;
-    using Rows = RowsOf<T, NS, TT, kWide>;
+__global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_constant__ ScanArgs a) {
+    constexpr int CB = PairShape<NS>::CB, L = PairShape<NS>::L, TT = kMarkTile, BT = L < 4 ? L : 4, N = kScanThreads;
+    constexpr int kPairs = PairShape<NS>::kPairs, R = BackTiles<T, NS>::kRing;
+    using Tile = TileOf<T, CB, TT, kEV, N, kWide>;
+    using Rows = RowsOf<T, NS, TT, N, kWide>;
     extern __shared__ float4 smem[];
-    float4 (*us)[kScanThreads][2] = reinterpret_cast<float4 (*)[kScanThreads][2]>(smem);   // [TT]
-    float4 (*dd)[CB / 2] = reinterpret_cast<float4 (*)[CB / 2]>(us + TT);                   // [TT]
-    float (*os)[CB] = reinterpret_cast<float (*)[CB]>(dd + TT);                             // [TT]
-    float (*Bs)[NS] = reinterpret_cast<float (*)[NS]>(os + TT);                             // [TT]
-    float (*Cs)[NS] = Bs + TT;                                                              // [TT]
-    float *bias = reinterpret_cast<float *>(Cs + TT), *skip = bias + CB;
+    BackTiles<T, NS> &m = *reinterpret_cast<BackTiles<T, NS> *>(smem);
 
     ScanPlace w;
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
-    if (!scan_place<NS>(a, blockIdx.x, &w)) {
+    if (!scan_place<CB>(a, blockIdx.x, &w)) {
         if (a.pack.status && w.item == items) check_offsets(a.pack);
         return;
     }
-    for (int i = threadIdx.x; i < CB; i += kScanThreads) {
+    for (int i = threadIdx.x; i < CB; i += 2 * N) {
         const bool there = w.c0 + i < w.cend && in_range(w.c0 + i, 1, a.C, a.pack.status);
-        bias[i] = there && a.dt_bias ? a.dt_bias[w.c0 + i] : 0.f;
-        skip[i] = there && a.D ? a.D[w.c0 + i] : 0.f;
+        m.bias[i] = there && a.dt_bias ? a.dt_bias[w.c0 + i] : 0.f;
+        m.skip[i] = there && a.D ? a.D[w.c0 + i] : 0.f;
     }
-    const ScanLane<NS> lane(a, w);
-    const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
+    __syncthreads();
     const int tiles = (w.f - w.b + TT - 1) / TT;
-    const T *x = static_cast<const T *>(a.x), *dt = static_cast<const T *>(a.dt), *z = static_cast<const T *>(a.z);
-    const T *dy = static_cast<const T *>(a.dy), *B = static_cast<const T *>(a.B), *Cm = static_cast<const T *>(a.Cm);
+    const float ln2 = 0.693147180559945309f;
+    const long long sums_extent = items * a.C * (NS + 2);
 
+    if (threadIdx.x < N) {
+        using V = typename Tile::V;
+        using U = typename Rows::V;
+        using Feed = FeedOf<Tile, T, N, kWide>;
+        using RowFeed = RowFeedOf<Rows, T, NS, N, kWide>;
+        const bool gated = a.z != nullptr;
+        const int col = Tile::col();
+        auto place = [&](T (*ring)[TT * CB], int i) { return reinterpret_cast<V *>(ring[i % R]); };
+        auto units = [&](T (*ring)[TT * NS], int i) { return reinterpret_cast<U *>(ring[i % R]); };
+        const T *xp = static_cast<const T *>(a.x), *dtp = static_cast<const T *>(a.dt), *Bp = static_cast<const T *>(a.B);
+        // d and d x of the tile at token t, the i-th of its walk
+        auto form = [&](int i, int t, int k, float (&d)[kEV]) {
+            const int row = Tile::row(k);
+            const V xv = place(m.x, i)[Tile::thread() + k * N], dv = place(m.dt, i)[Tile::thread() + k * N];
+#pragma unroll
+            for (int j = 0; j < kEV; j += 2) {
+                float2 v = softplus_of(add2(make_float2(as_float(dv.x[j]), as_float(dv.x[j + 1])),
+                                            *reinterpret_cast<const float2 *>(&m.bias[col + j])));
+                if (t + row >= w.f) v = both(0.f);   // (which leaves the states alone)
+                const float2 dx = mul2(v, make_float2(as_float(xv.x[j]), as_float(xv.x[j + 1])));
+                m.dd[i & 1][row][unit_at((col + j) / 2)] = make_float4(v.x, dx.x, v.y, dx.y);
+                d[j] = v.x;
+                d[j + 1] = v.y;
+            }
+        };
+        {   // forward, all tiles but the last
+            Feed x(xp, a.xs, a, w, TT), dt(dtp, a.dts, a, w, TT);
+            RowFeed B(Bp, a.bs, a, w, TT);
+            auto fetch = [&](int i) {
+                if (i < tiles - 1) {
+                    x.next(place(m.x, i), a, w, TT);
+                    dt.next(place(m.dt, i), a, w, TT);
+                    B.next(units(m.rB, i), a, TT);
+                }
+                copies_commit();
+            };
+            auto all = [&](int i) {
+                float d[kEV];
+#pragma unroll
+                for (int k = 0; k < Tile::NV; ++k)
+                    if (Tile::row(k) < TT) form(i, w.b + i * TT, k, d);
+                Rows::keep_copied(units(m.rB, i), m.B[i & 1]);
+            };
+            fetch(0);
+            fetch(1);
+            copies_wait<1>();
+            if (tiles > 1) all(0);
+            __syncthreads();
+            for (int i = 0; i < tiles - 1; ++i) {
+                fetch(i + 2);
+                copies_wait<1>();
+                if (i + 1 < tiles - 1) all(i + 1);
+                __syncthreads();
+            }
+        }
+        // backward: the i-th tile of the walk is the segment's tile tiles - 1 - i
+        Feed x(xp, a.xs, a, w, TT), dt(dtp, a.dts, a, w, TT);
+        Feed z(static_cast<const T *>(a.z), a.zs, a, w, TT), dy(static_cast<const T *>(a.dy), a.C, a, w, TT);
+        RowFeed B(Bp, a.bs, a, w, TT), C(static_cast<const T *>(a.Cm), a.cs, a, w, TT);
+        const int skipped = (tiles - 1) * TT;
+        x.turn(skipped, TT);
+        dt.turn(skipped, TT);
+        z.turn(skipped, TT);
+        dy.turn(skipped, TT);
+        B.turn(skipped, TT);
+        C.turn(skipped, TT);
+        float dD[kEV] = {}, db[kEV] = {};
+        auto fetch = [&](int i) {
+            if (i < tiles) {
+                x.next(place(m.x, i), a, w, -TT);
+                dt.next(place(m.dt, i), a, w, -TT);
+                dy.next(place(m.dy, i), a, w, -TT);
+                if (gated) z.next(place(m.z, i), a, w, -TT);
+                B.next(units(m.rB, i), a, -TT);
+                C.next(units(m.rC, i), a, -TT);
+            }
+            copies_commit();
+        };
+        auto all = [&](int i) {
+            float d[kEV];
+#pragma unroll
+            for (int k = 0; k < Tile::NV; ++k) {
+                const int row = Tile::row(k);
+                if (row >= TT) break;
+                form(i, w.b + (tiles - 1 - i) * TT, k, d);
+                const V dyv = place(m.dy, i)[Tile::thread() + k * N];
+                float2 o[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) o[j] = make_float2(as_float(dyv.x[2 * j]), as_float(dyv.x[2 * j + 1]));
+                if (gated) {
+                    const V zv = place(m.z, i)[Tile::thread() + k * N];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        o[j] = mul2(o[j], silu_of(make_float2(as_float(zv.x[2 * j]), as_float(zv.x[2 * j + 1]))));
+                }
+                *reinterpret_cast<float4 *>(&m.os[i & 1][row][col]) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
+            }
+            Rows::keep_copied(units(m.rB, i), m.B[i & 1]);
+            Rows::keep_copied(units(m.rC, i), m.C[i & 1]);
+        };
+        const int per_group = a.C / a.G, blocks = (per_group + CB - 1) / CB, mine = (w.c0 - w.g * per_group) / CB;
+        auto finish = [&](int i) {
+            const int t = w.b + (tiles - 1 - i) * TT;
+#pragma unroll
+            for (int k = 0; k < Tile::NV; ++k) {
+                const int row = Tile::row(k);
+                if (row >= TT) break;
+                const V xv = place(m.x, i)[Tile::thread() + k * N], dv = place(m.dt, i)[Tile::thread() + k * N];
+                const V dyv = place(m.dy, i)[Tile::thread() + k * N];
+                V zv, dxv, ddv, dzv;
+                if (gated) zv = place(m.z, i)[Tile::thread() + k * N];
+                const bool there = t + row < w.f;
+#pragma unroll
+                for (int j = 0; j < kEV; j += 2) {
+                    const float4 s = m.dd[i & 1][row][unit_at((col + j) / 2)];
+                    const float2 gB = make_float2(s.x, s.z), pA = make_float2(s.y, s.w);
+                    const float2 xj = make_float2(as_float(xv.x[j]), as_float(xv.x[j + 1]));
+                    const float2 skip = *reinterpret_cast<const float2 *>(&m.skip[col + j]);
+                    float2 o = make_float2(as_float(dyv.x[j]), as_float(dyv.x[j + 1]));
+                    if (gated) {
+                        const float2 zj = make_float2(as_float(zv.x[j]), as_float(zv.x[j + 1]));
+                        const float2 sig = make_float2(sigmoid_of(zj.x), sigmoid_of(zj.y)), silu = mul2(zj, sig);
+                        const float2 slope = fma2(silu, make_float2(1.f - sig.x, 1.f - sig.y), sig);
+                        const float2 y = fma2(skip, xj, *reinterpret_cast<const float2 *>(&m.os[i & 1][row][col + j]));
+                        const float2 dz = mul2(mul2(o, y), slope);
+                        dzv.x[j] = as_type<T>(dz.x);
+                        dzv.x[j + 1] = as_type<T>(dz.y);
+                        o = mul2(o, silu);
+                    }
+                    const float2 u = add2(make_float2(as_float(dv.x[j]), as_float(dv.x[j + 1])),
+                                          *reinterpret_cast<const float2 *>(&m.bias[col + j]));
+                    const float2 dxj = fma2(gB, softplus_of(u), mul2(skip, o));
+                    const float2 du = mul2(fma2(pA, both(ln2), mul2(gB, xj)), make_float2(sigmoid_of(u.x), sigmoid_of(u.y)));
+                    dxv.x[j] = as_type<T>(dxj.x);
+                    dxv.x[j + 1] = as_type<T>(dxj.y);
+                    ddv.x[j] = as_type<T>(du.x);
+                    ddv.x[j + 1] = as_type<T>(du.y);
+                    if (there) {
+                        dD[j] = fmaf(o.x, xj.x, dD[j]);
+                        dD[j + 1] = fmaf(o.y, xj.y, dD[j + 1]);
+                        db[j] += du.x;
+                        db[j + 1] += du.y;
+                    }
+                }
+                Tile::store(static_cast<T *>(a.dx), a, w, t, w.f, k, dxv);
+                Tile::store(static_cast<T *>(a.ddt), a, w, t, w.f, k, ddv);
+                if (gated) Tile::store(static_cast<T *>(a.dz), a, w, t, w.f, k, dzv);
+            }
+            // dC and dB of the tile over the block's channels: four states of one of them a thread
+            for (int v = threadIdx.x; v < TT * L * 2; v += N) {
+                const int j = v / (2 * L), which = v % (2 * L) / L, q = v % L;
+                float2 s0 = both(0.f), s1 = s0;
+#pragma unroll 8
+                for (int p = 0; p < kPairs; ++p) {
+                    const int th = p * L + q;
+                    const float4 u = m.us[i & 1][j][th][which ^ (th >> 2 & 1)];
+                    s0 = add2(s0, make_float2(u.x, u.y));
+                    s1 = add2(s1, make_float2(u.z, u.w));
+                }
+                if (t + j < w.f) {
+                    const long long at = (((long long)mine * a.pack.T + t + j) * a.G + w.g) * 2 * NS + which * NS + 4 * q;
+                    if (in_range(at, 4, (long long)blocks * a.pack.T * a.G * 2 * NS, a.pack.status))
+                        *reinterpret_cast<float4 *>(a.part_bc + at) = make_float4(s0.x, s0.y, s1.x, s1.y);
+                }
+            }
+        };
+        fetch(0);
+        fetch(1);
+        copies_wait<1>();
+        if (tiles > 0) all(0);
+        __syncthreads();
+        for (int i = 0; i <= tiles; ++i) {
+            fetch(i + 2);
+            copies_wait<1>();
+            // (what a thread reads of a finished tile it is the one to write over)
+            if (i > 0) finish(i - 1);
+            if (i + 1 < tiles) all(i + 1);
+            __syncthreads();
+        }
+        float (*rows)[CB][2] = reinterpret_cast<float (*)[CB][2]>(smem);   // the rows of threads, in order
+        constexpr int kRows = N / Tile::kCols;
+#pragma unroll
+        for (int j = 0; j < kEV; ++j) {
+            rows[threadIdx.x / Tile::kCols][col + j][0] = dD[j];
+            rows[threadIdx.x / Tile::kCols][col + j][1] = db[j];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < CB; i += N) {
+            float s[2] = {};
+            for (int r = 0; r < kRows; ++r) {
+                s[0] += rows[r][i][0];
+                s[1] += rows[r][i][1];
+            }
+            const long long at = ((long long)w.item * a.C + w.c0 + i) * (NS + 2) + NS;
+            if (w.c0 + i < w.cend && in_range(at, 2, sums_extent, a.pack.status)) {
+                a.part_c[at] = s[0];
+                a.part_c[at + 1] = s[1];
+            }
+        }
+        return;
+    }
+
+    const PairLane<NS, N> lane(a, w);
+    const int me = (int)threadIdx.x - N;
+    const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
     // Forward: the states ahead of the tiles.
     float2 h[2][2];
     if (w.seg == 0) {
@@ -144,254 +358,118 @@ __global__ void __launch_bounds__(kScanThreads) k_scan_bwd(const __grid_constant
         lane.load(a.rec_h, w.item - w.seg, items, a, w, h);
         for (int i = w.item - w.seg + 1; i < w.item; ++i) lane.join(a, w, a.rec_h, i, h);
     }
-    typename Tile::V xn[Tile::NV], dn[Tile::NV], zn[Tile::NV], on[Tile::NV];
-    typename Rows::V bn[Rows::NU], cn[Rows::NU];
-    auto fetch = [&](int t) {
-        Tile::load(x, a.xs, a, w, t, w.f, xn);
-        Tile::load(dt, a.dts, a, w, t, w.f, dn);
-        Rows::load(B, a.bs, a, w, t, w.f, bn);
-    };
-    auto fetch_more = [&](int t) {
-        Tile::load(dy, a.C, a, w, t, w.f, on);
-        if (z) Tile::load(z, a.zs, a, w, t, w.f, zn);
-        Rows::load(Cm, a.cs, a, w, t, w.f, cn);
-    };
-    if (tiles > 0) fetch(w.b);
     __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0; i < tiles - 1; ++i) {
         lane.store(a.marks, mark + i, marks, a, w, h);
-        if (i == tiles - 1) break;   // (its last tile's end is nobody's start)
-        const int t = w.b + i * TT;
-#pragma unroll
-        for (int k = 0; k < Tile::NV; ++k) {
-            float d[kEV];
-            keep_inputs<TT, CB>(w, t, k, Tile::row(k), Tile::col(), xn[k], dn[k], bias, d, dd);
-        }
-        Rows::keep(bn, Bs);
-        __syncthreads();
-        fetch(t + TT);
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
-            const float4 in = dd[j][unit_at(lane.pair)];
-            const float4 b = *reinterpret_cast<const float4 *>(&Bs[j][4 * lane.q]);
+            const float4 in = m.dd[i & 1][j][unit_at(lane.at)];
+            const float4 b = *reinterpret_cast<const float4 *>(&m.B[i & 1][j][4 * lane.q]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                float2 decay[2];
-                lane.decays(p, p ? in.z : in.x, decay);
-                const float2 dx = both(p ? in.w : in.y);
-                h[p][0] = fma2(decay[0], h[p][0], mul2(dx, make_float2(b.x, b.y)));
-                h[p][1] = fma2(decay[1], h[p][1], mul2(dx, make_float2(b.z, b.w)));
+                const float2 d = both(p ? in.z : in.x), dx = both(p ? in.w : in.y);
+                h[p][0] = fma2(lane.decay(p, 0, d), h[p][0], mul2(dx, make_float2(b.x, b.y)));
+                h[p][1] = fma2(lane.decay(p, 1, d), h[p][1], mul2(dx, make_float2(b.z, b.w)));
             }
         }
         __syncthreads();
     }
-
-    // Backward.  g holds e^{d A} G of the token behind.
+    // Backward.  g holds e^{d A} G of the token behind; h, the states ahead of the tile, is read a tile ahead.
     float2 g[2][2], dA[2][2] = {};
-    lane.load(w.segs > 1 && w.seg < w.segs - 1 ? nullptr : a.ds1, w.n, a.pack.N, a, w, g);
+    lane.load(w.seg < w.segs - 1 ? nullptr : a.ds1, w.n, a.pack.N, a, w, g);
     if (w.seg < w.segs - 1) {
         const int last = w.item - w.seg + w.segs - 1;
         lane.load(a.rec_g, last, items, a, w, g);
         for (int i = last - 1; i > w.item; --i) lane.join(a, w, a.rec_g, i, g);
     }
-    float dD[kEV] = {}, db[kEV] = {};
-    const float ln2 = 0.693147180559945309f;
-    if (tiles > 0) {
-        fetch(w.b + (tiles - 1) * TT);
-        fetch_more(w.b + (tiles - 1) * TT);
-    }
-    for (int i = tiles - 1; i >= 0; --i) {
-        const int t = w.b + i * TT;
-        typename Tile::V xc[Tile::NV], zc[Tile::NV], oc[Tile::NV], uc[Tile::NV];
-        float d[Tile::NV][kEV];
+    __syncthreads();
+    for (int i = 0; i <= tiles; ++i) {
+        if (i < tiles) {
+            float2 ahead[2][2];
+            lane.load(i + 1 < tiles ? a.marks : nullptr, mark + tiles - 2 - i, marks, a, w, ahead);
+            float4 (*us)[2] = &m.us[i & 1][0][me];   // a token is N of them apart
 #pragma unroll
-        for (int k = 0; k < Tile::NV; ++k) {
-            const int row = Tile::row(k), col = Tile::col();
-            keep_inputs<TT, CB>(w, t, k, row, col, xn[k], dn[k], bias, d[k], dd);
-            if (row < TT) {
-                float o[kEV];
-#pragma unroll
-                for (int j = 0; j < kEV; ++j) {
-                    o[j] = as_float(on[k].x[j]);
-                    if (z) {
-                        const float zj = as_float(zn[k].x[j]);
-                        o[j] *= zj * sigmoid_of(zj);
-                    }
-                }
-                *reinterpret_cast<float4 *>(&os[row][col]) = make_float4(o[0], o[1], o[2], o[3]);
-            }
-            xc[k] = xn[k];
-            uc[k] = dn[k];
-            zc[k] = zn[k];
-            oc[k] = on[k];
-        }
-        Rows::keep(bn, Bs);
-        Rows::keep(cn, Cs);
-        lane.load(a.marks, mark + i, marks, a, w, h);
-        __syncthreads();
-        if (i > 0) {
-            fetch(t - TT);
-            fetch_more(t - TT);
-        }
-#pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const float4 in = dd[j][unit_at(lane.pair)];
-            const float4 b = *reinterpret_cast<const float4 *>(&Bs[j][4 * lane.q]);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                float2 decay[2];
-                lane.decays(p, p ? in.z : in.x, decay);
-                const float2 dx = both(p ? in.w : in.y);
-                const float2 u0 = mul2(decay[0], h[p][0]), u1 = mul2(decay[1], h[p][1]);
-                us[j][threadIdx.x][p ^ (threadIdx.x >> 2 & 1)] = make_float4(u0.x, u0.y, u1.x, u1.y);
-                h[p][0] = fma2(dx, make_float2(b.x, b.y), u0);
-                h[p][1] = fma2(dx, make_float2(b.z, b.w), u1);
-            }
-        }
-        float2 tileA[2][2] = {};
-#pragma unroll
-        for (int j0 = TT - BT; j0 >= 0; j0 -= BT) {
-            float part[BT][6];   // of each token: sum G B, sum p A / ln 2, sum C h of the two channels
-#pragma unroll
-            for (int jj = BT - 1; jj >= 0; --jj) {
-                const int j = j0 + jj;
-                const float4 in = dd[j][unit_at(lane.pair)];
-                const float2 o = *reinterpret_cast<const float2 *>(&os[j][2 * lane.pair]);
-                const float4 bb = *reinterpret_cast<const float4 *>(&Bs[j][4 * lane.q]);
-                const float4 cc = *reinterpret_cast<const float4 *>(&Cs[j][4 * lane.q]);
-                const float2 b[2] = {make_float2(bb.x, bb.y), make_float2(bb.z, bb.w)};
-                const float2 c[2] = {make_float2(cc.x, cc.y), make_float2(cc.z, cc.w)};
-                float2 dC[2], dB[2];
+            for (int j = 0; j < TT; ++j) {
+                const float4 in = m.dd[i & 1][j][unit_at(lane.at)];
+                const float4 b = *reinterpret_cast<const float4 *>(&m.B[i & 1][j][4 * lane.q]);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const float dp = p ? in.z : in.x;
-                    const float2 dx = both(p ? in.w : in.y), op = both(p ? o.y : o.x);
-                    const float4 uu = us[j][threadIdx.x][p ^ (threadIdx.x >> 2 & 1)];
-                    const float2 u[2] = {make_float2(uu.x, uu.y), make_float2(uu.z, uu.w)};
-                    float2 decay[2], sB, sA, sC;
-                    lane.decays(p, dp, decay);
+                    const float2 d = both(p ? in.z : in.x), dx = both(p ? in.w : in.y);
+                    const float2 u0 = mul2(lane.decay(p, 0, d), h[p][0]), u1 = mul2(lane.decay(p, 1, d), h[p][1]);
+                    us[j * N][p ^ (me >> 2 & 1)] = make_float4(u0.x, u0.y, u1.x, u1.y);
+                    h[p][0] = fma2(dx, make_float2(b.x, b.y), u0);
+                    h[p][1] = fma2(dx, make_float2(b.z, b.w), u1);
+                }
+            }
+            float2 tileA[2][2] = {};
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 hk = fma2(dx, b[k], u[k]);
-                        const float2 G = fma2(c[k], op, g[p][k]);
-                        const float2 pk = mul2(G, u[k]);
-                        dC[k] = p ? fma2(op, hk, dC[k]) : mul2(op, hk);
-                        dB[k] = p ? fma2(dx, G, dB[k]) : mul2(dx, G);
-                        sB = k ? fma2(G, b[k], sB) : mul2(G, b[k]);
-                        sA = k ? fma2(pk, lane.A[p][k], sA) : mul2(pk, lane.A[p][k]);
-                        sC = k ? fma2(c[k], hk, sC) : mul2(c[k], hk);
-                        tileA[p][k] = fma2(pk, both(dp), tileA[p][k]);
-                        g[p][k] = mul2(decay[k], G);
+            for (int j0 = TT - BT; j0 >= 0; j0 -= BT) {
+                float part[BT][6];   // of each token: sum G B, sum p A / ln 2, sum C h of the two channels
+#pragma unroll
+                for (int jj = BT - 1; jj >= 0; --jj) {
+                    const int j = j0 + jj;
+                    const float4 in = m.dd[i & 1][j][unit_at(lane.at)];
+                    const float2 o = *reinterpret_cast<const float2 *>(&m.os[i & 1][j][2 * lane.at]);
+                    const float4 bb = *reinterpret_cast<const float4 *>(&m.B[i & 1][j][4 * lane.q]);
+                    const float4 cc = *reinterpret_cast<const float4 *>(&m.C[i & 1][j][4 * lane.q]);
+                    const float2 b[2] = {make_float2(bb.x, bb.y), make_float2(bb.z, bb.w)};
+                    const float2 c[2] = {make_float2(cc.x, cc.y), make_float2(cc.z, cc.w)};
+                    float2 dC[2], dB[2];
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float2 d = both(p ? in.z : in.x), dx = both(p ? in.w : in.y), op = both(p ? o.y : o.x);
+                        const float4 uu = us[j * N][p ^ (me >> 2 & 1)];
+                        const float2 u[2] = {make_float2(uu.x, uu.y), make_float2(uu.z, uu.w)};
+                        float2 sB, sA, sC;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 hk = fma2(dx, b[k], u[k]);
+                            const float2 G = fma2(c[k], op, g[p][k]);
+                            const float2 pk = mul2(G, u[k]);
+                            dC[k] = p ? fma2(op, hk, dC[k]) : mul2(op, hk);
+                            dB[k] = p ? fma2(dx, G, dB[k]) : mul2(dx, G);
+                            sB = k ? fma2(G, b[k], sB) : mul2(G, b[k]);
+                            sA = k ? fma2(pk, lane.A[p][k], sA) : mul2(pk, lane.A[p][k]);
+                            sC = k ? fma2(c[k], hk, sC) : mul2(c[k], hk);
+                            tileA[p][k] = fma2(pk, d, tileA[p][k]);
+                            g[p][k] = mul2(lane.decay(p, k, d), G);
+                        }
+                        part[jj][p] = sB.x + sB.y;
+                        part[jj][2 + p] = sA.x + sA.y;
+                        part[jj][4 + p] = sC.x + sC.y;
                     }
-                    part[jj][p] = sB.x + sB.y;
-                    part[jj][2 + p] = sA.x + sA.y;
-                    part[jj][4 + p] = sC.x + sC.y;
+                    us[j * N][me >> 2 & 1] = make_float4(dC[0].x, dC[0].y, dC[1].x, dC[1].y);
+                    us[j * N][1 ^ (me >> 2 & 1)] = make_float4(dB[0].x, dB[0].y, dB[1].x, dB[1].y);
                 }
-                us[j][threadIdx.x][threadIdx.x >> 2 & 1] = make_float4(dC[0].x, dC[0].y, dC[1].x, dC[1].y);
-                us[j][threadIdx.x][1 ^ (threadIdx.x >> 2 & 1)] = make_float4(dB[0].x, dB[0].y, dB[1].x, dB[1].y);
-            }
-            pair_sums<L, BT, 6>(part, lane.q);
-            // (the pair's threads, all of this warp, have read what this takes the place of)
-            __syncwarp();
-            if (lane.q < BT) {
-                dd[j0 + lane.q][unit_at(lane.pair)] = make_float4(part[0][0], part[0][2], part[0][1], part[0][3]);
-                *reinterpret_cast<float2 *>(&os[j0 + lane.q][2 * lane.pair]) = make_float2(part[0][4], part[0][5]);
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) dA[p][k] = add2(dA[p][k], tileA[p][k]);
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < Tile::NV; ++k) {
-            const int row = Tile::row(k), col = Tile::col();
-            if (row >= TT) break;
-            typename Tile::V dxv, ddv, dzv;
-            float sums[kEV][2];   // sum G B, sum p A / ln 2
-#pragma unroll
-            for (int j = 0; j < kEV; j += 2) {
-                const float4 v = dd[row][unit_at((col + j) / 2)];
-                sums[j][0] = v.x;
-                sums[j][1] = v.y;
-                sums[j + 1][0] = v.z;
-                sums[j + 1][1] = v.w;
-            }
-#pragma unroll
-            for (int j = 0; j < kEV; ++j) {
-                const bool there = t + row < w.f && w.c0 + col + j < w.cend;
-                const float xj = as_float(xc[k].x[j]), dyj = as_float(oc[k].x[j]);
-                float o = dyj;
-                if (z) {
-                    const float zj = as_float(zc[k].x[j]), sig = sigmoid_of(zj);
-                    o *= zj * sig;
-                    dzv.x[j] = as_type<T>(dyj * fmaf(skip[col + j], xj, os[row][col + j]) * fmaf(zj * sig, 1.f - sig, sig));
-                }
-                dxv.x[j] = as_type<T>(fmaf(sums[j][0], d[k][j], skip[col + j] * o));
-                const float u = as_float(uc[k].x[j]) + bias[col + j];
-                const float du = fmaf(sums[j][1], ln2, sums[j][0] * xj) * sigmoid_of(u);
-                ddv.x[j] = as_type<T>(du);
-                if (there) {
-                    dD[j] = fmaf(o, xj, dD[j]);
-                    db[j] += du;
+                lane_sums<L, BT, 6>(part, lane.q);
+                // (the pair's threads, all of this warp, have read what this takes the place of)
+                __syncwarp();
+                if (lane.q < BT) {
+                    m.dd[i & 1][j0 + lane.q][unit_at(lane.at)] = make_float4(part[0][0], part[0][2], part[0][1], part[0][3]);
+                    *reinterpret_cast<float2 *>(&m.os[i & 1][j0 + lane.q][2 * lane.at]) = make_float2(part[0][4], part[0][5]);
                 }
             }
-            Tile::store(static_cast<T *>(a.dx), a, w, t, w.f, k, dxv);
-            Tile::store(static_cast<T *>(a.ddt), a, w, t, w.f, k, ddv);
-            if (z) Tile::store(static_cast<T *>(a.dz), a, w, t, w.f, k, dzv);
-        }
-        // dC and dB of the tile over the block's channels: four states of one of them a thread
-        const int blocks = (a.C / a.G + CB - 1) / CB, mine = (w.c0 - w.g * (a.C / a.G)) / CB;
-        for (int v = threadIdx.x; v < TT * L * 2; v += kScanThreads) {
-            const int j = v / (2 * L), which = v % (2 * L) / L, q = v % L;
-            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-#pragma unroll 8
-            for (int p = 0; p < kPairs; ++p) {
-                const int th = p * L + q;
-                const float4 u = us[j][th][which ^ (th >> 2 & 1)];
-                s0 = add2(s0, make_float2(u.x, u.y));
-                s1 = add2(s1, make_float2(u.z, u.w));
-            }
-            if (t + j < w.f) {
-                const long long at = (((long long)mine * a.pack.T + t + j) * a.G + w.g) * 2 * NS + which * NS + 4 * q;
-                if (in_range(at, 4, (long long)blocks * a.pack.T * a.G * 2 * NS, a.pack.status))
-                    *reinterpret_cast<float4 *>(a.part_bc + at) = make_float4(s0.x, s0.y, s1.x, s1.y);
-            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    dA[p][k] = add2(dA[p][k], tileA[p][k]);
+                    h[p][k] = ahead[p][k];
+                }
         }
         __syncthreads();
     }
+    __syncthreads();
     if (w.seg == 0 && a.ds0) lane.store(a.ds0, w.n, a.pack.N, a, w, g);
     // the segment's sums for the parameters, [items, C, NS + 2]
-    const long long extent = items * a.C * (NS + 2);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const long long at = ((long long)w.item * a.C + lane.c + p) * (NS + 2) + 4 * lane.q;
-        if (lane.c + p >= w.cend || !in_range(at, 4, extent, a.pack.status)) continue;
+        if (lane.c + p >= w.cend || !in_range(at, 4, sums_extent, a.pack.status)) continue;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             a.part_c[at + 2 * k] = dA[p][k].x * lane.A[p][k].x * ln2;
             a.part_c[at + 2 * k + 1] = dA[p][k].y * lane.A[p][k].y * ln2;
-        }
-    }
-    float (*rows)[CB][2] = reinterpret_cast<float (*)[CB][2]>(smem);   // the rows of threads, in order
-    constexpr int kRows = kScanThreads / Tile::kCols;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kEV; ++j) {
-        rows[threadIdx.x / Tile::kCols][Tile::col() + j][0] = dD[j];
-        rows[threadIdx.x / Tile::kCols][Tile::col() + j][1] = db[j];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < CB; i += kScanThreads) {
-        float s[2] = {};
-        for (int r = 0; r < kRows; ++r) {
-            s[0] += rows[r][i][0];
-            s[1] += rows[r][i][1];
-        }
-        const long long at = ((long long)w.item * a.C + w.c0 + i) * (NS + 2) + NS;
-        if (w.c0 + i < w.cend && in_range(at, 2, extent, a.pack.status)) {
-            a.part_c[at] = s[0];
-            a.part_c[at + 1] = s[1];
         }
     }
 }
@@ -439,15 +517,16 @@ __global__ void __launch_bounds__(256) k_scan_params(const __grid_constant__ Sca
 
 template <typename T, int NS, bool kWide>
 cudaError_t bwd(const ScanArgs &a, cudaStream_t s) {
-    constexpr int CB = ScanShape<NS>::CB, TT = kMarkTile;
-    constexpr size_t bytes = (size_t)TT * (kScanThreads * 32 + CB * 8 + CB * 4 + NS * 8) + CB * 8;
-    static_assert(bytes <= 48 * 1024, "no more than a kernel has without asking");
-    static_assert(kScanThreads / (CB / kEV) * CB * 8 <= TT * kScanThreads * 32, "the last sums fit the states' place");
-    const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<NS>(a);
+    constexpr int CB = PairShape<NS>::CB;
+    constexpr int bytes = (int)sizeof(BackTiles<T, NS>);
+    static_assert(kScanThreads / (CB / kEV) * CB * 8 <= sizeof(BackTiles<T, NS>::us), "the last sums fit the states' place");
+    const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<PairShape<NS>::CB>(a);
     if (a.seg <= a.pack.T) k_scan_starts<T, NS, kWide><<<(unsigned)blocks, kScanThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_scan_bwd<T, NS, kWide><<<(unsigned)(blocks + (a.pack.status ? 1 : 0)), kScanThreads, bytes, s>>>(a);
+    e = cudaFuncSetAttribute(k_scan_bwd<T, NS, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    k_scan_bwd<T, NS, kWide><<<(unsigned)(blocks + (a.pack.status ? 1 : 0)), 2 * kScanThreads, bytes, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long units = (long long)a.pack.T * a.G * 2 * NS / 4;

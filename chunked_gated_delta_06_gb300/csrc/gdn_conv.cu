@@ -29,6 +29,21 @@ struct Channels {
     int c;
     float w[W][V], b[V];
     __device__ Channels(const ConvArgs &args, int channel) : a(args), c(channel) {
+        if constexpr (V % 4 == 0) {   // the V channels' weights lie together
+            if (reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && in_range((long long)c * W, V * W, (long long)a.C * W, a.pack.status)) {
+                float all[V * W];
+#pragma unroll
+                for (int i = 0; i < V * W / 4; ++i)
+                    reinterpret_cast<float4 *>(all)[i] = reinterpret_cast<const float4 *>(a.w + (long long)c * W)[i];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) w[j][v] = all[v * W + j];
+                    b[v] = a.bias ? a.bias[c + v] : 0.f;
+                }
+                return;
+            }
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const bool there = in_range((long long)(c + v) * W, W, (long long)a.C * W, a.pack.status);
@@ -58,9 +73,7 @@ struct Channels {
         for (int k = 0; k < W - 1; ++k) {
             const int p = t - (W - 1) + k;
             if (p >= s) {
-                const Vec<T, V> x = token(a.x, p, a.x_stride);
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[k][v] = as_float(x.x[v]);
+                unpack(token(a.x, p, a.x_stride), win[k]);
             } else {
                 state(a.s0, row, rows(), p - s + W - 1, win[k]);
             }
@@ -105,12 +118,40 @@ __device__ void final_state(const ConvArgs &a, int n, int c) {
         for (int k = 0; k < W - 1; ++k) static_cast<T *>(a.s1)[i + k] = as_type<T>(out[k]);
 }
 
-// A thread walks the tokens of a tile for V channels with the last W - 1 inputs in registers, U
-// tokens' loads at once.  The blocks behind those of the tiles write the states behind the
-// sequences (over a pool they are a launch of their own: the tiles still read the slots).
+// A thread's own inputs on their way: `kTensors` rows of V channels a token, kGroup tokens at a time,
+// kAhead groups ahead, copied into shared memory asynchronously (so that no registers wait for them).
+template <typename T, int V, int kTensors>
+struct Stream {
+    static constexpr int kGroup = 4, kAhead = 3, kStages = kAhead + 1;
+    using Row = Vec<T, V>;
+    Row *ring;           // [kStages][kGroup][kTensors][threads]
+    int t, end;          // the next token to fetch, the last one's successor
+    int stage;
+    __device__ Row *place(int st, int u, int k) const { return ring + ((st * kGroup + u) * kTensors + k) * kThreads + threadIdx.x; }
+    template <typename F>   // address(token, tensor): where its row is, null for none
+    __device__ void fetch(F address) {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+#pragma unroll
+            for (int k = 0; k < kTensors; ++k) {
+                const T *from = t + u < end ? address(t + u, k) : nullptr;
+                if (!from) continue;
+                if constexpr (sizeof(Row) >= 4) copy_async<(int)sizeof(Row)>(place(stage, u, k), from, true);
+                else *place(stage, u, k) = *reinterpret_cast<const Row *>(from);
+            }
+        copies_commit();
+        t += kGroup;
+        stage = (stage + 1) % kStages;
+    }
+};
+
+// A thread walks the tokens of a tile for V channels with the last W - 1 inputs in registers.  Bound by
+// HBM.  The blocks behind those of the tiles write the states behind the sequences (over a pool they
+// are a launch of their own: the tiles still read the slots).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ ConvArgs a, int across, long long blocks) {
-    constexpr int U = 8;
+    using In = Stream<T, V, 1>;
+    __shared__ __align__(16) T ring[In::kStages * In::kGroup * kThreads * V];
     const long long block = blockIdx.x;
     if (block >= blocks) {
         const int per = (a.C + kThreads - 1) / kThreads;
@@ -122,44 +163,59 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
     const int c = ((int)(block % across) * kThreads + (int)threadIdx.x) * V;
     if (c >= a.C) return;
     const int t0 = (int)(block / across) * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
+    const long long extent = (long long)a.pack.T * a.C, x_extent = (a.pack.T - 1) * a.x_stride + a.C;
+    In in{reinterpret_cast<Vec<T, V> *>(ring), t0, t1, 0};
+    auto address = [&](int t, int) -> const T * {
+        const long long at = t * a.x_stride + c;
+        return in_range(at, V, x_extent, a.pack.status) ? static_cast<const T *>(a.x) + at : nullptr;
+    };
+#pragma unroll
+    for (int g = 0; g < In::kAhead; ++g) in.fetch(address);
     const Channels<T, V, W> ch(a, c);
-    T *y = static_cast<T *>(a.y);
-    const long long extent = (long long)a.pack.T * a.C;
-    for (int t = t0; t < t1;) {
-        const int n = sequence_of(a.pack, t), s = min(offset_of(a.pack, n), t);
-        int end = offset_of(a.pack, n + 1);
-        end = end > t ? min(end, t1) : t1;
-        float win[W][V];
-        ch.window(n, s, t, win);
-        auto one = [&](const Vec<T, V> &x) {
-            Vec<T, V> out;
+    T *y = static_cast<T *>(a.y) + (long long)t0 * a.C + c;
+    float win[W][V];
+    int end = t0, stage = 0;
+    for (int t = t0; t < t1; t += In::kGroup) {
+        in.fetch(address);
+        copies_wait<In::kAhead>();
+        auto one = [&](int u) {
+            unpack(*in.place(stage, u, 0), win[W - 1]);
+            float out[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                win[W - 1][v] = as_float(x.x[v]);
-                const float u = ch.pre(win, v);
-                out.x[v] = as_type<T>(a.silu ? u * sigmoid_of(u) : u);
+                out[v] = ch.pre(win, v);
+                if (a.silu) out[v] *= sigmoid_of(out[v]);
             }
             ch.shift(win);
-            store_vec<V>(y, (long long)t * a.C + c, extent, a.pack.status, out);
-            ++t;
+            store_vec<V>(y, 0, extent - (y - static_cast<T *>(a.y)), a.pack.status, pack<T>(out));
+            y += a.C;
         };
-        for (; t + U <= end;) {
-            Vec<T, V> x[U];
+        if (t != end && t + In::kGroup <= end) {   // (all of one sequence: the window moves by names alone)
 #pragma unroll
-            for (int u = 0; u < U; ++u) x[u] = ch.token(a.x, t + u, a.x_stride);
-#pragma unroll
-            for (int u = 0; u < U; ++u) one(x[u]);
+            for (int u = 0; u < In::kGroup; ++u) one(u);
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < In::kGroup && t + u < t1; ++u) {
+                if (t + u == end) {   // the tile's first token, or a sequence's
+                    const int n = sequence_of(a.pack, end), s = min(offset_of(a.pack, n), end), e = offset_of(a.pack, n + 1);
+                    ch.window(n, s, end, win);
+                    end = e > end ? min(e, t1) : t1;
+                }
+                one(u);
+            }
         }
-        for (; t < end;) one(ch.token(a.x, t, a.x_stride));
+        stage = (stage + 1) % In::kStages;
     }
 }
 
 // A thread walks a tile and the W - 1 tokens behind it: at token t it has d_t and, with the d's
-// before, dx of token t - (W - 1) (where that lies ahead of the sequence, of its state's entry).
-// Sums for dw and dbias are of the tile's own tokens; k_fold adds the tiles.
+// before, dx of token t - (W - 1) (where that lies ahead of the sequence, of its state's entry); behind
+// the last token of a sequence come W - 1 more with d = 0.  Sums for dw and dbias are of the tile's own
+// tokens; k_fold adds the tiles.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ ConvArgs a, int across, long long blocks) {
-    constexpr int U = 4;
+    using In = Stream<T, V, 2>;
+    extern __shared__ __align__(16) unsigned char ring[];
     const long long block = blockIdx.x;
     if (block >= blocks) {   // sequences without tokens: the state passed through
         const int per = (a.C + kThreads - 1) / kThreads;
@@ -181,96 +237,118 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     if (c >= a.C) return;
     const int tile = (int)(block / across);
     const int t0 = tile * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
+    const int reach = (int)min((long long)t1 + W - 1, (long long)a.pack.T);
+    const long long extent = (long long)a.pack.T * a.C, x_extent = (a.pack.T - 1) * a.x_stride + a.C;
+    In in{reinterpret_cast<Vec<T, V> *>(ring), t0, reach, 0};
+    auto address = [&](int t, int k) -> const T * {
+        const long long at = t * (k ? (long long)a.C : a.x_stride) + c;
+        return in_range(at, V, k ? extent : x_extent, a.pack.status) ? static_cast<const T *>(k ? a.dy : a.x) + at : nullptr;
+    };
+#pragma unroll
+    for (int g = 0; g < In::kAhead; ++g) in.fetch(address);
     const Channels<T, V, W> ch(a, c);
     T *dx = static_cast<T *>(a.dx);
-    const long long extent = (long long)a.pack.T * a.C;
-    float dw[W][V] = {}, db[V] = {};
-    for (int p = t0; p < t1;) {
-        const int n = sequence_of(a.pack, p), s = min(offset_of(a.pack, n), p);
-        int e = offset_of(a.pack, n + 1);
-        e = e > p ? e : t1;
-        const int q = min(e, t1);
-        float win[W][V], d[W][V] = {};   // d[k] = d_{t-(W-1)+k}
-        ch.window(n, s, p, win);
-        auto slope = [&](const Vec<T, V> &x, const Vec<T, V> &dy) {   // d_t, with x_t in the window
+    float dw[W][V] = {}, db[V] = {}, win[W][V] = {}, d[W][V] = {};   // d[k] = d_{t-(W-1)+k}
+    int n = 0, s = t0, e = t0, p = t0;   // the sequence and its part of the tile, [p, min(e, t1))
+    // dx of token `at`, from the d's of `at` and the W - 1 behind it; past: of a sequence's last ones
+    auto emit = [&](int at, bool past) {
+        if (at >= min(e, t1) || (at < p && p != s)) return;
+        float g[V] = {};   // the final state's gradient: entry k holds input e - (W - 1) + k
+        if (past && a.ds1) ch.state(a.ds1, n, a.pack.N, at - e + W - 1, g);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < W; ++j) g[v] = fmaf(ch.w[j][v], d[W - 1 - j][v], g[v]);
+        const Vec<T, V> out = pack<T>(g);
+        if (at >= p) {
+            store_vec<V>(dx, (long long)at * a.C + c, extent, a.pack.status, out);
+        } else if (a.ds0) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                win[W - 1][v] = as_float(x.x[v]);
-                d[W - 1][v] = as_float(dy.x[v]);
+                const long long i = ((long long)n * a.C + c + v) * (W - 1) + (at - s + W - 1);
+                if (in_range(i, 1, (long long)a.pack.N * a.C * (W - 1), a.pack.status))
+                    static_cast<T *>(a.ds0)[i] = out.x[v];
+            }
+        }
+    };
+    auto run_out = [&] {
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[W - 1][v] = 0.f;
+            emit(e + i - (W - 1), true);
+            ch.shift(d);
+        }
+    };
+    int stage = 0;
+    bool open = false;   // a sequence is being walked
+    for (int t = t0; t < reach; t += In::kGroup) {
+        in.fetch(address);
+        copies_wait<In::kAhead>();
+        auto one = [&](int u, bool own) {   // d_t, and the sums of the tile's own tokens
+            unpack(*in.place(stage, u, 0), win[W - 1]);
+            unpack(*in.place(stage, u, 1), d[W - 1]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float g = d[W - 1][v];
                 if (a.silu) {
-                    const float u = ch.pre(win, v), sig = sigmoid_of(u);
-                    d[W - 1][v] *= fmaf(u * sig, 1.f - sig, sig);
+                    const float o = ch.pre(win, v), sig = sigmoid_of(o);
+                    g *= fmaf(o * sig, 1.f - sig, sig);
+                }
+                d[W - 1][v] = g;
+                if (own) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][v] = fmaf(g, win[j][v], dw[j][v]);
+                    db[v] += g;
                 }
             }
         };
-        auto sums = [&] {
+        if (open && t - (W - 1) >= p && t + In::kGroup <= min(e, t1)) {
+            // (all of one sequence, every token's dx of the tile: windows move by names alone)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+            for (int u = 0; u < In::kGroup; ++u) {
+                one(u, true);
+                float g[V];
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][v] = fmaf(d[W - 1][v], win[j][v], dw[j][v]);
-                db[v] += d[W - 1][v];
-            }
-        };
-        auto gradient = [&](int v) {
-            float g = 0.f;
+                for (int v = 0; v < V; ++v) {
+                    g[v] = 0.f;
 #pragma unroll
-            for (int j = 0; j < W; ++j) g = fmaf(ch.w[j][v], d[W - 1 - j][v], g);
-            return g;
-        };
-        for (int t = p; t < q + W - 1;) {
-            // in the middle: every token of the group has its own dx, none of them reaches the state
-            if (t - (W - 1) >= p && t + U <= q) {
-                Vec<T, V> x[U], dy[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    x[u] = ch.token(a.x, t + u, a.x_stride);
-                    dy[u] = ch.token(a.dy, t + u, a.C);
+                    for (int j = 0; j < W; ++j) g[v] = fmaf(ch.w[j][v], d[W - 1 - j][v], g[v]);
                 }
-#pragma unroll
-                for (int u = 0; u < U; ++u, ++t) {
-                    slope(x[u], dy[u]);
-                    sums();
-                    Vec<T, V> out;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) out.x[v] = as_type<T>(gradient(v));
-                    store_vec<V>(dx, (long long)(t - (W - 1)) * a.C + c, extent, a.pack.status, out);
-                    ch.shift(win);
-                    ch.shift(d);
-                }
-                continue;
+                store_vec<V>(dx, (long long)(t + u - (W - 1)) * a.C + c, extent, a.pack.status, pack<T>(g));
+                ch.shift(win);
+                ch.shift(d);
             }
-            if (t < e && t < a.pack.T) {
-                slope(ch.token(a.x, t, a.x_stride), ch.token(a.dy, t, a.C));
-            } else {
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < In::kGroup && t + u < reach; ++u) {
+                const int at = t + u;
+                if (at == e) {
+                    if (open) run_out();
+                    open = at < t1;
+                    if (open) {
+                        n = sequence_of(a.pack, at);
+                        s = min(offset_of(a.pack, n), at);
+                        e = offset_of(a.pack, n + 1);
+                        e = e > at ? e : t1;
+                        p = at;
+                        ch.window(n, s, p, win);
 #pragma unroll
-                for (int v = 0; v < V; ++v) d[W - 1][v] = 0.f;
-            }
-            if (t < q) sums();
-            const int at = t - (W - 1);
-            if (at >= p || p == s) {
-                // the final state's gradient: entry k holds input e - (W - 1) + k
-                float tail[V] = {};
-                if (a.ds1 && at >= e - (W - 1)) ch.state(a.ds1, n, a.pack.N, at - e + W - 1, tail);
-                Vec<T, V> out;
+                        for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-                for (int v = 0; v < V; ++v) out.x[v] = as_type<T>(gradient(v) + tail[v]);
-                if (at >= p) {
-                    store_vec<V>(dx, (long long)at * a.C + c, extent, a.pack.status, out);
-                } else if (a.ds0) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const long long i = ((long long)n * a.C + c + v) * (W - 1) + (at - s + W - 1);
-                        if (in_range(i, 1, (long long)a.pack.N * a.C * (W - 1), a.pack.status))
-                            static_cast<T *>(a.ds0)[i] = out.x[v];
+                            for (int v = 0; v < V; ++v) d[k][v] = 0.f;
                     }
                 }
+                if (!open) break;
+                one(u, at < t1);
+                emit(at - (W - 1), false);
+                ch.shift(win);
+                ch.shift(d);
             }
-            ch.shift(win);
-            ch.shift(d);
-            ++t;
         }
-        p = q;
+        stage = (stage + 1) % In::kStages;
     }
+    if (open && e <= reach) run_out();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const long long i = ((long long)tile * a.C + c + v) * (W + 1);
@@ -281,65 +359,78 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     }
 }
 
-// One thread for V channels of a row; their entries of the slot lie together, (W - 1) V of them.
+// One thread for V channels of `rows` rows, one after another (its weights are read once, the next
+// row's state while this one is computed); a row's entries of the slot lie together, (W - 1) V of them.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) k_conv_step(const __grid_constant__ ConvArgs a, int across) {
-    const int b = blockIdx.x / across;
+__global__ void __launch_bounds__(kThreads) k_conv_step(const __grid_constant__ ConvArgs a, int across, int rows) {
     const int c = ((int)(blockIdx.x % across) * kThreads + (int)threadIdx.x) * V;
     if (c >= a.C) return;
-    const int slot = slot_of(a.slots, b);
-    T *y = static_cast<T *>(a.y);
-    const long long extent = (long long)a.pack.T * a.C;
-    Vec<T, V> out;
-    if (slot < 0) {
-        if (c == 0 && a.slots.status && a.slots.idx[b] >= a.slots.num_slots) *a.slots.status = 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) out.x[v] = as_type<T>(0.f);
-        store_vec<V>(y, (long long)b * a.C + c, extent, a.pack.status, out);
-        return;
-    }
-    using Rows = Vec<T, V>;
-    const long long i = ((long long)slot * a.C + c) * (W - 1), n = (long long)a.slots.num_slots * a.C * (W - 1);
-    T *pool = static_cast<T *>(a.s1);
+    T *y = static_cast<T *>(a.y), *pool = static_cast<T *>(a.s1);
+    const long long extent = (long long)a.pack.T * a.C, n = (long long)a.slots.num_slots * a.C * (W - 1);
+    const int b0 = (int)(blockIdx.x / across) * rows, b1 = min(b0 + rows, a.pack.T);
     const Channels<T, V, W> ch(a, c);
-    const Vec<T, V> x = ch.token(a.x, b, a.x_stride);
-    Rows old[W - 1];
+    struct Row {
+        int slot;
+        Vec<T, V> x, old[W - 1];
+    };
+    auto entry_at = [&](int slot) { return ((long long)slot * a.C + c) * (W - 1); };
+    auto read = [&](int b, Row &r) {
+        r.slot = slot_of(a.slots, b);
+        if (r.slot < 0) return;
+        r.x = ch.token(a.x, b, a.x_stride);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) old[k] = load_vec<V>(pool, i + k * V, n, a.pack.status);
-    auto entry = [&](int at) { return old[at / V].x[at % V]; };
-    Rows next[W - 1];
+        for (int k = 0; k < W - 1; ++k) r.old[k] = load_vec<V>(pool, entry_at(r.slot) + k * V, n, a.pack.status);
+    };
+    Row row, next;
+    read(b0, row);
+    for (int b = b0; b < b1; ++b) {
+        // (no two active rows have one slot: what the next row reads this one does not write)
+        if (b + 1 < b1) read(b + 1, next);
+        Vec<T, V> out;
+        if (row.slot < 0) {
+            if (c == 0 && a.slots.status && a.slots.idx[b] >= a.slots.num_slots) *a.slots.status = 1;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float u = fmaf(ch.w[W - 1][v], as_float(x.x[v]), ch.b[v]);
+            for (int v = 0; v < V; ++v) out.x[v] = as_type<T>(0.f);
+        } else {
+            auto entry = [&](int at) { return row.old[at / V].x[at % V]; };
+            Vec<T, V> now[W - 1];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) u = fmaf(ch.w[j][v], as_float(entry(v * (W - 1) + j)), u);
-        out.x[v] = as_type<T>(a.silu ? u * sigmoid_of(u) : u);
+            for (int v = 0; v < V; ++v) {
+                float u = fmaf(ch.w[W - 1][v], as_float(row.x.x[v]), ch.b[v]);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const int at = v * (W - 1) + j;
-            next[at / V].x[at % V] = j + 1 < W - 1 ? entry(at + 1) : x.x[v];
+                for (int j = 0; j < W - 1; ++j) u = fmaf(ch.w[j][v], as_float(entry(v * (W - 1) + j)), u);
+                out.x[v] = as_type<T>(a.silu ? u * sigmoid_of(u) : u);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    const int at = v * (W - 1) + j;
+                    now[at / V].x[at % V] = j + 1 < W - 1 ? entry(at + 1) : row.x.x[v];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) store_vec<V>(pool, entry_at(row.slot) + k * V, n, a.pack.status, now[k]);
         }
+        store_vec<V>(y, (long long)b * a.C + c, extent, a.pack.status, out);
+        row = next;
     }
-    store_vec<V>(y, (long long)b * a.C + c, extent, a.pack.status, out);
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) store_vec<V>(pool, i + k * V, n, a.pack.status, next[k]);
 }
 
-// Block of 32 columns and 8 groups of rows: group g adds rows g, g + 8, ...; then the groups in order.
-__global__ void __launch_bounds__(256) k_fold(const __grid_constant__ FoldArgs a) {
-    __shared__ float sums[8][32];
+// Block of 32 columns and 32 groups of rows: group g adds rows g, g + 32, ...; then the groups in order.
+constexpr int kFoldGroups = 32;
+__global__ void __launch_bounds__(32 * kFoldGroups) k_fold(const __grid_constant__ FoldArgs a) {
+    __shared__ float sums[kFoldGroups][33];
     const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
     const long long col = (long long)blockIdx.x * 32 + lane;
     float sum = 0.f;
     if (col < a.cols && in_range(col, 1, a.cols, nullptr)) {
         const float *p = a.part + col;
 #pragma unroll 4
-        for (long long r = group; r < a.rows; r += 8) sum += p[r * a.cols];
+        for (long long r = group; r < a.rows; r += kFoldGroups) sum += p[r * a.cols];
     }
     sums[group][lane] = sum;
     __syncthreads();
     if (group || col >= a.cols) return;
-    for (int g = 1; g < 8; ++g) sum += sums[g][lane];
+#pragma unroll
+    for (int g = 1; g < kFoldGroups; ++g) sum += sums[g][lane];
     const long long at = col / a.per;
     const int k = (int)(col % a.per);
     if (k < a.keep) a.main[at * a.keep + k] = sum;
@@ -358,8 +449,8 @@ int tile_of(long long T, long long across, int most) {
 
 template <typename T, int W>
 cudaError_t conv_fwd(ConvArgs &a, cudaStream_t s) {
-    constexpr int V = 16 / (int)sizeof(T);
-    const bool wide = a.C % V == 0 && a.x_stride % V == 0 && fits(a.x, 16) && fits(a.y, 16);
+    constexpr int V = 16 / (int)sizeof(T), kBytes = 16;
+    const bool wide = a.C % V == 0 && a.x_stride % V == 0 && fits(a.x, kBytes) && fits(a.y, kBytes);
     const int vec = wide ? V : 1;
     const int across = (a.C + kThreads * vec - 1) / (kThreads * vec);
     a.tile = tile_of(a.pack.T, across, 64);
@@ -393,8 +484,15 @@ cudaError_t conv_bwd(ConvArgs &a, cudaStream_t s) {
     const int across = (a.C + kThreads * vec - 1) / (kThreads * vec);
     const long long blocks = (long long)a.tiles * across;
     const long long grid = blocks + (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads) + (a.pack.status ? 1 : 0);
-    if (wide) k_conv_bwd<T, V, W><<<(unsigned)grid, kThreads, 0, s>>>(a, across, blocks);
-    else k_conv_bwd<T, 1, W><<<(unsigned)grid, kThreads, 0, s>>>(a, across, blocks);
+    constexpr int kRing = Stream<T, 1, 2>::kStages * Stream<T, 1, 2>::kGroup * 2 * kThreads * (int)sizeof(T);   // a channel
+    static_assert(kRing * V <= 64 * 1024, "three blocks an SM");
+    if (wide) {
+        const cudaError_t e = cudaFuncSetAttribute(k_conv_bwd<T, V, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * V);
+        if (e != cudaSuccess) return e;
+        k_conv_bwd<T, V, W><<<(unsigned)grid, kThreads, kRing * V, s>>>(a, across, blocks);
+    } else {
+        k_conv_bwd<T, 1, W><<<(unsigned)grid, kThreads, kRing, s>>>(a, across, blocks);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     FoldArgs f{a.part, a.tiles, (long long)a.C * (W + 1), W + 1, W, a.dw, a.dbias};
@@ -407,9 +505,11 @@ cudaError_t conv_step(const ConvArgs &a, int batch, cudaStream_t s) {
     const bool wide = a.C % V == 0 && a.x_stride % V == 0 && fits(a.x, 16) && fits(a.y, 16) && fits(a.s1, 16);
     const int vec = wide ? V : 1;
     const int across = (a.C + kThreads * vec - 1) / (kThreads * vec);
-    const unsigned grid = (unsigned)((long long)batch * across);
-    if (wide) k_conv_step<T, V, W><<<grid, kThreads, 0, s>>>(a, across);
-    else k_conv_step<T, 1, W><<<grid, kThreads, 0, s>>>(a, across);
+    // rows of a thread: up to 8, as long as every SM has four blocks
+    const int rows = (int)std::max(1LL, std::min(8LL, (long long)batch * across / (4 * 152)));
+    const unsigned grid = (unsigned)((batch + rows - 1) / rows * (long long)across);
+    if (wide) k_conv_step<T, V, W><<<grid, kThreads, 0, s>>>(a, across, rows);
+    else k_conv_step<T, 1, W><<<grid, kThreads, 0, s>>>(a, across, rows);
     return cudaGetLastError();
 }
 
@@ -417,7 +517,7 @@ cudaError_t conv_step(const ConvArgs &a, int batch, cudaStream_t s) {
 
 cudaError_t launch_fold(const FoldArgs &a, cudaStream_t s) {
     if (a.cols == 0) return cudaSuccess;
-    k_fold<<<(unsigned)((a.cols + 31) / 32), 256, 0, s>>>(a);
+    k_fold<<<(unsigned)((a.cols + 31) / 32), 32 * kFoldGroups, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -19,6 +19,38 @@ __device__ __forceinline__ bf16 as_type<bf16>(float x) { return f2bf(x); }
 template <>
 __device__ __forceinline__ float as_type<float>(float x) { return x; }
 
+// All of a vector's elements as floats, and back, each rounded once.  (bf16 in words: a shift or a mask an
+// element, one conversion a pair; element by element the halves are taken apart and put together too.)
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V> &v, float (&f)[V]) {
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 p = bf2_to_f2(reinterpret_cast<const uint32_t *>(&v)[i]);
+            f[2 * i] = p.x;
+            f[2 * i + 1] = p.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = as_float(v.x[i]);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
+    Vec<T, V> v;
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            reinterpret_cast<uint32_t *>(&v)[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v.x[i] = as_type<T>(f[i]);
+    }
+    return v;
+}
+
 // V elements from i on of a buffer of n (zeros outside it, in the checked build).
 template <int V, typename T>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *p, long long i, long long n, int *status) {
@@ -51,6 +83,18 @@ __device__ __forceinline__ float reciprocal_of(float x) {
 // 1 / (1 + e^-x): good to about 2^-21 for |x| < 10 (2^-24 |x| beyond), which a result in bf16 does
 // not see and one in fp32 bears.
 __device__ __forceinline__ float sigmoid_of(float x) { return reciprocal_of(1.f + exp_of(-x)); }
+
+// Asynchronous copies of `bytes` (4, 8 or 16) into shared memory; zeros instead where there is nothing.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void *to, const void *from, bool there) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    const int n = there ? kBytes : 0;
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(kBytes), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
 
 // The sequence of token t: the last n with cu[n] <= t.
 __device__ __forceinline__ int sequence_of(const PackArgs &p, int t) {

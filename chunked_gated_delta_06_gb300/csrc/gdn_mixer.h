@@ -96,7 +96,7 @@ struct NormArgs {
     long long R;
     int D, f32, res;          // res: -1 none, else the stream's GDN_DTYPE_*
     int gate;                 // GDN_GATE_*
-    float eps, offset;
+    float eps, offset, per_d; // per_d: 1 / D
     const void *x, *residual; // forward: the branch and the stream; backward: x for dscale, or null
     const float *scale, *w;   // [D]; scale or null
     const void *z;            // or null
@@ -107,7 +107,7 @@ struct NormArgs {
     float *part;              // [blocks, 2 or 1, D]
 };
 // blocks of the backward (they set the size of its workspace)
-int norm_bwd_blocks(long long R, int D, int f32);
+int norm_bwd_blocks(long long R, int D);
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s);
 

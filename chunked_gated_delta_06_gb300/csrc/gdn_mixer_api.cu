@@ -183,8 +183,8 @@ constexpr int kNoSplit = 0x7fffffff;
 // 90 ns, backward 300 ns), a walk takes as long as its longest chain, a fifth more for the blocks that
 // share its SM, or as all its blocks' tokens over the SMs (which a second block on an SM makes worth 1.08
 // or 1.4) and half a segment for the last ones; a split scan walks its segments for their ends first
-// (0.66 of a forward, 0.3 of a backward), and costs about 60 tokens for the launches and two for each
-// record that a block joins.  Forward of 4 x 4096 tokens of 4096 channels: 365 us, split 510; of 65536
+// (0.66 of a forward, 0.3 of a backward), and costs about 60 tokens for the launches and one for each
+// segment of the longest sequence, whose records are joined one after another.  Forward of 4 x 4096 tokens of 4096 channels: 365 us, split 510; of 65536
 // tokens of 2048: 5710 us, split 1004.  Backward: 1699 and 1918, of 11 sequences up to 6969 tokens 2357
 // and 1958.
 int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &pack, int for_backward) {
@@ -209,7 +209,7 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         const double bytes = 4.0 * (pack.N + pack.T / L) * s->channels * (2.0 * s->state_dim + 1.0);
         if (bytes > 1073741824.0) continue;
         auto walk = [&](double tokens) { return std::max((double)L, tokens * across / places + 0.5 * L); };
-        const double t = first * walk(ends) + walk(pack.T) + 60.0 + 2.0 * (longest / L);
+        const double t = first * walk(ends) + walk(pack.T) + 60.0 + longest / L;
         if (t < best) {
             best = t;
             seg = L;
@@ -237,7 +237,8 @@ size_t carve_scan(const gdn_scan_shape *s, gdn::ScanArgs &a, int for_backward, v
 
 bool scan_grid_fits(const gdn_scan_shape *s, const gdn::ScanArgs &a) {
     const int64_t bc = (int64_t)a.pack.T * s->groups * s->state_dim / 512, par = (int64_t)s->channels * 34 / 256;
-    return (gdn::scan_items(a.pack.N, a.pack.T, a.seg) + 1) * scan_across(s, 1) < kGrid && bc + 1 < kGrid && par + 1 < kGrid;
+    const int64_t join = ((int64_t)s->channels * s->state_dim / 512 + 1) * a.pack.N;
+    return (gdn::scan_items(a.pack.N, a.pack.T, a.seg) + 1) * scan_across(s, 1) < kGrid && bc + 1 < kGrid && par + 1 < kGrid && join < kGrid;
 }
 
 gdn::ScanArgs scan_args(const gdn::PackArgs &pack, const gdn_scan_shape *s, const ScanWidth &w, const void *x,
@@ -358,15 +359,16 @@ gdn::NormArgs norm_args(int64_t rows, int32_t dim, int32_t dtype, int32_t residu
     a.gate = gate;
     a.eps = eps;
     a.offset = offset;
+    a.per_d = 1.f / (float)dim;
     a.scale = scale;
     a.w = weight;
     a.z = z;
     return a;
 }
 
-size_t norm_workspace(int64_t rows, int32_t dim, int32_t dtype, bool scale) {
+size_t norm_workspace(int64_t rows, int32_t dim, bool scale) {
     Carver c(nullptr);
-    c.take<float>((size_t)gdn::norm_bwd_blocks(rows, dim, dtype == GDN_DTYPE_F32) * (scale ? 2 : 1) * dim);
+    c.take<float>((size_t)gdn::norm_bwd_blocks(rows, dim) * (scale ? 2 : 1) * dim);
     return c.used();
 }
 
@@ -610,7 +612,7 @@ gdn_status gdn_rms_norm_fwd(int64_t rows, int32_t dim, int32_t dtype, int32_t re
 
 size_t gdn_rms_norm_workspace_bytes(int64_t rows, int32_t dim, int32_t dtype, int32_t with_scale) {
     if (rows < 0 || rows > ((int64_t)1 << 30) || dim < 1 || dim > 8192 || !known(dtype)) return 0;
-    return norm_workspace(rows, dim, dtype, with_scale != 0);
+    return norm_workspace(rows, dim, with_scale != 0);
 }
 
 gdn_status gdn_rms_norm_bwd(int64_t rows, int32_t dim, int32_t dtype, int32_t residual_dtype,
@@ -630,7 +632,7 @@ gdn_status gdn_rms_norm_bwd(int64_t rows, int32_t dim, int32_t dtype, int32_t re
     for (const void *q : ptrs)
         if (!aligned16(q)) return GDN_ERR_INVALID_ARG;
     if (!aligned_to(dweight, 4) || !aligned_to(dscale, 4)) return GDN_ERR_INVALID_ARG;
-    const size_t need = norm_workspace(rows, dim, dtype, scale != nullptr);
+    const size_t need = norm_workspace(rows, dim, scale != nullptr);
     if ((st = check_workspace(need, false, workspace, ws_size)) != GDN_OK) return st;
     const size_t n = (size_t)rows * dim, e = bytes_of(dtype), r = stream_there ? bytes_of(residual_dtype) : e;
     const size_t par = sizeof(float) * dim;

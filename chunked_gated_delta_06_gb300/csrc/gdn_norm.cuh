@@ -36,35 +36,14 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int turn) {
     }
 }
 
-// The gate's factor and its slope at z.
-__device__ __forceinline__ float gate_of(int gate, float z, float *slope) {
-    const float e = exp_of(-z), sig = reciprocal_of(1.f + e);
-    const float rest = z > 0.f ? e * sig : 1.f - sig;   // 1 - sig, which a sig near 1 has lost
-    if (gate == GDN_GATE_SIGMOID) {
-        if (slope) *slope = sig * rest;
-        return sig;
-    }
-    if (slope) *slope = fmaf(z * sig, rest, sig);
-    return z * sig;
+// The gate's factor at z, and its slope (1 - sigmoid as e^-z sigmoid, which a sigmoid near 1 has lost).
+__device__ __forceinline__ float gate_of(int gate, float z) {
+    return sigmoid_of(z) * (gate == GDN_GATE_SIGMOID ? 1.f : z);
 }
-
-// Picks threads a row and vectors a thread for nv vectors: as many threads as there are vectors, so
-// that no register array is longer than it has to be, up to 512.
-template <bool kWide, typename F>
-cudaError_t norm_shape(int nv, F launch) {
-    if constexpr (kWide) {
-        if (nv <= 16) return launch.template operator()<16, 1>();
-        if (nv <= 32) return launch.template operator()<32, 1>();
-        if (nv <= 128) return launch.template operator()<128, 1>();
-        if (nv <= 256) return launch.template operator()<256, 1>();
-        if (nv <= 512) return launch.template operator()<512, 1>();
-        if (nv <= 1024) return launch.template operator()<256, 4>();
-        return launch.template operator()<512, 4>();
-    } else {
-        if (nv <= 128) return launch.template operator()<128, 1>();
-        if (nv <= 2048) return launch.template operator()<512, 4>();
-        return launch.template operator()<1024, 8>();
-    }
+__device__ __forceinline__ float gate_of(int gate, float z, float *slope) {
+    const float e = exp_of(fminf(-z, 80.f)), sig = reciprocal_of(1.f + e), g = sig * (gate == GDN_GATE_SIGMOID ? 1.f : z);
+    *slope = fmaf(g, e * sig, gate == GDN_GATE_SIGMOID ? 0.f : sig);
+    return g;
 }
 
 }  // namespace gdn

@@ -4,98 +4,192 @@
 //   dh' = dh + r (e - n mean(e n)),   dresidual = dh',   dx = scale dh',   dscale = sum of dh' x
 // A row is read once: mean(h^2) and mean(e h) come from one pair of sums.  A block walks rows far
 // apart and keeps its sums for dw and dscale in registers; k_fold adds the blocks in their order.
+// Bound by HBM: each thread's part of the next rows is on its way into shared memory, by asynchronous
+// copies, while a row is computed (from registers alone a block has one row, and waits for it).
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_norm.cuh"
 
 namespace gdn {
 namespace {
 
-template <typename T, typename R, int V, int TPR, int VPT>
-__global__ void __launch_bounds__(norm_threads<TPR>()) k_norm_bwd(const __grid_constant__ NormArgs a) {
-    constexpr int kThreads = norm_threads<TPR>(), kRows = kThreads / TPR;
+// Threads a row and vectors (of V elements) a thread.
+template <typename F>
+cudaError_t norm_bwd_shape(bool wide, int nv, F launch) {
+    if (wide) {
+        if (nv <= 16) return launch.template operator()<16, 1, 4>();
+        if (nv <= 32) return launch.template operator()<32, 1, 4>();
+        if (nv <= 64) return launch.template operator()<32, 2, 4>();
+        if (nv <= 128) return launch.template operator()<64, 2, 4>();
+        if (nv <= 256) return launch.template operator()<128, 2, 4>();
+        if (nv <= 512) return launch.template operator()<256, 2, 4>();
+        if (nv <= 1024) return launch.template operator()<512, 2, 4>();
+        return launch.template operator()<512, 4, 4>();
+    }
+    if (nv <= 128) return launch.template operator()<128, 1, 1>();
+    if (nv <= 2048) return launch.template operator()<512, 4, 1>();
+    return launch.template operator()<1024, 8, 1>();
+}
+
+// Where a thread's vectors of the tensors are in its part of a stage, in bytes.
+template <typename T, typename R, int V>
+struct Places {
+    int h, dy, z, dh, x, all;
+    __host__ __device__ Places(bool has_z, bool has_dh, bool has_x) {
+        constexpr int t = V * (int)sizeof(T), r = V * (int)sizeof(R);
+        h = 0;
+        dy = r;
+        z = dy + t;
+        dh = z + (has_z ? t : 0);
+        x = dh + (has_dh ? r : 0);
+        all = x + (has_x ? t : 0);
+    }
+};
+
+// kAhead: rows come through shared memory, norm_stages of them: the next one, where a row is a block's
+// (and several blocks share an SM), three for the short ones.
+template <int TPR>
+constexpr int norm_stages() { return TPR <= 32 ? 4 : 2; }
+
+template <typename T, typename R, int V, int TPR, int VPT, bool kAhead>
+__global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT <= 1024 ? (TPR >= 1024 ? 1 : 1024 / TPR) : 1)
+    k_norm_bwd(const __grid_constant__ NormArgs a) {
+    constexpr int kThreads = norm_threads<TPR>(), kRows = kThreads / TPR, kStages = norm_stages<TPR>();
+    constexpr bool kKeep = TPR <= 32;   // a row's values stay in registers over its sums
+    extern __shared__ __align__(16) unsigned char ring[];   // [kStages][tensors][VPT][threads]
     const int lane = threadIdx.x % TPR, nv = a.D / V;
     const long long extent = a.R * a.D;
     const T *x = static_cast<const T *>(a.x), *z = static_cast<const T *>(a.z), *dy = static_cast<const T *>(a.dy);
     const R *hin = static_cast<const R *>(a.hin), *dh = static_cast<const R *>(a.dh);
+    const Places<T, R, V> places(a.z != nullptr, a.dh != nullptr, a.dscale != nullptr);
     float dw[VPT][V] = {}, ds[VPT][V] = {};
     int turn = 0;
-    for (long long row = (long long)blockIdx.x * kRows; row < a.R; row += (long long)gridDim.x * kRows, ++turn) {
-        const long long r = row + threadIdx.x / TPR;
-        Vec<R, V> hv[VPT], gv[VPT];
-        Vec<T, V> yv[VPT], zv[VPT], xv[VPT];
+    const long long step = (long long)gridDim.x * kRows, first = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+    auto place = [&](int stage, int tensor, int k, int bytes) {
+        return ring + (size_t)((stage * places.all + tensor) * VPT + k * bytes) * kThreads + threadIdx.x * bytes;
+    };
+    auto fetch = [&](long long r, int stage) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int i = lane + k * TPR;
             const long long at = r * a.D + (long long)i * V;
-            if (r < a.R && i < nv) {
-                hv[k] = load_vec<V>(hin, at, extent, nullptr);
-                yv[k] = load_vec<V>(dy, at, extent, nullptr);
-                if (a.z) zv[k] = load_vec<V>(z, at, extent, nullptr);
-                if (a.dh) gv[k] = load_vec<V>(dh, at, extent, nullptr);
-                if (a.dscale) xv[k] = load_vec<V>(x, at, extent, nullptr);
-            }
+            if (r >= a.R || i >= nv || !in_range(at, V, extent, nullptr)) continue;
+            auto copy = [&](int tensor, const auto *p) {
+                constexpr int kBytes = V * (int)sizeof(*p);
+                if constexpr (kBytes >= 4) copy_async<kBytes>(place(stage, tensor, k, kBytes), p + at, true);
+            };
+            copy(places.h, hin);
+            copy(places.dy, dy);
+            if (z) copy(places.z, z);
+            if (dh) copy(places.dh, dh);
+            if (a.dscale) copy(places.x, x);
         }
-        float sums[2] = {}, u[VPT][V];
+    };
+    if constexpr (kAhead) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            fetch(first + i * step, i);
+            copies_commit();
+        }
+    }
+    auto weight = [&](int k, float (&w)[V]) {
+        unpack(load_vec<V>(a.w, (long long)(lane + k * TPR) * V, a.D, nullptr), w);
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[v] += a.offset;
+    };
+    float kept_w[kKeep ? VPT : 1][V];
+    if constexpr (kKeep)
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            if (lane + k * TPR < nv) weight(k, kept_w[k]);
+    // (a block's rows: the same number for all of its threads)
+    for (long long row = (long long)blockIdx.x * kRows, r = first; row < a.R; row += step, r += step, ++turn) {
+        if constexpr (kAhead) {
+            fetch(r + (kStages - 1) * step, (turn + kStages - 1) % kStages);
+            copies_commit();
+            copies_wait<kStages - 1>();
+        }
+        const int stage = turn % kStages;
+        auto there = [&](int k) { return r < a.R && lane + k * TPR < nv; };
+        const long long at0 = r * a.D + lane * V;
+        // a vector of a tensor, from the ring or from memory
+        auto get = [&](const auto *p, int tensor, int k, float (&out)[V]) {
+            using E = std::remove_cv_t<std::remove_reference_t<decltype(*p)>>;
+            if constexpr (kAhead) unpack(*reinterpret_cast<const Vec<E, V> *>(place(stage, tensor, k, V * (int)sizeof(E))), out);
+            else unpack(load_vec<V>(p, at0 + k * TPR * V, extent, nullptr), out);
+        };
+        float sums[2] = {};
+        float h[VPT][V], u[VPT][V], slope[VPT][V];   // slope: of z, times dy; all but u to be had again
+        auto read = [&](int k) {
+            get(hin, places.h, k, h[k]);
+            get(dy, places.dy, k, u[k]);
+            if (z) {
+                float zv[V];
+                get(z, places.z, k, zv);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float s;
+                    const float g = gate_of(a.gate, zv[v], &s);
+                    slope[k][v] = u[k][v] * s;
+                    u[k][v] *= g;
+                }
+            }
+        };
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = lane + k * TPR;
-            if (r >= a.R || i >= nv) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) u[k][v] = 0.f;
-                continue;
-            }
-            const Vec<float, V> w = load_vec<V>(a.w, (long long)i * V, a.D, nullptr);
+            if (!there(k)) continue;
+            float w[V];
+            if constexpr (!kKeep) weight(k, w);
+            read(k);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float h = as_float(hv[k].x[v]);
-                u[k][v] = as_float(yv[k].x[v]);
-                if (a.z) u[k][v] *= gate_of(a.gate, as_float(zv[k].x[v]), nullptr);
-                sums[0] = fmaf(h, h, sums[0]);
-                sums[1] = fmaf(u[k][v] * (a.offset + w.x[v]), h, sums[1]);
+                sums[0] = fmaf(h[k][v], h[k][v], sums[0]);
+                sums[1] = fmaf(u[k][v] * (kKeep ? kept_w[k][v] : w[v]), h[k][v], sums[1]);
             }
         }
         row_sums<TPR>(sums, turn);
-        const float rs = rsqrtf(sums[0] / (float)a.D + a.eps), mean = sums[1] * rs / (float)a.D;
+        const float rs = rsqrtf(fmaf(sums[0], a.per_d, a.eps)), mean = sums[1] * rs * a.per_d;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int i = lane + k * TPR;
-            if (r >= a.R || i >= nv) break;
-            const long long at = r * a.D + (long long)i * V;
-            const Vec<float, V> w = load_vec<V>(a.w, (long long)i * V, a.D, nullptr);
-            Vec<float, V> scale;
-            if (a.scale) scale = load_vec<V>(a.scale, (long long)i * V, a.D, nullptr);
-            Vec<T, V> dx, dz;
-            Vec<R, V> dres;
+            if (!there(k)) break;
+            float w[V], scale[V], xv[V], gv[V], dx[V], dz[V];
+            if constexpr (!kKeep) {   // (a second time from where they are, for the blocks that the registers allow)
+                weight(k, w);
+                read(k);
+            }
+            if (a.scale) unpack(load_vec<V>(a.scale, (long long)(lane + k * TPR) * V, a.D, nullptr), scale);
+            if (dh) get(dh, places.dh, k, gv);
+            if (a.dscale) get(x, places.x, k, xv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float n = as_float(hv[k].x[v]) * rs, wv = a.offset + w.x[v];
-                if (a.z) {
-                    float slope;
-                    gate_of(a.gate, as_float(zv[k].x[v]), &slope);
-                    dz.x[v] = as_type<T>(as_float(yv[k].x[v]) * n * wv * slope);
-                }
+                const float n = h[k][v] * rs, wv = kKeep ? kept_w[k][v] : w[v];
+                if (z) dz[v] = slope[k][v] * (n * wv);
                 dw[k][v] = fmaf(u[k][v], n, dw[k][v]);
-                float d = rs * (u[k][v] * wv - n * mean);
-                if (a.dh) d += as_float(gv[k].x[v]);
-                dres.x[v] = as_type<R>(d);
-                if (a.dscale) ds[k][v] = fmaf(d, as_float(xv[k].x[v]), ds[k][v]);
-                dx.x[v] = as_type<T>(a.scale ? d * scale.x[v] : d);
+                float d = rs * fmaf(u[k][v], wv, -n * mean);
+                if (dh) d += gv[v];
+                gv[v] = d;
+                if (a.dscale) ds[k][v] = fmaf(d, xv[v], ds[k][v]);
+                dx[v] = a.scale ? d * scale[v] : d;
             }
-            store_vec<V>(static_cast<T *>(a.dx), at, extent, nullptr, dx);
-            if (a.dres) store_vec<V>(static_cast<R *>(a.dres), at, extent, nullptr, dres);
-            if (a.z) store_vec<V>(static_cast<T *>(a.dz), at, extent, nullptr, dz);
+            const long long at = at0 + k * TPR * V;
+            store_vec<V>(static_cast<T *>(a.dx), at, extent, nullptr, pack<T>(dx));
+            if (a.dres) store_vec<V>(static_cast<R *>(a.dres), at, extent, nullptr, pack<R>(gv));
+            if (z) store_vec<V>(static_cast<T *>(a.dz), at, extent, nullptr, pack<T>(dz));
         }
     }
     // the block's rows, in order
     const int parts = a.dscale ? 2 : 1;
     const long long n = (long long)gridDim.x * parts * a.D;
     if constexpr (kRows > 1) {
-        __shared__ float all[kRows][TPR * V];
+        __shared__ float all[kRows][TPR * VPT * V];
         for (int part = 0; part < parts; ++part) {
             __syncthreads();
 #pragma unroll
-            for (int v = 0; v < V; ++v) all[threadIdx.x / TPR][lane * V + v] = part ? ds[0][v] : dw[0][v];
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    all[threadIdx.x / TPR][(lane + k * TPR) * V + v] = part ? ds[k][v] : dw[k][v];
             __syncthreads();
             for (int i = threadIdx.x; i < a.D; i += kThreads) {
                 float s = 0.f;
@@ -119,28 +213,38 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) k_norm_bwd(const __grid_c
     }
 }
 
-template <typename T, typename R, int V>
+template <typename T, typename R>
 struct Launch {
     const NormArgs &a;
     cudaStream_t s;
-    template <int TPR, int VPT>
+    template <int TPR, int VPT, int V>
     cudaError_t operator()() const {
-        static_assert(TPR > 32 || VPT == 1, "the sum over a block's rows takes one vector a thread");
-        k_norm_bwd<T, R, V, TPR, VPT><<<norm_bwd_blocks(a.R, a.D, a.f32), norm_threads<TPR>(), 0, s>>>(a);
+        constexpr int kThreads = norm_threads<TPR>();
+        const int blocks = norm_bwd_blocks(a.R, a.D);
+        if constexpr (V > 1) {
+            const Places<T, R, V> places(a.z != nullptr, a.dh != nullptr, a.dscale != nullptr);
+            const int bytes = norm_stages<TPR>() * places.all * VPT * kThreads;
+            if (bytes <= 160 * 1024) {   // (wider rows are long enough to keep loads on their way by themselves)
+                const cudaError_t e = cudaFuncSetAttribute(k_norm_bwd<T, R, V, TPR, VPT, true>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                if (e != cudaSuccess) return e;
+                k_norm_bwd<T, R, V, TPR, VPT, true><<<blocks, kThreads, bytes, s>>>(a);
+                return cudaGetLastError();
+            }
+        }
+        k_norm_bwd<T, R, V, TPR, VPT, false><<<blocks, kThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
 };
 
 template <typename T, typename R>
 cudaError_t norm_bwd(const NormArgs &a, cudaStream_t s) {
-    constexpr int V = 16 / (int)sizeof(T);
-    if (a.D % V == 0) return norm_shape<true>(a.D / V, Launch<T, R, V>{a, s});
-    return norm_shape<false>(a.D, Launch<T, R, 1>{a, s});
+    return norm_bwd_shape(a.D % 4 == 0, a.D % 4 == 0 ? a.D / 4 : a.D, Launch<T, R>{a, s});
 }
 
 struct RowsOf {
     int *out;
-    template <int TPR, int VPT>
+    template <int TPR, int VPT, int V>
     cudaError_t operator()() const {
         out[0] = norm_threads<TPR>() / TPR;
         out[1] = norm_threads<TPR>();
@@ -151,12 +255,10 @@ struct RowsOf {
 }  // namespace
 
 // A block's sums stay in registers over its rows: as many blocks as run at once, no more.
-int norm_bwd_blocks(long long R, int D, int f32) {
-    const int V = f32 ? 4 : 8;
+int norm_bwd_blocks(long long R, int D) {
     int shape[2];
-    if (D % V == 0) norm_shape<true>(D / V, RowsOf{shape});
-    else norm_shape<false>(D, RowsOf{shape});
-    return (int)std::max(1LL, std::min((R + shape[0] - 1) / shape[0], 152LL * (1024 / shape[1])));
+    norm_bwd_shape(D % 4 == 0, D % 4 == 0 ? D / 4 : D, RowsOf{shape});
+    return (int)std::max(1LL, std::min((R + shape[0] - 1) / shape[0], 152LL * std::max(1, (shape[0] > 1 ? 768 : 1024) / shape[1])));
 }
 
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {
@@ -165,7 +267,7 @@ cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {
     else e = a.res == GDN_DTYPE_F32 ? norm_bwd<bf16, float>(a, s) : norm_bwd<bf16, bf16>(a, s);
     if (e != cudaSuccess) return e;
     const int parts = a.dscale ? 2 : 1, D = a.D;
-    return launch_fold(FoldArgs{a.part, norm_bwd_blocks(a.R, D, a.f32), (long long)parts * D, parts * D, D, a.dw, a.dscale}, s);
+    return launch_fold(FoldArgs{a.part, norm_bwd_blocks(a.R, D), (long long)parts * D, parts * D, D, a.dw, a.dscale}, s);
 }
 
 }  // namespace gdn

@@ -1,5 +1,7 @@
 // gdn_scan.cu -- the selective scan's forward (packed, and over pool slots), its state pass over the
 // segments of a split scan, and the step of one token for each row.
+#include <algorithm>
+
 #include "gdn_scan.cuh"
 
 namespace gdn {
@@ -87,15 +89,16 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
             for (int k = 0; k < Tile::NV; ++k) {
                 const int row = Tile::row(k);
                 if (row >= TT) break;
-                const V xv = place(m.x, i)[Tile::thread() + k * kHalf], dv = place(m.dt, i)[Tile::thread() + k * kHalf];
+                float xv[EV], dv[EV], d4[EV], dx4[EV];
+                unpack(place(m.x, i)[Tile::thread() + k * kHalf], xv);
+                unpack(place(m.dt, i)[Tile::thread() + k * kHalf], dv);
                 const bool there = w.b + i * TT + row < w.f;
-                float d4[EV], dx4[EV];
 #pragma unroll
                 for (int j = 0; j < EV; j += 2) {
-                    float2 d = softplus_of(add2(make_float2(as_float(dv.x[j]), as_float(dv.x[j + 1])),
+                    float2 d = softplus_of(add2(make_float2(dv[j], dv[j + 1]),
                                                 *reinterpret_cast<const float2 *>(&m.bias[col + j])));
                     if (!there) d = both(0.f);
-                    const float2 dx = mul2(d, make_float2(as_float(xv.x[j]), as_float(xv.x[j + 1])));
+                    const float2 dx = mul2(d, make_float2(xv[j], xv[j + 1]));
                     d4[j] = d.x;
                     d4[j + 1] = d.y;
                     dx4[j] = dx.x;
@@ -115,20 +118,19 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
             for (int k = 0; k < Tile::NV; ++k) {
                 const int row = Tile::row(k);
                 if (row >= TT) break;
-                const V xv = place(m.x, i)[Tile::thread() + k * kHalf];
-                V zv, out;
-                if (gated) zv = place(m.z, i)[Tile::thread() + k * kHalf];
+                float xv[EV], zv[EV], out[EV];
+                unpack(place(m.x, i)[Tile::thread() + k * kHalf], xv);
+                if (gated) unpack(place(m.z, i)[Tile::thread() + k * kHalf], zv);
                 const float *sums = m.y[i & 1][row] + col;
 #pragma unroll
                 for (int j = 0; j < EV; j += 2) {
                     float2 y = fma2(*reinterpret_cast<const float2 *>(&m.skip[col + j]),
-                                    make_float2(as_float(xv.x[j]), as_float(xv.x[j + 1])),
-                                    *reinterpret_cast<const float2 *>(&sums[j]));
-                    if (gated) y = mul2(y, silu_of(make_float2(as_float(zv.x[j]), as_float(zv.x[j + 1]))));
-                    out.x[j] = as_type<T>(y.x);
-                    out.x[j + 1] = as_type<T>(y.y);
+                                    make_float2(xv[j], xv[j + 1]), *reinterpret_cast<const float2 *>(&sums[j]));
+                    if (gated) y = mul2(y, silu_of(make_float2(zv[j], zv[j + 1])));
+                    out[j] = y.x;
+                    out[j + 1] = y.y;
                 }
-                Tile::store(static_cast<T *>(a.y), a, w, w.b + i * TT, w.f, k, out);
+                Tile::store(static_cast<T *>(a.y), a, w, w.b + i * TT, w.f, k, pack<T>(out));
             }
         };
         fetch(0);
@@ -151,19 +153,15 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
     const Lane lane(a, w);
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
     const int last = w.item - w.seg + w.segs - 1;   // the item of the sequence's last segment
-    // The state ahead of the segment.  The record of the last segment, which has no end to keep, holds
-    // the state ahead of the sequence: a slot is read once, before any block writes it.
+    // The state ahead of the segment.  The record of the last segment, which has no end to keep, first
+    // holds the state ahead of the sequence: a slot is read once, before any block writes it.
     typename Lane::States h;
-    if (w.seg == 0 && (kEnds || w.segs == 1)) {
-        lane.load(a.s0, scan_start_row(a, w.n), a.slots.idx ? a.slots.num_slots : a.pack.N, a, w, h);
-        if (kEnds) lane.store(a.rec_h, last, items, a, w, h);
-    } else if (kEnds) {
-        lane.load(nullptr, -1, 0, a, w, h);
-    } else if (w.seg == 0) {
-        lane.load(a.rec_h, last, items, a, w, h);
+    if (kEnds || w.segs == 1) {
+        const int from = w.seg == 0 ? scan_start_row(a, w.n) : -1;
+        lane.load(a.s0, from, a.slots.idx ? a.slots.num_slots : a.pack.N, a, w, h);
+        if (kEnds && w.seg == 0) lane.store(a.rec_h, last, items, a, w, h);
     } else {
-        lane.load(a.rec_h, w.item - w.seg, items, a, w, h);
-        for (int i = w.item - w.seg + 1; i < w.item; ++i) lane.join(a, w, a.rec_h, i, h);
+        lane.load(a.rec_h, w.item, items, a, w, h);
     }
     float total = 0.f;
     const int place = channel_at(lane.at);
@@ -235,52 +233,127 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
     lane.store(a.s1, to, a.slots.idx ? a.slots.num_slots : a.pack.N, a, w, h);
 }
 
-// One token for each row: a thread has four states of one channel.  Bound by HBM, the states read and
-// written once.
-template <typename T, int NS>
-__global__ void __launch_bounds__(256) k_scan_step(const __grid_constant__ ScanArgs a, int across) {
-    constexpr int L = NS / 4, CB = 256 / L;
-    const int b = blockIdx.x / across, c = (int)(blockIdx.x % across) * CB + (int)threadIdx.x / L, q = threadIdx.x % L;
-    const bool there = c < a.C;
-    const int slot = slot_of(a.slots, b);
-    T *y = static_cast<T *>(a.y);
-    const long long extent = (long long)a.pack.T * a.C, to = (long long)b * a.C + c;
-    if (slot < 0) {
-        if (threadIdx.x == 0 && a.slots.status && a.slots.idx[b] >= a.slots.num_slots) *a.slots.status = 1;
-        if (there && q == 0) store_vec<1>(y, to, extent, a.pack.status, Vec<T, 1>{{as_type<T>(0.f)}});
-        return;
+// One thread for four states of a channel, from segment to segment; eight records on their way at once.
+template <bool kBackward>
+__global__ void __launch_bounds__(128) k_scan_join(const __grid_constant__ ScanArgs a, int across) {
+    const int n = blockIdx.x / across;
+    const long long i = ((long long)(blockIdx.x % across) * 128 + threadIdx.x) * 4, per = (long long)a.C * a.Ns;
+    const int b = offset_of(a.pack, n), e = max(b, offset_of(a.pack, n + 1));
+    const int segs = max(1, (int)(((long long)e - b + a.seg - 1) / a.seg)), first = first_item(a, n);
+    if (i >= per || segs < 2) return;
+    const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
+    const int c = (int)(i / a.Ns);
+    float rate[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        rate[j] = in_range(i + j, 1, per, a.pack.status) ? fmaxf(-1.44269504088896341f * expf(a.A_log[i + j]), -3e38f) : 0.f;
+    float *rec = kBackward ? a.rec_g : a.rec_h;
+    auto read = [&](int seg) { return load_vec<4>(rec, (first + seg) * per + i, items * per, a.pack.status); };
+    auto write = [&](int seg, const Vec<float, 4> &v) { store_vec<4>(rec, (first + seg) * per + i, items * per, a.pack.status, v); };
+    // the j-th segment of the walk, and the last one that it reads
+    auto segment = [&](int j) { return kBackward ? segs - 1 - j : j; };
+    const Vec<float, 4> start = read(segs - 1);
+    Vec<float, 4> run = read(segment(0));
+    constexpr int U = 8;
+    for (int j0 = 1; j0 < segs; j0 += U) {
+        Vec<float, 4> end[U];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int seg = segment(j0 + u);
+            // (the last one has no decay: nothing is behind it that reads it)
+            if (j0 + u >= segs - 1) continue;
+            end[u] = read(seg);
+            d[u] = load_vec<1>(a.rec_d, (first + seg) * (long long)a.C + c, items * a.C, a.pack.status).x[0];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u >= segs) break;
+            write(segment(j0 + u), run);
+            if (j0 + u >= segs - 1) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) run.x[k] = fmaf(exp2_of(rate[k] * d[u]), run.x[k], end[u].x[k]);
+        }
     }
-    float sum = 0.f, x = 0.f;
-    if (there) {
-        const long long at = ((long long)slot * a.C + c) * NS + 4 * q, n = (long long)a.slots.num_slots * a.C * NS;
-        const Vec<float, 4> h = load_vec<4>(a.s1, at, n, a.pack.status);
-        const int g = c / (a.C / a.G);
-        auto in = [&](const void *p, long long stride) {
-            return as_float(load_vec<1>(static_cast<const T *>(p), b * stride + c, (a.pack.T - 1) * stride + a.C, a.pack.status).x[0]);
-        };
-        x = in(a.x, a.xs);
-        const float d = softplus_of(in(a.dt, a.dts) + (a.dt_bias ? a.dt_bias[c] : 0.f));
-        Vec<float, 4> out;
+    if (!kBackward) write(0, start);
+}
+
+// One token for each of `rows` rows, one after another (the rates are formed once).  A thread has four
+// states of L = NS / 4 channels in turn, so that its L lanes form d, the gate and the output of one
+// channel each.  Bound by HBM, the states read and written once.
+template <typename T, int NS, bool kWide>
+__global__ void __launch_bounds__(256, NS < 32 ? 3 : 1) k_scan_step(const __grid_constant__ ScanArgs a, int across, int rows) {
+    constexpr int L = NS / 4, kStart = 256 / L;   // groups of L lanes, L channels each
+    const int q = threadIdx.x % L, lane = threadIdx.x % 32;
+    const int c0 = ((int)(blockIdx.x % across) * kStart + (int)threadIdx.x / L) * L, c = c0 + q;   // c: the lane's own
+    const int b0 = (int)(blockIdx.x / across) * rows, b1 = min(b0 + rows, a.pack.T);
+    const int per_group = a.C / a.G;
+    const bool mine = c < a.C;
+    const long long extent = (long long)a.pack.T * a.C, states = (long long)a.slots.num_slots * a.C * NS;
+    float rate[L][4];
+#pragma unroll
+    for (int i = 0; i < L; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int s = g * NS + 4 * q + j;
-            const float bv = as_float(load_vec<1>(static_cast<const T *>(a.B), b * a.bs + s, (a.pack.T - 1) * a.bs + a.G * NS, a.pack.status).x[0]);
-            const float cv = as_float(load_vec<1>(static_cast<const T *>(a.Cm), b * a.cs + s, (a.pack.T - 1) * a.cs + a.G * NS, a.pack.status).x[0]);
-            const float rate = fmaxf(-1.44269504088896341f * expf(load_vec<1>(a.A_log, (long long)c * NS + 4 * q + j, (long long)a.C * NS, a.pack.status).x[0]), -3e38f);
-            out.x[j] = fmaf(exp2_of(d * rate), h.x[j], d * x * bv);
-            sum = fmaf(cv, out.x[j], sum);
+            const long long at = (long long)(c0 + i) * NS + 4 * q + j;
+            rate[i][j] = c0 + i < a.C && in_range(at, 1, (long long)a.C * NS, a.pack.status)
+                             ? fmaxf(-1.44269504088896341f * expf(a.A_log[at]), -3e38f)
+                             : 0.f;
         }
-        store_vec<4>(a.s1, at, n, a.pack.status, out);
-    }
+    const float bias = mine && a.dt_bias ? a.dt_bias[c] : 0.f, skip = mine && a.D ? a.D[c] : 0.f;
+    T *y = static_cast<T *>(a.y);
+    auto own = [&](const void *p, long long stride, int b) {
+        return mine && p ? as_float(load_vec<1>(static_cast<const T *>(p), b * stride + c, (a.pack.T - 1) * stride + a.C, a.pack.status).x[0]) : 0.f;
+    };
+    auto shared = [&](const void *p, long long stride, int b, int i, float (&out)[4]) {
+        const int g = min(c0 + i, a.C - 1) / per_group;
+        const long long at = b * stride + g * NS + 4 * q, n = (a.pack.T - 1) * stride + (long long)a.G * NS;
+        if (kWide) {
+            const Vec<T, 4> v = load_vec<4>(static_cast<const T *>(p), at, n, a.pack.status);
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!there || q) return;
-    if (a.D) sum = fmaf(a.D[c], x, sum);
-    if (a.z) {
-        const float z = as_float(load_vec<1>(static_cast<const T *>(a.z), b * a.zs + c, (a.pack.T - 1) * a.zs + a.C, a.pack.status).x[0]);
-        sum *= z * sigmoid_of(z);
+            for (int j = 0; j < 4; ++j) out[j] = as_float(v.x[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[j] = as_float(load_vec<1>(static_cast<const T *>(p), at + j, n, a.pack.status).x[0]);
+        }
+    };
+    const bool one_group = c0 / per_group == min(c0 + L - 1, a.C - 1) / per_group;
+    for (int b = b0; b < b1; ++b) {
+        const int slot = slot_of(a.slots, b);
+        if (slot < 0) {   // (the same for all threads of the block)
+            if (threadIdx.x == 0 && a.slots.status && a.slots.idx[b] >= a.slots.num_slots) *a.slots.status = 1;
+            if (mine) store_vec<1>(y, (long long)b * a.C + c, extent, a.pack.status, Vec<T, 1>{{as_type<T>(0.f)}});
+            continue;
+        }
+        Vec<float, 4> h[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if (c0 + i < a.C) h[i] = load_vec<4>(a.s1, ((long long)slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status);
+        const float x = own(a.x, a.xs, b), z = own(a.z, a.zs, b);
+        const float d = softplus_of(own(a.dt, a.dts, b) + bias), dx = d * x;
+        float B[4], C[4], sums[L][1];
+        shared(a.B, a.bs, b, 0, B);
+        shared(a.Cm, a.cs, b, 0, C);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const float di = __shfl_sync(0xffffffffu, d, lane - q + i), dxi = __shfl_sync(0xffffffffu, dx, lane - q + i);
+            if (i > 0 && !one_group) {
+                shared(a.B, a.bs, b, i, B);
+                shared(a.Cm, a.cs, b, i, C);
+            }
+            sums[i][0] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[i].x[j] = fmaf(exp2_of(di * rate[i][j]), h[i].x[j], dxi * B[j]);
+                sums[i][0] = fmaf(C[j], h[i].x[j], sums[i][0]);
+            }
+            if (c0 + i < a.C) store_vec<4>(a.s1, ((long long)slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status, h[i]);
+        }
+        lane_sums<L, L, 1>(sums, q);
+        float out = fmaf(skip, x, sums[0][0]);
+        if (a.z) out *= z * sigmoid_of(z);
+        if (mine) store_vec<1>(y, (long long)b * a.C + c, extent, a.pack.status, Vec<T, 1>{{as_type<T>(out)}});
     }
-    store_vec<1>(y, to, extent, a.pack.status, Vec<T, 1>{{as_type<T>(sum)}});
 }
 
 template <typename T, int NS, bool kWide, bool kEnds>
@@ -301,9 +374,15 @@ cudaError_t scan(const ScanArgs &a, cudaStream_t s) {
 
 template <typename T, int NS>
 cudaError_t step(const ScanArgs &a, int batch, cudaStream_t s) {
-    constexpr int CB = 256 / (NS / 4);
-    const int across = (a.C + CB - 1) / CB;
-    k_scan_step<T, NS><<<(unsigned)((long long)batch * across), 256, 0, s>>>(a, across);
+    const int across = (a.C + 255) / 256;
+    // rows of a block: up to 8, as long as every SM has eight blocks
+    const int rows = (int)std::max(1LL, std::min(8LL, (long long)batch * across / (8 * 152)));
+    const unsigned grid = (unsigned)((batch + rows - 1) / rows * (long long)across);
+    auto fits = [](const void *p, long long stride) {
+        return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && stride % 4 == 0;
+    };
+    if (fits(a.B, a.bs) && fits(a.Cm, a.cs)) k_scan_step<T, NS, true><<<grid, 256, 0, s>>>(a, across, rows);
+    else k_scan_step<T, NS, false><<<grid, 256, 0, s>>>(a, across, rows);
     return cudaGetLastError();
 }
 
@@ -317,9 +396,18 @@ cudaError_t scan_of(const ScanArgs &a, cudaStream_t s) {
 
 cudaError_t launch_scan_ends(const ScanArgs &a, cudaStream_t s) { return scan_of<true>(a, s); }
 
+cudaError_t launch_scan_join(const ScanArgs &a, bool backward, cudaStream_t s) {
+    const int across = (int)(((long long)a.C * a.Ns / 4 + 127) / 128);
+    const unsigned grid = (unsigned)((long long)a.pack.N * across);
+    if (backward) k_scan_join<true><<<grid, 128, 0, s>>>(a, across);
+    else k_scan_join<false><<<grid, 128, 0, s>>>(a, across);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
     if (a.seg <= a.pack.T) {
-        const cudaError_t e = launch_scan_ends(a, s);
+        cudaError_t e = launch_scan_ends(a, s);
+        if (e == cudaSuccess) e = launch_scan_join(a, false, s);
         if (e != cudaSuccess) return e;
     }
     return scan_of<false>(a, s);

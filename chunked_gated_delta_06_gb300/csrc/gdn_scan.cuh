@@ -68,18 +68,6 @@ __device__ __forceinline__ float2 silu_of(float2 z) {
     return mul2(z, make_float2(sigmoid_of(z.x), sigmoid_of(z.y)));
 }
 
-// Asynchronous copies of `bytes` (4, 8 or 16) into shared memory; zeros instead where there is nothing.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void *to, const void *from, bool there) {
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-    const int n = there ? kBytes : 0;
-    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(n) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(kBytes), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
-
 // Where a block works.
 struct ScanPlace {
     int n, item, seg, segs;      // sequence, its item, the segment and how many the sequence has
@@ -186,8 +174,9 @@ struct RowsOf {
         for (int k = 0; k < NU; ++k) {
             const int u = (int)threadIdx.x % N + k * N;
             if (u >= kUnits) break;
-            *reinterpret_cast<float4 *>(&rows[u / (NS / 4)][u % (NS / 4) * 4]) =
-                make_float4(as_float(v[u].x[0]), as_float(v[u].x[1]), as_float(v[u].x[2]), as_float(v[u].x[3]));
+            float f[4];
+            unpack(v[u], f);
+            *reinterpret_cast<float4 *>(&rows[u / (NS / 4)][u % (NS / 4) * 4]) = make_float4(f[0], f[1], f[2], f[3]);
         }
     }
     static __device__ void keep(const V (&v)[NU], float (*rows)[NS]) {
@@ -338,19 +327,6 @@ struct ScanLane {
             }
     }
     __device__ float2 decay(int i, int k, float2 d) const { return exp2_of(mul2(A[i][k], d)); }
-    // h <- e^{A sum of d} h + the record of segment `item`
-    __device__ void join(const ScanArgs &a, const ScanPlace &w, const float *rec, int item, States &h) const {
-        const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
-        States end;
-        load(rec, item, items, a, w, end);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const long long from = (long long)item * a.C + c + i;
-            const float d = c + i < w.cend && in_range(from, 1, items * a.C, a.pack.status) ? a.rec_d[from] : 0.f;
-#pragma unroll
-            for (int k = 0; k < H; ++k) h[i][k] = fma2(decay(i, k, both(d)), h[i][k], end[i][k]);
-        }
-    }
 };
 
 // Sums over the L threads that share channels: K values of each of BT <= L tokens come in, and thread
@@ -400,7 +376,10 @@ long long scan_across(const ScanArgs &a) {
     return (long long)a.G * ((a.C / a.G + CB - 1) / CB);
 }
 
-// end states (and sums of d) of every segment but the last of each sequence
+// The records of a split scan: end states and sums of d of every segment but the last of each sequence,
 cudaError_t launch_scan_ends(const ScanArgs &a, cudaStream_t s);
+// and then in the place of rec_h the state ahead of each segment, in the place of rec_g (backward) the
+// gradient behind each segment but the last.
+cudaError_t launch_scan_join(const ScanArgs &a, bool backward, cudaStream_t s);
 
 }  // namespace gdn

@@ -158,13 +158,15 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
         // d and d x of the tile at token t, the i-th of its walk
         auto form = [&](int i, int t, int k, float (&d)[kEV]) {
             const int row = Tile::row(k);
-            const V xv = place(m.x, i)[Tile::thread() + k * N], dv = place(m.dt, i)[Tile::thread() + k * N];
+            float xv[kEV], dv[kEV];
+            unpack(place(m.x, i)[Tile::thread() + k * N], xv);
+            unpack(place(m.dt, i)[Tile::thread() + k * N], dv);
 #pragma unroll
             for (int j = 0; j < kEV; j += 2) {
-                float2 v = softplus_of(add2(make_float2(as_float(dv.x[j]), as_float(dv.x[j + 1])),
+                float2 v = softplus_of(add2(make_float2(dv[j], dv[j + 1]),
                                             *reinterpret_cast<const float2 *>(&m.bias[col + j])));
                 if (t + row >= w.f) v = both(0.f);   // (which leaves the states alone)
-                const float2 dx = mul2(v, make_float2(as_float(xv.x[j]), as_float(xv.x[j + 1])));
+                const float2 dx = mul2(v, make_float2(xv[j], xv[j + 1]));
                 m.dd[i & 1][row][unit_at((col + j) / 2)] = make_float4(v.x, dx.x, v.y, dx.y);
                 d[j] = v.x;
                 d[j + 1] = v.y;
@@ -230,15 +232,13 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                 const int row = Tile::row(k);
                 if (row >= TT) break;
                 form(i, w.b + (tiles - 1 - i) * TT, k, d);
-                const V dyv = place(m.dy, i)[Tile::thread() + k * N];
-                float2 o[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) o[j] = make_float2(as_float(dyv.x[2 * j]), as_float(dyv.x[2 * j + 1]));
+                float dyv[kEV], zv[kEV];
+                unpack(place(m.dy, i)[Tile::thread() + k * N], dyv);
+                float2 o[2] = {make_float2(dyv[0], dyv[1]), make_float2(dyv[2], dyv[3])};
                 if (gated) {
-                    const V zv = place(m.z, i)[Tile::thread() + k * N];
+                    unpack(place(m.z, i)[Tile::thread() + k * N], zv);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        o[j] = mul2(o[j], silu_of(make_float2(as_float(zv.x[2 * j]), as_float(zv.x[2 * j + 1]))));
+                    for (int j = 0; j < 2; ++j) o[j] = mul2(o[j], silu_of(make_float2(zv[2 * j], zv[2 * j + 1])));
                 }
                 *reinterpret_cast<float4 *>(&m.os[i & 1][row][col]) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
             }
@@ -252,36 +252,37 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
             for (int k = 0; k < Tile::NV; ++k) {
                 const int row = Tile::row(k);
                 if (row >= TT) break;
-                const V xv = place(m.x, i)[Tile::thread() + k * N], dv = place(m.dt, i)[Tile::thread() + k * N];
-                const V dyv = place(m.dy, i)[Tile::thread() + k * N];
-                V zv, dxv, ddv, dzv;
-                if (gated) zv = place(m.z, i)[Tile::thread() + k * N];
+                float xv[kEV], dv[kEV], dyv[kEV], zv[kEV], dxv[kEV], ddv[kEV], dzv[kEV];
+                unpack(place(m.x, i)[Tile::thread() + k * N], xv);
+                unpack(place(m.dt, i)[Tile::thread() + k * N], dv);
+                unpack(place(m.dy, i)[Tile::thread() + k * N], dyv);
+                if (gated) unpack(place(m.z, i)[Tile::thread() + k * N], zv);
                 const bool there = t + row < w.f;
 #pragma unroll
                 for (int j = 0; j < kEV; j += 2) {
                     const float4 s = m.dd[i & 1][row][unit_at((col + j) / 2)];
                     const float2 gB = make_float2(s.x, s.z), pA = make_float2(s.y, s.w);
-                    const float2 xj = make_float2(as_float(xv.x[j]), as_float(xv.x[j + 1]));
+                    const float2 xj = make_float2(xv[j], xv[j + 1]);
                     const float2 skip = *reinterpret_cast<const float2 *>(&m.skip[col + j]);
-                    float2 o = make_float2(as_float(dyv.x[j]), as_float(dyv.x[j + 1]));
+                    float2 o = make_float2(dyv[j], dyv[j + 1]);
                     if (gated) {
-                        const float2 zj = make_float2(as_float(zv.x[j]), as_float(zv.x[j + 1]));
+                        const float2 zj = make_float2(zv[j], zv[j + 1]);
                         const float2 sig = make_float2(sigmoid_of(zj.x), sigmoid_of(zj.y)), silu = mul2(zj, sig);
                         const float2 slope = fma2(silu, make_float2(1.f - sig.x, 1.f - sig.y), sig);
                         const float2 y = fma2(skip, xj, *reinterpret_cast<const float2 *>(&m.os[i & 1][row][col + j]));
                         const float2 dz = mul2(mul2(o, y), slope);
-                        dzv.x[j] = as_type<T>(dz.x);
-                        dzv.x[j + 1] = as_type<T>(dz.y);
+                        dzv[j] = dz.x;
+                        dzv[j + 1] = dz.y;
                         o = mul2(o, silu);
                     }
-                    const float2 u = add2(make_float2(as_float(dv.x[j]), as_float(dv.x[j + 1])),
+                    const float2 u = add2(make_float2(dv[j], dv[j + 1]),
                                           *reinterpret_cast<const float2 *>(&m.bias[col + j]));
                     const float2 dxj = fma2(gB, softplus_of(u), mul2(skip, o));
                     const float2 du = mul2(fma2(pA, both(ln2), mul2(gB, xj)), make_float2(sigmoid_of(u.x), sigmoid_of(u.y)));
-                    dxv.x[j] = as_type<T>(dxj.x);
-                    dxv.x[j + 1] = as_type<T>(dxj.y);
-                    ddv.x[j] = as_type<T>(du.x);
-                    ddv.x[j + 1] = as_type<T>(du.y);
+                    dxv[j] = dxj.x;
+                    dxv[j + 1] = dxj.y;
+                    ddv[j] = du.x;
+                    ddv[j + 1] = du.y;
                     if (there) {
                         dD[j] = fmaf(o.x, xj.x, dD[j]);
                         dD[j + 1] = fmaf(o.y, xj.y, dD[j + 1]);
@@ -289,9 +290,9 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                         db[j + 1] += du.y;
                     }
                 }
-                Tile::store(static_cast<T *>(a.dx), a, w, t, w.f, k, dxv);
-                Tile::store(static_cast<T *>(a.ddt), a, w, t, w.f, k, ddv);
-                if (gated) Tile::store(static_cast<T *>(a.dz), a, w, t, w.f, k, dzv);
+                Tile::store(static_cast<T *>(a.dx), a, w, t, w.f, k, pack<T>(dxv));
+                Tile::store(static_cast<T *>(a.ddt), a, w, t, w.f, k, pack<T>(ddv));
+                if (gated) Tile::store(static_cast<T *>(a.dz), a, w, t, w.f, k, pack<T>(dzv));
             }
             // dC and dB of the tile over the block's channels: four states of one of them a thread
             for (int v = threadIdx.x; v < TT * L * 2; v += N) {
@@ -352,12 +353,8 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
     // Forward: the states ahead of the tiles.
     float2 h[2][2];
-    if (w.seg == 0) {
-        lane.load(a.s0, a.s0 ? w.n : -1, a.pack.N, a, w, h);
-    } else {
-        lane.load(a.rec_h, w.item - w.seg, items, a, w, h);
-        for (int i = w.item - w.seg + 1; i < w.item; ++i) lane.join(a, w, a.rec_h, i, h);
-    }
+    if (w.segs == 1) lane.load(a.s0, a.s0 ? w.n : -1, a.pack.N, a, w, h);
+    else lane.load(a.rec_h, w.item, items, a, w, h);
     __syncthreads();
     for (int i = 0; i < tiles - 1; ++i) {
         lane.store(a.marks, mark + i, marks, a, w, h);
@@ -376,12 +373,8 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     }
     // Backward.  g holds e^{d A} G of the token behind; h, the states ahead of the tile, is read a tile ahead.
     float2 g[2][2], dA[2][2] = {};
-    lane.load(w.seg < w.segs - 1 ? nullptr : a.ds1, w.n, a.pack.N, a, w, g);
-    if (w.seg < w.segs - 1) {
-        const int last = w.item - w.seg + w.segs - 1;
-        lane.load(a.rec_g, last, items, a, w, g);
-        for (int i = last - 1; i > w.item; --i) lane.join(a, w, a.rec_g, i, g);
-    }
+    if (w.seg == w.segs - 1) lane.load(a.ds1, w.n, a.pack.N, a, w, g);
+    else lane.load(a.rec_g, w.item, items, a, w, g);
     __syncthreads();
     for (int i = 0; i <= tiles; ++i) {
         if (i < tiles) {
@@ -521,8 +514,13 @@ cudaError_t bwd(const ScanArgs &a, cudaStream_t s) {
     constexpr int bytes = (int)sizeof(BackTiles<T, NS>);
     static_assert(kScanThreads / (CB / kEV) * CB * 8 <= sizeof(BackTiles<T, NS>::us), "the last sums fit the states' place");
     const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<PairShape<NS>::CB>(a);
-    if (a.seg <= a.pack.T) k_scan_starts<T, NS, kWide><<<(unsigned)blocks, kScanThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaSuccess;
+    if (a.seg <= a.pack.T) {
+        k_scan_starts<T, NS, kWide><<<(unsigned)blocks, kScanThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_scan_join(a, false, s);
+        if (e == cudaSuccess) e = launch_scan_join(a, true, s);
+    }
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(k_scan_bwd<T, NS, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;

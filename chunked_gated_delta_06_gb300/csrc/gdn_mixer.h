@@ -107,7 +107,7 @@ struct NormArgs {
     float *part;              // [blocks, 2 or 1, D]
 };
 // blocks of the backward (they set the size of its workspace)
-int norm_bwd_blocks(long long R, int D);
+int norm_bwd_blocks(long long R, int D, int f32);
 cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s);
 

@@ -208,7 +208,8 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         }
         const double bytes = 4.0 * (pack.N + pack.T / L) * s->channels * (2.0 * s->state_dim + 1.0);
         if (bytes > 1073741824.0) continue;
-        auto walk = [&](double tokens) { return std::max((double)L, tokens * across / places + 0.5 * L); };
+        // (a segment's pipeline fills and drains in about 24 tokens)
+        auto walk = [&](double tokens) { return std::max((double)L, tokens * (1.0 + 24.0 / L) * across / places + 0.5 * L); };
         const double t = first * walk(ends) + walk(pack.T) + 60.0 + longest / L;
         if (t < best) {
             best = t;
@@ -366,9 +367,9 @@ gdn::NormArgs norm_args(int64_t rows, int32_t dim, int32_t dtype, int32_t residu
     return a;
 }
 
-size_t norm_workspace(int64_t rows, int32_t dim, bool scale) {
+size_t norm_workspace(int64_t rows, int32_t dim, int32_t dtype, bool scale) {
     Carver c(nullptr);
-    c.take<float>((size_t)gdn::norm_bwd_blocks(rows, dim) * (scale ? 2 : 1) * dim);
+    c.take<float>((size_t)gdn::norm_bwd_blocks(rows, dim, dtype == GDN_DTYPE_F32) * (scale ? 2 : 1) * dim);
     return c.used();
 }
 
@@ -612,7 +613,7 @@ gdn_status gdn_rms_norm_fwd(int64_t rows, int32_t dim, int32_t dtype, int32_t re
 
 size_t gdn_rms_norm_workspace_bytes(int64_t rows, int32_t dim, int32_t dtype, int32_t with_scale) {
     if (rows < 0 || rows > ((int64_t)1 << 30) || dim < 1 || dim > 8192 || !known(dtype)) return 0;
-    return norm_workspace(rows, dim, with_scale != 0);
+    return norm_workspace(rows, dim, dtype, with_scale != 0);
 }
 
 gdn_status gdn_rms_norm_bwd(int64_t rows, int32_t dim, int32_t dtype, int32_t residual_dtype,
@@ -632,7 +633,7 @@ gdn_status gdn_rms_norm_bwd(int64_t rows, int32_t dim, int32_t dtype, int32_t re
     for (const void *q : ptrs)
         if (!aligned16(q)) return GDN_ERR_INVALID_ARG;
     if (!aligned_to(dweight, 4) || !aligned_to(dscale, 4)) return GDN_ERR_INVALID_ARG;
-    const size_t need = norm_workspace(rows, dim, scale != nullptr);
+    const size_t need = norm_workspace(rows, dim, dtype, scale != nullptr);
     if ((st = check_workspace(need, false, workspace, ws_size)) != GDN_OK) return st;
     const size_t n = (size_t)rows * dim, e = bytes_of(dtype), r = stream_there ? bytes_of(residual_dtype) : e;
     const size_t par = sizeof(float) * dim;

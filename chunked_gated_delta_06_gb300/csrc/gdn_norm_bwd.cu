@@ -14,13 +14,15 @@
 namespace gdn {
 namespace {
 
-// Threads a row and vectors (of V elements) a thread.
-template <typename F>
-cudaError_t norm_bwd_shape(bool wide, int nv, F launch) {
+// Threads a row and vectors (of V elements) a thread: 16 bytes of short rows, 4 elements of the others
+// (whose sums for dw and dscale would take the registers of half the blocks).
+template <int E, typename F>   // E: elements of 16 bytes
+cudaError_t norm_bwd_shape(int D, F launch) {
+    if (D % E == 0 && D <= 16 * E) return launch.template operator()<16, 1, E>();
+    if (D % E == 0 && D <= 32 * E) return launch.template operator()<32, 1, E>();
+    const bool wide = D % 4 == 0;
+    const int nv = wide ? D / 4 : D;
     if (wide) {
-        if (nv <= 16) return launch.template operator()<16, 1, 4>();
-        if (nv <= 32) return launch.template operator()<32, 1, 4>();
-        if (nv <= 64) return launch.template operator()<32, 2, 4>();
         if (nv <= 128) return launch.template operator()<64, 2, 4>();
         if (nv <= 256) return launch.template operator()<128, 2, 4>();
         if (nv <= 512) return launch.template operator()<256, 2, 4>();
@@ -52,8 +54,8 @@ struct Places {
 template <int TPR>
 constexpr int norm_stages() { return TPR <= 32 ? 4 : 2; }
 
-template <typename T, typename R, int V, int TPR, int VPT, bool kAhead>
-__global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT <= 1024 ? (TPR >= 1024 ? 1 : 1024 / TPR) : 1)
+template <typename T, typename R, int V, int TPR, int VPT, bool kAhead, bool kScale>
+__global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? (V > 4 ? 2 : 3) : TPR * VPT <= 1024 ? (TPR >= 1024 ? 1 : 1024 / TPR) : 1)
     k_norm_bwd(const __grid_constant__ NormArgs a) {
     constexpr int kThreads = norm_threads<TPR>(), kRows = kThreads / TPR, kStages = norm_stages<TPR>();
     constexpr bool kKeep = TPR <= 32;   // a row's values stay in registers over its sums
@@ -62,14 +64,14 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT
     const long long extent = a.R * a.D;
     const T *x = static_cast<const T *>(a.x), *z = static_cast<const T *>(a.z), *dy = static_cast<const T *>(a.dy);
     const R *hin = static_cast<const R *>(a.hin), *dh = static_cast<const R *>(a.dh);
-    const Places<T, R, V> places(a.z != nullptr, a.dh != nullptr, a.dscale != nullptr);
+    const Places<T, R, V> places(a.z != nullptr, a.dh != nullptr, kScale);
     float dw[VPT][V] = {}, ds[VPT][V] = {};
     int turn = 0;
     const long long step = (long long)gridDim.x * kRows, first = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
     auto place = [&](int stage, int tensor, int k, int bytes) {
         return ring + (size_t)((stage * places.all + tensor) * VPT + k * bytes) * kThreads + threadIdx.x * bytes;
     };
-    auto fetch = [&](long long r, int stage) {
+    [[maybe_unused]] auto fetch = [&](long long r, int stage) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int i = lane + k * TPR;
@@ -77,13 +79,17 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT
             if (r >= a.R || i >= nv || !in_range(at, V, extent, nullptr)) continue;
             auto copy = [&](int tensor, const auto *p) {
                 constexpr int kBytes = V * (int)sizeof(*p);
-                if constexpr (kBytes >= 4) copy_async<kBytes>(place(stage, tensor, k, kBytes), p + at, true);
+                constexpr int kEach = kBytes > 16 ? 16 : kBytes;
+                static_assert(!kAhead || kEach >= 4, "single elements do not come through the ring");
+#pragma unroll
+                for (int b = 0; b < kBytes; b += kEach)
+                    copy_async<kEach>(place(stage, tensor, k, kBytes) + b, reinterpret_cast<const char *>(p + at) + b, true);
             };
             copy(places.h, hin);
             copy(places.dy, dy);
             if (z) copy(places.z, z);
             if (dh) copy(places.dh, dh);
-            if (a.dscale) copy(places.x, x);
+            if (kScale) copy(places.x, x);
         }
     };
     if constexpr (kAhead) {
@@ -158,9 +164,9 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT
                 weight(k, w);
                 read(k);
             }
-            if (a.scale) unpack(load_vec<V>(a.scale, (long long)(lane + k * TPR) * V, a.D, nullptr), scale);
+            if (kScale) unpack(load_vec<V>(a.scale, (long long)(lane + k * TPR) * V, a.D, nullptr), scale);
             if (dh) get(dh, places.dh, k, gv);
-            if (a.dscale) get(x, places.x, k, xv);
+            if (kScale) get(x, places.x, k, xv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float n = h[k][v] * rs, wv = kKeep ? kept_w[k][v] : w[v];
@@ -169,8 +175,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT
                 float d = rs * fmaf(u[k][v], wv, -n * mean);
                 if (dh) d += gv[v];
                 gv[v] = d;
-                if (a.dscale) ds[k][v] = fmaf(d, xv[v], ds[k][v]);
-                dx[v] = a.scale ? d * scale[v] : d;
+                if (kScale) ds[k][v] = fmaf(d, xv[v], ds[k][v]);
+                dx[v] = kScale ? d * scale[v] : d;
             }
             const long long at = at0 + k * TPR * V;
             store_vec<V>(static_cast<T *>(a.dx), at, extent, nullptr, pack<T>(dx));
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? 3 : TPR * VPT
         }
     }
     // the block's rows, in order
-    const int parts = a.dscale ? 2 : 1;
+    constexpr int parts = kScale ? 2 : 1;
     const long long n = (long long)gridDim.x * parts * a.D;
     if constexpr (kRows > 1) {
         __shared__ float all[kRows][TPR * VPT * V];
@@ -219,27 +225,31 @@ struct Launch {
     cudaStream_t s;
     template <int TPR, int VPT, int V>
     cudaError_t operator()() const {
+        return a.scale ? kernel<TPR, VPT, V, true>() : kernel<TPR, VPT, V, false>();
+    }
+    template <int TPR, int VPT, int V, bool kScale>
+    cudaError_t kernel() const {
         constexpr int kThreads = norm_threads<TPR>();
-        const int blocks = norm_bwd_blocks(a.R, a.D);
+        const int blocks = norm_bwd_blocks(a.R, a.D, sizeof(T) == 4);
         if constexpr (V > 1) {
             const Places<T, R, V> places(a.z != nullptr, a.dh != nullptr, a.dscale != nullptr);
             const int bytes = norm_stages<TPR>() * places.all * VPT * kThreads;
             if (bytes <= 160 * 1024) {   // (wider rows are long enough to keep loads on their way by themselves)
-                const cudaError_t e = cudaFuncSetAttribute(k_norm_bwd<T, R, V, TPR, VPT, true>,
+                const cudaError_t e = cudaFuncSetAttribute(k_norm_bwd<T, R, V, TPR, VPT, true, kScale>,
                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
                 if (e != cudaSuccess) return e;
-                k_norm_bwd<T, R, V, TPR, VPT, true><<<blocks, kThreads, bytes, s>>>(a);
+                k_norm_bwd<T, R, V, TPR, VPT, true, kScale><<<blocks, kThreads, bytes, s>>>(a);
                 return cudaGetLastError();
             }
         }
-        k_norm_bwd<T, R, V, TPR, VPT, false><<<blocks, kThreads, 0, s>>>(a);
+        k_norm_bwd<T, R, V, TPR, VPT, false, kScale><<<blocks, kThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
 };
 
 template <typename T, typename R>
 cudaError_t norm_bwd(const NormArgs &a, cudaStream_t s) {
-    return norm_bwd_shape(a.D % 4 == 0, a.D % 4 == 0 ? a.D / 4 : a.D, Launch<T, R>{a, s});
+    return norm_bwd_shape<16 / (int)sizeof(T)>(a.D, Launch<T, R>{a, s});
 }
 
 struct RowsOf {
@@ -255,9 +265,10 @@ struct RowsOf {
 }  // namespace
 
 // A block's sums stay in registers over its rows: as many blocks as run at once, no more.
-int norm_bwd_blocks(long long R, int D) {
+int norm_bwd_blocks(long long R, int D, int f32) {
     int shape[2];
-    norm_bwd_shape(D % 4 == 0, D % 4 == 0 ? D / 4 : D, RowsOf{shape});
+    if (f32) norm_bwd_shape<4>(D, RowsOf{shape});
+    else norm_bwd_shape<8>(D, RowsOf{shape});
     return (int)std::max(1LL, std::min((R + shape[0] - 1) / shape[0], 152LL * std::max(1, (shape[0] > 1 ? 768 : 1024) / shape[1])));
 }
 
@@ -267,7 +278,7 @@ cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {
     else e = a.res == GDN_DTYPE_F32 ? norm_bwd<bf16, float>(a, s) : norm_bwd<bf16, bf16>(a, s);
     if (e != cudaSuccess) return e;
     const int parts = a.dscale ? 2 : 1, D = a.D;
-    return launch_fold(FoldArgs{a.part, norm_bwd_blocks(a.R, D), (long long)parts * D, parts * D, D, a.dw, a.dscale}, s);
+    return launch_fold(FoldArgs{a.part, norm_bwd_blocks(a.R, D, a.f32), (long long)parts * D, parts * D, D, a.dw, a.dscale}, s);
 }
 
 }  // namespace gdn

@@ -119,6 +119,16 @@ struct BackTiles {
     alignas(16) T rB[kRing][TT * NS], rC[kRing][TT * NS];
 };
 
+// The walk forward, ahead of the walk back and in the place of its us: longer tiles, of several marks.
+template <typename T, int NS>
+struct AheadTiles {
+    static constexpr int CB = PairShape<NS>::CB, TT = NS == 32 ? 32 : (sizeof(T) == 2 ? 2048 : 1024) / CB, kRing = 3;
+    float4 dd[2][TT][CB / 2];
+    float B[2][TT][NS];
+    alignas(16) T x[kRing][TT * CB], dt[kRing][TT * CB];
+    alignas(16) T rB[kRing][TT * NS];
+};
+
 // As in the forward, half of the threads are formers and half are walkers, a tile apart.
 template <typename T, int NS, bool kWide>
 __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_constant__ ScanArgs a) {
@@ -128,6 +138,11 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     using Rows = RowsOf<T, NS, TT, N, kWide>;
     extern __shared__ float4 smem[];
     BackTiles<T, NS> &m = *reinterpret_cast<BackTiles<T, NS> *>(smem);
+
+    using Ahead = AheadTiles<T, NS>;
+    constexpr int TF = Ahead::TT;
+    static_assert(sizeof(Ahead) <= sizeof(m.us) && TF % TT == 0, "in the place of us, whole marks");
+    Ahead &f = *reinterpret_cast<Ahead *>(smem);
 
     ScanPlace w;
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
@@ -142,6 +157,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     }
     __syncthreads();
     const int tiles = (w.f - w.b + TT - 1) / TT;
+    const int ahead = (max(tiles - 1, 0) * TT + TF - 1) / TF;   // of the walk forward, which ends at the last mark
     const float ln2 = 0.693147180559945309f;
     const long long sums_extent = items * a.C * (NS + 2);
 
@@ -155,50 +171,52 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
         auto place = [&](T (*ring)[TT * CB], int i) { return reinterpret_cast<V *>(ring[i % R]); };
         auto units = [&](T (*ring)[TT * NS], int i) { return reinterpret_cast<U *>(ring[i % R]); };
         const T *xp = static_cast<const T *>(a.x), *dtp = static_cast<const T *>(a.dt), *Bp = static_cast<const T *>(a.B);
-        // d and d x of the tile at token t, the i-th of its walk
-        auto form = [&](int i, int t, int k, float (&d)[kEV]) {
-            const int row = Tile::row(k);
+        // d and d x of four channels of a token
+        auto form = [&](const V &x, const V &dt, bool there, float4 *dd) {
             float xv[kEV], dv[kEV];
-            unpack(place(m.x, i)[Tile::thread() + k * N], xv);
-            unpack(place(m.dt, i)[Tile::thread() + k * N], dv);
+            unpack(x, xv);
+            unpack(dt, dv);
 #pragma unroll
             for (int j = 0; j < kEV; j += 2) {
-                float2 v = softplus_of(add2(make_float2(dv[j], dv[j + 1]),
-                                            *reinterpret_cast<const float2 *>(&m.bias[col + j])));
-                if (t + row >= w.f) v = both(0.f);   // (which leaves the states alone)
+                float2 v = softplus_of(add2(make_float2(dv[j], dv[j + 1]), *reinterpret_cast<const float2 *>(&m.bias[col + j])));
+                if (!there) v = both(0.f);   // (which leaves the states alone)
                 const float2 dx = mul2(v, make_float2(xv[j], xv[j + 1]));
-                m.dd[i & 1][row][unit_at((col + j) / 2)] = make_float4(v.x, dx.x, v.y, dx.y);
-                d[j] = v.x;
-                d[j + 1] = v.y;
+                dd[unit_at((col + j) / 2)] = make_float4(v.x, dx.x, v.y, dx.y);
             }
         };
-        {   // forward, all tiles but the last
-            Feed x(xp, a.xs, a, w, TT), dt(dtp, a.dts, a, w, TT);
-            RowFeed B(Bp, a.bs, a, w, TT);
+        {
+            using Long = TileOf<T, CB, TF, kEV, N, kWide>;
+            using LongRows = RowsOf<T, NS, TF, N, kWide>;
+            constexpr int RF = Ahead::kRing;
+            FeedOf<Long, T, N, kWide> x(xp, a.xs, a, w, TF), dt(dtp, a.dts, a, w, TF);
+            RowFeedOf<LongRows, T, NS, N, kWide> B(Bp, a.bs, a, w, TF);
             auto fetch = [&](int i) {
-                if (i < tiles - 1) {
-                    x.next(place(m.x, i), a, w, TT);
-                    dt.next(place(m.dt, i), a, w, TT);
-                    B.next(units(m.rB, i), a, TT);
+                if (i < ahead) {
+                    x.next(reinterpret_cast<V *>(f.x[i % RF]), a, w, TF);
+                    dt.next(reinterpret_cast<V *>(f.dt[i % RF]), a, w, TF);
+                    B.next(reinterpret_cast<U *>(f.rB[i % RF]), a, TF);
                 }
                 copies_commit();
             };
             auto all = [&](int i) {
-                float d[kEV];
 #pragma unroll
-                for (int k = 0; k < Tile::NV; ++k)
-                    if (Tile::row(k) < TT) form(i, w.b + i * TT, k, d);
-                Rows::keep_copied(units(m.rB, i), m.B[i & 1]);
+                for (int k = 0; k < Long::NV; ++k) {
+                    const int row = Long::row(k);
+                    if (row >= TF) break;
+                    form(reinterpret_cast<const V *>(f.x[i % RF])[Long::thread() + k * N],
+                         reinterpret_cast<const V *>(f.dt[i % RF])[Long::thread() + k * N], w.b + i * TF + row < w.f, f.dd[i & 1][row]);
+                }
+                LongRows::keep_copied(reinterpret_cast<const U *>(f.rB[i % RF]), f.B[i & 1]);
             };
             fetch(0);
             fetch(1);
             copies_wait<1>();
-            if (tiles > 1) all(0);
+            if (ahead > 0) all(0);
             __syncthreads();
-            for (int i = 0; i < tiles - 1; ++i) {
+            for (int i = 0; i < ahead; ++i) {
                 fetch(i + 2);
                 copies_wait<1>();
-                if (i + 1 < tiles - 1) all(i + 1);
+                if (i + 1 < ahead) all(i + 1);
                 __syncthreads();
             }
         }
@@ -226,12 +244,12 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
             copies_commit();
         };
         auto all = [&](int i) {
-            float d[kEV];
 #pragma unroll
             for (int k = 0; k < Tile::NV; ++k) {
                 const int row = Tile::row(k);
                 if (row >= TT) break;
-                form(i, w.b + (tiles - 1 - i) * TT, k, d);
+                form(place(m.x, i)[Tile::thread() + k * N], place(m.dt, i)[Tile::thread() + k * N],
+                     w.b + (tiles - 1 - i) * TT + row < w.f, m.dd[i & 1][row]);
                 float dyv[kEV], zv[kEV];
                 unpack(place(m.dy, i)[Tile::thread() + k * N], dyv);
                 float2 o[2] = {make_float2(dyv[0], dyv[1]), make_float2(dyv[2], dyv[3])};
@@ -294,18 +312,25 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                 Tile::store(static_cast<T *>(a.ddt), a, w, t, w.f, k, pack<T>(ddv));
                 if (gated) Tile::store(static_cast<T *>(a.dz), a, w, t, w.f, k, pack<T>(dzv));
             }
-            // dC and dB of the tile over the block's channels: four states of one of them a thread
-            for (int v = threadIdx.x; v < TT * L * 2; v += N) {
-                const int j = v / (2 * L), which = v % (2 * L) / L, q = v % L;
+            // dC and dB of the tile over the block's channels: two threads for four states of one of them
+            constexpr int kUnits = TT * 2 * L;
+            static_assert(kUnits % 16 == 0 && kPairs % 2 == 0, "whole warps take part");
+#pragma unroll
+            for (int v0 = 0; v0 < kUnits; v0 += N / 2) {
+                const int v = v0 + (int)threadIdx.x / 2, part = threadIdx.x % 2;
+                if (v >= kUnits) break;
+                const int q = v % L, which = v / L % 2, j = v / (2 * L);
                 float2 s0 = both(0.f), s1 = s0;
 #pragma unroll 8
-                for (int p = 0; p < kPairs; ++p) {
+                for (int p = part; p < kPairs; p += 2) {
                     const int th = p * L + q;
                     const float4 u = m.us[i & 1][j][th][which ^ (th >> 2 & 1)];
                     s0 = add2(s0, make_float2(u.x, u.y));
                     s1 = add2(s1, make_float2(u.z, u.w));
                 }
-                if (t + j < w.f) {
+                s0 = add2(s0, make_float2(__shfl_xor_sync(0xffffffffu, s0.x, 1), __shfl_xor_sync(0xffffffffu, s0.y, 1)));
+                s1 = add2(s1, make_float2(__shfl_xor_sync(0xffffffffu, s1.x, 1), __shfl_xor_sync(0xffffffffu, s1.y, 1)));
+                if (part == 0 && t + j < w.f) {
                     const long long at = (((long long)mine * a.pack.T + t + j) * a.G + w.g) * 2 * NS + which * NS + 4 * q;
                     if (in_range(at, 4, (long long)blocks * a.pack.T * a.G * 2 * NS, a.pack.status))
                         *reinterpret_cast<float4 *>(a.part_bc + at) = make_float4(s0.x, s0.y, s1.x, s1.y);
@@ -356,17 +381,21 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     if (w.segs == 1) lane.load(a.s0, a.s0 ? w.n : -1, a.pack.N, a, w, h);
     else lane.load(a.rec_h, w.item, items, a, w, h);
     __syncthreads();
-    for (int i = 0; i < tiles - 1; ++i) {
-        lane.store(a.marks, mark + i, marks, a, w, h);
+    for (int i = 0; i < ahead; ++i) {
+        for (int j0 = 0; j0 < TF; j0 += TT) {
+            const int tile = i * (TF / TT) + j0 / TT;
+            if (tile >= tiles - 1) break;   // (the last tile's end is nobody's start)
+            lane.store(a.marks, mark + tile, marks, a, w, h);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            const float4 in = m.dd[i & 1][j][unit_at(lane.at)];
-            const float4 b = *reinterpret_cast<const float4 *>(&m.B[i & 1][j][4 * lane.q]);
+            for (int j = 0; j < TT; ++j) {
+                const float4 in = f.dd[i & 1][j0 + j][unit_at(lane.at)];
+                const float4 b = *reinterpret_cast<const float4 *>(&f.B[i & 1][j0 + j][4 * lane.q]);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float2 d = both(p ? in.z : in.x), dx = both(p ? in.w : in.y);
-                h[p][0] = fma2(lane.decay(p, 0, d), h[p][0], mul2(dx, make_float2(b.x, b.y)));
-                h[p][1] = fma2(lane.decay(p, 1, d), h[p][1], mul2(dx, make_float2(b.z, b.w)));
+                for (int p = 0; p < 2; ++p) {
+                    const float2 d = both(p ? in.z : in.x), dx = both(p ? in.w : in.y);
+                    h[p][0] = fma2(lane.decay(p, 0, d), h[p][0], mul2(dx, make_float2(b.x, b.y)));
+                    h[p][1] = fma2(lane.decay(p, 1, d), h[p][1], mul2(dx, make_float2(b.z, b.w)));
+                }
             }
         }
         __syncthreads();
@@ -378,8 +407,8 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     __syncthreads();
     for (int i = 0; i <= tiles; ++i) {
         if (i < tiles) {
-            float2 ahead[2][2];
-            lane.load(i + 1 < tiles ? a.marks : nullptr, mark + tiles - 2 - i, marks, a, w, ahead);
+            float2 next[2][2];
+            lane.load(i + 1 < tiles ? a.marks : nullptr, mark + tiles - 2 - i, marks, a, w, next);
             float4 (*us)[2] = &m.us[i & 1][0][me];   // a token is N of them apart
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
@@ -394,7 +423,6 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                     h[p][1] = fma2(dx, make_float2(b.z, b.w), u1);
                 }
             }
-            float2 tileA[2][2] = {};
 #pragma unroll
             for (int j0 = TT - BT; j0 >= 0; j0 -= BT) {
                 float part[BT][6];   // of each token: sum G B, sum p A / ln 2, sum C h of the two channels
@@ -424,7 +452,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                             sB = k ? fma2(G, b[k], sB) : mul2(G, b[k]);
                             sA = k ? fma2(pk, lane.A[p][k], sA) : mul2(pk, lane.A[p][k]);
                             sC = k ? fma2(c[k], hk, sC) : mul2(c[k], hk);
-                            tileA[p][k] = fma2(pk, d, tileA[p][k]);
+                            dA[p][k] = fma2(pk, d, dA[p][k]);
                             g[p][k] = mul2(lane.decay(p, k, d), G);
                         }
                         part[jj][p] = sB.x + sB.y;
@@ -445,10 +473,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    dA[p][k] = add2(dA[p][k], tileA[p][k]);
-                    h[p][k] = ahead[p][k];
-                }
+                for (int k = 0; k < 2; ++k) h[p][k] = next[p][k];
         }
         __syncthreads();
     }

@@ -122,26 +122,38 @@ __device__ void final_state(const ConvArgs &a, int n, int c) {
 // kAhead groups ahead, copied into shared memory asynchronously (so that no registers wait for them).
 template <typename T, int V, int kTensors>
 struct Stream {
-    static constexpr int kGroup = 4, kAhead = 3, kStages = kAhead + 1;
+    static constexpr int kGroup = 4, kAhead = 3, kStages = kAhead + 1, kStage = kGroup * kTensors * kThreads;
     using Row = Vec<T, V>;
-    Row *ring;           // [kStages][kGroup][kTensors][threads]
-    int t, end;          // the next token to fetch, the last one's successor
-    int stage;
-    __device__ Row *place(int st, int u, int k) const { return ring + ((st * kGroup + u) * kTensors + k) * kThreads + threadIdx.x; }
-    template <typename F>   // address(token, tensor): where its row is, null for none
-    __device__ void fetch(F address) {
+    Row *ring;                  // the thread's place of [kStages][kGroup][kTensors][threads]
+    const T *at[kTensors];      // the next group's first rows
+    long long apart[kTensors];
+    int left, stage;            // tokens to fetch, where the next group goes
+    __device__ const Row &row(int stage, int u, int k) const { return ring[stage * kStage + (u * kTensors + k) * kThreads]; }
+    template <typename F>   // in(k, p): whether a row lies in tensor k
+    __device__ void fetch(F in) {
+        Row *to = ring + stage * kStage;
+        auto copy = [&](int u, int k) {
+            const T *from = at[k] + u * apart[k];
+            if (!in(k, from)) return;
+            if constexpr (sizeof(Row) >= 4) copy_async<(int)sizeof(Row)>(to + (u * kTensors + k) * kThreads, from, true);
+            else to[(u * kTensors + k) * kThreads] = *reinterpret_cast<const Row *>(from);
+        };
+        if (left >= kGroup) {
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
+            for (int u = 0; u < kGroup; ++u)
 #pragma unroll
-            for (int k = 0; k < kTensors; ++k) {
-                const T *from = t + u < end ? address(t + u, k) : nullptr;
-                if (!from) continue;
-                if constexpr (sizeof(Row) >= 4) copy_async<(int)sizeof(Row)>(place(stage, u, k), from, true);
-                else *place(stage, u, k) = *reinterpret_cast<const Row *>(from);
-            }
+                for (int k = 0; k < kTensors; ++k) copy(u, k);
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < left; ++u)
+#pragma unroll
+                for (int k = 0; k < kTensors; ++k) copy(u, k);
+        }
         copies_commit();
-        t += kGroup;
-        stage = (stage + 1) % kStages;
+#pragma unroll
+        for (int k = 0; k < kTensors; ++k) at[k] += kGroup * apart[k];
+        left -= kGroup;
+        stage = stage + 1 < kStages ? stage + 1 : 0;
     }
 };
 
@@ -164,11 +176,9 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
     if (c >= a.C) return;
     const int t0 = (int)(block / across) * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
     const long long extent = (long long)a.pack.T * a.C, x_extent = (a.pack.T - 1) * a.x_stride + a.C;
-    In in{reinterpret_cast<Vec<T, V> *>(ring), t0, t1, 0};
-    auto address = [&](int t, int) -> const T * {
-        const long long at = t * a.x_stride + c;
-        return in_range(at, V, x_extent, a.pack.status) ? static_cast<const T *>(a.x) + at : nullptr;
-    };
+    const T *x0 = static_cast<const T *>(a.x);
+    In in{reinterpret_cast<Vec<T, V> *>(ring) + threadIdx.x, {x0 + t0 * a.x_stride + c}, {a.x_stride}, t1 - t0, 0};
+    auto address = [&](int, const T *p) { return in_range(p - x0, V, x_extent, a.pack.status); };
 #pragma unroll
     for (int g = 0; g < In::kAhead; ++g) in.fetch(address);
     const Channels<T, V, W> ch(a, c);
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
         in.fetch(address);
         copies_wait<In::kAhead>();
         auto one = [&](int u) {
-            unpack(*in.place(stage, u, 0), win[W - 1]);
+            unpack(in.row(stage, u, 0), win[W - 1]);
             float out[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
                 one(u);
             }
         }
-        stage = (stage + 1) % In::kStages;
+        stage = stage + 1 < In::kStages ? stage + 1 : 0;
     }
 }
 
@@ -239,11 +249,10 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     const int t0 = tile * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
     const int reach = (int)min((long long)t1 + W - 1, (long long)a.pack.T);
     const long long extent = (long long)a.pack.T * a.C, x_extent = (a.pack.T - 1) * a.x_stride + a.C;
-    In in{reinterpret_cast<Vec<T, V> *>(ring), t0, reach, 0};
-    auto address = [&](int t, int k) -> const T * {
-        const long long at = t * (k ? (long long)a.C : a.x_stride) + c;
-        return in_range(at, V, k ? extent : x_extent, a.pack.status) ? static_cast<const T *>(k ? a.dy : a.x) + at : nullptr;
-    };
+    const T *x0 = static_cast<const T *>(a.x), *dy0 = static_cast<const T *>(a.dy);
+    In in{reinterpret_cast<Vec<T, V> *>(ring) + threadIdx.x, {x0 + t0 * a.x_stride + c, dy0 + (long long)t0 * a.C + c},
+          {a.x_stride, a.C}, reach - t0, 0};
+    auto address = [&](int k, const T *p) { return in_range(p - (k ? dy0 : x0), V, k ? extent : x_extent, a.pack.status); };
 #pragma unroll
     for (int g = 0; g < In::kAhead; ++g) in.fetch(address);
     const Channels<T, V, W> ch(a, c);
@@ -286,8 +295,8 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
         in.fetch(address);
         copies_wait<In::kAhead>();
         auto one = [&](int u, bool own) {   // d_t, and the sums of the tile's own tokens
-            unpack(*in.place(stage, u, 0), win[W - 1]);
-            unpack(*in.place(stage, u, 1), d[W - 1]);
+            unpack(in.row(stage, u, 0), win[W - 1]);
+            unpack(in.row(stage, u, 1), d[W - 1]);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float g = d[W - 1][v];
@@ -305,6 +314,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
         };
         if (open && t - (W - 1) >= p && t + In::kGroup <= min(e, t1)) {
             // (all of one sequence, every token's dx of the tile: windows move by names alone)
+            T *out = dx + (long long)(t - (W - 1)) * a.C + c;
 #pragma unroll
             for (int u = 0; u < In::kGroup; ++u) {
                 one(u, true);
@@ -315,7 +325,8 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
 #pragma unroll
                     for (int j = 0; j < W; ++j) g[v] = fmaf(ch.w[j][v], d[W - 1 - j][v], g[v]);
                 }
-                store_vec<V>(dx, (long long)(t + u - (W - 1)) * a.C + c, extent, a.pack.status, pack<T>(g));
+                store_vec<V>(out, 0, extent - (out - dx), a.pack.status, pack<T>(g));
+                out += a.C;
                 ch.shift(win);
                 ch.shift(d);
             }
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
                 ch.shift(d);
             }
         }
-        stage = (stage + 1) % In::kStages;
+        stage = stage + 1 < In::kStages ? stage + 1 : 0;
     }
     if (open && e <= reach) run_out();
 #pragma unroll

@@ -79,11 +79,11 @@ struct Channels {
             }
         }
     }
-    __device__ float pre(const float (&win)[W][V], int v) const {
-        float u = b[v];
+    __device__ void pre(const float (&win)[W][V], float (&u)[V]) const {
 #pragma unroll
-        for (int j = 0; j < W; ++j) u = fmaf(w[j][v], win[j][v], u);
-        return u;
+        for (int v = 0; v < V; ++v) u[v] = b[v];
+#pragma unroll
+        for (int j = 0; j < W; ++j) fma_all(u, w[j], win[j]);
     }
     __device__ static void shift(float (&win)[W][V]) {
 #pragma unroll
@@ -191,11 +191,10 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
         auto one = [&](int u) {
             unpack(in.row(stage, u, 0), win[W - 1]);
             float out[V];
+            ch.pre(win, out);
+            if (a.silu)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                out[v] = ch.pre(win, v);
-                if (a.silu) out[v] *= sigmoid_of(out[v]);
-            }
+                for (int v = 0; v < V; ++v) out[v] *= sigmoid_of(out[v]);
             ch.shift(win);
             store_vec<V>(y, 0, extent - (y - static_cast<T *>(a.y)), a.pack.status, pack<T>(out));
             y += a.C;
@@ -297,19 +296,23 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
         auto one = [&](int u, bool own) {   // d_t, and the sums of the tile's own tokens
             unpack(in.row(stage, u, 0), win[W - 1]);
             unpack(in.row(stage, u, 1), d[W - 1]);
+            if (a.silu) {
+                float o[V], sig[V], rest[V];
+                ch.pre(win, o);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float g = d[W - 1][v];
-                if (a.silu) {
-                    const float o = ch.pre(win, v), sig = sigmoid_of(o);
-                    g *= fmaf(o * sig, 1.f - sig, sig);
+                for (int v = 0; v < V; ++v) {
+                    sig[v] = sigmoid_of(o[v]);
+                    rest[v] = 1.f - sig[v];
                 }
-                d[W - 1][v] = g;
-                if (own) {
+                mul_all(o, o, sig);
+                fma_all(sig, o, rest);   // the slope
+                mul_all(d[W - 1], d[W - 1], sig);
+            }
+            if (own) {
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][v] = fmaf(g, win[j][v], dw[j][v]);
-                    db[v] += g;
-                }
+                for (int j = 0; j < W; ++j) fma_all(dw[j], d[W - 1], win[j]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) db[v] += d[W - 1][v];
             }
         };
         if (open && t - (W - 1) >= p && t + In::kGroup <= min(e, t1)) {
@@ -319,12 +322,9 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
             for (int u = 0; u < In::kGroup; ++u) {
                 one(u, true);
                 float g[V];
+                mul_all(g, ch.w[0], d[W - 1]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    g[v] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) g[v] = fmaf(ch.w[j][v], d[W - 1 - j][v], g[v]);
-                }
+                for (int j = 1; j < W; ++j) fma_all(g, ch.w[j], d[W - 1 - j]);
                 store_vec<V>(out, 0, extent - (out - dx), a.pack.status, pack<T>(g));
                 out += a.C;
                 ch.shift(win);

@@ -51,6 +51,56 @@ __device__ __forceinline__ Vec<T, V> pack(const float (&f)[V]) {
     return v;
 }
 
+// Pairs of fp32 in one instruction: the pipe takes two cycles for one, but a warp's turn is spent once.
+__device__ __forceinline__ unsigned long long as_bits(float2 x) { return *reinterpret_cast<unsigned long long *>(&x); }
+__device__ __forceinline__ float2 as_pair(unsigned long long x) { return *reinterpret_cast<float2 *>(&x); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
+    return as_pair(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
+    return as_pair(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)), "l"(as_bits(c)));
+    return as_pair(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The same for vectors (element by element where they are odd): the bits are those of fmaf and of products.
+template <int V>
+__device__ __forceinline__ void fma_all(float (&acc)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 r = fma2(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]), make_float2(acc[v], acc[v + 1]));
+            acc[v] = r.x;
+            acc[v + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(a[v], b[v], acc[v]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void mul_all(float (&out)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 r = mul2(make_float2(a[v], a[v + 1]), make_float2(b[v], b[v + 1]));
+            out[v] = r.x;
+            out[v + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = a[v] * b[v];
+    }
+}
+
 // V elements from i on of a buffer of n (zeros outside it, in the checked build).
 template <int V, typename T>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *p, long long i, long long n, int *status) {

@@ -14,24 +14,6 @@
 
 namespace gdn {
 
-__device__ __forceinline__ unsigned long long as_bits(float2 x) { return *reinterpret_cast<unsigned long long *>(&x); }
-__device__ __forceinline__ float2 as_pair(unsigned long long x) { return *reinterpret_cast<float2 *>(&x); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
-    return as_pair(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)));
-    return as_pair(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_bits(a)), "l"(as_bits(b)), "l"(as_bits(c)));
-    return as_pair(d);
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 exp2_of(float2 x) { return make_float2(exp2_of(x.x), exp2_of(x.y)); }
 
 // softplus(u) = max(u, 0) + log(1 + e^-|u|), the logarithm as 2 artanh(e / (2 + e)): its series in

@@ -93,8 +93,8 @@ def _ptr(t):
 
 # ------------------------------------------------------------------------------ convolution
 def _conv(x, weight, bias):
-    if x.dim() != 2 or weight.dim() != 2:
-        raise ValueError("x must be [tokens, channels] and weight [channels, width]")
+    if x.dim() != 2 or weight.dim() != 2 or not 2 <= weight.shape[1] <= 4:
+        raise ValueError("x must be [tokens, channels] and weight [channels, width], width 2, 3 or 4")
     dev, code = _first(x, "x")
     T, C = x.shape
     W = weight.shape[1]

@@ -79,7 +79,7 @@ struct ScanArgs {
     void *dx, *ddt, *dz, *dB, *dC;
     float *dA_log, *dD, *ddt_bias, *ds0;
     float *rec_g;                                 // [items, C, Ns] gradients at the segments' starts
-    float *marks;                                 // [marks, C, Ns] states ahead of each tile
+    float *marks, *mark_d;                        // [marks, C, Ns] states ahead of each tile; [marks, C], if split
     float *part_bc;                               // [blocks of a group, T, G, 2 Ns]
     float *part_c;                                // [items, C, Ns + 2]: dA, dD, ddt_bias
 };

@@ -178,15 +178,15 @@ int64_t scan_across(const gdn_scan_shape *s, int for_backward) {
 constexpr int kSegment = 32;   // segments are whole tiles of every kernel that walks them
 constexpr int kNoSplit = 0x7fffffff;
 
-// Tokens of a segment (kNoSplit: none).  A block walks its tokens one after another, so a few long
-// sequences leave SMs idle.  In units of a token's time in a block that has its SM for itself (forward
-// 90 ns, backward 300 ns), a walk takes as long as its longest chain, a fifth more for the blocks that
-// share its SM, or as all its blocks' tokens over the SMs (which a second block on an SM makes worth 1.08
-// or 1.4) and half a segment for the last ones; a split scan walks its segments for their ends first
-// (0.66 of a forward, 0.3 of a backward), and costs about 60 tokens for the launches and one for each
-// segment of the longest sequence, whose records are joined one after another.  Forward of 4 x 4096 tokens of 4096 channels: 365 us, split 510; of 65536
-// tokens of 2048: 5710 us, split 1004.  Backward: 1699 and 1918, of 11 sequences up to 6969 tokens 2357
-// and 1958.
+// Tokens of a segment (kNoSplit: none).  A block walks its tokens one after another, so a few long sequences
+// leave SMs idle, and blocks of one length end together, or one wave of them late.  Times are in units of a
+// token's in a block that has its SM for itself (forward 90 ns, backward 260 ns); a second block on an SM
+// makes it worth 1.08 or 1.27.  A split walk takes as long as its blocks' tokens over the SMs (a segment's
+// pipeline fills and drains in 24 or 32), half a segment for the last ones, about 60 for the launches and
+// one for each segment of the longest sequence, whose records are joined one after another.  A split
+// forward walks its segments for their ends first, at 0.66 of a token; the backward walks ahead anyway.
+// Measured, unsplit and split: forward of 4 x 4096 tokens of 4096 channels 351 and 500 us, of 65536 of 2048
+// 5480 and 970; backward of the same 4 x 4096 1715 and 1646, of 11 sequences up to 6969 tokens 2415 and 1654.
 int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &pack, int for_backward) {
     if (s->segment_tokens < 0) return kNoSplit;
     if (s->segment_tokens > 0) {
@@ -194,23 +194,29 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         return seg <= pack.T ? (int)seg : kNoSplit;
     }
     const int32_t *cu = p->cu_seqlens_host;
-    const double places = (for_backward ? 1.4 : 1.08) * 152.0, first = for_backward ? 0.3 : 0.66;
-    const double across = (double)scan_across(s, for_backward);
+    const double across = (double)scan_across(s, for_backward), blocks = across * pack.N;
+    const double each = pack.T * across / ((for_backward ? 1.27 : 1.08) * 152.0), fill = for_backward ? 32.0 : 24.0;
     int longest = 0;
     for (int n = 0; n < pack.N; ++n) longest = std::max(longest, cu[n + 1] - cu[n]);
-    double best = std::max(1.2 * longest, pack.T * across / places);
+    double best = std::max(1.2 * longest, each);
+    if (for_backward) {   // (up to 304 blocks run at once, 1.6 of a token's time each; more of them in waves)
+        const double waves = blocks <= 152 ? 0.0 : blocks <= 304 ? std::min(1.6 * longest, each + 0.5 * longest) : each + 0.45 * longest;
+        best = std::max(1.05 * longest, waves);
+    }
     int seg = kNoSplit;
     for (int L = 64; L < longest; L *= 2) {
-        double ends = 0.0;
-        for (int n = 0; n < pack.N; ++n) {
-            const int len = cu[n + 1] - cu[n];
-            ends += len > 0 ? (double)((len - 1) / L) * L : 0.0;
-        }
         const double bytes = 4.0 * (pack.N + pack.T / L) * s->channels * (2.0 * s->state_dim + 1.0);
         if (bytes > 1073741824.0) continue;
-        // (a segment's pipeline fills and drains in about 24 tokens)
-        auto walk = [&](double tokens) { return std::max((double)L, tokens * (1.0 + 24.0 / L) * across / places + 0.5 * L); };
-        const double t = first * walk(ends) + walk(pack.T) + 60.0 + longest / L;
+        auto walk = [&](double part) { return std::max((double)L, part * each * (1.0 + fill / L) + 0.5 * L); };
+        double t = walk(1.0) + 60.0 + longest / L;
+        if (!for_backward) {
+            double ends = 0.0;   // the tokens ahead of sequences' last segments
+            for (int n = 0; n < pack.N; ++n) {
+                const int len = cu[n + 1] - cu[n];
+                ends += len > 0 ? (double)((len - 1) / L) * L : 0.0;
+            }
+            t += 0.66 * walk(ends / std::max(1, pack.T));
+        }
         if (t < best) {
             best = t;
             seg = L;
@@ -229,7 +235,9 @@ size_t carve_scan(const gdn_scan_shape *s, gdn::ScanArgs &a, int for_backward, v
     }
     if (for_backward) {
         const size_t per = C / s->groups, blocks = (per + scan_block(s, 1) - 1) / scan_block(s, 1);
-        a.marks = c.take<float>(((size_t)a.pack.N + a.pack.T / gdn::scan_mark_tile()) * C * NS);
+        const size_t marks = (size_t)a.pack.N + a.pack.T / gdn::scan_mark_tile();
+        a.marks = c.take<float>(marks * C * NS);
+        if (a.seg <= a.pack.T) a.mark_d = c.take<float>(marks * C);
         a.part_bc = c.take<float>(blocks * (size_t)a.pack.T * s->groups * 2 * NS);
         a.part_c = c.take<float>(items * C * (NS + 2));
     }

@@ -1,57 +1,69 @@
 // gdn_scan.cu -- the selective scan's forward (packed, and over pool slots), its state pass over the
 // segments of a split scan, and the step of one token for each row.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_scan.cuh"
 
 namespace gdn {
 namespace {
 
+// What a walk is for: the outputs; a segment's end, for the segments behind it; or, for a gradient, the
+// states ahead of the tiles and, of a split sequence, both the segment's end and its start's gradient.
+enum WalkFor { kOutputs, kEnds, kMarks };
+
 // Half of a block's warps ("formers") form d, d x and the outputs, the others ("walkers") walk the
-// states, up to 16 of a channel a thread.  While one tile is walked the next one is formed, the
-// outputs of the one before are written and the inputs of the one after next are on their way.
-template <int NS>
+// states, up to 16 of a channel a thread (8 where each has its decay since the start and its gradient
+// too).  While one tile is walked the next one is formed, the outputs of the one before are written and
+// the inputs of the one after next are on their way.
+template <int NS, WalkFor kFor>
 struct WalkShape {
-    static constexpr int S = NS < 16 ? NS : 16, L = NS / S;   // states of a walker, walkers of a channel
+    static constexpr int kMost = kFor == kMarks ? 8 : 16;
+    static constexpr int S = NS < kMost ? NS : kMost, L = NS / S;   // states of a walker, walkers of a channel
     static constexpr int kHalf = 128;                         // threads of either kind
     static constexpr int CB = kHalf / L;                      // channels of a block
     static constexpr int TT = 16;                             // tokens of a tile
     static constexpr int kRing = 4;                           // tiles of inputs: finished, walked, formed, on their way
 };
 
-template <typename T, int NS, bool kEnds>
+template <typename T, int NS, WalkFor kFor>
 struct ScanTiles {
-    static constexpr int CB = WalkShape<NS>::CB, TT = WalkShape<NS>::TT, kRing = WalkShape<NS>::kRing;
+    using Shape = WalkShape<NS, kFor>;
+    static constexpr int CB = Shape::CB, TT = Shape::TT, kRing = Shape::kRing;
+    static constexpr int kMore = kFor == kEnds ? 1 : kRing, kDy = kFor == kMarks ? kRing : 1;
     float d[2][TT][CB], dx[2][TT][CB];   // d and d x, channels at channel_at
-    float B[2][TT][NS], C[2][kEnds ? 1 : TT][NS];
-    float y[2][kEnds ? 1 : TT][CB];
+    float B[2][TT][NS], C[2][kFor == kEnds ? 1 : TT][NS];
+    float y[2][kFor == kEnds ? 1 : TT][CB];   // the walkers' sums; for marks o, of the formers, at channel_at
     float bias[CB], skip[CB];
-    alignas(16) T x[kRing][TT * CB], dt[kRing][TT * CB], z[kEnds ? 1 : kRing][TT * CB];
-    alignas(16) T rB[kRing][TT * NS], rC[kEnds ? 1 : kRing][TT * NS];
+    alignas(16) T x[kRing][TT * CB], dt[kRing][TT * CB], z[kMore][TT * CB], dy[kDy][TT * CB];
+    alignas(16) T rB[kRing][TT * NS], rC[kMore][TT * NS];
 };
 
 // Runs of four channels change places, so that formers that write eight each meet no bank twice.
 __device__ __forceinline__ int channel_at(int c) { return c ^ (c >> 3 & 4); }
 
-// kEnds: the state pass alone (no outputs), for the segments that have another one behind them.
-template <typename T, int NS, bool kWide, bool kEnds>
-__global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
+// A segment's end is had without its start (from nothing): the join adds what the start leaves.  So is the
+// gradient at the start from nothing behind, walking forward too, as each token's part decays by what the
+// walk has gone through: with P_t the product of the decays up to t it is the sum of P_t C_t o_t.
+// In 32 bits, P loses 2^-22 a token, as the walked state does.
+template <typename T, int NS, bool kWide, WalkFor kFor>
+__global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
     k_scan_fwd(const __grid_constant__ ScanArgs a) {
-    using Shape = WalkShape<NS>;
+    using Shape = WalkShape<NS, kFor>;
     constexpr int CB = Shape::CB, L = Shape::L, S = Shape::S, TT = Shape::TT, R = Shape::kRing, EV = 8;
     constexpr int kHalf = Shape::kHalf;
     using Tile = TileOf<T, CB, TT, EV, kHalf, kWide>;
     using Rows = RowsOf<T, NS, TT, kHalf, kWide>;
-    using Tiles = ScanTiles<T, NS, kEnds>;
+    using Tiles = ScanTiles<T, NS, kFor>;
     extern __shared__ float4 smem[];
     Tiles &m = *reinterpret_cast<Tiles *>(smem);
 
     ScanPlace w;
     if (!scan_place<CB>(a, blockIdx.x, &w)) {
-        if (!kEnds && a.pack.status && w.item == a.pack.N + a.pack.T / a.seg) check_offsets(a.pack);
+        if (kFor == kOutputs && a.pack.status && w.item == a.pack.N + a.pack.T / a.seg) check_offsets(a.pack);
         return;
     }
-    if (kEnds && w.seg == w.segs - 1) return;
+    if (kFor == kEnds && w.seg == w.segs - 1) return;
     for (int i = threadIdx.x; i < CB; i += 2 * kHalf) {
         const bool there = w.c0 + i < w.cend && in_range(w.c0 + i, 1, a.C, a.pack.status);
         m.bias[i] = there && a.dt_bias ? a.dt_bias[w.c0 + i] : 0.f;
@@ -65,9 +77,9 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
         using U = typename Rows::V;
         using Feed = FeedOf<Tile, T, kHalf, kWide>;
         using RowFeed = RowFeedOf<Rows, T, NS, kHalf, kWide>;
-        const bool gated = a.z != nullptr;
+        const bool gated = a.z != nullptr, more = kFor == kOutputs || (kFor == kMarks && w.seg > 0);   // C, and the gate
         Feed x(static_cast<const T *>(a.x), a.xs, a, w, TT), dt(static_cast<const T *>(a.dt), a.dts, a, w, TT);
-        Feed z(static_cast<const T *>(a.z), a.zs, a, w, TT);
+        Feed z(static_cast<const T *>(a.z), a.zs, a, w, TT), dy(static_cast<const T *>(a.dy), a.C, a, w, TT);
         RowFeed B(static_cast<const T *>(a.B), a.bs, a, w, TT), C(static_cast<const T *>(a.Cm), a.cs, a, w, TT);
         const int col = Tile::col();
         auto place = [&](T (*ring)[TT * CB], int i) { return reinterpret_cast<V *>(ring[i % R]); };
@@ -76,8 +88,9 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
                 x.next(place(m.x, i), a, w, TT);
                 dt.next(place(m.dt, i), a, w, TT);
                 B.next(reinterpret_cast<U *>(m.rB[i % R]), a, TT);
-                if (!kEnds) {
+                if (more) {
                     if (gated) z.next(place(m.z, i), a, w, TT);
+                    if (kFor == kMarks) dy.next(place(m.dy, i), a, w, TT);
                     C.next(reinterpret_cast<U *>(m.rC[i % R]), a, TT);
                 }
             }
@@ -109,9 +122,24 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
                     *reinterpret_cast<float4 *>(&m.d[i & 1][row][channel_at(col + j)]) = make_float4(d4[j], d4[j + 1], d4[j + 2], d4[j + 3]);
                     *reinterpret_cast<float4 *>(&m.dx[i & 1][row][channel_at(col + j)]) = make_float4(dx4[j], dx4[j + 1], dx4[j + 2], dx4[j + 3]);
                 }
+                if (kFor != kMarks || !more) continue;
+                float o[EV], zv[EV];
+                unpack(place(m.dy, i)[Tile::thread() + k * kHalf], o);
+                if (gated) {
+                    unpack(place(m.z, i)[Tile::thread() + k * kHalf], zv);
+#pragma unroll
+                    for (int j = 0; j < EV; j += 2) {
+                        const float2 g = mul2(make_float2(o[j], o[j + 1]), silu_of(make_float2(zv[j], zv[j + 1])));
+                        o[j] = g.x;
+                        o[j + 1] = g.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < EV; j += 4)
+                    *reinterpret_cast<float4 *>(&m.y[i & 1][row][channel_at(col + j)]) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
             }
             Rows::keep_copied(reinterpret_cast<const U *>(m.rB[i % R]), m.B[i & 1]);
-            if (!kEnds) Rows::keep_copied(reinterpret_cast<const U *>(m.rC[i % R]), m.C[i & 1]);
+            if (more) Rows::keep_copied(reinterpret_cast<const U *>(m.rC[i % R]), m.C[i & 1]);
         };
         auto finish = [&](int i) {
 #pragma unroll
@@ -142,7 +170,7 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
             fetch(i + 2);
             copies_wait<1>();
             if (i + 1 < tiles) form(i + 1);
-            if (!kEnds && i > 0) finish(i - 1);
+            if (kFor == kOutputs && i > 0) finish(i - 1);
             __syncthreads();
         }
         return;
@@ -156,72 +184,113 @@ __global__ void __launch_bounds__(2 * WalkShape<NS>::kHalf, 2)
     // The state ahead of the segment.  The record of the last segment, which has no end to keep, first
     // holds the state ahead of the sequence: a slot is read once, before any block writes it.
     typename Lane::States h;
-    if (kEnds || w.segs == 1) {
+    if (kFor != kOutputs || w.segs == 1) {
         const int from = w.seg == 0 ? scan_start_row(a, w.n) : -1;
         lane.load(a.s0, from, a.slots.idx ? a.slots.num_slots : a.pack.N, a, w, h);
-        if (kEnds && w.seg == 0) lane.store(a.rec_h, last, items, a, w, h);
+        if (kFor != kOutputs && w.segs > 1 && w.seg == 0) lane.store(a.rec_h, last, items, a, w, h);
     } else {
         lane.load(a.rec_h, w.item, items, a, w, h);
     }
     float total = 0.f;
     const int place = channel_at(lane.at);
+    const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
     __syncthreads();
-    for (int i = 0; i <= tiles; ++i) {
-        if (i < tiles) {
-            const float *d = m.d[i & 1][0] + place, *dx = m.dx[i & 1][0] + place;
-            const float4 *B = reinterpret_cast<const float4 *>(m.B[i & 1][0] + S * lane.q);
-            const float4 *C = reinterpret_cast<const float4 *>(m.C[i & 1][0] + S * lane.q);
-            float *y = m.y[i & 1][0] + lane.at;
-            float sum = 0.f;
-            // All of the tile's tokens: those past the segment change nothing.  The decays, B and C are
-            // formed and read one token ahead of the states that take them.
-            float2 in = make_float2(d[0], dx[0]), dec[H], b[H], c[H];
-            auto ahead = [&](int t) {
+    // kBoth: with the gradient at the segment's start, from nothing behind it
+    auto walk = [&](auto both_) {
+        constexpr bool kBoth = decltype(both_)::value, kC = kFor == kOutputs || kBoth;
+        typename Lane::States P, g;
+        if constexpr (kBoth) {
 #pragma unroll
-                for (int k = 0; k < H; k += 2) {
-                    const float4 v = B[(t * NS + 2 * k) / 4];
-                    b[k] = make_float2(v.x, v.y);
-                    b[k + 1] = make_float2(v.z, v.w);
-                    if (!kEnds) {
-                        const float4 u = C[(t * NS + 2 * k) / 4];
-                        c[k] = make_float2(u.x, u.y);
-                        c[k + 1] = make_float2(u.z, u.w);
+            for (int k = 0; k < H; ++k) {
+                P[0][k] = both(1.f);
+                g[0][k] = both(0.f);
+            }
+        }
+        for (int i = 0; i <= tiles; ++i) {
+            if (i < tiles) {
+                const float *d = m.d[i & 1][0] + place, *dx = m.dx[i & 1][0] + place, *o = m.y[i & 1][0] + place;
+                const float4 *B = reinterpret_cast<const float4 *>(m.B[i & 1][0] + S * lane.q);
+                const float4 *C = reinterpret_cast<const float4 *>(m.C[i & 1][0] + S * lane.q);
+                float *y = m.y[i & 1][0] + lane.at;
+                // All of the tile's tokens: those past the segment change nothing.  The decays, B and C are
+                // formed and read one token ahead of the states that take them.
+                float2 in = make_float2(d[0], dx[0]), dec[H], b[H], c[H];
+                float oc = kBoth ? o[0] : 0.f;
+                auto ahead = [&](int t) {
+#pragma unroll
+                    for (int k = 0; k < H; k += 2) {
+                        const float4 v = B[(t * NS + 2 * k) / 4];
+                        b[k] = make_float2(v.x, v.y);
+                        b[k + 1] = make_float2(v.z, v.w);
+                        if (kC) {
+                            const float4 u = C[(t * NS + 2 * k) / 4];
+                            c[k] = make_float2(u.x, u.y);
+                            c[k + 1] = make_float2(u.z, u.w);
+                        }
                     }
-                }
-            };
-#pragma unroll
-            for (int k = 0; k < H; ++k) dec[k] = lane.decay(0, k, both(in.x));
-            ahead(0);
-            float2 next = make_float2(d[CB], dx[CB]);
-#pragma unroll 8
-            for (int t = 0; t < TT; ++t) {
-                float2 y2[2] = {both(0.f), both(0.f)};
-                const float2 input = both(in.y);
-#pragma unroll
-                for (int k = 0; k < H; ++k) {
-                    h[0][k] = fma2(dec[k], h[0][k], mul2(input, b[k]));
-                    if (!kEnds) y2[k & 1] = fma2(c[k], h[0][k], y2[k & 1]);
-                }
-                if (kEnds) sum += in.x;
-                const int u = min(t + 1, TT - 1);
-                in = next;
-                next = make_float2(d[min(t + 2, TT - 1) * CB], dx[min(t + 2, TT - 1) * CB]);
-                ahead(u);
+                };
 #pragma unroll
                 for (int k = 0; k < H; ++k) dec[k] = lane.decay(0, k, both(in.x));
-                if (!kEnds) {
-                    const float2 y1 = add2(y2[0], y2[1]);
-                    float out = y1.x + y1.y;
+                ahead(0);
+                float2 next = make_float2(d[CB], dx[CB]);
+                float sum = 0.f;
+#pragma unroll 8
+                for (int t = 0; t < TT; ++t) {
+                    if (kFor == kMarks && t % kMarkTile == 0 && w.b + i * TT + t < w.f) {
+                        const long long to = mark + (i * TT + t) / kMarkTile;
+                        lane.store(a.marks, to, marks, a, w, h);
+                        if (kBoth && lane.q == 0 && lane.c < w.cend && in_range(to * a.C + lane.c, 1, marks * a.C, a.pack.status))
+                            a.mark_d[to * a.C + lane.c] = total + sum;
+                    }
+                    float2 y2[2] = {both(0.f), both(0.f)};
+                    const float2 input = both(in.y);
 #pragma unroll
-                    for (int o = L / 2; o; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
-                    if (L == 1 || lane.q == 0) y[t * CB] = out;
+                    for (int k = 0; k < H; ++k) {
+                        h[0][k] = fma2(dec[k], h[0][k], mul2(input, b[k]));
+                        if (kFor == kOutputs) y2[k & 1] = fma2(c[k], h[0][k], y2[k & 1]);
+                        if constexpr (kBoth) {
+                            P[0][k] = mul2(P[0][k], dec[k]);
+                            g[0][k] = fma2(P[0][k], mul2(both(oc), c[k]), g[0][k]);
+                        }
+                    }
+                    if (kFor != kOutputs) sum += in.x;
+                    const int u = min(t + 1, TT - 1);
+                    in = next;
+                    if (kBoth) oc = o[u * CB];
+                    next = make_float2(d[min(t + 2, TT - 1) * CB], dx[min(t + 2, TT - 1) * CB]);
+                    ahead(u);
+#pragma unroll
+                    for (int k = 0; k < H; ++k) dec[k] = lane.decay(0, k, both(in.x));
+                    if (kFor == kOutputs) {
+                        const float2 y1 = add2(y2[0], y2[1]);
+                        float out = y1.x + y1.y;
+#pragma unroll
+                        for (int o = L / 2; o; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
+                        if (L == 1 || lane.q == 0) y[t * CB] = out;
+                    }
                 }
+                total += sum;
             }
-            total += sum;
+            __syncthreads();
         }
-        __syncthreads();
+        if constexpr (kBoth) {
+            if (w.seg == w.segs - 1 && a.ds1) {
+                typename Lane::States end;
+                lane.load(a.ds1, w.n, a.pack.N, a, w, end);
+#pragma unroll
+                for (int k = 0; k < H; ++k) g[0][k] = fma2(P[0][k], end[0][k], g[0][k]);
+            }
+            lane.store(a.rec_g, w.item, items, a, w, g);
+        }
+    };
+    if constexpr (kFor == kMarks) {
+        if (w.seg > 0) walk(std::true_type{});
+        else walk(std::false_type{});
+    } else {
+        walk(std::false_type{});
     }
-    if (kEnds) {
+    if (kFor != kOutputs) {
+        if (w.seg == w.segs - 1) return;
         lane.store(a.rec_h, w.item, items, a, w, h);
         const long long at = (long long)w.item * a.C + lane.c;
         if (lane.q == 0 && lane.c < w.cend && in_range(at, 1, items * a.C, a.pack.status)) a.rec_d[at] = total;
@@ -356,20 +425,21 @@ __global__ void __launch_bounds__(256, NS < 32 ? 3 : 1) k_scan_step(const __grid
     }
 }
 
-template <typename T, int NS, bool kWide, bool kEnds>
+template <typename T, int NS, bool kWide, WalkFor kFor>
 cudaError_t scan_kernel(const ScanArgs &a, cudaStream_t s) {
-    const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<WalkShape<NS>::CB>(a);
-    const unsigned grid = (unsigned)(blocks + (!kEnds && a.pack.status ? 1 : 0));
-    constexpr int bytes = (int)sizeof(ScanTiles<T, NS, kEnds>), threads = 2 * WalkShape<NS>::kHalf;
-    const cudaError_t e = cudaFuncSetAttribute(k_scan_fwd<T, NS, kWide, kEnds>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    using Shape = WalkShape<NS, kFor>;
+    const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<Shape::CB>(a);
+    const unsigned grid = (unsigned)(blocks + (kFor == kOutputs && a.pack.status ? 1 : 0));
+    constexpr int bytes = (int)sizeof(ScanTiles<T, NS, kFor>), threads = 2 * Shape::kHalf;
+    const cudaError_t e = cudaFuncSetAttribute(k_scan_fwd<T, NS, kWide, kFor>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k_scan_fwd<T, NS, kWide, kEnds><<<grid, threads, bytes, s>>>(a);
+    k_scan_fwd<T, NS, kWide, kFor><<<grid, threads, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, int NS, bool kEnds>
+template <typename T, int NS, WalkFor kFor>
 cudaError_t scan(const ScanArgs &a, cudaStream_t s) {
-    return scan_wide(a, 8) ? scan_kernel<T, NS, true, kEnds>(a, s) : scan_kernel<T, NS, false, kEnds>(a, s);
+    return scan_wide(a, 8) ? scan_kernel<T, NS, true, kFor>(a, s) : scan_kernel<T, NS, false, kFor>(a, s);
 }
 
 template <typename T, int NS>
@@ -386,15 +456,15 @@ cudaError_t step(const ScanArgs &a, int batch, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <bool kEnds>
+template <WalkFor kFor>
 cudaError_t scan_of(const ScanArgs &a, cudaStream_t s) {
-    if (a.f32) return a.Ns == 8 ? scan<float, 8, kEnds>(a, s) : a.Ns == 16 ? scan<float, 16, kEnds>(a, s) : scan<float, 32, kEnds>(a, s);
-    return a.Ns == 8 ? scan<bf16, 8, kEnds>(a, s) : a.Ns == 16 ? scan<bf16, 16, kEnds>(a, s) : scan<bf16, 32, kEnds>(a, s);
+    if (a.f32) return a.Ns == 8 ? scan<float, 8, kFor>(a, s) : a.Ns == 16 ? scan<float, 16, kFor>(a, s) : scan<float, 32, kFor>(a, s);
+    return a.Ns == 8 ? scan<bf16, 8, kFor>(a, s) : a.Ns == 16 ? scan<bf16, 16, kFor>(a, s) : scan<bf16, 32, kFor>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_ends(const ScanArgs &a, cudaStream_t s) { return scan_of<true>(a, s); }
+cudaError_t launch_scan_marks(const ScanArgs &a, cudaStream_t s) { return scan_of<kMarks>(a, s); }
 
 cudaError_t launch_scan_join(const ScanArgs &a, bool backward, cudaStream_t s) {
     const int across = (int)(((long long)a.C * a.Ns / 4 + 127) / 128);
@@ -406,11 +476,11 @@ cudaError_t launch_scan_join(const ScanArgs &a, bool backward, cudaStream_t s) {
 
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s) {
     if (a.seg <= a.pack.T) {
-        cudaError_t e = launch_scan_ends(a, s);
+        cudaError_t e = scan_of<kEnds>(a, s);
         if (e == cudaSuccess) e = launch_scan_join(a, false, s);
         if (e != cudaSuccess) return e;
     }
-    return scan_of<false>(a, s);
+    return scan_of<kOutputs>(a, s);
 }
 
 cudaError_t launch_scan_step(const ScanArgs &a, int batch, cudaStream_t s) {

@@ -57,6 +57,12 @@ struct ScanPlace {
 
 __device__ __forceinline__ int first_item(const ScanArgs &a, int n) { return n + offset_of(a.pack, n) / a.seg; }
 
+constexpr int kMarkTile = 8;   // tokens of a tile of the gradient's walk; the states ahead of each are its marks
+// (the marks of a sequence follow n + s / tile, as the items of a scan do; a segment is whole tiles)
+__device__ __forceinline__ long long first_mark(const ScanArgs &a, const ScanPlace &w) {
+    return (long long)w.n + w.s / kMarkTile + (w.b - w.s) / kMarkTile;
+}
+
 template <int CB>   // channels of a block
 __device__ __forceinline__ bool scan_place(const ScanArgs &a, long long block, ScanPlace *p) {
     const int per_group = a.C / a.G, blocks = (per_group + CB - 1) / CB, across = a.G * blocks;
@@ -355,8 +361,10 @@ long long scan_across(const ScanArgs &a) {
     return (long long)a.G * ((a.C / a.G + CB - 1) / CB);
 }
 
-// The records of a split scan: end states and sums of d of every segment but the last of each sequence,
-cudaError_t launch_scan_ends(const ScanArgs &a, cudaStream_t s);
+// For a gradient: marks, the states ahead of every tile (in a segment behind another one those that it
+// has from nothing, with mark_d, the sums of d since its start), and of split sequences the records:
+// end states and sums of d of every segment but the last, start gradients of every one but the first,
+cudaError_t launch_scan_marks(const ScanArgs &a, cudaStream_t s);
 // and then in the place of rec_h the state ahead of each segment, in the place of rec_g (backward) the
 // gradient behind each segment but the last.
 cudaError_t launch_scan_join(const ScanArgs &a, bool backward, cudaStream_t s);

@@ -7,8 +7,8 @@
 //   ddt_t = dd_t softplus'(u_t),                          dA_log = A sum_t p_t d_t
 //   dz_t = dy_t (sum_n C_t h_t + D x_t) silu'(z_t)
 //
-// A block walks its segment forward once for the states ahead of each tile (the marks, kept in
-// the workspace), then the tiles backwards: the states of a tile are formed again and wait in shared
+// A walk forward ahead of this one has left the states ahead of each tile in the workspace (the marks).
+// A block walks its segment's tiles backwards: the states of a tile are formed again and wait in shared
 // memory as e^{dA} h_{t-1}, 32 bytes a thread and token, and each is replaced by the thread's
 // dC and dB as the walk back reads it, which the block then adds over its channels.
 #include "gdn_scan.cuh"
@@ -31,102 +31,19 @@ using PairLane = ScanLane<NS, 2, 4, kFirst>;
 // runs of 8, so that threads that write the four units of eight channels meet no bank twice.
 __device__ __forceinline__ int unit_at(int unit) { return unit ^ (unit >> 3 & 3); }
 
-constexpr int kMarkTile = 8;   // tokens of a tile
 constexpr int kEV = 4;
-
-__device__ __forceinline__ long long first_mark(const ScanArgs &a, const ScanPlace &w) {
-    // (the marks of a sequence follow n + s / tile, as the items of a scan do; a segment is whole tiles)
-    return (long long)w.n + w.s / kMarkTile + (w.b - w.s) / kMarkTile;
-}
-
-// The gradient at the start of each segment but a sequence's first, from nothing behind it (for
-// the last segment, from the final state's gradient).
-template <typename T, int NS, bool kWide>
-__global__ void __launch_bounds__(kScanThreads) k_scan_starts(const __grid_constant__ ScanArgs a) {
-    constexpr int CB = PairShape<NS>::CB, TT = 16;
-    using Tile = TileOf<T, CB, TT, kEV, kScanThreads, kWide>;
-    using Rows = RowsOf<T, NS, TT, kScanThreads, kWide>;
-    __shared__ float ds[TT][CB], os[TT][CB];
-    __shared__ float Cs[TT][NS];
-    __shared__ float bias[CB];
-    ScanPlace w;
-    if (!scan_place<PairShape<NS>::CB>(a, blockIdx.x, &w) || w.seg == 0) return;
-    for (int i = threadIdx.x; i < CB; i += kScanThreads)
-        bias[i] = w.c0 + i < w.cend && a.dt_bias && in_range(w.c0 + i, 1, a.C, a.pack.status) ? a.dt_bias[w.c0 + i] : 0.f;
-    const PairLane<NS> lane(a, w);
-    float2 g[2][2];
-    lane.load(a.ds1, a.ds1 && w.seg == w.segs - 1 ? w.n : -1, a.pack.N, a, w, g);
-    const T *dt = static_cast<const T *>(a.dt), *z = static_cast<const T *>(a.z), *dy = static_cast<const T *>(a.dy);
-    typename Tile::V dn[Tile::NV], zn[Tile::NV], on[Tile::NV];
-    typename Rows::V cn[Rows::NU];
-    auto fetch = [&](int t) {
-        Tile::load(dt, a.dts, a, w, t, w.f, dn);
-        Tile::load(dy, a.C, a, w, t, w.f, on);
-        if (z) Tile::load(z, a.zs, a, w, t, w.f, zn);
-        Rows::load(static_cast<const T *>(a.Cm), a.cs, a, w, t, w.f, cn);
-    };
-    __syncthreads();
-    const int tiles = (w.f - w.b + TT - 1) / TT;
-    if (tiles > 0) fetch(w.b + (tiles - 1) * TT);
-    for (int i = tiles - 1; i >= 0; --i) {
-        const int t = w.b + i * TT;
-#pragma unroll
-        for (int k = 0; k < Tile::NV; ++k) {
-            const int row = Tile::row(k), col = Tile::col();
-            if (row >= TT) break;
-#pragma unroll
-            for (int j = 0; j < kEV; ++j) {
-                const bool there = t + row < w.f && w.c0 + col + j < w.cend;
-                float o = as_float(on[k].x[j]);
-                if (z) {
-                    const float zj = as_float(zn[k].x[j]);
-                    o *= zj * sigmoid_of(zj);
-                }
-                ds[row][col + j] = there ? softplus_of(as_float(dn[k].x[j]) + bias[col + j]) : 0.f;
-                os[row][col + j] = there ? o : 0.f;
-            }
-        }
-        Rows::keep(cn, Cs);
-        __syncthreads();
-        if (i > 0) fetch(t - TT);
-#pragma unroll 4
-        for (int j = TT - 1; j >= 0; --j) {
-            const float2 d = *reinterpret_cast<const float2 *>(&ds[j][2 * lane.at]);
-            const float2 o = *reinterpret_cast<const float2 *>(&os[j][2 * lane.at]);
-            const float4 c = *reinterpret_cast<const float4 *>(&Cs[j][4 * lane.q]);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float2 dp_ = both(p ? d.y : d.x), decay[2] = {lane.decay(p, 0, dp_), lane.decay(p, 1, dp_)};
-                const float2 op = both(p ? o.y : o.x);
-                g[p][0] = mul2(decay[0], fma2(make_float2(c.x, c.y), op, g[p][0]));
-                g[p][1] = mul2(decay[1], fma2(make_float2(c.z, c.w), op, g[p][1]));
-            }
-        }
-        __syncthreads();
-    }
-    lane.store(a.rec_g, w.item, a.pack.N + (long long)(a.pack.T / a.seg), a, w, g);
-}
 
 template <typename T, int NS>
 struct BackTiles {
     static constexpr int CB = PairShape<NS>::CB, TT = kMarkTile, kRing = 4;
     float4 us[2][TT][kScanThreads][2];   // e^{dA} h of a walker's two channels, then its dC and dB
     float4 dd[2][TT][CB / 2];            // d, d x of two channels, at unit_at; then sum G B, sum p A / ln 2
+    float4 start[2][kScanThreads];       // of a walker's two channels: the states ahead of the segment
     float os[2][TT][CB];                 // o, then sum C h
     float B[2][TT][NS], C[2][TT][NS];
     float bias[CB], skip[CB];
     alignas(16) T x[kRing][TT * CB], dt[kRing][TT * CB], z[kRing][TT * CB], dy[kRing][TT * CB];
     alignas(16) T rB[kRing][TT * NS], rC[kRing][TT * NS];
-};
-
-// The walk forward, ahead of the walk back and in the place of its us: longer tiles, of several marks.
-template <typename T, int NS>
-struct AheadTiles {
-    static constexpr int CB = PairShape<NS>::CB, TT = NS == 32 ? 32 : (sizeof(T) == 2 ? 2048 : 1024) / CB, kRing = 3;
-    float4 dd[2][TT][CB / 2];
-    float B[2][TT][NS];
-    alignas(16) T x[kRing][TT * CB], dt[kRing][TT * CB];
-    alignas(16) T rB[kRing][TT * NS];
 };
 
 // As in the forward, half of the threads are formers and half are walkers, a tile apart.
@@ -138,11 +55,6 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     using Rows = RowsOf<T, NS, TT, N, kWide>;
     extern __shared__ float4 smem[];
     BackTiles<T, NS> &m = *reinterpret_cast<BackTiles<T, NS> *>(smem);
-
-    using Ahead = AheadTiles<T, NS>;
-    constexpr int TF = Ahead::TT;
-    static_assert(sizeof(Ahead) <= sizeof(m.us) && TF % TT == 0, "in the place of us, whole marks");
-    Ahead &f = *reinterpret_cast<Ahead *>(smem);
 
     ScanPlace w;
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
@@ -157,7 +69,6 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     }
     __syncthreads();
     const int tiles = (w.f - w.b + TT - 1) / TT;
-    const int ahead = (max(tiles - 1, 0) * TT + TF - 1) / TF;   // of the walk forward, which ends at the last mark
     const float ln2 = 0.693147180559945309f;
     const long long sums_extent = items * a.C * (NS + 2);
 
@@ -184,43 +95,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                 dd[unit_at((col + j) / 2)] = make_float4(v.x, dx.x, v.y, dx.y);
             }
         };
-        {
-            using Long = TileOf<T, CB, TF, kEV, N, kWide>;
-            using LongRows = RowsOf<T, NS, TF, N, kWide>;
-            constexpr int RF = Ahead::kRing;
-            FeedOf<Long, T, N, kWide> x(xp, a.xs, a, w, TF), dt(dtp, a.dts, a, w, TF);
-            RowFeedOf<LongRows, T, NS, N, kWide> B(Bp, a.bs, a, w, TF);
-            auto fetch = [&](int i) {
-                if (i < ahead) {
-                    x.next(reinterpret_cast<V *>(f.x[i % RF]), a, w, TF);
-                    dt.next(reinterpret_cast<V *>(f.dt[i % RF]), a, w, TF);
-                    B.next(reinterpret_cast<U *>(f.rB[i % RF]), a, TF);
-                }
-                copies_commit();
-            };
-            auto all = [&](int i) {
-#pragma unroll
-                for (int k = 0; k < Long::NV; ++k) {
-                    const int row = Long::row(k);
-                    if (row >= TF) break;
-                    form(reinterpret_cast<const V *>(f.x[i % RF])[Long::thread() + k * N],
-                         reinterpret_cast<const V *>(f.dt[i % RF])[Long::thread() + k * N], w.b + i * TF + row < w.f, f.dd[i & 1][row]);
-                }
-                LongRows::keep_copied(reinterpret_cast<const U *>(f.rB[i % RF]), f.B[i & 1]);
-            };
-            fetch(0);
-            fetch(1);
-            copies_wait<1>();
-            if (ahead > 0) all(0);
-            __syncthreads();
-            for (int i = 0; i < ahead; ++i) {
-                fetch(i + 2);
-                copies_wait<1>();
-                if (i + 1 < ahead) all(i + 1);
-                __syncthreads();
-            }
-        }
-        // backward: the i-th tile of the walk is the segment's tile tiles - 1 - i
+        // the i-th tile of the walk is the segment's tile tiles - 1 - i
         Feed x(xp, a.xs, a, w, TT), dt(dtp, a.dts, a, w, TT);
         Feed z(static_cast<const T *>(a.z), a.zs, a, w, TT), dy(static_cast<const T *>(a.dy), a.C, a, w, TT);
         RowFeed B(Bp, a.bs, a, w, TT), C(static_cast<const T *>(a.Cm), a.cs, a, w, TT);
@@ -376,39 +251,41 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     const PairLane<NS, N> lane(a, w);
     const int me = (int)threadIdx.x - N;
     const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
-    // Forward: the states ahead of the tiles.
-    float2 h[2][2];
-    if (w.segs == 1) lane.load(a.s0, a.s0 ? w.n : -1, a.pack.N, a, w, h);
-    else lane.load(a.rec_h, w.item, items, a, w, h);
-    __syncthreads();
-    for (int i = 0; i < ahead; ++i) {
-        for (int j0 = 0; j0 < TF; j0 += TT) {
-            const int tile = i * (TF / TT) + j0 / TT;
-            if (tile >= tiles - 1) break;   // (the last tile's end is nobody's start)
-            lane.store(a.marks, mark + tile, marks, a, w, h);
-#pragma unroll
-            for (int j = 0; j < TT; ++j) {
-                const float4 in = f.dd[i & 1][j0 + j][unit_at(lane.at)];
-                const float4 b = *reinterpret_cast<const float4 *>(&f.B[i & 1][j0 + j][4 * lane.q]);
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const float2 d = both(p ? in.z : in.x), dx = both(p ? in.w : in.y);
-                    h[p][0] = fma2(lane.decay(p, 0, d), h[p][0], mul2(dx, make_float2(b.x, b.y)));
-                    h[p][1] = fma2(lane.decay(p, 1, d), h[p][1], mul2(dx, make_float2(b.z, b.w)));
-                }
-            }
-        }
-        __syncthreads();
-    }
-    // Backward.  g holds e^{d A} G of the token behind; h, the states ahead of the tile, is read a tile ahead.
-    float2 g[2][2], dA[2][2] = {};
+    // g holds e^{d A} G of the token behind.  h, the states ahead of the tile, is read a tile ahead; in a
+    // segment behind another one it is what the segment's start leaves of itself, and the mark.
+    const bool behind = w.seg > 0;
+    float2 h[2][2], g[2][2], dA[2][2] = {};
     if (w.seg == w.segs - 1) lane.load(a.ds1, w.n, a.pack.N, a, w, g);
     else lane.load(a.rec_g, w.item, items, a, w, g);
+    if (behind) {
+        lane.load(a.rec_h, w.item, items, a, w, h);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) m.start[p][me] = make_float4(h[p][0].x, h[p][0].y, h[p][1].x, h[p][1].y);
+    }
+    float since[2] = {};   // sums of d from the segment's start to the mark
+    auto read = [&](int tile, float2 (&to)[2][2]) {
+        lane.load(tile >= 0 ? a.marks : nullptr, mark + tile, marks, a, w, to);
+        if (!behind || tile < 0) return;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const long long at = (mark + tile) * a.C + lane.c + p;
+            since[p] = lane.c + p < w.cend && in_range(at, 1, marks * a.C, a.pack.status) ? a.mark_d[at] : 0.f;
+        }
+    };
+    read(tiles - 1, h);
     __syncthreads();
     for (int i = 0; i <= tiles; ++i) {
         if (i < tiles) {
+            if (behind) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float4 s = m.start[p][me];
+                    h[p][0] = fma2(lane.decay(p, 0, both(since[p])), make_float2(s.x, s.y), h[p][0]);
+                    h[p][1] = fma2(lane.decay(p, 1, both(since[p])), make_float2(s.z, s.w), h[p][1]);
+                }
+            }
             float2 next[2][2];
-            lane.load(i + 1 < tiles ? a.marks : nullptr, mark + tiles - 2 - i, marks, a, w, next);
+            read(tiles - 2 - i, next);
             float4 (*us)[2] = &m.us[i & 1][0][me];   // a token is N of them apart
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
@@ -539,15 +416,7 @@ cudaError_t bwd(const ScanArgs &a, cudaStream_t s) {
     constexpr int bytes = (int)sizeof(BackTiles<T, NS>);
     static_assert(kScanThreads / (CB / kEV) * CB * 8 <= sizeof(BackTiles<T, NS>::us), "the last sums fit the states' place");
     const long long blocks = scan_items(a.pack.N, a.pack.T, a.seg) * scan_across<PairShape<NS>::CB>(a);
-    cudaError_t e = cudaSuccess;
-    if (a.seg <= a.pack.T) {
-        k_scan_starts<T, NS, kWide><<<(unsigned)blocks, kScanThreads, 0, s>>>(a);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) e = launch_scan_join(a, false, s);
-        if (e == cudaSuccess) e = launch_scan_join(a, true, s);
-    }
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(k_scan_bwd<T, NS, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(k_scan_bwd<T, NS, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     k_scan_bwd<T, NS, kWide><<<(unsigned)(blocks + (a.pack.status ? 1 : 0)), 2 * kScanThreads, bytes, s>>>(a);
     e = cudaGetLastError();
@@ -568,10 +437,12 @@ cudaError_t bwd_of(const ScanArgs &a, cudaStream_t s) {
 int scan_mark_tile() { return kMarkTile; }
 
 cudaError_t launch_scan_bwd(const ScanArgs &a, cudaStream_t s) {
+    cudaError_t e = launch_scan_marks(a, s);
     if (a.seg <= a.pack.T) {
-        const cudaError_t e = launch_scan_ends(a, s);
-        if (e != cudaSuccess) return e;
+        if (e == cudaSuccess) e = launch_scan_join(a, false, s);
+        if (e == cudaSuccess) e = launch_scan_join(a, true, s);
     }
+    if (e != cudaSuccess) return e;
     if (a.f32) return a.Ns == 8 ? bwd_of<float, 8>(a, s) : a.Ns == 16 ? bwd_of<float, 16>(a, s) : bwd_of<float, 32>(a, s);
     return a.Ns == 8 ? bwd_of<bf16, 8>(a, s) : a.Ns == 16 ? bwd_of<bf16, 16>(a, s) : bwd_of<bf16, 32>(a, s);
 }

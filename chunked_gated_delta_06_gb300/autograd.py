@@ -202,6 +202,15 @@ def rotary(q, k, positions, freq, layout="half", mscale=1.0):
                          False)
 
 
+def _aligned(t):
+    """t, or a copy of it, dense and from 16 bytes on (the gradients that reach a function may be parts of
+    a wider tensor)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _mixer_functions():
     import torch
 
@@ -218,9 +227,9 @@ def _mixer_functions():
         def backward(ctx, dy, dht):
             x, weight, bias, h0, cu_dev = ctx.saved_tensors
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy
-            gr = mixer.short_conv_bwd(x, weight, dy.contiguous(), ctx.cu_host, cu_dev, bias=bias,
-                                      activation=ctx.activation, initial_state=h0,
-                                      d_final_state=None if dht is None else dht.contiguous(), want_dh0=h0 is not None)
+            gr = mixer.short_conv_bwd(x, weight, _aligned(dy), ctx.cu_host, cu_dev, bias=bias,
+                                      activation=ctx.activation, initial_state=h0, d_final_state=_aligned(dht),
+                                      want_dh0=h0 is not None)
             grads = _final("short_conv", [gr[n] for n in ("dx", "dw", "dbias", "dh0")],
                            (x, weight, bias, h0, dy, dht))
             return (*grads, None, None, None, None)
@@ -239,9 +248,8 @@ def _mixer_functions():
             *inputs, cu_dev = ctx.saved_tensors
             x, dt, A_log, B, C, D, z, dt_bias, h0 = inputs
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy
-            gr = mixer.selective_scan_bwd(x, dt, A_log, B, C, dy.contiguous(), ctx.cu_host, cu_dev, D=D, z=z,
-                                          dt_bias=dt_bias, initial_state=h0,
-                                          d_final_state=None if dht is None else dht.contiguous(),
+            gr = mixer.selective_scan_bwd(x, dt, A_log, B, C, _aligned(dy), ctx.cu_host, cu_dev, D=D, z=z,
+                                          dt_bias=dt_bias, initial_state=h0, d_final_state=_aligned(dht),
                                           want_dh0=h0 is not None)
             names = ("dx", "ddt", "dA_log", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
             grads = _final("selective_scan", [gr[n] for n in names], (*inputs, dy, dht))
@@ -260,8 +268,7 @@ def _mixer_functions():
         def backward(ctx, dy, dh):
             h, weight, z, scale, x = ctx.saved_tensors
             dy = torch.zeros(h.shape, dtype=ctx.kind, device=h.device) if dy is None else dy
-            gr = mixer.rms_norm_bwd(h, weight, dy.contiguous(), z=z, dh=None if dh is None else dh.contiguous(),
-                                    scale=scale, x=x, **ctx.args)
+            gr = mixer.rms_norm_bwd(h, weight, _aligned(dy), z=z, dh=_aligned(dh), scale=scale, x=x, **ctx.args)
             grads = _final("rms_norm", [gr[n] for n in ("dx", "dweight", "dz", "dresidual", "dscale")],
                            (h, weight, z, scale, x, dy, dh))
             return (*grads, None, None, None)
@@ -321,8 +328,8 @@ def short_conv(x, weight, bias=None, activation="silu", initial_state=None, outp
     if batched:
         (x,) = _one_batch(x)
     cu_host, cu_dev = _offsets(x.shape[0], x.device, cu_seqlens, cu_seqlens_cpu)
-    y, ht = _mixer(0).apply(_dense_rows(x), _float(weight), _float(bias), initial_state, cu_host, cu_dev, activation,
-                            output_final_state)
+    y, ht = _mixer(0).apply(_dense_rows(x), _float(weight), _float(bias), _aligned(initial_state), cu_host, cu_dev,
+                            activation, output_final_state)
     return (y.unsqueeze(0) if batched else y), ht
 
 
@@ -337,7 +344,8 @@ def selective_scan(x, dt, A_log, B, C, D=None, z=None, dt_bias=None, initial_sta
         x, dt, B, C, z = _one_batch(x, dt, B, C, z)
     cu_host, cu_dev = _offsets(x.shape[0], x.device, cu_seqlens, cu_seqlens_cpu)
     y, ht = _mixer(1).apply(_dense_rows(x), _dense_rows(dt), _float(A_log), _dense_rows(B), _dense_rows(C), _float(D),
-                            _dense_rows(z), _float(dt_bias), initial_state, cu_host, cu_dev, output_final_state)
+                            _dense_rows(z), _float(dt_bias), _aligned(initial_state), cu_host, cu_dev,
+                            output_final_state)
     return (y.unsqueeze(0) if batched else y), ht
 
 
@@ -345,6 +353,6 @@ def rms_norm(x, weight, z=None, residual=None, scale=None, gate="silu", eps=1e-6
     """Differentiable norm of rows with its gate and residual: y = h / rms(h) (offset + weight) act(z), with
     h = residual + scale x returned as well, (y, h), where there is a residual.  x, z, residual: [..., dim];
     weight and scale [dim] of any floating type (computed with in fp32)."""
-    dense = lambda t: None if t is None else t.contiguous()  # noqa: E731
-    y, h = _mixer(2).apply(dense(x), _float(weight), dense(z), dense(residual), _float(scale), gate, eps, offset)
+    y, h = _mixer(2).apply(_aligned(x), _aligned(_float(weight)), _aligned(z), _aligned(residual),
+                           _aligned(_float(scale)), gate, eps, offset)
     return y if residual is None else (y, h)

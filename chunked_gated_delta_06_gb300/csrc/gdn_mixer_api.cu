@@ -18,6 +18,7 @@ using gdn::kAlign;
 using gdn::Span;
 
 constexpr int64_t kGrid = 0x7fffffffLL;
+constexpr int32_t kChannels = 1 << 30;   // the kernels' indices of channels stay in 32 bits
 
 gdn_status check_pack(const gdn_pack *p, gdn::PackArgs *a) {
     if (!p || p->num_seqs < 1 || p->total_tokens < 0 || p->total_tokens > 0x7fffffffLL - 65535)
@@ -75,7 +76,7 @@ gdn::SlotArgs slots_of(const Pool *s) {
 
 // ------------------------------------------------------------------------------ convolution
 gdn_status check_conv(int32_t channels, int32_t width, int32_t activation, int32_t dtype, int64_t x_stride) {
-    if (channels < 1 || x_stride < channels || x_stride > ((int64_t)1 << 31)) return GDN_ERR_INVALID_ARG;
+    if (channels < 1 || channels > kChannels || x_stride < channels || x_stride > ((int64_t)1 << 31)) return GDN_ERR_INVALID_ARG;
     if (activation != GDN_ACT_NONE && activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
     if (!known(dtype)) return GDN_ERR_INVALID_ARG;
     if (width < 2 || width > 4) return GDN_ERR_UNSUPPORTED;
@@ -151,7 +152,7 @@ struct ScanWidth {
 };
 
 gdn_status check_scan(const gdn_scan_shape *s, ScanWidth *w) {
-    if (!s || s->channels < 1 || s->groups < 1 || s->groups > s->channels || !known(s->dtype) ||
+    if (!s || s->channels < 1 || s->channels > kChannels || s->groups < 1 || s->groups > s->channels || !known(s->dtype) ||
         s->segment_tokens < -1)
         return GDN_ERR_INVALID_ARG;
     if (s->channels % s->groups != 0) return GDN_ERR_UNSUPPORTED;
@@ -407,7 +408,7 @@ gdn_status gdn_short_conv_prefill_paged(const gdn_pack *p, int32_t channels, int
 
 size_t gdn_short_conv_workspace_bytes(const gdn_pack *p, int32_t channels, int32_t width) {
     gdn::PackArgs pack;
-    if (check_pack(p, &pack) != GDN_OK || channels < 1 || width < 2 || width > 4) return 0;
+    if (check_pack(p, &pack) != GDN_OK || channels < 1 || channels > kChannels || width < 2 || width > 4) return 0;
     return conv_workspace(pack, channels, width);
 }
 

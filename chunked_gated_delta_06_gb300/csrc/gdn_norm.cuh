@@ -36,12 +36,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int turn) {
     }
 }
 
-// The gate's factor at z, and its slope (1 - sigmoid as e^-z sigmoid, which a sigmoid near 1 has lost).
+// The gate's factor at z, and its slope (1 - sigmoid as e^-z sigmoid, which a sigmoid near 1 has lost; a
+// NaN stays one).
 __device__ __forceinline__ float gate_of(int gate, float z) {
     return sigmoid_of(z) * (gate == GDN_GATE_SIGMOID ? 1.f : z);
 }
 __device__ __forceinline__ float gate_of(int gate, float z, float *slope) {
-    const float e = exp_of(fminf(-z, 80.f)), sig = reciprocal_of(1.f + e), g = sig * (gate == GDN_GATE_SIGMOID ? 1.f : z);
+    const float e = exp_of(z < -80.f ? 80.f : -z), sig = reciprocal_of(1.f + e), g = sig * (gate == GDN_GATE_SIGMOID ? 1.f : z);
     *slope = fmaf(g, e * sig, gate == GDN_GATE_SIGMOID ? 0.f : sig);
     return g;
 }

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(128) k_scan_join(const __grid_constant__ ScanA
     float rate[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        rate[j] = in_range(i + j, 1, per, a.pack.status) ? fmaxf(-1.44269504088896341f * expf(a.A_log[i + j]), -3e38f) : 0.f;
+        rate[j] = in_range(i + j, 1, per, a.pack.status) ? rate_of(a.A_log[i + j]) : 0.f;
     float *rec = kBackward ? a.rec_g : a.rec_h;
     auto read = [&](int seg) { return load_vec<4>(rec, (first + seg) * per + i, items * per, a.pack.status); };
     auto write = [&](int seg, const Vec<float, 4> &v) { store_vec<4>(rec, (first + seg) * per + i, items * per, a.pack.status, v); };
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(256, NS < 32 ? 3 : 1) k_scan_step(const __grid
         for (int j = 0; j < 4; ++j) {
             const long long at = (long long)(c0 + i) * NS + 4 * q + j;
             rate[i][j] = c0 + i < a.C && in_range(at, 1, (long long)a.C * NS, a.pack.status)
-                             ? fmaxf(-1.44269504088896341f * expf(a.A_log[at]), -3e38f)
+                             ? rate_of(a.A_log[at])
                              : 0.f;
         }
     const float bias = mine && a.dt_bias ? a.dt_bias[c] : 0.f, skip = mine && a.D ? a.D[c] : 0.f;

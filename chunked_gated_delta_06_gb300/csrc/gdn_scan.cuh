@@ -265,13 +265,19 @@ struct RowFeedOf {
     }
 };
 
+// A / ln 2, kept finite, so that a token without an input (d = 0) decays nothing; NaN stays NaN.
+__device__ __forceinline__ float rate_of(float A_log) {
+    const float r = -1.44269504088896341f * expf(A_log);
+    return r < -3e38f ? -3e38f : r;
+}
+
 // A thread's part of a walk: channels c .. c + P - 1, states S q .. S q + S - 1 of each.
 template <int NS, int P, int S, int kFirst = 0>   // kFirst: the first thread that walks
 struct ScanLane {
     static constexpr int L = NS / S, H = S / 2;
     using States = float2[P][H];
     int at, q, c;        // its group of P channels in the block, its part of the states, its first channel
-    float2 A[P][H];      // rates / ln 2, <= 0 and finite (a token without an input has d = 0)
+    float2 A[P][H];      // rate_of its A_log
     __device__ ScanLane(const ScanArgs &a, const ScanPlace &w) {
         at = ((int)threadIdx.x - kFirst) / L;
         q = ((int)threadIdx.x - kFirst) % L;
@@ -280,9 +286,7 @@ struct ScanLane {
         for (int i = 0; i < P; ++i) {
             const long long from = (long long)(c + i) * NS + S * q;
             const bool there = c + i < w.cend && in_range(from, S, (long long)a.C * NS, a.pack.status);
-            auto rate = [&](int j) {
-                return there ? fmaxf(-1.44269504088896341f * expf(a.A_log[from + j]), -3e38f) : 0.f;
-            };
+            auto rate = [&](int j) { return there ? rate_of(a.A_log[from + j]) : 0.f; };
 #pragma unroll
             for (int k = 0; k < H; ++k) A[i][k] = make_float2(rate(2 * k), rate(2 * k + 1));
         }

@@ -3,7 +3,8 @@ residual on torch tensors: argument checks and marshalling only, every step of t
 in libgdn's CUDA kernels.
 
 Activations are bf16 or fp32 (all tensors of a call alike); parameters are fp32.  Rows of an input
-[T, ...] may lie apart (a slice of a wider projection): the elements of a row must be dense.
+[T, ...] may lie apart (a slice of a wider projection): the elements of a row must be dense.  Other
+tensors are dense and start on 16 bytes, as a new tensor does and a part of one may not.
 """
 from __future__ import annotations
 

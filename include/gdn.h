@@ -442,6 +442,7 @@ gdn_status gdn_rope(int64_t total_tokens, int32_t num_q_heads, int32_t num_k_hea
 /* ---------------------------------------------------------------------------
  * What stands around the recurrences in a layer: the short causal convolution,
  * the selective state space scan, and norms with their gate and residual.
+ * Up to 2^30 channels.
  * Tensors of these calls are bf16 or fp32 as `dtype` (GDN_DTYPE_*) says; all sums,
  * states of the scan and parameters are fp32.  Outputs and workspaces must
  * overlap neither inputs nor one another (GDN_ERR_INVALID_ARG); tensors start on

@@ -520,3 +520,26 @@ def test_offsets_changed_before_the_backward(monkeypatch):
     dev[1] = 3
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def test_channels_that_indices_do_not_hold_are_refused(lib):
+    most = 1 << 30
+    p = _pack()
+    assert lib.gdn_short_conv_workspace_bytes(ctypes.byref(p), most, 4) > 0
+    assert lib.gdn_short_conv_workspace_bytes(ctypes.byref(p), most + 1, 4) == 0
+    assert lib.gdn_selective_scan_workspace_bytes(ctypes.byref(p), ctypes.byref(_shape(most)), 0) > 0
+    assert lib.gdn_selective_scan_workspace_bytes(ctypes.byref(p), ctypes.byref(_shape(most + 1)), 0) == 0
+    assert lib.gdn_short_conv_step(1, most + 1, 4, 0, BF16, FAKE, most + 1, FAKE, None, 2 * FAKE, 2, 4, 3 * FAKE, None, None) == BAD
+    assert lib.gdn_selective_scan_step(1, ctypes.byref(_shape(most + 1)), *[FAKE] * 5, None, None, None, FAKE, 2, FAKE, FAKE,
+                                       None, None) == BAD
+
+
+def test_parts_of_tensors_become_whole_ones():
+    own = gdn.autograd._aligned
+    wide = torch.arange(64, dtype=torch.float32)
+    assert wide.data_ptr() % 16 == 0 and own(wide) is wide and own(None) is None
+    assert own(wide[4:]).data_ptr() == wide[4:].data_ptr()
+    part = own(wide[1:9])
+    assert part.data_ptr() % 16 == 0 and torch.equal(part, wide[1:9])
+    turned = own(wide.view(8, 8).t())
+    assert turned.is_contiguous() and torch.equal(turned, wide.view(8, 8).t())

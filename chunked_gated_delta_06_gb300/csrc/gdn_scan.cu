@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(256, NS < 32 ? 3 : 1) k_scan_step(const __grid
             sums[i][0] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                h[i].x[j] = fmaf(exp2_of(di * rate[i][j]), h[i].x[j], dxi * B[j]);
+                h[i].x[j] = fmaf(exp2_of(fmaf(di, rate[i][j], kLift)), h[i].x[j], dxi * B[j]);
                 sums[i][0] = fmaf(C[j], h[i].x[j], sums[i][0]);
             }
             if (c0 + i < a.C) store_vec<4>(a.s1, ((long long)slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status, h[i]);

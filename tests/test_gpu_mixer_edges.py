@@ -47,6 +47,49 @@ def test_a_rate_that_is_no_number_shows(seg):
     assert torch.isnan(y[:, 7]).all() and torch.isfinite(y[:, others]).all()
 
 
+@pytest.mark.parametrize("seg", [-1, 64])
+def test_tokens_without_a_step_leave_the_state(seg):
+    a, dy = _scan([1000, 13], 40)
+    a["dt"].fill_(-300.0)   # softplus is 0
+    cu, cu_dev = _cu([1000, 13])
+    h0 = _gen(9)(2, 40, 16, t=F32)
+    y, ht = gdn.selective_scan_fwd(**a, cu_host=cu, cu_dev=cu_dev, initial_state=h0, segment_tokens=seg)
+    assert torch.equal(ht, h0)
+    got = gdn.selective_scan_bwd(**a, dy=dy, cu_host=cu, cu_dev=cu_dev, initial_state=h0, d_final_state=h0, segment_tokens=seg)
+    assert not got["dB"].any() and not got["ddt"].any() and not got["dA_log"].any()
+    pool = torch.cat([torch.zeros_like(h0[:1]), h0])
+    idx = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+    one = {k: v[:2] if k in ("x", "dt", "B", "C", "z") else v for k, v in a.items()}
+    for _ in range(3):
+        gdn.selective_scan_step(**one, state_pool=pool, state_indices=idx)
+    assert torch.equal(pool[1:], h0)
+
+
+def test_a_long_memory_does_not_drift():
+    # steps of 0.001 .. 0.01 and rates near 1: after 2000 tokens a state keeps a part of its start, and what its
+    # decays are off by on average shows 2000 times
+    a, _ = _scan([2000], 64, 8, t=F32)
+    a["A_log"] *= 0.2
+    a["dt"].zero_()
+    a["x"].zero_()
+    step = torch.linspace(0.001, 0.01, 64, device="cuda", dtype=torch.float64)
+    a["dt_bias"] = torch.log(torch.expm1(step)).float()
+    h0 = 1 + _gen(2)(1, 64, 8, t=F32).abs()
+    cu, cu_dev = _cu([2000])
+    _, ht = gdn.selective_scan_fwd(**a, cu_host=cu, cu_dev=cu_dev, initial_state=h0, segment_tokens=-1)
+    d = torch.nn.functional.softplus(a["dt_bias"].double(), threshold=40)
+    total = 2000 * d[:, None] * torch.exp(a["A_log"].double())
+    want = h0.double() * torch.exp(-total)
+    off = ht[0].double() / want[0] - 1
+    # Every token of a state has the same decay here, so that its errors are no random ones: the exponential's
+    # 2^-22 and what it is lifted by, below 2^-25, and the state's own rounding, 2^-24, are below 2^-21.4 a token, all
+    # 2000 times; d is off by 2^-19 (as in the definition's bounds), A and its products by 2^-22, of the whole decay.
+    assert (off.abs() <= 2000 * 2.0 ** -21.4 + total * (2.0 ** -19 + 2.0 ** -22)).all()
+    # Of 512 states with errors of 3e-8 a token the mean is off by 3e-8 / 512^0.5 = 1.3e-9: what is left is the bias,
+    # which is 1.6e-8 for these steps without the lift and within 2e-9 of nothing with it.
+    assert abs(float(off.mean())) <= 2000 * (2e-9 + 4 * 1.3e-9)
+
+
 @pytest.mark.parametrize("gate", ["silu", "sigmoid"])
 def test_a_gate_that_is_no_number_shows(gate):
     rn = _gen()

@@ -347,21 +347,28 @@ __global__ void __launch_bounds__(128) k_scan_join(const __grid_constant__ ScanA
     if (!kBackward) write(0, start);
 }
 
-// One token for each of `rows` rows, one after another (the rates are formed once).  A thread has four
-// states of L = NS / 4 channels in turn, so that its L lanes form d, the gate and the output of one
-// channel each.  Bound by HBM, the states read and written once.
+// One token for each of `rows` rows, one after another (the rates are formed once, the next row is read while
+// this one is computed).  A thread has four states of K channels in turn, so that of its L lanes the first K
+// form d, the gate and the output of one channel each.  Bound by HBM, the states read and written once.
+template <int NS>
+struct StepShape {
+    static constexpr int L = NS / 4, K = L < 4 ? L : 4, kStart = 256 / L, CB = kStart * K;
+    static constexpr int kBlocks = NS == 8 ? 3 : 2;   // of an SM
+};
+
 template <typename T, int NS, bool kWide>
-__global__ void __launch_bounds__(256, NS < 32 ? 3 : 1) k_scan_step(const __grid_constant__ ScanArgs a, int across, int rows) {
-    constexpr int L = NS / 4, kStart = 256 / L;   // groups of L lanes, L channels each
+__global__ void __launch_bounds__(256, StepShape<NS>::kBlocks) k_scan_step(const __grid_constant__ ScanArgs a, int across, int rows) {
+    using Shape = StepShape<NS>;
+    constexpr int L = Shape::L, K = Shape::K, kStart = Shape::kStart;
     const int q = threadIdx.x % L, lane = threadIdx.x % 32;
-    const int c0 = ((int)(blockIdx.x % across) * kStart + (int)threadIdx.x / L) * L, c = c0 + q;   // c: the lane's own
+    const int c0 = ((int)(blockIdx.x % across) * kStart + (int)threadIdx.x / L) * K, c = c0 + q;   // c: the lane's own
     const int b0 = (int)(blockIdx.x / across) * rows, b1 = min(b0 + rows, a.pack.T);
     const int per_group = a.C / a.G;
-    const bool mine = c < a.C;
+    const bool mine = q < K && c < a.C;
     const long long extent = (long long)a.pack.T * a.C, states = (long long)a.slots.num_slots * a.C * NS;
-    float rate[L][4];
+    float rate[K][4];
 #pragma unroll
-    for (int i = 0; i < L; ++i)
+    for (int i = 0; i < K; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const long long at = (long long)(c0 + i) * NS + 4 * q + j;
@@ -386,42 +393,57 @@ __global__ void __launch_bounds__(256, NS < 32 ? 3 : 1) k_scan_step(const __grid
             for (int j = 0; j < 4; ++j) out[j] = as_float(load_vec<1>(static_cast<const T *>(p), at + j, n, a.pack.status).x[0]);
         }
     };
-    const bool one_group = c0 / per_group == min(c0 + L - 1, a.C - 1) / per_group;
+    const bool one_group = c0 / per_group == min(c0 + K - 1, a.C - 1) / per_group;
+    struct Row {
+        int slot;
+        Vec<float, 4> h[K];
+        float x, dt, z, B[4], C[4];
+    };
+    auto read = [&](int b, Row &r) {
+        r.slot = slot_of(a.slots, b);
+        if (r.slot < 0) return;
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (c0 + i < a.C) r.h[i] = load_vec<4>(a.s1, ((long long)r.slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status);
+        r.x = own(a.x, a.xs, b);
+        r.dt = own(a.dt, a.dts, b);
+        r.z = own(a.z, a.zs, b);
+        shared(a.B, a.bs, b, 0, r.B);
+        shared(a.Cm, a.cs, b, 0, r.C);
+    };
+    Row r, next;
+    read(b0, r);
     for (int b = b0; b < b1; ++b) {
-        const int slot = slot_of(a.slots, b);
-        if (slot < 0) {   // (the same for all threads of the block)
+        // (no two active rows have one slot: what the next row reads this one does not write)
+        if (b + 1 < b1) read(b + 1, next);
+        if (r.slot < 0) {   // (the same for all threads of the block)
             if (threadIdx.x == 0 && a.slots.status && a.slots.idx[b] >= a.slots.num_slots) *a.slots.status = 1;
             if (mine) store_vec<1>(y, (long long)b * a.C + c, extent, a.pack.status, Vec<T, 1>{{as_type<T>(0.f)}});
+            r = next;
             continue;
         }
-        Vec<float, 4> h[L];
+        const float d = softplus_of(r.dt + bias), dx = d * r.x;
+        float sums[K][1];
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-            if (c0 + i < a.C) h[i] = load_vec<4>(a.s1, ((long long)slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status);
-        const float x = own(a.x, a.xs, b), z = own(a.z, a.zs, b);
-        const float d = softplus_of(own(a.dt, a.dts, b) + bias), dx = d * x;
-        float B[4], C[4], sums[L][1];
-        shared(a.B, a.bs, b, 0, B);
-        shared(a.Cm, a.cs, b, 0, C);
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
+        for (int i = 0; i < K; ++i) {
             const float di = __shfl_sync(0xffffffffu, d, lane - q + i), dxi = __shfl_sync(0xffffffffu, dx, lane - q + i);
             if (i > 0 && !one_group) {
-                shared(a.B, a.bs, b, i, B);
-                shared(a.Cm, a.cs, b, i, C);
+                shared(a.B, a.bs, b, i, r.B);
+                shared(a.Cm, a.cs, b, i, r.C);
             }
             sums[i][0] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                h[i].x[j] = fmaf(exp2_of(fmaf(di, rate[i][j], kLift)), h[i].x[j], dxi * B[j]);
-                sums[i][0] = fmaf(C[j], h[i].x[j], sums[i][0]);
+                r.h[i].x[j] = fmaf(exp2_of(fmaf(di, rate[i][j], kLift)), r.h[i].x[j], dxi * r.B[j]);
+                sums[i][0] = fmaf(r.C[j], r.h[i].x[j], sums[i][0]);
             }
-            if (c0 + i < a.C) store_vec<4>(a.s1, ((long long)slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status, h[i]);
+            if (c0 + i < a.C) store_vec<4>(a.s1, ((long long)r.slot * a.C + c0 + i) * NS + 4 * q, states, a.pack.status, r.h[i]);
         }
-        lane_sums<L, L, 1>(sums, q);
-        float out = fmaf(skip, x, sums[0][0]);
-        if (a.z) out *= z * sigmoid_of(z);
+        lane_sums<L, K, 1>(sums, q);
+        float out = fmaf(skip, r.x, sums[0][0]);
+        if (a.z) out *= r.z * sigmoid_of(r.z);
         if (mine) store_vec<1>(y, (long long)b * a.C + c, extent, a.pack.status, Vec<T, 1>{{as_type<T>(out)}});
+        r = next;
     }
 }
 
@@ -444,9 +466,12 @@ cudaError_t scan(const ScanArgs &a, cudaStream_t s) {
 
 template <typename T, int NS>
 cudaError_t step(const ScanArgs &a, int batch, cudaStream_t s) {
-    const int across = (a.C + 255) / 256;
-    // rows of a block: up to 8, as long as every SM has eight blocks
-    const int rows = (int)std::max(1LL, std::min(8LL, (long long)batch * across / (8 * 152)));
+    using Shape = StepShape<NS>;
+    const int across = (a.C + Shape::CB - 1) / Shape::CB;
+    // Rows of a block: up to 8, as long as every SM has the blocks that it runs at once.  (256 rows x 4096 x 16,
+    // cold: 3 rows 38.0 us, 8 36.0, 13 41.1, the last in waves that end badly; one row after another, not
+    // read ahead, 42.1.)
+    const int rows = (int)std::max(1LL, std::min(8LL, (long long)batch * across / (NS == 8 ? 4 * 152 : 2 * 152)));
     const unsigned grid = (unsigned)((batch + rows - 1) / rows * (long long)across);
     auto fits = [](const void *p, long long stride) {
         return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && stride % 4 == 0;

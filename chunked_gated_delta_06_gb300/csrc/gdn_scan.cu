@@ -18,10 +18,14 @@ enum WalkFor { kOutputs, kEnds, kMarks };
 // the inputs of the one after next are on their way.
 template <int NS, WalkFor kFor>
 struct WalkShape {
-    static constexpr int kMost = kFor == kMarks ? 8 : 16;
-    static constexpr int S = NS < kMost ? NS : kMost, L = NS / S;   // states of a walker, walkers of a channel
+    static constexpr int kMost = kFor == kMarks ? 8 : 16;           // states of a walker
+    // its channels, and states of each: two channels read a token's B and C once (4 x 4096 tokens of 4096
+    // channels of 8 states 279 us, one channel 289), but of 32 states for outputs would make four sum up
+    // (2048 channels 351 us, one channel 338)
+    static constexpr int P = NS == 32 && kFor == kOutputs ? 1 : 2, S = (NS < kMost ? NS : kMost) / P;
+    static constexpr int L = NS / S;                                // walkers of a channel
     static constexpr int kHalf = 128;                         // threads of either kind
-    static constexpr int CB = kHalf / L;                      // channels of a block
+    static constexpr int CB = P * kHalf / L;                  // channels of a block
     static constexpr int TT = 16;                             // tokens of a tile
     static constexpr int kRing = 4;                           // tiles of inputs: finished, walked, formed, on their way
 };
@@ -50,7 +54,7 @@ template <typename T, int NS, bool kWide, WalkFor kFor>
 __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
     k_scan_fwd(const __grid_constant__ ScanArgs a) {
     using Shape = WalkShape<NS, kFor>;
-    constexpr int CB = Shape::CB, L = Shape::L, S = Shape::S, TT = Shape::TT, R = Shape::kRing, EV = 8;
+    constexpr int CB = Shape::CB, L = Shape::L, P = Shape::P, S = Shape::S, TT = Shape::TT, R = Shape::kRing, EV = 8;
     constexpr int kHalf = Shape::kHalf;
     using Tile = TileOf<T, CB, TT, EV, kHalf, kWide>;
     using Rows = RowsOf<T, NS, TT, kHalf, kWide>;
@@ -176,8 +180,8 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
         return;
     }
 
-    using Lane = ScanLane<NS, 1, S, kHalf>;
-    constexpr int H = S / 2;
+    using Lane = ScanLane<NS, P, S, kHalf>;
+    constexpr int H = S / 2, BT = L < 4 ? L : 4;
     const Lane lane(a, w);
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
     const int last = w.item - w.seg + w.segs - 1;   // the item of the sequence's last segment
@@ -191,31 +195,42 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
     } else {
         lane.load(a.rec_h, w.item, items, a, w, h);
     }
-    float total = 0.f;
-    const int place = channel_at(lane.at);
+    float2 total = both(0.f);   // sums of d, of each channel
+    const int place = channel_at(P * lane.at);
     const long long marks = a.pack.N + (long long)(a.pack.T / kMarkTile), mark = first_mark(a, w);
+    auto keep_total = [&](float *to, long long row, long long rows, float2 sum) {   // [rows, C]
+        const long long at = row * a.C + lane.c;
+        if (lane.q) return;
+        if (lane.c < w.cend && in_range(at, 1, rows * a.C, a.pack.status)) to[at] = sum.x;
+        if (P == 2 && lane.c + 1 < w.cend && in_range(at + 1, 1, rows * a.C, a.pack.status)) to[at + 1] = sum.y;
+    };
     __syncthreads();
     // kBoth: with the gradient at the segment's start, from nothing behind it
     auto walk = [&](auto both_) {
         constexpr bool kBoth = decltype(both_)::value, kC = kFor == kOutputs || kBoth;
-        typename Lane::States P, g;
+        typename Lane::States gone, g;   // the product of the decays, and the gradient
         if constexpr (kBoth) {
 #pragma unroll
-            for (int k = 0; k < H; ++k) {
-                P[0][k] = both(1.f);
-                g[0][k] = both(0.f);
-            }
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int k = 0; k < H; ++k) {
+                    gone[p][k] = both(1.f);
+                    g[p][k] = both(0.f);
+                }
         }
         for (int i = 0; i <= tiles; ++i) {
             if (i < tiles) {
-                const float *d = m.d[i & 1][0] + place, *dx = m.dx[i & 1][0] + place, *o = m.y[i & 1][0] + place;
+                auto row = [&](const float *rows, int t) {   // of the walker's channels
+                    const float *at = rows + t * CB + place;
+                    return P == 2 ? *reinterpret_cast<const float2 *>(at) : make_float2(*at, 0.f);
+                };
+                const float *ds = m.d[i & 1][0], *dxs = m.dx[i & 1][0], *os = m.y[i & 1][0];
                 const float4 *B = reinterpret_cast<const float4 *>(m.B[i & 1][0] + S * lane.q);
                 const float4 *C = reinterpret_cast<const float4 *>(m.C[i & 1][0] + S * lane.q);
-                float *y = m.y[i & 1][0] + lane.at;
                 // All of the tile's tokens: those past the segment change nothing.  The decays, B and C are
                 // formed and read one token ahead of the states that take them.
-                float2 in = make_float2(d[0], dx[0]), dec[H], b[H], c[H];
-                float oc = kBoth ? o[0] : 0.f;
+                float2 d = row(ds, 0), dx = row(dxs, 0), o = both(0.f), dec[P][H], b[H], c[H];
+                if (kBoth) o = row(os, 0);
                 auto ahead = [&](int t) {
 #pragma unroll
                     for (int k = 0; k < H; k += 2) {
@@ -229,47 +244,61 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
                         }
                     }
                 };
+                auto decays = [&] {
 #pragma unroll
-                for (int k = 0; k < H; ++k) dec[k] = lane.decay(0, k, both(in.x));
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int k = 0; k < H; ++k) dec[p][k] = lane.decay(p, k, both(p ? d.y : d.x));
+                };
+                decays();
                 ahead(0);
-                float2 next = make_float2(d[CB], dx[CB]);
-                float sum = 0.f;
-#pragma unroll 8
-                for (int t = 0; t < TT; ++t) {
-                    if (kFor == kMarks && t % kMarkTile == 0 && w.b + i * TT + t < w.f) {
-                        const long long to = mark + (i * TT + t) / kMarkTile;
+                float2 next_d = row(ds, 1), next_dx = row(dxs, 1), sum = both(0.f);
+#pragma unroll 8 / BT
+                for (int t0 = 0; t0 < TT; t0 += BT) {
+                    if (kFor == kMarks && t0 % kMarkTile == 0 && w.b + i * TT + t0 < w.f) {
+                        const long long to = mark + (i * TT + t0) / kMarkTile;
                         lane.store(a.marks, to, marks, a, w, h);
-                        if (kBoth && lane.q == 0 && lane.c < w.cend && in_range(to * a.C + lane.c, 1, marks * a.C, a.pack.status))
-                            a.mark_d[to * a.C + lane.c] = total + sum;
+                        if (kBoth) keep_total(a.mark_d, to, marks, add2(total, sum));
                     }
-                    float2 y2[2] = {both(0.f), both(0.f)};
-                    const float2 input = both(in.y);
+                    float part[BT][P];
 #pragma unroll
-                    for (int k = 0; k < H; ++k) {
-                        h[0][k] = fma2(dec[k], h[0][k], mul2(input, b[k]));
-                        if (kFor == kOutputs) y2[k & 1] = fma2(c[k], h[0][k], y2[k & 1]);
-                        if constexpr (kBoth) {
-                            P[0][k] = mul2(P[0][k], dec[k]);
-                            g[0][k] = fma2(P[0][k], mul2(both(oc), c[k]), g[0][k]);
+                    for (int j = 0; j < BT; ++j) {
+                        const int t = t0 + j;
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            float2 y = both(0.f);
+                            const float2 input = both(p ? dx.y : dx.x);
+#pragma unroll
+                            for (int k = 0; k < H; ++k) {
+                                h[p][k] = fma2(dec[p][k], h[p][k], mul2(input, b[k]));
+                                if (kFor == kOutputs) y = k ? fma2(c[k], h[p][k], y) : mul2(c[k], h[p][k]);
+                                if constexpr (kBoth) {
+                                    gone[p][k] = mul2(gone[p][k], dec[p][k]);
+                                    g[p][k] = fma2(gone[p][k], mul2(both(p ? o.y : o.x), c[k]), g[p][k]);
+                                }
+                            }
+                            part[j][p] = y.x + y.y;
+                        }
+                        if (kFor != kOutputs) sum = add2(sum, d);
+                        const int u = min(t + 1, TT - 1), v = min(t + 2, TT - 1);
+                        d = next_d;
+                        dx = next_dx;
+                        if (kBoth) o = row(os, u);
+                        next_d = row(ds, v);
+                        next_dx = row(dxs, v);
+                        ahead(u);
+                        decays();
+                    }
+                    if (kFor == kOutputs) {
+                        lane_sums<L, BT, P>(part, lane.q);
+                        if (lane.q < BT) {
+                            float *y = &m.y[i & 1][t0 + lane.q][P * lane.at];
+                            if constexpr (P == 2) *reinterpret_cast<float2 *>(y) = make_float2(part[0][0], part[0][1]);
+                            else *y = part[0][0];
                         }
                     }
-                    if (kFor != kOutputs) sum += in.x;
-                    const int u = min(t + 1, TT - 1);
-                    in = next;
-                    if (kBoth) oc = o[u * CB];
-                    next = make_float2(d[min(t + 2, TT - 1) * CB], dx[min(t + 2, TT - 1) * CB]);
-                    ahead(u);
-#pragma unroll
-                    for (int k = 0; k < H; ++k) dec[k] = lane.decay(0, k, both(in.x));
-                    if (kFor == kOutputs) {
-                        const float2 y1 = add2(y2[0], y2[1]);
-                        float out = y1.x + y1.y;
-#pragma unroll
-                        for (int o = L / 2; o; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
-                        if (L == 1 || lane.q == 0) y[t * CB] = out;
-                    }
                 }
-                total += sum;
+                total = add2(total, sum);
             }
             __syncthreads();
         }
@@ -278,7 +307,9 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
                 typename Lane::States end;
                 lane.load(a.ds1, w.n, a.pack.N, a, w, end);
 #pragma unroll
-                for (int k = 0; k < H; ++k) g[0][k] = fma2(P[0][k], end[0][k], g[0][k]);
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int k = 0; k < H; ++k) g[p][k] = fma2(gone[p][k], end[p][k], g[p][k]);
             }
             lane.store(a.rec_g, w.item, items, a, w, g);
         }
@@ -292,8 +323,7 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
     if (kFor != kOutputs) {
         if (w.seg == w.segs - 1) return;
         lane.store(a.rec_h, w.item, items, a, w, h);
-        const long long at = (long long)w.item * a.C + lane.c;
-        if (lane.q == 0 && lane.c < w.cend && in_range(at, 1, items * a.C, a.pack.status)) a.rec_d[at] = total;
+        keep_total(a.rec_d, w.item, items, total);
         return;
     }
     if (w.seg != w.segs - 1) return;

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
                 decays();
                 ahead(0);
                 float2 next_d = row(ds, 1), next_dx = row(dxs, 1), sum = both(0.f);
-#pragma unroll 8 / BT
+#pragma unroll
                 for (int t0 = 0; t0 < TT; t0 += BT) {
                     if (kFor == kMarks && t0 % kMarkTile == 0 && w.b + i * TT + t0 < w.f) {
                         const long long to = mark + (i * TT + t0) / kMarkTile;

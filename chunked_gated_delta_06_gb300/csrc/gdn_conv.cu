@@ -157,11 +157,27 @@ struct Stream {
     }
 };
 
+// A thread's channels and tile: a block's are of one tile, or (kFlat, few channels) threads go through a
+// tile's channels, then the next tile's.
+struct Place {
+    int c, tile;
+};
+template <int V, bool kFlat>
+__device__ __forceinline__ Place place_of(const ConvArgs &a, long long block) {
+    if (kFlat) {
+        const long long i = block * kThreads + threadIdx.x;
+        const int per = (a.C + V - 1) / V;
+        return {(int)(i % per) * V, (int)(i / per)};
+    }
+    const int across = (a.C + kThreads * V - 1) / (kThreads * V);
+    return {((int)(block % across) * kThreads + (int)threadIdx.x) * V, (int)(block / across)};
+}
+
 // A thread walks the tokens of a tile for V channels with the last W - 1 inputs in registers.  Bound by
 // HBM.  The blocks behind those of the tiles write the states behind the sequences (over a pool they
 // are a launch of their own: the tiles still read the slots).
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ ConvArgs a, int across, long long blocks) {
+template <typename T, int V, int W, bool kFlat>
+__global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ ConvArgs a, long long blocks) {
     using In = Stream<T, V, 1>;
     __shared__ __align__(16) T ring[In::kStages * In::kGroup * kThreads * V];
     const long long block = blockIdx.x;
@@ -172,9 +188,10 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
         else final_state<T, W>(a, (int)(i / per), (int)(i % per) * kThreads + (int)threadIdx.x);
         return;
     }
-    const int c = ((int)(block % across) * kThreads + (int)threadIdx.x) * V;
-    if (c >= a.C) return;
-    const int t0 = (int)(block / across) * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
+    const Place at = place_of<V, kFlat>(a, block);
+    const int c = at.c;
+    if (c >= a.C || (long long)at.tile * a.tile >= a.pack.T) return;
+    const int t0 = at.tile * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
     const long long extent = (long long)a.pack.T * a.C, x_extent = (a.pack.T - 1) * a.x_stride + a.C;
     const T *x0 = static_cast<const T *>(a.x);
     In in{reinterpret_cast<Vec<T, V> *>(ring) + threadIdx.x, {x0 + t0 * a.x_stride + c}, {a.x_stride}, t1 - t0, 0};
@@ -221,8 +238,8 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
 // before, dx of token t - (W - 1) (where that lies ahead of the sequence, of its state's entry); behind
 // the last token of a sequence come W - 1 more with d = 0.  Sums for dw and dbias are of the tile's own
 // tokens; k_fold adds the tiles.
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ ConvArgs a, int across, long long blocks) {
+template <typename T, int V, int W, bool kFlat>
+__global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ ConvArgs a, long long blocks) {
     using In = Stream<T, V, 2>;
     extern __shared__ __align__(16) unsigned char ring[];
     const long long block = blockIdx.x;
@@ -242,9 +259,9 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
             static_cast<T *>(a.ds0)[at + k] = a.ds1 ? static_cast<const T *>(a.ds1)[at + k] : as_type<T>(0.f);
         return;
     }
-    const int c = ((int)(block % across) * kThreads + (int)threadIdx.x) * V;
-    if (c >= a.C) return;
-    const int tile = (int)(block / across);
+    const Place place = place_of<V, kFlat>(a, block);
+    const int c = place.c, tile = place.tile;
+    if (c >= a.C || (long long)tile * a.tile >= a.pack.T) return;
     const int t0 = tile * a.tile, t1 = (int)min((long long)t0 + a.tile, (long long)a.pack.T);
     const int reach = (int)min((long long)t1 + W - 1, (long long)a.pack.T);
     const long long extent = (long long)a.pack.T * a.C, x_extent = (a.pack.T - 1) * a.x_stride + a.C;
@@ -450,32 +467,45 @@ __global__ void __launch_bounds__(32 * kFoldGroups) k_fold(const __grid_constant
 
 bool fits(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-// Tokens of a tile: long ones read fewer inputs twice (W - 1 of them a tile), short ones spread a
-// small call over the SMs.
-int tile_of(long long T, long long across, int most) {
-    int tile = most;
-    while (tile > 8 && (T + tile - 1) / tile * across < 8 * 152) tile /= 2;
-    return tile;
-}
+// How threads are laid out over `per` threads of a tile.  Blocks of one tile each leave some idle; where that
+// is more than a fifth the threads of several tiles share a block (17 channels, gradient of 2M tokens:
+// 326 us, flat 148; 8191 channels of 4096 tokens 94 and 119, as a tile's numbers are no longer a block's).
+struct Layout {
+    long long per;
+    bool flat;
+    explicit Layout(long long threads) : per(threads) {
+        const long long whole = (per + kThreads - 1) / kThreads * kThreads;
+        flat = 4 * whole > 5 * per;
+        if (!flat) per = whole;
+    }
+    long long blocks(long long T, int tile) const { return ((T + tile - 1) / tile * per + kThreads - 1) / kThreads; }
+    // Tokens of a tile: long ones read fewer inputs twice (W - 1 of them a tile), short ones spread a
+    // small call over the SMs.
+    int tile(long long T, int most) const {
+        int tile = most;
+        while (tile > 8 && blocks(T, tile) < 8 * 152) tile /= 2;
+        return tile;
+    }
+};
 
 template <typename T, int W>
 cudaError_t conv_fwd(ConvArgs &a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T), kBytes = 16;
     const bool wide = a.C % V == 0 && a.x_stride % V == 0 && fits(a.x, kBytes) && fits(a.y, kBytes);
-    const int vec = wide ? V : 1;
-    const int across = (a.C + kThreads * vec - 1) / (kThreads * vec);
-    a.tile = tile_of(a.pack.T, across, 64);
-    const long long blocks = ((long long)a.pack.T + a.tile - 1) / a.tile * across;
+    const Layout layout(wide ? a.C / V : a.C);
+    a.tile = layout.tile(a.pack.T, 64);
+    const long long blocks = layout.blocks(a.pack.T, a.tile);
     const long long ends = a.s1 ? (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads) : 0;
     const bool pool = a.slots.idx != nullptr, check = a.pack.status != nullptr;
     // (the check's block is the one behind the blocks of all states)
     auto launch = [&](long long first, long long grid) {
         if (grid == 0) return;
-        if (wide) k_conv_fwd<T, V, W><<<(unsigned)grid, kThreads, 0, s>>>(a, across, first);
-        else k_conv_fwd<T, 1, W><<<(unsigned)grid, kThreads, 0, s>>>(a, across, first);
+        auto with = [&](auto kernel) { kernel<<<(unsigned)grid, kThreads, 0, s>>>(a, first); };
+        if (wide) layout.flat ? with(k_conv_fwd<T, V, W, true>) : with(k_conv_fwd<T, V, W, false>);
+        else layout.flat ? with(k_conv_fwd<T, 1, W, true>) : with(k_conv_fwd<T, 1, W, false>);
     };
-    const long long per = (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads);
-    const long long behind = check ? per + 1 : ends;
+    const long long states = (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads);
+    const long long behind = check ? states + 1 : ends;
     if (pool) {
         launch(blocks, blocks);
         launch(0, behind);
@@ -491,20 +521,20 @@ cudaError_t conv_bwd(ConvArgs &a, cudaStream_t s) {
     constexpr int V = 4;
     const bool wide = a.C % V == 0 && a.x_stride % V == 0 && fits(a.x, V * sizeof(T)) && fits(a.dy, V * sizeof(T)) &&
                       fits(a.dx, V * sizeof(T));
-    const int vec = wide ? V : 1;
-    const int across = (a.C + kThreads * vec - 1) / (kThreads * vec);
-    const long long blocks = (long long)a.tiles * across;
+    const Layout layout(wide ? a.C / V : a.C);
+    const long long blocks = layout.blocks(a.pack.T, a.tile);
     const long long grid = blocks + (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads) + (a.pack.status ? 1 : 0);
     constexpr int kRing = Stream<T, 1, 2>::kStages * Stream<T, 1, 2>::kGroup * 2 * kThreads * (int)sizeof(T);   // a channel
     static_assert(kRing * V <= 64 * 1024, "three blocks an SM");
-    if (wide) {
-        const cudaError_t e = cudaFuncSetAttribute(k_conv_bwd<T, V, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing * V);
+    auto with = [&](auto kernel, int bytes) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
-        k_conv_bwd<T, V, W><<<(unsigned)grid, kThreads, kRing * V, s>>>(a, across, blocks);
-    } else {
-        k_conv_bwd<T, 1, W><<<(unsigned)grid, kThreads, kRing, s>>>(a, across, blocks);
-    }
-    const cudaError_t e = cudaGetLastError();
+        kernel<<<(unsigned)grid, kThreads, bytes, s>>>(a, blocks);
+        return cudaGetLastError();
+    };
+    cudaError_t e;
+    if (wide) e = layout.flat ? with(k_conv_bwd<T, V, W, true>, kRing * V) : with(k_conv_bwd<T, V, W, false>, kRing * V);
+    else e = layout.flat ? with(k_conv_bwd<T, 1, W, true>, kRing) : with(k_conv_bwd<T, 1, W, false>, kRing);
     if (e != cudaSuccess) return e;
     FoldArgs f{a.part, a.tiles, (long long)a.C * (W + 1), W + 1, W, a.dw, a.dbias};
     return launch_fold(f, s);

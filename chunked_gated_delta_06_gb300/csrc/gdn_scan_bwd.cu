@@ -67,6 +67,10 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
     if (!scan_place<CB>(a, blockIdx.x, &w)) {
         if (a.pack.status && w.item == items) check_offsets(a.pack);
+        // (an idle item's sums)
+        const long long from = ((long long)w.item * a.C + w.c0) * (NS + 2), n = min(CB, w.cend - w.c0) * (NS + 2);
+        for (int i = threadIdx.x; i < n; i += 2 * N)
+            if (w.item < items && in_range(from + i, 1, items * a.C * (NS + 2), a.pack.status)) a.part_c[from + i] = 0.f;
         return;
     }
     for (int i = threadIdx.x; i < CB; i += 2 * N) {
@@ -397,20 +401,23 @@ __global__ void __launch_bounds__(256) k_scan_bc(const __grid_constant__ ScanArg
                  Vec<T, 4>{{as_type<T>(s.x), as_type<T>(s.y), as_type<T>(s.z), as_type<T>(s.w)}});
 }
 
-// dA_log, dD and ddt_bias: the segments' sums in their order (idle items have none).
-__global__ void __launch_bounds__(256) k_scan_params(const __grid_constant__ ScanArgs a) {
-    const int per = a.Ns + 2;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, n = (long long)a.C * per;
-    if (i >= n) return;
+// dA_log, dD and ddt_bias: the items' sums, 32 columns a block, and 32 groups that take every 32nd item in
+// order; then the groups in order.
+constexpr int kSumGroups = 32;
+__global__ void __launch_bounds__(32 * kSumGroups) k_scan_params(const __grid_constant__ ScanArgs a) {
+    __shared__ float sums[kSumGroups][33];
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 5, per = a.Ns + 2;
+    const long long i = (long long)blockIdx.x * 32 + lane, n = (long long)a.C * per;
     const long long items = a.pack.N + (long long)(a.pack.T / a.seg);
     float s = 0.f;
-    for (int q = 0; q < a.pack.N; ++q) {
-        const int b = offset_of(a.pack, q), e = max(b, offset_of(a.pack, q + 1));
-        const int segs = max(1, (int)(((long long)e - b + a.seg - 1) / a.seg)), first = first_item(a, q);
 #pragma unroll 4
-        for (int k = 0; k < segs; ++k)
-            if (in_range((first + k) * n + i, 1, items * n, a.pack.status)) s += a.part_c[(first + k) * n + i];
-    }
+    for (long long k = group; k < items; k += kSumGroups)
+        if (i < n && in_range(k * n + i, 1, items * n, a.pack.status)) s += a.part_c[k * n + i];
+    sums[group][lane] = s;
+    __syncthreads();
+    if (group || i >= n) return;
+#pragma unroll
+    for (int g = 1; g < kSumGroups; ++g) s += sums[g][lane];
     const int c = (int)(i / per), k = (int)(i % per);
     if (k < a.Ns) a.dA_log[(long long)c * a.Ns + k] = s;
     else if (k == a.Ns && a.dD) a.dD[c] = s;
@@ -430,7 +437,7 @@ cudaError_t bwd(const ScanArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const long long units = (long long)a.pack.T * a.G * 2 * NS / 4;
     if (units > 0) k_scan_bc<T, NS><<<(unsigned)((units + 255) / 256), 256, 0, s>>>(a, (a.C / a.G + CB - 1) / CB);
-    k_scan_params<<<(unsigned)(((long long)a.C * (NS + 2) + 255) / 256), 256, 0, s>>>(a);
+    k_scan_params<<<(unsigned)(((long long)a.C * (NS + 2) + 31) / 32), 32 * kSumGroups, 0, s>>>(a);
     return cudaGetLastError();
 }
 

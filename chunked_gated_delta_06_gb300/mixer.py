@@ -194,16 +194,18 @@ def _scan(x, dt, A_log, B, C, D, z, dt_bias, segment_tokens):
                                         _maybe(D, "D", f32, (Ch,), dev), zp, _maybe(dt_bias, "dt_bias", f32, (Ch,), dev))
 
 
-def _scan_call(fn, name, p, shape, args, workspace, dev):
-    """Without a workspace first, which a call that is not split does not need."""
+def _scan_call(fn, name, p, shape, T, args, workspace, dev):
+    """With a workspace of the caller's or a new one; up to 64 tokens, which the library's plan does not
+    split, first without."""
     stream = linear._raw_stream(dev)
-    if workspace is None:
-        st = fn(p, shape, *args, None, 0, stream)
-        if st == GDN_ERR_WORKSPACE_TOO_SMALL:
-            ws, n, keep = _scratch(None, binding._lib.gdn_selective_scan_workspace_bytes(p, shape, 0), dev)
-            st = fn(p, shape, *args, ws, n, stream)
-    else:
+    ws, n = None, 0
+    if workspace is not None:
         ws, n, keep = _scratch(workspace, 0, dev)
+    elif T > 64:
+        ws, n, keep = _scratch(None, binding._lib.gdn_selective_scan_workspace_bytes(p, shape, 0), dev)
+    st = fn(p, shape, *args, ws, n, stream)
+    if st == GDN_ERR_WORKSPACE_TOO_SMALL and ws is None:   # (segments that the caller asked for)
+        ws, n, keep = _scratch(None, binding._lib.gdn_selective_scan_workspace_bytes(p, shape, 0), dev)
         st = fn(p, shape, *args, ws, n, stream)
     _done(st, name)
 
@@ -222,8 +224,8 @@ def selective_scan_fwd(x, dt, A_log, B, C, cu_host, cu_dev, D=None, z=None, dt_b
     h0 = _maybe(initial_state, "initial_state", torch.float32, state, dev)
     y = torch.empty((T, Ch), dtype=x.dtype, device=x.device)
     ht = torch.empty(state, dtype=torch.float32, device=x.device) if output_final_state else None
-    _scan_call(L.gdn_selective_scan_fwd, "gdn_selective_scan_fwd", p, shape, (*inputs, h0, y.data_ptr(), _ptr(ht)),
-               workspace, dev)
+    _scan_call(L.gdn_selective_scan_fwd, "gdn_selective_scan_fwd", p, shape, T,
+               (*inputs, h0, y.data_ptr(), _ptr(ht)), workspace, dev)
     return y, ht
 
 
@@ -240,7 +242,7 @@ def selective_scan_prefill_paged(x, dt, A_log, B, C, cu_host, cu_dev, state_pool
     idx = _need(state_indices, "state_indices", torch.int32, (N,), dev)
     resume = _maybe(has_initial_state, "has_initial_state", torch.int32, (N,), dev)
     y = torch.empty((T, Ch), dtype=x.dtype, device=x.device)
-    _scan_call(L.gdn_selective_scan_prefill_paged, "gdn_selective_scan_prefill_paged", p, shape,
+    _scan_call(L.gdn_selective_scan_prefill_paged, "gdn_selective_scan_prefill_paged", p, shape, T,
                (*inputs, pool, slots, idx, resume, y.data_ptr(), _status(device_status, dev)), workspace, dev)
     return y
 

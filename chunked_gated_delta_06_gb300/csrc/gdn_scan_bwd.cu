@@ -50,8 +50,8 @@ struct BackTiles {
 //
 // What bounds it: the traffic of shared memory (78 % of the LSU's wavefronts) and the packed fp32.  A state
 // takes two exponentials and some 20 products and sums a token here; the sums over states take 18 shuffles of a
-// warp for four tokens.  32768 packed tokens of 2048 channels of 16 states, bf16: 1639 us in all, of them this
-// kernel 1230, the walk ahead 365, dB and dC's fold 24, the parameters' 22, the joins 15; the bytes are 140.
+// warp for four tokens.  32768 packed tokens of 2048 channels of 16 states, bf16: 1627 us in all, of them this
+// kernel 1230, the walk ahead 350, dB and dC's fold 23, the joins 13, the parameters' sums 10; the bytes are 140.
 // Walking ahead for the marks, the ends and the starts' gradients in three passes took 1924.  Eight states
 // of a channel a thread (half the shuffles) leave one block an SM: slower.
 template <typename T, int NS, bool kWide>

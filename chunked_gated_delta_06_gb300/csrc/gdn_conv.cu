@@ -212,9 +212,11 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
             unpack(in.row(stage, u, 0), win[W - 1]);
             float out[V];
             ch.pre(win, out);
-            if (a.silu)
-#pragma unroll
-                for (int v = 0; v < V; ++v) out[v] *= sigmoid_of(out[v]);
+            if (a.silu) {
+                float sig[V];
+                sigmoid_all(sig, out);
+                mul_all(out, out, sig);
+            }
             ch.shift(win);
             store_vec<V>(y, 0, extent - (y - static_cast<T *>(a.y)), a.pack.status, pack<T>(out));
             y += a.C;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
 // A thread walks a tile and the W - 1 tokens behind it: at token t it has d_t and, with the d's
 // before, dx of token t - (W - 1) (where that lies ahead of the sequence, of its state's entry); behind
 // the last token of a sequence come W - 1 more with d = 0.  Sums for dw and dbias are of the tile's own
-// tokens; k_fold adds the tiles.  16384 tokens of 8192 channels, bf16, take 169 us, 4.8 TB/s or 0.70 of the
+// tokens; k_fold adds the tiles.  16384 tokens of 8192 channels, bf16, take 166 us, 4.9 TB/s or 0.72 of the
 // copy rate: instructions (issue 60 %) and the registers, which leave four blocks an SM, bound it together.  Tiles of 128 tokens read an eighth less twice than 64; 16 bytes a thread spilled.
 template <typename T, int V, int W, bool kFlat>
 __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ ConvArgs a, long long blocks) {
@@ -318,13 +320,15 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
             unpack(in.row(stage, u, 0), win[W - 1]);
             unpack(in.row(stage, u, 1), d[W - 1]);
             if (a.silu) {
-                float o[V], sig[V], rest[V];
+                float o[V], sig[V], rest[V], one_[V];
                 ch.pre(win, o);
+                sigmoid_all(sig, o);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    sig[v] = sigmoid_of(o[v]);
-                    rest[v] = 1.f - sig[v];
+                    one_[v] = 1.f;
+                    rest[v] = -sig[v];
                 }
+                add_all(rest, one_);
                 mul_all(o, o, sig);
                 fma_all(sig, o, rest);   // the slope
                 mul_all(d[W - 1], d[W - 1], sig);
@@ -332,8 +336,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
             if (own) {
 #pragma unroll
                 for (int j = 0; j < W; ++j) fma_all(dw[j], d[W - 1], win[j]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) db[v] += d[W - 1][v];
+                add_all(db, d[W - 1]);
             }
         };
         if (open && t - (W - 1) >= p && t + In::kGroup <= min(e, t1)) {
@@ -393,7 +396,8 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
 
 // One thread for V channels of `rows` rows, one after another (its weights are read once, the next
 // row's state while this one is computed); a row's entries of the slot lie together, (W - 1) V of them.
-// 256 rows of 8192 channels take 12.5 us, of which the launch and one row's latency are half (floor 4.6).
+// 256 rows of 8192 channels take 10.6 us (15.5 cold), half of it the launch and a row's latency (floor 4.6; blocks
+// of three rows in two waves 13.7 and 17.6).
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) k_conv_step(const __grid_constant__ ConvArgs a, int across, int rows) {
     const int c = ((int)(blockIdx.x % across) * kThreads + (int)threadIdx.x) * V;
@@ -551,8 +555,7 @@ cudaError_t conv_step(const ConvArgs &a, int batch, cudaStream_t s) {
     const bool wide = a.C % V == 0 && a.x_stride % V == 0 && fits(a.x, 16) && fits(a.y, 16) && fits(a.s1, 16);
     const int vec = wide ? V : 1;
     const int across = (a.C + kThreads * vec - 1) / (kThreads * vec);
-    // rows of a thread: up to 8, as long as every SM has four blocks
-    const int rows = (int)std::max(1LL, std::min(8LL, (long long)batch * across / (4 * 152)));
+    const int rows = step_rows(batch, across, (wide ? 4 : 16) * 152);   // (what the registers leave an SM)
     const unsigned grid = (unsigned)((batch + rows - 1) / rows * (long long)across);
     if (wide) k_conv_step<T, V, W><<<grid, kThreads, 0, s>>>(a, across, rows);
     else k_conv_step<T, 1, W><<<grid, kThreads, 0, s>>>(a, across, rows);

@@ -101,6 +101,21 @@ __device__ __forceinline__ void mul_all(float (&out)[V], const float (&a)[V], co
     }
 }
 
+template <int V>
+__device__ __forceinline__ void add_all(float (&acc)[V], const float (&a)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 r = add2(make_float2(acc[v], acc[v + 1]), make_float2(a[v], a[v + 1]));
+            acc[v] = r.x;
+            acc[v + 1] = r.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += a[v];
+    }
+}
+
 // V elements from i on of a buffer of n (zeros outside it, in the checked build).
 template <int V, typename T>
 __device__ __forceinline__ Vec<T, V> load_vec(const T *p, long long i, long long n, int *status) {
@@ -133,6 +148,27 @@ __device__ __forceinline__ float reciprocal_of(float x) {
 // 1 / (1 + e^-x): good to about 2^-21 for |x| < 10 (2^-24 |x| beyond), which a result in bf16 does
 // not see and one in fp32 bears.
 __device__ __forceinline__ float sigmoid_of(float x) { return reciprocal_of(1.f + exp_of(-x)); }
+// The same of two numbers, in packed products and sums, and of vectors.
+__device__ __forceinline__ float2 exp2_of(float2 x) { return make_float2(exp2_of(x.x), exp2_of(x.y)); }
+__device__ __forceinline__ float2 exp_of(float2 x) { return exp2_of(mul2(x, both(1.44269504088896341f))); }
+__device__ __forceinline__ float2 reciprocal_of(float2 x) { return make_float2(reciprocal_of(x.x), reciprocal_of(x.y)); }
+__device__ __forceinline__ float2 sigmoid_of(float2 x) {
+    return reciprocal_of(add2(both(1.f), exp2_of(mul2(x, both(-1.44269504088896341f)))));
+}
+template <int V>
+__device__ __forceinline__ void sigmoid_all(float (&out)[V], const float (&x)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) {
+            const float2 s = sigmoid_of(make_float2(x[v], x[v + 1]));
+            out[v] = s.x;
+            out[v + 1] = s.y;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = sigmoid_of(x[v]);
+    }
+}
 
 // Asynchronous copies of `bytes` (4, 8 or 16) into shared memory; zeros instead where there is nothing.
 template <int kBytes>

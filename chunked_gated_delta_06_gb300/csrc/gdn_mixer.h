@@ -87,6 +87,22 @@ struct ScanArgs {
 // segments fit at most; those past its end are idle.
 inline long long scan_items(int N, long long T, int seg) { return N + T / seg; }
 
+// Rows of a block of the steps, which walk their rows one after another: those that end soonest, in waves of
+// the blocks that run at once (a wave takes about a row's time before its first one).
+inline int step_rows(int batch, int across, int at_once) {
+    int best = 1;
+    long long least = 1LL << 62;
+    for (int rows = 1; rows <= 32; ++rows) {
+        const long long blocks = (batch + rows - 1) / rows * (long long)across;
+        const long long time = (blocks + at_once - 1) / at_once * (rows + 1);
+        if (time < least) {
+            least = time;
+            best = rows;
+        }
+    }
+    return best;
+}
+
 int scan_mark_tile();   // tokens of a tile of the backward's marks; a segment is whole tiles
 cudaError_t launch_scan_fwd(const ScanArgs &a, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanArgs &a, cudaStream_t s);

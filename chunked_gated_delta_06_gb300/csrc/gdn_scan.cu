@@ -506,10 +506,9 @@ template <typename T, int NS>
 cudaError_t step(const ScanArgs &a, int batch, cudaStream_t s) {
     using Shape = StepShape<NS>;
     const int across = (a.C + Shape::CB - 1) / Shape::CB;
-    // Rows of a block: up to 8, as long as every SM has the blocks that it runs at once.  (256 rows x 4096 x 16,
-    // cold: 3 rows 38.0 us, 8 36.0, 13 41.1, the last in waves that end badly; one row after another, not
-    // read ahead, 42.1.)
-    const int rows = (int)std::max(1LL, std::min(8LL, (long long)batch * across / (NS == 8 ? 4 * 152 : 2 * 152)));
+    // (256 rows x 4096 x 16, cold: 14 rows a block, one wave, 33 us; 8 rows, 1.7 waves, 36; one row after another, not
+    // read ahead, 42)
+    const int rows = step_rows(batch, across, 152 * Shape::kBlocks);
     const unsigned grid = (unsigned)((batch + rows - 1) / rows * (long long)across);
     auto fits = [](const void *p, long long stride) {
         return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && stride % 4 == 0;

@@ -14,8 +14,6 @@
 
 namespace gdn {
 
-__device__ __forceinline__ float2 exp2_of(float2 x) { return make_float2(exp2_of(x.x), exp2_of(x.y)); }
-
 // softplus(u) = max(u, 0) + log(1 + e^-|u|), the logarithm as 2 artanh(s) with s = e / (2 + e) <= 1/3, good
 // for a small e as well (where log(1 + e) from a rounded 1 + e would keep nothing of it).  artanh(s) / s is
 // a polynomial of s^2 fitted to the function at Chebyshev nodes, reweighted until its relative error is
@@ -31,9 +29,9 @@ __device__ __forceinline__ float softplus_of(float u) {
 
 // Of two numbers at once, without the larger of the number and 0 (to be added last).
 __device__ __forceinline__ float2 softplus_rest(float2 u) {
-    const float2 e = make_float2(exp_of(-fabsf(u.x)), exp_of(-fabsf(u.y)));
+    const float2 e = exp_of(make_float2(-fabsf(u.x), -fabsf(u.y)));
     const float2 n = add2(e, both(2.f));
-    const float2 s = mul2(e, make_float2(reciprocal_of(n.x), reciprocal_of(n.y))), q = mul2(s, s);
+    const float2 s = mul2(e, reciprocal_of(n)), q = mul2(s, s);
     float2 p = fma2(q, both(0.14089163f), both(0.13980302f));
     p = fma2(q, p, both(0.20012455f));
     p = fma2(q, p, both(0.33333157f));
@@ -44,7 +42,7 @@ __device__ __forceinline__ float2 softplus_of(float2 u) {
     return add2(softplus_rest(u), make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
 }
 __device__ __forceinline__ float2 silu_of(float2 z) {
-    return mul2(z, make_float2(sigmoid_of(z.x), sigmoid_of(z.y)));
+    return mul2(z, sigmoid_of(z));
 }
 
 // Where a block works.

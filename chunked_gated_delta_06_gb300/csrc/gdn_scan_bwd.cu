@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                     float2 o = make_float2(dyv[j], dyv[j + 1]);
                     if (gated) {
                         const float2 zj = make_float2(zv[j], zv[j + 1]);
-                        const float2 sig = make_float2(sigmoid_of(zj.x), sigmoid_of(zj.y)), silu = mul2(zj, sig);
-                        const float2 slope = fma2(silu, make_float2(1.f - sig.x, 1.f - sig.y), sig);
+                        const float2 sig = sigmoid_of(zj), silu = mul2(zj, sig);
+                        const float2 slope = fma2(silu, add2(both(1.f), make_float2(-sig.x, -sig.y)), sig);
                         const float2 y = fma2(skip, xj, *reinterpret_cast<const float2 *>(&m.os[i & 1][row][col + j]));
                         const float2 dz = mul2(mul2(o, y), slope);
                         dzv[j] = dz.x;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
                     const float2 u = add2(make_float2(dv[j], dv[j + 1]),
                                           *reinterpret_cast<const float2 *>(&m.bias[col + j]));
                     const float2 dxj = fma2(gB, softplus_of(u), mul2(skip, o));
-                    const float2 du = mul2(fma2(pA, both(ln2), mul2(gB, xj)), make_float2(sigmoid_of(u.x), sigmoid_of(u.y)));
+                    const float2 du = mul2(fma2(pA, both(ln2), mul2(gB, xj)), sigmoid_of(u));
                     dxv[j] = dxj.x;
                     dxv[j + 1] = dxj.y;
                     ddv[j] = du.x;

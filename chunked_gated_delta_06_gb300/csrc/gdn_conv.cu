@@ -6,8 +6,6 @@
 // and with d_t = dy_t y'(u_t):
 //   dx_t = sum_j w_j d_{t+(W-1)-j},   dw_j = sum_t d_t x_{t-(W-1)+j},   dbias = sum_t d_t
 // The state is the last W - 1 inputs, oldest first, so it has no arithmetic of its own.
-#include <algorithm>
-
 #include "gdn_mixer.cuh"
 
 namespace gdn {
@@ -93,29 +91,38 @@ struct Channels {
     }
 };
 
-// The state behind sequence n: its last W - 1 inputs, the older ones from the state ahead of it.
+// Channels of a thread that writes states.
+template <int V>
+constexpr int state_channels() { return V > 1 ? 4 : 1; }
+template <int V>
+__host__ __device__ int state_blocks(int C) {   // of a sequence
+    constexpr int per = kThreads * state_channels<V>();
+    return (C + per - 1) / per;
+}
+
+// The state behind sequence n for V channels: its last W - 1 inputs, the older ones from the state ahead of it.
 // The thread that reads a channel's old state writes the new one, so a slot may hold both.
-template <typename T, int W>
+template <typename T, int V, int W>
 __device__ void final_state(const ConvArgs &a, int n, int c) {
     if (c >= a.C || !a.s1) return;
     const int s = offset_of(a.pack, n), e = max(s, offset_of(a.pack, n + 1));
     const int row = start_row(a, n), to = a.slots.idx ? slot_of(a.slots, n) : n;
-    const Channels<T, 1, W> ch(a, c);
+    const Channels<T, V, W> ch(a, c);
     if (a.slots.idx && c == 0 && a.slots.status && a.slots.idx[n] >= a.slots.num_slots) *a.slots.status = 1;
     if (to < 0) return;
-    float out[W - 1];
+    float flat[W - 1][V];   // the V channels' entries as they lie together
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         const int p = e - (W - 1) + k;
-        float x[1];
-        if (p >= s) x[0] = as_float(ch.token(a.x, p, a.x_stride).x[0]);
+        float x[V];
+        if (p >= s) unpack(ch.token(a.x, p, a.x_stride), x);
         else ch.state(a.s0, row, ch.rows(), p - s + W - 1, x);
-        out[k] = x[0];
-    }
-    const long long i = ((long long)to * a.C + c) * (W - 1);
-    if (in_range(i, W - 1, (long long)ch.rows() * a.C * (W - 1), a.pack.status))
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) static_cast<T *>(a.s1)[i + k] = as_type<T>(out[k]);
+        for (int v = 0; v < V; ++v) flat[(v * (W - 1) + k) / V][(v * (W - 1) + k) % V] = x[v];
+    }
+    const long long i = ((long long)to * a.C + c) * (W - 1), extent = (long long)ch.rows() * a.C * (W - 1);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store_vec<V>(static_cast<T *>(a.s1), i + k * V, extent, a.pack.status, pack<T>(flat[k]));
 }
 
 // A thread's own inputs on their way: `kTensors` rows of V channels a token, kGroup tokens at a time,
@@ -185,10 +192,11 @@ __global__ void __launch_bounds__(kThreads) k_conv_fwd(const __grid_constant__ C
     __shared__ __align__(16) T ring[In::kStages * In::kGroup * kThreads * V];
     const long long block = blockIdx.x;
     if (block >= blocks) {
-        const int per = (a.C + kThreads - 1) / kThreads;
+        constexpr int SV = state_channels<V>();
+        const int per = state_blocks<V>(a.C);
         const long long i = block - blocks;
         if (i >= (long long)a.pack.N * per) check_offsets(a.pack);
-        else final_state<T, W>(a, (int)(i / per), (int)(i % per) * kThreads + (int)threadIdx.x);
+        else final_state<T, SV, W>(a, (int)(i / per), ((int)(i % per) * kThreads + (int)threadIdx.x) * SV);
         return;
     }
     const Place at = place_of<V, kFlat>(a, block);
@@ -250,19 +258,24 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     extern __shared__ __align__(16) unsigned char ring[];
     const long long block = blockIdx.x;
     if (block >= blocks) {   // sequences without tokens: the state passed through
-        const int per = (a.C + kThreads - 1) / kThreads;
+        constexpr int SV = state_channels<V>();
+        const int per = state_blocks<V>(a.C);
         const long long i = block - blocks;
         if (i >= (long long)a.pack.N * per) {
             check_offsets(a.pack);
             return;
         }
-        const int n = (int)(i / per), c = (int)(i % per) * kThreads + (int)threadIdx.x;
+        const int n = (int)(i / per), c = ((int)(i % per) * kThreads + (int)threadIdx.x) * SV;
         if (c >= a.C || !a.ds0 || offset_of(a.pack, n + 1) > offset_of(a.pack, n)) return;
-        const long long at = ((long long)n * a.C + c) * (W - 1);
-        if (!in_range(at, W - 1, (long long)a.pack.N * a.C * (W - 1), a.pack.status)) return;
+        const long long at = ((long long)n * a.C + c) * (W - 1), extent = (long long)a.pack.N * a.C * (W - 1);
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            static_cast<T *>(a.ds0)[at + k] = a.ds1 ? static_cast<const T *>(a.ds1)[at + k] : as_type<T>(0.f);
+        for (int k = 0; k < W - 1; ++k) {
+            Vec<T, SV> v;
+#pragma unroll
+            for (int j = 0; j < SV; ++j) v.x[j] = as_type<T>(0.f);
+            if (a.ds1) v = load_vec<SV>(static_cast<const T *>(a.ds1), at + k * SV, extent, a.pack.status);
+            store_vec<SV>(static_cast<T *>(a.ds0), at + k * SV, extent, a.pack.status, v);
+        }
         return;
     }
     const Place place = place_of<V, kFlat>(a, block);
@@ -504,7 +517,7 @@ cudaError_t conv_fwd(ConvArgs &a, cudaStream_t s) {
     const Layout layout(wide ? a.C / V : a.C);
     a.tile = layout.tile(a.pack.T, 64);
     const long long blocks = layout.blocks(a.pack.T, a.tile);
-    const long long ends = a.s1 ? (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads) : 0;
+    const long long states = (long long)a.pack.N * (wide ? state_blocks<V>(a.C) : state_blocks<1>(a.C)), ends = a.s1 ? states : 0;
     const bool pool = a.slots.idx != nullptr, check = a.pack.status != nullptr;
     // (the check's block is the one behind the blocks of all states)
     auto launch = [&](long long first, long long grid) {
@@ -513,7 +526,6 @@ cudaError_t conv_fwd(ConvArgs &a, cudaStream_t s) {
         if (wide) layout.flat ? with(k_conv_fwd<T, V, W, true>) : with(k_conv_fwd<T, V, W, false>);
         else layout.flat ? with(k_conv_fwd<T, 1, W, true>) : with(k_conv_fwd<T, 1, W, false>);
     };
-    const long long states = (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads);
     const long long behind = check ? states + 1 : ends;
     if (pool) {
         launch(blocks, blocks);
@@ -532,7 +544,8 @@ cudaError_t conv_bwd(ConvArgs &a, cudaStream_t s) {
                       fits(a.dx, V * sizeof(T));
     const Layout layout(wide ? a.C / V : a.C);
     const long long blocks = layout.blocks(a.pack.T, a.tile);
-    const long long grid = blocks + (long long)a.pack.N * ((a.C + kThreads - 1) / kThreads) + (a.pack.status ? 1 : 0);
+    const long long states = (long long)a.pack.N * (wide ? state_blocks<V>(a.C) : state_blocks<1>(a.C));
+    const long long grid = blocks + states + (a.pack.status ? 1 : 0);
     constexpr int kRing = Stream<T, 1, 2>::kStages * Stream<T, 1, 2>::kGroup * 2 * kThreads * (int)sizeof(T);   // a channel
     static_assert(kRing * V <= 64 * 1024, "three blocks an SM");
     auto with = [&](auto kernel, int bytes) {

@@ -1,6 +1,5 @@
 // gdn_scan.cu -- the selective scan's forward (packed, and over pool slots), its state pass over the
 // segments of a split scan, and the step of one token for each row.
-#include <algorithm>
 #include <type_traits>
 
 #include "gdn_scan.cuh"

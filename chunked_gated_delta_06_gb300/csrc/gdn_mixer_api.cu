@@ -186,8 +186,8 @@ constexpr int kNoSplit = 0x7fffffff;
 // pipeline fills and drains in 24 or 32), half a segment for the last ones, about 60 for the launches and
 // one for each segment of the longest sequence, whose records are joined one after another.  A split
 // forward walks its segments for their ends first, at 0.66 of a token; the backward walks ahead anyway.
-// Measured, unsplit and split: forward of 4 x 4096 tokens of 4096 channels 337 and 475 us, of 65536 of 2048
-// 5250 and 919; backward of the same 4 x 4096 1697 and 1635, of 11 sequences up to 6969 tokens 2360 and 1627.
+// Measured, unsplit and split: forward of 4 x 4096 tokens of 4096 channels 334 and 473 us, of 65536 of 2048
+// 5200 and 917; backward of the same 4 x 4096 1697 and 1635, of 11 sequences up to 6969 tokens 2360 and 1627.
 int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &pack, int for_backward) {
     if (s->segment_tokens < 0) return kNoSplit;
     if (s->segment_tokens > 0) {

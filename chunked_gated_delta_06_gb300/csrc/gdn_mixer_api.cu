@@ -183,7 +183,7 @@ constexpr int kNoSplit = 0x7fffffff;
 // leave SMs idle, and blocks of one length end together, or one wave of them late.  Times are in units of a
 // token's in a block that has its SM for itself (forward 90 ns, backward 260 ns); a second block on an SM
 // makes it worth 1.08 or 1.27.  A split walk takes as long as its blocks' tokens over the SMs (a segment's
-// pipeline fills and drains in 24 or 32), half a segment for the last ones, about 60 for the launches and
+// pipeline fills and drains in 24 or 32), half a segment for the last ones, 70 or 60 for the launches and
 // one for each segment of the longest sequence, whose records are joined one after another.  A split
 // forward walks its segments for their ends first, at 0.66 of a token; the backward walks ahead anyway.
 // Measured, unsplit and split: forward of 4 x 4096 tokens of 4096 channels 334 and 473 us, of 65536 of 2048
@@ -205,11 +205,11 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         best = std::max(1.05 * longest, waves);
     }
     int seg = kNoSplit;
-    for (int L = 64; L < longest; L *= 2) {
+    for (int L = kSegment; L < longest; L *= 2) {
         const double bytes = 4.0 * (pack.N + pack.T / L) * s->channels * (2.0 * s->state_dim + 1.0);
         if (bytes > 1073741824.0) continue;
         auto walk = [&](double part) { return std::max((double)L, part * each * (1.0 + fill / L) + 0.5 * L); };
-        double t = walk(1.0) + 60.0 + longest / L;
+        double t = walk(1.0) + (for_backward ? 60.0 : 70.0) + longest / L;
         if (!for_backward) {
             double ends = 0.0;   // the tokens ahead of sequences' last segments
             for (int n = 0; n < pack.N; ++n) {

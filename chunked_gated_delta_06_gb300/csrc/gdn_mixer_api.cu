@@ -205,7 +205,7 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
         best = std::max(1.05 * longest, waves);
     }
     int seg = kNoSplit;
-    for (int L = kSegment; L < longest; L *= 2) {
+    for (int64_t L = kSegment; L < longest; L *= 2) {   // (in 64 bits: sequences may be longer than 2^30)
         const double bytes = 4.0 * (pack.N + pack.T / L) * s->channels * (2.0 * s->state_dim + 1.0);
         if (bytes > 1073741824.0) continue;
         auto walk = [&](double part) { return std::max((double)L, part * each * (1.0 + fill / L) + 0.5 * L); };
@@ -214,13 +214,13 @@ int plan_scan(const gdn_pack *p, const gdn_scan_shape *s, const gdn::PackArgs &p
             double ends = 0.0;   // the tokens ahead of sequences' last segments
             for (int n = 0; n < pack.N; ++n) {
                 const int len = cu[n + 1] - cu[n];
-                ends += len > 0 ? (double)((len - 1) / L) * L : 0.0;
+                ends += len > 0 ? (double)((len - 1) / L * L) : 0.0;
             }
             t += 0.66 * walk(ends / std::max(1, pack.T));
         }
         if (t < best) {
             best = t;
-            seg = L;
+            seg = (int)L;   // (less than the longest sequence)
         }
     }
     return seg;

@@ -1,0 +1,43 @@
+"""Host side of the convolution, the scan and the norms at the limits of their sizes: nothing is launched."""
+import ctypes
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+from chunked_gated_delta_06_gb300 import binding, build
+
+MOST = (1 << 31) - 65536   # tokens of a pack
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.lib()
+
+
+def _pack(*lens):
+    host = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    p = binding.GdnPack(len(host) - 1, int(host[-1]), host.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), 0x10000, None)
+    p.keep = host
+    return p
+
+
+def _scan_bytes(lens, channels=1, state_dim=8, segment=0, backward=0):
+    s = binding.GdnScanShape(channels, 1, state_dim, binding.GDN_DTYPE_BF16, 0, 0, 0, 0, 0, segment)
+    return binding.lib().gdn_selective_scan_workspace_bytes(ctypes.byref(_pack(*lens)), ctypes.byref(s), backward)
+
+
+# (the library's plan tries longer and longer segments; in a process of its own, as one that does not end, or a
+# division by zero, ends the process)
+@pytest.mark.parametrize("lens", [(1 << 30,), ((1 << 30) + 1,), (MOST,), (100, (1 << 30) + 100, 0, 7)])
+def test_sequences_up_to_the_longest_have_a_plan(lens):
+    call = "import test_mixer_limits as t; print(*[t._scan_bytes(%r, backward=b) for b in (0, 1)])" % (lens,)
+    out = subprocess.run([sys.executable, "-c", call], cwd=os.path.dirname(os.path.abspath(__file__)), capture_output=True,
+                         text=True, timeout=60, env={**os.environ, "PYTHONPATH": os.path.dirname(build.PKG)})
+    assert out.returncode == 0, (out.returncode, out.stderr)
+    fwd, bwd = map(int, out.stdout.split())
+    # one channel of 8 states: one record of a segment is 36 bytes at least, marks of 32 bytes for each 8 tokens
+    assert fwd >= 36 and bwd >= sum(lens) // 8 * 32

@@ -36,14 +36,14 @@ __device__ __forceinline__ void row_sums(float (&v)[N], int turn) {
     }
 }
 
-// The gate's factor at z, and its slope (1 - sigmoid as e^-z sigmoid, which a sigmoid near 1 has lost; a
-// NaN stays one).
+// The gate's factor at z, and its slope: 1 - sigmoid as e^-z sigmoid where z >= 0 (a sigmoid near 1 has lost it), and
+// as it stands where z < 0 (there e^-z may be infinite, and the sigmoid 0).  A NaN stays one.
 __device__ __forceinline__ float gate_of(int gate, float z) {
     return sigmoid_of(z) * (gate == GDN_GATE_SIGMOID ? 1.f : z);
 }
 __device__ __forceinline__ float gate_of(int gate, float z, float *slope) {
-    const float e = exp_of(z < -80.f ? 80.f : -z), sig = reciprocal_of(1.f + e), g = sig * (gate == GDN_GATE_SIGMOID ? 1.f : z);
-    *slope = fmaf(g, e * sig, gate == GDN_GATE_SIGMOID ? 0.f : sig);
+    const float e = exp_of(-z), sig = reciprocal_of(1.f + e), g = sig * (gate == GDN_GATE_SIGMOID ? 1.f : z);
+    *slope = fmaf(g, z < 0.f ? 1.f - sig : e * sig, gate == GDN_GATE_SIGMOID ? 0.f : sig);
     return g;
 }
 

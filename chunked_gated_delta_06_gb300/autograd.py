@@ -299,13 +299,14 @@ def _dense_rows(t):
 
 
 def _offsets(T, device, cu_seqlens, cu_seqlens_cpu):
+    """The sequences' offsets on the host and on the device, either from the other where one is not given; one
+    sequence of T tokens without both."""
     import torch
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=device)
-        cu_seqlens_cpu = np.array([0, T], dtype=np.int32)
     if cu_seqlens_cpu is None:
-        cu_seqlens_cpu = cu_seqlens.cpu()
+        cu_seqlens_cpu = np.array([0, T], dtype=np.int32) if cu_seqlens is None else cu_seqlens.cpu()
     cu_host = np.asarray(cu_seqlens_cpu.cpu() if hasattr(cu_seqlens_cpu, "cpu") else cu_seqlens_cpu, dtype=np.int32)
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor(cu_host, dtype=torch.int32, device=device)
     return cu_host, cu_seqlens.to(torch.int32).contiguous()
 
 

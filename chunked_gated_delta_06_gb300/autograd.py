@@ -80,9 +80,8 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, out
     q, k: bf16 [1, T, H, 128] or [T, H, 128]; v: bf16 [.., T, HV, 128]; g: fp32 [.., T, HV];
     beta: bf16 or fp32 [.., T, HV]; initial_state: fp32 [N, HV, 128, 128] or None;
     cu_seqlens: int32 device [N + 1] (default: one sequence), cu_seqlens_cpu: the same
-    boundaries on the host (read from cu_seqlens when not given: one device-to-host copy).
+    boundaries on the host (either is copied from the other when not given).
     recompute_state: the backward rebuilds w, u, h and v_new instead of keeping them."""
-    import torch
     global _FN
     if _FN is None:
         _FN = _function()
@@ -91,16 +90,9 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, out
         if q.shape[0] != 1:
             raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
         q, k, v, g, beta = q[0], k[0], v[0], g[0], beta[0]
-    T = q.shape[0]
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, T], dtype=torch.int32, device=q.device)
-    if cu_seqlens_cpu is None:
-        cu_seqlens_cpu = cu_seqlens.cpu()
-    cu_host = np.asarray(cu_seqlens_cpu.cpu() if hasattr(cu_seqlens_cpu, "cpu") else cu_seqlens_cpu,
-                         dtype=np.int32)
+    cu_host, cu_dev = _offsets(q.shape[0], q.device, cu_seqlens, cu_seqlens_cpu)
     o, ht = _FN.apply(q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous(), beta.contiguous(),
-                      initial_state, cu_host, cu_seqlens.to(torch.int32).contiguous(), scale,
-                      output_final_state, recompute_state)
+                      initial_state, cu_host, cu_dev, scale, output_final_state, recompute_state)
     if batched:
         o = o.unsqueeze(0)
     return o, ht
@@ -171,21 +163,14 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
         raise ValueError("log_decay has no gradient: pass it detached")
     if _LINEAR is None:
         _LINEAR = _linear_function()
-    import torch
     batched = q.dim() == 4
     if batched:
         if q.shape[0] != 1:
             raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
         q, k, v = q[0], k[0], v[0]
-    if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, q.shape[0]], dtype=torch.int32, device=q.device)
-    if cu_seqlens_cpu is None:
-        cu_seqlens_cpu = cu_seqlens.cpu()
-    cu_host = np.asarray(cu_seqlens_cpu.cpu() if hasattr(cu_seqlens_cpu, "cpu") else cu_seqlens_cpu,
-                         dtype=np.int32)
+    cu_host, cu_dev = _offsets(q.shape[0], q.device, cu_seqlens, cu_seqlens_cpu)
     o, ht = _LINEAR.apply(q.contiguous(), k.contiguous(), v.contiguous(), log_decay.contiguous(),
-                          initial_state, cu_host, cu_seqlens.to(torch.int32).contiguous(), scale,
-                          output_final_state)
+                          initial_state, cu_host, cu_dev, scale, output_final_state)
     return (o.unsqueeze(0) if batched else o), ht
 
 

@@ -41,3 +41,24 @@ def test_offsets_of_the_host_alone(offsets, make):
 def test_no_offsets_are_one_sequence(offsets):
     _mixers()
     assert [(host.tolist(), dev.tolist()) for host, dev in offsets] == [([0, 10], [0, 10])] * 2
+
+
+def test_offsets_of_the_host_alone_of_the_attentions(monkeypatch):
+    # (the device's offsets were those of one sequence, shorter than the call reads them)
+    seen = []
+
+    def chunk(q, k, v, g, beta, host, dev, **kw):
+        seen.append((host.tolist(), dev.tolist()))
+        return v * 1.0, None, None
+
+    def linear(q, k, v, log_decay, host, dev, **kw):
+        seen.append((host.tolist(), dev.tolist()))
+        return v * 1.0, None
+    monkeypatch.setattr(gdn.autograd.binding, "chunk_fwd", chunk)
+    monkeypatch.setattr(gdn.autograd.linear, "linear_attn_fwd", linear)
+    q, g = torch.zeros(10, 1, 128), torch.zeros(10, 1)
+    for kw in (dict(cu_seqlens_cpu=[0, 3, 10]), dict(cu_seqlens=torch.tensor([0, 3, 10])),
+               dict(cu_seqlens=torch.tensor([0, 3, 10]), cu_seqlens_cpu=np.array([0, 3, 10])), {}):
+        gdn.chunk_gated_delta_rule(q, q, q, g, g, **kw)
+        gdn.linear_attention(q, q, q, torch.zeros(1), **kw)
+    assert seen == [([0, 3, 10],) * 2] * 6 + [([0, 10],) * 2] * 2

@@ -19,9 +19,10 @@ using gdn::Span;
 
 constexpr int64_t kGrid = 0x7fffffffLL;
 constexpr int32_t kChannels = 1 << 30;   // the kernels' indices of channels stay in 32 bits
+constexpr int64_t kTokens = (1LL << 31) - 65536;   // as do those of tokens (rows of a step), a tile past the last
 
 gdn_status check_pack(const gdn_pack *p, gdn::PackArgs *a) {
-    if (!p || p->num_seqs < 1 || p->total_tokens < 0 || p->total_tokens > 0x7fffffffLL - 65535)
+    if (!p || p->num_seqs < 1 || p->total_tokens < 0 || p->total_tokens > kTokens)
         return GDN_ERR_INVALID_ARG;
     if (!p->cu_seqlens_host || !p->cu_seqlens_dev || !aligned_to(p->cu_seqlens_dev, 4) ||
         !aligned_to(p->device_status, 4))
@@ -460,7 +461,7 @@ gdn_status gdn_short_conv_step(int32_t batch, int32_t channels, int32_t width, i
                                const float *bias, void *conv_pool, int32_t num_slots,
                                const int32_t *state_indices, void *y, int32_t *device_status,
                                gdn_stream_t stream) {
-    if (batch < 0) return GDN_ERR_INVALID_ARG;
+    if (batch < 0 || batch > kTokens) return GDN_ERR_INVALID_ARG;
     gdn_status st = check_conv(channels, width, activation, dtype, x_stride);
     if (st != GDN_OK) return st;
     const Pool pool{num_slots, state_indices, nullptr, device_status};
@@ -575,7 +576,7 @@ gdn_status gdn_selective_scan_step(int32_t batch, const gdn_scan_shape *s, const
                                    const int32_t *state_indices, void *y, int32_t *device_status,
                                    gdn_stream_t stream) {
     ScanWidth w;
-    if (batch < 0) return GDN_ERR_INVALID_ARG;
+    if (batch < 0 || batch > kTokens) return GDN_ERR_INVALID_ARG;
     gdn_status st = check_scan(s, &w);
     if (st != GDN_OK) return st;
     if (num_slots < 1 || (int64_t)batch * (((int64_t)s->channels + 31) / 32) > kGrid) return GDN_ERR_INVALID_ARG;

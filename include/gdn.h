@@ -505,7 +505,8 @@ gdn_status gdn_short_conv_bwd(const gdn_pack *p, int32_t channels, int32_t width
                               gdn_stream_t stream);
 
 /* One token per row: x, y [batch, channels], row b's state in slot
- * state_indices[b] of conv_pool, advanced in place (slots as in gdn_decode_step). */
+ * state_indices[b] of conv_pool, advanced in place (slots as in gdn_decode_step).
+ * batch <= 2^31 - 65536. */
 gdn_status gdn_short_conv_step(int32_t batch, int32_t channels, int32_t width, int32_t activation,
                                int32_t dtype, const void *x, int64_t x_stride, const float *weight,
                                const float *bias, void *conv_pool, int32_t num_slots,
@@ -582,7 +583,7 @@ gdn_status gdn_selective_scan_bwd(const gdn_pack *p, const gdn_scan_shape *s, co
 
 /* One token per row: x, dt, z, y [batch, channels], B, C [batch, groups, state_dim],
  * row b's state in slot state_indices[b] of state_pool, advanced in place (slots as
- * in gdn_decode_step). */
+ * in gdn_decode_step).  batch <= 2^31 - 65536. */
 gdn_status gdn_selective_scan_step(int32_t batch, const gdn_scan_shape *s, const void *x,
                                    const void *dt, const float *A_log, const void *B,
                                    const void *C, const float *D, const void *z,

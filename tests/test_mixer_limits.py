@@ -41,3 +41,13 @@ def test_sequences_up_to_the_longest_have_a_plan(lens):
     fwd, bwd = map(int, out.stdout.split())
     # one channel of 8 states: one record of a segment is 36 bytes at least, marks of 32 bytes for each 8 tokens
     assert fwd >= 36 and bwd >= sum(lens) // 8 * 32
+
+
+def test_rows_of_a_step_that_indices_do_not_hold_are_refused(lib):
+    # (what fits the check goes on to the launch, which this machine may have no device for: not made here)
+    bf, bad, fake = binding.GDN_DTYPE_BF16, binding.GDN_ERR_INVALID_ARG, [(i + 1) << 40 for i in range(12)]
+    s = binding.GdnScanShape(1, 1, 8, bf, 0, 0, 0, 0, 0, 0)
+    for batch in (MOST + 1, (1 << 31) - 32, (1 << 31) - 1):
+        assert lib.gdn_short_conv_step(batch, 1, 4, 1, bf, fake[0], 1, fake[1], None, fake[2], 4, fake[3], fake[4], None, None) == bad
+        assert lib.gdn_selective_scan_step(batch, ctypes.byref(s), *fake[:5], None, None, None, fake[5], 4, fake[6], fake[7], None,
+                                           None) == bad

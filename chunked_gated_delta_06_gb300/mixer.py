@@ -61,6 +61,12 @@ def _rows(t, name, dtype, shape, dev):
     return t.data_ptr(), stride[0] if shape[0] > 1 else 0
 
 
+def _int32(*sizes):
+    """Refuse sizes that the library's 32-bit arguments would wrap."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("sizes must be below 2^31, not %s" % (sizes,))
+
+
 def _pack(T, cu_host, cu_dev, status, dev):
     """gdn_pack as bytes, the array that it points at (to be kept alive), and N."""
     cu = cu_host
@@ -99,6 +105,7 @@ def _conv(x, weight, bias):
     dev, code = _first(x, "x")
     T, C = x.shape
     W = weight.shape[1]
+    _int32(T, C)
     xp, stride = _rows(x, "x", x.dtype, (T, C), dev)
     f32 = torch.float32
     return (T, C, W), dev, code, (xp, stride or C, _need(weight, "weight", f32, (C, W), dev),
@@ -130,6 +137,7 @@ def short_conv_prefill_paged(x, weight, cu_host, cu_dev, conv_pool, state_indice
     (T, C, W), dev, code, args = _conv(x, weight, bias)
     p, keep, N = _pack(T, cu_host, cu_dev, problem_status, dev)
     slots = conv_pool.shape[0]
+    _int32(slots)
     pool = _need(conv_pool, "conv_pool", x.dtype, (slots, C, W - 1), dev)
     idx = _need(state_indices, "state_indices", torch.int32, (N,), dev)
     resume = _maybe(has_initial_state, "has_initial_state", torch.int32, (N,), dev)
@@ -166,6 +174,7 @@ def short_conv_step(x, weight, conv_pool, state_indices, bias=None, activation="
     L = _ready()
     (B, C, W), dev, code, args = _conv(x, weight, bias)
     slots = conv_pool.shape[0]
+    _int32(slots)
     pool = _need(conv_pool, "conv_pool", x.dtype, (slots, C, W - 1), dev)
     idx = _need(state_indices, "state_indices", torch.int32, (B,), dev)
     y = torch.empty((B, C), dtype=x.dtype, device=x.device)
@@ -182,6 +191,7 @@ def _scan(x, dt, A_log, B, C, D, z, dt_bias, segment_tokens):
     dev, code = _first(x, "x")
     T, Ch = x.shape
     _, G, Ns = B.shape
+    _int32(T, Ch, G, Ns)
     t, f32 = x.dtype, torch.float32
     xp, xs = _rows(x, "x", t, (T, Ch), dev)
     dp, ds = _rows(dt, "dt", t, (T, Ch), dev)
@@ -238,6 +248,7 @@ def selective_scan_prefill_paged(x, dt, A_log, B, C, cu_host, cu_dev, state_pool
     (T, Ch, G, Ns), dev, shape, inputs = _scan(x, dt, A_log, B, C, D, z, dt_bias, segment_tokens)
     p, keep, N = _pack(T, cu_host, cu_dev, problem_status, dev)
     slots = state_pool.shape[0]
+    _int32(slots)
     pool = _need(state_pool, "state_pool", torch.float32, (slots, Ch, Ns), dev)
     idx = _need(state_indices, "state_indices", torch.int32, (N,), dev)
     resume = _maybe(has_initial_state, "has_initial_state", torch.int32, (N,), dev)
@@ -275,6 +286,7 @@ def selective_scan_step(x, dt, A_log, B, C, state_pool, state_indices, D=None, z
     L = _ready()
     (rows, Ch, G, Ns), dev, shape, inputs = _scan(x, dt, A_log, B, C, D, z, dt_bias, 0)
     slots = state_pool.shape[0]
+    _int32(slots)
     pool = _need(state_pool, "state_pool", torch.float32, (slots, Ch, Ns), dev)
     idx = _need(state_indices, "state_indices", torch.int32, (rows,), dev)
     y = torch.empty((rows, Ch), dtype=x.dtype, device=x.device)
@@ -294,6 +306,7 @@ def rms_norm_fwd(x, weight, z=None, residual=None, scale=None, gate="silu", eps=
     dev, code = _first(x, "x")
     shape, D, t = x.shape, x.shape[-1], x.dtype
     rows = x.numel() // D if D else 0
+    _int32(D)
     kind = GDN_NO_RESIDUAL if residual is None else _first(residual, "residual")[1]
     f32 = torch.float32
     args = (_need(x, "x", t, shape, dev), None if residual is None else _need(residual, "residual", residual.dtype, shape, dev),
@@ -317,6 +330,7 @@ def rms_norm_bwd(h, weight, dy, z=None, dh=None, scale=None, x=None, gate="silu"
     dev, code = _first(dy, "dy")
     shape, D, t = dy.shape, dy.shape[-1], dy.dtype
     rows = dy.numel() // D if D else 0
+    _int32(D)
     there = residual or dh is not None or scale is not None or h.dtype is not t
     if (scale is None) != (x is None):
         raise ValueError("x is given with a scale, and only then")

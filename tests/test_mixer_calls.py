@@ -62,3 +62,59 @@ def test_offsets_of_the_host_alone_of_the_attentions(monkeypatch):
         gdn.chunk_gated_delta_rule(q, q, q, g, g, **kw)
         gdn.linear_attention(q, q, q, torch.zeros(1), **kw)
     assert seen == [([0, 3, 10],) * 2] * 6 + [([0, 10],) * 2] * 2
+
+
+class _Wide:
+    """What the calls look at of a dense CUDA tensor of any size."""
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape, self.is_cuda, self.device = dtype, torch.Size(shape), True, 0
+
+    def get_device(self):
+        return 0
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    # (as an int32 argument of the library 2^32 + 8 is 8)
+    mixer._ready()
+
+    class Library:
+        def __getattr__(self, name):
+            raise AssertionError("%s is reached" % name)
+    monkeypatch.setattr(gdn.binding, "_lib", Library())
+    monkeypatch.setattr(mixer.linear, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: _Wide(torch.bfloat16, 1))
+    monkeypatch.setattr(torch, "empty_like", lambda t: t)
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    big = (1 << 32) + 8
+    row, w = _Wide(bf, 1, big), _Wide(f32, big)
+    A, B = _Wide(f32, 8, 8), _Wide(bf, big, 1, 8)
+    x, idx = _Wide(bf, big, 8), _Wide(i32, big)
+    few, one, cu = _Wide(bf, 4, 8), _Wide(i32, 4), (np.array([0, 4], np.int32), _Wide(i32, 2))
+    pool, Bf = _Wide(bf, big, 8, 3), _Wide(bf, 4, 1, 8)
+    for call in (lambda: gdn.rms_norm_fwd(row, w), lambda: gdn.rms_norm_bwd(row, w, row),
+                 lambda: gdn.short_conv_step(x, _Wide(f32, 8, 4), _Wide(bf, 4, 8, 3), idx),
+                 lambda: gdn.short_conv_step(few, _Wide(f32, 8, 4), pool, one),
+                 lambda: gdn.short_conv_prefill_paged(few, _Wide(f32, 8, 4), *cu, pool, _Wide(i32, 1)),
+                 lambda: gdn.short_conv_fwd(_Wide(bf, 4, big), _Wide(f32, big, 4), *cu),
+                 lambda: gdn.selective_scan_step(x, x, A, B, B, _Wide(f32, 4, 8, 8), idx),
+                 lambda: gdn.selective_scan_step(few, few, A, Bf, Bf, _Wide(f32, big, 8, 8), one),
+                 lambda: gdn.selective_scan_prefill_paged(few, few, A, Bf, Bf, *cu, _Wide(f32, big, 8, 8), _Wide(i32, 1)),
+                 lambda: gdn.selective_scan_fwd(_Wide(bf, 4, big), _Wide(bf, 4, big), _Wide(f32, big, 8), Bf, Bf, *cu)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()

@@ -296,7 +296,7 @@ def _offsets(T, device, cu_seqlens, cu_seqlens_cpu):
 
 
 def _one_batch(*tensors):
-    if tensors[0].shape[0] != 1:
+    if any(t is not None and t.shape[0] != 1 for t in tensors):
         raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
     return [None if t is None else t[0] for t in tensors]
 

@@ -118,3 +118,17 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
                  lambda: gdn.selective_scan_fwd(_Wide(bf, 4, big), _Wide(bf, 4, big), _Wide(f32, big, 8), Bf, Bf, *cu)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_batches_of_other_sizes_are_refused(offsets):
+    x, B = torch.randn(1, 10, 8), torch.ones(1, 10, 1, 8)
+    two = lambda t: torch.cat([t, t])  # noqa: E731
+    rest = dict(dt=x, A_log=torch.ones(8, 8), B=B, C=B, z=x)
+    gdn.selective_scan(x, **rest)
+    with pytest.raises(ValueError, match="B must be 1"):
+        gdn.short_conv(two(x), torch.ones(8, 4))
+    for name in ("dt", "B", "C", "z"):   # (only the first of the two was read)
+        with pytest.raises(ValueError, match="B must be 1"):
+            gdn.selective_scan(x, **{**rest, name: two(rest[name])})
+        with pytest.raises(ValueError, match="B must be 1"):
+            gdn.selective_scan(x, **{**rest, name: rest[name][0]})   # (without a batch, unlike x)

@@ -445,9 +445,10 @@ gdn_status gdn_rope(int64_t total_tokens, int32_t num_q_heads, int32_t num_k_hea
  * Up to 2^30 channels.
  * Tensors of these calls are bf16 or fp32 as `dtype` (GDN_DTYPE_*) says; all sums,
  * states of the scan and parameters are fp32.  Outputs and workspaces must
- * overlap neither inputs nor one another (GDN_ERR_INVALID_ARG); tensors start on
- * 16 bytes, indices, parameters and rows that are not dense on their element's
- * size, workspaces on 256.  Packed calls with T == 0 pass the states through.
+ * overlap neither inputs nor one another (GDN_ERR_INVALID_ARG); tensors and the
+ * norms' weight and scale start on 16 bytes, indices, the other parameters,
+ * parameters' gradients and rows that may lie apart on their element's size,
+ * workspaces on 256.  Packed calls with T == 0 pass the states through.
  * ------------------------------------------------------------------------- */
 
 /* Packed sequences of any width.  total_tokens <= 2^31 - 65536. */

@@ -51,3 +51,21 @@ def test_rows_of_a_step_that_indices_do_not_hold_are_refused(lib):
         assert lib.gdn_short_conv_step(batch, 1, 4, 1, bf, fake[0], 1, fake[1], None, fake[2], 4, fake[3], fake[4], None, None) == bad
         assert lib.gdn_selective_scan_step(batch, ctypes.byref(s), *fake[:5], None, None, None, fake[5], 4, fake[6], fake[7], None,
                                            None) == bad
+
+
+def test_parameters_start_where_the_header_says(lib):
+    # the convolution's and the scan's on their element's size, the norms' on 16 bytes (each call with a workspace
+    # too small or an output over an input, so that none gets as far as a launch)
+    bf, bad, small = binding.GDN_DTYPE_BF16, binding.GDN_ERR_INVALID_ARG, binding.GDN_ERR_WORKSPACE_TOO_SMALL
+    at = [(i + 1) << 30 for i in range(24)]
+    p, s = ctypes.byref(_pack(9)), ctypes.byref(binding.GdnScanShape(8, 1, 8, bf, 0, 0, 0, 0, 0, 0))
+    for off in (0, 4):
+        q = [a + off for a in at]   # parameters and their gradients
+        assert lib.gdn_short_conv_bwd(p, 8, 4, 1, bf, at[0], 8, q[1], q[2], None, at[3], None, at[4], q[5], q[6], None, at[7], 0,
+                                      None) == small
+        assert lib.gdn_selective_scan_bwd(p, s, at[0], at[1], q[2], at[3], at[4], q[5], None, q[6], None, at[7], None, at[8], at[9],
+                                          q[10], at[11], at[12], q[13], None, q[14], None, at[15], 0, None) == small
+    norm = lambda weight, scale, dw, ds: lib.gdn_rms_norm_bwd(  # noqa: E731
+        4, 128, bf, bf, 0, 1e-6, 0.0, at[0], at[1], scale, weight, None, at[2], None, at[3], at[4], None, dw, ds, at[5], 0, None)
+    assert norm(at[6], at[7], at[8] + 4, at[9] + 4) == small
+    assert norm(at[6] + 4, at[7], at[8], at[9]) == norm(at[6], at[7] + 4, at[8], at[9]) == bad

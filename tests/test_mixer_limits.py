@@ -69,3 +69,19 @@ def test_parameters_start_where_the_header_says(lib):
         4, 128, bf, bf, 0, 1e-6, 0.0, at[0], at[1], scale, weight, None, at[2], None, at[3], at[4], None, dw, ds, at[5], 0, None)
     assert norm(at[6], at[7], at[8] + 4, at[9] + 4) == small
     assert norm(at[6] + 4, at[7], at[8], at[9]) == norm(at[6], at[7] + 4, at[8], at[9]) == bad
+
+
+@pytest.mark.parametrize("lens, channels, state_dim", [((300, 0, 150), 96, 16), ((500, 260), 160, 8), ((700, 33), 96, 32),
+                                                       ((5000,), 32, 16), ((65536,), 2048, 16)])
+def test_long_sequences_of_few_channels_are_split(lens, channels, state_dim):
+    for back in (0, 1):
+        plan, whole = (_scan_bytes(lens, channels, state_dim, s, back) for s in (0, -1))
+        assert plan > whole, back
+
+
+def test_calls_of_few_tokens_are_not_split():
+    # (the Python calls of up to 64 tokens ask for no workspace first)
+    for lens in ((1,), (32,), (33,), (64,), (0, 63, 1), (33, 31), (1,) * 64):
+        for channels in (1, 17, 2048, 1 << 16, 1 << 20):
+            for state_dim in (8, 16, 32):
+                assert _scan_bytes(lens, channels, state_dim) == 256

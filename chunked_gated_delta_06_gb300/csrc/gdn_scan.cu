@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(2 * WalkShape<NS, kFor>::kHalf, 2)
     constexpr int CB = Shape::CB, L = Shape::L, P = Shape::P, S = Shape::S, TT = Shape::TT, R = Shape::kRing, EV = 8;
     constexpr int kHalf = Shape::kHalf;
     using Tile = TileOf<T, CB, TT, EV, kHalf, kWide>;
-    using Rows = RowsOf<T, NS, TT, kHalf, kWide>;
+    using Rows = RowsOf<T, NS, TT, kHalf>;
     using Tiles = ScanTiles<T, NS, kFor>;
     extern __shared__ float4 smem[];
     Tiles &m = *reinterpret_cast<Tiles *>(smem);

@@ -94,29 +94,7 @@ struct TileOf {
     static __device__ int thread() { return (int)threadIdx.x % N; }
     static __device__ int row(int k) { return (thread() + k * N) / kCols; }
     static __device__ int col() { return thread() % kCols * EV; }
-    // rows [t, end) of the tile that starts at token t; zeros elsewhere
-    static __device__ void load(const T *p, long long stride, const ScanArgs &a, const ScanPlace &w, int t, int end, V (&v)[NV]) {
-        const int c = w.c0 + col();
-        const long long extent = (a.pack.T - 1) * stride + a.C;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int at = t + row(k);
-            if (kWide) {
-                if (row(k) < TT && at < end && c < w.cend) {
-                    v[k] = load_vec<EV>(p, at * stride + c, extent, a.pack.status);
-                    continue;
-                }
-#pragma unroll
-                for (int i = 0; i < EV; ++i) v[k].x[i] = as_type<T>(0.f);
-            } else {
-#pragma unroll
-                for (int i = 0; i < EV; ++i)
-                    v[k].x[i] = row(k) < TT && at < end && c + i < w.cend
-                                    ? load_vec<1>(p, at * stride + c + i, extent, a.pack.status).x[0]
-                                    : as_type<T>(0.f);
-            }
-        }
-    }
+    // vector k of the tile that starts at token t, where its row is ahead of `end`
     static __device__ void store(T *p, const ScanArgs &a, const ScanPlace &w, int t, int end, int k, const V &v) {
         const int c = w.c0 + col(), at = t + row(k);
         const long long extent = (long long)a.pack.T * a.C;
@@ -132,26 +110,10 @@ struct TileOf {
 };
 
 // A tile's rows of B or C ([T, G, NS]), four elements a unit.
-template <typename T, int NS, int TT, int N, bool kWide>
+template <typename T, int NS, int TT, int N>
 struct RowsOf {
     static constexpr int kUnits = TT * NS / 4, NU = (kUnits + N - 1) / N;
     using V = Vec<T, 4>;
-    static __device__ void load(const T *p, long long stride, const ScanArgs &a, const ScanPlace &w, int t, int end, V (&v)[NU]) {
-        const long long extent = (a.pack.T - 1) * stride + (long long)a.G * NS;
-#pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int u = (int)threadIdx.x % N + k * N, at = t + u / (NS / 4), i = u % (NS / 4) * 4;
-            const long long from = at * stride + w.g * NS + i;
-            const bool there = u < kUnits && at < end;
-            if (kWide && there) {
-                v[k] = load_vec<4>(p, from, extent, a.pack.status);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[k].x[j] = there ? load_vec<1>(p, from + j, extent, a.pack.status).x[0] : as_type<T>(0.f);
-            }
-        }
-    }
     static __device__ void keep_copied(const V *v, float (*rows)[NS]) {
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
@@ -160,15 +122,6 @@ struct RowsOf {
             float f[4];
             unpack(v[u], f);
             *reinterpret_cast<float4 *>(&rows[u / (NS / 4)][u % (NS / 4) * 4]) = make_float4(f[0], f[1], f[2], f[3]);
-        }
-    }
-    static __device__ void keep(const V (&v)[NU], float (*rows)[NS]) {
-#pragma unroll
-        for (int k = 0; k < NU; ++k) {
-            const int u = (int)threadIdx.x % N + k * N;
-            if (u >= kUnits) break;
-            *reinterpret_cast<float4 *>(&rows[u / (NS / 4)][u % (NS / 4) * 4]) =
-                make_float4(as_float(v[k].x[0]), as_float(v[k].x[1]), as_float(v[k].x[2]), as_float(v[k].x[3]));
         }
     }
 };

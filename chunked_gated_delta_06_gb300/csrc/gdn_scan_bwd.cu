@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(2 * kScanThreads, 2) k_scan_bwd(const __grid_c
     constexpr int CB = PairShape<NS>::CB, L = PairShape<NS>::L, TT = kMarkTile, BT = L < 4 ? L : 4, N = kScanThreads;
     constexpr int kPairs = PairShape<NS>::kPairs, R = BackTiles<T, NS>::kRing;
     using Tile = TileOf<T, CB, TT, kEV, N, kWide>;
-    using Rows = RowsOf<T, NS, TT, N, kWide>;
+    using Rows = RowsOf<T, NS, TT, N>;
     extern __shared__ float4 smem[];
     BackTiles<T, NS> &m = *reinterpret_cast<BackTiles<T, NS> *>(smem);
 

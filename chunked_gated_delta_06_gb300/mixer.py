@@ -61,10 +61,10 @@ def _rows(t, name, dtype, shape, dev):
     return t.data_ptr(), stride[0] if shape[0] > 1 else 0
 
 
-def _int32(*sizes):
-    """Refuse sizes that the library's 32-bit arguments would wrap."""
-    if max(sizes) > 0x7fffffff:
-        raise ValueError("sizes must be below 2^31, not %s" % (sizes,))
+def _int32(sizes):
+    """Refuse sizes that the library's 32-bit arguments would wrap.  sizes: their bits, or-ed."""
+    if sizes >> 31:
+        raise ValueError("the sizes of a call must be below 2^31")
 
 
 def _pack(T, cu_host, cu_dev, status, dev):
@@ -105,7 +105,7 @@ def _conv(x, weight, bias):
     dev, code = _first(x, "x")
     T, C = x.shape
     W = weight.shape[1]
-    _int32(T, C)
+    _int32(T | C)
     xp, stride = _rows(x, "x", x.dtype, (T, C), dev)
     f32 = torch.float32
     return (T, C, W), dev, code, (xp, stride or C, _need(weight, "weight", f32, (C, W), dev),
@@ -191,7 +191,7 @@ def _scan(x, dt, A_log, B, C, D, z, dt_bias, segment_tokens):
     dev, code = _first(x, "x")
     T, Ch = x.shape
     _, G, Ns = B.shape
-    _int32(T, Ch, G, Ns)
+    _int32(T | Ch | G | Ns)
     t, f32 = x.dtype, torch.float32
     xp, xs = _rows(x, "x", t, (T, Ch), dev)
     dp, ds = _rows(dt, "dt", t, (T, Ch), dev)

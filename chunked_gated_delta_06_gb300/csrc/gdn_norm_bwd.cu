@@ -6,9 +6,12 @@
 // apart and keeps its sums for dw and dscale in registers; k_fold adds the blocks in their order.
 // Bound by HBM: each thread's part of the next rows is on its way into shared memory, by asynchronous
 // copies, while a row is computed (from registers alone a block has one row, and waits for it).
-// 512K rows of 128, silu gate, bf16: 109 us, 6.2 TB/s or 0.91 of the copy rate (8-byte vectors 174 us, 456 blocks where
-// 304 run at once 113).  16384 rows of 4096 with an fp32 stream and a scale: 211 us, 5.7 TB/s or 0.84, where the
-// sums for dw and dscale leave two blocks of 512 threads an SM.
+// 512K rows of 128, silu gate, bf16: 108 us, 6.2 TB/s or 0.91 of the copy rate (8-byte vectors 174 us, 456 blocks where
+// 304 run at once 113).  16384 rows of 4096 with an fp32 stream and a scale: 215 us, 5.6 TB/s or 0.83, where the
+// sums for dw and dscale leave two blocks of 512 threads an SM.  That is not the bytes alone: rows wider than 32
+// vectors of 16 bytes have 8 elements a thread, read and gated twice, with a barrier and two chains of shuffles a
+// row, 3 ps an element: of as many elements as those 512K rows, D = 512 .. 6000, gated, take 200 to 215 us, and a
+// bf16 stream without a gate or a scale 148, where their bytes are 99.
 #include <algorithm>
 #include <type_traits>
 

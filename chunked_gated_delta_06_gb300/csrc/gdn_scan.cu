@@ -18,11 +18,13 @@ enum WalkFor { kOutputs, kEnds, kMarks };
 //
 // What bounds it: a state takes an exponential and four products or multiply-adds a token (a gradient's walk
 // six), far more than its share of the bytes.  4 x 4096 tokens of 4096 channels of 16 states, bf16: 334 us, where
-// the bytes are 80, the exponentials alone 115 (8 a cycle and SM quarter) and the packed fp32 140 to 180 (2.4 to
-// 3.1 cycles an instruction, by its operands); 128 blocks of the 152 SMs work.  Left out one at a time, the
-// exponentials, the inputs' product, the outputs' sum or the formers' arithmetic are 20 to 40 us each: no pipe
-// alone is full.  (All in one kind of thread, states in registers and no tiles ahead: 835 us.  A tile's tokens
-// unrolled: 349 before.)  65536 tokens of 2048 channels in one sequence, split: 917 us, unsplit 5200.
+// the bytes are 80; 128 blocks of the 152 SMs work.  The walk's exponentials, products and multiply-adds by
+// themselves take 178 of it.  Left out one at a time, the walk's reads of d and d x are 47 us, the formers'
+// arithmetic 37, the exponentials 30, the sums over lanes 22, the outputs' product 18, the inputs' product 12, the
+// reads of B and C 11: the other half is what passes through shared memory and between lanes, and the formers.
+// (All in one kind of thread, states in registers and no tiles ahead: 835 us.  A tile's tokens unrolled: 349
+// before.)  65536 tokens of 2048 channels in one sequence, split: 917 us, unsplit 5200.  A tile is walked in full: 256
+// sequences of one token of 2048 channels take 97 us.
 template <int NS, WalkFor kFor>
 struct WalkShape {
     static constexpr int kMost = kFor == kMarks ? 8 : 16;           // states of a walker

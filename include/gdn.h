@@ -602,7 +602,8 @@ gdn_status gdn_selective_scan_step(int32_t batch, const gdn_scan_shape *s, const
  *   scale            fp32 [dim], or NULL for 1 (with a residual only)
  *   weight           fp32 [dim]; offset 1 for weights kept around zero
  *   gate             GDN_GATE_*
- * dim 1 .. 8192, eps >= 0 and finite, offset finite. */
+ * dim 1 .. 8192, eps >= 0 and finite, offset finite.  The squares of a row are summed in
+ * fp32: a row whose sum is not finite has y = 0 (h itself infinite or NaN: NaN). */
 #define GDN_NO_RESIDUAL (-1)
 #define GDN_GATE_NONE 0
 #define GDN_GATE_SILU 1

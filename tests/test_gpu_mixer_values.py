@@ -1,4 +1,4 @@
-"""The norms at the ends of their inputs' ranges, against their 64-bit definition."""
+"""The norms at the ends of their inputs' ranges: closed gates against the 64-bit definition, rows past fp32."""
 import pytest
 import torch
 
@@ -33,3 +33,11 @@ def test_gates_that_are_closed(gate, dtype, D):
             ref.check(name, got[name], v, off + ref.HALF[got[name].dtype] * v.abs() + 1e-30)
     closed = z < -1e3
     assert closed.any() and not got["dz"][closed].any() and not got["dx"][8].any()
+
+
+@pytest.mark.parametrize("D", [128, 129, 4096])
+def test_rows_whose_squares_leave_fp32_are_zeros(D):
+    x = torch.randn(5, D, device="cuda")
+    x[2] = 1e25
+    y, _ = gdn.rms_norm_fwd(x, torch.ones(D, device="cuda"))
+    assert not y[2].any() and y[[0, 1, 3, 4]].abs().sum(1).gt(0).all() and torch.isfinite(y).all()

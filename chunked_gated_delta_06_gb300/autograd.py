@@ -45,18 +45,19 @@ def _function():
         def forward(ctx, q, k, v, g, beta, initial_state, cu_host, cu_dev, scale, output_final_state,
                     recompute_state):
             ctx.set_materialize_grads(False)
+            cu_host = cu_host.copy()   # (the backward reads it again, and the caller may reuse its buffer)
             o, ht, c = binding.chunk_fwd(q, k, v, g, beta, cu_host, cu_dev, scale=scale,
                                          initial_state=initial_state,
                                          output_final_state=output_final_state,
                                          for_backward=not recompute_state)
             ctx.gdn = c
             ctx.has_h0 = initial_state is not None
-            ctx.save_for_backward(q, k, v, g, beta, initial_state)
+            ctx.save_for_backward(q, k, v, g, beta, initial_state, cu_dev)
             return o, ht
 
         @staticmethod
         def backward(ctx, d_o, d_ht):
-            q, k, v, g, beta, h0 = ctx.saved_tensors
+            q, k, v, g, beta, h0, _ = ctx.saved_tensors   # (the offsets too: they must not have changed)
             if d_o is None:
                 d_o = torch.zeros((q.shape[0], v.shape[1], v.shape[2]), dtype=torch.bfloat16,
                                   device=q.device)

@@ -132,3 +132,28 @@ def test_batches_of_other_sizes_are_refused(offsets):
             gdn.selective_scan(x, **{**rest, name: two(rest[name])})
         with pytest.raises(ValueError, match="B must be 1"):
             gdn.selective_scan(x, **{**rest, name: rest[name][0]})   # (without a batch, unlike x)
+
+
+def test_offsets_of_the_chunked_rule_changed_before_the_backward(monkeypatch):
+    # a loop that reuses its offset buffers: the backward has the forward's host copy, and a device copy that changed
+    # in place is an error
+    seen = []
+
+    def forward(q, k, v, g, beta, host, dev, **kw):
+        return v * 2.0, None, host
+
+    def backward(host, q, k, v, g, beta, d_o, **kw):
+        seen.append(host.tolist())
+        return dict(dq=q * 0, dk=k * 0, dv=v * 0, dg=g * 0, dbeta=beta * 0, dh0=None)
+    monkeypatch.setattr(gdn.autograd.binding, "chunk_fwd", forward)
+    monkeypatch.setattr(gdn.autograd.binding, "chunk_bwd", backward)
+    q, g = torch.zeros(10, 1, 128, requires_grad=True), torch.zeros(10, 1)
+    host, dev = torch.tensor([0, 3, 10], dtype=torch.int32), torch.tensor([0, 3, 10], dtype=torch.int32)
+    o, _ = gdn.chunk_gated_delta_rule(q, q, q, g, g, cu_seqlens=dev, cu_seqlens_cpu=host)
+    host[1] = 5
+    o.sum().backward()
+    assert seen == [[0, 3, 10]]
+    o, _ = gdn.chunk_gated_delta_rule(q, q, q, g, g, cu_seqlens=dev, cu_seqlens_cpu=host)
+    dev[1] = 5
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()

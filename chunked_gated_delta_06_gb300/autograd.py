@@ -88,9 +88,7 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, out
         _FN = _function()
     batched = q.dim() == 4
     if batched:
-        if q.shape[0] != 1:
-            raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
-        q, k, v, g, beta = q[0], k[0], v[0], g[0], beta[0]
+        q, k, v, g, beta = _one_batch(q, k, v, g, beta)
     cu_host, cu_dev = _offsets(q.shape[0], q.device, cu_seqlens, cu_seqlens_cpu)
     o, ht = _FN.apply(q.contiguous(), k.contiguous(), v.contiguous(), g.contiguous(), beta.contiguous(),
                       initial_state, cu_host, cu_dev, scale, output_final_state, recompute_state)
@@ -166,9 +164,7 @@ def linear_attention(q, k, v, log_decay, scale=None, initial_state=None, output_
         _LINEAR = _linear_function()
     batched = q.dim() == 4
     if batched:
-        if q.shape[0] != 1:
-            raise ValueError("packed sequences only: B must be 1 (use cu_seqlens)")
-        q, k, v = q[0], k[0], v[0]
+        q, k, v = _one_batch(q, k, v)
     cu_host, cu_dev = _offsets(q.shape[0], q.device, cu_seqlens, cu_seqlens_cpu)
     o, ht = _LINEAR.apply(q.contiguous(), k.contiguous(), v.contiguous(), log_decay.contiguous(),
                           initial_state, cu_host, cu_dev, scale, output_final_state)

@@ -157,3 +157,18 @@ def test_offsets_of_the_chunked_rule_changed_before_the_backward(monkeypatch):
     dev[1] = 5
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         o.sum().backward()
+
+
+def test_batches_of_other_sizes_are_refused_by_the_attentions(monkeypatch):
+    monkeypatch.setattr(gdn.autograd.binding, "chunk_fwd", lambda q, k, v, *a, **kw: (v * 1.0, None, None))
+    monkeypatch.setattr(gdn.autograd.linear, "linear_attn_fwd", lambda q, k, v, *a, **kw: (v * 1.0, None))
+    q, g = torch.zeros(1, 10, 1, 128), torch.zeros(1, 10, 1)
+    rule, linear = dict(q=q, k=q, v=q, g=g, beta=g), dict(q=q, k=q, v=q, log_decay=torch.zeros(1))
+    for call, args in ((gdn.chunk_gated_delta_rule, rule), (gdn.linear_attention, linear)):
+        assert call(**args)[0].shape == q.shape
+        for name in ("q", "k", "v", "g", "beta") if call is gdn.chunk_gated_delta_rule else ("q", "k", "v"):
+            with pytest.raises(ValueError, match="B must be 1"):
+                call(**{**args, name: torch.cat([args[name]] * 2)})
+            if name != "q":   # (a tensor without a batch lost all its tokens but the first)
+                with pytest.raises(ValueError, match="B must be 1"):
+                    call(**{**args, name: args[name][0]})
